@@ -367,6 +367,77 @@ kron_status_t kron_l1_penalty(int32_t ntensors, const float* const* tensors, con
 kron_status_t kron_l1_penalty_grad(int64_t n, const float* S, float lam, const float* g, float* dS,
                                    hipStream_t stream);
 
+/*
+ * What is kept of a teacher's answer for distillation: of each row of logits z (N x V, row
+ * stride ld >= V elements) the k largest values with their tokens, and
+ *   lse[n] = log sum_v exp(z[n][v] / temperature)
+ *   logits [N, V]  fp32 or bf16 (dtype), rows ld elements apart
+ *   ids    [N, k]  int32, the largest value's token first; equal values by the lower token
+ *   vals   [N, k]  fp32, the logits themselves (not divided by the temperature)
+ *   lse    [N]     fp32
+ * -0 counts as 0, a NaN stands above every number (lse is NaN then), and a row of -infinity
+ * has lse -infinity.  logits needs only its element's alignment; the outputs 16 bytes.
+ * Limits: 1 <= k <= KRON_DISTILL_MAX_K and k <= V, V <= KRON_VOCAB_MAX, temperature > 0.
+ */
+#define KRON_DISTILL_MAX_K 256
+#define KRON_VOCAB_MAX 262144
+kron_status_t kron_topk_logits(int64_t N, int32_t V, int64_t ld, int32_t k, int32_t dtype, float temperature,
+                               const void* logits, int32_t* ids, float* vals, float* lse, hipStream_t stream);
+
+typedef struct {
+  int64_t N;                 /* rows, >= 0                                                    */
+  int32_t V, k;              /* vocabulary, kept tokens of a row                               */
+  int64_t ld, ldd;           /* row strides of logits and dlogits, in elements, >= V           */
+  int32_t dtype;             /* of logits and dlogits: KRON_F32 or KRON_BF16                   */
+  uint32_t flags;            /* KRON_IDS_I64                                                   */
+  float temperature, alpha;  /* T > 0;  0 <= alpha <= 1                                        */
+} kron_distill_t;
+#define KRON_IDS_I64 1u      /* ids are int64 (else int32) */
+#define KRON_DISTILL_STATS 8 /* floats of stats for each row */
+
+/*
+ * Distillation of a student's logits z from a teacher's top k tokens (as kron_topk_logits
+ * gives them), mixed with the cross-entropy on labels.  With T the temperature and
+ * q = softmax(z / T), row n has
+ *   teacher_lse NULL:   p_j = softmax_j(teacher[n][j] / T) over the kept tokens,
+ *                       KD = sum_j p_j (log p_j - log q[ids[n][j]])
+ *   teacher_lse given:  p_j = exp(teacher[n][j] / T - teacher_lse[n]), p_t = 1 - sum_j p_j and
+ *                       q_t = 1 - sum_j q[ids[n][j]]: the rest of the vocabulary as one class;
+ *                       KD = sum_j p_j (log p_j - log q[ids[n][j]]) + p_t (log p_t - log q_t)
+ *   loss    = sum_n w_n (alpha T^2 KD_n + (1 - alpha) (logsumexp(z_n) - z_n[labels[n]]))
+ *   dlogits = d loss / d z
+ *   logits [N, V]  ids [N, k]  teacher [N, k] fp32  teacher_lse [N] fp32  labels [N] int64
+ *   weights [N] fp32 (NULL: 1 / N)  loss: one float  dlogits [N, V], dtype of logits
+ * ids and teacher are needed for alpha > 0 (k = 0 and NULL are allowed at alpha = 0, a plain
+ * cross-entropy), labels for alpha < 1.
+ *   - A row of weight 0 is left out whole (padding): nothing of it is read, its gradient is 0.
+ *   - A negative id is an unused slot.  A row without a used slot has KD = 0.  A teacher value
+ *     of -infinity has p = 0.  A token given twice counts with both p.  p_t is at least 0.
+ *   - An id >= V or a label outside [0, V) makes the loss and that row's gradient NaN (no
+ *     out-of-bounds access).
+ *   - Elements between V and the row stride are neither read nor written.
+ *   - dlogits may be logits itself (same address, ldd = ld): the gradient replaces the logits.
+ *     Any other overlap is refused.
+ *
+ * kron_distill computes loss and dlogits in one pass.  kron_distill_fwd computes the loss and
+ * keeps stats [N, KRON_DISTILL_STATS] for kron_distill_bwd, which gives gout[0] times the gradient
+ * (gout: one device float) of the same arguments; the stats' layout is private.
+ *
+ * logits and dlogits need only their element's alignment, the other arrays 16 bytes; workspace
+ * as for kron_linear_bwd (kron_distill_workspace_bytes; kron_distill_bwd needs none).  Sums and
+ * softmax statistics are fp32 or fp64, the gradient is rounded once.
+ */
+size_t kron_distill_workspace_bytes(const kron_distill_t* d);
+kron_status_t kron_distill(const kron_distill_t* d, const void* logits, const void* ids, const float* teacher,
+                           const float* teacher_lse, const int64_t* labels, const float* weights, float* loss,
+                           void* dlogits, void* workspace, size_t workspace_bytes, hipStream_t stream);
+kron_status_t kron_distill_fwd(const kron_distill_t* d, const void* logits, const void* ids, const float* teacher,
+                               const float* teacher_lse, const int64_t* labels, const float* weights, float* loss,
+                               float* stats, void* workspace, size_t workspace_bytes, hipStream_t stream);
+kron_status_t kron_distill_bwd(const kron_distill_t* d, const void* logits, const void* ids, const float* teacher,
+                               const float* teacher_lse, const int64_t* labels, const float* weights,
+                               const float* stats, const float* gout, void* dlogits, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

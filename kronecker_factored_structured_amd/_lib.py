@@ -31,6 +31,11 @@ KRON_SPARSE_ROWS = 4
 
 KRON_ACCUMULATE = 1
 
+KRON_IDS_I64 = 1
+KRON_DISTILL_STATS = 8
+KRON_DISTILL_MAX_K = 256
+KRON_VOCAB_MAX = 262144
+
 # Every symbol include/kron.h declares.
 EXPORTS = (
     "kron_abi_version", "kron_status_str", "kron_last_error", "kron_linear_check",
@@ -40,7 +45,8 @@ EXPORTS = (
     "ks_matmul_out", "ks_matmul_bwd_workspace_bytes", "ks_matmul_bwd", "ks_chain",
     "kron_van_loan_workspace_bytes", "kron_van_loan", "kron_relu_bwd", "kron_l1_penalty",
     "kron_l1_penalty_grad", "kron_linear_bwd_noalloc", "kron_linear_zcache_bytes", "kron_linear_fwd_save",
-    "kron_linear_bwd_saved",
+    "kron_linear_bwd_saved", "kron_topk_logits", "kron_distill_workspace_bytes", "kron_distill",
+    "kron_distill_fwd", "kron_distill_bwd",
 )
 
 KRON_NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -55,6 +61,12 @@ class KronShape(ctypes.Structure):
     _fields_ = [("N", ctypes.c_int64), ("p", ctypes.c_int32), ("q", ctypes.c_int32),
                 ("m", ctypes.c_int32), ("n", ctypes.c_int32), ("r", ctypes.c_int32),
                 ("flags", ctypes.c_uint32)]
+
+
+class KronDistill(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int64), ("V", ctypes.c_int32), ("k", ctypes.c_int32), ("ld", ctypes.c_int64),
+                ("ldd", ctypes.c_int64), ("dtype", ctypes.c_int32), ("flags", ctypes.c_uint32),
+                ("temperature", ctypes.c_float), ("alpha", ctypes.c_float)]
 
 
 class KronError(RuntimeError):
@@ -77,6 +89,7 @@ def lib() -> ctypes.CDLL:
         L = ctypes.CDLL(LIB_PATH)
         vp, i32, i64, u32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_size_t
         shp = ctypes.POINTER(KronShape)
+        dis = ctypes.POINTER(KronDistill)
         pp = ctypes.POINTER(ctypes.c_void_p)
         sig = {
             "kron_abi_version": (i32, []),
@@ -108,6 +121,11 @@ def lib() -> ctypes.CDLL:
             "kron_relu_bwd": (i32, [i64, vp, vp, vp, vp]),
             "kron_l1_penalty": (i32, [i32, pp, ctypes.POINTER(ctypes.c_int64), ctypes.c_float, vp, u32, vp]),
             "kron_l1_penalty_grad": (i32, [i64, vp, ctypes.c_float, vp, vp, vp]),
+            "kron_topk_logits": (i32, [i64, i32, i64, i32, i32, ctypes.c_float, vp, vp, vp, vp, vp]),
+            "kron_distill_workspace_bytes": (sz, [dis]),
+            "kron_distill": (i32, [dis, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+            "kron_distill_fwd": (i32, [dis, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+            "kron_distill_bwd": (i32, [dis, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)

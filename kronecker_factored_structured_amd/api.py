@@ -12,8 +12,8 @@ from typing import Optional, Sequence
 import torch
 
 from . import _lib
-from ._lib import (KRON_ACCUMULATE, KRON_BF16, KRON_DX_RELU_MASK, KRON_F32, KRON_RELU_OUT, KRON_SPARSE_ROWS, KronShape,
-                   check)
+from ._lib import (KRON_ACCUMULATE, KRON_BF16, KRON_DISTILL_STATS, KRON_DX_RELU_MASK, KRON_F32, KRON_IDS_I64,
+                   KRON_RELU_OUT, KRON_SPARSE_ROWS, KronDistill, KronShape, check)
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -478,3 +478,137 @@ def kron_l1_penalty_grad(S: torch.Tensor, lam: float, g: torch.Tensor,
     check("kron_l1_penalty_grad", _lib.lib().kron_l1_penalty_grad(S.numel(), _ptr(S), float(lam), _ptr(g), _ptr(o),
                                                                   _stream(S.device)))
     return o
+
+
+def _dtype_code(t: torch.Tensor) -> int:
+    if t.dtype == torch.float32:
+        return KRON_F32
+    if t.dtype == torch.bfloat16:
+        return KRON_BF16
+    raise ValueError(f"unsupported dtype {t.dtype}")
+
+
+def _logit_rows(t: torch.Tensor, name: str) -> int:
+    """The row stride of an N x V tensor of logits: its rows are dense but may lie apart (a
+    vocabulary padded in memory)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor (libkron has no CPU path)")
+    if t.dim() != 2 or t.shape[1] < 1:
+        raise ValueError(f"{name} must be N x V, got {tuple(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have dense rows (last stride 1, got {t.stride(1)})")
+    ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if ld < t.shape[1]:
+        raise ValueError(f"the rows of {name} overlap (row stride {ld} below {t.shape[1]})")
+    return ld
+
+
+def kron_topk_logits(logits: torch.Tensor, k: int, temperature: float = 1.0) -> tuple:
+    """The k largest logits of each row: (ids int32 [N, k], vals float32 [N, k], lse float32 [N])
+    with lse = logsumexp(logits / temperature) of the whole row; largest first, equal values by the
+    lower token.  logits is float32 or bfloat16 [N, V]; its rows may be padded (row stride > V)."""
+    dt, ld = _dtype_code(logits), _logit_rows(logits, "logits")
+    N, V = logits.shape
+    if not 1 <= k <= V:
+        raise ValueError(f"k must be in 1..{V}, got {k}")
+    dev = logits.device
+    ids = torch.empty(N, k, dtype=torch.int32, device=dev)
+    vals = torch.empty(N, k, device=dev)
+    lse = torch.empty(N, device=dev)
+    with torch.cuda.device(dev):
+        check("kron_topk_logits", _lib.lib().kron_topk_logits(
+            N, V, ld, k, dt, float(temperature), _ptr(logits), _ptr(ids), _ptr(vals), _ptr(lse), _stream(dev)))
+    return ids, vals, lse
+
+
+def _distill_args(logits, ids, teacher, teacher_lse, labels, weights, temperature, alpha):
+    """The checked sizes and pointers that the distillation calls share."""
+    dt, ld = _dtype_code(logits), _logit_rows(logits, "logits")
+    N, V = logits.shape
+    dev = logits.device
+    k = 0
+    if alpha > 0:
+        if ids is None or teacher is None:
+            raise ValueError("ids and teacher are needed when alpha > 0")
+        if ids.dim() != 2 or ids.shape[0] != N or ids.shape[1] < 1:
+            raise ValueError(f"ids must be {N} x k, got {tuple(ids.shape)}")
+        if ids.dtype not in (torch.int32, torch.int64):
+            raise ValueError(f"ids must be int32 or int64, got {ids.dtype}")
+        k = ids.shape[1]
+        _need(ids, "ids", (N, k), ids.dtype, dev)
+        _need(teacher, "teacher", (N, k), device=dev)
+        _need(teacher_lse, "teacher_lse", (N,), device=dev)
+    if alpha < 1:
+        if labels is None:
+            raise ValueError("labels are needed when alpha < 1")
+        _need(labels, "labels", (N,), torch.int64, dev)
+    _need(weights, "weights", (N,), device=dev)
+    flags = KRON_IDS_I64 if k and ids.dtype == torch.int64 else 0
+    d = KronDistill(N, V, k, ld, V, dt, flags, float(temperature), float(alpha))
+    ptrs = (_ptr(logits), _ptr(ids) if k else None, _ptr(teacher) if k else None, _ptr(teacher_lse) if k else None,
+            _ptr(labels) if alpha < 1 else None, _ptr(weights))
+    return d, ptrs
+
+
+def _distill_out(d: KronDistill, logits: torch.Tensor, out: Optional[torch.Tensor]) -> torch.Tensor:
+    if out is None:
+        return torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    if out.dtype != logits.dtype or out.device != logits.device or out.shape != logits.shape:
+        raise ValueError(f"out must be {tuple(logits.shape)} {logits.dtype} on {logits.device}")
+    d.ldd = _logit_rows(out, "out")
+    return out
+
+
+def kron_distill(logits: torch.Tensor, ids: Optional[torch.Tensor], teacher: Optional[torch.Tensor],
+                 teacher_lse: Optional[torch.Tensor] = None, labels: Optional[torch.Tensor] = None,
+                 weights: Optional[torch.Tensor] = None, temperature: float = 1.0, alpha: float = 1.0,
+                 out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> dict:
+    """Distillation from a teacher's top logits and its gradient in one pass: dict(loss (1-element
+    tensor), dlogits).  ids and teacher [N, k] as kron_topk_logits gives them (ids int32 or int64, a
+    negative id is an unused slot); with teacher_lse [N] the rest of the vocabulary counts as one class,
+    without it the teacher's top is renormalised.  loss = sum_n weights[n] (alpha T^2 KD_n + (1 - alpha)
+    CE_n(labels)), weights None: 1 / N, weight 0: the row is left out.  out may be logits itself (the
+    gradient replaces them)."""
+    d, ptrs = _distill_args(logits, ids, teacher, teacher_lse, labels, weights, temperature, alpha)
+    dz = _distill_out(d, logits, out)
+    dev = logits.device
+    loss = torch.empty(1, device=dev)
+    L = _lib.lib()
+    ws = _workspace(workspace, int(L.kron_distill_workspace_bytes(ctypes.byref(d))), dev)
+    with torch.cuda.device(dev):
+        check("kron_distill", L.kron_distill(ctypes.byref(d), *ptrs, _ptr(loss), _ptr(dz), _ptr(ws),
+                                             ctypes.c_size_t(ws.numel()), _stream(dev)))
+    return dict(loss=loss, dlogits=dz)
+
+
+def kron_distill_fwd(logits: torch.Tensor, ids: Optional[torch.Tensor], teacher: Optional[torch.Tensor],
+                     teacher_lse: Optional[torch.Tensor] = None, labels: Optional[torch.Tensor] = None,
+                     weights: Optional[torch.Tensor] = None, temperature: float = 1.0, alpha: float = 1.0,
+                     workspace: Optional[torch.Tensor] = None) -> tuple:
+    """kron_distill's loss alone, and the rows' statistics for kron_distill_bwd: (loss, stats)."""
+    d, ptrs = _distill_args(logits, ids, teacher, teacher_lse, labels, weights, temperature, alpha)
+    dev = logits.device
+    loss = torch.empty(1, device=dev)
+    stats = torch.empty(logits.shape[0], KRON_DISTILL_STATS, device=dev)
+    L = _lib.lib()
+    ws = _workspace(workspace, int(L.kron_distill_workspace_bytes(ctypes.byref(d))), dev)
+    with torch.cuda.device(dev):
+        check("kron_distill_fwd", L.kron_distill_fwd(ctypes.byref(d), *ptrs, _ptr(loss), _ptr(stats), _ptr(ws),
+                                                     ctypes.c_size_t(ws.numel()), _stream(dev)))
+    return loss, stats
+
+
+def kron_distill_bwd(logits: torch.Tensor, ids: Optional[torch.Tensor], teacher: Optional[torch.Tensor],
+                     stats: torch.Tensor, gout: torch.Tensor, teacher_lse: Optional[torch.Tensor] = None,
+                     labels: Optional[torch.Tensor] = None, weights: Optional[torch.Tensor] = None,
+                     temperature: float = 1.0, alpha: float = 1.0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """gout[0] times the gradient of the loss that kron_distill_fwd gave for the same arguments."""
+    d, ptrs = _distill_args(logits, ids, teacher, teacher_lse, labels, weights, temperature, alpha)
+    dz = _distill_out(d, logits, out)
+    dev = logits.device
+    _need(stats, "stats", (logits.shape[0], KRON_DISTILL_STATS), device=dev)
+    _need(gout, "gout", (1,), device=dev)
+    with torch.cuda.device(dev):
+        check("kron_distill_bwd", _lib.lib().kron_distill_bwd(ctypes.byref(d), *ptrs, _ptr(stats), _ptr(gout), _ptr(dz),
+                                                              _stream(dev)))
+    return dz

@@ -39,6 +39,8 @@ OBJECTS = [
     ("adam_l1.hip", [], "adam_l1"),
     ("head_ce.hip", [], "head_ce"),
     ("loss_terms.hip", [], "loss_terms"),
+    ("distill.hip", [], "distill"),
+    ("topk_logits.hip", [], "topk_logits"),
 ]
 SOURCES = sorted({src for src, _, _ in OBJECTS})
 

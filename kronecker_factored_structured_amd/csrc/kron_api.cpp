@@ -72,6 +72,15 @@ constexpr int32_t kMaxRank = 64;
 constexpr int64_t kMaxFeatures = 65536;
 constexpr int64_t kMaxParams = int64_t(1) << 24;
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxStride = int64_t(1) << 40;
+
+// Bytes from the first to the last element of N rows of V elements, ld elements apart
+// (saturating: sizes beyond the address space overlap everything).
+size_t strided_bytes(int64_t N, int64_t ld, int64_t V, size_t es) {
+  if (N <= 0) return 0;
+  const unsigned __int128 b = ((unsigned __int128)(N - 1) * (unsigned __int128)ld + (unsigned __int128)V) * es;
+  return b > ((unsigned __int128)1 << 62) ? (size_t)1 << 62 : (size_t)b;
+}
 
 kron_status_t check_shape(const kron_shape_t* s) {
   if (!s) return fail(KRON_E_NULL, "shape is NULL");
@@ -818,6 +827,140 @@ kron_status_t kron_head_ce(int64_t N, int32_t K, int32_t C, const float* h, cons
   hipError_t e = kron::launch_head(a, kron::head_groups(N), stream);
   if (e != hipSuccess) return hip_fail(e, "kron_head_ce launch");
   return ok();
+}
+
+kron_status_t kron_topk_logits(int64_t N, int32_t V, int64_t ld, int32_t k, int32_t dtype, float temperature,
+                               const void* logits, int32_t* ids, float* vals, float* lse, hipStream_t stream) {
+  if (N < 0 || N > kMaxRows) return fail(KRON_E_SHAPE, "N = %lld out of range", (long long)N);
+  if (V < 1 || k < 1 || k > V) return fail(KRON_E_SHAPE, "V = %d and k = %d: 1 <= k <= V is needed", V, k);
+  if (ld < V || ld > kMaxStride) return fail(KRON_E_SHAPE, "ld = %lld outside V = %d .. 2^40", (long long)ld, V);
+  if (V > KRON_VOCAB_MAX || k > KRON_DISTILL_MAX_K)
+    return fail(KRON_E_UNSUPPORTED, "V = %d, k = %d beyond the limits (V <= %d, k <= %d)", V, k, KRON_VOCAB_MAX,
+                KRON_DISTILL_MAX_K);
+  if (dtype != KRON_F32 && dtype != KRON_BF16) return fail(KRON_E_DTYPE, "dtype %d", dtype);
+  if (!(temperature > 0.f) || !std::isfinite(temperature))
+    return fail(KRON_E_ARG, "temperature = %g must be positive and finite", (double)temperature);
+  if (N == 0) return ok();
+  if (!logits || !ids || !vals || !lse) return fail(KRON_E_NULL, "logits, ids, vals and lse are required");
+  const size_t es = dtype == KRON_F32 ? 4 : 2;
+  if (((uintptr_t)logits & (es - 1)) != 0) return fail(KRON_E_ALIGN, "logits is not aligned to its elements");
+  const Range ins[1] = {{logits, strided_bytes(N, ld, V, es), "logits"}};
+  const Range outs[3] = {{ids, (size_t)N * k * 4, "ids"}, {vals, (size_t)N * k * 4, "vals"}, {lse, (size_t)N * 4, "lse"}};
+  kron_status_t st;
+  if ((st = check_align(outs, 3)) != KRON_OK || (st = check_alias(outs, 3, ins, 1)) != KRON_OK) return st;
+  const kron::TopkArgs a{N, ld, V, k, dtype == KRON_BF16, temperature, logits, ids, vals, lse};
+  const hipError_t e = kron::launch_topk(a, stream);
+  if (e != hipSuccess) return hip_fail(e, "kron_topk_logits launch");
+  return ok();
+}
+
+namespace {
+
+kron_status_t distill_check(const kron_distill_t* d) {
+  if (!d) return fail(KRON_E_NULL, "the distillation's sizes are NULL");
+  if (d->N < 0 || d->N > kMaxRows) return fail(KRON_E_SHAPE, "N = %lld out of range", (long long)d->N);
+  if (d->V < 1 || d->k < 0) return fail(KRON_E_SHAPE, "V = %d must be >= 1 and k = %d >= 0", d->V, d->k);
+  if (d->V > KRON_VOCAB_MAX || d->k > KRON_DISTILL_MAX_K)
+    return fail(KRON_E_UNSUPPORTED, "V = %d, k = %d beyond the limits (V <= %d, k <= %d)", d->V, d->k, KRON_VOCAB_MAX,
+                KRON_DISTILL_MAX_K);
+  if (d->dtype != KRON_F32 && d->dtype != KRON_BF16) return fail(KRON_E_DTYPE, "dtype %d", d->dtype);
+  if (d->flags & ~KRON_IDS_I64) return fail(KRON_E_ARG, "unknown flag bits 0x%x", d->flags);
+  if (!(d->temperature > 0.f) || !std::isfinite(d->temperature))
+    return fail(KRON_E_ARG, "temperature = %g must be positive and finite", (double)d->temperature);
+  if (!(d->alpha >= 0.f && d->alpha <= 1.f)) return fail(KRON_E_ARG, "alpha = %g outside [0, 1]", (double)d->alpha);
+  if (d->alpha > 0.f && d->k < 1) return fail(KRON_E_SHAPE, "k = %d must be >= 1 when alpha > 0", d->k);
+  if (d->ld < d->V || d->ld > kMaxStride)
+    return fail(KRON_E_SHAPE, "ld = %lld outside V = %d .. 2^40", (long long)d->ld, d->V);
+  return KRON_OK;
+}
+
+// mode 0: loss and gradient; 1: loss and stats; 2: gradient from stats
+kron_status_t distill_run(const kron_distill_t* d, int mode, const void* logits, const void* ids, const float* teacher,
+                          const float* teacher_lse, const int64_t* labels, const float* weights, float* loss,
+                          float* stats, const float* gout, void* dlogits, void* workspace, size_t workspace_bytes,
+                          hipStream_t stream) {
+  kron_status_t st = distill_check(d);
+  if (st != KRON_OK) return st;
+  const bool kd = d->alpha > 0.f, ce = d->alpha < 1.f, grad = mode != 1;
+  if (grad && (d->ldd < d->V || d->ldd > kMaxStride))
+    return fail(KRON_E_SHAPE, "ldd = %lld outside V = %d .. 2^40", (long long)d->ldd, d->V);
+  if (mode != 2 && !loss) return fail(KRON_E_NULL, "loss is required");
+  if (mode == 2 && !gout) return fail(KRON_E_NULL, "gout is required");
+  if (d->N > 0) {
+    if (!logits || (grad && !dlogits) || (mode != 0 && !stats))
+      return fail(KRON_E_NULL, "logits, dlogits and stats are required when N > 0");
+    if (kd && (!ids || !teacher)) return fail(KRON_E_NULL, "ids and teacher are required when alpha > 0");
+    if (ce && !labels) return fail(KRON_E_NULL, "labels are required when alpha < 1");
+  }
+  const size_t es = d->dtype == KRON_F32 ? 4 : 2, is = d->flags & KRON_IDS_I64 ? 8 : 4;
+  const size_t need = mode == 2 ? 0 : kron_distill_workspace_bytes(d);
+  if (mode != 2) {
+    if (!workspace || workspace_bytes < need)
+      return fail(KRON_E_WORKSPACE, "workspace of %zu bytes given, %zu needed", workspace_bytes, need);
+    if (((uintptr_t)workspace & 255u) != 0) return fail(KRON_E_ALIGN, "workspace is not 256-byte aligned");
+  }
+  if (((uintptr_t)logits & (es - 1)) != 0 || (grad && ((uintptr_t)dlogits & (es - 1)) != 0))
+    return fail(KRON_E_ALIGN, "logits or dlogits is not aligned to its elements");
+  const size_t nk = kd ? (size_t)d->N * d->k : 0;
+  const size_t zb = strided_bytes(d->N, d->ld, d->V, es), gb = grad ? strided_bytes(d->N, d->ldd, d->V, es) : 0;
+  const size_t sb = (size_t)d->N * KRON_DISTILL_STATS * 4;
+  const Range zr[1] = {{logits, zb, "logits"}};
+  const Range ins[8] = {{ids, nk * is, "ids"},
+                        {teacher, nk * 4, "teacher"},
+                        {teacher_lse, kd ? (size_t)d->N * 4 : 0, "teacher_lse"},
+                        {labels, ce ? (size_t)d->N * 8 : 0, "labels"},
+                        {weights, (size_t)d->N * 4, "weights"},
+                        {workspace, need, "workspace"},
+                        {mode == 2 ? stats : nullptr, sb, "stats"},
+                        {mode == 2 ? gout : nullptr, 4, "gout"}};
+  const Range outs[2] = {{mode == 2 ? nullptr : loss, 4, "loss"}, {mode == 1 ? stats : nullptr, sb, "stats"}};
+  const Range all[3] = {{mode == 2 ? nullptr : loss, 4, "loss"},
+                        {mode == 1 ? stats : nullptr, sb, "stats"},
+                        {grad ? dlogits : nullptr, gb, "dlogits"}};
+  if ((st = check_align(ins, 8)) != KRON_OK || (st = check_align(outs, 2)) != KRON_OK) return st;
+  if ((st = check_alias(all, 3, ins, 8)) != KRON_OK) return st;
+  // the gradient may replace the logits in place; any other overlap with them is refused
+  const bool in_place = grad && dlogits == logits && d->ldd == d->ld;
+  if ((st = check_alias(all, in_place ? 2 : 3, zr, 1)) != KRON_OK) return st;
+  if (mode == 2 && d->N == 0) return ok();
+  kron::DistillArgs a{};
+  a.N = d->N; a.ld = d->ld; a.ldd = grad ? d->ldd : d->ld; a.V = d->V; a.k = kd ? d->k : 0;
+  a.bf16 = d->dtype == KRON_BF16; a.ids64 = (d->flags & KRON_IDS_I64) != 0;
+  a.T = d->temperature; a.alpha = d->alpha;
+  a.logits = logits; a.ids = ids; a.teacher = teacher; a.teacher_lse = kd ? teacher_lse : nullptr;
+  a.labels = labels; a.weights = weights; a.gout = gout; a.stats = stats; a.lossrow = (float*)workspace;
+  a.loss = loss; a.dlogits = dlogits;
+  const hipError_t e = kron::launch_distill(a, mode, stream);
+  if (e != hipSuccess) return hip_fail(e, "kron_distill launch");
+  return ok();
+}
+
+}  // namespace
+
+size_t kron_distill_workspace_bytes(const kron_distill_t* d) {
+  if (distill_check(d) != KRON_OK) return 0;
+  return (((size_t)d->N * 4 + 255) & ~size_t(255)) + 256;
+}
+
+kron_status_t kron_distill(const kron_distill_t* d, const void* logits, const void* ids, const float* teacher,
+                           const float* teacher_lse, const int64_t* labels, const float* weights, float* loss,
+                           void* dlogits, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  return distill_run(d, 0, logits, ids, teacher, teacher_lse, labels, weights, loss, nullptr, nullptr, dlogits,
+                     workspace, workspace_bytes, stream);
+}
+
+kron_status_t kron_distill_fwd(const kron_distill_t* d, const void* logits, const void* ids, const float* teacher,
+                               const float* teacher_lse, const int64_t* labels, const float* weights, float* loss,
+                               float* stats, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  return distill_run(d, 1, logits, ids, teacher, teacher_lse, labels, weights, loss, stats, nullptr, nullptr,
+                     workspace, workspace_bytes, stream);
+}
+
+kron_status_t kron_distill_bwd(const kron_distill_t* d, const void* logits, const void* ids, const float* teacher,
+                               const float* teacher_lse, const int64_t* labels, const float* weights,
+                               const float* stats, const float* gout, void* dlogits, hipStream_t stream) {
+  return distill_run(d, 2, logits, ids, teacher, teacher_lse, labels, weights, nullptr, const_cast<float*>(stats),
+                     gout, dlogits, nullptr, 0, stream);
 }
 
 }  // extern "C"

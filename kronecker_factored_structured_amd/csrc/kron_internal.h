@@ -260,4 +260,41 @@ bool head_mfma_ok(int K, int C);
 int64_t head_rows_per_group(int64_t N);
 hipError_t launch_head(const HeadArgs& a, int G, hipStream_t s);
 
+// ---------------------------------------------------------------------------------
+// A teacher's top logits and the distillation loss (distill.hip, topk_logits.hip).
+// ---------------------------------------------------------------------------------
+constexpr int kDistillMaxK = 256;
+constexpr int kVocabMax = 1 << 18;
+constexpr int kDistillStats = 8;   // floats of a row's stats
+struct DistillArgs {
+  int64_t N, ld, ldd;
+  int32_t V, k;
+  int32_t bf16, ids64;
+  float T, alpha;
+  const void* logits;
+  const void* ids;
+  const float* teacher;
+  const float* teacher_lse;   // NULL: p over the kept tokens
+  const int64_t* labels;
+  const float* weights;       // NULL: 1 / N
+  const float* gout;          // the upstream gradient (mode 2)
+  float* stats;
+  float* lossrow;             // workspace: N
+  float* loss;
+  void* dlogits;
+};
+// mode 0: loss and gradient; 1: loss and stats; 2: gradient from stats
+hipError_t launch_distill(const DistillArgs& a, int mode, hipStream_t s);
+struct TopkArgs {
+  int64_t N, ld;
+  int32_t V, k;
+  int32_t bf16;
+  float T;
+  const void* logits;
+  int32_t* ids;
+  float* vals;
+  float* lse;
+};
+hipError_t launch_topk(const TopkArgs& a, hipStream_t s);
+
 }  // namespace kron
