@@ -368,6 +368,44 @@ kron_status_t kron_l1_penalty_grad(int64_t n, const float* S, float lam, const f
                                    hipStream_t stream);
 
 /*
+ * Gated Kronecker block: the feed-forward half of a gated language model whose two
+ * up-projections are Kronecker layers of one shape,
+ *   y = act(x W_0 + bias_0) o (x W_1 + bias_1),   W_f = sum_i kron(S_f o A_fi, B_fi)
+ * (W_0 is the gate).  The factors of both are one tensor each, the gate's first:
+ *   x [N, p*m]   S [2, p, q] or NULL   A [2, r, p, q]   B [2, r, m, n]
+ *   bias [2, q*n] or NULL              y [N, q*n]
+ * act: one of KRON_ACT_*.  dtype: KRON_F32, or KRON_BF16 for x, S, A, B, bias, dy, y and dx; the
+ * gradients of the factors and biases are fp32 for both.  Products are accurate to fp32 (bf16
+ * forward and dx: to 2^-16) and every output is rounded once.  A non-finite x gives non-finite
+ * outputs in its row.
+ *
+ * kron_glu_bwd, for the upstream gradient dy [N, q*n], recomputes both projections:
+ *   dx [N, p*m] or NULL (not computed)   dS [2, p, q] (NULL iff S is NULL)   dA [2, r, p, q]
+ *   dB [2, r, m, n]                      dbias [2, q*n] or NULL (not computed)
+ * relu'(0) = 0.  N == 0 is valid: the parameters' gradients are set to zero.
+ *
+ * shape->flags must be 0.  Limits: p, q, m, n <= KRON_GLU_MAX_SIDE, r <= KRON_GLU_MAX_RANK;
+ * other shapes return KRON_E_UNSUPPORTED.  The workspace (256-byte aligned, contents ignored) is
+ * kron_glu_workspace_bytes(shape, dtype, with_S, backward) bytes: the factors as matrix operands and,
+ * for the backward, the gradients of both projections, 8 bytes for each of the N*q*n values of y
+ * (n rounded up to 4), and partial sums.  Other rules as for kron_linear_fwd / kron_linear_bwd.
+ */
+#define KRON_ACT_SILU 0
+#define KRON_ACT_GELU 1        /* 0.5 v (1 + erf(v / sqrt 2)) */
+#define KRON_ACT_GELU_TANH 2   /* 0.5 v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) */
+#define KRON_ACT_RELU 3
+#define KRON_GLU_MAX_SIDE 64
+#define KRON_GLU_MAX_RANK 16
+size_t kron_glu_workspace_bytes(const kron_shape_t* shape, int32_t dtype, int32_t with_S, int32_t backward);
+kron_status_t kron_glu_fwd(const kron_shape_t* shape, int32_t act, int32_t dtype, const void* x, const void* S,
+                           const void* A, const void* B, const void* bias, void* y, void* workspace,
+                           size_t workspace_bytes, hipStream_t stream);
+kron_status_t kron_glu_bwd(const kron_shape_t* shape, int32_t act, int32_t dtype, const void* x, const void* S,
+                           const void* A, const void* B, const void* bias, const void* dy, void* dx, float* dS,
+                           float* dA, float* dB, float* dbias, void* workspace, size_t workspace_bytes,
+                           hipStream_t stream);
+
+/*
  * What is kept of a teacher's answer for distillation: of each row of logits z (N x V, row
  * stride ld >= V elements) the k largest values with their tokens, and
  *   lse[n] = log sum_v exp(z[n][v] / temperature)

@@ -9,7 +9,8 @@ from .api import (kron_adam_l1_step, kron_head_ce, kron_l1_penalty, kron_l1_pena
                   kron_linear_bwd_bf16, kron_linear_bwd_noalloc, kron_linear_bwd_bf16_workspace_bytes,
                   kron_linear_bwd_workspace_bytes, kron_linear_zcache_bytes, new_zcache, kron_linear_fwd, kron_linear_fwd_bf16, kron_relu_bwd, kron_van_loan, ks_chain, ks_matmul,
                   ks_matmul_bwd, ks_matmul_bwd_workspace_bytes, ks_matmul_out, layer_shape, kron_topk_logits, kron_distill,
-                  kron_distill_fwd, kron_distill_bwd)
+                  kron_distill_fwd, kron_distill_bwd, kron_glu_fwd, kron_glu_bwd, kron_glu_workspace_bytes,
+                  glu_shape)
 from .layers import KronLinear, KronMLPStep, KSLinear
 
 __all__ = [
@@ -19,4 +20,5 @@ __all__ = [
     "ks_matmul_bwd", "ks_matmul_bwd_workspace_bytes", "ks_chain", "kron_van_loan", "kron_relu_bwd",
     "kron_l1_penalty", "kron_l1_penalty_grad", "kron_linear_bwd_noalloc", "kron_linear_zcache_bytes", "new_zcache",
     "kron_topk_logits", "kron_distill", "kron_distill_fwd", "kron_distill_bwd",
+    "kron_glu_fwd", "kron_glu_bwd", "kron_glu_workspace_bytes", "glu_shape",
 ]

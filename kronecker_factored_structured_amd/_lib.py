@@ -31,6 +31,10 @@ KRON_SPARSE_ROWS = 4
 
 KRON_ACCUMULATE = 1
 
+KRON_ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
+KRON_GLU_MAX_SIDE = 64
+KRON_GLU_MAX_RANK = 16
+
 KRON_IDS_I64 = 1
 KRON_DISTILL_STATS = 8
 KRON_DISTILL_MAX_K = 256
@@ -46,7 +50,7 @@ EXPORTS = (
     "kron_van_loan_workspace_bytes", "kron_van_loan", "kron_relu_bwd", "kron_l1_penalty",
     "kron_l1_penalty_grad", "kron_linear_bwd_noalloc", "kron_linear_zcache_bytes", "kron_linear_fwd_save",
     "kron_linear_bwd_saved", "kron_topk_logits", "kron_distill_workspace_bytes", "kron_distill",
-    "kron_distill_fwd", "kron_distill_bwd",
+    "kron_distill_fwd", "kron_distill_bwd", "kron_glu_workspace_bytes", "kron_glu_fwd", "kron_glu_bwd",
 )
 
 KRON_NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -121,6 +125,9 @@ def lib() -> ctypes.CDLL:
             "kron_relu_bwd": (i32, [i64, vp, vp, vp, vp]),
             "kron_l1_penalty": (i32, [i32, pp, ctypes.POINTER(ctypes.c_int64), ctypes.c_float, vp, u32, vp]),
             "kron_l1_penalty_grad": (i32, [i64, vp, ctypes.c_float, vp, vp, vp]),
+            "kron_glu_workspace_bytes": (sz, [shp, i32, i32, i32]),
+            "kron_glu_fwd": (i32, [shp, i32, i32, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+            "kron_glu_bwd": (i32, [shp, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
             "kron_topk_logits": (i32, [i64, i32, i64, i32, i32, ctypes.c_float, vp, vp, vp, vp, vp]),
             "kron_distill_workspace_bytes": (sz, [dis]),
             "kron_distill": (i32, [dis, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),

@@ -12,7 +12,7 @@ from typing import Optional, Sequence
 import torch
 
 from . import _lib
-from ._lib import (KRON_ACCUMULATE, KRON_BF16, KRON_DISTILL_STATS, KRON_DX_RELU_MASK, KRON_F32, KRON_IDS_I64,
+from ._lib import (KRON_ACCUMULATE, KRON_ACTS, KRON_BF16, KRON_DISTILL_STATS, KRON_DX_RELU_MASK, KRON_F32, KRON_IDS_I64,
                    KRON_RELU_OUT, KRON_SPARSE_ROWS, KronDistill, KronShape, check)
 
 
@@ -486,6 +486,86 @@ def _dtype_code(t: torch.Tensor) -> int:
     if t.dtype == torch.bfloat16:
         return KRON_BF16
     raise ValueError(f"unsupported dtype {t.dtype}")
+
+
+def glu_shape(x_rows: int, S: Optional[torch.Tensor], A: torch.Tensor, B: torch.Tensor) -> KronShape:
+    """The shape of a gated block: A 2 x r x p x q and B 2 x r x m x n (the gate's factors first)."""
+    if A.dim() != 4 or B.dim() != 4 or A.shape[0] != 2 or B.shape[0] != 2:
+        raise ValueError("A must be 2 x r x p x q and B 2 x r x m x n")
+    _, r, p, q = A.shape
+    _, rb, m, n = B.shape
+    if rb != r:
+        raise ValueError(f"A has rank {r} but B has rank {rb}")
+    if S is not None and tuple(S.shape) != (2, p, q):
+        raise ValueError(f"S must be 2x{p}x{q}, got {tuple(S.shape)}")
+    return KronShape(int(x_rows), p, q, m, n, r, 0)
+
+
+def _glu_checks(x, S, A, B, bias, act):
+    dt = _dtype_code(x)
+    if act not in KRON_ACTS:
+        raise ValueError(f"act must be one of {sorted(KRON_ACTS)}, got {act!r}")
+    for t, nm in ((x, "x"), (S, "S"), (A, "A"), (B, "B"), (bias, "bias")):
+        _dev(t, nm, x.dtype)
+        if t is not None and t.device != x.device:
+            raise ValueError(f"{nm} is on {t.device}, expected {x.device}")
+    if x.dim() != 2:
+        raise ValueError(f"x must be N x p*m, got {tuple(x.shape)}")
+    shape = glu_shape(x.shape[0], S, A, B)
+    if x.shape[1] != shape.p * shape.m:
+        raise ValueError(f"x must be N x {shape.p * shape.m}, got {tuple(x.shape)}")
+    _need(bias, "bias", (2, shape.q * shape.n), x.dtype)
+    return dt, KRON_ACTS[act], shape
+
+
+def kron_glu_workspace_bytes(shape: KronShape, dtype: torch.dtype = torch.float32, with_S: bool = False,
+                             backward: bool = False) -> int:
+    dt = KRON_F32 if dtype == torch.float32 else KRON_BF16
+    return int(_lib.lib().kron_glu_workspace_bytes(ctypes.byref(shape), dt, int(with_S), int(backward)))
+
+
+def kron_glu_fwd(x: torch.Tensor, S: Optional[torch.Tensor], A: torch.Tensor, B: torch.Tensor,
+                 bias: Optional[torch.Tensor] = None, act: str = "silu", out: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The gated block y = act(x W_0 + bias_0) o (x W_1 + bias_1), W_f = sum_i kron(S_f o A_fi, B_fi): A is
+    2 x r x p x q, B 2 x r x m x n, S 2 x p x q or None, bias 2 x q*n or None (the gate's first), all float32 or
+    all bfloat16.  act: "silu", "gelu", "gelu_tanh" or "relu"."""
+    dt, code, shape = _glu_checks(x, S, A, B, bias, act)
+    dev = x.device
+    _need(out, "out", (x.shape[0], shape.q * shape.n), x.dtype, dev)
+    y = out if out is not None else torch.empty(x.shape[0], shape.q * shape.n, device=dev, dtype=x.dtype)
+    ws = _workspace(workspace, kron_glu_workspace_bytes(shape, x.dtype, S is not None), dev)
+    with torch.cuda.device(dev):
+        check("kron_glu_fwd", _lib.lib().kron_glu_fwd(
+            ctypes.byref(shape), code, dt, _ptr(x), _ptr(S), _ptr(A), _ptr(B), _ptr(bias), _ptr(y), _ptr(ws),
+            ctypes.c_size_t(ws.numel()), _stream(dev)))
+    return y
+
+
+def kron_glu_bwd(x: torch.Tensor, S: Optional[torch.Tensor], A: torch.Tensor, B: torch.Tensor,
+                 bias: Optional[torch.Tensor], dy: torch.Tensor, act: str = "silu", want_dx: bool = True,
+                 workspace: Optional[torch.Tensor] = None, outs: Optional[dict] = None) -> dict:
+    """Gradients of sum(dy * kron_glu_fwd(x, S, A, B, bias, act)): dict(dx in x's dtype; dS, dA, dB, dbias in
+    float32), None for dx where not asked and for dS, dbias without S, bias."""
+    dt, code, shape = _glu_checks(x, S, A, B, bias, act)
+    dev = x.device
+    N, p, q, m, n, r = x.shape[0], shape.p, shape.q, shape.m, shape.n, shape.r
+    _need(dy, "dy", (N, q * n), x.dtype, dev)
+    o = dict(outs or {})
+    want = dict(dx=((N, p * m), x.dtype, want_dx), dS=((2, p, q), torch.float32, S is not None),
+                dA=((2, r, p, q), torch.float32, True), dB=((2, r, m, n), torch.float32, True),
+                dbias=((2, q * n), torch.float32, bias is not None))
+    for k, (size, dtype, asked) in want.items():
+        _need(o.get(k), k, size, dtype, dev)
+        if k not in o:
+            o[k] = torch.empty(size, device=dev, dtype=dtype) if asked else None
+    ws = _workspace(workspace, kron_glu_workspace_bytes(shape, x.dtype, S is not None, True), dev)
+    with torch.cuda.device(dev):
+        check("kron_glu_bwd", _lib.lib().kron_glu_bwd(
+            ctypes.byref(shape), code, dt, _ptr(x), _ptr(S), _ptr(A), _ptr(B), _ptr(bias), _ptr(dy), _ptr(o["dx"]),
+            _ptr(o["dS"]), _ptr(o["dA"]), _ptr(o["dB"]), _ptr(o["dbias"]), _ptr(ws), ctypes.c_size_t(ws.numel()),
+            _stream(dev)))
+    return {k: o[k] for k in want}
 
 
 def _logit_rows(t: torch.Tensor, name: str) -> int:

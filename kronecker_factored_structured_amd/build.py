@@ -39,6 +39,7 @@ OBJECTS = [
     ("adam_l1.hip", [], "adam_l1"),
     ("head_ce.hip", [], "head_ce"),
     ("loss_terms.hip", [], "loss_terms"),
+    ("glu.hip", ["-mllvm", "-amdgpu-mfma-vgpr-form"], "glu"),
     ("distill.hip", [], "distill"),
     ("topk_logits.hip", [], "topk_logits"),
 ]

@@ -829,6 +829,102 @@ kron_status_t kron_head_ce(int64_t N, int32_t K, int32_t C, const float* h, cons
   return ok();
 }
 
+}  // extern "C"
+
+namespace {
+
+kron_status_t glu_check(const kron_shape_t* s, int32_t act, int32_t dtype) {
+  const kron_status_t st = check_shape(s);
+  if (st != KRON_OK) return st;
+  if (s->flags) return fail(KRON_E_ARG, "the gated block takes no shape flags (0x%x given)", s->flags);
+  if (s->p > KRON_GLU_MAX_SIDE || s->q > KRON_GLU_MAX_SIDE || s->m > KRON_GLU_MAX_SIDE || s->n > KRON_GLU_MAX_SIDE)
+    return fail(KRON_E_UNSUPPORTED, "p = %d, q = %d, m = %d or n = %d exceeds %d", s->p, s->q, s->m, s->n,
+                KRON_GLU_MAX_SIDE);
+  if (s->r > KRON_GLU_MAX_RANK) return fail(KRON_E_UNSUPPORTED, "r = %d exceeds %d", s->r, KRON_GLU_MAX_RANK);
+  if (act < KRON_ACT_SILU || act > KRON_ACT_RELU) return fail(KRON_E_ARG, "unknown activation %d", act);
+  if (dtype != KRON_F32 && dtype != KRON_BF16) return fail(KRON_E_DTYPE, "dtype %d", dtype);
+  return KRON_OK;
+}
+
+kron::GluArgs glu_args(const kron_shape_t* s, int32_t act, int32_t dtype) {
+  kron::GluArgs a{};
+  a.N = s->N; a.p = s->p; a.q = s->q; a.m = s->m; a.n = s->n; a.r = s->r;
+  a.act = act; a.bf16 = dtype == KRON_BF16;
+  return a;
+}
+
+size_t glu_workspace(const kron::GluArgs& a, bool backward) {
+  return (kron::glu_workspace_bytes(a, backward) + 255) & ~size_t(255);
+}
+
+kron_status_t glu_workspace_check(const void* workspace, size_t bytes, size_t need) {
+  if (!workspace || bytes < need) return fail(KRON_E_WORKSPACE, "workspace of %zu bytes given, %zu needed", bytes, need);
+  if (((uintptr_t)workspace & 255u) != 0) return fail(KRON_E_ALIGN, "workspace is not 256-byte aligned");
+  return KRON_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t kron_glu_workspace_bytes(const kron_shape_t* s, int32_t dtype, int32_t with_S, int32_t backward) {
+  if (glu_check(s, KRON_ACT_SILU, dtype) != KRON_OK) return 0;
+  kron::GluArgs a = glu_args(s, KRON_ACT_SILU, dtype);
+  a.S = with_S ? &a : nullptr;      // (only whether there is one counts)
+  return glu_workspace(a, backward != 0);
+}
+
+kron_status_t kron_glu_fwd(const kron_shape_t* s, int32_t act, int32_t dtype, const void* x, const void* S,
+                           const void* A, const void* B, const void* bias, void* y, void* workspace,
+                           size_t workspace_bytes, hipStream_t stream) {
+  kron_status_t st = glu_check(s, act, dtype);
+  if (st != KRON_OK) return st;
+  if (!A || !B) return fail(KRON_E_NULL, "A and B are required");
+  if (s->N > 0 && (!x || !y)) return fail(KRON_E_NULL, "x and y are required when N > 0");
+  kron::GluArgs a = glu_args(s, act, dtype);
+  a.x = x; a.S = S; a.A = A; a.B = B; a.bias = bias; a.y = y;
+  const size_t need = glu_workspace(a, false);
+  if ((st = glu_workspace_check(workspace, workspace_bytes, need)) != KRON_OK) return st;
+  const size_t es = a.bf16 ? 2 : 4, in = (size_t)s->p * s->m, out = (size_t)s->q * s->n;
+  const size_t pq = (size_t)s->p * s->q, mn = (size_t)s->m * s->n;
+  const Range ins[5] = {{x, (size_t)s->N * in * es, "x"}, {S, 2 * pq * es, "S"}, {A, 2 * s->r * pq * es, "A"},
+                        {B, 2 * s->r * mn * es, "B"},     {bias, 2 * out * es, "bias"}};
+  const Range outs[2] = {{y, (size_t)s->N * out * es, "y"}, {workspace, need, "workspace"}};
+  if ((st = check_align(ins, 5)) != KRON_OK || (st = check_align(outs, 2)) != KRON_OK) return st;
+  if ((st = check_alias(outs, 2, ins, 5)) != KRON_OK) return st;
+  if (s->N == 0) return ok();
+  const hipError_t e = kron::launch_glu_fwd(a, workspace, stream);
+  if (e != hipSuccess) return hip_fail(e, "kron_glu_fwd launch");
+  return ok();
+}
+
+kron_status_t kron_glu_bwd(const kron_shape_t* s, int32_t act, int32_t dtype, const void* x, const void* S,
+                           const void* A, const void* B, const void* bias, const void* dy, void* dx, float* dS,
+                           float* dA, float* dB, float* dbias, void* workspace, size_t workspace_bytes,
+                           hipStream_t stream) {
+  kron_status_t st = glu_check(s, act, dtype);
+  if (st != KRON_OK) return st;
+  if (!A || !B || !dA || !dB) return fail(KRON_E_NULL, "A, B, dA and dB are required");
+  if ((S == nullptr) != (dS == nullptr)) return fail(KRON_E_NULL, "dS must be given exactly when S is");
+  if (s->N > 0 && (!x || !dy)) return fail(KRON_E_NULL, "x and dy are required when N > 0");
+  kron::GluArgs a = glu_args(s, act, dtype);
+  a.x = x; a.S = S; a.A = A; a.B = B; a.bias = bias; a.dy = dy;
+  a.dx = s->N > 0 ? dx : nullptr; a.dS = dS; a.dA = dA; a.dB = dB; a.dbias = dbias;
+  const size_t need = glu_workspace(a, true);
+  if ((st = glu_workspace_check(workspace, workspace_bytes, need)) != KRON_OK) return st;
+  const size_t es = a.bf16 ? 2 : 4, in = (size_t)s->p * s->m, out = (size_t)s->q * s->n;
+  const size_t pq = (size_t)s->p * s->q, mn = (size_t)s->m * s->n;
+  const Range ins[6] = {{x, (size_t)s->N * in * es, "x"}, {S, 2 * pq * es, "S"}, {A, 2 * s->r * pq * es, "A"},
+                        {B, 2 * s->r * mn * es, "B"},     {bias, 2 * out * es, "bias"}, {dy, (size_t)s->N * out * es, "dy"}};
+  const Range outs[6] = {{dx, (size_t)s->N * in * es, "dx"}, {dS, 2 * pq * 4, "dS"}, {dA, 2 * s->r * pq * 4, "dA"},
+                         {dB, 2 * s->r * mn * 4, "dB"},      {dbias, 2 * out * 4, "dbias"}, {workspace, need, "workspace"}};
+  if ((st = check_align(ins, 6)) != KRON_OK || (st = check_align(outs, 6)) != KRON_OK) return st;
+  if ((st = check_alias(outs, 6, ins, 6)) != KRON_OK) return st;
+  const hipError_t e = kron::launch_glu_bwd(a, workspace, stream);
+  if (e != hipSuccess) return hip_fail(e, "kron_glu_bwd launch");
+  return ok();
+}
+
 kron_status_t kron_topk_logits(int64_t N, int32_t V, int64_t ld, int32_t k, int32_t dtype, float temperature,
                                const void* logits, int32_t* ids, float* vals, float* lse, hipStream_t stream) {
   if (N < 0 || N > kMaxRows) return fail(KRON_E_SHAPE, "N = %lld out of range", (long long)N);

@@ -261,6 +261,32 @@ int64_t head_rows_per_group(int64_t N);
 hipError_t launch_head(const HeadArgs& a, int G, hipStream_t s);
 
 // ---------------------------------------------------------------------------------
+// Gated Kronecker block (glu.hip): the gate's factors first, then the up-projection's.
+// ---------------------------------------------------------------------------------
+constexpr int kGluMaxSide = 64;
+constexpr int kGluMaxRank = 16;
+struct GluArgs {
+  int64_t N;
+  int32_t p, q, m, n, r;
+  int32_t act, bf16;
+  const void* x;
+  const void* S;      // NULL: all ones
+  const void* A;
+  const void* B;
+  const void* bias;   // NULL: none
+  const void* dy;
+  void* y;
+  void* dx;           // NULL: not computed
+  float* dS;
+  float* dA;
+  float* dB;
+  float* dbias;       // NULL: not computed
+};
+size_t glu_workspace_bytes(const GluArgs& a, bool backward);
+hipError_t launch_glu_fwd(const GluArgs& a, void* ws, hipStream_t s);
+hipError_t launch_glu_bwd(const GluArgs& a, void* ws, hipStream_t s);
+
+// ---------------------------------------------------------------------------------
 // A teacher's top logits and the distillation loss (distill.hip, topk_logits.hip).
 // ---------------------------------------------------------------------------------
 constexpr int kDistillMaxK = 256;
