@@ -8,14 +8,21 @@
 //   loss  = sum_n w_n (alpha T^2 KD_n + (1 - alpha) (logsumexp(z_n) - z_n[label]))
 //   dKD/dz_v = (M q_v - p_v) / T           on the kept tokens,  M = sum_j p_j + p_t
 //            = q_v (M - p_t / q_t) / T     elsewhere (p_t = 0 without a tail)
-// One workgroup per row.  The row stays in registers between its one read and the write of its
-// gradient; only rows longer than the registers hold are read twice more.  What bounds it is
-// memory: V logits in, V gradients out.
 //
-// The kept tokens are marked in a bitmap of the row in LDS.  It tells the sum over the tail
-// which exponentials to leave out (q_t as a sum of its own: total minus kept would cancel), it
-// finds repeated tokens, and it keeps the thread that writes a vector of gradients off the kept
-// tokens, which their own threads write: no address is written twice, so nothing waits.
+// Many rows: one workgroup per row (distill_row_kernel).  The row stays in registers between its one
+// read and the write of its gradient: V logits in, V gradients out is all the traffic, and what bounds it.
+// Few rows, rows longer than the registers hold, and the two-call form: chunks of rows, one workgroup
+// each.  distill_part_kernel takes a chunk's maximum and sums, distill_emit_kernel joins a row's chunks
+// and writes a chunk's gradient; the logits are read twice, the second time mostly from cache.
+//
+// The kept tokens are marked in a bitmap in LDS.  It tells the sum over the tail which exponentials
+// to leave out (q_t as a sum of its own: total minus kept would cancel), it finds repeated tokens,
+// and it keeps the thread that writes a vector of gradients off the kept tokens, which their own
+// threads write: no address is written twice, so nothing waits.
+//
+// Exponentials are 2^(z s - c) with c = m s rounded once: the rounding of c cancels in every
+// softmax.  One exponential serves a row that needs one temperature (KD or CE alone, or T = 1);
+// at T = 2 the one of CE is the square of KD's; otherwise CE takes a second one (`two`).
 #include "kron_internal.h"
 #include "row_tile.h"
 
@@ -24,22 +31,123 @@ namespace {
 
 constexpr int kMaxK = kDistillMaxK;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr double kLn2 = 0.69314718055994531;
 
 // stats of a row (8 floats), from the forward for the backward
-enum { kStM = 0, kStInvT, kStInv1, kStBase, kStMass, kStTa, kStTb, kStBad, kStN };
+enum { kStM = 0, kStInvT, kStInv1, kStBase, kStMass, kStTa, kStTb, kStN = kDistillStats };
 
 __device__ inline int64_t kept_id(const DistillArgs& a, int64_t row, int j) {
   const int64_t i = row * a.k + j;
   return a.ids64 ? ((const int64_t*)a.ids)[i] : (int64_t)((const int32_t*)a.ids)[i];
 }
 
-// The packed row as new values: what one pass unpacked is not kept for the next (it would take
-// twice the row's registers or more).
-template <int NV>
-__device__ inline void fresh(u32x4 (&reg)[NV]) {
+// e^x for x <= 0 in 64 bits: 2^n times a polynomial of the rest, |r| <= ln 2 / 2 (the series to the
+// 13th power is exact to 2^-58).  Few registers, while the row holds most of them.
+__device__ inline double exp64(double x) {
+  if (x < -700.0) return 0.0;
+  const double n = rint(x * 1.4426950408889634);
+  const double r = fma(n, -1.9082149292705877e-10, fma(n, -0.6931471803691238, x));
+  double p = 1.0 / 6227020800.0;
+  const double c[13] = {1.0 / 479001600.0, 1.0 / 39916800.0, 1.0 / 3628800.0, 1.0 / 362880.0, 1.0 / 40320.0,
+                        1.0 / 5040.0,      1.0 / 720.0,      1.0 / 120.0,     1.0 / 24.0,     1.0 / 6.0,
+                        0.5,               1.0,              1.0};
 #pragma unroll
-  for (int i = 0; i < NV; ++i) asm volatile("" : "+v"(reg[i]));
+  for (int i = 0; i < 13; ++i) p = fma(p, r, c[i]);
+  return ldexp(p, (int)n);
 }
+
+// Bits of vector j's kept tokens: the bitmap counts from a vector's first element, so a vector's bits
+// are one byte (bf16) or half of one.
+template <int VE>
+__device__ inline uint32_t kept_bits(const uint32_t* bits, int j) {
+  const uint8_t* b = reinterpret_cast<const uint8_t*>(bits);
+  return VE == 8 ? b[j] : (b[j >> 1] >> (4 * (j & 1))) & 15u;
+}
+
+// How the exponentials of a row are taken.
+struct Scale {
+  bool kd, ce;
+  int two;          // CE's exponential: 0 the first one, 1 its square, 2 one of its own
+  float invT, sA;   // of the first exponential
+  float m0, cA, cB; // the maximum, and the shifts
+  bool huge;
+
+  __device__ Scale(const DistillArgs& a) {
+    kd = a.alpha > 0.f;
+    ce = a.alpha < 1.f;
+    invT = 1.f / a.T;
+    sA = kd ? invT * kLog2e : kLog2e;
+    two = !(kd && ce) || a.T == 1.f ? 0 : a.T == 2.f ? 1 : 2;
+  }
+  // Where m s overflows (a row of the type's lowest or largest values), values differ from the maximum
+  // by nothing or by more than any exponential holds: they become 0 and -infinity.
+  __device__ void at(float m) {
+    m0 = m;
+    huge = fabsf(m) < INFINITY && !(fabsf(m) * fmaxf(sA, kLog2e) < 1e38f);
+    if (huge) m = 0.f;
+    cA = m * sA;
+    cB = two == 1 ? 2.f * cA : m * kLog2e;
+  }
+  __device__ float place(float x) const { return huge ? (x == m0 ? 0.f : -INFINITY) : x; }
+  __device__ float first(float x) const { return __builtin_amdgcn_exp2f(fmaf(x, sA, -cA)); }
+  __device__ float second(float x) const { return __builtin_amdgcn_exp2f(fmaf(x, kLog2e, -cB)); }
+};
+
+template <bool BF>
+struct Sums {      // of first exponentials off the kept tokens, and of second ones
+  using Tile = RowTile<BF>;
+  static constexpr int VE = Tile::VE;
+  float sr = 0.f, s1 = 0.f;
+  __device__ void add(const Scale& c, const u32x4& v, uint32_t kept) {
+    float x[VE], y[VE];
+    Tile::values(v, x);
+    if (c.huge) {
+#pragma unroll
+      for (int e = 0; e < VE; ++e) x[e] = c.place(x[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < VE; ++e) y[e] = c.first(x[e]);
+    if (c.two == 1) {
+#pragma unroll
+      for (int e = 0; e < VE; ++e) s1 = fmaf(y[e], y[e], s1);
+    } else if (c.two == 2) {
+#pragma unroll
+      for (int e = 0; e < VE; ++e) s1 += c.second(x[e]);
+    }
+    if (kept != 0u) {
+#pragma unroll
+      for (int e = 0; e < VE; ++e) y[e] = (kept >> e) & 1u ? 0.f : y[e];
+    }
+#pragma unroll
+    for (int e = 0; e < VE; ++e) sr += y[e];
+  }
+};
+
+template <bool BF>
+__device__ inline float vec_max(const u32x4& v) {
+  float x[RowTile<BF>::VE];
+  RowTile<BF>::values(v, x);
+  float m = x[0];
+#pragma unroll
+  for (int e = 1; e < RowTile<BF>::VE; ++e) m = fmaxf(m, x[e]);
+  return m;
+}
+
+// Shared memory of a workgroup of NT threads; thread j < k has the row's kept token j.
+template <int NT>
+struct Shared {
+  float red[NT / 64], redT[NT / 64], red1[NT / 64], redk[NT / 64], reds[NT / 64];
+  double redp[NT / 64], redd[NT / 64];
+  int32_t kid[kMaxK];
+  float kp[kMaxK];
+  int flag[4];        // a repeated token, a bad id, a used slot, the label is kept
+};
+
+struct Kept {
+  int64_t id = -1;
+  float t = 0.f, z = 0.f;
+  bool have = false, own = false, near = false;      // near: inside this workgroup's chunk
+};
 
 template <int NT>
 __device__ inline float block_max(float v, float* red) {
@@ -52,356 +160,613 @@ __device__ inline float block_max(float v, float* red) {
   return r;
 }
 
-// MODE 0: loss and gradient;  1: loss and stats;  2: gradient from stats
-template <bool BF, int NT, int NV, bool RES, int MODE>
-__global__ __launch_bounds__(NT) void distill_kernel(DistillArgs a) {
-  using Tile = RowTile<BF>;
-  constexpr int VE = Tile::VE;
-  constexpr int NW = NT / 64;
-  extern __shared__ uint32_t bits[];      // bitmap of the kept tokens, (V + 31) / 32 + 1 words
-  __shared__ float red[NW], redT[NW], red1[NW], redk[NW];
-  __shared__ double redp[NW], redd[NW];
-  __shared__ int32_t kid[kMaxK];
-  __shared__ float kp[kMaxK];             // p of the kept tokens
-  __shared__ int sflag[4];                // a repeated token, a bad id, a used slot, the label is kept
-
-  const int64_t row = blockIdx.x;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const float w = a.weights ? a.weights[row] : 1.f / (float)a.N;
-  const Tile z(a.logits, row, a.ld, a.V);
-  const int nvec = z.vectors();
-  if (w == 0.f) {      // a row without weight: nothing of it is read
-    if (MODE != 2 && tid == 0) a.lossrow[row] = 0.f;
-    if (MODE == 1 && tid < kStN) a.stats[row * kStN + tid] = 0.f;
-    if (MODE != 1) {
-      const Tile o(a.dlogits, row, a.ldd, a.V);
-      const int no = o.vectors();
-      for (int j = tid; j < no; j += NT) {
-        if (o.inside(j)) {
-          *reinterpret_cast<u32x4*>(o.base + (uint64_t)j * 16) = u32x4{0u, 0u, 0u, 0u};
-        } else {
-          for (int i = 0; i < VE; ++i)
-            if (o.first(j) + i >= 0 && o.first(j) + i < a.V) o.put(o.first(j) + i, 0.f);
-        }
-      }
-    }
-    return;
-  }
-
-  u32x4 reg[RES ? NV : 1];
-  if (RES) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) reg[RES ? i : 0] = z.load(tid + i * NT);
-  }
-  const float invT = 1.f / a.T, sT = invT * kLog2e;
-  const bool kd = a.alpha > 0.f, ce = a.alpha < 1.f;
-  const int nwords = (a.V + 31) / 32 + 1;
+// Clears the bitmap of the chunk [bit0, bit0 + 32 nwords) and marks the row's kept tokens in it
+// (positions are token + off).  A barrier has to follow; then settle().
+template <int NT, bool BF>
+__device__ inline Kept mark_kept(const DistillArgs& a, int64_t row, const RowTile<BF>& z, int64_t lab, uint32_t* bits,
+                                 int bit0, int nwords, Shared<NT>& sh) {
+  const int tid = threadIdx.x;
   for (int i = tid; i < nwords; i += NT) bits[i] = 0u;
-  if (tid < 4) sflag[tid] = 0;
+  if (tid < 4) sh.flag[tid] = 0;
   __syncthreads();
-
-  // the kept tokens: thread j < k has token j
-  const int64_t lab = ce ? a.labels[row] : -1;
-  int64_t id = -1;
-  float t = 0.f, zk = 0.f;
-  bool have = false, own = false;
-  if (kd && tid < a.k) {
-    id = kept_id(a, row, tid);
-    t = a.teacher[row * a.k + tid];
-    if (id >= a.V) sflag[1] = 1;
-    have = id >= 0 && id < a.V;
-    if (have) {
-      if (!(t == -INFINITY)) sflag[2] = 1;      // (a teacher of -infinity has p = 0)
-      zk = z.at((int)id);
-      const uint32_t bit = 1u << (id & 31);
-      own = !(atomicOr(&bits[id >> 5], bit) & bit);
-      if (!own) sflag[0] = 1;
-      if (id == lab) sflag[3] = 1;
+  Kept k;
+  if (tid < a.k) {
+    k.id = kept_id(a, row, tid);
+    k.t = a.teacher[row * a.k + tid];
+    if (k.id >= a.V) sh.flag[1] = 1;
+    k.have = k.id >= 0 && k.id < a.V;
+    if (k.have) {
+      if (!(k.t == -INFINITY)) sh.flag[2] = 1;      // (a teacher of -infinity has p = 0)
+      const int at = (int)k.id + z.off - bit0;
+      k.near = at >= 0 && at < 32 * nwords;
+      k.own = true;
+      if (k.near) {
+        const uint32_t bit = 1u << (at & 31);
+        k.own = !(atomicOr(&bits[at >> 5], bit) & bit);
+        if (!k.own) sh.flag[0] = 1;
+      }
+      if (k.id == lab) sh.flag[3] = 1;
     }
-    kid[tid] = have ? (int32_t)id : -1;
+    sh.kid[tid] = k.have ? (int32_t)k.id : -1;
   }
-  // of a token given twice the first slot owns it, whichever came first to the bitmap
-  auto settle = [&]() {
-    if (!sflag[0] || !have) return;
-    own = true;
-    for (int l = 0; l < tid; ++l) own = own && kid[l] != (int32_t)id;
-  };
-  const bool labok = !ce || (lab >= 0 && lab < a.V);
+  return k;
+}
+// Of a token given twice the first slot owns it, whichever came first to the bitmap.
+template <int NT>
+__device__ inline void settle(Kept& k, const Shared<NT>& sh) {
+  if (!sh.flag[0] || !k.near) return;
+  k.own = true;
+  for (int l = 0; l < (int)threadIdx.x; ++l) k.own = k.own && sh.kid[l] != (int32_t)k.id;
+}
 
-  float m, invsT, invs1 = 0.f, base, mass, ta, tb;
-  if (MODE == 2) {
-    const float* st = a.stats + row * kStN;
-    m = st[kStM]; invsT = st[kStInvT]; invs1 = st[kStInv1];
-    base = st[kStBase]; mass = st[kStMass]; ta = st[kStTa]; tb = st[kStTb];
-    __syncthreads();
-    settle();
-  } else {
-    // the row's maximum
-    float mx = -INFINITY;
-    if (RES) {
+// What the gradient needs of a row.
+struct RowStats {
+  float invsT, invs1, base, mass, ta, tb;
+};
+
+// The row's sums into its statistics.  tr, t1: the sums off the kept tokens and of the second
+// exponentials (without one: anything); k.own marks each token once over the whole row.  Thread 0 leaves
+// what the loss needs in a.rows[row].  zl: the label's logit (thread 0, if the label is one).
+template <int NT>
+__device__ inline RowStats finish_row(const DistillArgs& a, int64_t row, float w, const Scale& c, const Kept& k, float tr,
+                                      float t1, bool labok, float zl, Shared<NT>& sh) {
+  constexpr int NW = NT / 64;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  RowStats r;
+  const bool tail = a.teacher_lse != nullptr;
+  float tm = -INFINITY;
+  if (c.kd && !tail) {
+    tm = wave_max(k.have ? k.t : -INFINITY);
+    if (lane == 0) sh.redk[wave] = tm;
+  }
+  const float sk = wave_sum(k.own ? c.first(k.z) : 0.f);
+  if (lane == 0) sh.reds[wave] = sk;
+  __syncthreads();
+  float tk = 0.f;
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int e = 0; e < VE; ++e) mx = fmaxf(mx, Tile::value(reg[RES ? i : 0], e));
+  for (int v = 0; v < NW; ++v) tk += sh.reds[v];
+  const float total = tr + tk;
+  if (c.two == 0) t1 = total;
+  r.invsT = 1.f / total;
+  r.invs1 = 1.f / t1;
+  r.ta = 0.f;
+  r.tb = 1.f;
+  r.mass = r.base = 1.f;
+  double kl = 0.0, pmass = 0.0, ptail = 0.0;
+  if (c.kd) {
+    if (tail) {
+      r.ta = a.teacher_lse[row];
     } else {
-      for (int j = tid; j < nvec; j += NT) {
-        const u32x4 v = z.load(j);
+      tm = sh.redk[0];
 #pragma unroll
-        for (int e = 0; e < VE; ++e) mx = fmaxf(mx, Tile::value(v, e));
-      }
-    }
-    m = block_max<NT>(mx, red);      // (its barrier also completes the bitmap)
-    settle();
-    fresh(reg);
-    // sums of exp((z - m) / T) off and on the kept tokens, and of exp(z - m)
-    float sr = 0.f, sk = 0.f, s1 = 0.f;
-    auto add = [&](const u32x4& v, int j) {
-      const int e0 = z.first(j);
-      uint32_t b = 0u;
-      if (kd && e0 < a.V) {
-        const int f = e0 < 0 ? 0 : e0;
-        const uint64_t two = (uint64_t)bits[f >> 5] | ((uint64_t)bits[(f >> 5) + 1] << 32);
-        b = (uint32_t)(two >> (f & 31)) << (f - e0);
-      }
-      float p = 0.f, o = 0.f;
-#pragma unroll
-      for (int e = 0; e < VE; ++e) {
-        const float d = Tile::value(v, e) - m;
-        if (kd) {
-          const float x = __builtin_amdgcn_exp2f(d * sT);
-          p += (b >> e) & 1u ? 0.f : x;
-        }
-        if (ce) o += __builtin_amdgcn_exp2f(d * kLog2e);
-      }
-      sr += p;
-      s1 += o;
-    };
-    if (RES) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (tid + i * NT < nvec) add(reg[RES ? i : 0], tid + i * NT);
-    } else {
-      for (int j = tid; j < nvec; j += NT) add(z.load(j), j);
-    }
-    if (own) sk = __builtin_amdgcn_exp2f((zk - m) * sT);
-    // the teacher's p: over the kept tokens, or with the rest of the vocabulary
-    const bool tail = a.teacher_lse != nullptr;
-    float tm = -INFINITY;
-    if (kd && !tail) {
-      tm = have ? t : -INFINITY;
-      tm = wave_max(tm);
-      if (lane == 0) redk[wave] = tm;
-    }
-    sr = wave_sum(sr);
-    s1 = wave_sum(s1);
-    sk = wave_sum(sk);
-    if (lane == 0) { red1[wave] = s1; redT[wave] = sr; redp[wave] = (double)sk; }
-    __syncthreads();
-    float tr = 0.f, tk = 0.f, t1 = 0.f;
-#pragma unroll
-    for (int v = 0; v < NW; ++v) { tr += redT[v]; tk += (float)redp[v]; t1 += red1[v]; }
-    const float total = tr + tk;
-    invsT = 1.f / total;
-    invs1 = 1.f / t1;
-    double pj = 0.0, logp = 0.0;
-    if (kd) {
-      if (tail) {
-        ta = a.teacher_lse[row];
-        tb = 1.f;
-      } else {
-        tm = redk[0];
-#pragma unroll
-        for (int v = 1; v < NW; ++v) tm = fmaxf(tm, redk[v]);
-        ta = sflag[2] ? tm * invT : 0.f;
-        tb = 1.f;
-      }
-    } else {
-      ta = 0.f; tb = 1.f;
+      for (int v = 1; v < NW; ++v) tm = fmaxf(tm, sh.redk[v]);
+      r.ta = sh.flag[2] ? tm * c.invT : 0.f;
     }
     // the masses of the teacher are sums next to one: 64 bits, one exponential a thread
-    if (have && !(t == -INFINITY)) {
-      logp = (double)t / (double)a.T - (double)(tail ? ta : 0.f);
-      if (!tail) logp = ((double)t - (double)tm) / (double)a.T;
-      pj = exp(logp);
+    double pj = 0.0, logp = 0.0;
+    if (k.have && !(k.t == -INFINITY)) {
+      logp = tail ? (double)k.t / (double)a.T - (double)r.ta : ((double)k.t - (double)tm) / (double)a.T;
+      pj = exp64(logp);
     }
-    double sp = wave_sum(pj);
-    __syncthreads();
-    if (lane == 0) redp[wave] = sp;
+    // sum p and sum p (log p - log q), log q short of the sum's logarithm
+    const double lq = ((double)k.z * (double)c.sA - (double)c.cA) * kLn2;
+    double term = pj != 0.0 ? pj * (logp - lq) : 0.0;
+    const double sp = wave_sum(pj);
+    term = wave_sum(term);
+    if (lane == 0) { sh.redp[wave] = sp; sh.redd[wave] = term; }
     __syncthreads();
     double psum = 0.0;
 #pragma unroll
-    for (int v = 0; v < NW; ++v) psum += redp[v];
-    if (kd && !tail && sflag[2]) {
-      tb = (float)(1.0 / psum);
-      pj /= psum;
-      logp -= log(psum);
-    }
-    // the row's divergence
-    const double ltot = (double)logf(total);
-    double term = 0.0;
-    if (have && pj != 0.0) term = pj * (logp - ((double)(zk - m) * (double)invT - ltot));
-    term = wave_sum(term);
-    if (lane == 0) redd[wave] = term;
-    __syncthreads();
-    double kl = 0.0;
-#pragma unroll
-    for (int v = 0; v < NW; ++v) kl += redd[v];
-    mass = 1.f;
-    base = 1.f;
-    if (kd) {
-      if (!tail) {
-        mass = base = sflag[2] ? 1.f : 0.f;
-      } else {
-        // (with every token kept there is no tail, whatever rounding leaves of its mass)
-        const bool rest = psum < 1.0 && !(tr == 0.f && a.k >= a.V);
-        const double pt = rest ? 1.0 - psum : 0.0;
-        mass = (float)(psum + pt);
-        base = mass;
-        if (rest) {
-          const double qt = (double)tr / (double)total;
-          kl += pt * (log(pt) - log(qt));
-          base = (float)((double)mass - pt / qt);
-        }
-      }
-    }
-    const bool bad = sflag[1] || !labok;
-    if (tid == 0) {
-      double l = 0.0;
-      if (kd) l += (double)a.alpha * (double)a.T * (double)a.T * kl;
-      if (ce && labok) l += (1.0 - (double)a.alpha) * ((double)logf(t1) - (double)(z.at((int)lab) - m));
-      a.lossrow[row] = bad ? __builtin_nanf("") : (float)((double)w * l);
-    }
-    if (bad) invsT = invs1 = __builtin_nanf("");
-    if (MODE == 1) {
-      if (tid == 0) {
-        float* st = a.stats + row * kStN;
-        st[kStM] = m; st[kStInvT] = invsT; st[kStInv1] = invs1;
-        st[kStBase] = base; st[kStMass] = mass; st[kStTa] = ta; st[kStTb] = tb; st[kStBad] = bad ? 1.f : 0.f;
-      }
-      return;
+    for (int v = 0; v < NW; ++v) { psum += sh.redp[v]; kl += sh.redd[v]; }
+    if (!tail) {
+      r.mass = r.base = sh.flag[2] ? 1.f : 0.f;
+      r.tb = sh.flag[2] ? (float)(1.0 / psum) : 1.f;
+      pmass = sh.flag[2] ? psum : 0.0;
+    } else {
+      // (with every token kept there is no tail, whatever rounding leaves of its mass)
+      const bool rest = psum < 1.0 && !(tr == 0.f && a.k >= a.V);
+      ptail = rest ? 1.0 - psum : 0.0;
+      pmass = psum;
+      r.mass = (float)(psum + ptail);
+      r.base = rest ? (float)((double)r.mass - ptail * ((double)total / (double)tr)) : r.mass;
     }
   }
+  const bool bad = sh.flag[1] || !labok;
+  if (threadIdx.x == 0) {
+    DistillRow o;
+    o.kl = kl;
+    o.psum = pmass;
+    o.pt = ptail;
+    o.total = total;
+    o.rest = tr;
+    o.t1 = t1;
+    // the label's z s - c of CE's exponential
+    o.zl = !c.ce || !labok ? 0.f
+           : c.two == 0    ? fmaf(zl, c.sA, -c.cA)
+                           : fmaf(zl, c.two == 1 ? 2.f * c.sA : kLog2e, -c.cB);
+    o.w = bad ? __builtin_nanf("") : w;
+    o.pad_ = 0.f;
+    a.rows[row] = o;
+  }
+  if (bad) r.invsT = r.invs1 = __builtin_nanf("");
+  return r;
+}
 
-  // the gradient; kc = alpha w T and cc = (1 - alpha) w, times the upstream gradient
-  const float up = MODE == 2 ? w * a.gout[0] : w;
-  const float kc = kd ? a.alpha * a.T * up * invsT : 0.f, cc = ce ? (1.f - a.alpha) * up : 0.f;
-  const float kb = kc * base, c1 = cc * invs1;
-  if (kd && tid < a.k)
-    kp[tid] = have ? __builtin_amdgcn_exp2f((t * invT - ta) * kLog2e) * tb : 0.f;
-  __syncthreads();
-  const Tile o(a.dlogits, row, a.ldd, a.V);
-  const bool same = z.off == o.off;      // both rows start at the same place of a vector
-  float zl = 0.f;
-  const bool putlab = ce && labok && tid == 0 && !sflag[3];
-  if (putlab) zl = z.at((int)lab);
-  // in place, every gather of the row is done before the first store
-  float mine = 0.f;
-  if (own) {
-    float p = kp[tid];
-    if (sflag[0])      // (the owner is the first slot)
-      for (int l = tid + 1; l < a.k; ++l) p += kid[l] == (int32_t)id ? kp[l] : 0.f;
-    const float d = zk - m;
-    const float pk = a.alpha * a.T * up * p;
-    mine = __builtin_amdgcn_exp2f(d * sT) * kc * mass - pk;
-    if (ce) mine += __builtin_amdgcn_exp2f(d * kLog2e) * c1 - (id == lab ? cc : 0.f);
+// The gradient's factors of a row, `up` its weight times the upstream gradient.
+struct Grad {
+  float kw, cc, kc, kb, c1;
+  __device__ Grad(const DistillArgs& a, const Scale& c, const RowStats& r, float up) {
+    kw = c.kd ? a.alpha * a.T * up : 0.f;
+    cc = c.ce ? (1.f - a.alpha) * up : 0.f;
+    kc = kw * r.invsT;
+    kb = kc * r.base;
+    c1 = cc * r.invs1;
   }
-  float labv = 0.f;
-  if (putlab) {
-    const float d = zl - m;
-    labv = (kd ? __builtin_amdgcn_exp2f(d * sT) * kb : 0.f) + __builtin_amdgcn_exp2f(d * kLog2e) * c1 - cc;
-    atomicOr(&bits[lab >> 5], 1u << (lab & 31));
+  // of a value: kq times the first exponential, and CE's part
+  __device__ float one(const Scale& c, float x, float kq) const {
+    const float y = c.first(x);
+    if (c.two == 0) return y * (kq + c1);
+    if (c.two == 1) return y * fmaf(y, c1, kq);
+    return fmaf(y, kq, c.second(x) * c1);
   }
-  // the values above wait for the gathered logits: written to LDS, they are there before any
-  // thread passes the barrier
-  if (own) kp[tid] = mine;
-  if (putlab) redT[0] = labv;
-  __syncthreads();
-  if (own) o.put((int)id, mine);
-  if (putlab) o.put((int)lab, labv);
-  auto emit = [&](const u32x4& v, int j) {
-    const int e0 = z.first(j);
-    if (e0 >= a.V) return;
-    const int f = e0 < 0 ? 0 : e0;
-    const uint64_t two = (uint64_t)bits[f >> 5] | ((uint64_t)bits[(f >> 5) + 1] << 32);
-    const uint32_t b = ((uint32_t)(two >> (f & 31)) << (f - e0)) & ((1u << VE) - 1u);
-    float g[VE];
+  template <bool BF>
+  __device__ void vec(const Scale& c, const u32x4& v, float (&g)[RowTile<BF>::VE]) const {
+    constexpr int VE = RowTile<BF>::VE;
+    float x[VE];
+    RowTile<BF>::values(v, x);
+    if (c.huge) {
 #pragma unroll
-    for (int e = 0; e < VE; ++e) {
-      const float d = Tile::value(v, e) - m;
-      float x = 0.f;
-      if (kd) x = __builtin_amdgcn_exp2f(d * sT) * kb;
-      if (ce) x = fmaf(__builtin_amdgcn_exp2f(d * kLog2e), c1, x);
-      g[e] = x;
+      for (int e = 0; e < VE; ++e) x[e] = c.place(x[e]);
     }
-    if (same && b == 0u && z.inside(j)) {
-      u32x4 r;
+    if (c.two == 0) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        r[i] = BF ? (bf16_rne(g[(2 * i) % VE]) | (bf16_rne(g[(2 * i + 1) % VE]) << 16)) : __float_as_uint(g[i]);
-      *reinterpret_cast<u32x4*>(o.base + (uint64_t)j * 16) = r;
+      for (int e = 0; e < VE; ++e) g[e] = c.first(x[e]) * (kb + c1);
+    } else if (c.two == 1) {
+#pragma unroll
+      for (int e = 0; e < VE; ++e) {
+        const float y = c.first(x[e]);
+        g[e] = y * fmaf(y, c1, kb);
+      }
     } else {
 #pragma unroll
-      for (int e = 0; e < VE; ++e)
-        if (e0 + e >= 0 && e0 + e < a.V && !((b >> e) & 1u)) o.put(e0 + e, g[e]);
+      for (int e = 0; e < VE; ++e) g[e] = fmaf(c.first(x[e]), kb, c.second(x[e]) * c1);
     }
-  };
-  if (RES) {
-    fresh(reg);
+  }
+};
+
+// Writes the gradients of the kept tokens near this workgroup, and of its label where that is not
+// kept (zl: thread 0's, if `putlab`).  In place every gather has to be done before the first store of
+// the workgroup: the gradients wait for the gathered logits, and written to LDS they are there before
+// any thread passes the barrier.
+template <int NT, bool BF>
+__device__ inline void emit_kept(const DistillArgs& a, const Scale& c, const RowStats& r, const Grad& g, const Kept& k,
+                                 int64_t lab, bool putlab, float zl, int bit0, const RowTile<BF>& z, const RowTile<BF>& o,
+                                 uint32_t* bits, Shared<NT>& sh) {
+  const int tid = threadIdx.x;
+  if (tid < a.k) sh.kp[tid] = k.have ? __builtin_amdgcn_exp2f((k.t * c.invT - r.ta) * kLog2e) * r.tb : 0.f;
+  __syncthreads();
+  const bool mine = k.own && k.near;
+  float gk = 0.f, gl = 0.f;
+  if (mine) {
+    float p = sh.kp[tid];
+    if (sh.flag[0])      // (the owner is the first slot)
+      for (int l = tid + 1; l < a.k; ++l) p += sh.kid[l] == (int32_t)k.id ? sh.kp[l] : 0.f;
+    gk = g.one(c, k.z, g.kc * r.mass) - g.kw * p - (k.id == lab ? g.cc : 0.f);
+  }
+  if (putlab) {
+    gl = g.one(c, zl, g.kb) - g.cc;
+    const int at = (int)lab + z.off - bit0;
+    atomicOr(&bits[at >> 5], 1u << (at & 31));
+  }
+  __syncthreads();      // (kp has been read)
+  if (mine) sh.kp[tid] = gk;
+  if (putlab) sh.redT[0] = gl;
+  __syncthreads();
+  if (mine) o.put((int)k.id, gk);
+  if (putlab) o.put((int)lab, gl);
+}
+
+// A vector's gradients, element by element: those inside the row and not kept.
+template <bool BF>
+__device__ inline void emit_slow(const Scale& c, const Grad& g, int j, uint32_t kept, const RowTile<BF>& z,
+                                 const RowTile<BF>& o) {
+  constexpr int VE = RowTile<BF>::VE;
+  float x[VE];
+  g.vec<BF>(c, z.load(j), x);
+  const int e0 = z.first(j);
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (tid + i * NT < nvec) emit(reg[RES ? i : 0], tid + i * NT);
-  } else {
-    for (int j = tid; j < nvec; j += NT) emit(z.load(j), j);
+  for (int e = 0; e < VE; ++e)
+    if (e0 + e >= 0 && e0 + e < z.V && !((kept >> e) & 1u)) o.put(e0 + e, x[e]);
+}
+
+// Zero gradients for vectors [j0, j1) of a row.
+template <bool BF>
+__device__ inline void emit_zero(const RowTile<BF>& o, int j0, int j1, int nt) {
+  for (int j = j0 + threadIdx.x; j < j1; j += nt) {
+    if (o.inside(j)) {
+      *reinterpret_cast<u32x4*>(o.base + (uint32_t)(j * 16)) = u32x4{0u, 0u, 0u, 0u};
+    } else {
+      for (int i = 0; i < RowTile<BF>::VE; ++i)
+        if (o.first(j) + i >= 0 && o.first(j) + i < o.V) o.put(o.first(j) + i, 0.f);
+    }
   }
 }
 
-// The rows' losses, summed by one workgroup in 64 bits in a fixed order.
-__global__ __launch_bounds__(1024) void distill_loss_kernel(int64_t N, const float* __restrict__ lossrow,
-                                                            float* __restrict__ loss) {
+// ---------------------------------------------------------------------------------
+// One workgroup per row, the row in registers.
+// ---------------------------------------------------------------------------------
+template <bool BF, int NT, int NV>
+__global__ __launch_bounds__(NT, 4) void distill_row_kernel(DistillArgs a) {
+  using Tile = RowTile<BF>;
+  constexpr int VE = Tile::VE;
+  constexpr int NW = NT / 64;
+  extern __shared__ uint32_t bits[];
+  __shared__ Shared<NT> sh;
+  const int64_t row = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const float w = a.weights ? a.weights[row] : 1.f / (float)a.N;
+  const Tile z(a.logits, row, a.ld, a.V), o(a.dlogits, row, a.ldd, a.V);
+  if (w == 0.f) {      // a row without weight: nothing of it is read
+    if (tid == 0) a.rows[row].w = 0.f;
+    emit_zero<BF>(o, 0, o.vectors(), NT);
+    return;
+  }
+  u32x4 reg[NV];
+  const int nvec = z.vectors();
+  z.template fetch<NT>(reg, tid, 0, nvec);
+  Scale c(a);
+  const int64_t lab = c.ce ? a.labels[row] : -1;
+  const bool labok = !c.ce || (lab >= 0 && lab < a.V);
+  Kept k = mark_kept<NT, BF>(a, row, z, lab, bits, 0, (a.V + z.off + 31) / 32, sh);
+  if (k.have) k.z = z.at((int)k.id);
+  float zl = c.ce && labok && tid == 0 ? z.at((int)lab) : 0.f;
+
+  float mx = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) mx = fmaxf(mx, vec_max<BF>(reg[i]));
+  c.at(block_max<NT>(mx, sh.red));      // (its barrier also completes the bitmap)
+  settle(k, sh);
+  k.z = c.place(k.z);
+  zl = c.place(zl);
+
+  Sums<BF> s;
+  fresh(reg);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int j = tid + i * NT;
+    if (j < nvec) s.add(c, reg[i], c.kd ? kept_bits<VE>(bits, j) : 0u);
+  }
+  s.sr = wave_sum(s.sr);
+  s.s1 = wave_sum(s.s1);
+  if (lane == 0) { sh.red1[wave] = s.s1; sh.redT[wave] = s.sr; }
+  __syncthreads();
+  float tr = 0.f, t1 = 0.f;
+#pragma unroll
+  for (int v = 0; v < NW; ++v) { tr += sh.redT[v]; t1 += sh.red1[v]; }
+  const RowStats r = finish_row<NT>(a, row, w, c, k, tr, t1, labok, zl, sh);
+
+  const Grad g(a, c, r, w);
+  emit_kept<NT, BF>(a, c, r, g, k, lab, c.ce && labok && tid == 0 && !sh.flag[3], zl, 0, z, o, bits, sh);
+  // vectors without a kept token and inside the row go out whole; the others (a few) are read again, and
+  // go out element by element.  (In place those are still as they were, but for the kept tokens.)
+  const bool same = z.off == o.off;
+  uint32_t left = 0u;
+  fresh(reg);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int j = tid + i * NT;
+    if (j < nvec) {
+      if (same && kept_bits<VE>(bits, j) == 0u && z.inside(j)) {
+        float x[VE];
+        g.vec<BF>(c, reg[i], x);
+        *reinterpret_cast<u32x4*>(o.base + (uint32_t)(j * 16)) = Tile::packed(x);
+      } else {
+        left |= 1u << i;
+      }
+    }
+  }
+  while (left) {
+    const int j = tid + (__ffs(left) - 1) * NT;
+    emit_slow<BF>(c, g, j, kept_bits<VE>(bits, j), z, o);
+    left &= left - 1;
+  }
+}
+
+// ---------------------------------------------------------------------------------
+// Chunks of rows: workgroup (row, chunk) has the vectors [chunk cv, (chunk + 1) cv).
+// ---------------------------------------------------------------------------------
+constexpr int kCT = 256;      // threads
+constexpr int kCV = 8;        // vectors of a thread at most
+struct PartSum {
+  float m, sr, s1, pad_;
+};
+
+template <bool BF>
+__global__ __launch_bounds__(kCT) void distill_part_kernel(DistillArgs a) {
+  using Tile = RowTile<BF>;
+  constexpr int VE = Tile::VE;
+  __shared__ uint32_t bits[kCT * kCV * VE / 32];
+  __shared__ Shared<kCT> sh;
+  const int64_t row = blockIdx.x / a.chunks;
+  const int chunk = (int)(blockIdx.x % a.chunks), tid = threadIdx.x;
+  const float w = a.weights ? a.weights[row] : 1.f / (float)a.N;
+  if (w == 0.f) return;
+  const Tile z(a.logits, row, a.ld, a.V);
+  const int j0 = chunk * a.cv, j1 = min(j0 + a.cv, z.vectors());
+  u32x4 reg[kCV];
+  z.template fetch<kCT>(reg, tid, j0, j1);
+  Scale c(a);
+  const int64_t lab = c.ce ? a.labels[row] : -1;
+  const int bit0 = j0 * VE;
+  Kept k = mark_kept<kCT, BF>(a, row, z, lab, bits, bit0, (max(j1 - j0, 0) * VE + 31) / 32, sh);
+  if (k.near) a.zk[row * a.k + tid] = z.at((int)k.id);
+  if (tid == 0 && c.ce && lab >= 0 && lab < a.V) {
+    const int j = ((int)lab + z.off) / VE;
+    if (j >= j0 && j < j1) a.zl[row] = z.at((int)lab);
+  }
+  float mx = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kCV; ++i) mx = fmaxf(mx, vec_max<BF>(reg[i]));
+  const float m = block_max<kCT>(mx, sh.red);
+  c.at(m);
+  Sums<BF> s;
+  fresh(reg);
+  if (m > -INFINITY) {
+#pragma unroll
+    for (int i = 0; i < kCV; ++i) {
+      const int j = j0 + tid + i * kCT;
+      if (j < j1) s.add(c, reg[i], c.kd ? kept_bits<VE>(bits, j - j0) : 0u);
+    }
+  } else {      // a chunk of -infinity has no mass; one of NaN (which no maximum shows) has NaN
+#pragma unroll
+    for (int i = 0; i < kCV; ++i) {
+      float x[VE];
+      Tile::values(reg[i], x);
+#pragma unroll
+      for (int e = 0; e < VE; ++e)
+        if (x[e] != x[e]) s.sr = s.s1 = x[e];
+    }
+  }
+  s.sr = wave_sum(s.sr);
+  s.s1 = wave_sum(s.s1);
+  if ((tid & 63) == 0) { sh.red1[tid >> 6] = s.s1; sh.redT[tid >> 6] = s.sr; }
+  __syncthreads();
+  if (tid == 0) {
+    PartSum p{m, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int v = 0; v < kCT / 64; ++v) { p.sr += sh.redT[v]; p.s1 += sh.red1[v]; }
+    reinterpret_cast<PartSum*>(a.part)[row * a.chunks + chunk] = p;
+  }
+}
+
+// A row's chunks joined: the maximum into c, the sums rescaled to it.  One thread a chunk.
+static_assert((kVocabMax / 4 + 2 + 2 * kCT - 1) / (2 * kCT) <= kCT, "a row's chunks fit one to a thread");
+__device__ inline void join_row(const DistillArgs& a, int64_t row, Scale& c, float& tr, float& t1, Shared<kCT>& sh) {
+  const int tid = threadIdx.x;
+  PartSum p{-INFINITY, 0.f, 0.f, 0.f};
+  if (tid < a.chunks) p = reinterpret_cast<const PartSum*>(a.part)[row * a.chunks + tid];
+  c.at(block_max<kCT>(p.m, sh.red));
+  float fA = 1.f, fB = 1.f;
+  if (p.m != c.m0) {      // the chunk's own shifts against the row's
+    Scale d = c;
+    d.at(p.m);
+    const bool none = c.huge || d.huge || p.m == -INFINITY;
+    fA = none ? 0.f : __builtin_amdgcn_exp2f(d.cA - c.cA);
+    fB = none ? 0.f : __builtin_amdgcn_exp2f(d.cB - c.cB);
+  }
+  // (a row of -infinity throughout has no distribution: NaN)
+  const float bad = c.m0 == -INFINITY ? __builtin_nanf("") : 0.f;
+  const float x = wave_sum(fA > 0.f || p.sr != p.sr ? p.sr * fA + bad : bad);
+  const float y = wave_sum(fB > 0.f || p.s1 != p.s1 ? p.s1 * fB + bad : bad);
+  if ((tid & 63) == 0) { sh.redT[tid >> 6] = x; sh.red1[tid >> 6] = y; }
+  __syncthreads();
+  tr = t1 = 0.f;
+#pragma unroll
+  for (int v = 0; v < kCT / 64; ++v) { tr += sh.redT[v]; t1 += sh.red1[v]; }
+}
+
+// STATS: joins the row's chunks and keeps the statistics (one workgroup a row, nothing emitted).
+// JOIN: joins them and emits; else emits from kept statistics.
+template <bool BF, bool STATS, bool JOIN>
+__global__ __launch_bounds__(kCT) void distill_emit_kernel(DistillArgs a) {
+  using Tile = RowTile<BF>;
+  constexpr int VE = Tile::VE;
+  __shared__ uint32_t bits[kCT * kCV * VE / 32];
+  __shared__ Shared<kCT> sh;
+  const int64_t row = STATS ? blockIdx.x : blockIdx.x / a.chunks;
+  const int chunk = STATS ? 0 : (int)(blockIdx.x % a.chunks), tid = threadIdx.x;
+  const float w = a.weights ? a.weights[row] : 1.f / (float)a.N;
+  const Tile z(a.logits, row, a.ld, a.V), o(a.dlogits, row, a.ldd, a.V);
+  const int j0 = chunk * a.cv, j1 = min(j0 + a.cv, z.vectors());
+  if (w == 0.f) {
+    if (STATS && tid < kStN) a.stats[row * kStN + tid] = 0.f;
+    if ((STATS || JOIN) && chunk == 0 && tid == 0) a.rows[row].w = 0.f;
+    // (the last chunk takes what rounding of the two starts to vectors leaves over)
+    if (!STATS) emit_zero<BF>(o, j0, chunk == a.chunks - 1 ? o.vectors() : min(j0 + a.cv, o.vectors()), kCT);
+    return;
+  }
+  u32x4 reg[STATS ? 1 : kCV];
+  if (!STATS) {
+#pragma unroll
+    for (int i = 0; i < kCV; ++i) {
+      const int j = j0 + tid + i * kCT;
+      reg[STATS ? 0 : i] = j < j1 ? z.whole(j) : Tile::empty();
+    }
+  }
+  Scale c(a);
+  const int64_t lab = c.ce ? a.labels[row] : -1;
+  const bool labok = !c.ce || (lab >= 0 && lab < a.V);
+  const int bit0 = j0 * VE;
+  Kept k = mark_kept<kCT, BF>(a, row, z, lab, bits, bit0, STATS ? 0 : (max(j1 - j0, 0) * VE + 31) / 32, sh);
+  const bool lnear = labok && c.ce && !STATS && ((int)lab + z.off) / VE >= j0 && ((int)lab + z.off) / VE < j1;
+  float zl = 0.f, tr = 0.f, t1 = 0.f;
+  RowStats r;
+  if (STATS || JOIN) {
+    // the gathered logits come from the parts: in place, other workgroups may have written theirs
+    if (k.have) k.z = a.zk[row * a.k + tid];
+    if (c.ce && labok) zl = a.zl[row];
+    join_row(a, row, c, tr, t1, sh);      // (its barriers also complete the slots)
+    // over the whole row a token may be repeated far from this chunk
+    if (k.have) {
+      k.own = true;
+      for (int l = 0; l < tid; ++l)
+        if (sh.kid[l] == (int32_t)k.id) {
+          k.own = false;
+          sh.flag[0] = 1;
+        }
+    }
+    k.z = c.place(k.z);
+    zl = c.place(zl);
+    r = finish_row<kCT>(a, row, w, c, k, tr, t1, labok, zl, sh);
+    if (STATS) {
+      if (tid == 0) {
+        float* st = a.stats + row * kStN;
+        st[kStM] = c.m0; st[kStInvT] = r.invsT; st[kStInv1] = r.invs1;
+        st[kStBase] = r.base; st[kStMass] = r.mass; st[kStTa] = r.ta; st[kStTb] = r.tb; st[kStN - 1] = 0.f;
+      }
+      return;
+    }
+  } else {
+    const float* st = a.stats + row * kStN;
+    c.at(st[kStM]);
+    r.invsT = st[kStInvT]; r.invs1 = st[kStInv1]; r.base = st[kStBase];
+    r.mass = st[kStMass]; r.ta = st[kStTa]; r.tb = st[kStTb];
+    if (k.near) k.z = c.place(z.at((int)k.id));
+    if (lnear && tid == 0) zl = c.place(z.at((int)lab));
+    __syncthreads();
+    settle(k, sh);
+  }
+  const Grad g(a, c, r, a.gout ? w * a.gout[0] : w);
+  emit_kept<kCT, BF>(a, c, r, g, k, lab, lnear && tid == 0 && !sh.flag[3], zl, bit0, z, o, bits, sh);
+  const bool same = z.off == o.off;
+  uint32_t left = 0u;
+#pragma unroll
+  for (int i = 0; i < kCV; ++i) {
+    const int j = j0 + tid + i * kCT;
+    if (j < j1) {
+      if (same && kept_bits<VE>(bits, j - j0) == 0u && z.inside(j)) {
+        float x[VE];
+        g.vec<BF>(c, reg[STATS ? 0 : i], x);
+        *reinterpret_cast<u32x4*>(o.base + (uint32_t)(j * 16)) = Tile::packed(x);
+      } else {
+        left |= 1u << i;
+      }
+    }
+  }
+  while (left) {
+    const int j = j0 + tid + (__ffs(left) - 1) * kCT;
+    emit_slow<BF>(c, g, j, kept_bits<VE>(bits, j - j0), z, o);
+    left &= left - 1;
+  }
+}
+
+// The rows' losses from their sums, added up by one workgroup in 64 bits in a fixed order.  (The
+// logarithms stand here because 64-bit ones take registers that the rows' kernel has no room for.)
+__global__ __launch_bounds__(1024) void distill_loss_kernel(DistillArgs a) {
   __shared__ double red[16];
   double s = 0.0;
-  for (int64_t i = threadIdx.x; i < N; i += 1024) s += (double)lossrow[i];
+  for (int64_t i = threadIdx.x; i < a.N; i += 1024) {
+    const DistillRow r = a.rows[i];
+    if (r.w == 0.f) continue;
+    double l = 0.0;
+    if (a.alpha > 0.f) {
+      // sum p (log p - log q) with log q = (as summed) - log total, and p over its sum without a tail
+      double kl = r.kl + r.psum * log((double)r.total);
+      if (!a.teacher_lse)
+        kl = r.psum > 0.0 ? kl / r.psum - log(r.psum) : 0.0;
+      else if (r.pt > 0.0)
+        kl += r.pt * (log(r.pt) - log((double)r.rest / (double)r.total));
+      l += (double)a.alpha * (double)a.T * (double)a.T * kl;
+    }
+    if (a.alpha < 1.f) l += (1.0 - (double)a.alpha) * (log((double)r.t1) - (double)r.zl * kLn2);
+    s += (double)(float)((double)r.w * l);
+  }
   s = wave_sum(s);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
   __syncthreads();
   if (threadIdx.x == 0) {
     double t = 0.0;
     for (int v = 0; v < 16; ++v) t += red[v];
-    loss[0] = (float)t;
+    a.loss[0] = (float)t;
   }
 }
 
-template <bool BF, int NT, int NV, bool RES>
-hipError_t launch_mode(const DistillArgs& a, int mode, size_t lds, hipStream_t s) {
-  const dim3 grid((unsigned)a.N);
-  if (mode == 0)
-    hipLaunchKernelGGL((distill_kernel<BF, NT, NV, RES, 0>), grid, dim3(NT), lds, s, a);
-  else if (mode == 1)
-    hipLaunchKernelGGL((distill_kernel<BF, NT, NV, RES, 1>), grid, dim3(NT), lds, s, a);
-  else
-    hipLaunchKernelGGL((distill_kernel<BF, NT, NV, RES, 2>), grid, dim3(NT), lds, s, a);
+int64_t max_vectors(int V, bool bf16) { return ((int64_t)V + 7) / (bf16 ? 8 : 4) + 1; }   // of a row that starts anywhere
+
+// Rows in registers for enough rows to fill the GPU (two workgroups a CU).
+constexpr int kRowVectors = 13 * 1024;
+bool whole_rows(const DistillArgs& a) { return a.N >= 512 && max_vectors(a.V, a.bf16) <= kRowVectors; }
+
+// Vectors of a chunk: as many as a workgroup holds, fewer while there are not 1024 workgroups, at least two a
+// thread.  Depends on the sizes alone.
+int chunk_vectors(int64_t N, int V, bool bf16) {
+  const int64_t nv = max_vectors(V, bf16);
+  int per = kCV;
+  while (per > 2 && N * ((nv + per * kCT - 1) / (per * kCT)) < 1024) per /= 2;
+  return per * kCT;
+}
+
+template <bool BF, int NT, int NV>
+hipError_t launch_row(const DistillArgs& a, hipStream_t s) {
+  const size_t lds = ((size_t)a.V + 7 + 31) / 32 * 4;
+  hipLaunchKernelGGL((distill_row_kernel<BF, NT, NV>), dim3((unsigned)a.N), dim3(NT), lds, s, a);
   return hipGetLastError();
 }
 
 template <bool BF>
 hipError_t launch_type(const DistillArgs& a, int mode, hipStream_t s) {
-  const size_t lds = ((size_t)(a.V + 31) / 32 + 1) * 4;
-  const int64_t nvec = ((int64_t)a.V + 7) / (BF ? 8 : 4) + 1;   // of a row that starts anywhere
-  if (nvec <= 256 * 8) return launch_mode<BF, 256, 8, true>(a, mode, lds, s);
-  if (nvec <= 512 * 16) return launch_mode<BF, 512, 16, true>(a, mode, lds, s);
-  if (nvec <= 1024 * 16) return launch_mode<BF, 1024, 16, true>(a, mode, lds, s);
-  return launch_mode<BF, 1024, 1, false>(a, mode, lds, s);
+  if (mode == 0 && whole_rows(a)) {
+    const int64_t nv = max_vectors(a.V, BF);
+    if (nv <= 4 * 512) return launch_row<BF, 512, 4>(a, s);
+    if (nv <= 7 * 512) return launch_row<BF, 512, 7>(a, s);
+    if (nv <= 10 * 512) return launch_row<BF, 512, 10>(a, s);
+    if (nv <= 13 * 512) return launch_row<BF, 512, 13>(a, s);
+    if (nv <= 8 * 1024) return launch_row<BF, 1024, 8>(a, s);
+    return launch_row<BF, 1024, 13>(a, s);
+  }
+  const dim3 grid((unsigned)(a.N * a.chunks)), rows((unsigned)a.N), nt(kCT);
+  if (mode != 2) {
+    hipLaunchKernelGGL((distill_part_kernel<BF>), grid, nt, 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (mode == 0)
+    hipLaunchKernelGGL((distill_emit_kernel<BF, false, true>), grid, nt, 0, s, a);
+  else if (mode == 1)
+    hipLaunchKernelGGL((distill_emit_kernel<BF, true, true>), rows, nt, 0, s, a);
+  else
+    hipLaunchKernelGGL((distill_emit_kernel<BF, false, false>), grid, nt, 0, s, a);
+  return hipGetLastError();
 }
+
+size_t up256(size_t n) { return (n + 255) & ~size_t(255); }
 
 }  // namespace
 
-hipError_t launch_distill(const DistillArgs& a, int mode, hipStream_t s) {
+size_t distill_workspace_bytes(int64_t N, int V, int k, bool bf16) {
+  const int64_t chunks = (max_vectors(V, bf16) + chunk_vectors(N, V, bf16) - 1) / chunk_vectors(N, V, bf16);
+  return up256(N * sizeof(DistillRow)) + up256(N * chunks * sizeof(PartSum)) + up256((size_t)N * k * 4) + up256(N * 4) + 256;
+}
+
+hipError_t launch_distill(DistillArgs a, int mode, void* ws, hipStream_t s) {
+  a.cv = chunk_vectors(a.N, a.V, a.bf16);
+  a.chunks = (int)((max_vectors(a.V, a.bf16) + a.cv - 1) / a.cv);
+  if (mode != 2) {
+    char* w = (char*)ws;
+    a.rows = (DistillRow*)w;
+    w += up256(a.N * sizeof(DistillRow));
+    a.part = (float*)w;
+    w += up256(a.N * a.chunks * sizeof(PartSum));
+    a.zk = (float*)w;
+    w += up256((size_t)a.N * a.k * 4);
+    a.zl = (float*)w;
+  }
   if (a.N > 0) {
     const hipError_t e = a.bf16 ? launch_type<true>(a, mode, s) : launch_type<false>(a, mode, s);
     if (e != hipSuccess) return e;
   }
   if (mode != 2) {
-    hipLaunchKernelGGL(distill_loss_kernel, dim3(1), dim3(1024), 0, s, a.N, a.lossrow, a.loss);
+    hipLaunchKernelGGL(distill_loss_kernel, dim3(1), dim3(1024), 0, s, a);
     return hipGetLastError();
   }
   return hipSuccess;

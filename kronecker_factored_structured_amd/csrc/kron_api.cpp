@@ -1024,9 +1024,9 @@ kron_status_t distill_run(const kron_distill_t* d, int mode, const void* logits,
   a.bf16 = d->dtype == KRON_BF16; a.ids64 = (d->flags & KRON_IDS_I64) != 0;
   a.T = d->temperature; a.alpha = d->alpha;
   a.logits = logits; a.ids = ids; a.teacher = teacher; a.teacher_lse = kd ? teacher_lse : nullptr;
-  a.labels = labels; a.weights = weights; a.gout = gout; a.stats = stats; a.lossrow = (float*)workspace;
+  a.labels = labels; a.weights = weights; a.gout = gout; a.stats = stats;
   a.loss = loss; a.dlogits = dlogits;
-  const hipError_t e = kron::launch_distill(a, mode, stream);
+  const hipError_t e = kron::launch_distill(a, mode, workspace, stream);
   if (e != hipSuccess) return hip_fail(e, "kron_distill launch");
   return ok();
 }
@@ -1035,7 +1035,7 @@ kron_status_t distill_run(const kron_distill_t* d, int mode, const void* logits,
 
 size_t kron_distill_workspace_bytes(const kron_distill_t* d) {
   if (distill_check(d) != KRON_OK) return 0;
-  return (((size_t)d->N * 4 + 255) & ~size_t(255)) + 256;
+  return kron::distill_workspace_bytes(d->N, d->V, d->k, d->dtype == KRON_BF16);
 }
 
 kron_status_t kron_distill(const kron_distill_t* d, const void* logits, const void* ids, const float* teacher,

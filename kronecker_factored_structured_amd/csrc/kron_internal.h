@@ -292,6 +292,11 @@ hipError_t launch_glu_bwd(const GluArgs& a, void* ws, hipStream_t s);
 constexpr int kDistillMaxK = 256;
 constexpr int kVocabMax = 1 << 18;
 constexpr int kDistillStats = 8;   // floats of a row's stats
+// A row's part of the loss, before the logarithms (see distill_loss_kernel).
+struct DistillRow {
+  double kl, psum, pt;
+  float total, rest, t1, zl, w, pad_;
+};
 struct DistillArgs {
   int64_t N, ld, ldd;
   int32_t V, k;
@@ -305,12 +310,18 @@ struct DistillArgs {
   const float* weights;       // NULL: 1 / N
   const float* gout;          // the upstream gradient (mode 2)
   float* stats;
-  float* lossrow;             // workspace: N
   float* loss;
   void* dlogits;
+  // set by launch_distill: vectors of a chunk, chunks of a row, and the workspace
+  int32_t cv, chunks;
+  DistillRow* rows;           // N
+  float* part;                // N x chunks partial sums
+  float* zk;                  // N x k logits of the kept tokens
+  float* zl;                  // N logits of the labels
 };
-// mode 0: loss and gradient; 1: loss and stats; 2: gradient from stats
-hipError_t launch_distill(const DistillArgs& a, int mode, hipStream_t s);
+size_t distill_workspace_bytes(int64_t N, int V, int k, bool bf16);
+// mode 0: loss and gradient; 1: loss and stats; 2: gradient from stats (no workspace)
+hipError_t launch_distill(DistillArgs a, int mode, void* ws, hipStream_t s);
 struct TopkArgs {
   int64_t N, ld;
   int32_t V, k;

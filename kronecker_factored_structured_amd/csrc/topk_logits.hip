@@ -6,8 +6,9 @@
 // lower bound's witness: the k-th largest of the threads' maxima is a threshold that at least k
 // values reach, and for k below the thread count few more do (for values in random order about
 // NT ln(NT / (NT - k)) in all).  Those candidates go to LDS and are ranked by counting.  Rows
-// that defeat the threshold (many equal values, or the top in few threads) take an exact
-// bisection on the value, then on the token among the equal ones.  Bound by the one read of z.
+// that defeat the threshold (many equal values, the top in few threads, fewer vectors than k) and
+// rows with a NaN or an infinite maximum take an exact bisection on the value's key, then on the
+// token among the equal ones.  Bound by the one read of z.
 #include "kron_internal.h"
 #include "row_tile.h"
 
@@ -28,68 +29,68 @@ __device__ inline float value_of(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
 
-// The packed row as new values, so that one pass's unpacked values are not kept for the next.
-template <int NV>
-__device__ inline void fresh(u32x4 (&reg)[NV]) {
-#pragma unroll
-  for (int i = 0; i < NV; ++i) asm volatile("" : "+v"(reg[i]));
-}
-
 template <bool BF, int NT, int NV, bool RES>
-__global__ __launch_bounds__(NT) void topk_kernel(TopkArgs a) {
+__global__ __launch_bounds__(NT, 4) void topk_kernel(TopkArgs a) {
   using Tile = RowTile<BF>;
   constexpr int VE = Tile::VE;
   constexpr int NW = NT / 64;
   __shared__ uint64_t cand[kCap];      // key, then the complement of the token: larger is better
   __shared__ uint32_t tmax[NT];
   __shared__ float red[NW];
-  __shared__ uint32_t cnt[NW];
-  __shared__ uint32_t ncand, tau_s;
+  __shared__ uint32_t cnt[2][NW];
+  __shared__ uint32_t ncand, tau_s, top_s;
 
   const int64_t row = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const Tile z(a.logits, row, a.ld, a.V);
   const int nvec = z.vectors();
   u32x4 reg[RES ? NV : 1];
-  if (RES) {
+  if constexpr (RES) z.template fetch<NT>(reg, tid, 0, nvec);
+  // calls f(vector, its index) for each of this thread's vectors
+  auto each_vec = [&](auto f) {
+    if constexpr (RES) {
+      fresh(reg);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) reg[RES ? i : 0] = z.load(tid + i * NT);
-  }
+      for (int i = 0; i < NV; ++i)
+        if (tid + i * NT < nvec) f(reg[i], tid + i * NT);
+    } else {
+      for (int j = tid; j < nvec; j += NT) f(z.load(j), j);
+    }
+  };
   // calls f(value, token) for each of this thread's values
   auto each = [&](auto f) {
-    auto vec = [&](const u32x4& v, int j) {
+    each_vec([&](const u32x4& v, int j) {
       const int e0 = z.first(j);
 #pragma unroll
       for (int e = 0; e < VE; ++e)
         if (e0 + e >= 0 && e0 + e < a.V) f(Tile::value(v, e), e0 + e);
-    };
-    if (RES) {
-      fresh(reg);
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (tid + i * NT < nvec) vec(reg[RES ? i : 0], tid + i * NT);
-    } else {
-      for (int j = tid; j < nvec; j += NT) vec(z.load(j), j);
-    }
+    });
   };
+  int turn = 0;
   auto total = [&](uint32_t c) -> uint32_t {      // over the workgroup
 #pragma unroll
     for (int o = 32; o >= 1; o /= 2) c += __shfl_xor(c, o, 64);
-    __syncthreads();
-    if (lane == 0) cnt[wave] = c;
+    turn ^= 1;      // (the other half is still being read)
+    if (lane == 0) cnt[turn][wave] = c;
     __syncthreads();
     uint32_t s = 0;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) s += cnt[w];
+    for (int w = 0; w < NW; ++w) s += cnt[turn][w];
     return s;
   };
+  auto keep = [&](uint32_t key, int e) {
+    const uint32_t at = atomicAdd(&ncand, 1u);
+    if (at < kCap) cand[at] = ((uint64_t)key << 32) | (uint32_t)~(uint32_t)e;
+  };
 
-  uint32_t best = 0u;
-  each([&](float f, int) {
-    const uint32_t k = key_of(f);
-    best = k > best ? k : best;
+  float mx = -INFINITY;      // (a NaN does not show: the sum tells)
+  each_vec([&](const u32x4& v, int) {
+    float x[VE];
+    Tile::values(v, x);
+#pragma unroll
+    for (int e = 0; e < VE; e += 2) mx = fmaxf(mx, fmaxf(x[e], x[e + 1]));
   });
-  tmax[tid] = best;
+  tmax[tid] = tid < nvec ? key_of(mx) : 0u;
   if (tid == 0) ncand = 0u;
   __syncthreads();
   // wave 0: the largest 16-bit prefix that at least k of the threads' maxima reach
@@ -115,70 +116,81 @@ __global__ __launch_bounds__(NT) void topk_kernel(TopkArgs a) {
     }
     if (lane == 0) {
       tau_s = t;
-      red[0] = value_of(top);
+      top_s = top;
     }
   }
   __syncthreads();
-  const float m = red[0];
-  uint32_t tau = tau_s;
-  const float sT = kLog2e / a.T;
-  // the sum, and the candidates
+  const float m = value_of(top_s);
+  const float sT = kLog2e / a.T, c = m * sT;
+  // the sum, and the candidates.  Below this threshold (or with k >= 2^16 of no witness) it says nothing.
+  const bool finite = fabsf(c) < 1e38f;
+  const bool use = finite && tau_s > key_of(-INFINITY);
+  const float tau_f = use ? value_of(tau_s) : INFINITY;
   float s = 0.f;
-  each([&](float f, int e) {
-    s += f == m ? 1.f : __builtin_amdgcn_exp2f((f - m) * sT);      // (equal infinities differ by nothing)
-    const uint32_t k = key_of(f);
-    if (k >= tau) {
-      const uint32_t at = atomicAdd(&ncand, 1u);
-      if (at < kCap) cand[at] = ((uint64_t)k << 32) | (uint32_t)~(uint32_t)e;
-    }
-  });
-  s = wave_sum(s);
-  __syncthreads();      // (red[0] has been read, the candidates are written)
-  if (lane == 0) red[wave] = s;
-  uint32_t nc = ncand;
-  __syncthreads();
-  if (tid == 0) {
-    float t = 0.f;
+  if (finite) {
+    each_vec([&](const u32x4& v, int j) {
+      float x[VE];
+      Tile::values(v, x);
+      float h = x[0];
 #pragma unroll
-    for (int w = 0; w < NW; ++w) t += red[w];
-    a.lse[row] = m / a.T + logf(t);
+      for (int e = 1; e < VE; ++e) h = fmaxf(h, x[e]);
+#pragma unroll
+      for (int e = 0; e < VE; ++e) s += __builtin_amdgcn_exp2f(fmaf(x[e], sT, -c));
+      if (h >= tau_f) {      // (the padding of a partial vector is -infinity)
+#pragma unroll
+        for (int e = 0; e < VE; ++e)
+          if (x[e] >= tau_f) keep(key_of(x[e]), z.first(j) + e);
+      }
+    });
+  } else {
+    each([&](float f, int) { s += f != f ? f : f == m ? 1.f : 0.f; });      // (see lse below)
   }
-  if (nc > kCap) {
+  s = wave_sum(s);
+  if (lane == 0) red[wave] = s;
+  __syncthreads();
+  s = 0.f;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) s += red[w];
+  if (tid == 0) {
+    // m / T + ln s with the rounded m log2 e / T that the exponentials used; where that overflows the values
+    // equal to the maximum are all the sum
+    const double base = finite ? (double)c * 0.69314718055994531 : (double)m / (double)a.T;
+    a.lse[row] = (float)(base + (double)logf(s));
+  }
+  uint32_t nc = ncand;
+  if (!use || s != s || nc > kCap) {
     // the k-th largest key exactly: tau = max {t : at least k keys >= t}
-    tau = 0u;
+    uint32_t tau = 0u;
     for (int b = 31; b >= 0; --b) {
-      const uint32_t c = tau | (1u << b);
+      const uint32_t t = tau | (1u << b);
       uint32_t n = 0;
-      each([&](float f, int) { n += key_of(f) >= c ? 1u : 0u; });
-      if (total(n) >= (uint32_t)a.k) tau = c;
+      each([&](float f, int) { n += key_of(f) >= t ? 1u : 0u; });
+      if (total(n) >= (uint32_t)a.k) tau = t;
     }
     uint32_t above = 0;
     each([&](float f, int) { above += key_of(f) > tau ? 1u : 0u; });
     const uint32_t need = (uint32_t)a.k - total(above);      // of the equal ones: those with the lowest tokens
-    int lim = 0;      // largest lim such that fewer than `need` equal ones stand below token lim
-    for (int b = 30; b >= 0; --b) {
-      const int64_t c = (int64_t)lim + (int64_t(1) << b);
-      if (c >= a.V) continue;
+    int lim = 0;      // the largest lim such that fewer than `need` equal ones stand below token lim
+    for (int b = 17; b >= 0; --b) {
+      const int t = lim + (1 << b);
+      if (t >= a.V) continue;
       uint32_t n = 0;
-      each([&](float f, int e) { n += (key_of(f) == tau && e < (int)c) ? 1u : 0u; });
-      if (total(n) < need) lim = (int)c;
+      each([&](float f, int e) { n += (key_of(f) == tau && e < t) ? 1u : 0u; });
+      if (total(n) < need) lim = t;
     }
     __syncthreads();
     if (tid == 0) ncand = 0u;
     __syncthreads();
     each([&](float f, int e) {
       const uint32_t k = key_of(f);
-      if (k > tau || (k == tau && e <= lim)) {
-        const uint32_t at = atomicAdd(&ncand, 1u);
-        if (at < kCap) cand[at] = ((uint64_t)k << 32) | (uint32_t)~(uint32_t)e;
-      }
+      if (k > tau || (k == tau && e <= lim)) keep(k, e);
     });
     __syncthreads();
     nc = ncand < (uint32_t)kCap ? ncand : (uint32_t)kCap;      // (exactly k)
   }
   // a candidate's place is the number of better ones (all are distinct: the tokens differ)
-  for (uint32_t c = tid; c < nc; c += NT) {
-    const uint64_t x = cand[c];
+  for (uint32_t i = tid; i < nc; i += NT) {
+    const uint64_t x = cand[i];
     int place = 0;
     for (uint32_t l = 0; l < nc; ++l) place += cand[l] > x ? 1 : 0;
     if (place < a.k) {
@@ -194,10 +206,12 @@ hipError_t launch_type(const TopkArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)a.N);
   if (nvec <= 512 * 4)
     hipLaunchKernelGGL((topk_kernel<BF, 512, 4, true>), grid, dim3(512), 0, s, a);
-  else if (nvec <= 512 * 16)
-    hipLaunchKernelGGL((topk_kernel<BF, 512, 16, true>), grid, dim3(512), 0, s, a);
-  else if (nvec <= 1024 * 16)
-    hipLaunchKernelGGL((topk_kernel<BF, 1024, 16, true>), grid, dim3(1024), 0, s, a);
+  else if (nvec <= 512 * 8)
+    hipLaunchKernelGGL((topk_kernel<BF, 512, 8, true>), grid, dim3(512), 0, s, a);
+  else if (nvec <= 512 * 13)
+    hipLaunchKernelGGL((topk_kernel<BF, 512, 13, true>), grid, dim3(512), 0, s, a);
+  else if (nvec <= 1024 * 13)
+    hipLaunchKernelGGL((topk_kernel<BF, 1024, 13, true>), grid, dim3(1024), 0, s, a);
   else
     hipLaunchKernelGGL((topk_kernel<BF, 1024, 1, false>), grid, dim3(1024), 0, s, a);
   return hipGetLastError();

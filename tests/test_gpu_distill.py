@@ -155,6 +155,63 @@ def test_distill(N, V, k, dtype, T, alpha, tail, pad, off):
     assert torch.equal(torch.isnan(buf[behind]), torch.isnan(ref[behind])) and bool(torch.isnan(buf[behind]).all())
 
 
+@pytest.mark.parametrize("V,dtype,T,alpha,tail", [
+    (700, BF, 2.0, 0.5, True), (20001, BF, 1.0, 0.5, False), (40000, BF, 1.5, 0.5, True), (50257, BF, 2.0, 1.0, True),
+    (60001, BF, 2.0, 0.5, True), (100003, BF, 2.0, 0.5, False), (106489, BF, 1.0, 0.0, False), (7000, F32, 2.0, 0.5, True),
+    (26600, F32, 1.5, 0.5, True), (53001, F32, 1.0, 1.0, False)])
+def test_distill_many_rows(V, dtype, T, alpha, tail):
+    """Enough rows for one workgroup per row; most of them without weight, so that the oracle has few to do."""
+    N, k = 530, 48
+    print(f"[distill rows] V={V} {dtype} T={T} alpha={alpha} tail={tail}", flush=True)
+    _, z = rows(N, V, 3, dtype, V)
+    ids, t, lse, lab, w = teacher(N, V, k, V, T, tail)
+    w[np.arange(N) % 90 != 7] = 0
+    ids[97, 5:9] = ids[97, 2]
+    ids[187, ::2] = -1
+    if tail:
+        lse[97] += 3
+    d = dict(teacher_lse=dev(lse), labels=dev(lab), weights=dev(w), temperature=T, alpha=alpha)
+    gi = dev(ids.astype(np.int32))
+    a = K().kron_distill(z, gi, dev(t), **d)
+    close(a["loss"], a["dlogits"], z, ids, t, lse, lab, w, T, alpha, dtype)
+    got = K().kron_distill(z, gi, dev(t), out=z, **d)      # in place
+    assert torch.equal(z, a["dlogits"]) and torch.equal(got["loss"], a["loss"])
+
+
+@pytest.mark.parametrize("N", [3, 600])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_distill_rows_of_the_lowest_and_largest_values(N, dtype):
+    """Rows of the type's lowest value throughout, of its largest one among the lowest, of -infinity but for a few."""
+    V, k, T = 9000, 4, 2.0
+    _, z = rows(N, V, 0, dtype, 3)
+    lo, hi = torch.finfo(dtype).min, torch.finfo(dtype).max
+    z[0] = lo
+    z[1] = lo
+    z[1, 40] = z[1, 8999] = hi
+    z[2] = -float("inf")
+    z[2, 100:110] = 1.0
+    ids = np.tile(np.array([100, 101, 102, 103]), (N, 1))
+    ids[1] = [40, 8999, -1, -1]
+    t = np.zeros((N, k), np.float32)
+    w = np.zeros(N, np.float32)
+    w[:3] = 0.5
+    lab = np.full(N, 105)
+    lab[1] = 40
+    d = dict(labels=dev(lab), weights=dev(w), temperature=T, alpha=0.5)
+    a = K().kron_distill(z, dev(ids.astype(np.int32)), dev(t), **d)
+    close(a["loss"], a["dlogits"], z, ids, t, None, lab, w, T, 0.5, dtype)
+    # nothing but -infinity has no distribution: NaN, in its own row only
+    z[0] = -float("inf")
+    b = K().kron_distill(z, dev(ids.astype(np.int32)), dev(t), **d)
+    assert torch.isnan(b["loss"]).all() and torch.isnan(b["dlogits"][0]).all()
+    assert torch.equal(b["dlogits"][1:], a["dlogits"][1:])
+    # a NaN logit shows
+    z[0] = 0
+    z[0, 4321] = float("nan")
+    b = K().kron_distill(z, dev(ids.astype(np.int32)), dev(t), **d)
+    assert torch.isnan(b["loss"]).all() and torch.isnan(b["dlogits"][0]).any() and torch.equal(b["dlogits"][1:], a["dlogits"][1:])
+
+
 @pytest.mark.parametrize("V", [300, 9001, 140001])
 @pytest.mark.parametrize("tail", [False, True])
 def test_distill_slots(V, tail):
