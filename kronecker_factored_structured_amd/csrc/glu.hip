@@ -19,6 +19,9 @@
 // k-slots {4g..4g+3, 16+4g..16+4g+3} ("chained" order), so Z goes from the first product into the
 // second without leaving its registers; the other operand is laid out in the same order.  The
 // factors are laid out as such blocks once per call by glu_pack_kernel.
+#include <algorithm>
+#include <type_traits>
+
 #include "kron_internal.h"
 #include "row_tile.h"
 
@@ -100,6 +103,17 @@ __device__ inline float activate(int act, float v, float* d) {
   return v < 0.f ? 0.f : v;
 }
 
+// Of four values: the activation, and its derivative.
+template <bool GRAD>
+__device__ inline void activate4(int act, const f4& v, f4& out, f4& d) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float t = 0.f;
+    out[i] = activate<GRAD>(act, v[i], &t);
+    d[i] = t;
+  }
+}
+
 // ---------------------------------------------------------------------------------
 // The factors as operand blocks.  A table holds, for projection f and rank i, the blocks
 // [tile of 16 columns][step of 32 k][part], 64 lanes x 16 bytes each.
@@ -166,7 +180,12 @@ __global__ __launch_bounds__(256) void glu_pack_kernel(PackArgs a) {
 // Two products for each row: out (q x n) = sum_fi C_fi^T (X_f B_fi), with the gate at its end.
 //   MODE 0  y = act(g) o u           MODE 1  dg and du, from dy
 //   MODE 2  dX: the same products with X_f = d_f, B^T and C^T, summed over both projections
-// A wavefront takes RW rows and one 16-column tile of n, and for it all q (at most 64).
+// A wavefront owns a row and at most two of its n tiles: X in registers as operand parts, out in
+// accumulators (4 x 2 tiles of each projection).  The wavefronts of a workgroup share the factors,
+// which stream through two LDS buffers, one (f, i) at a time: the next one's blocks are on their way
+// (global to LDS directly) while this one's are multiplied.  Two workgroups a CU, so that one's
+// activations and memory run beside the other's products.  Few rows: the q tiles are spread over
+// gridDim.y workgroups.
 // ---------------------------------------------------------------------------------
 struct RowsArgs {
   int64_t N;
@@ -174,7 +193,7 @@ struct RowsArgs {
   int ldm;                 // elements from one row of X_f to the next
   int64_t ldx;             // elements from one X to the next
   int act;
-  int ntiles, qsplit;      // tiles of n; workgroups that share the q tiles
+  int qsplit;              // workgroups that share the q tiles
   const void* x[2];
   const u4* tb;            // B blocks
   const u4* tc;            // C blocks
@@ -185,171 +204,232 @@ struct RowsArgs {
   int n4;
 };
 
-constexpr int kQT = 4;
+constexpr int kTiles = 4;       // of 16: sides up to 64
 
 template <bool BF>
 __device__ inline float load1(const void* p, int64_t i) {
   return BF ? __uint_as_float((uint32_t)((const uint16_t*)p)[i] << 16) : ((const float*)p)[i];
 }
 
-// XBF: X is bf16 (one part); else fp32 in NX parts.  OBF: bias, dy and the output are bf16.
-template <int MODE, bool XBF, bool OBF, int NX, int NB, int NZ, int NC, int LIM, int MK, int RW>
-__global__ __launch_bounds__(256) void glu_rows_kernel(RowsArgs a) {
+// Four values from i on, of which the first `left` exist; vec: all do and the place is aligned.
+template <bool BF>
+__device__ inline f4 load4(const void* p, int64_t i, int left, bool vec) {
+  f4 r = f4{0.f, 0.f, 0.f, 0.f};
+  if (vec) {
+    if (!BF) return *reinterpret_cast<const f4*>((const float*)p + i);
+    typedef uint32_t u2v __attribute__((ext_vector_type(2)));
+    const u2v h = *reinterpret_cast<const u2v*>((const uint16_t*)p + i);
+    return f4{bf16_lo(h[0]), bf16_hi(h[0]), bf16_lo(h[1]), bf16_hi(h[1])};
+  }
+#pragma unroll
+  for (int v = 0; v < 4; ++v)
+    if (v < left) r[v] = load1<BF>(p, i + v);
+  return r;
+}
+
+// 1 KB (64 lanes x 16 bytes) from global memory into LDS at a wavefront-uniform place.
+__device__ inline void block_to_lds(const u4* src_lane, u4* dst) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src_lane,
+                                   (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+}
+
+// XBF: X is bf16 (one part); else fp32 in NX parts.  OBF: bias, dy and the output are bf16.  W wavefronts.
+template <int MODE, bool XBF, bool OBF, int NX, int NB, int NZ, int NC, int LIM, int MK, int PK, int W, int WPE>
+__global__ __launch_bounds__(64 * W, WPE) void glu_rows_kernel(RowsArgs a) {
   constexpr int NF = MODE == 2 ? 1 : 2;
-  const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
-  const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int nt = (int)(unit % a.ntiles);
-  const int64_t u2 = unit / a.ntiles;
-  const int qs = (int)(u2 % a.qsplit);
-  const int64_t row0 = (u2 / a.qsplit) * RW;
-  if (row0 >= a.N) return;
-  const int QT = (a.q + 15) / 16, PK = (a.p + 31) / 32;
-  const int qt0 = QT * qs / a.qsplit, qtn = QT * (qs + 1) / a.qsplit - qt0;
-  f4 acc[NF][kQT][RW];
+  extern __shared__ u4 lds[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, c = lane & 15;
+  const int QT = (a.q + 15) / 16, NT = (a.n + 15) / 16;
+  const int64_t unit = (int64_t)blockIdx.x * W + wave;
+  const int64_t row = NT > 2 ? unit >> 1 : unit;
+  const int nt0 = NT > 2 ? 2 * (int)(unit & 1) : 0, ntn = min(2, NT - nt0);
+  const bool live = row < a.N;
+  const int qt0 = QT * blockIdx.y / a.qsplit, qtn = QT * (blockIdx.y + 1) / a.qsplit - qt0;
+  const int nbB = NT * MK * NB, nbC = qtn * PK * NC, nb = nbB + nbC;      // blocks of a buffer
+
+  auto stage = [&](int fi) {
+    u4* dst = lds + (fi & 1) * nb * 64;
+    const u4* sb = a.tb + (int64_t)fi * NT * (MK * NB * 64) + lane;
+    const u4* sc = a.tc + (int64_t)(fi * QT + qt0) * (PK * NC * 64) + lane;
+    for (int b = wave; b < nb; b += W) block_to_lds(b < nbB ? sb + b * 64 : sc + (b - nbB) * 64, dst + b * 64);
+  };
+  stage(0);
+
+  Op xa[PK][2][MK][NX];
+  const bool vec = XBF ? (a.ldm & 7) == 0 : (a.ldm & 3) == 0;
+  auto load_x = [&](int f) {
+#pragma unroll
+    for (int pk = 0; pk < PK; ++pk)
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int mk = 0; mk < MK; ++mk) {
+          const int pi = 32 * pk + 16 * t + c, k = 32 * mk + 8 * g;
+          const int64_t at = row * a.ldx + (int64_t)pi * a.ldm + k;
+          const bool in = live && pi < a.p;
+          if (XBF) {
+            Op o;
+            o.u = u4{0u, 0u, 0u, 0u};
+            if (in && vec) {
+              if (k < a.m) o.u = *reinterpret_cast<const u4*>((const uint16_t*)a.x[f] + at);
+            } else if (in) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (k + e < a.m) o.u[e / 2] |= (uint32_t)((const uint16_t*)a.x[f])[at + e] << (16 * (e & 1));
+            }
+            xa[pk][t][mk][0] = o;
+          } else {
+            f4 lo = f4{0.f, 0.f, 0.f, 0.f}, hi = lo;
+            const float* xp = (const float*)a.x[f] + at;
+            if (in && vec) {
+              if (k < a.m) lo = *reinterpret_cast<const f4*>(xp);
+              if (k + 4 < a.m) hi = *reinterpret_cast<const f4*>(xp + 4);
+            } else if (in) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if (k + e < a.m) lo[e] = xp[e];
+                if (k + 4 + e < a.m) hi[e] = xp[4 + e];
+              }
+            }
+            split<NX>(lo, hi, xa[pk][t][mk]);
+          }
+        }
+  };
+
+  f4 acc[NF][kTiles][2];      // [projection][q tile][n tile]
 #pragma unroll
   for (int f = 0; f < NF; ++f)
 #pragma unroll
-    for (int j = 0; j < kQT; ++j)
+    for (int j = 0; j < kTiles; ++j)
 #pragma unroll
-      for (int w = 0; w < RW; ++w) acc[f][j][w] = f4{0.f, 0.f, 0.f, 0.f};
+      for (int t = 0; t < 2; ++t) acc[f][j][t] = f4{0.f, 0.f, 0.f, 0.f};
 
-  const bool vec = XBF ? (a.ldm & 7) == 0 : (a.ldm & 3) == 0;
-  for (int pk = 0; pk < PK; ++pk) {
-    Op xa[RW][2][MK][NX];
 #pragma unroll
-    for (int f = 0; f < 2; ++f) {
-      if (f == 0 || MODE == 2) {
+  for (int f = 0; f < 2; ++f) {
+    if (f == 0 || MODE == 2) load_x(f);
+    for (int i = 0; i < a.r; ++i) {
+      const int fi = f * a.r + i;
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");      // this (f, i)'s blocks have landed
+      __syncthreads();                                      // everybody's; and the other buffer has been read
+      if (fi + 1 < 2 * a.r) stage(fi + 1);
+      if (!live) continue;
+      const u4* tc = lds + (fi & 1) * nb * 64 + nbB * 64 + lane;
+      const u4* tb = tc + (nt0 * MK * NB - nbB) * 64;
 #pragma unroll
-        for (int w = 0; w < RW; ++w)
+      for (int pk = 0; pk < PK; ++pk) {
+        // (both n tiles always, so that no branch stands between the products: beside an odd last one, whatever
+        // the next blocks hold goes into accumulators that nothing reads)
+        Op zb[2][NZ];
+        f4 zt[2][2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) zt[t][0] = zt[t][1] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int mk = 0; mk < MK; ++mk) {
+          Op b[2][NB];
 #pragma unroll
           for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int mk = 0; mk < MK; ++mk) {
-              const int pi = 32 * pk + 16 * t + c, k = 32 * mk + 8 * g;
-              const int64_t at = (row0 + w) * a.ldx + (int64_t)pi * a.ldm + k;
-              const bool in = row0 + w < a.N && pi < a.p;
-              if (XBF) {
-                Op o;
-                o.u = u4{0u, 0u, 0u, 0u};
-                if (in && vec) {
-                  if (k < a.m) o.u = *reinterpret_cast<const u4*>((const uint16_t*)a.x[f] + at);
-                } else if (in) {
+            for (int s = 0; s < NB; ++s) b[t][s].u = tb[((t * MK + mk) * NB + s) * 64];
 #pragma unroll
-                  for (int e = 0; e < 8; ++e)
-                    if (k + e < a.m)
-                      o.u[e / 2] |= (uint32_t)((const uint16_t*)a.x[f])[at + e] << (16 * (e & 1));
-                }
-                xa[w][t][mk][0] = o;
-              } else {
-                f4 lo = f4{0.f, 0.f, 0.f, 0.f}, hi = lo;
-                const float* xp = (const float*)a.x[f] + at;
-                if (in && vec) {
-                  if (k < a.m) lo = *reinterpret_cast<const f4*>(xp);
-                  if (k + 4 < a.m) hi = *reinterpret_cast<const f4*>(xp + 4);
-                } else if (in) {
+          for (int o = LIM; o >= 0; --o)
 #pragma unroll
-                  for (int e = 0; e < 4; ++e) {
-                    if (k + e < a.m) lo[e] = xp[e];
-                    if (k + 4 + e < a.m) hi[e] = xp[4 + e];
-                  }
-                }
-                split<NX>(lo, hi, xa[w][t][mk]);
-              }
-            }
-      }
-      for (int i = 0; i < a.r; ++i) {
-        const int fi = f * a.r + i;
-        Op zb[RW][NZ];
-        {
-          f4 z[RW][2];
+            for (int s = 0; s < NX; ++s)
+              if (o - s >= 0 && o - s < NB)
 #pragma unroll
-          for (int w = 0; w < RW; ++w) z[w][0] = z[w][1] = f4{0.f, 0.f, 0.f, 0.f};
-          const u4* tb = a.tb + ((int64_t)(fi * a.ntiles + nt) * MK * NB) * 64 + lane;
+                for (int t = 0; t < 2; ++t)
 #pragma unroll
-          for (int mk = 0; mk < MK; ++mk) {
-            Op b[NB];
-#pragma unroll
-            for (int s = 0; s < NB; ++s) b[s].u = tb[(mk * NB + s) * 64];
-#pragma unroll
-            for (int w = 0; w < RW; ++w)
-#pragma unroll
-              for (int t = 0; t < 2; ++t) z[w][t] = dot<NX, NB, LIM>(xa[w][t][mk], b, z[w][t]);
-          }
-#pragma unroll
-          for (int w = 0; w < RW; ++w) split<NZ>(z[w][0], z[w][1], zb[w]);
+                  for (int h = 0; h < 2; ++h) zt[t][h] = mfma(xa[pk][h][mk][s], b[t][o - s], zt[t][h]);
         }
-        const u4* tc = a.tc + ((int64_t)(fi * QT + qt0) * PK + pk) * NC * 64 + lane;
 #pragma unroll
-        for (int j = 0; j < kQT; ++j)
-          if (j < qtn) {
-            Op b[NC];
+        for (int t = 0; t < 2; ++t) split<NZ>(zt[t][0], zt[t][1], zb[t]);
+        // the q tiles in twos as well (the terms of one order over four products before the next)
 #pragma unroll
-            for (int s = 0; s < NC; ++s) b[s].u = tc[((int64_t)j * PK * NC + s) * 64];
+        for (int j0 = 0; j0 < kTiles; j0 += 2)
+          if (j0 < qtn) {
+            Op b[2][NC];
 #pragma unroll
-            for (int w = 0; w < RW; ++w) acc[MODE == 2 ? 0 : f][j][w] = dot<NZ, NC, LIM>(zb[w], b, acc[MODE == 2 ? 0 : f][j][w]);
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int s = 0; s < NC; ++s) b[j][s].u = tc[(((j0 + j) * PK + pk) * NC + s) * 64];
+#pragma unroll
+            for (int o = LIM; o >= 0; --o)
+#pragma unroll
+              for (int s = 0; s < NZ; ++s)
+                if (o - s >= 0 && o - s < NC)
+#pragma unroll
+                  for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+                      acc[f % NF][j0 + j][t] = mfma(zb[t][s], b[j][o - s], acc[f % NF][j0 + j][t]);
           }
       }
     }
   }
-
-  const int n0 = 16 * nt + 4 * g;
+  // Out: a q tile at a time through the wavefront's own part of LDS, so that the lanes then take groups
+  // of four values in the order that they have in memory (whole lines out and, of dy, in).
+  __syncthreads();      // the factors have been read
+  if (!live) return;
+  const int w4 = min(a.n4 / 4 - 4 * nt0, 4 * ntn);      // groups of a q row
+  constexpr int ls = 32 + 4;                            // LDS floats of a q row
+  float* mine = reinterpret_cast<float*>(lds) + wave * (NF * 16 * ls);
   const int64_t qn = (int64_t)a.q * a.n;
   const bool ovec = (a.n & 3) == 0;
+  const float inv = 1.f / (float)w4;
 #pragma unroll
-  for (int j = 0; j < kQT; ++j) {
-    const int qi = 16 * (qt0 + j) + c;
-    if (j >= qtn || qi >= a.q || n0 >= a.n) continue;
-    const int64_t at = (int64_t)qi * a.n + n0;
-    float bg[4] = {0.f, 0.f, 0.f, 0.f}, bu[4] = {0.f, 0.f, 0.f, 0.f};
-    if (MODE != 2 && a.bias) {
+  for (int j = 0; j < kTiles; ++j) {
+    if (j >= qtn) break;
 #pragma unroll
-      for (int v = 0; v < 4; ++v)
-        if (n0 + v < a.n) {
-          bg[v] = load1<OBF>(a.bias, at + v);
-          bu[v] = load1<OBF>(a.bias, qn + at + v);
-        }
-    }
+    for (int f = 0; f < NF; ++f)
 #pragma unroll
-    for (int w = 0; w < RW; ++w) {
-      const int64_t row = row0 + w;
-      if (row >= a.N) continue;
-      const int64_t o = row * qn + at;
-      f4 out;
-      if (MODE == 1) {
+      for (int t = 0; t < 2; ++t)
+        if (t < ntn) *reinterpret_cast<f4*>(mine + (f * 16 + c) * ls + 16 * t + 4 * g) = acc[f][j][t];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    const int q0 = 16 * (qt0 + j), groups = min(16, a.q - q0) * w4;
+#pragma unroll 1
+    for (int e = lane; e < groups; e += 64) {
+      int qq = (int)((float)e * inv);      // e / w4: e < 256, off by one at most
+      int gi = e - qq * w4;
+      if (gi < 0) { gi += w4; --qq; }
+      if (gi >= w4) { gi -= w4; ++qq; }
+      const int n0 = 16 * nt0 + 4 * gi;
+      const int64_t at = (int64_t)(q0 + qq) * a.n + n0, o = row * qn + at;
+      f4 ag = *reinterpret_cast<const f4*>(mine + qq * ls + 4 * gi);
+      f4 au = *reinterpret_cast<const f4*>(mine + ((NF - 1) * 16 + qq) * ls + 4 * gi);
+      if (MODE != 2 && a.bias) {
+        ag += load4<OBF>(a.bias, at, a.n - n0, ovec);
+        au += load4<OBF>(a.bias, qn + at, a.n - n0, ovec);
+      }
+      if (MODE == 1) {      // (the padding of the workspace's rows gets zero: dy is zero there)
+        const f4 dy = load4<OBF>(a.dy, o, a.n - n0, ovec);
         f4 dg, du;
+        activate4<true>(a.act, ag, du, dg);
+        dg *= dy * au;
+        du *= dy;
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const float dy = n0 + v < a.n ? load1<OBF>(a.dy, o + v) : 0.f;
-          const float gv = acc[0][j][w][v] + bg[v], uv = acc[NF - 1][j][w][v] + bu[v];
-          float dact;
-          const float av = activate<true>(a.act, gv, &dact);
-          dg[v] = dy * uv * dact;
-          du[v] = dy * av;
-          if (n0 + v >= a.n) dg[v] = du[v] = 0.f;      // (the padding of the workspace's rows)
-        }
-        const int64_t od = (row * a.q + qi) * a.n4 + n0;
+        for (int v = 0; v < 4; ++v)
+          if (n0 + v >= a.n) dg[v] = du[v] = 0.f;
+        const int64_t od = (row * a.q + q0 + qq) * a.n4 + n0;
         *reinterpret_cast<f4*>(a.d[0] + od) = dg;
         *reinterpret_cast<f4*>(a.d[1] + od) = du;
         continue;
       }
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        if (MODE == 0)
-          out[v] = activate<false>(a.act, acc[0][j][w][v] + bg[v], nullptr) * (acc[NF - 1][j][w][v] + bu[v]);
-        else
-          out[v] = acc[0][j][w][v];
+      f4 out = ag;
+      if (MODE == 0) {
+        f4 unused;
+        activate4<false>(a.act, ag, out, unused);
+        out *= au;
       }
       if (OBF) {
         uint16_t* y = (uint16_t*)a.y + o;
-        const uint32_t h0 = bf16_rne(out[0]), h1 = bf16_rne(out[1]), h2 = bf16_rne(out[2]), h3 = bf16_rne(out[3]);
+        const uint32_t h0 = bf16_pair(out[0], out[1]), h1 = bf16_pair(out[2], out[3]);
         if (ovec) {
           typedef uint32_t u2v __attribute__((ext_vector_type(2)));
-          *reinterpret_cast<u2v*>(y) = u2v{h0 | (h1 << 16), h2 | (h3 << 16)};
+          *reinterpret_cast<u2v*>(y) = u2v{h0, h1};
         } else {
           y[0] = (uint16_t)h0;
-          if (n0 + 1 < a.n) y[1] = (uint16_t)h1;
-          if (n0 + 2 < a.n) y[2] = (uint16_t)h2;
-          if (n0 + 3 < a.n) y[3] = (uint16_t)h3;
+          if (n0 + 1 < a.n) y[1] = (uint16_t)(h0 >> 16);
+          if (n0 + 2 < a.n) y[2] = (uint16_t)h1;
+          if (n0 + 3 < a.n) y[3] = (uint16_t)(h1 >> 16);
         }
       } else {
         float* y = (float*)a.y + o;
@@ -362,19 +442,25 @@ __global__ __launch_bounds__(256) void glu_rows_kernel(RowsArgs a) {
         }
       }
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
 }
 
 // ---------------------------------------------------------------------------------
-// The factors' gradients.  A workgroup takes rows in turn; each of its wavefronts owns one of
-//   dC_fi (p x q) += Z_fi d_f^T, Z_fi = X B_fi       dB_fi (m x n) += X^T G_fi, G_fi = C_fi d_f
-// in registers.  A row's X and d_f are split into parts once and staged in LDS as operand blocks
-// in both orders that the products contract over.
+// The factors' gradients.  A workgroup has one kind and a group of pairs (f, i):
+//   kind 0  dC_fi (p x q) += Z_fi d_f^T, Z_fi = X B_fi       kind 1  dB_fi (m x n) += X^T G_fi, G_fi = C_fi d_f
+// Each wavefront owns a pair's sum in registers, with B_fi (or C_fi) beside it; with fewer pairs than
+// wavefronts several share a pair and take rows in turn.  A step's rows of X and d_f are split
+// into parts once and staged in LDS as operand blocks in the order that the kind contracts over (4 x 4
+// patches, which a thread turns in its registers); the next step's values are loaded while this
+// one's are multiplied.
 // ---------------------------------------------------------------------------------
 struct ParamArgs {
   int64_t N;
   int p, q, m, n, r, n4;
   int64_t rows;            // rows of a workgroup
+  int rs;                  // rows of a step
+  int share;               // wavefronts of a pair
   const void* x;
   const float* d[2];
   const u4* tb;            // B blocks (k = m)
@@ -382,40 +468,50 @@ struct ParamArgs {
   float* part;             // partial rows: dB (2 r m n) | dC (2 r p q) | dbias (2 q n)
 };
 
-constexpr int kPPW = 4;    // pairs (f, i) of a workgroup: wavefronts 0..3 take dC, 4..7 dB
+// Sizes of a step that both the host and the kernel use.
+struct ParamSizes {
+  int PT, QT, MT, NT, PK, QK, MK, NK;
+  int dk, dpat, xk, xpat;          // patches
+  int xa, ya;                      // u4 of a row's X blocks, and of one d_f's
+  __host__ __device__ ParamSizes(const ParamArgs& a, int nx, int kind) {
+    PT = (a.p + 15) / 16; QT = (a.q + 15) / 16; MT = (a.m + 15) / 16; NT = (a.n + 15) / 16;
+    PK = (a.p + 31) / 32; QK = (a.q + 31) / 32; MK = (a.m + 31) / 32; NK = (a.n + 31) / 32;
+    dk = a.n4 / 4; dpat = (a.q + 3) / 4 * dk;
+    xk = (a.m + 3) / 4; xpat = (a.p + 3) / 4 * xk;
+    // [k step][tile][part].  Kind 0: X k = m, p tiles; d_f k = n, q tiles.  Kind 1: X k = p, m tiles; d_f k = q,
+    // n tiles.  The tiles of the inner loops (p and n) are made even.
+    xa = (kind == 0 ? MK * 2 * PK : PK * MT) * nx * 64;
+    ya = (kind == 0 ? NK * QT : QK * 2 * NK) * 3 * 64;
+  }
+  __host__ __device__ int row(int nf) const { return xa + nf * ya; }
+};
 
-template <bool XBF, int NX, int NB, int NC>
-__global__ __launch_bounds__(512) void glu_param_kernel(ParamArgs a) {
-  extern __shared__ u4 lds[];
+template <bool XBF, int NX, int NT_, int KIND, int NTH>
+__device__ inline void param_body(const ParamArgs& a, int group, int groups, const u4* table, u4* lds) {
   constexpr int NY = 3;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, c = lane & 15;
-  const int PT = (a.p + 15) / 16, QT = (a.q + 15) / 16, MT = (a.m + 15) / 16, NT = (a.n + 15) / 16;
-  const int PK = (a.p + 31) / 32, QK = (a.q + 31) / 32, MK = (a.m + 31) / 32, NK = (a.n + 31) / 32;
-  const int pair0 = blockIdx.y * kPPW, pairs = 2 * a.r;
-  const int pairn = min(kPPW, pairs - pair0);
-  const int f_lo = pair0 / a.r, f_hi = (pair0 + pairn - 1) / a.r;
-  // LDS: XA [PT][MK][NX] k = m; XB [MT][PK][NX] k = p; for each f: YA [QT][NK][NY] k = n; YB [NT][QK][NY] k = q
-  const int xa0 = 0, xb0 = xa0 + PT * MK * NX * 64, y0 = xb0 + MT * PK * NX * 64;
-  const int ysz = (QT * NK + NT * QK) * NY * 64;
-  const int all = y0 + ysz * (f_hi - f_lo + 1);
-  for (int i = tid; i < all; i += 512) lds[i] = u4{0u, 0u, 0u, 0u};      // the tiles' padding stays zero
+  constexpr int SLOTS = (1024 + NTH - 1) / NTH;            // patches of a thread: at most 1024 a step
+  constexpr int BS = 512 / NTH;                            // of them of d_f: at most 512
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4, c = lane & 15;
+  const ParamSizes z(a, NX, KIND);
+  const int pairs = 2 * a.r, ppw = (pairs + groups - 1) / groups, pair0 = group * ppw;
+  const int pairn = min(ppw, pairs - pair0);
+  const int f_lo = pair0 / a.r, nf = (pair0 + pairn - 1) / a.r - f_lo + 1;
+  const int area = z.row(nf);
+  for (int i = tid; i < area * a.rs; i += NTH) lds[i] = u4{0u, 0u, 0u, 0u};      // the tiles' padding stays zero
 
-  const int pl = wave % kPPW, kind = wave / kPPW;
-  const bool active = pl < pairn;
+  const int pl = wave % ppw, sub = wave / ppw;
+  const bool active = pl < pairn && sub < a.share;
   const int fi = pair0 + (active ? pl : 0), f = fi / a.r;
-  Op tab[4][2][3];         // kind 0: B_fi [NT][MK]; kind 1: C_fi^T [PT][QK]
+  Op tab[4][2][NT_];       // kind 0: B_fi [NT][MK]; kind 1: C_fi^T [PT][QK]
+  const int tabT = KIND == 0 ? z.NT : z.PT, tabK = KIND == 0 ? z.MK : z.QK;
 #pragma unroll
   for (int t = 0; t < 4; ++t)
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
-      for (int s = 0; s < 3; ++s) {
+      for (int s = 0; s < NT_; ++s) {
         tab[t][k][s].u = u4{0u, 0u, 0u, 0u};
-        if (kind == 0) {
-          if (s < NB && t < NT && k < MK) tab[t][k][s].u = a.tb[((int64_t)((fi * NT + t) * MK + k) * NB + s) * 64 + lane];
-        } else {
-          if (s < NC && t < PT && k < QK) tab[t][k][s].u = a.tc[((int64_t)((fi * PT + t) * QK + k) * NC + s) * 64 + lane];
-        }
+        if (t < tabT && k < tabK) tab[t][k][s].u = table[((int64_t)((fi * tabT + t) * tabK + k) * NT_ + s) * 64 + lane];
       }
   f4 acc[4][4];
 #pragma unroll
@@ -423,187 +519,222 @@ __global__ __launch_bounds__(512) void glu_param_kernel(ParamArgs a) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f4{0.f, 0.f, 0.f, 0.f};
 
-  // 4 x 4 patches of a row's matrices: of d_f first (at most 512: one a thread), then of X
-  const int dj = (a.q + 3) / 4, dk = a.n4 / 4, dpat = dj * dk;
-  const int xj = (a.p + 3) / 4, xk = (a.m + 3) / 4, xpat = xj * xk;
-  const int nf = f_hi - f_lo + 1, npat = nf * dpat + xpat;
-  float bsum[16];
+  // patches of a step: those of d_f of all its rows, then those of X
+  const int nd = nf * z.dpat, ndall = a.rs * nd, npat = ndall + a.rs * z.xpat;
+  float bsum[BS][16];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) bsum[e] = 0.f;
-  const bool xvec = XBF ? (a.m & 3) == 0 : (a.m & 3) == 0;
-
+  for (int b = 0; b < BS; ++b)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) bsum[b][e] = 0.f;
+  const bool xvec = (a.m & 3) == 0;
   const int64_t r0 = (int64_t)blockIdx.x * a.rows, r1 = min(a.N, r0 + a.rows);
-  for (int64_t row = r0; row < r1; ++row) {
-    __syncthreads();       // the previous row's operands have been read
-    for (int pt = tid; pt < npat; pt += 512) {
-      f4 v[4];
-      int j0, k0;
-      const bool isd = pt < nf * dpat;
-      if (isd) {
-        const int ff = pt / dpat, e = pt - ff * dpat;
-        j0 = 4 * (e / dk);
-        k0 = 4 * (e % dk);
-        const float* src = a.d[f_lo + ff] + (row * a.q + j0) * a.n4 + k0;
+
+  f4 v[SLOTS][4];
+  auto fetch = [&](int64_t step) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          v[i] = j0 + i < a.q ? *reinterpret_cast<const f4*>(src + (int64_t)i * a.n4) : f4{0.f, 0.f, 0.f, 0.f};
-        if (pt == tid) {
+    for (int s = 0; s < SLOTS; ++s) {
+      const int pt = tid + s * NTH;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[s][i] = f4{0.f, 0.f, 0.f, 0.f};
+      if (pt < ndall) {
+        const int rr = pt / nd, e = pt % nd, ff = e / z.dpat, o = e % z.dpat;
+        const int j0 = 4 * (o / z.dk), k0 = 4 * (o % z.dk);
+        const int64_t row = step + rr;
+        const float* src = a.d[f_lo + ff] + (row * a.q + j0) * a.n4 + k0;
+        if (row < r1) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e2 = 0; e2 < 4; ++e2) bsum[4 * i + e2] += v[i][e2];
+            if (j0 + i < a.q) v[s][i] = *reinterpret_cast<const f4*>(src + i * a.n4);
         }
-      } else {
-        const int e = pt - nf * dpat;
-        j0 = 4 * (e / xk);
-        k0 = 4 * (e % xk);
-        const int64_t src = (row * a.p + j0) * a.m + k0;
+      } else if (pt < npat) {
+        const int rr = (pt - ndall) / z.xpat, o = (pt - ndall) % z.xpat;
+        const int j0 = 4 * (o / z.xk), k0 = 4 * (o % z.xk);
+        const int64_t row = step + rr, src = (row * a.p + j0) * a.m + k0;
+        if (row < r1) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v[i] = f4{0.f, 0.f, 0.f, 0.f};
-          if (j0 + i < a.p) {
-            if (!XBF && xvec) {
-              v[i] = *reinterpret_cast<const f4*>((const float*)a.x + src + (int64_t)i * a.m);
+          for (int i = 0; i < 4; ++i) {
+            if (j0 + i >= a.p) continue;
+            if (xvec && XBF) {
+              typedef uint32_t u2v __attribute__((ext_vector_type(2)));
+              const u2v h = *reinterpret_cast<const u2v*>((const uint16_t*)a.x + src + i * a.m);
+              v[s][i] = f4{bf16_lo(h[0]), bf16_hi(h[0]), bf16_lo(h[1]), bf16_hi(h[1])};
+            } else if (xvec) {
+              v[s][i] = *reinterpret_cast<const f4*>((const float*)a.x + src + i * a.m);
             } else {
 #pragma unroll
-              for (int e2 = 0; e2 < 4; ++e2)
-                if (k0 + e2 < a.m) v[i][e2] = load1<XBF>(a.x, src + (int64_t)i * a.m + e2);
+              for (int e = 0; e < 4; ++e)
+                if (k0 + e < a.m) v[s][i][e] = load1<XBF>(a.x, src + i * a.m + e);
             }
           }
         }
       }
-      // into the blocks: [column tile][k step][part], lane (g, c), slots 0..3 or 4..7
-      const int np = isd ? NY : NX;
-      const int ff = isd ? pt / dpat : 0;
-      const int baseA = isd ? y0 + ff * ysz : xa0, baseB = isd ? y0 + ff * ysz + QT * NK * NY * 64 : xb0;
-      const int ksA = isd ? NK : MK, ksB = isd ? QK : PK;
-      typedef uint32_t u2v __attribute__((ext_vector_type(2)));
-      u2v* l2 = reinterpret_cast<u2v*>(lds);
-      // order A: k along the row.  d_f: chained; X: natural (its partner is the packed B)
-      const int kk = k0 & 31;
-      const int gA = isd ? (kk & 15) >> 2 : kk >> 3, hA = isd ? kk >> 4 : (kk >> 2) & 1;
-      // order B: k down the column, chained
-      const int jj = j0 & 31;
-      const int gB = (jj & 15) >> 2, hB = jj >> 4;
-      for (int s = 0; s < np; ++s) {
+    }
+  };
+  // A patch (rows j0.., columns k0..) into blocks [k step][tile][part], lane (g, c), slots 0..3 or 4..7.
+  // Kind 0 contracts along the row, kind 1 down the column; chained order, but X of kind 0 natural (its
+  // partner is the packed B).
+  auto place = [&](const f4 (&w)[4], int j0, int k0, int base, int tiles, bool natural, int np) {
+    typedef uint32_t u2v __attribute__((ext_vector_type(2)));
+    u2v* l2 = reinterpret_cast<u2v*>(lds);
+    const int kc = KIND == 0 ? k0 : j0, cc = KIND == 0 ? j0 : k0, kk = kc & 31;
+    const int gg = natural ? kk >> 3 : (kk & 15) >> 2, h = natural ? (kk >> 2) & 1 : kk >> 4;
+    const int at = 2 * (base + (((kc >> 5) * tiles + (cc >> 4)) * np) * 64 + gg * 16 + (cc & 15)) + h;
+    f4 u[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int j = j0 + i;
-          const int blk = baseA + (((j >> 4) * ksA + (k0 >> 5)) * np + s) * 64 + gA * 16 + (j & 15);
-          if (j < 16 * (isd ? QT : PT)) l2[2 * blk + hA] = u2v{tops(v[i][0], v[i][1]), tops(v[i][2], v[i][3])};
-        }
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int k = k0 + i;
-          const int blk = baseB + (((k >> 4) * ksB + (j0 >> 5)) * np + s) * 64 + gB * 16 + (k & 15);
-          l2[2 * blk + hB] = u2v{tops(v[0][i], v[1][i]), tops(v[2][i], v[3][i])};
-        }
+      for (int e = 0; e < 4; ++e) u[i][e] = KIND == 0 ? w[i][e] : w[e][i];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+    for (int s = 0; s < 3; ++s) {
+      if (s >= np) break;
 #pragma unroll
-          for (int e2 = 0; e2 < 4; ++e2) v[i][e2] -= top(v[i][e2]);
+      for (int i = 0; i < 4; ++i) {
+        l2[at + 128 * s + 2 * i] = u2v{tops(u[i][0], u[i][1]), tops(u[i][2], u[i][3])};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[i][e] -= top(u[i][e]);
       }
     }
+  };
+  auto store = [&]() {
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s) {
+      const int pt = tid + s * NTH;
+      if (pt < ndall) {
+        const int rr = pt / nd, e = pt % nd, ff = e / z.dpat, o = e % z.dpat;
+        place(v[s], 4 * (o / z.dk), 4 * (o % z.dk), rr * area + z.xa + ff * z.ya, KIND == 0 ? z.QT : 2 * z.NK, false, NY);
+        if (KIND == 0 && s < BS) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) bsum[s < BS ? s : 0][i] += v[s][i / 4][i % 4];
+        }
+      } else if (pt < npat) {
+        const int rr = (pt - ndall) / z.xpat, o = (pt - ndall) % z.xpat;
+        place(v[s], 4 * (o / z.xk), 4 * (o % z.xk), rr * area, KIND == 0 ? 2 * z.PK : z.MT, KIND == 0, NX);
+      }
+    }
+  };
+  // One row's products.  First product: into tile pairs; the inner tiles of the second (p or n) in twos, so
+  // that no branch stands between the products (an odd one's blocks are zero).
+  auto multiply = [&](auto count, const u4* xl, const u4* yl) {
+    constexpr int TI = decltype(count)::value;
+    const int steps = KIND == 0 ? z.NK : z.PK;
+#pragma unroll
+    for (int ko = 0; ko < 2; ++ko)
+      if (ko < steps) {
+        Op h[TI][3];
+#pragma unroll
+        for (int t = 0; t < TI; ++t) {
+          f4 w[2];
+          w[0] = w[1] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            if (k < tabK) {
+              if (KIND == 0) {
+                Op x[NX];
+#pragma unroll
+                for (int s = 0; s < NX; ++s) x[s].u = xl[k * 2 * z.PK * NX * 64 + (t * NX + s) * 64];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) w[u] = dot<NT_, NX, 2>(tab[2 * ko + u][k], x, w[u]);
+              } else {
+                Op y[NY];
+#pragma unroll
+                for (int s = 0; s < NY; ++s) y[s].u = yl[k * 2 * z.NK * NY * 64 + (t * NY + s) * 64];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) w[u] = dot<NT_, NY, 2>(tab[2 * ko + u][k], y, w[u]);
+              }
+            }
+          split<3>(w[0], w[1], h[t]);
+        }
+        const int outer = KIND == 0 ? z.QT : z.MT;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          if (t < outer) {
+            constexpr int NO = KIND == 0 ? NY : NX;
+            Op y[NO];
+#pragma unroll
+            for (int s = 0; s < NO; ++s)
+              y[s].u = KIND == 0 ? yl[ko * z.QT * NY * 64 + (t * NY + s) * 64] : xl[ko * z.MT * NX * 64 + (t * NX + s) * 64];
+#pragma unroll
+            for (int o = 2; o >= 0; --o)
+#pragma unroll
+              for (int s = 0; s <= o; ++s)
+                if (o - s < NO)
+#pragma unroll
+                  for (int i = 0; i < TI; ++i) {
+                    if (KIND == 0) acc[i][t] = mfma(h[i][s], y[o - s], acc[i][t]);
+                    if (KIND == 1) acc[t][i] = mfma(y[o - s], h[i][s], acc[t][i]);
+                  }
+          }
+      }
+  };
+
+  fetch(r0);
+  for (int64_t step = r0; step < r1; step += a.rs) {
+    __syncthreads();       // the previous step's operands have been read
+    store();
     __syncthreads();
+    if (step + a.rs < r1) fetch(step + a.rs);
     if (!active) continue;
-    const u4* ya = lds + y0 + (f - f_lo) * ysz;
-    const u4* yb = ya + QT * NK * NY * 64;
-    if (kind == 0) {
-#pragma unroll
-      for (int nk = 0; nk < 2; ++nk)
-        if (nk < NK) {
-          Op zp[4][3];
-#pragma unroll
-          for (int pt = 0; pt < 4; ++pt)
-            if (pt < PT) {
-              f4 z[2];
-              z[0] = z[1] = f4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-              for (int mk = 0; mk < 2; ++mk)
-                if (mk < MK) {
-                  Op x[NX];
-#pragma unroll
-                  for (int s = 0; s < NX; ++s) x[s].u = lds[xa0 + ((pt * MK + mk) * NX + s) * 64 + lane];
-#pragma unroll
-                  for (int t = 0; t < 2; ++t) z[t] = dot<NB, NX, 2>(tab[2 * nk + t][mk], x, z[t]);
-                }
-              split<3>(z[0], z[1], zp[pt]);
-            }
-#pragma unroll
-          for (int qt = 0; qt < 4; ++qt)
-            if (qt < QT) {
-              Op y[NY];
-#pragma unroll
-              for (int s = 0; s < NY; ++s) y[s].u = ya[((qt * NK + nk) * NY + s) * 64 + lane];
-#pragma unroll
-              for (int pt = 0; pt < 4; ++pt)
-                if (pt < PT) acc[pt][qt] = dot<3, NY, 2>(zp[pt], y, acc[pt][qt]);
-            }
-        }
-    } else {
-#pragma unroll
-      for (int pk = 0; pk < 2; ++pk)
-        if (pk < PK) {
-          Op gp[4][3];
-#pragma unroll
-          for (int nt = 0; nt < 4; ++nt)
-            if (nt < NT) {
-              f4 z[2];
-              z[0] = z[1] = f4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-              for (int qk = 0; qk < 2; ++qk)
-                if (qk < QK) {
-                  Op y[NY];
-#pragma unroll
-                  for (int s = 0; s < NY; ++s) y[s].u = yb[((nt * QK + qk) * NY + s) * 64 + lane];
-#pragma unroll
-                  for (int t = 0; t < 2; ++t) z[t] = dot<NC, NY, 2>(tab[2 * pk + t][qk], y, z[t]);
-                }
-              split<3>(z[0], z[1], gp[nt]);
-            }
-#pragma unroll
-          for (int mt = 0; mt < 4; ++mt)
-            if (mt < MT) {
-              Op x[NX];
-#pragma unroll
-              for (int s = 0; s < NX; ++s) x[s].u = lds[xb0 + ((mt * PK + pk) * NX + s) * 64 + lane];
-#pragma unroll
-              for (int nt = 0; nt < 4; ++nt)
-                if (nt < NT) acc[mt][nt] = dot<NX, 3, 2>(x, gp[nt], acc[mt][nt]);
-            }
-        }
+    for (int rr = sub; rr < a.rs; rr += a.share) {
+      const u4* xl = lds + rr * area + lane;
+      const u4* yl = xl + z.xa + (f - f_lo) * z.ya;
+      if ((KIND == 0 ? z.PT : z.NT) > 2)
+        multiply(std::integral_constant<int, 4>{}, xl, yl);
+      else
+        multiply(std::integral_constant<int, 2>{}, xl, yl);
     }
   }
 
-  // this workgroup's partial row
+  // partial rows: one for each wavefront of a pair
   const int64_t mn = (int64_t)a.m * a.n, pq = (int64_t)a.p * a.q;
-  const PartRow out{a.part, (int64_t)gridDim.x, (int64_t)blockIdx.x, 0};
+  const PartRow out{a.part, (int64_t)gridDim.x * a.share, (int64_t)blockIdx.x * a.share + (active ? sub : 0), 0};
   if (active) {
-    const int R = kind == 0 ? a.p : a.m, Cn = kind == 0 ? a.q : a.n;
-    const int64_t base = kind == 0 ? pairs * mn + fi * pq : fi * mn;
+    const int R = KIND == 0 ? a.p : a.m, Cn = KIND == 0 ? a.q : a.n;
+    const int64_t base = KIND == 0 ? pairs * mn + fi * pq : fi * mn;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int ri = 16 * i + 4 * g + v, ci = 16 * j + c;
-          if (ri < R && ci < Cn) out[base + (int64_t)ri * Cn + ci] = acc[i][j][v];
+        for (int e = 0; e < 4; ++e) {
+          const int ri = 16 * i + 4 * g + e, ci = 16 * j + c;
+          if (ri < R && ci < Cn) out[base + (int64_t)ri * Cn + ci] = acc[i][j][e];
         }
   }
-  if (tid < nf * dpat) {
-    const int ff = f_lo + tid / dpat, e = tid % dpat;
-    if (ff * a.r >= pair0 && ff * a.r < pair0 + pairn) {      // the workgroup with f's first pair
+  if (KIND != 0) return;
+  // dbias: the sums of a step's rows are joined in LDS (row 0's threads first: a fixed order)
+  float* bl = reinterpret_cast<float*>(lds);
+  for (int rr = 0; rr < a.rs; ++rr) {
+    __syncthreads();
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+    for (int s = 0; s < BS; ++s) {
+      const int pt = tid + s * NTH;
+      if (pt < ndall && pt / nd == rr) {
 #pragma unroll
-        for (int e2 = 0; e2 < 4; ++e2) {
-          const int j = 4 * (e / dk) + i, k = 4 * (e % dk) + e2;
-          if (j < a.q && k < a.n)
-            out[pairs * (mn + pq) + (int64_t)ff * a.q * a.n + (int64_t)j * a.n + k] = bsum[4 * i + e2];
-        }
+        for (int e = 0; e < 16; ++e) bl[(pt % nd) * 16 + e] = bsum[s][e] + (rr ? bl[(pt % nd) * 16 + e] : 0.f);
+      }
     }
   }
+  __syncthreads();
+  for (int i = tid; i < nd * 16; i += NTH) {
+    const int e = i >> 4, ff = f_lo + e / z.dpat, o = e % z.dpat;
+    const int j = 4 * (o / z.dk) + ((i >> 2) & 3), k = 4 * (o % z.dk) + (i & 3);
+    // (the workgroup with the projection's first pair; its other partial rows have nothing to add)
+    if (ff * a.r >= pair0 && ff * a.r < pair0 + pairn && j < a.q && k < a.n)
+      for (int w = 0; w < a.share; ++w) {
+        const PartRow ow{a.part, (int64_t)gridDim.x * a.share, (int64_t)blockIdx.x * a.share + w, 0};
+        ow[pairs * (mn + pq) + (int64_t)ff * a.q * a.n + (int64_t)j * a.n + k] = w == 0 ? bl[i] : 0.f;
+      }
+  }
+}
+
+template <bool XBF, int NX, int NB, int NC, int NTH>
+__global__ __launch_bounds__(NTH) void glu_param_kernel(ParamArgs a) {
+  extern __shared__ u4 lds[];
+  const int groups = gridDim.y / 2;
+  if ((int)blockIdx.y < groups)
+    param_body<XBF, NX, NB, 0, NTH>(a, blockIdx.y, groups, a.tb, lds);
+  else
+    param_body<XBF, NX, NC, 1, NTH>(a, blockIdx.y - groups, groups, a.tc, lds);
 }
 
 // dA = S o dC, dS = sum_i A_i o dC_i from the summed dC (2 x r x p x q).
@@ -629,7 +760,7 @@ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 struct Sizes {
   int parts_b, parts_c;
   int64_t lanes[4], bytes[4];
-  int n4, groups;
+  int n4, groups, waves, share;
   int64_t PW, off_d, off_part, off_dc, fwd_bytes, bwd_bytes;
 };
 
@@ -648,13 +779,16 @@ Sizes sizes_of(const GluArgs& a) {
   z.n4 = (a.n + 3) & ~3;
   z.off_d = (off + 255) & ~int64_t(255);
   z.off_part = z.off_d + ((2 * a.N * a.q * z.n4 * 4 + 255) & ~int64_t(255));
-  const int Y = ceil_div(2 * a.r, kPPW);
-  // one workgroup a CU (its LDS), every one with at least four rows where there are that many
-  int64_t G = 256 / Y;
+  // the parameters' kernel: fp32 in four wavefronts (its parts take the registers of two), bf16 in eight;
+  // one workgroup a CU (its LDS), each with at least four rows where there are that many
+  z.waves = a.bf16 ? 8 : 4;
+  z.share = 1;
+  while (2 * z.share * 2 * a.r <= z.waves) z.share *= 2;
+  int64_t G = 256 / (2 * ceil_div(2 * a.r, z.waves / z.share));
   if (G > (a.N + 3) / 4) G = (a.N + 3) / 4;
   z.groups = G < 1 ? 1 : (int)G;
   z.PW = (int64_t)2 * a.r * (a.m * a.n + a.p * a.q) + 2 * a.q * a.n;
-  z.off_dc = z.off_part + ((part_floats(z.groups, z.PW) * 4 + 255) & ~int64_t(255));
+  z.off_dc = z.off_part + ((part_floats(z.groups * z.share, z.PW) * 4 + 255) & ~int64_t(255));
   z.bwd_bytes = z.off_dc + (int64_t)2 * a.r * a.p * a.q * 4;
   return z;
 }
@@ -671,34 +805,60 @@ hipError_t launch_pack(const GluArgs& a, const Sizes& z, int tables, u4* const t
   return hipGetLastError();
 }
 
-template <int MODE, bool XBF, bool OBF, int NX, int NB, int NZ, int NC, int LIM>
-hipError_t launch_rows(RowsArgs k, hipStream_t s) {
-  constexpr int RW = 2;
-  k.ntiles = ceil_div(k.n, 16);
-  const int QT = ceil_div(k.q, 16);
-  const int64_t groups = (k.N + RW - 1) / RW;
+template <int MODE, bool XBF, bool OBF, int NX, int NB, int NZ, int NC, int LIM, int MK, int PK>
+hipError_t launch_rows_k(RowsArgs k, hipStream_t s) {
+  // two workgroups of eight wavefronts a CU (128 registers), one where the parts of a wide X need more
+  constexpr int W = 8, WPE = (NX == 3 ? MK * PK == 1 : MK * PK < 4 || NZ < 3) ? 4 : 2;
+  constexpr auto kernel = glu_rows_kernel<MODE, XBF, OBF, NX, NB, NZ, NC, LIM, MK, PK, W, WPE>;
+  const int NT = ceil_div(k.n, 16), QT = ceil_div(k.q, 16);
+  const int64_t units = k.N * (NT > 2 ? 2 : 1), groups = (units + W - 1) / W;
+  // few rows: the q tiles of a row are spread until there are 256 workgroups
   k.qsplit = 1;
-  while (k.qsplit < QT && groups * k.ntiles * k.qsplit < 1024) ++k.qsplit;
-  const int64_t units = groups * k.ntiles * k.qsplit;
-  const dim3 grid((unsigned)((units + 3) / 4));
-  if (k.m <= 32)
-    hipLaunchKernelGGL((glu_rows_kernel<MODE, XBF, OBF, NX, NB, NZ, NC, LIM, 1, RW>), grid, dim3(256), 0, s, k);
-  else
-    hipLaunchKernelGGL((glu_rows_kernel<MODE, XBF, OBF, NX, NB, NZ, NC, LIM, 2, RW>), grid, dim3(256), 0, s, k);
+  while (k.qsplit < QT && groups * k.qsplit < 256) ++k.qsplit;
+  // two buffers, and the blocks beside an odd last tile; out goes through the same LDS
+  constexpr size_t kOut = (size_t)W * (MODE == 2 ? 1 : 2) * 16 * 36 * 4;
+  const size_t need = (size_t)(2 * (NT * MK * NB + ceil_div(QT, k.qsplit) * PK * NC) + MK * NB + PK * NC) * 1024;
+  const size_t lds = std::max(need, kOut);
+  static const hipError_t attr =
+      hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
+                          (int)std::max(kOut, (size_t)((2 * kTiles + 1) * (MK * NB + PK * NC)) * 1024));
+  if (attr != hipSuccess) return attr;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)groups, (unsigned)k.qsplit), dim3(64 * W), lds, s, k);
   return hipGetLastError();
 }
 
-template <bool XBF, int NX, int NB, int NC>
-hipError_t launch_param(const ParamArgs& k, int G, hipStream_t s) {
-  const int PT = ceil_div(k.p, 16), QT = ceil_div(k.q, 16), MT = ceil_div(k.m, 16), NT = ceil_div(k.n, 16);
-  const int PK = ceil_div(k.p, 32), QK = ceil_div(k.q, 32), MK = ceil_div(k.m, 32), NK = ceil_div(k.n, 32);
-  const int nf = k.r >= 4 && k.r % kPPW == 0 ? 1 : 2;
-  const size_t lds = (size_t)((PT * MK + MT * PK) * NX + nf * (QT * NK + NT * QK) * 3) * 1024;
-  static const hipError_t attr = hipFuncSetAttribute((const void*)glu_param_kernel<XBF, NX, NB, NC>,
+template <int MODE, bool XBF, bool OBF, int NX, int NB, int NZ, int NC, int LIM>
+hipError_t launch_rows(const RowsArgs& k, hipStream_t s) {
+  if (k.m <= 32)
+    return k.p <= 32 ? launch_rows_k<MODE, XBF, OBF, NX, NB, NZ, NC, LIM, 1, 1>(k, s)
+                     : launch_rows_k<MODE, XBF, OBF, NX, NB, NZ, NC, LIM, 1, 2>(k, s);
+  return k.p <= 32 ? launch_rows_k<MODE, XBF, OBF, NX, NB, NZ, NC, LIM, 2, 1>(k, s)
+                   : launch_rows_k<MODE, XBF, OBF, NX, NB, NZ, NC, LIM, 2, 2>(k, s);
+}
+
+template <bool XBF, int NX, int NB, int NC, int NTH>
+hipError_t launch_param(ParamArgs k, const Sizes& sz, hipStream_t s) {
+  k.rows = (k.N + sz.groups - 1) / sz.groups;
+  k.share = sz.share;
+  const int Y = ceil_div(2 * k.r, sz.waves / sz.share), ppw = ceil_div(2 * k.r, Y);
+  int nf = 1;      // most projections of a workgroup
+  for (int y = 0; y < Y; ++y)
+    if ((std::min(2 * k.r, (y + 1) * ppw) - 1) / k.r != y * ppw / k.r) nf = 2;
+  // as many rows a step as LDS and the threads' slots hold (but no more than four a wavefront)
+  const ParamSizes z0(k, NX, 0), z1(k, NX, 1);
+  const size_t one = (size_t)std::max(z0.row(nf), z1.row(nf)) * 16;
+  const int nd = nf * z0.dpat, np = nd + z0.xpat;
+  k.rs = 1;
+  while (k.rs < 4 * k.share && k.rs < k.rows && (k.rs + 1) * one <= 160 * 1024 && (k.rs + 1) * nd <= 512 &&
+         (k.rs + 1) * np <= 1024)
+    ++k.rs;
+  static const hipError_t attr = hipFuncSetAttribute((const void*)glu_param_kernel<XBF, NX, NB, NC, NTH>,
                                                      hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
   if (attr != hipSuccess) return attr;
-  hipLaunchKernelGGL((glu_param_kernel<XBF, NX, NB, NC>), dim3((unsigned)G, (unsigned)ceil_div(2 * k.r, kPPW)),
-                     dim3(512), lds, s, k);
+  // (dbias is joined in the same LDS: 64 bytes a patch of d_f)
+  const size_t lds = std::max(one * k.rs, (size_t)nd * 64);
+  hipLaunchKernelGGL((glu_param_kernel<XBF, NX, NB, NC, NTH>), dim3((unsigned)sz.groups, (unsigned)(2 * Y)), dim3(NTH),
+                     lds, s, k);
   return hipGetLastError();
 }
 
@@ -717,7 +877,7 @@ hipError_t launch_glu_fwd(const GluArgs& a, void* ws, hipStream_t s) {
   RowsArgs k{};
   k.N = a.N; k.p = a.p; k.q = a.q; k.m = a.m; k.n = a.n; k.r = a.r;
   k.ldm = a.m; k.ldx = (int64_t)a.p * a.m; k.act = a.act;
-  k.x[0] = k.x[1] = a.x; k.tb = t[0]; k.tc = t[1]; k.bias = a.bias; k.y = a.y;
+  k.x[0] = k.x[1] = a.x; k.tb = t[0]; k.tc = t[1]; k.bias = a.bias; k.y = a.y; k.n4 = z.n4;
   if (!a.bf16) return launch_rows<0, false, false, 3, 3, 3, 3, 2>(k, s);
   return a.S ? launch_rows<0, true, true, 1, 1, 2, 2, 1>(k, s) : launch_rows<0, true, true, 1, 1, 2, 1, 1>(k, s);
 }
@@ -749,7 +909,7 @@ hipError_t launch_glu_bwd(const GluArgs& a, void* ws, hipStream_t s) {
     if (a.dx) {
       RowsArgs x{};
       x.N = a.N; x.p = a.q; x.q = a.p; x.m = a.n; x.n = a.m; x.r = a.r;
-      x.ldm = z.n4; x.ldx = (int64_t)a.q * z.n4;
+      x.ldm = z.n4; x.ldx = (int64_t)a.q * z.n4; x.n4 = (a.m + 3) & ~3;
       x.x[0] = d; x.x[1] = d2; x.tb = t[2]; x.tc = t[3]; x.y = a.dx;
       if (!a.bf16) e = launch_rows<2, false, false, 3, 3, 3, 3, 2>(x, s);
       else if (a.S) e = launch_rows<2, false, true, 2, 1, 2, 2, 1>(x, s);
@@ -759,18 +919,17 @@ hipError_t launch_glu_bwd(const GluArgs& a, void* ws, hipStream_t s) {
   }
   ParamArgs k{};
   k.N = a.N; k.p = a.p; k.q = a.q; k.m = a.m; k.n = a.n; k.r = a.r; k.n4 = z.n4;
-  k.rows = (a.N + z.groups - 1) / z.groups;
   k.x = a.x; k.d[0] = d; k.d[1] = d2; k.tb = t[0]; k.tc = t[3]; k.part = part;
-  if (!a.bf16) e = launch_param<false, 3, 3, 3>(k, z.groups, s);
-  else if (a.S) e = launch_param<true, 1, 1, 2>(k, z.groups, s);
-  else e = launch_param<true, 1, 1, 1>(k, z.groups, s);
+  if (!a.bf16) e = launch_param<false, 3, 3, 3, 256>(k, z, s);
+  else if (a.S) e = launch_param<true, 1, 1, 2, 512>(k, z, s);
+  else e = launch_param<true, 1, 1, 1, 512>(k, z, s);
   if (e != hipSuccess) return e;
   RedPlan rp{};
   rp.nseg = 3;
   rp.seg[0] = RedSeg{a.dB, 2 * a.r * a.m * a.n, 1.f, 0};
   rp.seg[1] = RedSeg{a.S ? dC : a.dA, 2 * a.r * a.p * a.q, 1.f, 0};
   rp.seg[2] = RedSeg{a.dbias, 2 * a.q * a.n, 1.f, 0};
-  e = launch_column_reduce(part, z.groups, (int32_t)z.PW, rp, s);
+  e = launch_column_reduce(part, z.groups * z.share, (int32_t)z.PW, rp, s);
   if (e != hipSuccess || !a.S) return e;
   const int pq = a.p * a.q;
   hipLaunchKernelGGL(glu_ds_kernel, dim3((unsigned)((2 * pq + 255) / 256)), dim3(256), 0, s, pq, a.r, a.bf16, a.S, a.A,
