@@ -44,7 +44,8 @@ __device__ inline f4 mfma(const Op& a, const Op& b, f4 c) {
 __device__ inline uint32_t tops(float a, float b) {
   return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
 }
-__device__ inline float top(float a) { return __uint_as_float(__float_as_uint(a) & 0xffff0000u); }
+// what a bf16 part off the top of `a` leaves (exact)
+__device__ inline float rest(float a) { return a - __uint_as_float(__float_as_uint(a) & 0xffff0000u); }
 
 // Eight fp32 values (two f4) as NP bf16 operand parts, off the top bits.
 template <int NP>
@@ -58,8 +59,8 @@ __device__ inline void split(f4 lo, f4 hi, Op* o) {
     if (s + 1 < NP) {
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        lo[v] -= top(lo[v]);
-        hi[v] -= top(hi[v]);
+        lo[v] = rest(lo[v]);
+        hi[v] = rest(hi[v]);
       }
     }
   }
@@ -458,20 +459,26 @@ __global__ __launch_bounds__(64 * W, W / 4) void glu_rows_kernel(RowsArgs a) {
 // Each wavefront owns a pair's sum in registers, with B_fi (or C_fi) beside it; with fewer pairs than
 // wavefronts several share a pair and take rows in turn.  A step's rows of X and d_f are split
 // into parts once and staged in LDS as operand blocks in the order that the kind contracts over (4 x 4
-// patches, which a thread turns in its registers); the next step's values are loaded while this
-// one's are multiplied.
+// patches, which a thread turns in its registers).  Two buffers: while one step is multiplied the next
+// is staged, half of the wavefronts staging first and half multiplying first, and the values of the one
+// after that are on their way.
+//
+// Slots of a block are permuted so that neither side has bank conflicts: column c of k-group g stands
+// at 16 g + 4 ((c % 4) ^ g) + c / 4.  A wavefront stores columns of one residue mod 4 at a time: their
+// quarters of a 256-byte row differ by g.
 // ---------------------------------------------------------------------------------
 struct ParamArgs {
   int64_t N;
   int p, q, m, n, r, n4;
-  int64_t rows;            // rows of a workgroup
+  int groups[2];           // row groups of each kind
+  int pair_groups;
   int rs;                  // rows of a step
   int share;               // wavefronts of a pair
   const void* x;
   const float* d[2];
   const u4* tb;            // B blocks (k = m)
   const u4* tc;            // C^T blocks (k = q)
-  float* part;             // partial rows: dB (2 r m n) | dC (2 r p q) | dbias (2 q n)
+  float* part[2];          // partial rows: kind 0 dC (2 r p q) | dbias (2 q n), kind 1 dB (2 r m n)
 };
 
 // Sizes of a step that both the host and the kernel use.
@@ -492,38 +499,40 @@ struct ParamSizes {
   __host__ __device__ int row(int nf) const { return xa + nf * ya; }
 };
 
-template <bool XBF, int NX, int NT_, int KIND, int NTH>
-__device__ inline void param_body(const ParamArgs& a, int group, int groups, const u4* table, u4* lds) {
-  constexpr int NY = 3;
-  constexpr int SLOTS = (1024 + NTH - 1) / NTH;            // patches of a thread: at most 1024 a step
-  constexpr int BS = 512 / NTH;                            // of them of d_f: at most 512
+// TC: tiles of a side at most (2: all sides up to 32, a fraction of the registers; 4).
+template <bool XBF, int NX, int NTAB, int KIND, int TC, int NTH>
+__device__ inline void param_body(const ParamArgs& a, int rowgroup, int pairgroup, const u4* table, u4* lds) {
+  constexpr int NY = 3, KC = TC / 2;
+  constexpr int SLOTS = 1024 / NTH;            // patches of a thread: at most 1024 a step
+  constexpr int BS = 512 / NTH;                // of them of d_f: at most 512
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), g = lane >> 4, c = lane & 15;
+  const int slot = 16 * g + 4 * ((c & 3) ^ g) + (c >> 2);
   const ParamSizes z(a, NX, KIND);
-  const int pairs = 2 * a.r, ppw = (pairs + groups - 1) / groups, pair0 = group * ppw;
+  const int pairs = 2 * a.r, ppw = (pairs + a.pair_groups - 1) / a.pair_groups, pair0 = pairgroup * ppw;
   const int pairn = min(ppw, pairs - pair0);
   const int f_lo = pair0 / a.r, nf = (pair0 + pairn - 1) / a.r - f_lo + 1;
-  const int area = z.row(nf);
-  for (int i = tid; i < area * a.rs; i += NTH) lds[i] = u4{0u, 0u, 0u, 0u};      // the tiles' padding stays zero
+  const int area = z.row(nf), buf = area * a.rs;
+  for (int i = tid; i < 2 * buf; i += NTH) lds[i] = u4{0u, 0u, 0u, 0u};      // the tiles' padding stays zero
 
   const int pl = wave % ppw, sub = wave / ppw;
   const bool active = pl < pairn && sub < a.share;
   const int fi = pair0 + (active ? pl : 0), f = fi / a.r;
-  Op tab[4][2][NT_];       // kind 0: B_fi [NT][MK]; kind 1: C_fi^T [PT][QK]
+  Op tab[TC][KC][NTAB];    // kind 0: B_fi [NT][MK]; kind 1: C_fi^T [PT][QK]
   const int tabT = KIND == 0 ? z.NT : z.PT, tabK = KIND == 0 ? z.MK : z.QK;
 #pragma unroll
-  for (int t = 0; t < 4; ++t)
+  for (int t = 0; t < TC; ++t)
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
+    for (int k = 0; k < KC; ++k)
 #pragma unroll
-      for (int s = 0; s < NT_; ++s) {
+      for (int s = 0; s < NTAB; ++s) {
         tab[t][k][s].u = u4{0u, 0u, 0u, 0u};
-        if (t < tabT && k < tabK) tab[t][k][s].u = table[((int64_t)((fi * tabT + t) * tabK + k) * NT_ + s) * 64 + lane];
+        if (t < tabT && k < tabK) tab[t][k][s].u = table[((int64_t)((fi * tabT + t) * tabK + k) * NTAB + s) * 64 + lane];
       }
-  f4 acc[4][4];
+  f4 acc[TC][TC];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < TC; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < TC; ++j) acc[i][j] = f4{0.f, 0.f, 0.f, 0.f};
 
   // patches of a step: those of d_f of all its rows, then those of X
   const int nd = nf * z.dpat, ndall = a.rs * nd, npat = ndall + a.rs * z.xpat;
@@ -533,88 +542,100 @@ __device__ inline void param_body(const ParamArgs& a, int group, int groups, con
 #pragma unroll
     for (int e = 0; e < 16; ++e) bsum[b][e] = 0.f;
   const bool xvec = (a.m & 3) == 0;
-  const int64_t r0 = (int64_t)blockIdx.x * a.rows, r1 = min(a.N, r0 + a.rows);
+  const int64_t rows = (a.N + a.groups[KIND] - 1) / a.groups[KIND];
+  const int64_t r0 = rowgroup * rows, r1 = min(a.N, r0 + rows);
 
+  // This thread's patches: where the rows of each come from (advancing by a step's rows) and where it
+  // goes in LDS.  A patch (rows j0.., columns k0..) goes into blocks [k step][tile][part].  Kind 0 contracts
+  // along the row, kind 1 down the column; chained order, but X of kind 0 natural (its partner is the packed B).
+  struct Patch {
+    const char* src;
+    int step, stride;      // bytes from one step, one row of the patch, to the next
+    int kind;              // 0 none, 1 d_f, 2 X
+    int rr, rows, cols;    // row of the step; rows, columns of the patch that exist
+    int at, gg;            // LDS place (in 8 bytes, of part 0 and column 0), k-group
+  } ps[SLOTS];
   f4 v[SLOTS][4];
-  auto fetch = [&](int64_t step) {
+  constexpr int XS = XBF ? 2 : 4;
+#pragma unroll
+  for (int s = 0; s < SLOTS; ++s) {
+    const int pt = tid + s * NTH;
+    Patch& w = ps[s];
+    w.kind = pt < ndall ? 1 : pt < npat ? 2 : 0;
+    const bool isd = w.kind != 2;
+    const int e = isd ? pt : pt - ndall, per = isd ? nd : z.xpat, dk = isd ? z.dk : z.xk;
+    w.rr = e / per;
+    const int ff = isd ? (e % per) / z.dpat : 0, o = isd ? (e % per) % z.dpat : e % per;
+    const int j0 = 4 * (o / dk), k0 = 4 * (o % dk);
+    w.rows = (isd ? a.q : a.p) - j0;
+    w.cols = isd ? 4 : a.m - k0;
+    w.stride = isd ? a.n4 * 4 : a.m * XS;
+    w.step = a.rs * (isd ? a.q * a.n4 * 4 : a.p * a.m * XS);
+    w.src = isd ? (const char*)(a.d[f_lo + (w.kind == 1 ? ff : 0)] + ((r0 + w.rr) * a.q + j0) * a.n4 + k0)
+                : (const char*)a.x + ((r0 + w.rr) * a.p * a.m + (int64_t)j0 * a.m + k0) * XS;
+    const int np = isd ? NY : NX, tiles = isd ? (KIND == 0 ? z.QT : 2 * z.NK) : (KIND == 0 ? 2 * z.PK : z.MT);
+    const int kc = KIND == 0 ? k0 : j0, cc = KIND == 0 ? j0 : k0, kk = kc & 31;
+    const bool natural = KIND == 0 && !isd;
+    w.gg = natural ? kk >> 3 : (kk & 15) >> 2;
+    const int h = natural ? (kk >> 2) & 1 : kk >> 4, base = w.rr * area + (isd ? z.xa + ff * z.ya : 0);
+    w.at = 2 * (base + (((kc >> 5) * tiles + (cc >> 4)) * np) * 64 + w.gg * 16 + ((cc >> 2) & 3)) + h;
+  }
+  int64_t next = r0;      // the step that fetch() takes
+  auto fetch = [&]() {
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
-      const int pt = tid + s * NTH;
+      Patch& w = ps[s];
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[s][i] = f4{0.f, 0.f, 0.f, 0.f};
-      if (pt < ndall) {
-        const int rr = pt / nd, e = pt % nd, ff = e / z.dpat, o = e % z.dpat;
-        const int j0 = 4 * (o / z.dk), k0 = 4 * (o % z.dk);
-        const int64_t row = step + rr;
-        const float* src = a.d[f_lo + ff] + (row * a.q + j0) * a.n4 + k0;
-        if (row < r1) {
+      if (w.kind != 0 && next + w.rr < r1) {
+        const bool whole = w.kind == 1 || (xvec && !XBF);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (j0 + i < a.q) v[s][i] = *reinterpret_cast<const f4*>(src + i * a.n4);
-        }
-      } else if (pt < npat) {
-        const int rr = (pt - ndall) / z.xpat, o = (pt - ndall) % z.xpat;
-        const int j0 = 4 * (o / z.xk), k0 = 4 * (o % z.xk);
-        const int64_t row = step + rr, src = (row * a.p + j0) * a.m + k0;
-        if (row < r1) {
+        for (int i = 0; i < 4; ++i) {
+          if (i >= w.rows) continue;
+          const char* src = w.src + i * w.stride;
+          if (whole) {
+            v[s][i] = *reinterpret_cast<const f4*>(src);
+          } else if (xvec) {
+            typedef uint32_t u2v __attribute__((ext_vector_type(2)));
+            const u2v h = *reinterpret_cast<const u2v*>(src);
+            v[s][i] = f4{bf16_lo(h[0]), bf16_hi(h[0]), bf16_lo(h[1]), bf16_hi(h[1])};
+          } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (j0 + i >= a.p) continue;
-            if (xvec && XBF) {
-              typedef uint32_t u2v __attribute__((ext_vector_type(2)));
-              const u2v h = *reinterpret_cast<const u2v*>((const uint16_t*)a.x + src + i * a.m);
-              v[s][i] = f4{bf16_lo(h[0]), bf16_hi(h[0]), bf16_lo(h[1]), bf16_hi(h[1])};
-            } else if (xvec) {
-              v[s][i] = *reinterpret_cast<const f4*>((const float*)a.x + src + i * a.m);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (k0 + e < a.m) v[s][i][e] = load1<XBF>(a.x, src + i * a.m + e);
-            }
+            for (int e = 0; e < 4; ++e)
+              if (e < w.cols) v[s][i][e] = load1<XBF>(src, e);
           }
         }
       }
+      w.src += w.step;
     }
+    next += a.rs;
   };
-  // A patch (rows j0.., columns k0..) into blocks [k step][tile][part], lane (g, c), slots 0..3 or 4..7.
-  // Kind 0 contracts along the row, kind 1 down the column; chained order, but X of kind 0 natural (its
-  // partner is the packed B).
-  auto place = [&](const f4 (&w)[4], int j0, int k0, int base, int tiles, bool natural, int np) {
+  auto store = [&](int base) {
     typedef uint32_t u2v __attribute__((ext_vector_type(2)));
-    u2v* l2 = reinterpret_cast<u2v*>(lds);
-    const int kc = KIND == 0 ? k0 : j0, cc = KIND == 0 ? j0 : k0, kk = kc & 31;
-    const int gg = natural ? kk >> 3 : (kk & 15) >> 2, h = natural ? (kk >> 2) & 1 : kk >> 4;
-    const int at = 2 * (base + (((kc >> 5) * tiles + (cc >> 4)) * np) * 64 + gg * 16 + (cc & 15)) + h;
-    f4 u[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) u[i][e] = KIND == 0 ? w[i][e] : w[e][i];
-#pragma unroll
-    for (int s = 0; s < 3; ++s) {
-      if (s >= np) break;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        l2[at + 128 * s + 2 * i] = u2v{tops(u[i][0], u[i][1]), tops(u[i][2], u[i][3])};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) u[i][e] -= top(u[i][e]);
-      }
-    }
-  };
-  auto store = [&]() {
+    u2v* l2 = reinterpret_cast<u2v*>(lds + base);
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
-      const int pt = tid + s * NTH;
-      if (pt < ndall) {
-        const int rr = pt / nd, e = pt % nd, ff = e / z.dpat, o = e % z.dpat;
-        place(v[s], 4 * (o / z.dk), 4 * (o % z.dk), rr * area + z.xa + ff * z.ya, KIND == 0 ? z.QT : 2 * z.NK, false, NY);
-        if (KIND == 0 && s < BS) {
+      const Patch& w = ps[s];
+      if (w.kind == 0) continue;
+      f4 u[4];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) bsum[s < BS ? s : 0][i] += v[s][i / 4][i % 4];
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[i][e] = KIND == 0 ? v[s][i][e] : v[s][e][i];
+      if (KIND == 0 && s < BS && w.kind == 1) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) bsum[s < BS ? s : 0][i] += v[s][i / 4][i % 4];
+      }
+      const int np = w.kind == 1 ? NY : NX;
+#pragma unroll
+      for (int part = 0; part < 3; ++part) {
+        if (part >= np) break;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          l2[w.at + 128 * part + 8 * (i ^ w.gg)] = u2v{tops(u[i][0], u[i][1]), tops(u[i][2], u[i][3])};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) u[i][e] = rest(u[i][e]);
         }
-      } else if (pt < npat) {
-        const int rr = (pt - ndall) / z.xpat, o = (pt - ndall) % z.xpat;
-        place(v[s], 4 * (o / z.xk), 4 * (o % z.xk), rr * area, KIND == 0 ? 2 * z.PK : z.MT, KIND == 0, NX);
       }
     }
   };
@@ -624,7 +645,7 @@ __device__ inline void param_body(const ParamArgs& a, int group, int groups, con
     constexpr int TI = decltype(count)::value;
     const int steps = KIND == 0 ? z.NK : z.PK;
 #pragma unroll
-    for (int ko = 0; ko < 2; ++ko)
+    for (int ko = 0; ko < KC; ++ko)
       if (ko < steps) {
         Op h[TI][3];
 #pragma unroll
@@ -632,27 +653,27 @@ __device__ inline void param_body(const ParamArgs& a, int group, int groups, con
           f4 w[2];
           w[0] = w[1] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
+          for (int k = 0; k < KC; ++k)
             if (k < tabK) {
               if (KIND == 0) {
                 Op x[NX];
 #pragma unroll
                 for (int s = 0; s < NX; ++s) x[s].u = xl[k * 2 * z.PK * NX * 64 + (t * NX + s) * 64];
 #pragma unroll
-                for (int u = 0; u < 2; ++u) w[u] = dot<NT_, NX, 2>(tab[2 * ko + u][k], x, w[u]);
+                for (int u = 0; u < 2; ++u) w[u] = dot<NTAB, NX, 2>(tab[2 * ko + u][k], x, w[u]);
               } else {
                 Op y[NY];
 #pragma unroll
                 for (int s = 0; s < NY; ++s) y[s].u = yl[k * 2 * z.NK * NY * 64 + (t * NY + s) * 64];
 #pragma unroll
-                for (int u = 0; u < 2; ++u) w[u] = dot<NT_, NY, 2>(tab[2 * ko + u][k], y, w[u]);
+                for (int u = 0; u < 2; ++u) w[u] = dot<NTAB, NY, 2>(tab[2 * ko + u][k], y, w[u]);
               }
             }
           split<3>(w[0], w[1], h[t]);
         }
         const int outer = KIND == 0 ? z.QT : z.MT;
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int t = 0; t < TC; ++t)
           if (t < outer) {
             constexpr int NO = KIND == 0 ? NY : NX;
             Op y[NO];
@@ -672,34 +693,50 @@ __device__ inline void param_body(const ParamArgs& a, int group, int groups, con
           }
       }
   };
-
-  fetch(r0);
-  for (int64_t step = r0; step < r1; step += a.rs) {
-    __syncthreads();       // the previous step's operands have been read
-    store();
-    __syncthreads();
-    if (step + a.rs < r1) fetch(step + a.rs);
-    if (!active) continue;
+  auto work = [&](int base) {
+    if (!active) return;
+#pragma unroll 1
     for (int rr = sub; rr < a.rs; rr += a.share) {
-      const u4* xl = lds + rr * area + lane;
+      const u4* xl = lds + base + rr * area + slot;
       const u4* yl = xl + z.xa + (f - f_lo) * z.ya;
-      if ((KIND == 0 ? z.PT : z.NT) > 2)
-        multiply(std::integral_constant<int, 4>{}, xl, yl);
-      else
+      if constexpr (TC == 4) {
+        if ((KIND == 0 ? z.PT : z.NT) > 2)
+          multiply(std::integral_constant<int, 4>{}, xl, yl);
+        else
+          multiply(std::integral_constant<int, 2>{}, xl, yl);
+      } else {
         multiply(std::integral_constant<int, 2>{}, xl, yl);
+      }
     }
+  };
+
+  fetch();
+  __syncthreads();
+  store(0);
+  fetch();
+  __syncthreads();
+  int cur = 0;
+  const bool late = wave >= NTH / 128;      // (the second wavefront of a SIMD)
+  for (int64_t step = r0; step < r1; step += a.rs) {
+    if (late) work(cur);
+    if (step + a.rs < r1) store(buf - cur);
+    if (step + 2 * a.rs < r1) fetch();
+    if (!late) work(cur);
+    cur = buf - cur;
+    __syncthreads();
   }
 
   // partial rows: one for each wavefront of a pair
   const int64_t mn = (int64_t)a.m * a.n, pq = (int64_t)a.p * a.q;
-  const PartRow out{a.part, (int64_t)gridDim.x * a.share, (int64_t)blockIdx.x * a.share + (active ? sub : 0), 0};
+  const int64_t prow = (int64_t)rowgroup * a.share, prows = (int64_t)a.groups[KIND] * a.share;
+  const PartRow out{a.part[KIND], prows, prow + (active ? sub : 0), 0};
   if (active) {
     const int R = KIND == 0 ? a.p : a.m, Cn = KIND == 0 ? a.q : a.n;
-    const int64_t base = KIND == 0 ? pairs * mn + fi * pq : fi * mn;
+    const int64_t base = KIND == 0 ? fi * pq : fi * mn;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < TC; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < TC; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int ri = 16 * i + 4 * g + e, ci = 16 * j + c;
@@ -710,7 +747,6 @@ __device__ inline void param_body(const ParamArgs& a, int group, int groups, con
   // dbias: the sums of a step's rows are joined in LDS (row 0's threads first: a fixed order)
   float* bl = reinterpret_cast<float*>(lds);
   for (int rr = 0; rr < a.rs; ++rr) {
-    __syncthreads();
 #pragma unroll
     for (int s = 0; s < BS; ++s) {
       const int pt = tid + s * NTH;
@@ -719,46 +755,112 @@ __device__ inline void param_body(const ParamArgs& a, int group, int groups, con
         for (int e = 0; e < 16; ++e) bl[(pt % nd) * 16 + e] = bsum[s][e] + (rr ? bl[(pt % nd) * 16 + e] : 0.f);
       }
     }
+    __syncthreads();
   }
-  __syncthreads();
   for (int i = tid; i < nd * 16; i += NTH) {
     const int e = i >> 4, ff = f_lo + e / z.dpat, o = e % z.dpat;
     const int j = 4 * (o / z.dk) + ((i >> 2) & 3), k = 4 * (o % z.dk) + (i & 3);
     // (the workgroup with the projection's first pair; its other partial rows have nothing to add)
     if (ff * a.r >= pair0 && ff * a.r < pair0 + pairn && j < a.q && k < a.n)
       for (int w = 0; w < a.share; ++w) {
-        const PartRow ow{a.part, (int64_t)gridDim.x * a.share, (int64_t)blockIdx.x * a.share + w, 0};
-        ow[pairs * (mn + pq) + (int64_t)ff * a.q * a.n + (int64_t)j * a.n + k] = w == 0 ? bl[i] : 0.f;
+        const PartRow ow{a.part[0], prows, prow + w, 0};
+        ow[pairs * pq + (int64_t)ff * a.q * a.n + (int64_t)j * a.n + k] = w == 0 ? bl[i] : 0.f;
       }
   }
 }
 
-template <bool XBF, int NX, int NB, int NC, int NTH>
+template <bool XBF, int NX, int NB, int NC, int TC, int NTH>
 __global__ __launch_bounds__(NTH) void glu_param_kernel(ParamArgs a) {
   extern __shared__ u4 lds[];
-  const int groups = gridDim.y / 2;
-  if ((int)blockIdx.y < groups)
-    param_body<XBF, NX, NB, 0, NTH>(a, blockIdx.y, groups, a.tb, lds);
-  else
-    param_body<XBF, NX, NC, 1, NTH>(a, blockIdx.y - groups, groups, a.tc, lds);
+  int b = blockIdx.x;
+  const int n0 = a.groups[0] * a.pair_groups;
+  if (b < n0) {
+    param_body<XBF, NX, NB, 0, TC, NTH>(a, b / a.pair_groups, b % a.pair_groups, a.tb, lds);
+  } else {
+    b -= n0;
+    param_body<XBF, NX, NC, 1, TC, NTH>(a, b / a.pair_groups, b % a.pair_groups, a.tc, lds);
+  }
 }
 
-// dA = S o dC, dS = sum_i A_i o dC_i from the summed dC (2 x r x p x q).
-__global__ __launch_bounds__(256) void glu_ds_kernel(int pq, int r, int bf16, const void* S, const void* A,
-                                                     const float* __restrict__ dC, float* __restrict__ dS,
-                                                     float* __restrict__ dA) {
-  const int e = blockIdx.x * 256 + threadIdx.x;
-  if (e >= 2 * pq) return;
-  const int f = e / pq, o = e - f * pq;
-  const float s = raw(S, e, bf16);
-  float sum = 0.f;
-  for (int i = 0; i < r; ++i) {
-    const int64_t at = ((int64_t)f * r + i) * pq + o;
-    const float d = dC[at];
-    dA[at] = s * d;
-    sum = fmaf(raw(A, at, bf16), d, sum);
+// ---------------------------------------------------------------------------------
+// The partial rows summed in 64 bits in a fixed order, and dA = S o dC, dS = sum_i A_i o dC_i from dC.  A
+// workgroup has a block of 32 columns (part_index): of dB, of dbias, or with S of dC's e-th elements of
+// every rank.
+// ---------------------------------------------------------------------------------
+struct ReduceArgs {
+  const float* part[2];
+  int rows[2];             // partial rows of each kind
+  int nB, nC, nbias;       // columns: dB, dC, dbias
+  int pq, r, bf16;
+  const void* S;
+  const void* A;
+  float* dB;
+  float* dA;
+  float* dS;
+  float* dbias;
+};
+
+// Sum over `rows` of column c0 + col (32 consecutive ones; they may cross a block's end): thread (col, y).
+__device__ inline double column_sum(const float* part, int rows, int64_t column, bool in, int y, double (*red)[33],
+                                    int col) {
+  double s0 = 0.0, s1 = 0.0;
+  if (in) {
+    const float* src = part + part_index(rows, 0, column);
+    int g = y;
+    for (; g + 8 < rows; g += 16) {
+      const float u = src[(int64_t)g * kRedCols], w = src[(int64_t)(g + 8) * kRedCols];
+      s0 += (double)u;
+      s1 += (double)w;
+    }
+    if (g < rows) s0 += (double)src[(int64_t)g * kRedCols];
   }
-  dS[e] = sum;
+  __syncthreads();
+  red[y][col] = s0 + s1;
+  __syncthreads();
+  double t = 0.0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) t += red[i][col];
+  return t;
+}
+
+__global__ __launch_bounds__(256) void glu_reduce_kernel(ReduceArgs a) {
+  __shared__ double red[8][33];
+  const int col = threadIdx.x & 31, y = threadIdx.x >> 5;
+  int b = blockIdx.x;
+  const int bB = (a.nB + 31) / 32, bb = a.dbias ? (a.nbias + 31) / 32 : 0;
+  if (b < bB) {
+    const int c = 32 * b + col;
+    const double t = column_sum(a.part[1], a.rows[1], c, c < a.nB, y, red, col);
+    if (y == 0 && c < a.nB) a.dB[c] = (float)t;
+    return;
+  }
+  b -= bB;
+  if (b < bb) {
+    const int c = 32 * b + col;
+    const double t = column_sum(a.part[0], a.rows[0], a.nC + c, c < a.nbias, y, red, col);
+    if (y == 0 && c < a.nbias) a.dbias[c] = (float)t;
+    return;
+  }
+  b -= bb;
+  if (!a.S) {
+    const int c = 32 * b + col;
+    const double t = column_sum(a.part[0], a.rows[0], c, c < a.nC, y, red, col);
+    if (y == 0 && c < a.nC) a.dA[c] = (float)t;
+    return;
+  }
+  const int per = (a.pq + 31) / 32, f = b / per, e = 32 * (b % per) + col;
+  const bool in = e < a.pq;
+  const float s = in ? raw(a.S, (int64_t)f * a.pq + e, a.bf16) : 0.f;
+  double ds = 0.0;
+  for (int i = 0; i < a.r; ++i) {
+    const int64_t c = ((int64_t)f * a.r + i) * a.pq + e;
+    const double t = column_sum(a.part[0], a.rows[0], c, in, y, red, col);
+    if (y == 0 && in) {
+      a.dA[c] = (float)((double)s * t);
+      ds += (double)raw(a.A, c, a.bf16) * t;
+    }
+  }
+  if (y == 0 && in) a.dS[(int64_t)f * a.pq + e] = (float)ds;
 }
 
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
@@ -766,8 +868,9 @@ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 struct Sizes {
   int parts_b, parts_c;
   int64_t lanes[4], bytes[4];
-  int n4, groups, waves, share;
-  int64_t PW, off_d, off_part, off_dc, fwd_bytes, bwd_bytes;
+  int n4, groups[2], waves, share, pair_groups;
+  bool small;
+  int64_t off_d, off_part[2], fwd_bytes, bwd_bytes;
 };
 
 Sizes sizes_of(const GluArgs& a) {
@@ -784,18 +887,27 @@ Sizes sizes_of(const GluArgs& a) {
   }
   z.n4 = (a.n + 3) & ~3;
   z.off_d = (off + 255) & ~int64_t(255);
-  z.off_part = z.off_d + ((2 * a.N * a.q * z.n4 * 4 + 255) & ~int64_t(255));
-  // the parameters' kernel: fp32 in four wavefronts (its parts take the registers of two), bf16 in eight;
-  // one workgroup a CU (its LDS), each with at least four rows where there are that many
-  z.waves = a.bf16 ? 8 : 4;
+  z.off_part[0] = z.off_d + ((2 * a.N * a.q * z.n4 * 4 + 255) & ~int64_t(255));
+  // The parameters' kernel: eight wavefronts; four for fp32 with a side over 32, whose parts take the registers
+  // of two.  One workgroup a CU, the kinds' numbers of them by their numbers of products, each with at least
+  // four rows where there are that many.
+  z.small = std::max(std::max(a.p, a.q), std::max(a.m, a.n)) <= 32;
+  z.waves = !z.small && !a.bf16 ? 4 : 8;
   z.share = 1;
   while (2 * z.share * 2 * a.r <= z.waves) z.share *= 2;
-  int64_t G = 256 / (2 * ceil_div(2 * a.r, z.waves / z.share));
-  if (G > (a.N + 3) / 4) G = (a.N + 3) / 4;
-  z.groups = G < 1 ? 1 : (int)G;
-  z.PW = (int64_t)2 * a.r * (a.m * a.n + a.p * a.q) + 2 * a.q * a.n;
-  z.off_dc = z.off_part + ((part_floats(z.groups * z.share, z.PW) * 4 + 255) & ~int64_t(255));
-  z.bwd_bytes = z.off_dc + (int64_t)2 * a.r * a.p * a.q * 4;
+  z.pair_groups = ceil_div(2 * a.r, z.waves / z.share);
+  const int PT = ceil_div(a.p, 16), QT = ceil_div(a.q, 16), MT = ceil_div(a.m, 16), NT = ceil_div(a.n, 16);
+  const int PK = ceil_div(a.p, 32), QK = ceil_div(a.q, 32), MK = ceil_div(a.m, 32), NK = ceil_div(a.n, 32);
+  const int tb = a.bf16 ? 1 : 6, tc = a.bf16 ? (a.S ? 5 : 3) : 6, tx = a.bf16 ? 3 : 6;      // instructions of a product
+  const double w0 = PT * 2 * NK * MK * tb + PT * QT * NK * 6, w1 = 2 * PK * NT * QK * tc + MT * NT * PK * tx;
+  const int total = std::max(2, 256 / z.pair_groups);
+  const int64_t most = (a.N + 3) / 4;
+  z.groups[0] = std::min(std::max((int)(total * w0 / (w0 + w1) + 0.5), 1), total - 1);
+  z.groups[1] = total - z.groups[0];
+  for (int k = 0; k < 2; ++k) z.groups[k] = (int)std::max<int64_t>(1, std::min<int64_t>(z.groups[k], most));
+  const int64_t PW0 = (int64_t)2 * a.r * a.p * a.q + 2 * a.q * a.n, PW1 = (int64_t)2 * a.r * a.m * a.n;
+  z.off_part[1] = z.off_part[0] + ((part_floats(z.groups[0] * z.share, PW0) * 4 + 255) & ~int64_t(255));
+  z.bwd_bytes = z.off_part[1] + part_floats(z.groups[1] * z.share, PW1) * 4;
   return z;
 }
 
@@ -851,30 +963,38 @@ hipError_t launch_rows(const RowsArgs& k, hipStream_t s) {
                    : launch_rows_k<MODE, XBF, OBF, NX, NB, NZ, NC, LIM, 2, 2>(k, s);
 }
 
-template <bool XBF, int NX, int NB, int NC, int NTH>
+template <bool XBF, int NX, int NB, int NC, int TC, int NTH>
+hipError_t launch_param_k(const ParamArgs& k, size_t lds, hipStream_t s) {
+  constexpr auto kernel = glu_param_kernel<XBF, NX, NB, NC, TC, NTH>;
+  static const hipError_t attr =
+      hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)kLds);
+  if (attr != hipSuccess) return attr;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)((k.groups[0] + k.groups[1]) * k.pair_groups)), dim3(NTH), lds, s, k);
+  return hipGetLastError();
+}
+
+template <bool XBF, int NX, int NB, int NC>
 hipError_t launch_param(ParamArgs k, const Sizes& sz, hipStream_t s) {
-  k.rows = (k.N + sz.groups - 1) / sz.groups;
   k.share = sz.share;
-  const int Y = ceil_div(2 * k.r, sz.waves / sz.share), ppw = ceil_div(2 * k.r, Y);
+  k.pair_groups = sz.pair_groups;
+  for (int i = 0; i < 2; ++i) k.groups[i] = sz.groups[i];
+  const int ppw = ceil_div(2 * k.r, sz.pair_groups);
   int nf = 1;      // most projections of a workgroup
-  for (int y = 0; y < Y; ++y)
+  for (int y = 0; y < sz.pair_groups; ++y)
     if ((std::min(2 * k.r, (y + 1) * ppw) - 1) / k.r != y * ppw / k.r) nf = 2;
-  // as many rows a step as LDS and the threads' slots hold (but no more than four a wavefront)
+  // as many rows a step as two LDS buffers and the threads' slots hold (but no more than four a wavefront)
   const ParamSizes z0(k, NX, 0), z1(k, NX, 1);
   const size_t one = (size_t)std::max(z0.row(nf), z1.row(nf)) * 16;
   const int nd = nf * z0.dpat, np = nd + z0.xpat;
+  const int64_t rows = (k.N + k.groups[0] - 1) / k.groups[0];
   k.rs = 1;
-  while (k.rs < 4 * k.share && k.rs < k.rows && (k.rs + 1) * one <= 160 * 1024 && (k.rs + 1) * nd <= 512 &&
+  while (k.rs < 4 * k.share && k.rs < rows && 2 * (k.rs + 1) * one <= kLds && (k.rs + 1) * nd <= 512 &&
          (k.rs + 1) * np <= 1024)
     ++k.rs;
-  static const hipError_t attr = hipFuncSetAttribute((const void*)glu_param_kernel<XBF, NX, NB, NC, NTH>,
-                                                     hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
-  if (attr != hipSuccess) return attr;
   // (dbias is joined in the same LDS: 64 bytes a patch of d_f)
-  const size_t lds = std::max(one * k.rs, (size_t)nd * 64);
-  hipLaunchKernelGGL((glu_param_kernel<XBF, NX, NB, NC, NTH>), dim3((unsigned)sz.groups, (unsigned)(2 * Y)), dim3(NTH),
-                     lds, s, k);
-  return hipGetLastError();
+  const size_t lds = std::max(2 * one * k.rs, (size_t)nd * 64);
+  if (sz.small) return launch_param_k<XBF, NX, NB, NC, 2, 512>(k, lds, s);
+  return launch_param_k<XBF, NX, NB, NC, 4, XBF ? 512 : 256>(k, lds, s);
 }
 
 }  // namespace
@@ -906,8 +1026,6 @@ hipError_t launch_glu_bwd(const GluArgs& a, void* ws, hipStream_t s) {
     w += z.bytes[i];
   }
   float* d = (float*)((char*)ws + z.off_d);
-  float* part = (float*)((char*)ws + z.off_part);
-  float* dC = (float*)((char*)ws + z.off_dc);
   hipError_t e = launch_pack(a, z, 4, t, s);
   if (e != hipSuccess) return e;
   float* d2 = d + a.N * a.q * z.n4;
@@ -934,21 +1052,23 @@ hipError_t launch_glu_bwd(const GluArgs& a, void* ws, hipStream_t s) {
   }
   ParamArgs k{};
   k.N = a.N; k.p = a.p; k.q = a.q; k.m = a.m; k.n = a.n; k.r = a.r; k.n4 = z.n4;
-  k.x = a.x; k.d[0] = d; k.d[1] = d2; k.tb = t[0]; k.tc = t[3]; k.part = part;
-  if (!a.bf16) e = launch_param<false, 3, 3, 3, 256>(k, z, s);
-  else if (a.S) e = launch_param<true, 1, 1, 2, 512>(k, z, s);
-  else e = launch_param<true, 1, 1, 1, 512>(k, z, s);
+  k.x = a.x; k.d[0] = d; k.d[1] = d2; k.tb = t[0]; k.tc = t[3];
+  for (int i = 0; i < 2; ++i) k.part[i] = (float*)((char*)ws + z.off_part[i]);
+  if (!a.bf16) e = launch_param<false, 3, 3, 3>(k, z, s);
+  else if (a.S) e = launch_param<true, 1, 1, 2>(k, z, s);
+  else e = launch_param<true, 1, 1, 1>(k, z, s);
   if (e != hipSuccess) return e;
-  RedPlan rp{};
-  rp.nseg = 3;
-  rp.seg[0] = RedSeg{a.dB, 2 * a.r * a.m * a.n, 1.f, 0};
-  rp.seg[1] = RedSeg{a.S ? dC : a.dA, 2 * a.r * a.p * a.q, 1.f, 0};
-  rp.seg[2] = RedSeg{a.dbias, 2 * a.q * a.n, 1.f, 0};
-  e = launch_column_reduce(part, z.groups * z.share, (int32_t)z.PW, rp, s);
-  if (e != hipSuccess || !a.S) return e;
-  const int pq = a.p * a.q;
-  hipLaunchKernelGGL(glu_ds_kernel, dim3((unsigned)((2 * pq + 255) / 256)), dim3(256), 0, s, pq, a.r, a.bf16, a.S, a.A,
-                     dC, a.dS, a.dA);
+  ReduceArgs ra{};
+  for (int i = 0; i < 2; ++i) {
+    ra.part[i] = k.part[i];
+    ra.rows[i] = z.groups[i] * z.share;
+  }
+  ra.pq = a.p * a.q; ra.r = a.r; ra.bf16 = a.bf16;
+  ra.nB = 2 * a.r * a.m * a.n; ra.nC = 2 * a.r * ra.pq; ra.nbias = 2 * a.q * a.n;
+  ra.S = a.S; ra.A = a.A; ra.dB = a.dB; ra.dA = a.dA; ra.dS = a.dS; ra.dbias = a.dbias;
+  const int blocks = ceil_div(ra.nB, 32) + (a.dbias ? ceil_div(ra.nbias, 32) : 0) +
+                     (a.S ? 2 * ceil_div(ra.pq, 32) : ceil_div(ra.nC, 32));
+  hipLaunchKernelGGL(glu_reduce_kernel, dim3((unsigned)blocks), dim3(256), 0, s, ra);
   return hipGetLastError();
 }
 
