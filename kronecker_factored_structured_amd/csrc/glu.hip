@@ -44,8 +44,16 @@ __device__ inline f4 mfma(const Op& a, const Op& b, f4 c) {
 __device__ inline uint32_t tops(float a, float b) {
   return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
 }
-// what a bf16 part off the top of `a` leaves (exact)
-__device__ inline float rest(float a) { return a - __uint_as_float(__float_as_uint(a) & 0xffff0000u); }
+// What the bf16 parts in `t` (a's low, b's high) leave of a and b: exact, in one instruction each, as a
+// two-term product whose other factor is 0.  (The pairs (-1, 0) and (0, -1) come from registers: as a
+// constant of the instruction 0x0000bf80 stands for both halves.)
+__device__ inline void rest(uint32_t t, float& a, float& b) {
+  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+  uint32_t lo = 0x0000bf80u, hi = 0xbf800000u;
+  asm("" : "+s"(lo), "+s"(hi));
+  a = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(b2, t), __builtin_bit_cast(b2, lo), a, false);
+  b = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(b2, t), __builtin_bit_cast(b2, hi), b, false);
+}
 
 // Eight fp32 values (two f4) as NP bf16 operand parts, off the top bits.
 template <int NP>
@@ -57,11 +65,11 @@ __device__ inline void split(f4 lo, f4 hi, Op* o) {
     o[s].u[2] = tops(hi[0], hi[1]);
     o[s].u[3] = tops(hi[2], hi[3]);
     if (s + 1 < NP) {
+      float l[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        lo[v] = rest(lo[v]);
-        hi[v] = rest(hi[v]);
-      }
+      for (int v = 0; v < 4; ++v) rest(o[s].u[v], l[2 * v], l[2 * v + 1]);
+      lo = f4{l[0], l[1], l[2], l[3]};
+      hi = f4{l[4], l[5], l[6], l[7]};
     }
   }
 }
@@ -632,9 +640,14 @@ __device__ inline void param_body(const ParamArgs& a, int rowgroup, int pairgrou
         if (part >= np) break;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          l2[w.at + 128 * part + 8 * (i ^ w.gg)] = u2v{tops(u[i][0], u[i][1]), tops(u[i][2], u[i][3])};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) u[i][e] = rest(u[i][e]);
+          const u2v t = u2v{tops(u[i][0], u[i][1]), tops(u[i][2], u[i][3])};
+          l2[w.at + 128 * part + 8 * (i ^ w.gg)] = t;
+          if (part < 2) {
+            float r0 = u[i][0], r1 = u[i][1], r2 = u[i][2], r3 = u[i][3];
+            rest(t[0], r0, r1);
+            rest(t[1], r2, r3);
+            u[i] = f4{r0, r1, r2, r3};
+          }
         }
       }
     }
