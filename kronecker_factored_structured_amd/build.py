@@ -21,16 +21,21 @@ LIB = os.path.join(HERE, "libkron.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
+# Accumulators of matrix instructions in the ordinary registers instead of the accumulation ones: for
+# kernels that read and write them between the products.
+VGPR_MFMA = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
+
 # (source, extra flags, object name): kron_mfma.hip is compiled twice, its forward kernels
 # with LLVM's instruction-level-parallelism scheduler (measured faster for them) and the
-# rest with the default one.
+# rest with the default one.  glu_rows.hip and glu_param.hip are compiled once for each of their
+# variants, to build in parallel.
 OBJECTS = [
     ("kron_api.cpp", [], "kron_api"),
     ("kron_generic.hip", [], "kron_generic"),
     ("kron_mfma.hip", ["-DKRON_MFMA_PASS=1", "-mllvm", "-amdgpu-sched-strategy=max-ilp"], "kron_mfma_fwd"),
     ("kron_mfma.hip", ["-DKRON_MFMA_PASS=2"], "kron_mfma_bwd"),
     ("kron_small.hip", [], "kron_small"),
-    ("kron_bf16.hip", ["-mllvm", "-amdgpu-mfma-vgpr-form"], "kron_bf16"),
+    ("kron_bf16.hip", VGPR_MFMA, "kron_bf16"),
     ("ks_matmul.hip", [], "ks_matmul"),
     ("ks_mfma.hip", [], "ks_mfma"),
     ("ks_bwd.hip", [], "ks_bwd"),
@@ -39,7 +44,13 @@ OBJECTS = [
     ("adam_l1.hip", [], "adam_l1"),
     ("head_ce.hip", [], "head_ce"),
     ("loss_terms.hip", [], "loss_terms"),
-    ("glu.hip", ["-mllvm", "-amdgpu-mfma-vgpr-form"], "glu"),
+    ("glu.hip", [], "glu"),
+    ("glu_rows.hip", ["-DKRON_GLU_MODE=0", *VGPR_MFMA], "glu_rows0"),
+    ("glu_rows.hip", ["-DKRON_GLU_MODE=1", *VGPR_MFMA], "glu_rows1"),
+    ("glu_rows.hip", ["-DKRON_GLU_MODE=2", *VGPR_MFMA], "glu_rows2"),
+    ("glu_param.hip", ["-DKRON_GLU_TYPE=0", *VGPR_MFMA], "glu_param0"),
+    ("glu_param.hip", ["-DKRON_GLU_TYPE=1", *VGPR_MFMA], "glu_param1"),
+    ("glu_param.hip", ["-DKRON_GLU_TYPE=2", *VGPR_MFMA], "glu_param2"),
     ("distill.hip", [], "distill"),
     ("topk_logits.hip", [], "topk_logits"),
 ]

@@ -1,0 +1,141 @@
+// What the gated Kronecker block's sources share (glu.hip, glu_rows.hip, glu_param.hip): operand parts and
+// blocks of the bf16 matrix instruction, and the kernels' arguments.
+//
+// All products run on the bf16 matrix instruction with fp32 accumulation.  A factor wider than
+// bf16 is the sum of bf16 parts taken off its top bits (8 + 8 + 8 bits: an fp32 value is exactly
+// three), and a product keeps the pairs of parts whose orders sum to at most two: six instructions
+// for fp32 times fp32, dropped terms below 2^-21 of the product.  The bf16 instruction has sixteen
+// times the rate of the fp32 one, so six of them are still 2.7 times faster; bf16 inputs need
+// fewer parts and keep their intermediates exact to fp32 in the backward (its parameter gradients
+// are fp32) and to 2^-16 in the forward (its y is bf16).  A non-finite input gives non-finite outputs.
+//
+// Operand blocks.  The instruction takes 16 (row or column) x 32 (k): lane l = 16 g + c holds
+// k-slots 8 g .. 8 g + 7 of row c.  Its result has lane (g, c) holding rows 4 g .. 4 g + 3 of
+// column c.  Two results stacked (rows 0..15 and 16..31) are, lane by lane, an operand with
+// k-slots {4g..4g+3, 16+4g..16+4g+3} ("chained" order), so Z goes from the first product into the
+// second without leaving its registers; the other operand is laid out in the same order.  The
+// factors are laid out as such blocks once per call by glu_pack_kernel.
+#pragma once
+
+#include <algorithm>
+#include <type_traits>
+
+#include "kron_internal.h"
+#include "row_tile.h"
+
+namespace kron {
+
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+
+struct GluRows {
+  int64_t N;
+  int p, q, m, n, r;       // of these products (MODE 2: q, p, n, m of the layer)
+  int ldm;                 // elements from one row of X_f to the next
+  int64_t ldx;             // elements from one X to the next
+  int act;
+  int qsplit;              // workgroups that share the q tiles
+  const void* x[2];
+  const u4* tb;            // B blocks
+  const u4* tc;            // C blocks
+  const void* bias;        // 2 x q n, or NULL
+  const void* dy;
+  void* y;
+  float* d[2];             // dg, du: rows of q x n4
+  int n4;
+};
+
+struct GluParam {
+  int64_t N;
+  int p, q, m, n, r, n4;
+  int groups[2];           // row groups of each kind
+  int pair_groups;         // workgroups that share the pairs
+  int rs;                  // rows of a step (set by launch_glu_param)
+  int share;               // wavefronts of a pair
+  const void* x;
+  const float* d[2];
+  const u4* tb;            // B blocks (k = m)
+  const u4* tc;            // C^T blocks (k = q)
+  float* part[2];          // partial rows: kind 0 dC (2 r p q) | dbias (2 q n), kind 1 dB (2 r m n)
+};
+
+hipError_t launch_glu_rows0(const GluRows& k, bool bf16, bool with_S, hipStream_t s);      // y
+hipError_t launch_glu_rows1(const GluRows& k, bool bf16, bool with_S, hipStream_t s);      // dg, du
+hipError_t launch_glu_rows2(const GluRows& k, bool bf16, bool with_S, hipStream_t s);      // dX
+hipError_t launch_glu_param_f32(const GluParam& k, hipStream_t s);
+hipError_t launch_glu_param_bf16(const GluParam& k, hipStream_t s);
+hipError_t launch_glu_param_bf16_S(const GluParam& k, hipStream_t s);
+// Wavefronts of a workgroup of the parameters' kernel: eight, four where the sums and parts of sides over 32
+// (p, n, q or m) take the registers of two.
+constexpr int param_waves(bool bf16, bool p, bool n, bool qm) {
+  return qm && (bf16 ? p && n : p || n) ? 4 : 8;
+}
+
+namespace {
+
+typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+typedef float f4 __attribute__((ext_vector_type(4)));
+
+union Op {        // an operand block's registers
+  u4 u;
+  bf8 b;
+};
+
+__device__ inline f4 mfma(const Op& a, const Op& b, f4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.b, b.b, c, 0, 0, 0);
+}
+// the top halves of a (low) and b (high)
+__device__ inline uint32_t tops(float a, float b) {
+  return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+}
+// What the bf16 parts in `t` (a's low, b's high) leave of a and b: exact, in one instruction each, as a
+// two-term product whose other factor is 0.  (The pairs (-1, 0) and (0, -1) come from registers: as a
+// constant of the instruction 0x0000bf80 stands for both halves.)
+__device__ inline void rest(uint32_t t, float& a, float& b) {
+  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+  uint32_t lo = 0x0000bf80u, hi = 0xbf800000u;
+  asm("" : "+s"(lo), "+s"(hi));
+  a = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(b2, t), __builtin_bit_cast(b2, lo), a, false);
+  b = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(b2, t), __builtin_bit_cast(b2, hi), b, false);
+}
+
+// Eight fp32 values (two f4) as NP bf16 operand parts, off the top bits.
+template <int NP>
+__device__ inline void split(f4 lo, f4 hi, Op* o) {
+#pragma unroll
+  for (int s = 0; s < NP; ++s) {
+    o[s].u[0] = tops(lo[0], lo[1]);
+    o[s].u[1] = tops(lo[2], lo[3]);
+    o[s].u[2] = tops(hi[0], hi[1]);
+    o[s].u[3] = tops(hi[2], hi[3]);
+    if (s + 1 < NP) {
+      float l[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+#pragma unroll
+      for (int v = 0; v < 4; ++v) rest(o[s].u[v], l[2 * v], l[2 * v + 1]);
+      lo = f4{l[0], l[1], l[2], l[3]};
+      hi = f4{l[4], l[5], l[6], l[7]};
+    }
+  }
+}
+
+// c += a b over the pairs of parts of order at most LIM, smallest first
+template <int NA, int NB, int LIM>
+__device__ inline f4 dot(const Op* a, const Op* b, f4 c) {
+#pragma unroll
+  for (int o = LIM; o >= 0; --o)
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (o - i >= 0 && o - i < NB) c = mfma(a[i], b[o - i], c);
+  return c;
+}
+
+template <bool BF>
+__device__ inline float load1(const void* p, int64_t i) {
+  return BF ? __uint_as_float((uint32_t)((const uint16_t*)p)[i] << 16) : ((const float*)p)[i];
+}
+
+int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+constexpr size_t kLds = 160 * 1024;
+
+}  // namespace
+}  // namespace kron
