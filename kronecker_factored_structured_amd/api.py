@@ -632,7 +632,14 @@ def _distill_args(logits, ids, teacher, teacher_lse, labels, weights, temperatur
 
 def _distill_out(d: KronDistill, logits: torch.Tensor, out: Optional[torch.Tensor]) -> torch.Tensor:
     if out is None:
-        return torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        # rows as far apart as the logits' and as aligned: the gradients then move as whole vectors, like the logits
+        (N, V), es, ld = logits.shape, logits.element_size(), d.ld
+        if ld >= 2 * V:      # (a view of some columns of something wide: dense)
+            ld = V
+        d.ldd = ld
+        lead = logits.data_ptr() % 16 // es
+        buf = torch.empty(lead + max(N, 1) * ld, dtype=logits.dtype, device=logits.device)
+        return buf[lead:lead + N * ld].view(N, ld)[:, :V]
     if out.dtype != logits.dtype or out.device != logits.device or out.shape != logits.shape:
         raise ValueError(f"out must be {tuple(logits.shape)} {logits.dtype} on {logits.device}")
     d.ldd = _logit_rows(out, "out")

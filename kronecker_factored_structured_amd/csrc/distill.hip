@@ -23,6 +23,8 @@
 // Exponentials are 2^(z s - c) with c = m s rounded once: the rounding of c cancels in every
 // softmax.  One exponential serves a row that needs one temperature (KD or CE alone, or T = 1);
 // at T = 2 the one of CE is the square of KD's; otherwise CE takes a second one (`two`).
+#include <algorithm>
+
 #include "kron_internal.h"
 #include "row_tile.h"
 
@@ -402,7 +404,7 @@ __global__ __launch_bounds__(NT, 4) void distill_row_kernel(DistillArgs a) {
   constexpr int NW = NT / 64;
   extern __shared__ uint32_t bits[];
   __shared__ Shared<NT> sh;
-  const int64_t row = blockIdx.x;
+  const int64_t row = a.row0 + blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const float w = a.weights ? a.weights[row] : 1.f / (float)a.N;
   const Tile z(a.logits, row, a.ld, a.V), o(a.dlogits, row, a.ldd, a.V);
@@ -487,7 +489,7 @@ __global__ __launch_bounds__(kCT) void distill_part_kernel(DistillArgs a) {
   constexpr int VE = Tile::VE;
   __shared__ uint32_t bits[kCT * kCV * VE / 32];
   __shared__ Shared<kCT> sh;
-  const int64_t row = blockIdx.x / a.chunks;
+  const int64_t row = a.row0 + blockIdx.x / a.chunks;
   const int chunk = (int)(blockIdx.x % a.chunks), tid = threadIdx.x;
   const float w = a.weights ? a.weights[row] : 1.f / (float)a.N;
   if (w == 0.f) return;
@@ -572,8 +574,9 @@ __global__ __launch_bounds__(kCT) void distill_emit_kernel(DistillArgs a) {
   using Tile = RowTile<BF>;
   constexpr int VE = Tile::VE;
   __shared__ uint32_t bits[kCT * kCV * VE / 32];
+  __shared__ int32_t seen[STATS || JOIN ? 2 * kMaxK : 1];      // the row's tokens, hashed
   __shared__ Shared<kCT> sh;
-  const int64_t row = STATS ? blockIdx.x : blockIdx.x / a.chunks;
+  const int64_t row = a.row0 + (STATS ? blockIdx.x : blockIdx.x / a.chunks);
   const int chunk = STATS ? 0 : (int)(blockIdx.x % a.chunks), tid = threadIdx.x;
   const float w = a.weights ? a.weights[row] : 1.f / (float)a.N;
   const Tile z(a.logits, row, a.ld, a.V), o(a.dlogits, row, a.ldd, a.V);
@@ -597,6 +600,8 @@ __global__ __launch_bounds__(kCT) void distill_emit_kernel(DistillArgs a) {
   const int64_t lab = c.ce ? a.labels[row] : -1;
   const bool labok = !c.ce || (lab >= 0 && lab < a.V);
   const int bit0 = j0 * VE;
+  if (STATS || JOIN)
+    for (int i = tid; i < 2 * kMaxK; i += kCT) seen[i] = -1;
   Kept k = mark_kept<kCT, BF>(a, row, z, lab, bits, bit0, STATS ? 0 : (max(j1 - j0, 0) * VE + 31) / 32, sh);
   const bool lnear = labok && c.ce && !STATS && ((int)lab + z.off) / VE >= j0 && ((int)lab + z.off) / VE < j1;
   float zl = 0.f, tr = 0.f, t1 = 0.f;
@@ -605,15 +610,21 @@ __global__ __launch_bounds__(kCT) void distill_emit_kernel(DistillArgs a) {
     // the gathered logits come from the parts: in place, other workgroups may have written theirs
     if (k.have) k.z = a.zk[row * a.k + tid];
     if (c.ce && labok) zl = a.zl[row];
-    join_row(a, row, c, tr, t1, sh);      // (its barriers also complete the slots)
-    // over the whole row a token may be repeated far from this chunk
+    // over the whole row a token may be repeated far from this chunk (the table is twice what there can be:
+    // a free place ends the search)
     if (k.have) {
-      k.own = true;
-      for (int l = 0; l < tid; ++l)
-        if (sh.kid[l] == (int32_t)k.id) {
-          k.own = false;
+      uint32_t h = (uint32_t)k.id * 2654435761u >> 23;
+      static_assert(2 * kMaxK == 1 << (32 - 23), "the table's size");
+      for (int old; (old = atomicCAS(&seen[h], -1, (int32_t)k.id)) != -1; h = (h + 1) % (2 * kMaxK))
+        if (old == (int32_t)k.id) {
           sh.flag[0] = 1;
+          break;
         }
+    }
+    join_row(a, row, c, tr, t1, sh);      // (its barriers also complete the slots)
+    if (k.have && sh.flag[0]) {
+      k.own = true;
+      for (int l = 0; l < tid; ++l) k.own = k.own && sh.kid[l] != (int32_t)k.id;
     }
     k.z = c.place(k.z);
     zl = c.place(zl);
@@ -707,24 +718,24 @@ int chunk_vectors(int64_t N, int V, bool bf16) {
 }
 
 template <bool BF, int NT, int NV>
-hipError_t launch_row(const DistillArgs& a, hipStream_t s) {
+hipError_t launch_row(const DistillArgs& a, int64_t rows, hipStream_t s) {
   const size_t lds = ((size_t)a.V + 7 + 31) / 32 * 4;
-  hipLaunchKernelGGL((distill_row_kernel<BF, NT, NV>), dim3((unsigned)a.N), dim3(NT), lds, s, a);
+  hipLaunchKernelGGL((distill_row_kernel<BF, NT, NV>), dim3((unsigned)rows), dim3(NT), lds, s, a);
   return hipGetLastError();
 }
 
 template <bool BF>
-hipError_t launch_type(const DistillArgs& a, int mode, hipStream_t s) {
+hipError_t launch_type(const DistillArgs& a, int mode, int64_t rows, hipStream_t s) {
   if (mode == 0 && whole_rows(a)) {
     const int64_t nv = max_vectors(a.V, BF);
-    if (nv <= 4 * 512) return launch_row<BF, 512, 4>(a, s);
-    if (nv <= 7 * 512) return launch_row<BF, 512, 7>(a, s);
-    if (nv <= 10 * 512) return launch_row<BF, 512, 10>(a, s);
-    if (nv <= 13 * 512) return launch_row<BF, 512, 13>(a, s);
-    if (nv <= 8 * 1024) return launch_row<BF, 1024, 8>(a, s);
-    return launch_row<BF, 1024, 13>(a, s);
+    if (nv <= 4 * 512) return launch_row<BF, 512, 4>(a, rows, s);
+    if (nv <= 7 * 512) return launch_row<BF, 512, 7>(a, rows, s);
+    if (nv <= 10 * 512) return launch_row<BF, 512, 10>(a, rows, s);
+    if (nv <= 13 * 512) return launch_row<BF, 512, 13>(a, rows, s);
+    if (nv <= 8 * 1024) return launch_row<BF, 1024, 8>(a, rows, s);
+    return launch_row<BF, 1024, 13>(a, rows, s);
   }
-  const dim3 grid((unsigned)(a.N * a.chunks)), rows((unsigned)a.N), nt(kCT);
+  const dim3 grid((unsigned)(rows * a.chunks)), nt(kCT);
   if (mode != 2) {
     hipLaunchKernelGGL((distill_part_kernel<BF>), grid, nt, 0, s, a);
     const hipError_t e = hipGetLastError();
@@ -733,7 +744,7 @@ hipError_t launch_type(const DistillArgs& a, int mode, hipStream_t s) {
   if (mode == 0)
     hipLaunchKernelGGL((distill_emit_kernel<BF, false, true>), grid, nt, 0, s, a);
   else if (mode == 1)
-    hipLaunchKernelGGL((distill_emit_kernel<BF, true, true>), rows, nt, 0, s, a);
+    hipLaunchKernelGGL((distill_emit_kernel<BF, true, true>), dim3((unsigned)rows), nt, 0, s, a);
   else
     hipLaunchKernelGGL((distill_emit_kernel<BF, false, false>), grid, nt, 0, s, a);
   return hipGetLastError();
@@ -761,8 +772,10 @@ hipError_t launch_distill(DistillArgs a, int mode, void* ws, hipStream_t s) {
     w += up256((size_t)a.N * a.k * 4);
     a.zl = (float*)w;
   }
-  if (a.N > 0) {
-    const hipError_t e = a.bf16 ? launch_type<true>(a, mode, s) : launch_type<false>(a, mode, s);
+  const int64_t most = kMaxGroups / a.chunks;
+  for (a.row0 = 0; a.row0 < a.N; a.row0 += most) {
+    const int64_t rows = std::min(most, a.N - a.row0);
+    const hipError_t e = a.bf16 ? launch_type<true>(a, mode, rows, s) : launch_type<false>(a, mode, rows, s);
     if (e != hipSuccess) return e;
   }
   if (mode != 2) {

@@ -944,7 +944,7 @@ kron_status_t kron_topk_logits(int64_t N, int32_t V, int64_t ld, int32_t k, int3
   const Range outs[3] = {{ids, (size_t)N * k * 4, "ids"}, {vals, (size_t)N * k * 4, "vals"}, {lse, (size_t)N * 4, "lse"}};
   kron_status_t st;
   if ((st = check_align(outs, 3)) != KRON_OK || (st = check_alias(outs, 3, ins, 1)) != KRON_OK) return st;
-  const kron::TopkArgs a{N, ld, V, k, dtype == KRON_BF16, temperature, logits, ids, vals, lse};
+  kron::TopkArgs a{N, ld, V, k, dtype == KRON_BF16, temperature, logits, ids, vals, lse};
   const hipError_t e = kron::launch_topk(a, stream);
   if (e != hipSuccess) return hip_fail(e, "kron_topk_logits launch");
   return ok();

@@ -297,6 +297,9 @@ struct DistillRow {
   double kl, psum, pt;
   float total, rest, t1, zl, w, pad_;
 };
+// Workgroups of a launch (of at most 1024 threads: a grid has less than 2^32 of them); more rows take several.
+constexpr int64_t kMaxGroups = int64_t(1) << 21;
+
 struct DistillArgs {
   int64_t N, ld, ldd;
   int32_t V, k;
@@ -312,7 +315,8 @@ struct DistillArgs {
   float* stats;
   float* loss;
   void* dlogits;
-  // set by launch_distill: vectors of a chunk, chunks of a row, and the workspace
+  // set by launch_distill: the launch's first row, vectors of a chunk, chunks of a row, and the workspace
+  int64_t row0;
   int32_t cv, chunks;
   DistillRow* rows;           // N
   float* part;                // N x chunks partial sums
@@ -331,7 +335,8 @@ struct TopkArgs {
   int32_t* ids;
   float* vals;
   float* lse;
+  int64_t row0;       // set by launch_topk: the launch's first row
 };
-hipError_t launch_topk(const TopkArgs& a, hipStream_t s);
+hipError_t launch_topk(TopkArgs a, hipStream_t s);
 
 }  // namespace kron

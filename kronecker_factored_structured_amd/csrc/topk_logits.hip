@@ -9,6 +9,8 @@
 // that defeat the threshold (many equal values, the top in few threads, fewer vectors than k) and
 // rows with a NaN or an infinite maximum take an exact bisection on the value's key, then on the
 // token among the equal ones.  Bound by the one read of z.
+#include <algorithm>
+
 #include "kron_internal.h"
 #include "row_tile.h"
 
@@ -34,13 +36,13 @@ __global__ __launch_bounds__(NT, 4) void topk_kernel(TopkArgs a) {
   using Tile = RowTile<BF>;
   constexpr int VE = Tile::VE;
   constexpr int NW = NT / 64;
-  __shared__ uint64_t cand[kCap];      // key, then the complement of the token: larger is better
+  __shared__ alignas(16) uint64_t cand[kCap];      // key, then the complement of the token: larger is better
   __shared__ uint32_t tmax[NT];
   __shared__ float red[NW];
   __shared__ uint32_t cnt[2][NW];
   __shared__ uint32_t ncand, tau_s, top_s;
 
-  const int64_t row = blockIdx.x;
+  const int64_t row = a.row0 + blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const Tile z(a.logits, row, a.ld, a.V);
   const int nvec = z.vectors();
@@ -50,9 +52,11 @@ __global__ __launch_bounds__(NT, 4) void topk_kernel(TopkArgs a) {
   auto each_vec = [&](auto f) {
     if constexpr (RES) {
       fresh(reg);
+      int first = tid;      // (a new value as well: the masks of every vector's and value's place are not kept either)
+      asm volatile("" : "+v"(first));
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if (tid + i * NT < nvec) f(reg[i], tid + i * NT);
+        if (first + i * NT < nvec) f(reg[i], first + i * NT);
     } else {
       for (int j = tid; j < nvec; j += NT) f(z.load(j), j);
     }
@@ -189,10 +193,15 @@ __global__ __launch_bounds__(NT, 4) void topk_kernel(TopkArgs a) {
     nc = ncand < (uint32_t)kCap ? ncand : (uint32_t)kCap;      // (exactly k)
   }
   // a candidate's place is the number of better ones (all are distinct: the tokens differ)
+  if (tid < 8 && nc + tid < kCap) cand[nc + tid] = 0;
+  __syncthreads();
   for (uint32_t i = tid; i < nc; i += NT) {
     const uint64_t x = cand[i];
     int place = 0;
-    for (uint32_t l = 0; l < nc; ++l) place += cand[l] > x ? 1 : 0;
+    for (uint32_t l = 0; l < nc; l += 8) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) place += cand[l + j] > x ? 1 : 0;
+    }
     if (place < a.k) {
       a.ids[row * a.k + place] = (int32_t)~(uint32_t)x;
       a.vals[row * a.k + place] = value_of((uint32_t)(x >> 32));
@@ -201,9 +210,9 @@ __global__ __launch_bounds__(NT, 4) void topk_kernel(TopkArgs a) {
 }
 
 template <bool BF>
-hipError_t launch_type(const TopkArgs& a, hipStream_t s) {
+hipError_t launch_type(const TopkArgs& a, int64_t rows, hipStream_t s) {
   const int64_t nvec = ((int64_t)a.V + 7) / (BF ? 8 : 4) + 1;   // of a row that starts anywhere
-  const dim3 grid((unsigned)a.N);
+  const dim3 grid((unsigned)rows);
   if (nvec <= 512 * 4)
     hipLaunchKernelGGL((topk_kernel<BF, 512, 4, true>), grid, dim3(512), 0, s, a);
   else if (nvec <= 512 * 8)
@@ -219,9 +228,13 @@ hipError_t launch_type(const TopkArgs& a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_topk(const TopkArgs& a, hipStream_t s) {
-  if (a.N == 0) return hipSuccess;
-  return a.bf16 ? launch_type<true>(a, s) : launch_type<false>(a, s);
+hipError_t launch_topk(TopkArgs a, hipStream_t s) {
+  for (a.row0 = 0; a.row0 < a.N; a.row0 += kMaxGroups) {
+    const int64_t rows = std::min(kMaxGroups, a.N - a.row0);
+    const hipError_t e = a.bf16 ? launch_type<true>(a, rows, s) : launch_type<false>(a, rows, s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace kron

@@ -360,3 +360,85 @@ def test_binding_refusals():
         k.kron_topk_logits(z, 51)
     with pytest.raises(ValueError, match="stats"):
         k.kron_distill_bwd(z, ids, t, torch.zeros(4, 4, device="cuda"), torch.ones(1, device="cuda"))
+
+
+@pytest.mark.parametrize("V,dtype,T,alpha,tail", [
+    (900, F32, 1.5, 0.5, True), (32003, F32, 1.0, 1.0, True), (50257, BF, 2.0, 0.5, False), (106489, BF, 1.0, 0.0, False)])
+def test_two_calls_over_many_rows(V, dtype, T, alpha, tail):
+    """The forward of many rows keeps the statistics that the backward call takes."""
+    N, k = 520, 30
+    print(f"[distill two calls] V={V} {dtype} T={T} alpha={alpha} tail={tail}", flush=True)
+    _, z = rows(N, V, 1, dtype, V)
+    ids, t, lse, lab, w = teacher(N, V, k, V, T, tail)
+    w[np.arange(N) % 90 != 7] = 0
+    ids[97, 5:9] = ids[97, 2]
+    ids[187, ::2] = -1
+    if tail:
+        lse[97] += 3
+    d = dict(teacher_lse=dev(lse), labels=dev(lab), weights=dev(w), temperature=T, alpha=alpha)
+    gi = dev(ids.astype(np.int32))
+    loss, stats = K().kron_distill_fwd(z, gi, dev(t), **d)
+    dz = K().kron_distill_bwd(z, gi, dev(t), stats, torch.tensor([0.5], device="cuda"), **d)
+    close(loss, dz, z, ids, t, lse, lab, w, T, alpha, dtype, up=0.5)
+    assert bool(torch.isfinite(stats).all()) and not dz[0].any()
+    got = K().kron_distill_bwd(z, gi, dev(t), stats, torch.tensor([0.5], device="cuda"), out=z, **d)
+    assert got is z and torch.equal(z, dz)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_topk_nan_and_infinity_in_long_rows(dtype):
+    """In rows that are cut: a NaN, infinities in several parts, a part of -infinity, fewer than k finite values."""
+    V, k = 200001, 50
+    z = torch.randn(5, V, generator=torch.Generator().manual_seed(3)).to(dtype)
+    z[0, V - 3] = float("nan")
+    z[1, 21] = z[1, V - 1] = float("inf")
+    z[2, :V // 2] = -float("inf")
+    z[3] = -float("inf")
+    z[3, [5, V // 2, V - 2]] = torch.tensor([1.0, 3.0, 2.0], dtype=dtype)
+    z[4] = 7.0
+    ids, vals, lse = K().kron_topk_logits(z.cuda(), k)
+    assert ids[0, 0].item() == V - 3 and bool(torch.isnan(vals[0, 0])) and bool(torch.isnan(lse[0]))
+    assert ids[1, :2].tolist() == [21, V - 1] and vals[1, 1].item() == float("inf") and lse[1].item() == float("inf")
+    for r in range(2, 5):
+        wi, wv, wl = OD.topk(f64(z[r:r + 1]), k)
+        assert np.array_equal(ids[r].cpu().numpy(), wi[0]) and np.array_equal(f64(vals[r]), wv[0])
+        assert abs(lse[r].item() - wl[0]) <= REL + 4 * 2.0 ** -24 * abs(wl[0])
+
+
+def test_more_rows_than_a_launch_has_workgroups():
+    """2^21 + 70 rows of a small vocabulary: the rows behind the first launch are as right as those in it."""
+    N, V, k = 2 ** 21 + 70, 6, 2
+    print("[rows] topk", flush=True)
+    z = torch.randn(N, V, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1))
+    ids, vals, lse = K().kron_topk_logits(z, k)
+    v, i = torch.sort(z, dim=1, descending=True, stable=True)
+    assert torch.equal(vals, v[:, :k]) and torch.equal(ids, i[:, :k].int())
+    assert bool(((lse - torch.logsumexp(z.double(), 1)).abs() <= REL + 4 * 2.0 ** -24 * lse.abs()).all())
+    print("[rows] distill", flush=True)
+    t = vals * 0.5
+    out = K().kron_distill(z, ids, t)
+    loss, stats = K().kron_distill_fwd(z, ids, t)
+    dz = K().kron_distill_bwd(z, ids, t, stats, torch.ones(1, device="cuda"))
+    p = torch.softmax(t.double(), 1)
+    q = torch.softmax(z.double(), 1)
+    want = q.clone().scatter_add_(1, ids.long(), -p) / N
+    # (absolute sizes of a row's terms sum to two)
+    for got in (out["dlogits"], dz):
+        assert bool(((got.double() - want).abs() <= 2 * REL / N).all())
+    kd = (p * (torch.log(p) - torch.log(torch.gather(q, 1, ids.long())))).sum(1)
+    scale = (p * (torch.log(p).abs() + torch.log(torch.gather(q, 1, ids.long())).abs())).sum(1).mean()
+    for got in (out["loss"], loss):
+        assert abs(got.item() - kd.mean().item()) <= REL * float(scale)
+
+
+@pytest.mark.parametrize("dtype,pad,off", [(F32, 47, 1), (BF, 47, 3), (BF, 0, 5), (F32, 200, 0)])
+def test_gradient_rows_stand_like_the_logits(dtype, pad, off):
+    """Without `out` the gradients' rows are as far apart and as aligned as the logits', or dense behind wide gaps."""
+    N, V, k = 5, 150, 3
+    _, z = rows(N, V, pad, dtype, 4, off=off)
+    ids, t, _, _, w = teacher(N, V, k, 4, 1.0, False)
+    a = K().kron_distill(z, dev(ids.astype(np.int32)), dev(t), weights=dev(w))
+    close(a["loss"], a["dlogits"], z, ids, t, None, None, w, 1.0, 1.0, dtype)
+    dz = a["dlogits"]
+    assert dz.shape == z.shape and dz.stride(1) == 1 and dz.stride(0) == (V if pad >= V else V + pad)
+    assert (dz.data_ptr() - z.data_ptr()) % 16 == 0
