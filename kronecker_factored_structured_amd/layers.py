@@ -1,5 +1,6 @@
-"""torch modules over libkron: the Kronecker-factored layer, the Kronecker-sparse layer
-and the tutorial's MLP training step.  Marshalling only; every step runs in libkron.
+"""torch modules over libkron: the Kronecker-factored layer, its gated form, the Kronecker-sparse
+layer, the distillation loss and the tutorial's MLP training step.  Marshalling only; every step
+runs in libkron.
 """
 from __future__ import annotations
 
@@ -8,6 +9,7 @@ from typing import Optional
 
 import torch
 from torch import nn
+from torch.autograd.function import once_differentiable
 
 from . import api
 
@@ -82,6 +84,88 @@ class _L1Fn(torch.autograd.Function):
     def backward(ctx, g):
         (S,) = ctx.saved_tensors
         return api.kron_l1_penalty_grad(S.contiguous(), 1.0, g.reshape(1).contiguous())
+
+
+class _KronGLUFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, S, A, B, bias, act: str):
+        rows = x.reshape(-1, x.shape[-1]).contiguous()
+        ctx.save_for_backward(rows, S, A, B, bias)
+        ctx.act, ctx.shape = act, x.shape
+        y = api.kron_glu_fwd(rows, S, A, B, bias, act=act)
+        return y.view(*x.shape[:-1], y.shape[1])
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, S, A, B, bias = ctx.saved_tensors
+        g = api.kron_glu_bwd(x, S, A, B, bias, dy.reshape(x.shape[0], dy.shape[-1]).contiguous(), act=ctx.act,
+                             want_dx=ctx.needs_input_grad[0])
+        dx = g["dx"]
+        # the parameters' gradients come in float32
+        to = [None if g[k] is None else g[k].to(x.dtype) for k in ("dS", "dA", "dB", "dbias")]
+        return (None if dx is None else dx.view(ctx.shape), *to, None)
+
+
+class KronGLU(nn.Module):
+    """y = act(x W_0 + b_0) o (x W_1 + b_1) with W_f = sum_i kron(S_f o A_fi, B_fi): the gated half
+    of a feed-forward block, both projections Kronecker layers of one shape in one kernel.  Parameters
+    as KronLinear's with a leading 2 (gate, up).  x: [..., in_features], float32 or bfloat16 like the
+    parameters; act: silu, gelu, gelu_tanh or relu.  The backward recomputes the projections."""
+
+    def __init__(self, in_features: int, out_features: int, m: int, r: int, n: Optional[int] = None, act: str = "silu",
+                 with_S: bool = True, bias: bool = True, device=None, dtype=None):
+        super().__init__()
+        n = m if n is None else n
+        if in_features % m or out_features % n:
+            raise ValueError("in_features must be a multiple of m and out_features of n")
+        if act not in api.KRON_ACTS:
+            raise ValueError(f"act must be one of {sorted(api.KRON_ACTS)}, got {act!r}")
+        p, q = in_features // m, out_features // n
+        kw = dict(device=device, dtype=dtype)
+        self.S = nn.Parameter(torch.ones(2, p, q, **kw)) if with_S else None
+        self.A = nn.Parameter(torch.randn(2, r, p, q, **kw) / math.sqrt(p))
+        self.B = nn.Parameter(torch.randn(2, r, m, n, **kw) / math.sqrt(m))
+        self.bias = nn.Parameter(torch.zeros(2, out_features, **kw)) if bias else None
+        self.act = act
+
+    def forward(self, x):
+        return _KronGLUFn.apply(x, self.S, self.A, self.B, self.bias, self.act)
+
+
+class _KronDistillFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, ids, teacher, teacher_lse, labels, weights, temperature: float, alpha: float):
+        ctx.kw = dict(temperature=temperature, alpha=alpha)
+        loss, stats = api.kron_distill_fwd(logits, ids, teacher, teacher_lse, labels, weights, **ctx.kw)
+        ctx.save_for_backward(logits, ids, teacher, teacher_lse, labels, weights, stats)
+        return loss.view(())
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, gout):
+        logits, ids, teacher, lse, labels, weights, stats = ctx.saved_tensors
+        dz = api.kron_distill_bwd(logits, ids, teacher, stats, gout.reshape(1).contiguous(), lse, labels, weights, **ctx.kw)
+        return (dz,) + (None,) * 7
+
+
+class KronDistillLoss(nn.Module):
+    """Distillation from a teacher's top logits (kron_topk_logits), mixed with the cross-entropy on
+    labels: alpha T^2 KD + (1 - alpha) CE over the rows, weighted (weights None: their mean, weight 0: a
+    padded position).  logits [..., V] with ids and teacher [..., k], the others [...]; the gradient goes to
+    the logits alone."""
+
+    def __init__(self, temperature: float = 1.0, alpha: float = 1.0):
+        super().__init__()
+        if not (temperature > 0 and 0 <= alpha <= 1):
+            raise ValueError(f"temperature must be positive and alpha in [0, 1], got {temperature} and {alpha}")
+        self.temperature, self.alpha = float(temperature), float(alpha)
+
+    def forward(self, logits, ids=None, teacher=None, teacher_lse=None, labels=None, weights=None):
+        def rows(t, last):
+            return None if t is None else t.flatten(0, -1 - last) if t.dim() > 1 + last else t
+        return _KronDistillFn.apply(rows(logits, 1), rows(ids, 1), rows(teacher, 1), rows(teacher_lse, 0), rows(labels, 0),
+                                    rows(weights, 0), self.temperature, self.alpha)
 
 
 class KSLinear(nn.Module):

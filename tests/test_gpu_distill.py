@@ -442,3 +442,36 @@ def test_gradient_rows_stand_like_the_logits(dtype, pad, off):
     dz = a["dlogits"]
     assert dz.shape == z.shape and dz.stride(1) == 1 and dz.stride(0) == (V if pad >= V else V + pad)
     assert (dz.data_ptr() - z.data_ptr()) % 16 == 0
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_loss_module(dtype):
+    """KronDistillLoss over a batch of sequences whose vocabulary is padded in memory: the loss and, behind another
+    factor, the logits' gradient."""
+    Bs, L, V, k, T, alpha = 2, 9, 333, 12, 2.0, 0.5
+    _, z = rows(Bs * L, V, 7, dtype, 21)
+    ids, t, lse, lab, w = teacher(Bs * L, V, k, 21, T, True)
+    w[4] = 0
+    leaf = z.view(Bs, L, V).detach().requires_grad_()
+    mod = K().KronDistillLoss(temperature=T, alpha=alpha)
+    shape = lambda a, *s: dev(a).view(Bs, L, *s)
+    loss = mod(leaf, shape(ids.astype(np.int32), k), shape(t, k), shape(lse), shape(lab), shape(w))
+    assert loss.shape == () and loss.dtype == F32
+    (g,) = torch.autograd.grad(3 * loss, [leaf])
+    close(loss.view(1), g.reshape(Bs * L, V), z, ids, t, lse, lab, w, T, alpha, dtype, up=3.0)
+    ce = K().KronDistillLoss(alpha=0.0)(leaf, labels=shape(lab))
+    close(ce.view(1), None, z, None, None, None, lab, None, 1.0, 0.0, dtype)
+
+
+def test_loss_module_refusals():
+    k = K()
+    for kw in (dict(temperature=0.0), dict(alpha=1.5)):
+        with pytest.raises(ValueError, match="temperature"):
+            k.KronDistillLoss(**kw)
+    with pytest.raises(ValueError, match="needed when alpha"):
+        k.KronDistillLoss()(torch.zeros(2, 10, device="cuda", requires_grad=True))
+    z = torch.randn(2, 10, device="cuda", requires_grad=True)
+    ids, t = torch.zeros(2, 1, device="cuda", dtype=torch.int32), torch.zeros(2, 1, device="cuda")
+    (g,) = torch.autograd.grad(k.KronDistillLoss()(z, ids, t), [z], create_graph=True)
+    with pytest.raises(RuntimeError):      # one derivative only
+        g.sum().backward()

@@ -205,3 +205,61 @@ def test_binding_refusals():
     with pytest.raises(k._lib.KronError, match="exceeds 64"):
         big, _ = inputs(1, 2, 65, 2, 2, 2, 1, F32)
         k.kron_glu_fwd(*big)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("p,q,m,n,r", [(50, 20, 30, 28, 2), (20, 30, 28, 50, 3), (50, 40, 30, 28, 3), (50, 28, 20, 50, 1),
+                                       (33, 20, 40, 33, 7), (20, 40, 50, 20, 2)])
+def test_glu_sides_either_side_of_32(p, q, m, n, r, dtype):
+    """One side of a factor above 32 and the other below, with S and without, over more rows than a pass holds."""
+    for k, (N, S) in enumerate(((701, True), (300, False))):
+        print(f"[glu 32] N={N} p={p} q={q} m={m} n={n} r={r} {dtype} S={S}", flush=True)
+        a, dy = inputs(N + k, N, p, q, m, n, r, dtype, S, True)
+        h = [f64(v) for v in a]
+        same(K().kron_glu_fwd(*a), OG.forward(*h, "silu"), "y")
+        got, want = K().kron_glu_bwd(*a, dy), OG.backward(*h, f64(dy), "silu")
+        for key in ("dx", "dA", "dB", "dbias") + (("dS",) if S else ()):
+            same(got[key], want[key], key)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_module(dtype):
+    """KronGLU: leading dimensions, gradients of the input and of each parameter, no gradient asked of x."""
+    k = K()
+    torch.manual_seed(0)
+    mod = k.KronGLU(4 * 5, 6 * 3, m=5, r=2, n=3, act="gelu", device="cuda", dtype=dtype)
+    with torch.no_grad():
+        mod.bias.normal_(std=0.3)
+        mod.S.mul_(torch.rand_like(mod.S))
+    x = torch.randn(3, 7, 20, device="cuda").to(dtype).requires_grad_()
+    y = mod(x)
+    dy = torch.randn(3, 7, 18, device="cuda").to(dtype)
+    assert y.shape == (3, 7, 18) and y.dtype == dtype
+    h = [f64(v) for v in (x.reshape(21, 20), mod.S, mod.A, mod.B, mod.bias)]
+    same(y.reshape(21, 18), OG.forward(*h, "gelu"), "y")
+    y.backward(dy)
+    want = OG.backward(*h, f64(dy).reshape(21, 18), "gelu")
+    for key, t in (("dx", x), ("dS", mod.S), ("dA", mod.A), ("dB", mod.B), ("dbias", mod.bias)):
+        assert t.grad.shape == t.shape and t.grad.dtype == dtype
+        same(t.grad.reshape(want[key].shape), want[key], key)
+    y2 = mod(x.detach())
+    y2.sum().backward()
+    assert mod(x[:, :0]).shape == (3, 0, 18)
+    plain = k.KronGLU(20, 18, m=5, r=1, n=3, with_S=False, bias=False, device="cuda")
+    (g,) = torch.autograd.grad(plain(x.detach().float()).sum(), [plain.A])
+    assert bool(g.abs().sum() > 0) and len(list(plain.parameters())) == 2
+
+
+def test_module_refusals():
+    k = K()
+    with pytest.raises(ValueError, match="multiple of m"):
+        k.KronGLU(21, 18, m=5, r=1, n=3, device="cuda")
+    with pytest.raises(ValueError, match="act"):
+        k.KronGLU(20, 18, m=5, r=1, n=3, act="tanh", device="cuda")
+    with pytest.raises(ValueError, match="x must be"):
+        k.KronGLU(20, 18, m=5, r=1, n=3, device="cuda")(torch.zeros(2, 19, device="cuda"))
+    mod = k.KronGLU(20, 18, m=5, r=1, n=3, device="cuda")
+    x = torch.randn(2, 20, device="cuda", requires_grad=True)
+    (g,) = torch.autograd.grad(mod(x).sum(), [x], create_graph=True)
+    with pytest.raises(RuntimeError):      # one derivative only
+        g.sum().backward()

@@ -1,0 +1,157 @@
+"""The gated block, the teacher's top logits, the distillation loss and the fused Adam step together: a
+student with a gated Kronecker block distilled from a teacher's answers.
+
+Tolerances: the block's and the loss's own (TOL_F32 of the largest value, 600 * 2^-24 of the terms' sizes), the
+dense products between them in fp64 here and there.  A gradient behind the head is a sum of V products of the
+logits' gradient with the head's weights: off by the two bars added, against the sum of their sizes."""
+import numpy as np
+import pytest
+
+from _harness import TOL_F32
+from oracle import distill as OD
+from oracle import glu as OG
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+REL = 600 * 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _needs_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def f64(t):
+    return None if t is None else t.detach().cpu().double().numpy()
+
+
+def student(seed=0):
+    import kronecker_factored_structured_amd as K
+    torch.manual_seed(seed)
+    mod = K.KronGLU(8 * 6, 10 * 7, m=6, r=2, n=7, act="silu", device="cuda")
+    with torch.no_grad():
+        mod.S.mul_(torch.rand_like(mod.S).round())
+        mod.bias.normal_(std=0.2)
+    return K, mod, torch.randn(70, 501, device="cuda") * 0.3
+
+
+class Head(torch.autograd.Function):
+    """y @ W through 64 bits: what is tested stands on either side of it."""
+    @staticmethod
+    def forward(ctx, y, W):
+        ctx.save_for_backward(W)
+        return (y.double() @ W.double()).float()
+
+    @staticmethod
+    def backward(ctx, dz):
+        (W,) = ctx.saved_tensors
+        return (dz.double() @ W.double().t().contiguous()).float(), None
+
+
+def oracle(mod, W, x, ids, vals, lse, w, T):
+    h = [f64(v) for v in (x, mod.S, mod.A, mod.B, mod.bias)]
+    z = OG.forward(*h, "silu") @ f64(W)
+    loss, dz, scale, lscale = OD.loss_and_grad(z, ids.cpu().numpy().astype(int), f64(vals), f64(lse), None, f64(w), T, 1.0)
+    return loss, lscale, OG.backward(*h, dz @ f64(W).T, "silu"), OG.backward(*h, np.abs(scale) @ np.abs(f64(W)).T, "silu")
+
+
+def test_a_distillation_step():
+    """Loss and every parameter's gradient against the oracle, then one Adam step of the gradients."""
+    K, mod, W = student()
+    N, k, T = 57, 20, 2.0
+    x = torch.randn(N, 48, device="cuda")
+    zt = torch.randn(N, 501, device="cuda") * 2
+    ids, vals, lse = K.kron_topk_logits(zt, k, temperature=T)
+    w = torch.ones(N, device="cuda")
+    w[::9] = 0
+    w /= w.sum()
+    loss = K.KronDistillLoss(temperature=T)(Head.apply(mod(x), W), ids, vals, lse, weights=w)
+    loss.backward()
+    want, lscale, grads, bound = oracle(mod, W, x, ids, vals, lse, w, T)
+    # logits off by TOL_F32 of their largest value move the loss by at most twice that times T (weights sum to one)
+    z = f64(Head.apply(mod(x), W))
+    move = TOL_F32 * np.abs(f64(mod(x))).max() * np.abs(f64(W)).sum(0).max()
+    assert abs(loss.item() - want) <= REL * lscale + 2 * T * move
+    params = [mod.S, mod.A, mod.B, mod.bias]
+    for key, t in zip(("dS", "dA", "dB", "dbias"), params):
+        # (each logit's gradient moves by at most 2 move / T of its row's size: the same bar on the sizes' gradient)
+        top = np.abs(grads[key]).max()
+        size = np.abs(bound[key]).max()
+        assert np.abs(f64(t.grad) - grads[key]).max() <= TOL_F32 * max(top, size) + (REL + 4 * move) * size, key
+    m, v = [torch.zeros_like(p) for p in params], [torch.zeros_like(p) for p in params]
+    old = [f64(p) for p in params]
+    K.kron_adam_l1_step([p.data for p in params], [p.grad for p in params], m, v, 1, 1e-3)
+    for o, p in zip(old, params):      # a first step moves each value by lr g / (|g| + eps)
+        g = f64(p.grad)
+        assert np.abs(f64(p) - (o - 1e-3 * g / (np.abs(g) + 1e-8))).max() <= 4 * 2.0 ** -24 * (np.abs(o).max() + 1e-3) + 1e-9
+
+
+def test_the_step_captured():
+    """The calls of a step in one graph, replayed over new data, against the same calls made eagerly."""
+    K, mod, W = student(1)
+    N, k, T = 33, 16, 1.5
+    x = torch.randn(N, 48, device="cuda")
+    zt = torch.randn(N, 501, device="cuda") * 2
+    S, A, B, bias = (p.detach() for p in (mod.S, mod.A, mod.B, mod.bias))
+    Wt = W.t().contiguous()
+
+    def step():
+        ids, vals, lse = K.kron_topk_logits(zt, k, temperature=T)
+        y = K.kron_glu_fwd(x, S, A, B, bias)
+        out = K.kron_distill(y @ W, ids, vals, teacher_lse=lse, temperature=T)
+        g = K.kron_glu_bwd(x, S, A, B, bias, out["dlogits"] @ Wt)
+        return [out["loss"], g["dx"], g["dS"], g["dA"], g["dB"], g["dbias"]]
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cap = step()
+    for i in range(4):
+        g = torch.Generator().manual_seed(i)
+        x.copy_(torch.randn(N, 48, generator=g))
+        zt.copy_(torch.randn(N, 501, generator=g) * 2)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(cap, step()):
+            assert torch.equal(a, b), i
+
+
+def test_two_graphs_and_eager_calls_side_by_side():
+    """Two captured steps and an eager one on three streams at once: each its own workspace, each its own answer."""
+    K, mod, _ = student(2)
+    S, A, B, bias = (p.detach() for p in (mod.S, mod.A, mod.B, mod.bias))
+    xs = [torch.randn(400, 48, device="cuda") for _ in range(3)]
+    dys = [torch.randn(400, 70, device="cuda") for _ in range(3)]
+    zs = [torch.randn(40, 30011, device="cuda") for _ in range(3)]
+    tops = [K.kron_topk_logits(torch.randn(40, 30011, device="cuda"), 8) for _ in range(3)]
+
+    def step(i):
+        g = K.kron_glu_bwd(xs[i], S, A, B, bias, dys[i])
+        d = K.kron_distill(zs[i], tops[i][0], tops[i][1], tops[i][2])
+        return [K.kron_glu_fwd(xs[i], S, A, B, bias), g["dx"], g["dA"], g["dB"], d["loss"], d["dlogits"]]
+
+    want = [step(i) for i in range(3)]
+    graphs = []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = step(i)
+        graphs.append((g, out))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for _ in range(5):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                graphs[i][0].replay()
+        with torch.cuda.stream(streams[2]):
+            eager = step(2)
+    torch.cuda.synchronize()
+    for i, got in enumerate((graphs[0][1], graphs[1][1], eager)):
+        for a, b in zip(got, want[i]):
+            assert torch.equal(a, b), i
