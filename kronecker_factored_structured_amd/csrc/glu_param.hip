@@ -327,9 +327,8 @@ template <bool XBF, int NX, int NB, int NC, int TP, int TN, int TO>
 hipError_t launch_param_k(const GluParam& k, size_t lds, hipStream_t s) {
   constexpr int NTH = 64 * param_waves(XBF, TP > 2, TN > 2, TO > 2);
   constexpr auto kernel = glu_param_kernel<XBF, NX, NB, NC, TP, TN, TO, NTH>;
-  static const hipError_t attr =
-      hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)kLds);
-  if (attr != hipSuccess) return attr;
+  const hipError_t e = allow_lds<kernel>();
+  if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kernel, dim3((unsigned)((k.groups[0] + k.groups[1]) * k.pair_groups)), dim3(NTH), lds, s, k);
   return hipGetLastError();
 }

@@ -18,6 +18,7 @@
 #pragma once
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "kron_internal.h"
@@ -136,6 +137,20 @@ __device__ inline float load1(const void* p, int64_t i) {
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 constexpr size_t kLds = 160 * 1024;
+
+// Lets a kernel have all of a CU's LDS, once for each device.
+template <auto kernel>
+hipError_t allow_lds() {
+  static std::atomic<uint64_t> done{0};
+  int device = 0;
+  hipError_t e = hipGetDevice(&device);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (device & 63);
+  if (done.load(std::memory_order_relaxed) & bit) return hipSuccess;
+  e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)kLds);
+  if (e == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 }  // namespace
 }  // namespace kron

@@ -299,9 +299,8 @@ __global__ __launch_bounds__(64 * W, W / 4) void glu_rows_kernel(GluRows a) {
 
 template <auto kernel, int W>
 hipError_t launch_rows_g(const GluRows& k, int64_t groups, size_t lds, hipStream_t s) {
-  static const hipError_t attr =
-      hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)kLds);
-  if (attr != hipSuccess) return attr;
+  const hipError_t e = allow_lds<kernel>();
+  if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kernel, dim3((unsigned)groups, (unsigned)k.qsplit), dim3(64 * W), lds, s, k);
   return hipGetLastError();
 }
@@ -322,8 +321,24 @@ hipError_t launch_rows_k(GluRows k, hipStream_t s) {
   if (all <= kLds && units > 256 * WS)
     return launch_rows_g<glu_rows_kernel<MODE, XBF, OBF, NX, NB, NZ, NC, LIM, MK, PK, WR, true>, WR>(
         k, std::min<int64_t>(256, (units + WR - 1) / WR), all, s);
-  return launch_rows_g<glu_rows_kernel<MODE, XBF, OBF, NX, NB, NZ, NC, LIM, MK, PK, WS, false>, WS>(
-      k, (units + WS - 1) / WS, 2 * one + over, s);
+  // a grid has less than 2^32 threads: more rows take several launches
+  constexpr int64_t kMost = int64_t(1) << 24;
+  for (int64_t r0 = 0; r0 < k.N; r0 += kMost) {
+    GluRows part = k;
+    const int64_t out = r0 * k.q * k.n * (OBF ? 2 : 4);
+    part.N = std::min(kMost, k.N - r0);
+    for (int f = 0; f < 2; ++f) {
+      part.x[f] = (const char*)k.x[f] + r0 * k.ldx * (XBF ? 2 : 4);
+      if (MODE == 1) part.d[f] = k.d[f] + r0 * k.q * k.n4;
+    }
+    if (MODE == 1) part.dy = (const char*)k.dy + out;
+    else part.y = (char*)k.y + out;
+    const int64_t groups = (part.N * (NT > 2 ? 2 : 1) + WS - 1) / WS;
+    const hipError_t e = launch_rows_g<glu_rows_kernel<MODE, XBF, OBF, NX, NB, NZ, NC, LIM, MK, PK, WS, false>, WS>(
+        part, groups, 2 * one + over, s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <int MODE, bool XBF, bool OBF, int NX, int NB, int NZ, int NC, int LIM>

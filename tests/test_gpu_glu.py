@@ -263,3 +263,29 @@ def test_module_refusals():
     (g,) = torch.autograd.grad(mod(x).sum(), [x], create_graph=True)
     with pytest.raises(RuntimeError):      # one derivative only
         g.sum().backward()
+
+
+def test_more_rows_than_a_launch_takes():
+    """2^24 + 9 rows of one value each, with factors of more ranks than fit a workgroup: the last rows are as
+    right as the first."""
+    N, r = 2 ** 24 + 9, 16
+    print("[glu] many rows", flush=True)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x, dy = (torch.randn(N, 1, device="cuda", generator=g) for _ in range(2))
+    A, B = torch.randn(2, r, 1, 1, device="cuda", generator=g), torch.randn(2, r, 1, 1, device="cuda", generator=g)
+    W = (A.double() * B.double()).sum((1, 2, 3))
+    y = K().kron_glu_fwd(x, None, A, B, act="relu").double()
+    xd, dyd = x.double(), dy.double()
+    gate, up = xd * W[0], xd * W[1]
+    want = torch.relu(gate) * up
+    assert (y - want).abs().max() <= TOL_F32 * want.abs().max()
+    got = K().kron_glu_bwd(x, None, A, B, None, dy, act="relu")
+    dg, du = dyd * up * (gate > 0), dyd * torch.relu(gate)
+    dx = dg * W[0] + du * W[1]
+    assert (got["dx"].double() - dx).abs().max() <= TOL_F32 * dx.abs().max()
+    dW = torch.stack([(xd * dg).sum(), (xd * du).sum()])
+    # (a sum of N terms of either sign, each within the bar of its size)
+    size = torch.stack([(xd * dg).abs().sum(), (xd * du).abs().sum()])
+    for f in range(2):
+        assert bool(((got["dA"][f].double() - B[f].double() * dW[f]).abs() <= TOL_F32 * B[f].double().abs() * size[f]).all())
+        assert bool(((got["dB"][f].double() - A[f].double() * dW[f]).abs() <= TOL_F32 * A[f].double().abs() * size[f]).all())

@@ -155,3 +155,32 @@ def test_two_graphs_and_eager_calls_side_by_side():
     for i, got in enumerate((graphs[0][1], graphs[1][1], eager)):
         for a, b in zip(got, want[i]):
             assert torch.equal(a, b), i
+
+
+def test_modules_captured():
+    """Forward and backward of the modules in one graph, with no eager graph of the same leaves alive."""
+    K, mod, W = student(3)
+    N, k = 24, 6
+    x = torch.randn(N, 48, device="cuda")
+    ids, vals, lse = K.kron_topk_logits(torch.randn(N, 501, device="cuda"), k)
+    lossf = K.KronDistillLoss(temperature=2.0)
+    params = list(mod.parameters())
+
+    def grads():
+        return torch.autograd.grad(lossf(mod(x) @ W, ids, vals), params)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        for _ in range(2):
+            grads()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cap = grads()
+    for i in range(3):
+        x.copy_(torch.randn(N, 48, generator=torch.Generator().manual_seed(i)))
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(cap, grads()):
+            assert torch.equal(a, b), i
