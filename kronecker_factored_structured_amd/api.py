@@ -6,6 +6,7 @@ tensors on a GPU; anything else raises (there is no CPU fallback).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import Optional, Sequence
 
@@ -46,7 +47,16 @@ def _need(t: Optional[torch.Tensor], name: str, shape: tuple, dtype=torch.float3
 
 
 def _stream(device: torch.device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    # (the handle itself: torch.cuda.current_stream makes a Stream object around it, 2 us of a call's 15)
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(device.index))
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(device: torch.device):
+    """The context of a call on `device`: nothing to switch where it is the current one (as it mostly is)."""
+    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
 def layer_shape(x_rows: int, S, A: torch.Tensor, B: torch.Tensor, flags: int = 0) -> KronShape:
@@ -535,7 +545,7 @@ def kron_glu_fwd(x: torch.Tensor, S: Optional[torch.Tensor], A: torch.Tensor, B:
     _need(out, "out", (x.shape[0], shape.q * shape.n), x.dtype, dev)
     y = out if out is not None else torch.empty(x.shape[0], shape.q * shape.n, device=dev, dtype=x.dtype)
     ws = _workspace(workspace, kron_glu_workspace_bytes(shape, x.dtype, S is not None), dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         check("kron_glu_fwd", _lib.lib().kron_glu_fwd(
             ctypes.byref(shape), code, dt, _ptr(x), _ptr(S), _ptr(A), _ptr(B), _ptr(bias), _ptr(y), _ptr(ws),
             ctypes.c_size_t(ws.numel()), _stream(dev)))
@@ -560,7 +570,7 @@ def kron_glu_bwd(x: torch.Tensor, S: Optional[torch.Tensor], A: torch.Tensor, B:
         if k not in o:
             o[k] = torch.empty(size, device=dev, dtype=dtype) if asked else None
     ws = _workspace(workspace, kron_glu_workspace_bytes(shape, x.dtype, S is not None, True), dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         check("kron_glu_bwd", _lib.lib().kron_glu_bwd(
             ctypes.byref(shape), code, dt, _ptr(x), _ptr(S), _ptr(A), _ptr(B), _ptr(bias), _ptr(dy), _ptr(o["dx"]),
             _ptr(o["dS"]), _ptr(o["dA"]), _ptr(o["dB"]), _ptr(o["dbias"]), _ptr(ws), ctypes.c_size_t(ws.numel()),
@@ -595,7 +605,7 @@ def kron_topk_logits(logits: torch.Tensor, k: int, temperature: float = 1.0) -> 
     ids = torch.empty(N, k, dtype=torch.int32, device=dev)
     vals = torch.empty(N, k, device=dev)
     lse = torch.empty(N, device=dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         check("kron_topk_logits", _lib.lib().kron_topk_logits(
             N, V, ld, k, dt, float(temperature), _ptr(logits), _ptr(ids), _ptr(vals), _ptr(lse), _stream(dev)))
     return ids, vals, lse
@@ -633,11 +643,13 @@ def _distill_args(logits, ids, teacher, teacher_lse, labels, weights, temperatur
 def _distill_out(d: KronDistill, logits: torch.Tensor, out: Optional[torch.Tensor]) -> torch.Tensor:
     if out is None:
         # rows as far apart as the logits' and as aligned: the gradients then move as whole vectors, like the logits
-        (N, V), es, ld = logits.shape, logits.element_size(), d.ld
+        (N, V), ld = logits.shape, d.ld
         if ld >= 2 * V:      # (a view of some columns of something wide: dense)
             ld = V
         d.ldd = ld
-        lead = logits.data_ptr() % 16 // es
+        lead = logits.data_ptr() % 16 // logits.element_size()
+        if lead == 0:
+            return torch.empty_strided((N, V), (ld, 1), dtype=logits.dtype, device=logits.device)
         buf = torch.empty(lead + max(N, 1) * ld, dtype=logits.dtype, device=logits.device)
         return buf[lead:lead + N * ld].view(N, ld)[:, :V]
     if out.dtype != logits.dtype or out.device != logits.device or out.shape != logits.shape:
@@ -662,7 +674,7 @@ def kron_distill(logits: torch.Tensor, ids: Optional[torch.Tensor], teacher: Opt
     loss = torch.empty(1, device=dev)
     L = _lib.lib()
     ws = _workspace(workspace, int(L.kron_distill_workspace_bytes(ctypes.byref(d))), dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         check("kron_distill", L.kron_distill(ctypes.byref(d), *ptrs, _ptr(loss), _ptr(dz), _ptr(ws),
                                              ctypes.c_size_t(ws.numel()), _stream(dev)))
     return dict(loss=loss, dlogits=dz)
@@ -679,7 +691,7 @@ def kron_distill_fwd(logits: torch.Tensor, ids: Optional[torch.Tensor], teacher:
     stats = torch.empty(logits.shape[0], KRON_DISTILL_STATS, device=dev)
     L = _lib.lib()
     ws = _workspace(workspace, int(L.kron_distill_workspace_bytes(ctypes.byref(d))), dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         check("kron_distill_fwd", L.kron_distill_fwd(ctypes.byref(d), *ptrs, _ptr(loss), _ptr(stats), _ptr(ws),
                                                      ctypes.c_size_t(ws.numel()), _stream(dev)))
     return loss, stats
@@ -695,7 +707,7 @@ def kron_distill_bwd(logits: torch.Tensor, ids: Optional[torch.Tensor], teacher:
     dev = logits.device
     _need(stats, "stats", (logits.shape[0], KRON_DISTILL_STATS), device=dev)
     _need(gout, "gout", (1,), device=dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         check("kron_distill_bwd", _lib.lib().kron_distill_bwd(ctypes.byref(d), *ptrs, _ptr(stats), _ptr(gout), _ptr(dz),
                                                               _stream(dev)))
     return dz

@@ -23,7 +23,7 @@ struct PackArgs {
   const void* A;
   const void* B;
   u4* t[4];               // see GluTables
-  int64_t lanes[4];       // lanes of each table (all f, i): tile x step x 64, without parts
+  int lanes[4];           // lanes of each table (all f, i): tile x step x 64, without parts
 };
 
 __device__ inline float raw(const void* t, int64_t i, int bf16) {
@@ -32,7 +32,7 @@ __device__ inline float raw(const void* t, int64_t i, int bf16) {
 __device__ inline int chained(int g, int e) { return e < 4 ? 4 * g + e : 12 + 4 * g + e; }
 
 __global__ __launch_bounds__(256) void glu_pack_kernel(PackArgs a) {
-  int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  int id = blockIdx.x * 256 + threadIdx.x;      // (32 bits throughout: divisions are most of this kernel's time)
   int w = 0;
   while (w < a.tables && id >= a.lanes[w]) id -= a.lanes[w++];
   if (w >= a.tables) return;
@@ -40,12 +40,9 @@ __global__ __launch_bounds__(256) void glu_pack_kernel(PackArgs a) {
   const int kd = w == 0 ? a.m : w == 1 ? a.p : w == 2 ? a.n : a.q;
   const int cd = w == 0 ? a.n : w == 1 ? a.q : w == 2 ? a.m : a.p;
   const int steps = (kd + 31) / 32, tiles = (cd + 15) / 16;
-  const int lane = (int)(id & 63), g = lane >> 4, c = lane & 15;
-  int64_t b = id >> 6;
-  const int ks = (int)(b % steps);
-  b /= steps;
-  const int tile = (int)(b % tiles);
-  const int fi = (int)(b / tiles), f = fi / a.r;
+  const int lane = id & 63, g = lane >> 4, c = lane & 15;
+  const int b = id >> 6, ks = b & (steps - 1), bt = steps == 2 ? b >> 1 : b;      // (a side of at most 64 has one step or two)
+  const int fi = bt / tiles, tile = bt % tiles, f = fi >= a.r;
   const bool isb = (w & 1) == 0;
   const int col = 16 * tile + c;
   float v[8];
@@ -56,12 +53,12 @@ __global__ __launch_bounds__(256) void glu_pack_kernel(PackArgs a) {
     if (k < kd && col < cd) {
       if (isb) {
         const int mi = w == 0 ? k : col, ni = w == 0 ? col : k;
-        x = raw(a.B, ((int64_t)fi * a.m + mi) * a.n + ni, a.bf16);
+        x = raw(a.B, (fi * a.m + mi) * a.n + ni, a.bf16);
       } else {
         const int pi = w == 1 ? k : col, qi = w == 1 ? col : k;
-        x = raw(a.A, ((int64_t)fi * a.p + pi) * a.q + qi, a.bf16);
+        x = raw(a.A, (fi * a.p + pi) * a.q + qi, a.bf16);
         // the product of two bf16 values has 16 bits: exact in fp32 and in two parts
-        if (a.S) x *= raw(a.S, ((int64_t)f * a.p + pi) * a.q + qi, a.bf16);
+        if (a.S) x *= raw(a.S, (f * a.p + pi) * a.q + qi, a.bf16);
       }
     }
     v[e] = x;
@@ -69,7 +66,7 @@ __global__ __launch_bounds__(256) void glu_pack_kernel(PackArgs a) {
   Op o[3];
   split<3>(f4{v[0], v[1], v[2], v[3]}, f4{v[4], v[5], v[6], v[7]}, o);
   const int parts = isb ? a.parts_b : a.parts_c;
-  u4* dst = a.t[w] + (id >> 6) * parts * 64 + lane;
+  u4* dst = a.t[w] + b * parts * 64 + lane;
   for (int s = 0; s < parts; ++s) dst[s * 64] = s == 0 ? o[0].u : s == 1 ? o[1].u : o[2].u;
 }
 
@@ -91,67 +88,66 @@ struct ReduceArgs {
   float* dbias;
 };
 
-// Sum over `rows` of column c0 + col (32 consecutive ones; they may cross a block's end): thread (col, y).
-__device__ inline double column_sum(const float* part, int rows, int64_t column, bool in, int y, double (*red)[33],
-                                    int col) {
-  double s0 = 0.0, s1 = 0.0;
+// 32 rows of threads: thread y's share of a column's sum over `rows` (rows y, y + 32, ...; four loads on their way).
+constexpr int kRedY = 32;
+__device__ inline double column_part(const float* part, int rows, int64_t column, bool in, int y) {
+  double s = 0.0;
   if (in) {
     const float* src = part + part_index(rows, 0, column);
     int g = y;
-    for (; g + 8 < rows; g += 16) {
-      const float u = src[(int64_t)g * kRedCols], w = src[(int64_t)(g + 8) * kRedCols];
-      s0 += (double)u;
-      s1 += (double)w;
-    }
-    if (g < rows) s0 += (double)src[(int64_t)g * kRedCols];
-  }
-  __syncthreads();
-  red[y][col] = s0 + s1;
-  __syncthreads();
-  double t = 0.0;
+    for (; g + 3 * kRedY < rows; g += 4 * kRedY) {
+      float u[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) t += red[i][col];
-  return t;
+      for (int i = 0; i < 4; ++i) u[i] = src[(int64_t)(g + kRedY * i) * kRedCols];
+      s += ((double)u[0] + (double)u[1]) + ((double)u[2] + (double)u[3]);
+    }
+    for (; g < rows; g += kRedY) s += (double)src[(int64_t)g * kRedCols];
+  }
+  return s + __shfl_xor(s, 32, 64);      // (y and y + 1 stand in one wavefront)
 }
 
-__global__ __launch_bounds__(256) void glu_reduce_kernel(ReduceArgs a) {
-  __shared__ double red[8][33];
+__global__ __launch_bounds__(32 * kRedY) void glu_reduce_kernel(ReduceArgs a) {
+  __shared__ double red[KRON_GLU_MAX_RANK][kRedY / 2][32];
   const int col = threadIdx.x & 31, y = threadIdx.x >> 5;
+  auto total = [&](int i) {
+    double t = 0.0;
+#pragma unroll
+    for (int k = 0; k < kRedY / 2; ++k) t += red[i][k][col];
+    return t;
+  };
   int b = blockIdx.x;
   const int bB = (a.nB + 31) / 32, bb = a.dbias ? (a.nbias + 31) / 32 : 0;
-  if (b < bB) {
-    const int c = 32 * b + col;
-    const double t = column_sum(a.part[1], a.rows[1], c, c < a.nB, y, red, col);
-    if (y == 0 && c < a.nB) a.dB[c] = (float)t;
+  if (b < bB + bb || !a.S) {
+    // dB; then dbias, dA
+    const int kind = b < bB ? 1 : 0, at = b < bB ? 0 : b < bB + bb ? a.nC : 0;
+    const int c = 32 * (b < bB ? b : b < bB + bb ? b - bB : b - bB - bb) + col;
+    const bool in = c < (b < bB ? a.nB : b < bB + bb ? a.nbias : a.nC);
+    float* out = b < bB ? a.dB : b < bB + bb ? a.dbias : a.dA;
+    red[0][y / 2][col] = column_part(a.part[kind], a.rows[kind], at + c, in, y);
+    __syncthreads();
+    if (y == 0 && in) out[c] = (float)total(0);
     return;
   }
-  b -= bB;
-  if (b < bb) {
-    const int c = 32 * b + col;
-    const double t = column_sum(a.part[0], a.rows[0], a.nC + c, c < a.nbias, y, red, col);
-    if (y == 0 && c < a.nbias) a.dbias[c] = (float)t;
-    return;
-  }
-  b -= bb;
-  if (!a.S) {
-    const int c = 32 * b + col;
-    const double t = column_sum(a.part[0], a.rows[0], c, c < a.nC, y, red, col);
-    if (y == 0 && c < a.nC) a.dA[c] = (float)t;
-    return;
-  }
+  b -= bB + bb;
   const int per = (a.pq + 31) / 32, f = b / per, e = 32 * (b % per) + col;
   const bool in = e < a.pq;
-  const float s = in ? raw(a.S, (int64_t)f * a.pq + e, a.bf16) : 0.f;
-  double ds = 0.0;
-  for (int i = 0; i < a.r; ++i) {
-    const int64_t c = ((int64_t)f * a.r + i) * a.pq + e;
-    const double t = column_sum(a.part[0], a.rows[0], c, in, y, red, col);
-    if (y == 0 && in) {
-      a.dA[c] = (float)((double)s * t);
-      ds += (double)raw(a.A, c, a.bf16) * t;
-    }
+  for (int i = 0; i < a.r; ++i)
+    red[i][y / 2][col] = column_part(a.part[0], a.rows[0], ((int64_t)f * a.r + i) * a.pq + e, in, y);
+  __syncthreads();
+  double t = 0.0;      // thread y < r has rank y's dC; then its part of dS
+  if (y < a.r && in) {
+    const int64_t c = ((int64_t)f * a.r + y) * a.pq + e;
+    t = total(y);
+    a.dA[c] = (float)((double)raw(a.S, (int64_t)f * a.pq + e, a.bf16) * t);
+    t *= (double)raw(a.A, c, a.bf16);
   }
-  if (y == 0 && in) a.dS[(int64_t)f * a.pq + e] = (float)ds;
+  __syncthreads();
+  if (y < a.r) red[y][0][col] = t;
+  __syncthreads();
+  if (!in || y != 0) return;
+  double ds = 0.0;
+  for (int i = 0; i < a.r; ++i) ds += red[i][0][col];
+  a.dS[(int64_t)f * a.pq + e] = (float)ds;
 }
 
 struct Sizes {
@@ -202,7 +198,7 @@ hipError_t launch_pack(const GluArgs& a, const Sizes& z, int tables, u4* const t
   int64_t total = 0;
   for (int i = 0; i < tables; ++i) {
     k.t[i] = t[i];
-    k.lanes[i] = z.lanes[i];
+    k.lanes[i] = (int)z.lanes[i];
     total += z.lanes[i];
   }
   hipLaunchKernelGGL(glu_pack_kernel, dim3((unsigned)((total + 255) / 256)), dim3(256), 0, s, k);
@@ -276,7 +272,7 @@ hipError_t launch_glu_bwd(const GluArgs& a, void* ws, hipStream_t s) {
   ra.S = a.S; ra.A = a.A; ra.dB = a.dB; ra.dA = a.dA; ra.dS = a.dS; ra.dbias = a.dbias;
   const int blocks = ceil_div(ra.nB, 32) + (a.dbias ? ceil_div(ra.nbias, 32) : 0) +
                      (a.S ? 2 * ceil_div(ra.pq, 32) : ceil_div(ra.nC, 32));
-  hipLaunchKernelGGL(glu_reduce_kernel, dim3((unsigned)blocks), dim3(256), 0, s, ra);
+  hipLaunchKernelGGL(glu_reduce_kernel, dim3((unsigned)blocks), dim3(32 * kRedY), 0, s, ra);
   return hipGetLastError();
 }
 
