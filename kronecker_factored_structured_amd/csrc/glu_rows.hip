@@ -160,7 +160,8 @@ __global__ __launch_bounds__(64 * W, W / 4) void glu_rows_kernel(GluRows a) {
   }
 
   const bool vec = XBF ? (a.ldm & 7) == 0 : (a.ldm & 3) == 0;
-  for (int64_t unit = (int64_t)blockIdx.x * W + wave;; unit += (int64_t)gridDim.x * W) {
+  // pairs of units (a row's two, or two rows) go round the workgroups, so that few rows are spread over the CUs
+  for (int64_t unit = 2 * ((int64_t)(wave >> 1) * gridDim.x + blockIdx.x) + (wave & 1);; unit += (int64_t)gridDim.x * W) {
     const int64_t row = NT > 2 ? unit >> 1 : unit;
     const int nt0 = NT > 2 ? 2 * (int)(unit & 1) : 0, ntn = min(2, NT - nt0);
     const bool live = row < a.N;
@@ -318,9 +319,9 @@ hipError_t launch_rows_k(GluRows k, hipStream_t s) {
   // the blocks of one (f, i); those beside an odd last tile are read too
   const size_t one = (size_t)(NT * MK * NB + ceil_div(QT, k.qsplit) * PK * NC) * 1024, over = (MK * NB + PK * NC) * 1024;
   const size_t all = 2 * k.r * one + over;
-  if (all <= kLds && units > 256 * WS)
+  if (all <= kLds)
     return launch_rows_g<glu_rows_kernel<MODE, XBF, OBF, NX, NB, NZ, NC, LIM, MK, PK, WR, true>, WR>(
-        k, std::min<int64_t>(256, (units + WR - 1) / WR), all, s);
+        k, std::min<int64_t>(std::max(1, 256 / k.qsplit), (units + 1) / 2), all, s);
   // a grid has less than 2^32 threads: more rows take several launches
   constexpr int64_t kMost = int64_t(1) << 24;
   for (int64_t r0 = 0; r0 < k.N; r0 += kMost) {
