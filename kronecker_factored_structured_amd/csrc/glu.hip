@@ -172,8 +172,10 @@ Sizes sizes_of(const GluArgs& a) {
   z.n4 = (a.n + 3) & ~3;
   z.off_d = (off + 255) & ~int64_t(255);
   z.off_part[0] = z.off_d + ((2 * a.N * a.q * z.n4 * 4 + 255) & ~int64_t(255));
-  // The parameters' kernel: one workgroup a CU, the kinds' numbers of them by their numbers of products, each
-  // with at least four rows where there are that many.
+  // The parameters' kernel: one workgroup a CU, each with at least four rows where there are that many.  The
+  // kinds get numbers of them by their products for a row and pair, and what staging and splitting it costs
+  // either kind: as much as 150 products (by the products alone 8192 x (768 -> 2048) bf16 took 292 us and 8192 x
+  // (1024 -> 2048) 546, so 274 and 515; half each 276 and 509, but r = 6 of 64 x 32 and 16 x 64 308, so 297).
   z.waves = param_waves(a.bf16, a.p > 32, a.n > 32, std::max(a.q, a.m) > 32);
   z.share = 1;
   while (2 * z.share * 2 * a.r <= z.waves) z.share *= 2;
@@ -181,7 +183,7 @@ Sizes sizes_of(const GluArgs& a) {
   const int PT = ceil_div(a.p, 16), QT = ceil_div(a.q, 16), MT = ceil_div(a.m, 16), NT = ceil_div(a.n, 16);
   const int PK = ceil_div(a.p, 32), QK = ceil_div(a.q, 32), MK = ceil_div(a.m, 32), NK = ceil_div(a.n, 32);
   const int tb = a.bf16 ? 1 : 6, tc = a.bf16 ? (a.S ? 5 : 3) : 6, tx = a.bf16 ? 3 : 6;      // instructions of a product
-  const double w0 = PT * 2 * NK * MK * tb + PT * QT * NK * 6, w1 = 2 * PK * NT * QK * tc + MT * NT * PK * tx;
+  const double w0 = 150 + PT * 2 * NK * MK * tb + PT * QT * NK * 6, w1 = 150 + 2 * PK * NT * QK * tc + MT * NT * PK * tx;
   const int total = std::max(2, 256 / z.pair_groups);
   const int64_t most = (a.N + 3) / 4;
   z.groups[0] = std::min(std::max((int)(total * w0 / (w0 + w1) + 0.5), 1), total - 1);

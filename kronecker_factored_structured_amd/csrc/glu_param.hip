@@ -205,24 +205,35 @@ __device__ inline void param_body(const GluParam& a, int rowgroup, int pairgroup
     };
     Op o1[2][KO][N1], o2[2][NO];
     read1(0, o1[0]);
+    read1(1, o1[1]);
 #pragma unroll
     for (int ko = 0; ko < KI; ++ko)
       if (ko < steps) {
         Op h[TI][3];
         read2(ko, 0, o2[0]);
+        // tiles in pairs: four products side by side, so that none waits for the one before it
 #pragma unroll
-        for (int t = 0; t < TI; ++t) {
-          if (t + 1 < TI) read1(t + 1, o1[(t + 1) & 1]);
-          else if (ko + 1 < KI) read1(0, o1[0]);
-          f4 w[2];
-          w[0] = w[1] = f4{0.f, 0.f, 0.f, 0.f};
+        for (int t = 0; t < TI; t += 2) {
+          f4 w[2][2];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i / 2][i % 2] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int k = 0; k < KO; ++k)
             if (k < tabK) {
 #pragma unroll
-              for (int u = 0; u < 2; ++u) w[u] = dot<NTAB, N1, 2>(tab[2 * ko + u][k], o1[t & 1][k], w[u]);
+              for (int o = 2; o >= 0; --o)
+#pragma unroll
+                for (int i = 0; i < NTAB; ++i)
+                  if (o - i >= 0 && o - i < N1)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) w[j / 2][j % 2] = mfma(tab[2 * ko + j % 2][k][i], o1[j / 2][k][o - i], w[j / 2][j % 2]);
             }
-          split<3>(w[0], w[1], h[t]);
+          if (TI > 2 && (t + 2 < TI || ko + 1 < KI)) {      // (two tiles stay for the next step)
+            read1((t + 2) % TI, o1[0]);
+            read1((t + 3) % TI, o1[1]);
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j) split<3>(w[j][0], w[j][1], h[t + j]);
         }
 #pragma unroll
         for (int t = 0; t < TO; ++t)
