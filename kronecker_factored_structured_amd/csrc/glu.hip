@@ -6,6 +6,10 @@
 //   dC_fi = sum_rows Z_fi d_f^T,  dB_fi = sum_rows X^T (C_fi d_f),  dA = S o dC,  dS = sum_i A_i o dC_i
 // The products are in glu_rows.hip (forward, gradients of both projections, dX) and glu_param.hip (the
 // factors' gradients); here are the layout of the factors, the last sums and the order of the launches.
+//
+// Small calls are bound by their launches: one token through 768 -> 2048 takes 13 to 14 us, 4.5 of them the
+// layout of the factors and 5.3 the products; a backward of 61 rows 31 us in five launches of 4 to 12.  (The
+// layout is made in each call: factors change with every training step.)
 #include "glu_parts.h"
 
 namespace kron {
@@ -73,7 +77,8 @@ __global__ __launch_bounds__(256) void glu_pack_kernel(PackArgs a) {
 // ---------------------------------------------------------------------------------
 // The partial rows summed in 64 bits in a fixed order, and dA = S o dC, dS = sum_i A_i o dC_i from dC.  A
 // workgroup has a block of 32 columns (part_index): of dB, of dbias, or with S of dC's e-th elements of
-// every rank.
+// every rank.  32 rows of threads, four loads each on their way: 5.2 us for 18432 columns of 128 rows (with
+// eight rows of threads and a barrier for each rank 12).
 // ---------------------------------------------------------------------------------
 struct ReduceArgs {
   const float* part[2];

@@ -11,6 +11,13 @@
 // at 16 g + 4 ((c % 4) ^ g) + c / 4.  A wavefront stores columns of one residue mod 4 at a time: their
 // quarters of a 256-byte row differ by g.
 //
+// Measured at 8192 x (768 -> 2048) bf16, r = 4: 125 us; its products alone would take 43 (88 instructions a row
+// and pair), its reads of d_f 27.  What bounds it: two wavefronts a SIMD (their sums and B take 190 registers)
+// do not cover the LDS reads, the splits of d_f, Z and G into parts and the staging beside the products; without
+// the products the staging alone took 82 us.  2048 x 1024^2 fp32: 35 us.  Operands read one product ahead and
+// instances by the sides' tiles took it from 156 to 140 us, the kinds' shares of the workgroups (glu.hip) to
+// 125; raised wave priorities and first products four side by side changed nothing beyond 3%.
+//
 // Compiled once for each type (KRON_GLU_TYPE: 0 fp32, 1 bf16, 2 bf16 with S).
 #include "glu_parts.h"
 

@@ -11,6 +11,14 @@
 //        directly) while this one's are multiplied; a wavefront has one row
 // Few rows: the q tiles are spread over gridDim.y workgroups.
 //
+// Why in registers and LDS: nothing but X and the outputs passes through memory, and the products need
+// 21 us of the matrix cores for 8192 x (1024 -> 4096) bf16, r = 4, whose bytes need 17.  Measured there 51 us
+// (506 TFLOP/s of the formula's work, 0.42 of the rate of a large library product); streamed factors took 64.
+// What bounds it: beside 320 products a row the vector unit splits Z into parts, applies the activation and
+// packs y; four wavefronts a SIMD overlap the two only in part.  3001 x (750 -> 2021) fp32, r = 3: 48 us, six products for each of the formula's.
+// MODE 1 and 2 (8192 x (768 -> 2048) bf16): 58 and 44 us, of which the fp32 dg, du in the workspace (134 MB
+// written, then read) take 27 and 27 at the rate of a large copy.
+//
 // Compiled once for each MODE (KRON_GLU_MODE).
 #include "glu_parts.h"
 
@@ -308,7 +316,8 @@ hipError_t launch_rows_g(const GluRows& k, int64_t groups, size_t lds, hipStream
 
 template <int MODE, bool XBF, bool OBF, int NX, int NB, int NZ, int NC, int LIM, int MK, int PK>
 hipError_t launch_rows_k(GluRows k, hipStream_t s) {
-  // wavefronts of a workgroup that has a CU to itself: as many as the parts leave registers for
+  // wavefronts of a workgroup that has a CU to itself: as many as the parts leave registers for (X, the
+  // accumulators and the parts of Z: 128 registers hold one bf16 part, 168 three fp32 ones of sides up to 32)
   constexpr int WR = NX == 3 ? (MK * PK == 4 ? 8 : 12) : NZ == 3 && MK * PK == 4 ? 12 : 16;
   constexpr int WS = 8;
   const int NT = ceil_div(k.n, 16), QT = ceil_div(k.q, 16);
@@ -319,6 +328,8 @@ hipError_t launch_rows_k(GluRows k, hipStream_t s) {
   // the blocks of one (f, i); those beside an odd last tile are read too
   const size_t one = (size_t)(NT * MK * NB + ceil_div(QT, k.qsplit) * PK * NC) * 1024, over = (MK * NB + PK * NC) * 1024;
   const size_t all = 2 * k.r * one + over;
+  // Resident wherever they fit.  (Streamed, 2048 rows of 32 x 32 fp32 factors take 23 + 18 us forward and dX, resident
+  // 21 + 16.5; 61 rows of 9 x 17 and 11 x 13 9 + 8, resident 7.7 + 6.8; r = 4 of 64 x 64 fp32 does not fit.)
   if (all <= kLds)
     return launch_rows_g<glu_rows_kernel<MODE, XBF, OBF, NX, NB, NZ, NC, LIM, MK, PK, WR, true>, WR>(
         k, std::min<int64_t>(std::max(1, 256 / k.qsplit), (units + 1) / 2), all, s);
