@@ -24,10 +24,10 @@
 // softmax.  One exponential serves a row that needs one temperature (KD or CE alone, or T = 1);
 // at T = 2 the one of CE is the square of KD's; otherwise CE takes a second one (`two`).
 //
-// Measured: 8192 x 50257 bf16, k = 64, tail and labels: 412 us for 1.65 GB, 4.0 TB/s (a large copy reaches 4.9).
+// Measured: 8192 x 50257 bf16, k = 64, tail and labels: 389 us for 1.65 GB, 4.2 TB/s (a large copy reaches 4.9).
 // Two workgroups of 512 threads a CU hold 13 vectors each in registers; the passes over them (maximum, sums,
-// gradient) run while the other workgroup loads or stores.  Two calls over 2050 x 32003 fp32, k = 256: 224 us
-// (part 70, statistics 13, gradient 126 at 4.2 TB/s, loss 7).  16 x 50257 fp32: 18 us, three launches of 5, 8 and 2.
+// gradient) run while the other workgroup loads or stores.  Two calls over 2050 x 32003 fp32, k = 256: 207
+// to 210 us (part 52 at 5.0 TB/s, statistics 13, gradient 131 at 4.0, loss 7).  16 x 50257 fp32: 18 us, three launches of 5, 8 and 2.
 #include <algorithm>
 
 #include "kron_internal.h"
@@ -391,7 +391,7 @@ template <bool BF>
 __device__ inline void emit_zero(const RowTile<BF>& o, int j0, int j1, int nt) {
   for (int j = j0 + threadIdx.x; j < j1; j += nt) {
     if (o.inside(j)) {
-      *reinterpret_cast<u32x4*>(o.base + (uint32_t)(j * 16)) = u32x4{0u, 0u, 0u, 0u};
+      o.store(j, u32x4{0u, 0u, 0u, 0u});
     } else {
       for (int i = 0; i < RowTile<BF>::VE; ++i)
         if (o.first(j) + i >= 0 && o.first(j) + i < o.V) o.put(o.first(j) + i, 0.f);
@@ -466,7 +466,7 @@ __global__ __launch_bounds__(NT, 4) void distill_row_kernel(DistillArgs a) {
       if (same && kept_bits<VE>(bits, j) == 0u && z.inside(j)) {
         float x[VE];
         g.vec<BF>(c, reg[i], x);
-        *reinterpret_cast<u32x4*>(o.base + (uint32_t)(j * 16)) = Tile::packed(x);
+        o.store(j, Tile::packed(x));
       } else {
         left |= 1u << i;
       }
@@ -663,7 +663,7 @@ __global__ __launch_bounds__(kCT) void distill_emit_kernel(DistillArgs a) {
       if (same && kept_bits<VE>(bits, j - j0) == 0u && z.inside(j)) {
         float x[VE];
         g.vec<BF>(c, reg[STATS ? 0 : i], x);
-        *reinterpret_cast<u32x4*>(o.base + (uint32_t)(j * 16)) = Tile::packed(x);
+        o.store(j, Tile::packed(x));
       } else {
         left |= 1u << i;
       }
@@ -710,7 +710,8 @@ __global__ __launch_bounds__(1024) void distill_loss_kernel(DistillArgs a) {
 int64_t max_vectors(int V, bool bf16) { return ((int64_t)V + 7) / (bf16 ? 8 : 4) + 1; }   // of a row that starts anywhere
 
 // Rows in registers for enough rows to fill the GPU (two workgroups a CU).  Loss and gradient of 4096 x 50257
-// fp32: 466 us, by chunks 535; 2050 x 32003 fp32 209 and 220; 2050 x 65000 bf16 230 and 227.
+// fp32 (before non-temporal accesses): 466 us, by chunks 535; 2050 x 32003 fp32 209 and 220; 2050 x 65000 bf16
+// 230 and 227.
 constexpr int kRowVectors = 13 * 1024;
 bool whole_rows(const DistillArgs& a) { return a.N >= 512 && max_vectors(a.V, a.bf16) <= kRowVectors; }
 

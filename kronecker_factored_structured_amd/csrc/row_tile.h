@@ -52,15 +52,21 @@ struct RowTile {
     for (int w = 0; w < 4; ++w) r[w] = BF ? 0xff80ff80u : 0xff800000u;
     return r;
   }
-  // Vector j if it is wholly inside the row, else -infinity throughout.
+  // Vector j if it is wholly inside the row, else -infinity throughout.  Loads and stores of whole vectors are
+  // non-temporal: rows stream through once (loss and gradient of 8192 x 50257 bf16 446 -> 415 us, of 2050 x 32003
+  // fp32 207 -> 184, its gradient alone 163 -> 149; stores alone 436, 201 and 174; the top of 8192 x 50257 275 -> 250).
   __device__ u32x4 whole(int j) const {
-    return inside(j) ? *reinterpret_cast<const u32x4*>(base + (uint32_t)(j * 16)) : empty();
+    return inside(j) ? __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(base + (uint32_t)(j * 16))) : empty();
   }
-  // Vector j; elements outside the row are -infinity.
+  __device__ void store(int j, const u32x4& v) const {      // inside the row
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(base + (uint32_t)(j * 16)));
+  }
+  // Vector j; elements outside the row are -infinity.  (An ordinary load: what is read again.)
   __device__ u32x4 load(int j) const {
-    u32x4 r = whole(j);
+    if (inside(j)) return *reinterpret_cast<const u32x4*>(base + (uint32_t)(j * 16));
+    u32x4 r = empty();
     const int e = first(j);
-    if (inside(j) || e >= V || e + VE <= 0) return r;
+    if (e >= V || e + VE <= 0) return r;
 #pragma unroll
     for (int i = 0; i < VE; ++i) {
       if (e + i >= 0 && e + i < V) {

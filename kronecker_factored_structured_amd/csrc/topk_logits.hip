@@ -10,8 +10,8 @@
 // rows with a NaN or an infinite maximum take an exact bisection on the value's key, then on the
 // token among the equal ones.  Rows beyond 13 vectors a thread are read twice, the second time mostly from cache.
 //
-// Measured: 8192 x 50257 bf16, k = 64: 233 us, 3.55 TB/s (a large sum reads at 4.0); 257 x 131072 fp32, k = 256:
-// 60 us, 54 of them the kernel (28 at a copy's rate; one workgroup a CU passes twice over its row); one row of
+// Measured: 8192 x 50257 bf16, k = 64: 232 us, 3.56 TB/s (a large sum reads at 4.0); 257 x 131072 fp32, k = 256:
+// 59 us, 51 of them the kernel (28 at a copy's rate; one workgroup a CU passes twice over its row); one row of
 // 50257 bf16 values 10.5 us, the latency of one workgroup's passes.  Cutting long rows into chunks and joining
 // their tops took 61 to 80 us at 257 rows (each chunk ranks k candidates of its own) and 276 instead of 363 at
 // 2048 rows, k = 64; one row cut over six workgroups 15.6 us: not kept.
