@@ -86,10 +86,19 @@ class _L1Fn(torch.autograd.Function):
         return api.kron_l1_penalty_grad(S.contiguous(), 1.0, g.reshape(1).contiguous())
 
 
+def _whole(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+    """t contiguous and at a 16-byte boundary, as libkron takes it: a slice of a batch, or a gradient that
+    autograd cut out of a larger one, may start anywhere."""
+    if t is None:
+        return None
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class _KronGLUFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, S, A, B, bias, act: str):
-        rows = x.reshape(-1, x.shape[-1]).contiguous()
+        rows = _whole(x.reshape(-1, x.shape[-1]))
         ctx.save_for_backward(rows, S, A, B, bias)
         ctx.act, ctx.shape = act, x.shape
         y = api.kron_glu_fwd(rows, S, A, B, bias, act=act)
@@ -99,7 +108,7 @@ class _KronGLUFn(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy):
         x, S, A, B, bias = ctx.saved_tensors
-        g = api.kron_glu_bwd(x, S, A, B, bias, dy.reshape(x.shape[0], dy.shape[-1]).contiguous(), act=ctx.act,
+        g = api.kron_glu_bwd(x, S, A, B, bias, _whole(dy.reshape(x.shape[0], dy.shape[-1])), act=ctx.act,
                              want_dx=ctx.needs_input_grad[0])
         dx = g["dx"]
         # the parameters' gradients come in float32
@@ -145,7 +154,7 @@ class _KronDistillFn(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, gout):
         logits, ids, teacher, lse, labels, weights, stats = ctx.saved_tensors
-        dz = api.kron_distill_bwd(logits, ids, teacher, stats, gout.reshape(1).contiguous(), lse, labels, weights, **ctx.kw)
+        dz = api.kron_distill_bwd(logits, ids, teacher, stats, _whole(gout.reshape(1)), lse, labels, weights, **ctx.kw)
         return (dz,) + (None,) * 7
 
 
@@ -164,8 +173,8 @@ class KronDistillLoss(nn.Module):
     def forward(self, logits, ids=None, teacher=None, teacher_lse=None, labels=None, weights=None):
         def rows(t, last):
             return None if t is None else t.flatten(0, -1 - last) if t.dim() > 1 + last else t
-        return _KronDistillFn.apply(rows(logits, 1), rows(ids, 1), rows(teacher, 1), rows(teacher_lse, 0), rows(labels, 0),
-                                    rows(weights, 0), self.temperature, self.alpha)
+        other = [_whole(rows(t, last)) for t, last in ((ids, 1), (teacher, 1), (teacher_lse, 0), (labels, 0), (weights, 0))]
+        return _KronDistillFn.apply(rows(logits, 1), *other, self.temperature, self.alpha)
 
 
 class KSLinear(nn.Module):

@@ -184,3 +184,32 @@ def test_modules_captured():
         torch.cuda.synchronize()
         for a, b in zip(cap, grads()):
             assert torch.equal(a, b), i
+
+
+def test_modules_take_slices():
+    """Inputs and gradients that start anywhere: rows cut out of a batch, halves of a concatenation, losses stacked."""
+    K, _, _ = student()
+    torch.manual_seed(5)
+    mod = K.KronGLU(5 * 3, 7 * 3, m=3, r=2, n=3, device="cuda")
+    x = torch.randn(9, 15, device="cuda")
+    ref = mod(x)
+    cut = [mod(x[:4]), mod(x[4:5]), mod(x[5:])]
+    assert torch.equal(torch.cat(cut), ref)
+    dy = torch.randn(9, 21, device="cuda")
+    (want,) = torch.autograd.grad(mod(x), [mod.B], dy)
+    leaf = x.clone().requires_grad_()
+    y = torch.cat([mod(leaf[:4]), mod(leaf[4:5]), mod(leaf[5:])])
+    got, dx = torch.autograd.grad(y, [mod.B, leaf], dy)
+    h = [f64(v) for v in (x, mod.S, mod.A, mod.B, mod.bias)]
+    grads = OG.backward(*h, f64(dy), "silu")
+    for g in (got, want):
+        assert np.abs(f64(g) - grads["dB"]).max() <= TOL_F32 * np.abs(grads["dB"]).max()
+    assert np.abs(f64(dx) - grads["dx"]).max() <= TOL_F32 * np.abs(grads["dx"]).max()
+    # two losses stacked: the second one's upstream gradient stands four bytes into a tensor
+    z = torch.randn(6, 33, device="cuda", requires_grad=True)
+    ids, vals, lse = K.kron_topk_logits(torch.randn(7, 33, device="cuda"), 3)
+    loss = K.KronDistillLoss()
+    each = [loss(z, ids[1:], vals[1:], lse[1:]) for _ in range(2)]
+    (a,) = torch.autograd.grad((torch.stack(each) * torch.tensor([0.0, 2.0], device="cuda")).sum(), [z])
+    (b,) = torch.autograd.grad(2 * loss(z, ids[1:].clone(), vals[1:].clone(), lse[1:].clone()), [z])
+    assert torch.equal(a, b)
