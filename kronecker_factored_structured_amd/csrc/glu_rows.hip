@@ -328,7 +328,7 @@ hipError_t launch_rows_k(GluRows k, hipStream_t s) {
   // the blocks of one (f, i); those beside an odd last tile are read too
   const size_t one = (size_t)(NT * MK * NB + ceil_div(QT, k.qsplit) * PK * NC) * 1024, over = (MK * NB + PK * NC) * 1024;
   const size_t all = 2 * k.r * one + over;
-  // Resident wherever they fit.  (Streamed, 2048 rows of 32 x 32 fp32 factors take 23 + 18 us forward and dX, resident
+  // Resident wherever they fit.  (Streamed, 2048 rows of 32 x 32 fp32 factors take 23 + 18 us for dg, du and dX, resident
   // 21 + 16.5; 61 rows of 9 x 17 and 11 x 13 9 + 8, resident 7.7 + 6.8; r = 4 of 64 x 64 fp32 does not fit.)
   if (all <= kLds)
     return launch_rows_g<glu_rows_kernel<MODE, XBF, OBF, NX, NB, NZ, NC, LIM, MK, PK, WR, true>, WR>(

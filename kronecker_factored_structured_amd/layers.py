@@ -120,7 +120,9 @@ class KronGLU(nn.Module):
     """y = act(x W_0 + b_0) o (x W_1 + b_1) with W_f = sum_i kron(S_f o A_fi, B_fi): the gated half
     of a feed-forward block, both projections Kronecker layers of one shape in one kernel.  Parameters
     as KronLinear's with a leading 2 (gate, up).  x: [..., in_features], float32 or bfloat16 like the
-    parameters; act: silu, gelu, gelu_tanh or relu.  The backward recomputes the projections."""
+    parameters; act: silu, gelu, gelu_tanh or relu.  The backward recomputes the projections.
+    A backward captured into a graph has to be the only autograd graph of the parameters alive (or
+    taken with torch.autograd.grad): torch ends the process otherwise, for this module as for any."""
 
     def __init__(self, in_features: int, out_features: int, m: int, r: int, n: Optional[int] = None, act: str = "silu",
                  with_S: bool = True, bias: bool = True, device=None, dtype=None):
