@@ -369,7 +369,7 @@ hipError_t launch_rows(const GluRows& k, hipStream_t s) {
 #if KRON_GLU_MODE == 0
 hipError_t launch_glu_rows0(const GluRows& k, bool bf16, bool with_S, hipStream_t s) {
   if (!bf16) return launch_rows<0, false, false, 3, 3, 3, 3, 2>(k, s);
-  return with_S ? launch_rows<0, true, true, 1, 1, 2, 2, 1>(k, s) : launch_rows<0, true, true, 1, 1, 2, 1, 1>(k, s);
+  return with_S ? launch_rows<0, true, true, 1, 1, 2, 2, 2>(k, s) : launch_rows<0, true, true, 1, 1, 2, 1, 1>(k, s);
 }
 #elif KRON_GLU_MODE == 1
 hipError_t launch_glu_rows1(const GluRows& k, bool bf16, bool with_S, hipStream_t s) {
@@ -379,7 +379,7 @@ hipError_t launch_glu_rows1(const GluRows& k, bool bf16, bool with_S, hipStream_
 #else
 hipError_t launch_glu_rows2(const GluRows& k, bool bf16, bool with_S, hipStream_t s) {
   if (!bf16) return launch_rows<2, false, false, 3, 3, 3, 3, 2>(k, s);
-  return with_S ? launch_rows<2, false, true, 2, 1, 2, 2, 1>(k, s) : launch_rows<2, false, true, 2, 1, 2, 1, 1>(k, s);
+  return with_S ? launch_rows<2, false, true, 2, 1, 2, 2, 2>(k, s) : launch_rows<2, false, true, 2, 1, 2, 1, 1>(k, s);
 }
 #endif
 

@@ -1,0 +1,56 @@
+"""Precision of the gated block where the largest value does not hide it: positive data, each output against its own size.
+
+bf16 outputs: half a step of the value, and 2^-16 of the sum that it comes from for intermediates carried as two
+rounded bf16 parts (off by half a unit of the second one: 2^-17 of a value, once in y and twice in dx; sums are
+fp32, below 2^-17 for the 64 terms here)."""
+import numpy as np
+import pytest
+
+from oracle import glu as OG
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+F32, BF = torch.float32, torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _needs_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def K():
+    import kronecker_factored_structured_amd as mod
+    return mod
+
+
+def f64(t):
+    return None if t is None else t.detach().cpu().double().numpy()
+
+
+def half_step(v):
+    """Half a bf16 step at the size of v."""
+    return 2.0 ** (np.floor(np.log2(np.abs(v))) - 8)
+
+
+@pytest.mark.parametrize("S", [False, True])
+@pytest.mark.parametrize("N,p,q,m,n", [(256, 8, 16, 8, 32), (4096, 1, 1, 8, 32)])
+def test_bf16_intermediates_are_rounded(N, p, q, m, n, S):
+    """u = 1 exactly, so y is the gate's sum of positive terms; dx of d = dy u, which bf16 does not hold, likewise."""
+    g = torch.Generator().manual_seed(11)
+    pos = lambda *s: (0.5 + torch.rand(*s, generator=g)).to(BF).cuda()
+    x, A, B, dy = pos(N, p * m), pos(2, 1, p, q), pos(2, 1, m, n), pos(N, q * n)
+    mask = pos(2, p, q) if S else None
+    bias = torch.zeros(2, q * n, dtype=BF, device="cuda")
+    bias[1] = 1
+    A1 = A.clone()
+    A1[1] = 0
+    y = f64(K().kron_glu_fwd(x, mask, A1, B, bias, act="relu"))
+    want = OG.forward(f64(x), f64(mask), f64(A1), f64(B), f64(bias), "relu")
+    err = np.abs(y - want) - half_step(want)
+    assert (err <= 2.0 ** -16 * want).all(), (err / want).max() * 2 ** 16
+    got = f64(K().kron_glu_bwd(x, mask, A, B, bias, dy, act="relu")["dx"])
+    want = OG.backward(f64(x), f64(mask), f64(A), f64(B), f64(bias), f64(dy), "relu")["dx"]
+    err = np.abs(got - want) - half_step(want)
+    assert (err <= 2.0 ** -16 * want).all(), (err / want).max() * 2 ** 16
