@@ -20,8 +20,8 @@
 // and it keeps the thread that writes a vector of gradients off the kept tokens, which their own
 // threads write: no address is written twice, so nothing waits.
 //
-// Exponentials are 2^(z s - c) with c = m s rounded once: the rounding of c cancels in every
-// softmax.  One exponential serves a row that needs one temperature (KD or CE alone, or T = 1);
+// Exponentials are 2^(z s - c) with c = m s rounded once: the rounding of c is a factor of every one
+// and cancels in every softmax, as long as it is a moderate one (see Scale::at).  One exponential serves a row that needs one temperature (KD or CE alone, or T = 1);
 // at T = 2 the one of CE is the square of KD's; otherwise CE takes a second one (`two`).
 //
 // Measured: 8192 x 50257 bf16, k = 64, tail and labels: 389 us for 1.65 GB, 4.2 TB/s (a large copy reaches 4.9).
@@ -77,7 +77,7 @@ struct Scale {
   int two;          // CE's exponential: 0 the first one, 1 its square, 2 one of its own
   float invT, sA;   // of the first exponential
   float m0, cA, cB; // the maximum, and the shifts
-  bool huge;
+  bool far;
 
   __device__ Scale(const DistillArgs& a) {
     kd = a.alpha > 0.f;
@@ -86,16 +86,25 @@ struct Scale {
     sA = kd ? invT * kLog2e : kLog2e;
     two = !(kd && ce) || a.T == 1.f ? 0 : a.T == 2.f ? 1 : 2;
   }
-  // Where m s overflows (a row of the type's lowest or largest values), values differ from the maximum
-  // by nothing or by more than any exponential holds: they become 0 and -infinity.
+  // The rounding of c = m s stays in every exponential as a factor of up to 2^(half a unit of c): 2^8 below 2^28, but
+  // no number any more for a row of -1e10 or -1e30.  From there on the maximum is subtracted first (exact next to it).
   __device__ void at(float m) {
     m0 = m;
-    huge = fabsf(m) < INFINITY && !(fabsf(m) * fmaxf(sA, kLog2e) < 1e38f);
-    if (huge) m = 0.f;
+    far = fabsf(m) < INFINITY && !(fabsf(m) * fmaxf(sA, kLog2e) < 0x1p28f);
+    if (far) m = 0.f;
     cA = m * sA;
     cB = two == 1 ? 2.f * cA : m * kLog2e;
   }
-  __device__ float place(float x) const { return huge ? (x == m0 ? 0.f : -INFINITY) : x; }
+  __device__ float place(float x) const { return far ? x - m0 : x; }
+  // log2 of what takes sums of this shift to those of `to`, a larger maximum; sums of first exponentials, of CE's
+  __device__ float change(const Scale& to, float s, float c, float cto) const {
+    if (far) return to.far ? (m0 - to.m0) * s : fmaf(m0, s, -cto);
+    return to.far ? -fmaf(to.m0, s, -c) : c - cto;
+  }
+  __device__ float changeA(const Scale& to) const { return change(to, sA, cA, to.cA); }
+  __device__ float changeB(const Scale& to) const {
+    return two == 1 ? 2.f * changeA(to) : change(to, kLog2e, cB, to.cB);
+  }
   __device__ float first(float x) const { return __builtin_amdgcn_exp2f(fmaf(x, sA, -cA)); }
   __device__ float second(float x) const { return __builtin_amdgcn_exp2f(fmaf(x, kLog2e, -cB)); }
 };
@@ -108,7 +117,7 @@ struct Sums {      // of first exponentials off the kept tokens, and of second o
   __device__ void add(const Scale& c, const u32x4& v, uint32_t kept) {
     float x[VE], y[VE];
     Tile::values(v, x);
-    if (c.huge) {
+    if (c.far) {
 #pragma unroll
       for (int e = 0; e < VE; ++e) x[e] = c.place(x[e]);
     }
@@ -321,7 +330,7 @@ struct Grad {
     constexpr int VE = RowTile<BF>::VE;
     float x[VE];
     RowTile<BF>::values(v, x);
-    if (c.huge) {
+    if (c.far) {
 #pragma unroll
       for (int e = 0; e < VE; ++e) x[e] = c.place(x[e]);
     }
@@ -557,9 +566,9 @@ __device__ inline void join_row(const DistillArgs& a, int64_t row, Scale& c, flo
   if (p.m != c.m0) {      // the chunk's own shifts against the row's
     Scale d = c;
     d.at(p.m);
-    const bool none = c.huge || d.huge || p.m == -INFINITY;
-    fA = none ? 0.f : __builtin_amdgcn_exp2f(d.cA - c.cA);
-    fB = none ? 0.f : __builtin_amdgcn_exp2f(d.cB - c.cB);
+    const bool none = p.m == -INFINITY;
+    fA = none ? 0.f : __builtin_amdgcn_exp2f(d.changeA(c));
+    fB = none ? 0.f : __builtin_amdgcn_exp2f(d.changeB(c));
   }
   // (a row of -infinity throughout has no distribution: NaN)
   const float bad = c.m0 == -INFINITY ? __builtin_nanf("") : 0.f;
