@@ -7,7 +7,7 @@
 // values reach, and for k below the thread count few more do (for values in random order about
 // NT ln(NT / (NT - k)) in all).  Those candidates go to LDS and are ranked by counting.  Rows
 // that defeat the threshold (many equal values, the top in few threads, fewer vectors than k) and
-// rows with a NaN or an infinite maximum take an exact bisection on the value's key, then on the
+// rows with a NaN, an infinite maximum or one that is large against T take an exact bisection on the value's key, then on the
 // token among the equal ones.  Rows beyond 13 vectors a thread are read twice, the second time mostly from cache.
 //
 // Measured: 8192 x 50257 bf16, k = 64: 232 us, 3.56 TB/s (a large sum reads at 4.0); 257 x 131072 fp32, k = 256:
@@ -133,7 +133,9 @@ __global__ __launch_bounds__(NT, 4) void topk_kernel(TopkArgs a) {
   const float m = value_of(top_s);
   const float sT = kLog2e / a.T, c = m * sT;
   // the sum, and the candidates.  Below this threshold (or with k >= 2^16 of no witness) it says nothing.
-  const bool finite = fabsf(c) < 1e38f;
+  // The rounding of c is a factor of up to 2^(half a unit of c) of the sum: 2^8 below 2^28, but no number any more for
+  // a row of -1e10 or -1e30.  From there on the maximum is subtracted first (exact next to it).
+  const bool finite = fabsf(c) < 0x1p28f;
   const bool use = finite && tau_s > key_of(-INFINITY);
   const float tau_f = use ? value_of(tau_s) : INFINITY;
   float s = 0.f;
@@ -153,7 +155,8 @@ __global__ __launch_bounds__(NT, 4) void topk_kernel(TopkArgs a) {
       }
     });
   } else {
-    each([&](float f, int) { s += f != f ? f : f == m ? 1.f : 0.f; });      // (see lse below)
+    const bool some = fabsf(m) < INFINITY;
+    each([&](float f, int) { s += f != f ? f : some ? __builtin_amdgcn_exp2f((f - m) * sT) : f == m ? 1.f : 0.f; });
   }
   s = wave_sum(s);
   if (lane == 0) red[wave] = s;
@@ -162,8 +165,7 @@ __global__ __launch_bounds__(NT, 4) void topk_kernel(TopkArgs a) {
 #pragma unroll
   for (int w = 0; w < NW; ++w) s += red[w];
   if (tid == 0) {
-    // m / T + ln s with the rounded m log2 e / T that the exponentials used; where that overflows the values
-    // equal to the maximum are all the sum
+    // m / T + ln s, with the rounded m log2 e / T where the exponentials used that
     const double base = finite ? (double)c * 0.69314718055994531 : (double)m / (double)a.T;
     a.lse[row] = (float)(base + (double)logf(s));
   }

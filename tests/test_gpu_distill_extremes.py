@@ -90,3 +90,15 @@ def test_distill_rows_of_large_values(dtype, T, N):
         wr = np.zeros(N, np.float32)
         wr[list(rows)] = w[list(rows)]
         check(z, ids, t, None, lab, wr, T, a, OD.loss_and_grad(f64(z), ids, t, None, lab, wr, T, a), dtype)
+
+
+@pytest.mark.parametrize("V", [9000, 131073])
+@pytest.mark.parametrize("T", [0.5, 1.0, 2.0, 30000.0])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_topk_rows_of_large_values(dtype, T, V):
+    print(f"[topk large] {dtype} T={T} V={V}", flush=True)
+    z, k = large_rows(16, V, dtype), 30
+    ids, vals, lse = K().kron_topk_logits(z, k, temperature=T)
+    wi, wv, wl = OD.topk(f64(z), k, T)
+    assert np.array_equal(ids.cpu().numpy(), wi) and np.array_equal(f64(vals), wv)
+    assert np.all(np.abs(f64(lse) - wl) <= REL + 4 * 2.0 ** -24 * np.abs(wl)), (f64(lse), wl)
