@@ -451,6 +451,10 @@ typedef struct {
  *   - A row of weight 0 is left out whole (padding): nothing of it is read, its gradient is 0.
  *   - A negative id is an unused slot.  A row without a used slot has KD = 0.  A teacher value
  *     of -infinity has p = 0.  A token given twice counts with both p.  p_t is at least 0.
+ *   - Where the student's mass off the kept tokens is below about 2^-80 of the row's (they are
+ *     masked, or far below), a p_t within the rounding of teacher_lse, 2^-20 + 2^-23 |teacher_lse|,
+ *     counts as 0.  With a larger p_t and every logit off the kept tokens -infinity the loss is
+ *     infinite; those logits' gradient is 0.
  *   - An id >= V or a label outside [0, V) makes the loss and that row's gradient NaN (no
  *     out-of-bounds access).
  *   - Elements between V and the row stride are neither read nor written.

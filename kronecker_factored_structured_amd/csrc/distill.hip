@@ -24,6 +24,10 @@
 // and cancels in every softmax, as long as it is a moderate one (see Scale::at).  One exponential serves a row that needs one temperature (KD or CE alone, or T = 1);
 // at T = 2 the one of CE is the square of KD's; otherwise CE takes a second one (`two`).
 //
+// With a tail the gradient off the kept tokens needs q_v / q_t.  Where the kept tokens stand so far above
+// the rest that exponentials beside the row's maximum cannot hold it (cold_rest), the rest has a maximum of
+// its own: one more pass over the registers, and its sum and gradients beside that one.
+//
 // Measured: 8192 x 50257 bf16, k = 64, tail and labels: 389 us for 1.65 GB, 4.2 TB/s (a large copy reaches 4.9).
 // Two workgroups of 512 threads a CU hold 13 vectors each in registers; the passes over them (maximum, sums,
 // gradient) run while the other workgroup loads or stores.  Two calls over 2050 x 32003 fp32, k = 256: 207
@@ -41,7 +45,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr double kLn2 = 0.69314718055994531;
 
 // stats of a row (8 floats), from the forward for the backward
-enum { kStM = 0, kStInvT, kStInv1, kStBase, kStMass, kStTa, kStTb, kStN = kDistillStats };
+enum { kStM = 0, kStInvT, kStInv1, kStBase, kStMass, kStTa, kStTb, kStRest, kStN = kDistillStats };
 
 __device__ inline int64_t kept_id(const DistillArgs& a, int64_t row, int j) {
   const int64_t i = row * a.k + j;
@@ -103,7 +107,7 @@ struct Scale {
   }
   __device__ float changeA(const Scale& to) const { return change(to, sA, cA, to.cA); }
   __device__ float changeB(const Scale& to) const {
-    return two == 1 ? 2.f * changeA(to) : change(to, kLog2e, cB, to.cB);
+    return two == 0 ? changeA(to) : two == 1 ? 2.f * changeA(to) : change(to, kLog2e, cB, to.cB);
   }
   __device__ float first(float x) const { return __builtin_amdgcn_exp2f(fmaf(x, sA, -cA)); }
   __device__ float second(float x) const { return __builtin_amdgcn_exp2f(fmaf(x, kLog2e, -cB)); }
@@ -149,6 +153,29 @@ __device__ inline float vec_max(const u32x4& v) {
   return m;
 }
 
+// Whether the sum off the kept tokens, beside the whole maximum, is too small to be relied on: terms below
+// 2^-126 are lost, at most 2^18 of them, which is nothing beside 2^-80.
+__device__ inline bool cold_rest(const DistillArgs& a, const Scale& c, float sr) {
+  return c.kd && a.teacher_lse && sr < 0x1p-80f;
+}
+// The largest value of a vector off the kept tokens, and the sum of their first exponentials beside it.
+template <bool BF>
+__device__ inline float rest_max(const u32x4& v, uint32_t kept) {
+  float x[RowTile<BF>::VE], m = -INFINITY;
+  RowTile<BF>::values(v, x);
+#pragma unroll
+  for (int e = 0; e < RowTile<BF>::VE; ++e) m = (kept >> e) & 1u ? m : fmaxf(m, x[e]);
+  return m;
+}
+template <bool BF>
+__device__ inline float rest_sum(const Scale& c, const u32x4& v, uint32_t kept) {
+  float x[RowTile<BF>::VE], s = 0.f;
+  RowTile<BF>::values(v, x);
+#pragma unroll
+  for (int e = 0; e < RowTile<BF>::VE; ++e) s += (kept >> e) & 1u ? 0.f : c.first(c.place(x[e]));
+  return s;
+}
+
 // Shared memory of a workgroup of NT threads; thread j < k has the row's kept token j.
 template <int NT>
 struct Shared {
@@ -174,6 +201,37 @@ __device__ inline float block_max(float v, float* red) {
 #pragma unroll
   for (int w = 1; w < NT / 64; ++w) r = fmaxf(r, red[w]);
   return r;
+}
+
+// The rest's own maximum into cr (left as it is where the rest has no finite value) and its sum beside it into sr,
+// over the vectors [j0, j1) in registers.
+template <int NT, int NV, bool BF>
+__device__ inline void rest_alone(u32x4 (&reg)[NV], int j0, int j1, const uint32_t* bits, Scale& cr, float& sr, Shared<NT>& sh) {
+  constexpr int VE = RowTile<BF>::VE;
+  const int tid = threadIdx.x;
+  float m = -INFINITY;
+  fresh(reg);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int j = tid + i * NT;
+    if (j0 + j < j1) m = fmaxf(m, rest_max<BF>(reg[i], kept_bits<VE>(bits, j)));
+  }
+  m = block_max<NT>(m, sh.red);
+  sr = 0.f;
+  if (m == -INFINITY) return;
+  cr.at(m);
+  float s = 0.f;
+  fresh(reg);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int j = tid + i * NT;
+    if (j0 + j < j1) s += rest_sum<BF>(cr, reg[i], kept_bits<VE>(bits, j));
+  }
+  s = wave_sum(s);
+  if ((tid & 63) == 0) sh.redT[tid >> 6] = s;
+  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < NT / 64; ++v) sr += sh.redT[v];
 }
 
 // Clears the bitmap of the chunk [bit0, bit0 + 32 nwords) and marks the row's kept tokens in it
@@ -220,12 +278,12 @@ struct RowStats {
   float invsT, invs1, base, mass, ta, tb;
 };
 
-// The row's sums into its statistics.  tr, t1: the sums off the kept tokens and of the second
-// exponentials (without one: anything); k.own marks each token once over the whole row.  Thread 0 leaves
+// The row's sums into its statistics.  tr, t1: the sums off the kept tokens (beside the maximum of cr) and of the
+// second exponentials (without one: anything); k.own marks each token once over the whole row.  Thread 0 leaves
 // what the loss needs in a.rows[row].  zl: the label's logit (thread 0, if the label is one).
 template <int NT>
-__device__ inline RowStats finish_row(const DistillArgs& a, int64_t row, float w, const Scale& c, const Kept& k, float tr,
-                                      float t1, bool labok, float zl, Shared<NT>& sh) {
+__device__ inline RowStats finish_row(const DistillArgs& a, int64_t row, float w, const Scale& c, const Scale& cr, bool cold,
+                                      const Kept& k, float tr, float t1, bool labok, float zl, Shared<NT>& sh) {
   constexpr int NW = NT / 64;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   RowStats r;
@@ -241,7 +299,8 @@ __device__ inline RowStats finish_row(const DistillArgs& a, int64_t row, float w
   float tk = 0.f;
 #pragma unroll
   for (int v = 0; v < NW; ++v) tk += sh.reds[v];
-  const float total = tr + tk;
+  const float lift = cr.changeA(c);      // (0 but for a cold rest)
+  const float total = (cold ? tr * __builtin_amdgcn_exp2f(lift) : tr) + tk;
   if (c.two == 0) t1 = total;
   r.invsT = 1.f / total;
   r.invs1 = 1.f / t1;
@@ -282,9 +341,16 @@ __device__ inline RowStats finish_row(const DistillArgs& a, int64_t row, float w
       // (with every token kept there is no tail, whatever rounding leaves of its mass)
       const bool rest = psum < 1.0 && !(tr == 0.f && a.k >= a.V);
       ptail = rest ? 1.0 - psum : 0.0;
+      // Beside so small a q_t what the rounding of teacher_lse (half a step, and the error of a sum in 32 bits) leaves
+      // of p_t would be all of the loss, and infinite where the rest is masked: it is no mass.
+      if (cold && ptail <= 0x1p-20 + 0x1p-23 * fabs((double)r.ta)) ptail = 0.0;
       pmass = psum;
       r.mass = (float)(psum + ptail);
-      r.base = rest ? (float)((double)r.mass - ptail * ((double)total / (double)tr)) : r.mass;
+      r.base = r.mass;      // (a rest of -infinity throughout has gradient 0 whatever this is)
+      if (cold && tr > 0.f)
+        r.base = (float)((double)r.mass * exp64((double)lift * kLn2) - ptail * ((double)total / (double)tr));
+      else if (!cold && ptail > 0.0)
+        r.base = (float)((double)r.mass - ptail * ((double)total / (double)tr));
     }
   }
   const bool bad = sh.flag[1] || !labok;
@@ -298,32 +364,34 @@ __device__ inline RowStats finish_row(const DistillArgs& a, int64_t row, float w
     o.t1 = t1;
     // the label's z s - c of CE's exponential
     o.zl = !c.ce || !labok ? 0.f
-           : c.two == 0    ? fmaf(zl, c.sA, -c.cA)
-                           : fmaf(zl, c.two == 1 ? 2.f * c.sA : kLog2e, -c.cB);
+           : c.two == 0    ? fmaf(c.place(zl), c.sA, -c.cA)
+                           : fmaf(c.place(zl), c.two == 1 ? 2.f * c.sA : kLog2e, -c.cB);
     o.w = bad ? __builtin_nanf("") : w;
-    o.pad_ = 0.f;
+    o.lift = cold ? lift : 0.f;
     a.rows[row] = o;
   }
   if (bad) r.invsT = r.invs1 = __builtin_nanf("");
   return r;
 }
 
-// The gradient's factors of a row, `up` its weight times the upstream gradient.
+// The gradient's factors of a row, `up` its weight times the upstream gradient; kb and cb are those of the
+// exponentials off the kept tokens (beside cr's maximum).
 struct Grad {
-  float kw, cc, kc, kb, c1;
-  __device__ Grad(const DistillArgs& a, const Scale& c, const RowStats& r, float up) {
+  float kw, cc, kc, kb, c1, cb;
+  __device__ Grad(const DistillArgs& a, const Scale& c, const Scale& cr, const RowStats& r, float up) {
     kw = c.kd ? a.alpha * a.T * up : 0.f;
     cc = c.ce ? (1.f - a.alpha) * up : 0.f;
     kc = kw * r.invsT;
     kb = kc * r.base;
     c1 = cc * r.invs1;
+    cb = cr.m0 == c.m0 ? c1 : c1 * __builtin_amdgcn_exp2f(cr.changeB(c));
   }
-  // of a value: kq times the first exponential, and CE's part
-  __device__ float one(const Scale& c, float x, float kq) const {
+  // of a value: kq times the first exponential, and cq times CE's
+  __device__ float one(const Scale& c, float x, float kq, float cq) const {
     const float y = c.first(x);
-    if (c.two == 0) return y * (kq + c1);
-    if (c.two == 1) return y * fmaf(y, c1, kq);
-    return fmaf(y, kq, c.second(x) * c1);
+    if (c.two == 0) return y * (kq + cq);
+    if (c.two == 1) return y * fmaf(y, cq, kq);
+    return fmaf(y, kq, c.second(x) * cq);
   }
   template <bool BF>
   __device__ void vec(const Scale& c, const u32x4& v, float (&g)[RowTile<BF>::VE]) const {
@@ -336,16 +404,16 @@ struct Grad {
     }
     if (c.two == 0) {
 #pragma unroll
-      for (int e = 0; e < VE; ++e) g[e] = c.first(x[e]) * (kb + c1);
+      for (int e = 0; e < VE; ++e) g[e] = c.first(x[e]) * (kb + cb);
     } else if (c.two == 1) {
 #pragma unroll
       for (int e = 0; e < VE; ++e) {
         const float y = c.first(x[e]);
-        g[e] = y * fmaf(y, c1, kb);
+        g[e] = y * fmaf(y, cb, kb);
       }
     } else {
 #pragma unroll
-      for (int e = 0; e < VE; ++e) g[e] = fmaf(c.first(x[e]), kb, c.second(x[e]) * c1);
+      for (int e = 0; e < VE; ++e) g[e] = fmaf(c.first(x[e]), kb, c.second(x[e]) * cb);
     }
   }
 };
@@ -355,7 +423,7 @@ struct Grad {
 // the workgroup: the gradients wait for the gathered logits, and written to LDS they are there before
 // any thread passes the barrier.
 template <int NT, bool BF>
-__device__ inline void emit_kept(const DistillArgs& a, const Scale& c, const RowStats& r, const Grad& g, const Kept& k,
+__device__ inline void emit_kept(const DistillArgs& a, const Scale& c, const Scale& cr, const RowStats& r, const Grad& g, const Kept& k,
                                  int64_t lab, bool putlab, float zl, int bit0, const RowTile<BF>& z, const RowTile<BF>& o,
                                  uint32_t* bits, Shared<NT>& sh) {
   const int tid = threadIdx.x;
@@ -367,10 +435,10 @@ __device__ inline void emit_kept(const DistillArgs& a, const Scale& c, const Row
     float p = sh.kp[tid];
     if (sh.flag[0])      // (the owner is the first slot)
       for (int l = tid + 1; l < a.k; ++l) p += sh.kid[l] == (int32_t)k.id ? sh.kp[l] : 0.f;
-    gk = g.one(c, k.z, g.kc * r.mass) - g.kw * p - (k.id == lab ? g.cc : 0.f);
+    gk = g.one(c, k.z, g.kc * r.mass, g.c1) - g.kw * p - (k.id == lab ? g.cc : 0.f);
   }
   if (putlab) {
-    gl = g.one(c, zl, g.kb) - g.cc;
+    gl = g.one(cr, cr.place(zl), g.kb, g.cb) - g.cc;
     const int at = (int)lab + z.off - bit0;
     atomicOr(&bits[at >> 5], 1u << (at & 31));
   }
@@ -435,7 +503,7 @@ __global__ __launch_bounds__(NT, 4) void distill_row_kernel(DistillArgs a) {
   const bool labok = !c.ce || (lab >= 0 && lab < a.V);
   Kept k = mark_kept<NT, BF>(a, row, z, lab, bits, 0, (a.V + z.off + 31) / 32, sh);
   if (k.have) k.z = z.at((int)k.id);
-  float zl = c.ce && labok && tid == 0 ? z.at((int)lab) : 0.f;
+  const float zl = c.ce && labok && tid == 0 ? z.at((int)lab) : 0.f;
 
   float mx = -INFINITY;
 #pragma unroll
@@ -443,7 +511,6 @@ __global__ __launch_bounds__(NT, 4) void distill_row_kernel(DistillArgs a) {
   c.at(block_max<NT>(mx, sh.red));      // (its barrier also completes the bitmap)
   settle(k, sh);
   k.z = c.place(k.z);
-  zl = c.place(zl);
 
   Sums<BF> s;
   fresh(reg);
@@ -459,10 +526,13 @@ __global__ __launch_bounds__(NT, 4) void distill_row_kernel(DistillArgs a) {
   float tr = 0.f, t1 = 0.f;
 #pragma unroll
   for (int v = 0; v < NW; ++v) { tr += sh.redT[v]; t1 += sh.red1[v]; }
-  const RowStats r = finish_row<NT>(a, row, w, c, k, tr, t1, labok, zl, sh);
+  Scale cr = c;
+  const bool cold = cold_rest(a, c, tr);
+  if (cold) rest_alone<NT, NV, BF>(reg, 0, nvec, bits, cr, tr, sh);
+  const RowStats r = finish_row<NT>(a, row, w, c, cr, cold, k, tr, t1, labok, zl, sh);
 
-  const Grad g(a, c, r, w);
-  emit_kept<NT, BF>(a, c, r, g, k, lab, c.ce && labok && tid == 0 && !sh.flag[3], zl, 0, z, o, bits, sh);
+  const Grad g(a, c, cr, r, w);
+  emit_kept<NT, BF>(a, c, cr, r, g, k, lab, c.ce && labok && tid == 0 && !sh.flag[3], zl, 0, z, o, bits, sh);
   // vectors without a kept token and inside the row go out whole; the others (a few) are read again, and
   // go out element by element.  (In place those are still as they were, but for the kept tokens.)
   const bool same = z.off == o.off;
@@ -474,7 +544,7 @@ __global__ __launch_bounds__(NT, 4) void distill_row_kernel(DistillArgs a) {
     if (j < nvec) {
       if (same && kept_bits<VE>(bits, j) == 0u && z.inside(j)) {
         float x[VE];
-        g.vec<BF>(c, reg[i], x);
+        g.vec<BF>(cr, reg[i], x);
         o.store(j, Tile::packed(x));
       } else {
         left |= 1u << i;
@@ -483,7 +553,7 @@ __global__ __launch_bounds__(NT, 4) void distill_row_kernel(DistillArgs a) {
   }
   while (left) {
     const int j = tid + (__ffs(left) - 1) * NT;
-    emit_slow<BF>(c, g, j, kept_bits<VE>(bits, j), z, o);
+    emit_slow<BF>(cr, g, j, kept_bits<VE>(bits, j), z, o);
     left &= left - 1;
   }
 }
@@ -494,7 +564,8 @@ __global__ __launch_bounds__(NT, 4) void distill_row_kernel(DistillArgs a) {
 constexpr int kCT = 256;      // threads
 constexpr int kCV = 8;        // vectors of a thread at most
 struct PartSum {
-  float m, sr, s1, pad_;
+  float m, sr, s1;      // the maximum, and the sums beside it (sr beside mr)
+  float mr;             // the maximum off the kept tokens where it is far below, else m
 };
 
 template <bool BF>
@@ -547,38 +618,54 @@ __global__ __launch_bounds__(kCT) void distill_part_kernel(DistillArgs a) {
   s.s1 = wave_sum(s.s1);
   if ((tid & 63) == 0) { sh.red1[tid >> 6] = s.s1; sh.redT[tid >> 6] = s.sr; }
   __syncthreads();
-  if (tid == 0) {
-    PartSum p{m, 0.f, 0.f, 0.f};
+  PartSum p{m, 0.f, 0.f, m};
 #pragma unroll
-    for (int v = 0; v < kCT / 64; ++v) { p.sr += sh.redT[v]; p.s1 += sh.red1[v]; }
-    reinterpret_cast<PartSum*>(a.part)[row * a.chunks + chunk] = p;
+  for (int v = 0; v < kCT / 64; ++v) { p.sr += sh.redT[v]; p.s1 += sh.red1[v]; }
+  if (m > -INFINITY && cold_rest(a, c, p.sr)) {
+    rest_alone<kCT, kCV, BF>(reg, j0, j1, bits, c, p.sr, sh);
+    p.mr = p.sr > 0.f ? c.m0 : -INFINITY;
   }
+  if (tid == 0) reinterpret_cast<PartSum*>(a.part)[row * a.chunks + chunk] = p;
 }
 
-// A row's chunks joined: the maximum into c, the sums rescaled to it.  One thread a chunk.
+// A row's chunks joined: the maximum into c, the sums rescaled to it; a cold rest's maximum into cr, and tr beside
+// that.  One thread a chunk.
 static_assert((kVocabMax / 4 + 2 + 2 * kCT - 1) / (2 * kCT) <= kCT, "a row's chunks fit one to a thread");
-__device__ inline void join_row(const DistillArgs& a, int64_t row, Scale& c, float& tr, float& t1, Shared<kCT>& sh) {
+// A thread's sum at the maximum m, rescaled by `change` (log2) to another one; a NaN stays.
+__device__ inline float rescaled(float sum, float m, float to, float change) {
+  const float f = m == to ? 1.f : m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(change);
+  return f > 0.f || sum != sum ? sum * f : 0.f;
+}
+__device__ inline void join_row(const DistillArgs& a, int64_t row, Scale& c, Scale& cr, bool& cold, float& tr, float& t1,
+                                Shared<kCT>& sh) {
   const int tid = threadIdx.x;
-  PartSum p{-INFINITY, 0.f, 0.f, 0.f};
+  PartSum p{-INFINITY, 0.f, 0.f, -INFINITY};
   if (tid < a.chunks) p = reinterpret_cast<const PartSum*>(a.part)[row * a.chunks + tid];
   c.at(block_max<kCT>(p.m, sh.red));
-  float fA = 1.f, fB = 1.f;
-  if (p.m != c.m0) {      // the chunk's own shifts against the row's
-    Scale d = c;
-    d.at(p.m);
-    const bool none = p.m == -INFINITY;
-    fA = none ? 0.f : __builtin_amdgcn_exp2f(d.changeA(c));
-    fB = none ? 0.f : __builtin_amdgcn_exp2f(d.changeB(c));
-  }
+  cr = c;
+  Scale d = c, dr = c;      // the chunk's own shifts
+  d.at(p.m);
+  dr.at(p.mr);
   // (a row of -infinity throughout has no distribution: NaN)
   const float bad = c.m0 == -INFINITY ? __builtin_nanf("") : 0.f;
-  const float x = wave_sum(fA > 0.f || p.sr != p.sr ? p.sr * fA + bad : bad);
-  const float y = wave_sum(fB > 0.f || p.s1 != p.s1 ? p.s1 * fB + bad : bad);
+  const float x = wave_sum(rescaled(p.sr, p.mr, c.m0, dr.changeA(c)) + bad);
+  const float y = wave_sum(rescaled(p.s1, p.m, c.m0, d.changeB(c)) + bad);
   if ((tid & 63) == 0) { sh.redT[tid >> 6] = x; sh.red1[tid >> 6] = y; }
   __syncthreads();
   tr = t1 = 0.f;
 #pragma unroll
   for (int v = 0; v < kCT / 64; ++v) { tr += sh.redT[v]; t1 += sh.red1[v]; }
+  cold = cold_rest(a, c, tr);
+  if (!cold) return;
+  tr = 0.f;
+  const float m = block_max<kCT>(p.sr > 0.f ? p.mr : -INFINITY, sh.red);
+  if (m == -INFINITY) return;
+  cr.at(m);
+  const float u = wave_sum(p.sr > 0.f ? rescaled(p.sr, p.mr, m, dr.changeA(cr)) : 0.f);
+  if ((tid & 63) == 0) sh.redT[tid >> 6] = u;
+  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < kCT / 64; ++v) tr += sh.redT[v];
 }
 
 // STATS: joins the row's chunks and keeps the statistics (one workgroup a row, nothing emitted).
@@ -610,7 +697,7 @@ __global__ __launch_bounds__(kCT) void distill_emit_kernel(DistillArgs a) {
       reg[STATS ? 0 : i] = j < j1 ? z.whole(j) : Tile::empty();
     }
   }
-  Scale c(a);
+  Scale c(a), cr(a);
   const int64_t lab = c.ce ? a.labels[row] : -1;
   const bool labok = !c.ce || (lab >= 0 && lab < a.V);
   const int bit0 = j0 * VE;
@@ -635,34 +722,35 @@ __global__ __launch_bounds__(kCT) void distill_emit_kernel(DistillArgs a) {
           break;
         }
     }
-    join_row(a, row, c, tr, t1, sh);      // (its barriers also complete the slots)
+    bool cold;
+    join_row(a, row, c, cr, cold, tr, t1, sh);      // (its barriers also complete the slots)
     if (k.have && sh.flag[0]) {
       k.own = true;
       for (int l = 0; l < tid; ++l) k.own = k.own && sh.kid[l] != (int32_t)k.id;
     }
     k.z = c.place(k.z);
-    zl = c.place(zl);
-    r = finish_row<kCT>(a, row, w, c, k, tr, t1, labok, zl, sh);
+    r = finish_row<kCT>(a, row, w, c, cr, cold, k, tr, t1, labok, zl, sh);
     if (STATS) {
       if (tid == 0) {
         float* st = a.stats + row * kStN;
         st[kStM] = c.m0; st[kStInvT] = r.invsT; st[kStInv1] = r.invs1;
-        st[kStBase] = r.base; st[kStMass] = r.mass; st[kStTa] = r.ta; st[kStTb] = r.tb; st[kStN - 1] = 0.f;
+        st[kStBase] = r.base; st[kStMass] = r.mass; st[kStTa] = r.ta; st[kStTb] = r.tb; st[kStRest] = cr.m0;
       }
       return;
     }
   } else {
     const float* st = a.stats + row * kStN;
     c.at(st[kStM]);
+    cr.at(st[kStRest]);
     r.invsT = st[kStInvT]; r.invs1 = st[kStInv1]; r.base = st[kStBase];
     r.mass = st[kStMass]; r.ta = st[kStTa]; r.tb = st[kStTb];
     if (k.near) k.z = c.place(z.at((int)k.id));
-    if (lnear && tid == 0) zl = c.place(z.at((int)lab));
+    if (lnear && tid == 0) zl = z.at((int)lab);
     __syncthreads();
     settle(k, sh);
   }
-  const Grad g(a, c, r, a.gout ? w * a.gout[0] : w);
-  emit_kept<kCT, BF>(a, c, r, g, k, lab, lnear && tid == 0 && !sh.flag[3], zl, bit0, z, o, bits, sh);
+  const Grad g(a, c, cr, r, a.gout ? w * a.gout[0] : w);
+  emit_kept<kCT, BF>(a, c, cr, r, g, k, lab, lnear && tid == 0 && !sh.flag[3], zl, bit0, z, o, bits, sh);
   const bool same = z.off == o.off;
   uint32_t left = 0u;
 #pragma unroll
@@ -671,7 +759,7 @@ __global__ __launch_bounds__(kCT) void distill_emit_kernel(DistillArgs a) {
     if (j < j1) {
       if (same && kept_bits<VE>(bits, j - j0) == 0u && z.inside(j)) {
         float x[VE];
-        g.vec<BF>(c, reg[STATS ? 0 : i], x);
+        g.vec<BF>(cr, reg[STATS ? 0 : i], x);
         o.store(j, Tile::packed(x));
       } else {
         left |= 1u << i;
@@ -680,7 +768,7 @@ __global__ __launch_bounds__(kCT) void distill_emit_kernel(DistillArgs a) {
   }
   while (left) {
     const int j = j0 + tid + (__ffs(left) - 1) * kCT;
-    emit_slow<BF>(c, g, j, kept_bits<VE>(bits, j - j0), z, o);
+    emit_slow<BF>(cr, g, j, kept_bits<VE>(bits, j - j0), z, o);
     left &= left - 1;
   }
 }
@@ -700,7 +788,7 @@ __global__ __launch_bounds__(1024) void distill_loss_kernel(DistillArgs a) {
       if (!a.teacher_lse)
         kl = r.psum > 0.0 ? kl / r.psum - log(r.psum) : 0.0;
       else if (r.pt > 0.0)
-        kl += r.pt * (log(r.pt) - log((double)r.rest / (double)r.total));
+        kl += r.pt * (log(r.pt) - log((double)r.rest / (double)r.total) - (double)r.lift * kLn2);
       l += (double)a.alpha * (double)a.T * (double)a.T * kl;
     }
     if (a.alpha < 1.f) l += (1.0 - (double)a.alpha) * (log((double)r.t1) - (double)r.zl * kLn2);

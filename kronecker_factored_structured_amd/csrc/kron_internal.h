@@ -295,7 +295,7 @@ constexpr int kDistillStats = 8;   // floats of a row's stats
 // A row's part of the loss, before the logarithms (see distill_loss_kernel).
 struct DistillRow {
   double kl, psum, pt;
-  float total, rest, t1, zl, w, pad_;
+  float total, rest, t1, zl, w, lift;
 };
 // Workgroups of a launch (of at most 1024 threads: a grid has less than 2^32 of them); more rows take several.
 constexpr int64_t kMaxGroups = int64_t(1) << 21;

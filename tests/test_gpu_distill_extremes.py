@@ -102,3 +102,73 @@ def test_topk_rows_of_large_values(dtype, T, V):
     wi, wv, wl = OD.topk(f64(z), k, T)
     assert np.array_equal(ids.cpu().numpy(), wi) and np.array_equal(f64(vals), wv)
     assert np.all(np.abs(f64(lse) - wl) <= REL + 4 * 2.0 ** -24 * np.abs(wl)), (f64(lse), wl)
+
+
+@pytest.mark.parametrize("N,V", [(3, 9001), (600, 9001), (2, 140001)])
+@pytest.mark.parametrize("T,alpha,gap", [(1.0, 1.0, 150.0), (1.0, 0.5, 150.0), (2.0, 0.5, 290.0), (1.5, 0.5, 200.0), (0.5, 0.7, 75.0)])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_distill_kept_tokens_far_above_the_rest(dtype, T, alpha, gap, N, V):
+    """The student's mass off the kept tokens is e^-gap/T of the row: no exponential beside the row's maximum holds
+    it, but its logarithm and its tokens' shares of it are ordinary numbers."""
+    k = 24
+    print(f"[distill gap] {dtype} T={T} alpha={alpha} gap={gap} N={N} V={V}", flush=True)
+    g = np.random.default_rng(2)
+    z = torch.randn(N, V, generator=torch.Generator().manual_seed(5)) * 2
+    ids = np.stack([g.permutation(V)[:k] for _ in range(N)])
+    t = (g.standard_normal((N, k)) * 2 + 6).astype(np.float32)
+    lse = (np.log(np.exp(t.astype(np.float64) / T).sum(1)) + g.uniform(0.01, 0.3, N)).astype(np.float32)
+    lab = g.integers(0, V, N)
+    lab[1] = ids[1, 3]
+    z.scatter_(1, torch.from_numpy(ids), torch.gather(z, 1, torch.from_numpy(ids)) + gap)
+    if N > 2:      # only one kept token stands out, and one of the others does as well
+        z[2, torch.from_numpy(ids[2, 1:])] -= gap
+        z[2, (ids[2, 0] + 1) % V] += 30
+    z = z.to(dtype).cuda()
+    w = np.zeros(N, np.float32)
+    w[:3] = g.uniform(0.2, 1.0, min(N, 3))
+    check(z, ids, t, lse, lab, w, T, alpha, OD.loss_and_grad(f64(z), ids, t, lse, lab, w, T, alpha), dtype)
+
+
+@pytest.mark.parametrize("mask", ["infinity", "lowest", "large"])
+@pytest.mark.parametrize("N,V", [(40, 9001), (600, 9001), (4, 140001)])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_distill_teacher_and_student_masked_alike(dtype, N, V, mask):
+    """Both models allow the same u < k tokens of a row: there is no tail, and what the rounded lse leaves of one is
+    no mass.  The loss is the one over the kept tokens, with the teacher's sum off one by the rounding of lse."""
+    k, u, T, alpha = 32, 20, 2.0, 0.5
+    fill = dict(infinity=-float("inf"), lowest=torch.finfo(dtype).min, large=-1e30)[mask]
+    print(f"[distill masked] {dtype} N={N} V={V} {mask}", flush=True)
+    g = np.random.default_rng(7)
+    gen = torch.Generator().manual_seed(5)
+    zt, z = torch.full((N, V), fill), torch.full((N, V), fill)
+    live = torch.from_numpy(np.stack([g.permutation(V)[:u] for _ in range(N)]))
+    zt.scatter_(1, live, torch.randn(N, u, generator=gen) * 2 + 4)
+    z.scatter_(1, live, torch.randn(N, u, generator=gen) * 2)
+    zt, z = zt.to(dtype).cuda(), z.to(dtype).cuda()
+    ids, vals, lse = K().kron_topk_logits(zt, k, temperature=T)
+    ids, t, lse = ids.cpu().numpy(), vals.cpu().numpy(), lse.cpu().numpy()
+    lab = live[:, 0].numpy()
+    w = np.zeros(N, np.float32)
+    w[:40] = g.uniform(0.2, 1.0, min(N, 40))
+    want = OD.loss_and_grad(f64(z), ids[:, :u], t[:, :u], None, lab, w, T, alpha)
+    # p is off by the rounding of lse and of its sum, below 2^-20 in all
+    check(z, ids, t, lse, lab, w, T, alpha, want, dtype, extra=2.0 ** -20)
+
+
+def test_distill_a_tail_that_the_student_cannot_have():
+    """Every logit off the kept tokens is -infinity and the teacher's tail is not small: the loss is infinite, and the
+    gradient a number."""
+    N, V, k = 3, 500, 8
+    z = torch.full((N, V), -float("inf"), device="cuda")
+    z[:, :k] = torch.randn(N, k, generator=torch.Generator().manual_seed(1)).cuda()
+    z[2] = torch.randn(V, generator=torch.Generator().manual_seed(2)).cuda()
+    ids = torch.arange(k, device="cuda", dtype=torch.int32).repeat(N, 1)
+    t = torch.zeros(N, k, device="cuda")
+    lse = torch.full((N,), float(np.log(k)) + 0.1, device="cuda")
+    a = K().kron_distill(z, ids, t, teacher_lse=lse)
+    assert a["loss"].item() == float("inf")
+    # M q - p on the kept tokens with M = 1, nothing elsewhere
+    p = np.exp(-f64(lse)[:2, None]) * np.ones(k)
+    q = torch.softmax(z[:2, :k].double(), 1).cpu().numpy()
+    assert np.abs(f64(a["dlogits"])[:2, :k] - (q - p) / N).max() <= REL * 2 / N
+    assert not a["dlogits"][:2, k:].any() and bool(torch.isfinite(a["dlogits"]).all())
