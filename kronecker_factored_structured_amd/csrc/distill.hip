@@ -427,7 +427,8 @@ __device__ inline void emit_kept(const DistillArgs& a, const Scale& c, const Sca
                                  int64_t lab, bool putlab, float zl, int bit0, const RowTile<BF>& z, const RowTile<BF>& o,
                                  uint32_t* bits, Shared<NT>& sh) {
   const int tid = threadIdx.x;
-  if (tid < a.k) sh.kp[tid] = k.have ? __builtin_amdgcn_exp2f((k.t * c.invT - r.ta) * kLog2e) * r.tb : 0.f;
+  // (a teacher of -infinity has p = 0, also beside a teacher_lse of -infinity)
+  if (tid < a.k) sh.kp[tid] = k.have && k.t != -INFINITY ? __builtin_amdgcn_exp2f((k.t * c.invT - r.ta) * kLog2e) * r.tb : 0.f;
   __syncthreads();
   const bool mine = k.own && k.near;
   float gk = 0.f, gl = 0.f;

@@ -172,3 +172,18 @@ def test_distill_a_tail_that_the_student_cannot_have():
     q = torch.softmax(z[:2, :k].double(), 1).cpu().numpy()
     assert np.abs(f64(a["dlogits"])[:2, :k] - (q - p) / N).max() <= REL * 2 / N
     assert not a["dlogits"][:2, k:].any() and bool(torch.isfinite(a["dlogits"]).all())
+
+
+@pytest.mark.parametrize("N", [2, 600])
+def test_distill_a_teacher_without_any_value(N):
+    """A row of -infinity as kron_topk_logits keeps it: values and lse are -infinity, every p is 0 and the rest of the
+    vocabulary has all the mass, whatever lse is."""
+    V, k, T = 3000, 6, 1.5
+    z = torch.randn(N, V, generator=torch.Generator().manual_seed(4)).cuda()
+    ids, vals, lse = K().kron_topk_logits(torch.full((N, V), -float("inf"), device="cuda"), k, temperature=T)
+    assert bool((lse == -float("inf")).all())
+    ids, t = ids.cpu().numpy(), vals.cpu().numpy()
+    w = np.zeros(N, np.float32)
+    w[:2] = 0.5
+    want = OD.loss_and_grad(f64(z), ids, t, np.zeros(N, np.float32), None, w, T, 1.0)
+    check(z, ids, t, lse.cpu().numpy(), None, w, T, 1.0, want, F32)
