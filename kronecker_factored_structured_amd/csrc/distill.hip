@@ -273,6 +273,15 @@ __device__ inline void settle(Kept& k, const Shared<NT>& sh) {
   for (int l = 0; l < (int)threadIdx.x; ++l) k.own = k.own && sh.kid[l] != (int32_t)k.id;
 }
 
+// log p of a kept token and p, short of tb: `ta` is teacher_lse with a tail, else the teacher's largest value.  In 64
+// bits, because t / T may be thousands.  (A teacher of -infinity has p = 0, also beside a teacher_lse of -infinity.)
+__device__ inline double kept_p(const DistillArgs& a, const Kept& k, float ta, double& logp) {
+  logp = 0.0;
+  if (!k.have || k.t == -INFINITY) return 0.0;
+  logp = a.teacher_lse ? (double)k.t / (double)a.T - (double)ta : ((double)k.t - (double)ta) / (double)a.T;
+  return exp64(logp);
+}
+
 // What the gradient needs of a row.
 struct RowStats {
   float invsT, invs1, base, mass, ta, tb;
@@ -315,14 +324,12 @@ __device__ inline RowStats finish_row(const DistillArgs& a, int64_t row, float w
       tm = sh.redk[0];
 #pragma unroll
       for (int v = 1; v < NW; ++v) tm = fmaxf(tm, sh.redk[v]);
-      r.ta = sh.flag[2] ? tm * c.invT : 0.f;
+      r.ta = sh.flag[2] ? tm : 0.f;
     }
     // the masses of the teacher are sums next to one: 64 bits, one exponential a thread
-    double pj = 0.0, logp = 0.0;
-    if (k.have && !(k.t == -INFINITY)) {
-      logp = tail ? (double)k.t / (double)a.T - (double)r.ta : ((double)k.t - (double)tm) / (double)a.T;
-      pj = exp64(logp);
-    }
+    double logp;
+    const double pj = kept_p(a, k, r.ta, logp);
+    if (threadIdx.x < a.k) sh.kp[threadIdx.x] = (float)pj;
     // sum p and sum p (log p - log q), log q short of the sum's logarithm
     const double lq = ((double)k.z * (double)c.sA - (double)c.cA) * kLn2;
     double term = pj != 0.0 ? pj * (logp - lq) : 0.0;
@@ -427,16 +434,14 @@ __device__ inline void emit_kept(const DistillArgs& a, const Scale& c, const Sca
                                  int64_t lab, bool putlab, float zl, int bit0, const RowTile<BF>& z, const RowTile<BF>& o,
                                  uint32_t* bits, Shared<NT>& sh) {
   const int tid = threadIdx.x;
-  // (a teacher of -infinity has p = 0, also beside a teacher_lse of -infinity)
-  if (tid < a.k) sh.kp[tid] = k.have && k.t != -INFINITY ? __builtin_amdgcn_exp2f((k.t * c.invT - r.ta) * kLog2e) * r.tb : 0.f;
   __syncthreads();
   const bool mine = k.own && k.near;
   float gk = 0.f, gl = 0.f;
   if (mine) {
-    float p = sh.kp[tid];
+    float p = sh.kp[tid];      // (times tb)
     if (sh.flag[0])      // (the owner is the first slot)
       for (int l = tid + 1; l < a.k; ++l) p += sh.kid[l] == (int32_t)k.id ? sh.kp[l] : 0.f;
-    gk = g.one(c, k.z, g.kc * r.mass, g.c1) - g.kw * p - (k.id == lab ? g.cc : 0.f);
+    gk = g.one(c, k.z, g.kc * r.mass, g.c1) - g.kw * (p * r.tb) - (k.id == lab ? g.cc : 0.f);
   }
   if (putlab) {
     gl = g.one(cr, cr.place(zl), g.kb, g.cb) - g.cc;
@@ -745,6 +750,8 @@ __global__ __launch_bounds__(kCT) void distill_emit_kernel(DistillArgs a) {
     cr.at(st[kStRest]);
     r.invsT = st[kStInvT]; r.invs1 = st[kStInv1]; r.base = st[kStBase];
     r.mass = st[kStMass]; r.ta = st[kStTa]; r.tb = st[kStTb];
+    double logp;
+    if (tid < a.k) sh.kp[tid] = (float)kept_p(a, k, r.ta, logp);
     if (k.near) k.z = c.place(z.at((int)k.id));
     if (lnear && tid == 0) zl = z.at((int)lab);
     __syncthreads();

@@ -187,3 +187,25 @@ def test_distill_a_teacher_without_any_value(N):
     w[:2] = 0.5
     want = OD.loss_and_grad(f64(z), ids, t, np.zeros(N, np.float32), None, w, T, 1.0)
     check(z, ids, t, lse.cpu().numpy(), None, w, T, 1.0, want, F32)
+
+
+@pytest.mark.parametrize("N", [4, 600])
+@pytest.mark.parametrize("tail", [False, True])
+@pytest.mark.parametrize("T", [0.003, 0.02])
+def test_distill_small_temperatures(T, tail, N):
+    """The teacher's values over T are thousands: p = exp of their differences, not of a rounded quotient's.  (The
+    calls take T as a 32-bit float; the oracle gets that number.)"""
+    T = float(np.float32(T))
+    V, k = 4000, 12
+    g = np.random.default_rng(9)
+    z = torch.randn(N, V, generator=torch.Generator().manual_seed(5)) * T
+    ids = np.stack([g.permutation(V)[:k] for _ in range(N)])
+    t = (g.standard_normal((N, k)) * T + 20).astype(np.float32)
+    lse = None
+    if tail:      # (the rounding of an lse of thousands is an input like any other)
+        m = t.astype(np.float64).max(1)
+        lse = (m / T + np.log(np.exp((t.astype(np.float64) - m[:, None]) / T).sum(1)) + g.uniform(0.1, 0.3, N)).astype(np.float32)
+    w = np.zeros(N, np.float32)
+    w[:4] = g.uniform(0.2, 1.0, 4)
+    z = z.cuda()
+    check(z, ids, t, lse, None, w, T, 1.0, OD.loss_and_grad(f64(z), ids, t, lse, None, w, T, 1.0), F32)
