@@ -415,7 +415,8 @@ kron_status_t kron_glu_bwd(const kron_shape_t* shape, int32_t act, int32_t dtype
  *   lse    [N]     fp32
  * -0 counts as 0, a NaN stands above every number (lse is NaN then), and a row of -infinity
  * has lse -infinity.  logits needs only its element's alignment; the outputs 16 bytes.
- * Limits: 1 <= k <= KRON_DISTILL_MAX_K and k <= V, V <= KRON_VOCAB_MAX, temperature > 0.
+ * Limits: 1 <= k <= KRON_DISTILL_MAX_K and k <= V, V <= KRON_VOCAB_MAX, temperature > 0 (and log2(e)
+ * over it finite: above 4.3e-39).
  */
 #define KRON_DISTILL_MAX_K 256
 #define KRON_VOCAB_MAX 262144
@@ -428,7 +429,7 @@ typedef struct {
   int64_t ld, ldd;           /* row strides of logits and dlogits, in elements, >= V           */
   int32_t dtype;             /* of logits and dlogits: KRON_F32 or KRON_BF16                   */
   uint32_t flags;            /* KRON_IDS_I64                                                   */
-  float temperature, alpha;  /* T > 0;  0 <= alpha <= 1                                        */
+  float temperature, alpha;  /* T > 0 (log2(e) / T finite);  0 <= alpha <= 1                  */
 } kron_distill_t;
 #define KRON_IDS_I64 1u      /* ids are int64 (else int32) */
 #define KRON_DISTILL_STATS 8 /* floats of stats for each row */

@@ -857,6 +857,13 @@ size_t glu_workspace(const kron::GluArgs& a, bool backward) {
   return (kron::glu_workspace_bytes(a, backward) + 255) & ~size_t(255);
 }
 
+// The kernels scale logits by log2(e) / temperature, which has to be a number.
+kron_status_t check_temperature(float T) {
+  if (!(T > 0.f) || !std::isfinite(T) || !std::isfinite(1.4426950408889634f / T))
+    return fail(KRON_E_ARG, "temperature = %g must be positive and finite, and so must log2(e) over it", (double)T);
+  return KRON_OK;
+}
+
 kron_status_t glu_workspace_check(const void* workspace, size_t bytes, size_t need) {
   if (!workspace || bytes < need) return fail(KRON_E_WORKSPACE, "workspace of %zu bytes given, %zu needed", bytes, need);
   if (((uintptr_t)workspace & 255u) != 0) return fail(KRON_E_ALIGN, "workspace is not 256-byte aligned");
@@ -927,6 +934,7 @@ kron_status_t kron_glu_bwd(const kron_shape_t* s, int32_t act, int32_t dtype, co
 
 kron_status_t kron_topk_logits(int64_t N, int32_t V, int64_t ld, int32_t k, int32_t dtype, float temperature,
                                const void* logits, int32_t* ids, float* vals, float* lse, hipStream_t stream) {
+  kron_status_t st;
   if (N < 0 || N > kMaxRows) return fail(KRON_E_SHAPE, "N = %lld out of range", (long long)N);
   if (V < 1 || k < 1 || k > V) return fail(KRON_E_SHAPE, "V = %d and k = %d: 1 <= k <= V is needed", V, k);
   if (ld < V || ld > kMaxStride) return fail(KRON_E_SHAPE, "ld = %lld outside V = %d .. 2^40", (long long)ld, V);
@@ -934,15 +942,13 @@ kron_status_t kron_topk_logits(int64_t N, int32_t V, int64_t ld, int32_t k, int3
     return fail(KRON_E_UNSUPPORTED, "V = %d, k = %d beyond the limits (V <= %d, k <= %d)", V, k, KRON_VOCAB_MAX,
                 KRON_DISTILL_MAX_K);
   if (dtype != KRON_F32 && dtype != KRON_BF16) return fail(KRON_E_DTYPE, "dtype %d", dtype);
-  if (!(temperature > 0.f) || !std::isfinite(temperature))
-    return fail(KRON_E_ARG, "temperature = %g must be positive and finite", (double)temperature);
+  if ((st = check_temperature(temperature)) != KRON_OK) return st;
   if (N == 0) return ok();
   if (!logits || !ids || !vals || !lse) return fail(KRON_E_NULL, "logits, ids, vals and lse are required");
   const size_t es = dtype == KRON_F32 ? 4 : 2;
   if (((uintptr_t)logits & (es - 1)) != 0) return fail(KRON_E_ALIGN, "logits is not aligned to its elements");
   const Range ins[1] = {{logits, strided_bytes(N, ld, V, es), "logits"}};
   const Range outs[3] = {{ids, (size_t)N * k * 4, "ids"}, {vals, (size_t)N * k * 4, "vals"}, {lse, (size_t)N * 4, "lse"}};
-  kron_status_t st;
   if ((st = check_align(outs, 3)) != KRON_OK || (st = check_alias(outs, 3, ins, 1)) != KRON_OK) return st;
   kron::TopkArgs a{N, ld, V, k, dtype == KRON_BF16, temperature, logits, ids, vals, lse};
   const hipError_t e = kron::launch_topk(a, stream);
@@ -961,8 +967,8 @@ kron_status_t distill_check(const kron_distill_t* d) {
                 KRON_DISTILL_MAX_K);
   if (d->dtype != KRON_F32 && d->dtype != KRON_BF16) return fail(KRON_E_DTYPE, "dtype %d", d->dtype);
   if (d->flags & ~KRON_IDS_I64) return fail(KRON_E_ARG, "unknown flag bits 0x%x", d->flags);
-  if (!(d->temperature > 0.f) || !std::isfinite(d->temperature))
-    return fail(KRON_E_ARG, "temperature = %g must be positive and finite", (double)d->temperature);
+  const kron_status_t st = check_temperature(d->temperature);
+  if (st != KRON_OK) return st;
   if (!(d->alpha >= 0.f && d->alpha <= 1.f)) return fail(KRON_E_ARG, "alpha = %g outside [0, 1]", (double)d->alpha);
   if (d->alpha > 0.f && d->k < 1) return fail(KRON_E_SHAPE, "k = %d must be >= 1 when alpha > 0", d->k);
   if (d->ld < d->V || d->ld > kMaxStride)

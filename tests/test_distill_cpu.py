@@ -170,3 +170,11 @@ def test_binding_refuses():
         K.kron_topk_logits(z.double(), 2)
     with pytest.raises(ValueError, match="GPU tensor"):
         K.kron_distill(z, torch.zeros(3, 2, dtype=torch.int32), torch.zeros(3, 2))
+
+
+def test_temperature_whose_reciprocal_overflows():
+    """The kernels scale by log2(e) / T: below 4.3e-39 that is infinite, and 0 times it NaN."""
+    for T in (1e-45, 1e-39, 4.2e-39):
+        assert topk(T=T) == _lib.KRON_E_ARG
+        for mode in (0, 1, 2):
+            assert distill(mode, temperature=T) == _lib.KRON_E_ARG
