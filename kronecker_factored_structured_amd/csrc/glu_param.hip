@@ -18,11 +18,16 @@
 // instances by the sides' tiles took it from 156 to 140 us, the kinds' shares of the workgroups (glu.hip) to
 // 125; raised wave priorities and first products four side by side changed nothing beyond 3%.
 //
+// A run of fp32 additions covers at most 512 rows of a group (8192 rows in all with 16 groups of each kind, 65536
+// with 128); more rows take several launches, which add to the partial rows.
+//
 // Compiled once for each type (KRON_GLU_TYPE: 0 fp32, 1 bf16, 2 bf16 with S).
 #include "glu_parts.h"
 
 namespace kron {
 namespace {
+
+constexpr int64_t kRunRows = 512;      // rows of a group in one run of additions
 
 // Sizes of a step that both the host and the kernel use.
 struct ParamSizes {
@@ -299,7 +304,10 @@ __device__ inline void param_body(const GluParam& a, int rowgroup, int pairgroup
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int ri = 16 * (KIND == 0 ? i : j) + 4 * g + e, ci = 16 * (KIND == 0 ? j : i) + c;
-          if (ri < R && ci < Cn) out[base + (int64_t)ri * Cn + ci] = acc[i][j][e];
+          if (ri < R && ci < Cn) {
+            float& o = out[base + (int64_t)ri * Cn + ci];
+            o = a.add ? o + acc[i][j][e] : acc[i][j][e];
+          }
         }
   }
   if (KIND != 0) return;
@@ -323,7 +331,9 @@ __device__ inline void param_body(const GluParam& a, int rowgroup, int pairgroup
     if (ff * a.r >= pair0 && ff * a.r < pair0 + pairn && j < a.q && k < a.n)
       for (int w = 0; w < a.share; ++w) {
         const PartRow ow{a.part[0], prows, prow + w, 0};
-        ow[pairs * pq + (int64_t)ff * a.q * a.n + (int64_t)j * a.n + k] = w == 0 ? bl[i] : 0.f;
+        float& o = ow[pairs * pq + (int64_t)ff * a.q * a.n + (int64_t)j * a.n + k];
+        const float d = w == 0 ? bl[i] : 0.f;
+        o = a.add ? o + d : d;
       }
   }
 }
@@ -345,10 +355,23 @@ template <bool XBF, int NX, int NB, int NC, int TP, int TN, int TO>
 hipError_t launch_param_k(const GluParam& k, size_t lds, hipStream_t s) {
   constexpr int NTH = 64 * param_waves(XBF, TP > 2, TN > 2, TO > 2);
   constexpr auto kernel = glu_param_kernel<XBF, NX, NB, NC, TP, TN, TO, NTH>;
-  const hipError_t e = allow_lds<kernel>();
+  hipError_t e = allow_lds<kernel>();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)((k.groups[0] + k.groups[1]) * k.pair_groups)), dim3(NTH), lds, s, k);
-  return hipGetLastError();
+  // A group sums at most kRunRows rows in one run of fp32 additions; more rows take several launches, each of which
+  // adds its runs to the partial rows.  (Runs of 131072 equal rows were off by 4.7e-3.)
+  const int64_t most = kRunRows * std::min(k.groups[0], k.groups[1]), parts = std::max<int64_t>(1, (k.N + most - 1) / most);
+  const int64_t rows = (k.N + parts - 1) / parts;
+  for (int64_t i = 0; i < parts; ++i) {
+    GluParam part = k;
+    const int64_t r0 = i * rows;
+    part.N = std::min(rows, k.N - r0);
+    part.x = (const char*)k.x + r0 * k.p * k.m * (XBF ? 2 : 4);
+    for (int f = 0; f < 2; ++f) part.d[f] = k.d[f] + r0 * k.q * k.n4;
+    part.add = i > 0;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((k.groups[0] + k.groups[1]) * k.pair_groups)), dim3(NTH), lds, s, part);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <bool XBF, int NX, int NB, int NC>

@@ -55,6 +55,7 @@ struct GluParam {
   int pair_groups;         // workgroups that share the pairs
   int rs;                  // rows of a step (set by launch_glu_param)
   int share;               // wavefronts of a pair
+  int add;                 // to the partial rows of the launch before (set by launch_glu_param)
   const void* x;
   const float* d[2];
   const u4* tb;            // B blocks (k = m)

@@ -54,3 +54,20 @@ def test_bf16_intermediates_are_rounded(N, p, q, m, n, S):
     want = OG.backward(f64(x), f64(mask), f64(A), f64(B), f64(bias), f64(dy), "relu")["dx"]
     err = np.abs(got - want) - half_step(want)
     assert (err <= 2.0 ** -16 * want).all(), (err / want).max() * 2 ** 16
+
+
+def test_sums_over_many_rows_of_one_sign():
+    """The same row four million times: every rounding of a running sum has the same sign.  At most 512 rows are
+    summed in one run of at most six additions each (half a unit of the running sum, which grows evenly: 512 * 6 *
+    2^-25 of the result), and the runs of a group, at most 256 here, in another (2^-17)."""
+    N, r = 2 ** 22 + 5, 16
+    print("[glu] many rows of one sign", flush=True)
+    g = torch.Generator().manual_seed(3)
+    pos = lambda *s: (0.5 + torch.rand(*s, generator=g)).cuda()
+    x0, dy0, A, B, bias = pos(1, 1), pos(1, 2), pos(2, r, 1, 2), pos(2, r, 1, 1), pos(2, 2)
+    x, dy = x0.expand(N, 1).contiguous(), dy0.expand(N, 2).contiguous()
+    got = K().kron_glu_bwd(x, None, A, B, bias, dy, act="relu")
+    want = OG.backward(*(f64(v) for v in (x0, None, A, B, bias, dy0)), "relu")
+    for key in ("dA", "dB", "dbias"):
+        err = np.abs(f64(got[key]) / (N * want[key]) - 1).max()
+        assert err <= 512 * 6 * 2.0 ** -25 + 2.0 ** -17, (key, err)
