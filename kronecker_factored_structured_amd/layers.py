@@ -99,9 +99,13 @@ class _KronGLUFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, S, A, B, bias, act: str):
         rows = _whole(x.reshape(-1, x.shape[-1]))
-        ctx.save_for_backward(rows, S, A, B, bias)
+        params = (S, A, B, bias)
+        ctx.types = [None if t is None else t.dtype for t in params]
+        if rows.dtype == torch.bfloat16:      # (float32 parameters: the block runs in the input's type)
+            params = [t.to(rows.dtype) if t is not None and t.dtype == torch.float32 else t for t in params]
+        ctx.save_for_backward(rows, *params)
         ctx.act, ctx.shape = act, x.shape
-        y = api.kron_glu_fwd(rows, S, A, B, bias, act=act)
+        y = api.kron_glu_fwd(rows, *params, act=act)
         return y.view(*x.shape[:-1], y.shape[1])
 
     @staticmethod
@@ -111,8 +115,8 @@ class _KronGLUFn(torch.autograd.Function):
         g = api.kron_glu_bwd(x, S, A, B, bias, _whole(dy.reshape(x.shape[0], dy.shape[-1])), act=ctx.act,
                              want_dx=ctx.needs_input_grad[0])
         dx = g["dx"]
-        # the parameters' gradients come in float32
-        to = [None if g[k] is None else g[k].to(x.dtype) for k in ("dS", "dA", "dB", "dbias")]
+        # the parameters' gradients come in float32, which parameters in float32 get as they are
+        to = [None if g[k] is None else g[k].to(t) for k, t in zip(("dS", "dA", "dB", "dbias"), ctx.types)]
         return (None if dx is None else dx.view(ctx.shape), *to, None)
 
 
@@ -120,7 +124,8 @@ class KronGLU(nn.Module):
     """y = act(x W_0 + b_0) o (x W_1 + b_1) with W_f = sum_i kron(S_f o A_fi, B_fi): the gated half
     of a feed-forward block, both projections Kronecker layers of one shape in one kernel.  Parameters
     as KronLinear's with a leading 2 (gate, up).  x: [..., in_features], float32 or bfloat16 like the
-    parameters; act: silu, gelu, gelu_tanh or relu.  The backward recomputes the projections.
+    parameters, or bfloat16 with float32 parameters: they are rounded to bfloat16 for the products, and their
+    gradients stay float32.  act: silu, gelu, gelu_tanh or relu.  The backward recomputes the projections.
     A backward captured into a graph has to be the only autograd graph of the parameters alive (or
     taken with torch.autograd.grad): torch ends the process otherwise, for this module as for any."""
 

@@ -71,3 +71,27 @@ def test_sums_over_many_rows_of_one_sign():
     for key in ("dA", "dB", "dbias"):
         err = np.abs(f64(got[key]) / (N * want[key]) - 1).max()
         assert err <= 512 * 6 * 2.0 ** -25 + 2.0 ** -17, (key, err)
+
+
+def test_module_with_float32_parameters_and_a_bfloat16_input():
+    """The products take the parameters rounded to bfloat16; their gradients are the float32 ones of those (the
+    layer's bar, 1e-5 of the largest value), which bfloat16 could hold to 2^-8 alone."""
+    from _harness import TOL_F32, rel_err
+    torch.manual_seed(2)
+    mod = K().KronGLU(8 * 6, 10 * 7, m=6, r=3, n=7, act="gelu", device="cuda")
+    with torch.no_grad():
+        mod.S.mul_(torch.rand_like(mod.S))
+        mod.bias.normal_(std=0.3)
+    x = torch.randn(5, 40, 48, device="cuda").to(BF).requires_grad_()
+    dy = torch.randn(5, 40, 70, device="cuda").to(BF)
+    y = mod(x)
+    assert y.dtype == BF and y.shape == (5, 40, 70)
+    y.backward(dy)
+    h = [f64(x).reshape(200, 48)] + [f64(p.to(BF)) for p in (mod.S, mod.A, mod.B, mod.bias)]
+    want = OG.backward(*h, f64(dy).reshape(200, 70), "gelu")
+    for key, t in (("dS", mod.S), ("dA", mod.A), ("dB", mod.B), ("dbias", mod.bias)):
+        assert t.grad.dtype == F32 and rel_err(f64(t.grad), want[key].reshape(t.shape)) <= TOL_F32, key
+    assert x.grad.dtype == BF
+    # the other way round stays refused: a float32 input of bfloat16 parameters
+    with pytest.raises(ValueError, match="must be torch.float32"):
+        mod.to(BF)(x.detach().float())
