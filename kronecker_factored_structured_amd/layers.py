@@ -168,8 +168,9 @@ class _KronDistillFn(torch.autograd.Function):
 class KronDistillLoss(nn.Module):
     """Distillation from a teacher's top logits (kron_topk_logits), mixed with the cross-entropy on
     labels: alpha T^2 KD + (1 - alpha) CE over the rows, weighted (weights None: their mean, weight 0: a
-    padded position).  logits [..., V] with ids and teacher [..., k], the others [...]; the gradient goes to
-    the logits alone."""
+    padded position).  logits [..., V] with ids and teacher [..., k], the others [...] (nothing: one row); the
+    gradient goes to the logits alone.  Logits whose leading dimensions are not one stride apart are copied:
+    give a batch's last positions weight 0 rather than cutting them off (logits[:, :-1])."""
 
     def __init__(self, temperature: float = 1.0, alpha: float = 1.0):
         super().__init__()
@@ -179,7 +180,9 @@ class KronDistillLoss(nn.Module):
 
     def forward(self, logits, ids=None, teacher=None, teacher_lse=None, labels=None, weights=None):
         def rows(t, last):
-            return None if t is None else t.flatten(0, -1 - last) if t.dim() > 1 + last else t
+            if t is None or t.dim() == 1 + last:
+                return t
+            return t.flatten(0, -1 - last) if t.dim() > 1 + last else t.unsqueeze(0)
         other = [_whole(rows(t, last)) for t, last in ((ids, 1), (teacher, 1), (teacher_lse, 0), (labels, 0), (weights, 0))]
         return _KronDistillFn.apply(rows(logits, 1), *other, self.temperature, self.alpha)
 

@@ -209,3 +209,18 @@ def test_distill_small_temperatures(T, tail, N):
     w[:4] = g.uniform(0.2, 1.0, 4)
     z = z.cuda()
     check(z, ids, t, lse, None, w, T, 1.0, OD.loss_and_grad(f64(z), ids, t, lse, None, w, T, 1.0), F32)
+
+
+def test_loss_module_takes_a_single_row():
+    """logits [V] with ids and teacher [k] and nothing before them: one row, as with a leading dimension of one."""
+    V, k = 333, 12
+    gen = torch.Generator().manual_seed(8)
+    z = torch.randn(V, generator=gen).cuda().requires_grad_()
+    ids, vals, lse = K().kron_topk_logits(torch.randn(1, V, generator=gen).cuda(), k)
+    lab, w = torch.tensor(7, device="cuda"), torch.tensor(0.5, device="cuda")
+    mod = K().KronDistillLoss(temperature=2.0, alpha=0.5)
+    loss = mod(z, ids[0], vals[0], lse[0], lab, w)
+    (g,) = torch.autograd.grad(loss, [z])
+    want = mod(z.view(1, V), ids, vals, lse, lab.view(1), w.view(1))
+    (gw,) = torch.autograd.grad(want, [z])
+    assert loss.shape == () and torch.equal(loss, want) and g.shape == (V,) and torch.equal(g, gw)
