@@ -12,6 +12,7 @@ from torch import nn
 from torch.autograd.function import once_differentiable
 
 from . import api
+from ._lib import KRON_GLU_MAX_RANK, KRON_GLU_MAX_SIDE
 
 
 class _KronLinearFn(torch.autograd.Function):
@@ -125,7 +126,8 @@ class KronGLU(nn.Module):
     of a feed-forward block, both projections Kronecker layers of one shape in one kernel.  Parameters
     as KronLinear's with a leading 2 (gate, up).  x: [..., in_features], float32 or bfloat16 like the
     parameters, or bfloat16 with float32 parameters: they are rounded to bfloat16 for the products, and their
-    gradients stay float32.  act: silu, gelu, gelu_tanh or relu.  The backward recomputes the projections.
+    gradients stay float32.  m, n, in_features / m and out_features / n are at most 64, r at most 16.  act: silu,
+    gelu, gelu_tanh or relu.  The backward recomputes the projections.
     A backward captured into a graph has to be the only autograd graph of the parameters alive (or
     taken with torch.autograd.grad): torch ends the process otherwise, for this module as for any."""
 
@@ -138,6 +140,9 @@ class KronGLU(nn.Module):
         if act not in api.KRON_ACTS:
             raise ValueError(f"act must be one of {sorted(api.KRON_ACTS)}, got {act!r}")
         p, q = in_features // m, out_features // n
+        if not 1 <= min(p, q, m, n) <= max(p, q, m, n) <= KRON_GLU_MAX_SIDE or not 1 <= r <= KRON_GLU_MAX_RANK:
+            raise ValueError(f"the factors' sides p = {p}, q = {q}, m = {m}, n = {n} must be in 1..{KRON_GLU_MAX_SIDE} "
+                             f"and r = {r} in 1..{KRON_GLU_MAX_RANK}")
         kw = dict(device=device, dtype=dtype)
         self.S = nn.Parameter(torch.ones(2, p, q, **kw)) if with_S else None
         self.A = nn.Parameter(torch.randn(2, r, p, q, **kw) / math.sqrt(p))

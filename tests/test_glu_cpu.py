@@ -111,3 +111,13 @@ def test_binding_refuses():
         K.kron_glu_fwd(x, None, A, B, act="tanh")
     with pytest.raises(ValueError, match="unsupported dtype"):
         K.kron_glu_fwd(x.half(), None, A, B)
+
+
+def test_module_refuses_sizes_that_its_forward_would():
+    pytest.importorskip("torch")
+    import kronecker_factored_structured_amd as K
+    for kw in (dict(in_features=65 * 4), dict(out_features=65 * 4), dict(in_features=65, m=65, n=4), dict(n=65, out_features=65),
+               dict(r=17), dict(r=0), dict(in_features=0)):
+        with pytest.raises(ValueError, match="must be in 1"):
+            K.KronGLU(**{**dict(in_features=64, out_features=32, m=4, r=2), **kw})
+    assert sum(p.numel() for p in K.KronGLU(64, 32, m=4, r=2).parameters()) == 2 * (16 * 8 * 3 + 2 * 16 + 32)
