@@ -46,9 +46,15 @@ def _need(t: Optional[torch.Tensor], name: str, shape: tuple, dtype=torch.float3
         raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
+# The current stream's handle itself: torch.cuda.current_stream makes a Stream object around it, 2 us of a call's 15.
+# (Not part of torch's public interface, so a torch without it has the object made.)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device: torch.device):
-    # (the handle itself: torch.cuda.current_stream makes a Stream object around it, 2 us of a call's 15)
-    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(device.index))
+    if _raw_stream is None:
+        return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    return ctypes.c_void_p(_raw_stream(device.index))
 
 
 _HERE = contextlib.nullcontext()

@@ -121,3 +121,16 @@ def test_module_refuses_sizes_that_its_forward_would():
         with pytest.raises(ValueError, match="must be in 1"):
             K.KronGLU(**{**dict(in_features=64, out_features=32, m=4, r=2), **kw})
     assert sum(p.numel() for p in K.KronGLU(64, 32, m=4, r=2).parameters()) == 2 * (16 * 8 * 3 + 2 * 16 + 32)
+
+
+def test_stream_without_the_private_handle(monkeypatch):
+    """A torch without the private call has its public one asked, of the tensors' device."""
+    torch = pytest.importorskip("torch")
+    from types import SimpleNamespace
+
+    from kronecker_factored_structured_amd import api
+    monkeypatch.setattr(api, "_raw_stream", None)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d: SimpleNamespace(cuda_stream=0x1230 + d.index))
+    assert api._stream(torch.device("cuda", 5)).value == 0x1235
+    monkeypatch.setattr(api, "_raw_stream", lambda i: 0x4560 + i)
+    assert api._stream(torch.device("cuda", 5)).value == 0x4565
