@@ -52,12 +52,13 @@ __device__ inline int64_t kept_id(const DistillArgs& a, int64_t row, int j) {
   return a.ids64 ? ((const int64_t*)a.ids)[i] : (int64_t)((const int32_t*)a.ids)[i];
 }
 
-// e^x for x <= 0 in 64 bits: 2^n times a polynomial of the rest, |r| <= ln 2 / 2 (the series to the
-// 13th power is exact to 2^-58).  Few registers, while the row holds most of them.
+// e^x for x <= 0 in 64 bits: 2^n times a polynomial of the rest r = x - n ln 2, |r| <= ln 2 / 2 (the series to the
+// 13th power is exact to 2^-58).  The rest is taken in two steps (Cody and Waite): ln 2 rounded to 40 binary places,
+// whose product with n < 2^11 is exact, and what that leaves of ln 2.  Few registers, while the row holds most of them.
 __device__ inline double exp64(double x) {
   if (x < -700.0) return 0.0;
   const double n = rint(x * 1.4426950408889634);
-  const double r = fma(n, -1.9082149292705877e-10, fma(n, -0.6931471803691238, x));
+  const double r = fma(n, 1.7239444525614835e-13, fma(n, -0x1.62e42fefa4p-1, x));
   double p = 1.0 / 6227020800.0;
   const double c[13] = {1.0 / 479001600.0, 1.0 / 39916800.0, 1.0 / 3628800.0, 1.0 / 362880.0, 1.0 / 40320.0,
                         1.0 / 5040.0,      1.0 / 720.0,      1.0 / 120.0,     1.0 / 24.0,     1.0 / 6.0,
