@@ -263,8 +263,6 @@ hipError_t launch_head(const HeadArgs& a, int G, hipStream_t s);
 // ---------------------------------------------------------------------------------
 // Gated Kronecker block (glu.hip): the gate's factors first, then the up-projection's.
 // ---------------------------------------------------------------------------------
-constexpr int kGluMaxSide = 64;
-constexpr int kGluMaxRank = 16;
 struct GluArgs {
   int64_t N;
   int32_t p, q, m, n, r;
