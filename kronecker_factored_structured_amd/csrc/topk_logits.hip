@@ -165,8 +165,9 @@ __global__ __launch_bounds__(NT, 4) void topk_kernel(TopkArgs a) {
 #pragma unroll
   for (int w = 0; w < NW; ++w) s += red[w];
   if (tid == 0) {
-    // m / T + ln s, with the rounded m log2 e / T where the exponentials used that
-    const double base = finite ? (double)c * 0.69314718055994531 : (double)m / (double)a.T;
+    // m / T + ln s, less what the exponentials' rounded shift and scale put into s beside 2^((x - m) sT)
+    double base = (double)m / (double)a.T;
+    if (finite) base -= ((double)m * (double)sT - (double)c) * 0.69314718055994531;
     a.lse[row] = (float)(base + (double)logf(s));
   }
   uint32_t nc = ncand;

@@ -224,3 +224,15 @@ def test_loss_module_takes_a_single_row():
     want = mod(z.view(1, V), ids, vals, lse, lab.view(1), w.view(1))
     (gw,) = torch.autograd.grad(want, [z])
     assert loss.shape == () and torch.equal(loss, want) and g.shape == (V,) and torch.equal(g, gw)
+
+
+@pytest.mark.parametrize("V", [7, 3000, 140000])
+def test_topk_lse_of_one_value(V):
+    """A row with one finite value z has lse z / T exactly: rounded once (and the quotient in 64 bits)."""
+    T = 1.7
+    z = torch.full((50, V), -float("inf"))
+    v = torch.randn(50, generator=torch.Generator().manual_seed(6)) * 50
+    z[:, V // 2] = v
+    lse = K().kron_topk_logits(z.cuda(), 2, temperature=T)[2]
+    want = v.double().numpy() / float(np.float32(T))
+    assert np.all(np.abs(f64(lse) - want) <= 2.0 ** -24 * np.abs(want) * (1 + 2.0 ** -20))
