@@ -95,3 +95,42 @@ def test_module_with_float32_parameters_and_a_bfloat16_input():
     # the other way round stays refused: a float32 input of bfloat16 parameters
     with pytest.raises(ValueError, match="must be torch.float32"):
         mod.to(BF)(x.detach().float())
+
+
+def test_float32_products():
+    """Outputs of one product after another, x B and then C, beside their own size.  Three bf16 parts cut off the top
+    bits leave less than 2^-7, 2^-15 and nothing, so the terms left out of a product are below 2 * 2^-22 and a
+    little, and what is left is summed from the small terms up: one rounding of its size (2^-24, or 2^-23 if it is
+    cut off)."""
+    N = 512
+    g = torch.Generator().manual_seed(12)
+    pos = lambda *s: (1 + torch.rand(*s, generator=g)).cuda()
+    x, A, B = pos(N, 1), pos(2, 1, 1, 64), pos(2, 1, 1, 64)
+    A[1] = 0
+    bias = torch.zeros(2, 64 * 64, device="cuda")
+    bias[1] = 1
+    want = OG.forward(*(f64(v) for v in (x, None, A, B, bias)), "relu")
+    err = np.abs(f64(K().kron_glu_fwd(x, None, A, B, bias, act="relu")) / want - 1).max()
+    assert err <= 2 * (2.0 ** -21 + 2.0 ** -23), err * 2 ** 24
+    # the gradient of x through the gate alone: u = 1 (its weight is 0), d = dy, one term a sum
+    x, A, B, dy = pos(N, 64 * 64), pos(2, 1, 64, 1), pos(2, 1, 64, 1), pos(N, 1)
+    A[1] = 0
+    bias = torch.zeros(2, 1, device="cuda")
+    bias[1] = 1
+    got = f64(K().kron_glu_bwd(x, None, A, B, bias, dy, act="relu")["dx"])
+    want = f64(dy)[:, :, None] * (f64(A)[0, 0] * f64(B)[0, 0].T).reshape(1, 1, -1)
+    err = np.abs(got / want.reshape(N, -1) - 1).max()
+    assert err <= 2 * (2.0 ** -21 + 2.0 ** -23), err * 2 ** 24
+
+
+def test_float32_values_up_to_the_largest():
+    """Values that bf16 rounds to infinity (3.39e38 to fp32's largest) count as themselves."""
+    top = torch.finfo(F32).max
+    x = torch.tensor([[top, -top], [3.395e38, 1.0]], device="cuda")
+    A = torch.tensor([2.0 ** -100, 0.0]).view(2, 1, 1, 1).cuda()
+    B = torch.zeros(2, 1, 2, 2, device="cuda")
+    B[0, 0] = torch.tensor([[1.0, 0.0], [0.0, 1.0]])
+    bias = torch.tensor([[0.0, 0.0], [1.0, 1.0]], device="cuda")
+    y = f64(K().kron_glu_fwd(x, None, A, B, bias, act="relu"))
+    want = np.maximum(f64(x) * 2.0 ** -100, 0)
+    assert (np.abs(y - want) <= 2 * (2.0 ** -21 + 2.0 ** -23) * np.abs(want)).all(), (y, want)
