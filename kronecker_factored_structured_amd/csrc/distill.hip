@@ -28,10 +28,12 @@
 // the rest that exponentials beside the row's maximum cannot hold it (cold_rest), the rest has a maximum of
 // its own: one more pass over the registers, and its sum and gradients beside that one.
 //
-// Measured: 8192 x 50257 bf16, k = 64, tail and labels: 389 us for 1.65 GB, 4.2 TB/s (a large copy reaches 4.9).
+// Measured: 8192 x 50257 bf16, k = 64, tail and labels: 392 us for 1.65 GB, 4.2 TB/s (a large copy reaches 4.9); 27
+// of them the loss kernel's one workgroup (under the profiler).
 // Two workgroups of 512 threads a CU hold 13 vectors each in registers; the passes over them (maximum, sums,
-// gradient) run while the other workgroup loads or stores.  Two calls over 2050 x 32003 fp32, k = 256: 207
-// to 210 us (part 52 at 5.0 TB/s, statistics 13, gradient 131 at 4.0, loss 7).  16 x 50257 fp32: 18 us, three launches of 5, 8 and 2.
+// gradient) run while the other workgroup loads or stores.  Two calls over 2050 x 32003 fp32, k = 256: 205
+// to 211 us (part 53 at 5.0 TB/s, statistics 13, gradient 131 at 4.0, loss 7).
+// 16 x 50257 fp32: 18.6 us, three launches of 5, 9 and 2.
 #include <algorithm>
 
 #include "kron_internal.h"
@@ -815,14 +817,22 @@ __global__ __launch_bounds__(1024) void distill_loss_kernel(DistillArgs a) {
 
 int64_t max_vectors(int V, bool bf16) { return ((int64_t)V + 7) / (bf16 ? 8 : 4) + 1; }   // of a row that starts anywhere
 
-// Rows in registers for enough rows to fill the GPU (two workgroups a CU).  Loss and gradient of 4096 x 50257
-// fp32 (before non-temporal accesses): 466 us, by chunks 535; 2050 x 32003 fp32 209 and 220; 2050 x 65000 bf16
-// 230 and 227.
+// Rows in registers for enough rows to fill the GPU (two workgroups a CU), else chunks.  Loss and gradient, k = 64 and a
+// tail, by rows and by chunks:
+//   bf16       N = 16        256         512         1024         4096
+//   5000       20 / 27    21 / 28     24 / 32      34 / 34     93 / 91 us
+//   32003      26 / 26    28 / 35     34 / 44      57 / 69   171 / 210
+//   50257      27 / 19    32 / 41     40 / 63     66 / 103   205 / 337
+//   100003     31 / 26    40 / 56     68 / 86    125 / 145   465 / 495
+//   fp32 50257 23 / 25    36 / 53     64 / 81    118 / 137   426 / 464
+// (From 128 rows on rows have the better of it as well, 22 to 33 against 26 to 43 us; at 64 it is even.)
 constexpr int kRowVectors = 13 * 1024;
 bool whole_rows(const DistillArgs& a) { return a.N >= 512 && max_vectors(a.V, a.bf16) <= kRowVectors; }
 
 // Vectors of a chunk: as many as a workgroup holds, fewer while there are not 1024 workgroups, at least two a
-// thread.  Depends on the sizes alone.
+// thread.  Depends on the sizes alone.  (With 512 workgroups instead all sizes of the table below are within 5% but
+// 512 x 5000, 29 us for 32; with 2048 bf16 32003 takes 44 and 52 us at 256 and 512 rows for 35 and 44, and 1024 x 5000
+// 48 for 34.)
 int chunk_vectors(int64_t N, int V, bool bf16) {
   const int64_t nv = max_vectors(V, bf16);
   int per = kCV;

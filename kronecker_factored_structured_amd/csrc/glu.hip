@@ -7,9 +7,10 @@
 // The products are in glu_rows.hip (forward, gradients of both projections, dX) and glu_param.hip (the
 // factors' gradients); here are the layout of the factors, the last sums and the order of the launches.
 //
-// Small calls are bound by their launches: one token through 768 -> 2048 takes 13 to 14 us, 4.5 of them the
-// layout of the factors and 5.3 the products; a backward of 61 rows 31 us in five launches of 4 to 12.  (The
-// layout is made in each call: factors change with every training step.)
+// Small calls are bound by their launches and the latency in them: one token through 768 -> 2048 takes 13 to 15 us, 4.4
+// of them the layout of the factors and 5.5 the products (on four workgroups); a backward of 61 rows 31 us in five
+// launches of 4 to 13 under the profiler.  The layout is made in each call, from the plain factors that the
+// calls take: training changes them with every step, serving pays the 4.4 us for each token.
 #include "glu_parts.h"
 
 namespace kron {

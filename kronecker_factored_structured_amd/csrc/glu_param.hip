@@ -7,14 +7,15 @@
 // is staged, half of the wavefronts staging first and half multiplying first, and the values of the one
 // after that are on their way.
 //
-// Slots of a block are permuted so that neither side has bank conflicts: column c of k-group g stands
-// at 16 g + 4 ((c % 4) ^ g) + c / 4.  A wavefront stores columns of one residue mod 4 at a time: their
-// quarters of a 256-byte row differ by g.
+// Slots of a block are permuted against bank conflicts: column c of k-group g stands at 16 g + 4 ((c % 4) ^ g) + c / 4.
+// A wavefront stores columns of one residue mod 4 at a time: their quarters of a 256-byte row differ by g.  (Conflicts
+// are a quarter of the LDS cycles that are left, by counter 3.6 M of 14.9 M at the size below.)
 //
-// Measured at 8192 x (768 -> 2048) bf16, r = 4: 125 us; its products alone would take 43 (88 instructions a row
-// and pair), its reads of d_f 27.  What bounds it: two wavefronts a SIMD (their sums and B take 190 registers)
-// do not cover the LDS reads, the splits of d_f, Z and G into parts and the staging beside the products; without
-// the products the staging alone took 82 us.  2048 x 1024^2 fp32: 35 us.  Operands read one product ahead and
+// Measured at 8192 x (768 -> 2048) bf16, r = 4: 125 us; its products (5,666 instructions a SIMD) would take 38 at the
+// matrix cores' peak and 79 at the rate of a large library product, its reads of d_f 27.  What bounds it: matrix
+// cores 0.32 of the time, vector instructions 0.30, and a wavefront waits 0.39 of its time; two wavefronts a SIMD
+// (their sums and B take 190 registers) do not cover the LDS reads, the splits of d_f, Z and G into parts and the
+// staging beside the products.  Without the products the staging alone took 82 us.  2048 x 1024^2 fp32: 35 us.  Operands read one product ahead and
 // instances by the sides' tiles took it from 156 to 140 us, the kinds' shares of the workgroups (glu.hip) to
 // 125; raised wave priorities and first products four side by side changed nothing beyond 3%.
 //

@@ -11,13 +11,16 @@
 //        directly) while this one's are multiplied; a wavefront has one row
 // Few rows: the q tiles are spread over gridDim.y workgroups.
 //
-// Why in registers and LDS: nothing but X and the outputs passes through memory, and the products need
-// 21 us of the matrix cores for 8192 x (1024 -> 4096) bf16, r = 4, whose bytes need 17.  Measured there 51 us
-// (506 TFLOP/s of the formula's work, 0.42 of the rate of a large library product); streamed factors took 64.
-// What bounds it: beside 320 products a row the vector unit splits Z into parts, applies the activation and
-// packs y; four wavefronts a SIMD overlap the two only in part.  3001 x (750 -> 2021) fp32, r = 3: 48 us, six products for each of the formula's.
-// MODE 1 and 2 (8192 x (768 -> 2048) bf16): 58 and 44 us, of which the fp32 dg, du in the workspace (134 MB
-// written, then read) take 27 and 27 at the rate of a large copy.
+// Why in registers and LDS: nothing but X and the outputs passes through memory.  8192 x (1024 -> 4096) bf16, r = 4:
+// at the rate of a large library product (1206 TFLOP/s) the formula's work is 21 us and the 320 products a row that are
+// made of it (42.9 GFLOP: Z in two parts) 36; the bytes need 17.  Measured 51 us (506 TFLOP/s of the formula's work);
+// streamed factors took 64.  What bounds it, by counters: the matrix cores are busy 0.34 of the time, and vector
+// instructions (Z's parts, the activation, y) fill another 0.34; they alternate in a wavefront, which waits a quarter
+// of its time, and four wavefronts a SIMD overlap them in part.
+// 3001 x (750 -> 2021) fp32, r = 3: 48 us; six products for one and sides of 25, 43, 30 and 47 in tiles make 42.5 GFLOP
+// of 3.1 (35 us at that rate); matrix 0.34, vector 0.26.
+// MODE 1 and 2 (8192 x (768 -> 2048) bf16): 57 and 44 us, of which the fp32 dg, du in the workspace (134 MB
+// written, then read) take 27 and 27 at the rate of a large copy; MODE 1 waits 0.70 of its time for them.
 //
 // Compiled once for each MODE (KRON_GLU_MODE).
 #include "glu_parts.h"

@@ -7,12 +7,13 @@
 // values reach, and for k below the thread count few more do (for values in random order about
 // NT ln(NT / (NT - k)) in all).  Those candidates go to LDS and are ranked by counting.  Rows
 // that defeat the threshold (many equal values, the top in few threads, fewer vectors than k) and
-// rows with a NaN, an infinite maximum or one that is large against T take an exact bisection on the value's key, then on the
-// token among the equal ones.  Rows beyond 13 vectors a thread are read twice, the second time mostly from cache.
+// rows with a NaN, an infinite maximum or one that is large against T take an exact bisection on the value's
+// key, then on the token among the equal ones.  Rows beyond 13 vectors a thread are read twice, the second time mostly from cache.
 //
-// Measured: 8192 x 50257 bf16, k = 64: 232 us, 3.56 TB/s (a large sum reads at 4.0); 257 x 131072 fp32, k = 256:
-// 59 us, 51 of them the kernel (28 at a copy's rate; one workgroup a CU passes twice over its row); one row of
-// 50257 bf16 values 10.5 us, the latency of one workgroup's passes.  Cutting long rows into chunks and joining
+// Measured: 8192 x 50257 bf16, k = 64: 233 us, 3.56 TB/s (a large sum reads at 4.0; vector instructions fill 0.65 of the
+// time under the profiler); 257 x 131072 fp32, k = 256: 59 us, 55 of them the kernel under the profiler (28 at a copy's
+// rate; one workgroup a CU passes twice over its row); one row of 50257 bf16 values 10.4 us, the latency of one
+// workgroup's passes.  Cutting long rows into chunks and joining
 // their tops took 61 to 80 us at 257 rows (each chunk ranks k candidates of its own) and 276 instead of 363 at
 // 2048 rows, k = 64; one row cut over six workgroups 15.6 us: not kept.
 #include <algorithm>
@@ -218,6 +219,10 @@ __global__ __launch_bounds__(NT, 4) void topk_kernel(TopkArgs a) {
   }
 }
 
+// Registers by the row's vectors: fewer of them let more workgroups on a CU.  4096 rows, k = 64, with 4, 8 and 13 vectors
+// a thread and with 1024 threads: 5000 bf16 values 46, 50, 65 and 132 us; 16000 59, 61, 81 and 151; 32003 - , 82, 107 and
+// 190; 50257 -, -, 127 and 217.  1024 threads hold 100003 bf16 values in 298 us and read them twice in 269, 32003 fp32
+// ones in 202 and 172, 50257 in 250 and 248; up to 512 rows the two are within 8% of each other, either way.
 template <bool BF>
 hipError_t launch_type(const TopkArgs& a, int64_t rows, hipStream_t s) {
   const int64_t nvec = ((int64_t)a.V + 7) / (BF ? 8 : 4) + 1;   // of a row that starts anywhere
