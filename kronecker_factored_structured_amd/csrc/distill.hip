@@ -21,8 +21,9 @@
 // threads write: no address is written twice, so nothing waits.
 //
 // Exponentials are 2^(z s - c) with c = m s rounded once: the rounding of c is a factor of every one
-// and cancels in every softmax, as long as it is a moderate one (see Scale::at).  One exponential serves a row that needs one temperature (KD or CE alone, or T = 1);
-// at T = 2 the one of CE is the square of KD's; otherwise CE takes a second one (`two`).
+// and cancels in every softmax, as long as it is a moderate one (see Scale::at).  One exponential serves
+// a row that needs one temperature (KD or CE alone, or T = 1); at T = 2 the one of CE is the square of
+// KD's; otherwise CE takes a second one (`two`).
 //
 // With a tail the gradient off the kept tokens needs q_v / q_t.  Where the kept tokens stand so far above
 // the rest that exponentials beside the row's maximum cannot hold it (cold_rest), the rest has a maximum of
