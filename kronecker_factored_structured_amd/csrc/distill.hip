@@ -353,8 +353,8 @@ __device__ inline RowStats finish_row(const DistillArgs& a, int64_t row, float w
       const bool rest = psum < 1.0 && !(tr == 0.f && a.k >= a.V);
       ptail = rest ? 1.0 - psum : 0.0;
       // Beside so small a q_t what the rounding of teacher_lse (half a step, and the error of a sum in 32 bits) leaves
-      // of p_t would be all of the loss, and infinite where the rest is masked: it is no mass.
-      if (cold && ptail <= 0x1p-20 + 0x1p-23 * fabs((double)r.ta)) ptail = 0.0;
+      // of p_t would be all of the loss, and infinite where the rest is masked: it is no mass.  (An infinity is exact.)
+      if (cold && fabsf(r.ta) < INFINITY && ptail <= 0x1p-20 + 0x1p-23 * fabs((double)r.ta)) ptail = 0.0;
       pmass = psum;
       r.mass = (float)(psum + ptail);
       r.base = r.mass;      // (a rest of -infinity throughout has gradient 0 whatever this is)

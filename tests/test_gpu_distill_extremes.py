@@ -236,3 +236,37 @@ def test_topk_lse_of_one_value(V):
     lse = K().kron_topk_logits(z.cuda(), 2, temperature=T)[2]
     want = v.double().numpy() / float(np.float32(T))
     assert np.all(np.abs(f64(lse) - want) <= 2.0 ** -24 * np.abs(want) * (1 + 2.0 ** -20))
+
+
+@pytest.mark.parametrize("V,dtype", [(110003, BF), (60001, F32)])
+def test_many_rows_of_a_long_vocabulary(V, dtype):
+    """Rows that no workgroup's registers hold, more of them than one to a CU: chunks, in one call (in place too) and
+    in two.  Most have no weight, so that the oracle has few to do."""
+    N, k, T, alpha = 520, 40, 2.0, 0.5
+    print(f"[distill long] V={V} {dtype}", flush=True)
+    g = np.random.default_rng(3)
+    z = (torch.randn(N, V, generator=torch.Generator().manual_seed(5)) * 2).to(dtype).cuda()
+    ids = np.stack([g.permutation(V)[:k] for _ in range(N)])
+    t = (g.standard_normal((N, k)) * 2 + 6).astype(np.float32)
+    lse = (np.log(np.exp(t.astype(np.float64) / T).sum(1)) + g.uniform(0.01, 0.3, N)).astype(np.float32)
+    lab = g.integers(0, V, N)
+    w = np.zeros(N, np.float32)
+    w[5::100] = g.uniform(0.2, 1.0, len(w[5::100]))
+    z[105] = -1e10
+    z[205, torch.from_numpy(ids[205]).cuda()] += 300
+    check(z, ids, t, lse, lab, w, T, alpha, OD.loss_and_grad(f64(z), ids, t, lse, lab, w, T, alpha), dtype)
+    args = dict(teacher_lse=dev(lse), labels=dev(lab), weights=dev(w), temperature=T, alpha=alpha)
+    want = K().kron_distill(z, dev(ids.astype(np.int32)), dev(t), **args)
+    got = K().kron_distill(z, dev(ids.astype(np.int32)), dev(t), out=z, **args)
+    assert torch.equal(z, want["dlogits"]) and torch.equal(got["loss"], want["loss"])
+
+
+def test_distill_a_teacher_without_any_value_far_above_the_rest():
+    """teacher_lse of -infinity is no rounding: the rest has all the mass also where the student has next to none there."""
+    V, k = 3000, 6
+    z = torch.randn(2, V, generator=torch.Generator().manual_seed(4)).cuda()
+    z[:, :k] += 150
+    ids = np.tile(np.arange(k), (2, 1))
+    t, lse = np.full((2, k), -np.inf, np.float32), np.full(2, -np.inf, np.float32)
+    want = OD.loss_and_grad(f64(z), ids, t, np.zeros(2, np.float32), None, None, 1.0, 1.0)
+    check(z, ids, t, lse, None, None, 1.0, 1.0, want, F32)
