@@ -373,10 +373,10 @@ __device__ inline RowStats finish_row(const DistillArgs& a, int64_t row, float w
     o.total = total;
     o.rest = tr;
     o.t1 = t1;
-    // the label's z s - c of CE's exponential
-    o.zl = !c.ce || !labok ? 0.f
-           : c.two == 0    ? fmaf(c.place(zl), c.sA, -c.cA)
-                           : fmaf(c.place(zl), c.two == 1 ? 2.f * c.sA : kLog2e, -c.cB);
+    // the label's logit beside the maximum as CE's exponentials had it, in 64 bits: z s - c of the type's lowest value
+    // is beyond 32
+    const double s = c.two == 0 ? c.sA : c.two == 1 ? 2.f * c.sA : kLog2e;
+    o.zl = !c.ce || !labok ? 0.f : (float)(((double)c.place(zl) * s - (double)(c.two == 0 ? c.cA : c.cB)) * kLn2);
     o.w = bad ? __builtin_nanf("") : w;
     o.lift = cold ? lift : 0.f;
     a.rows[row] = o;
@@ -803,7 +803,7 @@ __global__ __launch_bounds__(1024) void distill_loss_kernel(DistillArgs a) {
         kl += r.pt * (log(r.pt) - log((double)r.rest / (double)r.total) - (double)r.lift * kLn2);
       l += (double)a.alpha * (double)a.T * (double)a.T * kl;
     }
-    if (a.alpha < 1.f) l += (1.0 - (double)a.alpha) * (log((double)r.t1) - (double)r.zl * kLn2);
+    if (a.alpha < 1.f) l += (1.0 - (double)a.alpha) * (log((double)r.t1) - (double)r.zl);
     s += (double)(float)((double)r.w * l);
   }
   s = wave_sum(s);

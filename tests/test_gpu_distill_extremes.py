@@ -270,3 +270,19 @@ def test_distill_a_teacher_without_any_value_far_above_the_rest():
     t, lse = np.full((2, k), -np.inf, np.float32), np.full(2, -np.inf, np.float32)
     want = OD.loss_and_grad(f64(z), ids, t, np.zeros(2, np.float32), None, None, 1.0, 1.0)
     check(z, ids, t, lse, None, None, 1.0, 1.0, want, F32)
+
+
+@pytest.mark.parametrize("N", [3, 600])
+@pytest.mark.parametrize("T", [1.0, 2.0, 1.5])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_label_of_the_lowest_value(dtype, T, N):
+    """The cross-entropy of a label that the type's lowest value masks is as large as that, and a number."""
+    V, alpha = 700, 0.25
+    z = torch.randn(N, V, generator=torch.Generator().manual_seed(3))
+    z[1, 50:60] = torch.finfo(dtype).min
+    z = z.to(dtype).cuda()
+    ids, t = np.tile(np.arange(4), (N, 1)), np.zeros((N, 4), np.float32)
+    lab = np.full(N, 55)
+    w = np.zeros(N, np.float32)
+    w[:3] = 0.25
+    check(z, ids, t, None, lab, w, T, alpha, OD.loss_and_grad(f64(z), ids, t, None, lab, w, T, alpha), dtype)
