@@ -158,9 +158,9 @@ __device__ inline float vec_max(const u32x4& v) {
 }
 
 // Whether the sum off the kept tokens, beside the whole maximum, is too small to be relied on: terms below
-// 2^-126 are lost, at most 2^18 of them, which is nothing beside 2^-80.
+// 2^-126 are lost, and with them the gradients p_t q_v / q_t of tokens that have less than 2^-86 of the rest.
 __device__ inline bool cold_rest(const DistillArgs& a, const Scale& c, float sr) {
-  return c.kd && a.teacher_lse && sr < 0x1p-80f;
+  return c.kd && a.teacher_lse && sr < 0x1p-40f;
 }
 // The largest value of a vector off the kept tokens, and the sum of their first exponentials beside it.
 template <bool BF>
@@ -352,14 +352,15 @@ __device__ inline RowStats finish_row(const DistillArgs& a, int64_t row, float w
       // (with every token kept there is no tail, whatever rounding leaves of its mass)
       const bool rest = psum < 1.0 && !(tr == 0.f && a.k >= a.V);
       ptail = rest ? 1.0 - psum : 0.0;
-      // Beside so small a q_t what the rounding of teacher_lse (half a step, and the error of a sum in 32 bits) leaves
+      const double qt = cold ? (double)tr * exp64((double)lift * kLn2) / (double)total : 1.0;
+      // Beside a q_t below 2^-80 what the rounding of teacher_lse (half a step, and the error of a sum in 32 bits) leaves
       // of p_t would be all of the loss, and infinite where the rest is masked: it is no mass.  (An infinity is exact.)
-      if (cold && fabsf(r.ta) < INFINITY && ptail <= 0x1p-20 + 0x1p-23 * fabs((double)r.ta)) ptail = 0.0;
+      if (qt < 0x1p-80 && fabsf(r.ta) < INFINITY && ptail <= 0x1p-20 + 0x1p-23 * fabs((double)r.ta)) ptail = 0.0;
       pmass = psum;
       r.mass = (float)(psum + ptail);
       r.base = r.mass;      // (a rest of -infinity throughout has gradient 0 whatever this is)
       if (cold && tr > 0.f)
-        r.base = (float)((double)r.mass * exp64((double)lift * kLn2) - ptail * ((double)total / (double)tr));
+        r.base = (float)(((double)r.mass * qt - ptail) * ((double)total / (double)tr));
       else if (!cold && ptail > 0.0)
         r.base = (float)((double)r.mass - ptail * ((double)total / (double)tr));
     }

@@ -286,3 +286,21 @@ def test_label_of_the_lowest_value(dtype, T, N):
     w = np.zeros(N, np.float32)
     w[:3] = 0.25
     check(z, ids, t, None, lab, w, T, alpha, OD.loss_and_grad(f64(z), ids, t, None, lab, w, T, alpha), dtype)
+
+
+@pytest.mark.parametrize("N,V", [(3, 5001), (600, 5001), (2, 140001)])
+@pytest.mark.parametrize("gap", [26.0, 30.0, 50.0, 52.0, 70.0])
+def test_distill_a_wide_rest_far_below(gap, N, V):
+    """Off the kept tokens, themselves e^-gap of the row, logits spread over 45: e^-45 = 2^-65 of the rest's largest share
+    is still a gradient of its own."""
+    k = 24
+    g = np.random.default_rng(6)
+    z = torch.rand(N, V, generator=torch.Generator().manual_seed(5)) * 45
+    ids = np.stack([g.permutation(V)[:k] for _ in range(N)])
+    z.scatter_(1, torch.from_numpy(ids), 45 + gap + torch.rand(N, k, generator=torch.Generator().manual_seed(6)))
+    t = (g.standard_normal((N, k)) * 2 + 6).astype(np.float32)
+    lse = (np.log(np.exp(t.astype(np.float64)).sum(1)) + g.uniform(0.01, 0.3, N)).astype(np.float32)
+    w = np.zeros(N, np.float32)
+    w[:3] = g.uniform(0.2, 1.0, min(N, 3))
+    z = z.cuda()
+    check(z, ids, t, lse, None, w, 1.0, 1.0, OD.loss_and_grad(f64(z), ids, t, lse, None, w, 1.0, 1.0), F32)
