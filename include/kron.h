@@ -375,7 +375,7 @@ kron_status_t kron_l1_penalty_grad(int64_t n, const float* S, float lam, const f
  *   x [N, p*m]   S [2, p, q] or NULL   A [2, r, p, q]   B [2, r, m, n]
  *   bias [2, q*n] or NULL              y [N, q*n]
  * act: one of KRON_ACT_*.  dtype: KRON_F32, or KRON_BF16 for x, S, A, B, bias, dy, y and dx; the
- * gradients of the factors and biases are fp32 for both.  Products leave out less than 2^-21 of
+ * gradients of the factors and biases are fp32 for both.  Products leave out less than 2^-22 of
  * each (fp32, and the bf16 gradients of the factors), intermediates of the bf16 y and dx are off by
  * at most 2^-17 each, sums are fp32 and every output is rounded once.  A non-finite x gives
  * non-finite outputs in its row.

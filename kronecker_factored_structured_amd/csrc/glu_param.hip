@@ -182,7 +182,7 @@ __device__ inline void param_body(const GluParam& a, int rowgroup, int pairgroup
         if (part >= np) break;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const u2v t = u2v{tops(u[i][0], u[i][1]), tops(u[i][2], u[i][3])};
+          const u2v t = u2v{kron::part(part, 3, u[i][0], u[i][1]), kron::part(part, 3, u[i][2], u[i][3])};
           l2[w.at + 128 * part + 8 * (i ^ w.gg)] = t;
           if (part < 2) {
             float r0 = u[i][0], r1 = u[i][1], r2 = u[i][2], r3 = u[i][3];

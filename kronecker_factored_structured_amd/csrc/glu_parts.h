@@ -2,12 +2,13 @@
 // blocks of the bf16 matrix instruction, and the kernels' arguments.
 //
 // All products run on the bf16 matrix instruction with fp32 accumulation.  A factor wider than
-// bf16 is the sum of bf16 parts.  Three take 8 bits each off the top (an fp32 value is exactly
-// three), and a product keeps the pairs of parts whose orders sum to at most two: six instructions
-// for fp32 times fp32, dropped terms below 2^-21 of the product.  The bf16 instruction has sixteen
-// times the rate of the fp32 one, so six of them are still 2.7 times faster; bf16 inputs need
-// fewer parts and keep their intermediates exact to fp32 in the backward (its parameter gradients
-// are fp32).  What a bf16 y or dX is summed from has two parts, each rounded to nearest: off by at most
+// bf16 is the sum of bf16 parts.  Of three the first is cut off the top bits (rounded, values next to fp32's
+// largest would be infinite) and the second rounded to nearest, which leaves less than 2^-7, at most 2^-16
+// of either sign, and nothing: an fp32 value is exactly three.  A product keeps the pairs of parts whose orders sum
+// to at most two: six instructions for fp32 times fp32, dropped terms below 2^-22 of the product.  The bf16
+// instruction has sixteen times the rate of the fp32 one, so six of them are still 2.7 times faster; bf16 inputs
+// need fewer parts and keep their intermediates exact to fp32 in the backward (its parameter gradients are
+// fp32).  What a bf16 y or dX is summed from has two parts, each rounded to nearest: off by at most
 // 2^-17 either way (off the top bits they left up to 2^-15, always toward zero), and products of two such
 // values keep all four terms.  A non-finite input gives non-finite outputs, and so does such an
 // intermediate within half a bf16 step of fp32's largest value.
@@ -103,19 +104,19 @@ __device__ inline void rest(uint32_t t, float& a, float& b) {
   b = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(b2, t), __builtin_bit_cast(b2, hi), b, false);
 }
 
-// Eight fp32 values (two f4) as NP bf16 operand parts: three off the top bits, fewer rounded to nearest.
-template <int NP>
-__device__ inline uint32_t part(float a, float b) {
-  return NP == 3 ? tops(a, b) : bf16_pair(a, b);
+// The s-th of `of` bf16 parts of a (low) and b (high): rounded to nearest, but the first of three cut off the top bits.
+__device__ inline uint32_t part(int s, int of, float a, float b) {
+  return s == 0 && of == 3 ? tops(a, b) : bf16_pair(a, b);
 }
+// Eight fp32 values (two f4) as NP bf16 operand parts.
 template <int NP>
 __device__ inline void split(f4 lo, f4 hi, Op* o) {
 #pragma unroll
   for (int s = 0; s < NP; ++s) {
-    o[s].u[0] = part<NP>(lo[0], lo[1]);
-    o[s].u[1] = part<NP>(lo[2], lo[3]);
-    o[s].u[2] = part<NP>(hi[0], hi[1]);
-    o[s].u[3] = part<NP>(hi[2], hi[3]);
+    o[s].u[0] = part(s, NP, lo[0], lo[1]);
+    o[s].u[1] = part(s, NP, lo[2], lo[3]);
+    o[s].u[2] = part(s, NP, hi[0], hi[1]);
+    o[s].u[3] = part(s, NP, hi[2], hi[3]);
     if (s + 1 < NP) {
       float l[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
 #pragma unroll
