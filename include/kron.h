@@ -482,6 +482,109 @@ kron_status_t kron_distill_bwd(const kron_distill_t* d, const void* logits, cons
                                const float* teacher_lse, const int64_t* labels, const float* weights,
                                const float* stats, const float* gout, void* dlogits, hipStream_t stream);
 
+/*
+ * Cross-entropy of a large vocabulary from the hidden states (kron_head_ce without its bound on the
+ * classes and without the logits in memory):
+ *   z = h W^T,  nll_n = log sum_v exp(z[n][v]) - z[n][labels[n]],  loss = sum_n w_n nll_n
+ *   h [N, K]  W [V, K] (an embedding table's layout)  labels [N] int64
+ *   weights [N] fp32 (NULL: 1 / N)   loss: one float   nll [N] fp32   stats [N, KRON_VOCAB_CE_STATS]
+ * h and W are fp32 or bf16 (dtype), and so are their gradients, for kron_vocab_ce_bwd of the same
+ * arguments, the stats that the forward gave (their layout is private) and gout (one device float):
+ *   dh [N, K] or NULL, dW [V, K] or NULL (not computed): gout[0] times the gradient of loss
+ * The backward computes the logits once more, in pieces of the vocabulary: the workspace holds the
+ * gradient of one piece in 16 bits (512 MB at most, or 256 tokens' if that is more).
+ *   - A row of weight 0 is left out whole (padding): nothing of it is read, its nll and gradient are 0.
+ *     The backward of the other rows costs what they do.
+ *   - A label outside [0, V) makes the loss, that row's nll and the gradients that it takes part in NaN
+ *     (no out-of-bounds access).  So does a row with a NaN or a +infinity among its logits.
+ *   - Sums and softmax statistics are fp32 or fp64.  fp32 operands of the products are the sum of two
+ *     fp16 parts after a scaling by a power of two: off by less than 2^-22 of the value, or 2^-50 of the
+ *     tensor's largest where that is more.  For bf16 tensors the logits' gradient is rounded to
+ *     bf16 once.  Every output is rounded once.
+ * Limits: N <= KRON_VOCAB_CE_MAX_ROWS, K <= KRON_VOCAB_CE_MAX_WIDTH, V <= KRON_VOCAB_MAX.  N == 0 is
+ * valid: loss 0, dW 0.  All arrays 16-byte aligned; workspace as for kron_linear_bwd:
+ * kron_vocab_ce_workspace_bytes(N, K, V, dtype, with_weights, backward) bytes, 0 for rejected sizes.
+ */
+#define KRON_VOCAB_CE_STATS 2
+#define KRON_VOCAB_CE_MAX_ROWS 1048576
+#define KRON_VOCAB_CE_MAX_WIDTH 16384
+size_t kron_vocab_ce_workspace_bytes(int64_t N, int32_t K, int32_t V, int32_t dtype, int32_t with_weights,
+                                     int32_t backward);
+kron_status_t kron_vocab_ce_fwd(int64_t N, int32_t K, int32_t V, int32_t dtype, const void* h, const void* W,
+                                const int64_t* labels, const float* weights, float* loss, float* nll,
+                                float* stats, void* workspace, size_t workspace_bytes, hipStream_t stream);
+kron_status_t kron_vocab_ce_bwd(int64_t N, int32_t K, int32_t V, int32_t dtype, const void* h, const void* W,
+                                const int64_t* labels, const float* weights, const float* stats,
+                                const float* gout, void* dh, void* dW, void* workspace, size_t workspace_bytes,
+                                hipStream_t stream);
+
+/*
+ * Low-rank adapters of many requests at once beside a shared projection (a Kronecker layer, or any).
+ * Request i is the rows [starts[i], starts[i+1]) of the batch, with adapter e = ids[i]:
+ *   y = base + scales[e] (x down[e]^T) up[e]^T
+ *   x [N, K]   base, y [N, M]   down [E, R, K]   up [E, M, R]   scales [E] fp32 (NULL: 1)
+ *   starts [B + 1] int32, not decreasing (NULL: B = N requests of one row)   ids [B] int32
+ * x, base, down, up, y are fp32 or bf16 (dtype).  y may be base itself.  Rows of a request with a
+ * negative id, before starts[0] and from starts[B] on have no adapter: y = base there (left as they
+ * are where y is base) and nothing of x is read.  An id >= E makes its rows NaN.  starts outside
+ * [0, N] count as the nearer bound; where they decrease, the rows concerned are unspecified.
+ *
+ * kron_adapters_bwd, for the upstream gradient dy [N, M] of y:
+ *   dx [N, K] = dx_base + scales[e] (dy up[e]) down[e], in dtype.  NULL: not computed.  dx_base [N, K]: the
+ *        projection's own dx (NULL: 0); dx may be dx_base itself
+ *   ddown [E, R, K] = sum over e's rows of scales[e] (dy up[e])^T x        (fp32)
+ *   dup   [E, M, R] = sum over e's rows of scales[e] dy^T (x down[e]^T)    (fp32)
+ * An adapter without rows has gradients 0; rows with an id >= E have dx NaN and no part in the others.
+ * All products and sums are fp32; every output is rounded once.
+ * Limits: 1 <= K, M <= 65536, 1 <= R <= KRON_ADAPTERS_MAX_RANK, 1 <= E <= 65535, N <= 2^24, B <= 2^20.
+ * All arrays 16-byte aligned but ids and starts (4).  The forward needs no workspace; the backward's is
+ * kron_adapters_workspace_bytes(N, K, M, R, E) bytes, 256-byte aligned (0 for rejected sizes).
+ */
+#define KRON_ADAPTERS_MAX_RANK 128
+typedef struct {
+  int64_t N;                 /* rows, >= 0                                  */
+  int32_t K, M, R, E, B;     /* widths, rank, adapters, requests            */
+  int32_t dtype;
+} kron_adapters_t;
+size_t kron_adapters_workspace_bytes(const kron_adapters_t* d);
+kron_status_t kron_adapters_fwd(const kron_adapters_t* d, const void* x, const void* base, const void* down,
+                                const void* up, const int32_t* ids, const int32_t* starts, const float* scales,
+                                void* y, hipStream_t stream);
+kron_status_t kron_adapters_bwd(const kron_adapters_t* d, const void* x, const void* dy, const void* down,
+                                const void* up, const int32_t* ids, const int32_t* starts, const float* scales,
+                                const void* dx_base, void* dx, float* ddown, float* dup, void* workspace,
+                                size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Orthogonalised update of matrices (Muon), beside kron_adam_l1_step for what is no matrix.  Tensor t is
+ * count[t] matrices of rows[t] x cols[t], dense one after the other (a Kronecker layer's A and B are such
+ * stacks).  For each matrix, with gradient g and momentum m:
+ *   m = momentum m + g,   u = nesterov ? g + momentum m : m,   X = u / (|u|_F + eps)
+ *   steps times, with A = X X^T (on the smaller side):  X = a X + (b A + c A^2) X
+ *   param = param (1 - lr weight_decay) - lr scale[t] X
+ * param and grad are fp32 or bf16 (dtype), m fp32.  All arguments but the device pointers in params,
+ * grads and m are read from the host.  scale may be NULL (1).  A matrix of zeros stays zero (X = 0); one with
+ * a non-finite value becomes non-finite and no other does.
+ * Sums are fp32, norms fp64.  fp32: products of matrices that do not fit a CU's LDS take their operands as two
+ * fp16 parts each (less than 2^-22 of the value, or 2^-38, of matrices whose entries are at most 1.3).
+ * bf16: as one fp16 part (2^-11).
+ * Limits: ntensors <= 4096, 1 <= rows, cols <= KRON_MUON_MAX_SIDE, count <= 2^20 (0: skipped),
+ * 1 <= steps <= KRON_MUON_MAX_STEPS, momentum >= 0, eps > 0.  Tensors must not overlap.  The workspace
+ * is kron_muon_workspace_bytes(...) bytes, 256-byte aligned (0: none is needed, or rejected sizes).
+ */
+#define KRON_MUON_MAX_SIDE 16384
+#define KRON_MUON_MAX_STEPS 16
+typedef struct {
+  double lr, momentum, weight_decay, a, b, c, eps;
+  int32_t nesterov, steps;
+} kron_muon_t;
+size_t kron_muon_workspace_bytes(int32_t ntensors, const int64_t* count, const int32_t* rows,
+                                 const int32_t* cols, int32_t dtype);
+kron_status_t kron_muon_step(const kron_muon_t* h, int32_t ntensors, int32_t dtype, void* const* params,
+                             const void* const* grads, float* const* m, const int64_t* count,
+                             const int32_t* rows, const int32_t* cols, const float* scale, void* workspace,
+                             size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -40,6 +40,13 @@ KRON_DISTILL_STATS = 8
 KRON_DISTILL_MAX_K = 256
 KRON_VOCAB_MAX = 262144
 
+KRON_VOCAB_CE_STATS = 2
+KRON_VOCAB_CE_MAX_ROWS = 1048576
+KRON_VOCAB_CE_MAX_WIDTH = 16384
+KRON_ADAPTERS_MAX_RANK = 128
+KRON_MUON_MAX_SIDE = 16384
+KRON_MUON_MAX_STEPS = 16
+
 # Every symbol include/kron.h declares.
 EXPORTS = (
     "kron_abi_version", "kron_status_str", "kron_last_error", "kron_linear_check",
@@ -51,6 +58,8 @@ EXPORTS = (
     "kron_l1_penalty_grad", "kron_linear_bwd_noalloc", "kron_linear_zcache_bytes", "kron_linear_fwd_save",
     "kron_linear_bwd_saved", "kron_topk_logits", "kron_distill_workspace_bytes", "kron_distill",
     "kron_distill_fwd", "kron_distill_bwd", "kron_glu_workspace_bytes", "kron_glu_fwd", "kron_glu_bwd",
+    "kron_vocab_ce_workspace_bytes", "kron_vocab_ce_fwd", "kron_vocab_ce_bwd", "kron_adapters_workspace_bytes",
+    "kron_adapters_fwd", "kron_adapters_bwd", "kron_muon_workspace_bytes", "kron_muon_step",
 )
 
 KRON_NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -71,6 +80,16 @@ class KronDistill(ctypes.Structure):
     _fields_ = [("N", ctypes.c_int64), ("V", ctypes.c_int32), ("k", ctypes.c_int32), ("ld", ctypes.c_int64),
                 ("ldd", ctypes.c_int64), ("dtype", ctypes.c_int32), ("flags", ctypes.c_uint32),
                 ("temperature", ctypes.c_float), ("alpha", ctypes.c_float)]
+
+
+class KronAdapters(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int64), ("K", ctypes.c_int32), ("M", ctypes.c_int32), ("R", ctypes.c_int32),
+                ("E", ctypes.c_int32), ("B", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class KronMuon(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "momentum", "weight_decay", "a", "b", "c", "eps")] + \
+               [("nesterov", ctypes.c_int32), ("steps", ctypes.c_int32)]
 
 
 class KronError(RuntimeError):
@@ -94,6 +113,8 @@ def lib() -> ctypes.CDLL:
         vp, i32, i64, u32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_size_t
         shp = ctypes.POINTER(KronShape)
         dis = ctypes.POINTER(KronDistill)
+        ada = ctypes.POINTER(KronAdapters)
+        i64p, i32p, f32p = ctypes.POINTER(i64), ctypes.POINTER(i32), ctypes.POINTER(ctypes.c_float)
         pp = ctypes.POINTER(ctypes.c_void_p)
         sig = {
             "kron_abi_version": (i32, []),
@@ -133,6 +154,14 @@ def lib() -> ctypes.CDLL:
             "kron_distill": (i32, [dis, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
             "kron_distill_fwd": (i32, [dis, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
             "kron_distill_bwd": (i32, [dis, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
+            "kron_vocab_ce_workspace_bytes": (sz, [i64, i32, i32, i32, i32, i32]),
+            "kron_vocab_ce_fwd": (i32, [i64, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+            "kron_vocab_ce_bwd": (i32, [i64, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+            "kron_adapters_workspace_bytes": (sz, [ada]),
+            "kron_adapters_fwd": (i32, [ada, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
+            "kron_adapters_bwd": (i32, [ada, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+            "kron_muon_workspace_bytes": (sz, [i32, i64p, i32p, i32p, i32]),
+            "kron_muon_step": (i32, [ctypes.POINTER(KronMuon), i32, i32, pp, pp, pp, i64p, i32p, i32p, f32p, vp, sz, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)

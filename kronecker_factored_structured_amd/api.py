@@ -14,7 +14,7 @@ import torch
 
 from . import _lib
 from ._lib import (KRON_ACCUMULATE, KRON_ACTS, KRON_BF16, KRON_DISTILL_STATS, KRON_DX_RELU_MASK, KRON_F32, KRON_IDS_I64,
-                   KRON_RELU_OUT, KRON_SPARSE_ROWS, KronDistill, KronShape, check)
+                   KRON_RELU_OUT, KRON_SPARSE_ROWS, KRON_VOCAB_CE_STATS, KronAdapters, KronDistill, KronMuon, KronShape, check)
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -717,3 +717,175 @@ def kron_distill_bwd(logits: torch.Tensor, ids: Optional[torch.Tensor], teacher:
         check("kron_distill_bwd", _lib.lib().kron_distill_bwd(ctypes.byref(d), *ptrs, _ptr(stats), _ptr(gout), _ptr(dz),
                                                               _stream(dev)))
     return dz
+
+
+def _vocab_checks(h, W, labels, weights):
+    dt = _dtype_code(h)
+    _dev(h, "h", h.dtype)
+    if h.dim() != 2 or W.dim() != 2:
+        raise ValueError("h must be N x K and W V x K")
+    N, K = h.shape
+    V = W.shape[0]
+    _need(W, "W", (V, K), h.dtype, h.device)
+    _need(labels, "labels", (N,), torch.int64, h.device)
+    _need(weights, "weights", (N,), device=h.device)
+    return dt, N, K, V
+
+
+def kron_vocab_ce_workspace_bytes(N: int, K: int, V: int, dtype: torch.dtype = torch.float32, with_weights: bool = False,
+                                  backward: bool = False) -> int:
+    dt = KRON_F32 if dtype == torch.float32 else KRON_BF16
+    return int(_lib.lib().kron_vocab_ce_workspace_bytes(N, K, V, dt, int(with_weights), int(backward)))
+
+
+def kron_vocab_ce_fwd(h: torch.Tensor, W: torch.Tensor, labels: torch.Tensor, weights: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None) -> tuple:
+    """Cross-entropy of the logits h W^T without keeping them: (loss, nll, stats) with nll[n] = logsumexp(z_n) -
+    z_n[labels[n]] (float32 [N]), loss = sum_n weights[n] nll[n] (1-element tensor; weights None: 1 / N, weight 0: the
+    row is left out) and the rows' statistics for kron_vocab_ce_bwd.  h [N, K] and W [V, K] (an embedding table) are
+    both float32 or both bfloat16."""
+    dt, N, K, V = _vocab_checks(h, W, labels, weights)
+    dev = h.device
+    loss = torch.empty(1, device=dev)
+    nll = torch.empty(N, device=dev)
+    stats = torch.empty(N, KRON_VOCAB_CE_STATS, device=dev)
+    ws = _workspace(workspace, kron_vocab_ce_workspace_bytes(N, K, V, h.dtype, weights is not None), dev)
+    with _on(dev):
+        check("kron_vocab_ce_fwd", _lib.lib().kron_vocab_ce_fwd(
+            N, K, V, dt, _ptr(h), _ptr(W), _ptr(labels), _ptr(weights), _ptr(loss), _ptr(nll), _ptr(stats), _ptr(ws),
+            ctypes.c_size_t(ws.numel()), _stream(dev)))
+    return loss, nll, stats
+
+
+def kron_vocab_ce_bwd(h: torch.Tensor, W: torch.Tensor, labels: torch.Tensor, stats: torch.Tensor, gout: torch.Tensor,
+                      weights: Optional[torch.Tensor] = None, want_dh: bool = True, want_dW: bool = True,
+                      workspace: Optional[torch.Tensor] = None, outs: Optional[dict] = None) -> dict:
+    """gout[0] times the gradients of the loss that kron_vocab_ce_fwd gave for the same arguments: dict(dh, dW) in h's
+    dtype, None where not asked."""
+    dt, N, K, V = _vocab_checks(h, W, labels, weights)
+    dev = h.device
+    _need(stats, "stats", (N, KRON_VOCAB_CE_STATS), device=dev)
+    _need(gout, "gout", (1,), device=dev)
+    o = dict(outs or {})
+    for k, size, asked in (("dh", (N, K), want_dh), ("dW", (V, K), want_dW)):
+        _need(o.get(k), k, size, h.dtype, dev)
+        if k not in o:
+            o[k] = torch.empty(size, device=dev, dtype=h.dtype) if asked else None
+    ws = _workspace(workspace, kron_vocab_ce_workspace_bytes(N, K, V, h.dtype, weights is not None, True), dev)
+    with _on(dev):
+        check("kron_vocab_ce_bwd", _lib.lib().kron_vocab_ce_bwd(
+            N, K, V, dt, _ptr(h), _ptr(W), _ptr(labels), _ptr(weights), _ptr(stats), _ptr(gout), _ptr(o["dh"]),
+            _ptr(o["dW"]), _ptr(ws), ctypes.c_size_t(ws.numel()), _stream(dev)))
+    return dict(dh=o["dh"], dW=o["dW"])
+
+
+def _adapters_args(x, wide, wide_name, down, up, ids, starts, scales):
+    """The checked sizes that both directions share; `wide` is N x M."""
+    dt = _dtype_code(x)
+    _dev(x, "x", x.dtype)
+    if x.dim() != 2 or down.dim() != 3 or up.dim() != 3:
+        raise ValueError("x must be N x K, down E x R x K and up E x M x R")
+    dev = x.device
+    N, K = x.shape
+    E, R, _ = down.shape
+    M = up.shape[1]
+    _need(down, "down", (E, R, K), x.dtype, dev)
+    _need(up, "up", (E, M, R), x.dtype, dev)
+    _need(wide, wide_name, (N, M), x.dtype, dev)
+    _need(scales, "scales", (E,), device=dev)
+    B = N if starts is None else starts.numel() - 1
+    if B < 0:
+        raise ValueError("starts must hold the requests' bounds, one more than there are requests")
+    _need(starts, "starts", (B + 1,), torch.int32, dev)
+    _need(ids, "ids", (B,), torch.int32, dev)
+    ptrs = (_ptr(down), _ptr(up), _ptr(ids), _ptr(starts), _ptr(scales))
+    return KronAdapters(N, K, M, R, E, B, dt), ptrs
+
+
+def kron_adapters_fwd(x: torch.Tensor, base: torch.Tensor, down: torch.Tensor, up: torch.Tensor, ids: torch.Tensor,
+                      starts: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
+                      out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y = base + scales[e] (x down[e]^T) up[e]^T for the rows of each request, e = ids[i] its adapter (negative: none):
+    request i is the rows starts[i] to starts[i + 1] (int32 [B + 1]; None: one row each).  x [N, K], base [N, M] (the
+    shared projection's output), down [E, R, K] and up [E, M, R] are all float32 or all bfloat16, scales [E] is float32
+    (None: 1).  out may be base itself; rows of no request and without an adapter are base's."""
+    d, ptrs = _adapters_args(x, base, "base", down, up, ids, starts, scales)
+    _need(out, "out", tuple(base.shape), x.dtype, x.device)
+    y = out if out is not None else torch.empty_like(base)
+    with _on(x.device):
+        check("kron_adapters_fwd", _lib.lib().kron_adapters_fwd(ctypes.byref(d), _ptr(x), _ptr(base), *ptrs, _ptr(y),
+                                                                _stream(x.device)))
+    return y
+
+
+def kron_adapters_bwd(x: torch.Tensor, dy: torch.Tensor, down: torch.Tensor, up: torch.Tensor, ids: torch.Tensor,
+                      starts: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
+                      dx_base: Optional[torch.Tensor] = None, want_dx: bool = True,
+                      workspace: Optional[torch.Tensor] = None, outs: Optional[dict] = None) -> dict:
+    """Gradients of sum(dy * kron_adapters_fwd(x, ...)): dict(dx in x's dtype, ddown and dup in float32).  dx_base (the
+    projection's own gradient of x) is added to dx; outs["dx"] may be dx_base itself."""
+    d, ptrs = _adapters_args(x, dy, "dy", down, up, ids, starts, scales)
+    dev = x.device
+    _need(dx_base, "dx_base", tuple(x.shape), x.dtype, dev)
+    o = dict(outs or {})
+    for k, size, dtype, asked in (("dx", x.shape, x.dtype, want_dx), ("ddown", down.shape, torch.float32, True),
+                                  ("dup", up.shape, torch.float32, True)):
+        _need(o.get(k), k, tuple(size), dtype, dev)
+        if k not in o:
+            o[k] = torch.empty(size, device=dev, dtype=dtype) if asked else None
+    L = _lib.lib()
+    ws = _workspace(workspace, int(L.kron_adapters_workspace_bytes(ctypes.byref(d))), dev)
+    with _on(dev):
+        check("kron_adapters_bwd", L.kron_adapters_bwd(
+            ctypes.byref(d), _ptr(x), _ptr(dy), *ptrs, _ptr(dx_base), _ptr(o["dx"]), _ptr(o["ddown"]), _ptr(o["dup"]),
+            _ptr(ws), ctypes.c_size_t(ws.numel()), _stream(dev)))
+    return dict(dx=o["dx"], ddown=o["ddown"], dup=o["dup"])
+
+
+MUON_COEFFS = (3.4445, -4.7750, 2.0315)
+
+
+def kron_muon_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], m: Sequence[torch.Tensor], lr: float,
+                   momentum: float = 0.95, nesterov: bool = True, weight_decay: float = 0.0,
+                   scales: Optional[Sequence[float]] = None, steps: int = 5, coeffs: tuple = MUON_COEFFS,
+                   eps: float = 1e-7, workspace: Optional[torch.Tensor] = None) -> None:
+    """One orthogonalised (Muon) update of every tensor, in place: the last two dimensions of a tensor are matrices, each
+    on its own.  m = momentum m + g; u = g + momentum m (nesterov) or m; u / (|u|_F + eps) goes through `steps`
+    Newton-Schulz steps of the quintic `coeffs`; param = param (1 - lr weight_decay) - lr scales[t] u.  params and grads
+    are all float32 or all bfloat16, m float32.  scales None: sqrt(max(1, rows / cols)) of each tensor."""
+    nt = len(params)
+    if not (len(grads) == len(m) == nt) or (scales is not None and len(scales) != nt):
+        raise ValueError("params, grads, m (and scales) must have the same length")
+    if nt == 0:
+        return
+    dev, dtype = params[0].device, params[0].dtype
+    dt = _dtype_code(params[0])
+    count, rows, cols = [], [], []
+    for i in range(nt):
+        p = params[i]
+        _dev(p, f"param[{i}]", dtype)
+        if p.device != dev:
+            raise ValueError(f"param[{i}] is on {p.device}, expected {dev}")
+        if p.dim() < 2:
+            raise ValueError(f"param[{i}] must hold matrices, got {tuple(p.shape)}")
+        _need(grads[i], f"grad[{i}]", tuple(p.shape), dtype, dev)
+        _need(m[i], f"m[{i}]", tuple(p.shape), torch.float32, dev)
+        r, c = p.shape[-2:]
+        n = p.numel()
+        count.append(n // (r * c) if n else 0)
+        rows.append(max(r, 1))
+        cols.append(max(c, 1))
+    if scales is None:
+        scales = [max(1.0, r / c) ** 0.5 for r, c in zip(rows, cols)]
+    arr = ctypes.c_void_p * nt
+    ptrs = [arr(*[t.data_ptr() for t in ts]) for ts in (params, grads, m)]
+    sizes = ((ctypes.c_int64 * nt)(*count), (ctypes.c_int32 * nt)(*rows), (ctypes.c_int32 * nt)(*cols))
+    L = _lib.lib()
+    need = int(L.kron_muon_workspace_bytes(nt, *sizes, dt))
+    ws = _workspace(workspace, need, dev) if need else None
+    h = KronMuon(float(lr), float(momentum), float(weight_decay), *(float(v) for v in coeffs), float(eps), int(bool(nesterov)),
+                 int(steps))
+    with _on(dev):
+        check("kron_muon_step", L.kron_muon_step(
+            ctypes.byref(h), nt, dt, *ptrs, *sizes, (ctypes.c_float * nt)(*scales), _ptr(ws),
+            ctypes.c_size_t(ws.numel() if ws is not None else 0), _stream(dev)))

@@ -53,6 +53,9 @@ OBJECTS = [
     ("glu_param.hip", ["-DKRON_GLU_TYPE=2", *VGPR_MFMA], "glu_param2"),
     ("distill.hip", [], "distill"),
     ("topk_logits.hip", [], "topk_logits"),
+    ("vocab_ce.hip", [], "vocab_ce"),
+    ("muon.hip", [], "muon"),
+    ("adapters.hip", [], "adapters"),
 ]
 SOURCES = sorted({src for src, _, _ in OBJECTS})
 

@@ -1,11 +1,14 @@
 // C ABI of libkron: argument validation (host only, before any HIP call), launch
 // planning and dispatch to the kernels.  See include/kron.h for the contract.
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
 #include <string>
+#include <utility>
+#include <vector>
 
 #include "kron_internal.h"
 
@@ -1063,6 +1066,243 @@ kron_status_t kron_distill_bwd(const kron_distill_t* d, const void* logits, cons
                                const float* stats, const float* gout, void* dlogits, hipStream_t stream) {
   return distill_run(d, 2, logits, ids, teacher, teacher_lse, labels, weights, nullptr, const_cast<float*>(stats),
                      gout, dlogits, nullptr, 0, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+kron_status_t vocab_check(int64_t N, int32_t K, int32_t V, int32_t dtype) {
+  if (N < 0) return fail(KRON_E_SHAPE, "N = %lld out of range", (long long)N);
+  if (K < 1 || V < 1) return fail(KRON_E_SHAPE, "K = %d and V = %d must be >= 1", K, V);
+  if (N > KRON_VOCAB_CE_MAX_ROWS || K > KRON_VOCAB_CE_MAX_WIDTH || V > KRON_VOCAB_MAX)
+    return fail(KRON_E_UNSUPPORTED, "N = %lld, K = %d, V = %d beyond the limits (%d, %d, %d)", (long long)N, K, V,
+                KRON_VOCAB_CE_MAX_ROWS, KRON_VOCAB_CE_MAX_WIDTH, KRON_VOCAB_MAX);
+  if (dtype != KRON_F32 && dtype != KRON_BF16) return fail(KRON_E_DTYPE, "dtype %d", dtype);
+  return KRON_OK;
+}
+
+kron_status_t vocab_run(bool backward, int64_t N, int32_t K, int32_t V, int32_t dtype, const void* h, const void* W,
+                        const int64_t* labels, const float* weights, float* loss, float* nll, float* stats,
+                        const float* gout, void* dh, void* dW, void* workspace, size_t workspace_bytes,
+                        hipStream_t stream) {
+  kron_status_t st = vocab_check(N, K, V, dtype);
+  if (st != KRON_OK) return st;
+  if (!W) return fail(KRON_E_NULL, "W is required");
+  if (N > 0 && (!h || !labels || !stats || (!backward && !nll)))
+    return fail(KRON_E_NULL, "h, labels, nll and stats are required when N > 0");
+  if (!backward && !loss) return fail(KRON_E_NULL, "loss is required");
+  if (backward && !gout) return fail(KRON_E_NULL, "gout is required");
+  const size_t need = kron_vocab_ce_workspace_bytes(N, K, V, dtype, weights != nullptr, backward);
+  if ((st = glu_workspace_check(workspace, workspace_bytes, need)) != KRON_OK) return st;
+  const size_t es = dtype == KRON_F32 ? 4 : 2, n = (size_t)N;
+  const size_t hb = n * K * es, wb = (size_t)V * K * es, sb = n * KRON_VOCAB_CE_STATS * 4;
+  const Range ins[6] = {{h, hb, "h"}, {W, wb, "W"}, {labels, n * 8, "labels"}, {weights, n * 4, "weights"},
+                        {backward ? stats : nullptr, sb, "stats"}, {gout, 4, "gout"}};
+  const Range outs[6] = {{loss, 4, "loss"}, {nll, n * 4, "nll"}, {backward ? nullptr : stats, sb, "stats"},
+                         {dh, hb, "dh"}, {dW, wb, "dW"}, {workspace, need, "workspace"}};
+  if ((st = check_align(ins, 6)) != KRON_OK || (st = check_align(outs, 6)) != KRON_OK) return st;
+  if ((st = check_alias(outs, 6, ins, 6)) != KRON_OK) return st;
+  if (backward && !dh && !dW) return ok();
+  kron::VocabCE a{};
+  a.N = N; a.K = K; a.V = V;
+  a.h = h; a.W = W; a.labels = labels; a.weights = weights; a.mean = N > 0 ? (float)(1.0 / (double)N) : 0.f;
+  a.loss = loss; a.nll = nll; a.stats = backward ? nullptr : stats; a.stats_in = stats; a.gout = gout;
+  a.dh = dh; a.dW = dW;
+  const hipError_t e = kron::launch_vocab_ce(a, dtype == KRON_BF16, backward, workspace, stream);
+  if (e != hipSuccess) return hip_fail(e, "kron_vocab_ce launch");
+  return ok();
+}
+
+kron_status_t adapters_check(const kron_adapters_t* d) {
+  if (!d) return fail(KRON_E_NULL, "the adapters' sizes are NULL");
+  if (d->N < 0 || d->B < 0) return fail(KRON_E_SHAPE, "N = %lld and B = %d must be >= 0", (long long)d->N, d->B);
+  if (d->K < 1 || d->M < 1 || d->R < 1 || d->E < 1)
+    return fail(KRON_E_SHAPE, "K = %d, M = %d, R = %d, E = %d must be >= 1", d->K, d->M, d->R, d->E);
+  if (d->N > (int64_t(1) << 24) || d->B > (1 << 20) || d->K > kMaxFeatures || d->M > kMaxFeatures ||
+      d->R > KRON_ADAPTERS_MAX_RANK || d->E > 65535)
+    return fail(KRON_E_UNSUPPORTED, "N = %lld, B = %d, K = %d, M = %d, R = %d, E = %d beyond the limits", (long long)d->N,
+                d->B, d->K, d->M, d->R, d->E);
+  if (d->dtype != KRON_F32 && d->dtype != KRON_BF16) return fail(KRON_E_DTYPE, "dtype %d", d->dtype);
+  return KRON_OK;
+}
+
+kron::Adapters adapters_args(const kron_adapters_t* d) {
+  kron::Adapters a{};
+  a.N = d->N; a.K = d->K; a.M = d->M; a.R = d->R; a.E = d->E; a.B = d->B;
+  a.bf16 = d->dtype == KRON_BF16;
+  return a;
+}
+
+kron_status_t adapters_tables(const kron_adapters_t* d, const int32_t* ids, const int32_t* starts) {
+  if (d->N > 0 && !ids) return fail(KRON_E_NULL, "ids is required");
+  if (!starts && d->B != d->N) return fail(KRON_E_SHAPE, "B = %d requests of one row each, but N = %lld", d->B, (long long)d->N);
+  if ((((uintptr_t)ids | (uintptr_t)starts) & 3u) != 0) return fail(KRON_E_ALIGN, "ids or starts is not aligned to its elements");
+  return KRON_OK;
+}
+
+bool muon_sizes(int32_t n, const int64_t* count, const int32_t* rows, const int32_t* cols, int32_t dtype, kron_status_t& st) {
+  st = KRON_OK;
+  if (n < 0 || n > 4096) st = fail(KRON_E_ARG, "ntensors = %d out of range", n);
+  else if (dtype != KRON_F32 && dtype != KRON_BF16) st = fail(KRON_E_DTYPE, "dtype %d", dtype);
+  else if (n > 0 && (!count || !rows || !cols)) st = fail(KRON_E_NULL, "count, rows and cols are required");
+  for (int32_t t = 0; t < n && st == KRON_OK; ++t) {
+    if (count[t] < 0 || rows[t] < 1 || cols[t] < 1)
+      st = fail(KRON_E_SHAPE, "tensor %d: %lld matrices of %d x %d", t, (long long)count[t], rows[t], cols[t]);
+    else if (count[t] > (1 << 20) || rows[t] > KRON_MUON_MAX_SIDE || cols[t] > KRON_MUON_MAX_SIDE)
+      st = fail(KRON_E_UNSUPPORTED, "tensor %d: %lld matrices of %d x %d beyond the limits (2^20, %d)", t, (long long)count[t],
+                rows[t], cols[t], KRON_MUON_MAX_SIDE);
+  }
+  return st == KRON_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t kron_vocab_ce_workspace_bytes(int64_t N, int32_t K, int32_t V, int32_t dtype, int32_t with_weights,
+                                     int32_t backward) {
+  if (vocab_check(N, K, V, dtype) != KRON_OK) return 0;
+  return kron::vocab_ce_workspace(N, K, V, dtype == KRON_BF16, with_weights != 0, backward != 0);
+}
+
+kron_status_t kron_vocab_ce_fwd(int64_t N, int32_t K, int32_t V, int32_t dtype, const void* h, const void* W,
+                                const int64_t* labels, const float* weights, float* loss, float* nll, float* stats,
+                                void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  return vocab_run(false, N, K, V, dtype, h, W, labels, weights, loss, nll, stats, nullptr, nullptr, nullptr, workspace,
+                   workspace_bytes, stream);
+}
+
+kron_status_t kron_vocab_ce_bwd(int64_t N, int32_t K, int32_t V, int32_t dtype, const void* h, const void* W,
+                                const int64_t* labels, const float* weights, const float* stats, const float* gout,
+                                void* dh, void* dW, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  return vocab_run(true, N, K, V, dtype, h, W, labels, weights, nullptr, nullptr, const_cast<float*>(stats), gout, dh, dW,
+                   workspace, workspace_bytes, stream);
+}
+
+size_t kron_adapters_workspace_bytes(const kron_adapters_t* d) {
+  if (adapters_check(d) != KRON_OK) return 0;
+  return (kron::adapters_workspace(adapters_args(d), true) + 255) & ~size_t(255);
+}
+
+kron_status_t kron_adapters_fwd(const kron_adapters_t* d, const void* x, const void* base, const void* down,
+                                const void* up, const int32_t* ids, const int32_t* starts, const float* scales, void* y,
+                                hipStream_t stream) {
+  kron_status_t st = adapters_check(d);
+  if (st != KRON_OK || (st = adapters_tables(d, ids, starts)) != KRON_OK) return st;
+  if (!down || !up || (d->N > 0 && (!x || !base || !y))) return fail(KRON_E_NULL, "x, base, down, up and y are required");
+  const size_t es = d->dtype == KRON_F32 ? 4 : 2, n = (size_t)d->N, er = (size_t)d->E * d->R;
+  const Range ins[5] = {{x, n * d->K * es, "x"}, {base, n * d->M * es, "base"}, {down, er * d->K * es, "down"},
+                        {up, er * d->M * es, "up"}, {scales, (size_t)d->E * 4, "scales"}};
+  const Range tables[2] = {{ids, (size_t)d->B * 4, "ids"}, {starts, ((size_t)d->B + 1) * 4, "starts"}};
+  const Range outs[1] = {{y, n * d->M * es, "y"}};
+  if ((st = check_align(ins, 5)) != KRON_OK || (st = check_align(outs, 1)) != KRON_OK) return st;
+  for (int i = 0; i < 5; ++i)
+    if (!(i == 1 && y == base) && (st = check_alias(outs, 1, ins + i, 1)) != KRON_OK) return st;
+  if ((st = check_alias(outs, 1, tables, 2)) != KRON_OK) return st;
+  if (d->N == 0) return ok();
+  kron::Adapters a = adapters_args(d);
+  a.x = x; a.base = base; a.down = down; a.up = up; a.ids = ids; a.starts = starts; a.scales = scales; a.y = y;
+  const hipError_t e = kron::launch_adapters(a, false, nullptr, stream);
+  if (e != hipSuccess) return hip_fail(e, "kron_adapters_fwd launch");
+  return ok();
+}
+
+kron_status_t kron_adapters_bwd(const kron_adapters_t* d, const void* x, const void* dy, const void* down,
+                                const void* up, const int32_t* ids, const int32_t* starts, const float* scales,
+                                const void* dx_base, void* dx, float* ddown, float* dup, void* workspace,
+                                size_t workspace_bytes, hipStream_t stream) {
+  kron_status_t st = adapters_check(d);
+  if (st != KRON_OK || (st = adapters_tables(d, ids, starts)) != KRON_OK) return st;
+  if (!down || !up || !ddown || !dup || (d->N > 0 && (!x || !dy)))
+    return fail(KRON_E_NULL, "x, dy, down, up, ddown and dup are required");
+  if (dx_base && !dx) return fail(KRON_E_NULL, "dx is required with dx_base");
+  const size_t need = kron_adapters_workspace_bytes(d);
+  if ((st = glu_workspace_check(workspace, workspace_bytes, need)) != KRON_OK) return st;
+  const size_t es = d->dtype == KRON_F32 ? 4 : 2, n = (size_t)d->N, er = (size_t)d->E * d->R;
+  const Range ins[8] = {{x, n * d->K * es, "x"}, {dy, n * d->M * es, "dy"}, {down, er * d->K * es, "down"},
+                        {up, er * d->M * es, "up"}, {scales, (size_t)d->E * 4, "scales"},
+                        {ids, (size_t)d->B * 4, "ids"}, {starts, ((size_t)d->B + 1) * 4, "starts"},
+                        {dx_base == dx ? nullptr : dx_base, n * d->K * es, "dx_base"}};
+  const Range outs[4] = {{dx, n * d->K * es, "dx"}, {ddown, er * d->K * 4, "ddown"}, {dup, er * d->M * 4, "dup"},
+                         {workspace, need, "workspace"}};
+  if ((st = check_align(ins, 5)) != KRON_OK || (st = check_align(ins + 7, 1)) != KRON_OK || (st = check_align(outs, 4)) != KRON_OK)
+    return st;
+  if ((st = check_alias(outs, 4, ins, 8)) != KRON_OK) return st;
+  kron::Adapters a = adapters_args(d);
+  a.x = x; a.dy = dy; a.base = dx_base; a.down = down; a.up = up; a.ids = ids; a.starts = starts; a.scales = scales;
+  a.y = d->N > 0 ? dx : nullptr; a.ddown = ddown; a.dup = dup;
+  const hipError_t e = kron::launch_adapters(a, true, workspace, stream);
+  if (e != hipSuccess) return hip_fail(e, "kron_adapters_bwd launch");
+  return ok();
+}
+
+size_t kron_muon_workspace_bytes(int32_t ntensors, const int64_t* count, const int32_t* rows, const int32_t* cols,
+                                 int32_t dtype) {
+  kron_status_t st;
+  if (!muon_sizes(ntensors, count, rows, cols, dtype, st)) return 0;
+  try {
+    std::vector<kron::MuonTensor> t((size_t)ntensors);
+    for (int32_t i = 0; i < ntensors; ++i) t[i].count = count[i], t[i].rows = rows[i], t[i].cols = cols[i];
+    return (kron::muon_workspace(t.data(), ntensors, dtype == KRON_BF16) + 255) & ~size_t(255);
+  } catch (...) {
+    return 0;
+  }
+}
+
+kron_status_t kron_muon_step(const kron_muon_t* h, int32_t ntensors, int32_t dtype, void* const* params,
+                             const void* const* grads, float* const* m, const int64_t* count, const int32_t* rows,
+                             const int32_t* cols, const float* scale, void* workspace, size_t workspace_bytes,
+                             hipStream_t stream) {
+  kron_status_t st;
+  if (!h) return fail(KRON_E_NULL, "the hyper-parameters are NULL");
+  if (!muon_sizes(ntensors, count, rows, cols, dtype, st)) return st;
+  if (!std::isfinite(h->lr) || !(h->momentum >= 0.0) || !std::isfinite(h->momentum) || !std::isfinite(h->weight_decay) ||
+      !std::isfinite(h->a) || !std::isfinite(h->b) || !std::isfinite(h->c) || !(h->eps > 0.0) || h->steps < 1 ||
+      h->steps > KRON_MUON_MAX_STEPS)
+    return fail(KRON_E_ARG, "hyper-parameters out of range");
+  if (ntensors == 0) return ok();
+  if (!params || !grads || !m) return fail(KRON_E_NULL, "pointer arrays are required");
+  try {
+    std::vector<kron::MuonTensor> t((size_t)ntensors);
+    std::vector<std::pair<Range, bool>> all;      // what is touched, and whether it is written
+    const size_t es = dtype == KRON_F32 ? 4 : 2;
+    for (int32_t i = 0; i < ntensors; ++i) {
+      t[i] = kron::MuonTensor{params[i], grads[i], m[i], count[i], rows[i], cols[i], scale ? scale[i] : 1.f};
+      if (count[i] == 0) continue;
+      if (!params[i] || !grads[i] || !m[i]) return fail(KRON_E_NULL, "tensor %d has a NULL pointer", i);
+      const size_t n = (size_t)count[i] * rows[i] * cols[i];
+      const Range rs[3] = {{params[i], n * es, "param"}, {grads[i], n * es, "grad"}, {m[i], n * 4, "m"}};
+      if ((st = check_align(rs, 3)) != KRON_OK) return st;
+      for (int k = 0; k < 3; ++k) all.push_back({rs[k], k != 1});
+    }
+    const size_t need = kron_muon_workspace_bytes(ntensors, count, rows, cols, dtype);
+    if (need > 0) {
+      if ((st = glu_workspace_check(workspace, workspace_bytes, need)) != KRON_OK) return st;
+      all.push_back({{workspace, need, "workspace"}, true});
+    }
+    std::sort(all.begin(), all.end(), [](const auto& a, const auto& b) { return (uintptr_t)a.first.p < (uintptr_t)b.first.p; });
+    // sorted by address: a range that something written overlaps starts before an earlier one's end
+    size_t last = 0, wrote = 0;      // the ranges so far that reach furthest, of all and of the written ones
+    bool any = false;
+    auto end = [&](size_t i) { return (uintptr_t)all[i].first.p + all[i].first.bytes; };
+    for (size_t i = 0; i < all.size(); ++i) {
+      const uintptr_t at = (uintptr_t)all[i].first.p;
+      const size_t with = i > 0 && all[i].second && at < end(last) ? last : any && at < end(wrote) ? wrote : i;
+      if (with != i) return fail(KRON_E_ALIAS, "a %s overlaps a %s", all[i].first.name, all[with].first.name);
+      if (i == 0 || end(i) > end(last)) last = i;
+      if (all[i].second && (!any || end(i) > end(wrote))) wrote = i, any = true;
+    }
+    kron::MuonHyper hp{};
+    hp.lr = (float)h->lr; hp.mu = (float)h->momentum; hp.keep = (float)(1.0 - h->lr * h->weight_decay);
+    hp.a = (float)h->a; hp.b = (float)h->b; hp.c = (float)h->c; hp.eps = (float)h->eps;
+    hp.nesterov = h->nesterov != 0; hp.steps = h->steps; hp.bf16 = dtype == KRON_BF16;
+    const hipError_t e = kron::launch_muon(t.data(), ntensors, hp, workspace, stream);
+    if (e != hipSuccess) return hip_fail(e, "kron_muon_step launch");
+  } catch (...) {
+    return fail(KRON_E_ARG, "out of host memory");
+  }
+  return ok();
 }
 
 }  // extern "C"

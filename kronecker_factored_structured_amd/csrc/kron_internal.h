@@ -337,4 +337,81 @@ struct TopkArgs {
 };
 hipError_t launch_topk(TopkArgs a, hipStream_t s);
 
+// ---------------------------------------------------------------------------------
+// Cross-entropy of a large vocabulary from the hidden states (vocab_ce.hip).
+// ---------------------------------------------------------------------------------
+struct VocabScales;
+struct VocabCE {
+  int64_t N;
+  int32_t K, V;
+  const void* h;
+  const void* W;
+  const int64_t* labels;
+  const float* weights;       // NULL: `mean` each
+  float mean;
+  float* loss;
+  float* nll;
+  float* stats;
+  const float* stats_in;      // backward
+  const float* gout;
+  void* dh;                   // NULL: not computed
+  void* dW;                   // NULL: not computed
+  // set by launch_vocab_ce: K rounded up, the operands, and the workspace
+  int32_t Kp;
+  VocabScales* sc;            // NULL: every row in use, nothing scaled
+  int* idx;                   // rows in use (NULL: all)
+  int* pos;                   // a row's place among them
+  uint16_t* hp;
+  uint16_t* wp;
+  int64_t hplane, wplane, dzplane;
+  float* part;                // tiles x N: maximum and sum
+  float* zlab;                // N logits of the labels
+  uint16_t* dz;
+  float* dhpart;
+};
+size_t vocab_ce_workspace(int64_t N, int K, int V, bool bf, bool weights, bool backward);
+hipError_t launch_vocab_ce(const VocabCE& k, bool bf, bool backward, void* ws, hipStream_t s);
+
+// ---------------------------------------------------------------------------------
+// Orthogonalised update (muon.hip).
+// ---------------------------------------------------------------------------------
+struct MuonTensor {
+  void* p;
+  const void* g;
+  float* m;
+  int64_t count;              // matrices
+  int32_t rows, cols;
+  float scale;
+};
+struct MuonHyper {
+  float lr, mu, keep;         // keep = 1 - lr * weight decay
+  float a, b, c, eps;
+  int32_t nesterov, steps, bf16;
+};
+size_t muon_workspace(const MuonTensor* t, int n, bool bf16);
+hipError_t launch_muon(const MuonTensor* t, int n, const MuonHyper& h, void* ws, hipStream_t s);
+
+// ---------------------------------------------------------------------------------
+// Low-rank adapters of many requests (adapters.hip).
+// ---------------------------------------------------------------------------------
+struct Adapters {
+  int64_t N;                  // rows
+  int32_t K, M, R, E, B;      // B requests
+  int32_t bf16;
+  const void* x;              // N x K
+  const void* dy;             // N x M (backward)
+  const void* base;           // N x M (forward) or N x K (backward, may be NULL)
+  const void* down;           // E x R x K
+  const void* up;             // E x M x R
+  const int32_t* ids;         // B
+  const int32_t* starts;      // B + 1, or NULL: request i is row i
+  const float* scales;        // E, or NULL: 1
+  void* y;                    // N x M (forward) or N x K (backward: dx, may be NULL)
+  float* ddown;
+  float* dup;
+  float* ws;
+};
+size_t adapters_workspace(const Adapters& a, bool backward);
+hipError_t launch_adapters(const Adapters& a, bool backward, void* ws, hipStream_t s);
+
 }  // namespace kron

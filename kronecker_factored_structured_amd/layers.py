@@ -1,6 +1,6 @@
-"""torch modules over libkron: the Kronecker-factored layer, its gated form, the Kronecker-sparse
-layer, the distillation loss and the tutorial's MLP training step.  Marshalling only; every step
-runs in libkron.
+"""torch modules over libkron: the Kronecker-factored layer, its gated form, adapters beside a
+projection, the Kronecker-sparse layer, the losses over a vocabulary and the tutorial's MLP training
+step.  Marshalling only; every step runs in libkron.
 """
 from __future__ import annotations
 
@@ -12,7 +12,7 @@ from torch import nn
 from torch.autograd.function import once_differentiable
 
 from . import api
-from ._lib import KRON_GLU_MAX_RANK, KRON_GLU_MAX_SIDE
+from ._lib import KRON_ADAPTERS_MAX_RANK, KRON_GLU_MAX_RANK, KRON_GLU_MAX_SIDE
 
 
 class _KronLinearFn(torch.autograd.Function):
@@ -192,6 +192,87 @@ class KronDistillLoss(nn.Module):
         return _KronDistillFn.apply(rows(logits, 1), *other, self.temperature, self.alpha)
 
 
+class _KronVocabCEFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, h, W, labels, weights):
+        ctx.type = W.dtype
+        w = _whole(W if W.dtype == h.dtype or h.dtype != torch.bfloat16 else W.to(h.dtype))
+        loss, _, stats = api.kron_vocab_ce_fwd(h, w, labels, weights)
+        ctx.save_for_backward(h, w, labels, weights, stats)
+        return loss.view(())
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, gout):
+        h, W, labels, weights, stats = ctx.saved_tensors
+        g = api.kron_vocab_ce_bwd(h, W, labels, stats, _whole(gout.reshape(1)), weights,
+                                  want_dh=ctx.needs_input_grad[0], want_dW=ctx.needs_input_grad[1])
+        return g["dh"], None if g["dW"] is None else g["dW"].to(ctx.type), None, None
+
+
+class KronVocabCE(nn.Module):
+    """The cross-entropy of the logits h W^T on labels, without the logits in memory: sum_n weights[n] nll[n]
+    (weights None: the mean over the rows; weight 0: a padded position, or one of a prompt).  h [..., K], W [V, K]
+    (an embedding table; a float32 one with bfloat16 h is rounded to bfloat16), labels and weights [...].  The
+    backward computes the logits once more."""
+
+    def forward(self, h, W, labels, weights=None):
+        rows = _whole(h.reshape(-1, h.shape[-1]))
+        labels = _whole(labels.reshape(-1))
+        return _KronVocabCEFn.apply(rows, W, labels, None if weights is None else _whole(weights.reshape(-1)))
+
+
+class _KronAdaptersFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, base, down, up, ids, starts, scales):
+        ctx.types = (down.dtype, up.dtype)
+        d, u = (_whole(t.to(x.dtype)) for t in (down, up))
+        ctx.save_for_backward(x, d, u, ids, starts, scales)
+        return api.kron_adapters_fwd(x, base, d, u, ids, starts, scales)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, down, up, ids, starts, scales = ctx.saved_tensors
+        dy = _whole(dy)
+        dx = None
+        dd = du = None
+        if any(ctx.needs_input_grad[i] for i in (0, 2, 3)):
+            g = api.kron_adapters_bwd(x, dy, down, up, ids, starts, scales, want_dx=ctx.needs_input_grad[0])
+            dx, dd, du = g["dx"], g["ddown"].to(ctx.types[0]), g["dup"].to(ctx.types[1])
+        return dx, dy if ctx.needs_input_grad[1] else None, dd, du, None, None, None
+
+
+class KronAdapters(nn.Module):
+    """Low-rank adapters beside a projection (a KronLinear, or any module of rows): y = projection(x) + scale (x
+    down[e]^T) up[e]^T, for each request with its own adapter e.  down ~ randn / sqrt(in), up zeros, scale = alpha /
+    rank (alpha None: rank).  forward(x, ids, starts): x [N, in] (or [..., in] without ids: adapter 0 everywhere), request
+    i the rows starts[i] to starts[i + 1] (int32; None: one row each) with adapter ids[i] (int32, negative: none).
+    down and up are rounded to x's type for the products; their gradients are computed in float32."""
+
+    def __init__(self, projection: nn.Module, in_features: int, out_features: int, rank: int, adapters: int = 1,
+                 alpha: Optional[float] = None, device=None, dtype=None):
+        super().__init__()
+        if not 1 <= rank <= KRON_ADAPTERS_MAX_RANK:
+            raise ValueError(f"rank must be in 1..{KRON_ADAPTERS_MAX_RANK}, got {rank}")
+        kw = dict(device=device, dtype=dtype)
+        self.projection = projection
+        self.down = nn.Parameter(torch.randn(adapters, rank, in_features, **kw) / math.sqrt(in_features))
+        self.up = nn.Parameter(torch.zeros(adapters, out_features, rank, **kw))
+        scale = 1.0 if alpha is None else alpha / rank
+        self.register_buffer("scales", torch.full((adapters,), scale, device=device, dtype=torch.float32))
+
+    def forward(self, x, ids=None, starts=None):
+        base = self.projection(x)
+        rows, wide = _whole(x.reshape(-1, x.shape[-1])), _whole(base.reshape(-1, base.shape[-1]))
+        if ids is None:
+            if starts is not None:
+                raise ValueError("starts needs ids")
+            ids = torch.zeros(1, dtype=torch.int32, device=x.device)
+            starts = torch.arange(2, dtype=torch.int32, device=x.device) * rows.shape[0]
+        return _KronAdaptersFn.apply(rows, wide, self.down, self.up, ids, starts, self.scales).view(base.shape)
+
+
 class KSLinear(nn.Module):
     """Y = X K with K Kronecker-sparse of support I_a (x) 1_{b x c} (x) I_d ("Fast Inference
     with Kronecker-Sparse Matrices"); values a x d x b x c ~ N(0, 1/b).  Forward only."""
@@ -215,10 +296,19 @@ class KronMLPStep:
     Parameters live in flat lists of device tensors in the order
     S1, A1, B1, bias1, S2, A2, B2, bias2, head_w (hidden x classes), head_b.
     One step is 10 kernel launches plus the column reductions, independent of r.
+
+    optimizer "muon": the factors A and B (matrices of p x q and m x n) take an orthogonalised update
+    of rate muon_lr and momentum beta1 instead of Adam's, everything else Adam's.
     """
 
+    MUON = (1, 2, 5, 6)      # A1, B1, A2, B2
+
     def __init__(self, layers, head_w, head_b, lam: float, lr: float, device,
-                 beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8):
+                 beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8, optimizer: str = "adam",
+                 muon_lr: float = 0.02):
+        if optimizer not in ("adam", "muon"):
+            raise ValueError(f"optimizer must be adam or muon, got {optimizer!r}")
+
         def t(a):
             return torch.as_tensor(a, dtype=torch.float32, device=device).contiguous()
         self.params = []
@@ -230,6 +320,7 @@ class KronMLPStep:
         self.l1 = [lam, 0.0, 0.0, 0.0, lam, 0.0, 0.0, 0.0, 0.0, 0.0]
         self.lam, self.lr = lam, lr
         self.beta1, self.beta2, self.eps = beta1, beta2, eps
+        self.optimizer, self.muon_lr = optimizer, muon_lr
         self.step_count = 0
         self.device = device
         self._ws = {}
@@ -264,6 +355,11 @@ class KronMLPStep:
         """One full training step; returns the loss (cross-entropy + l1 penalty, device tensor)."""
         loss, grads, _ = self.grads(x, labels)
         self.step_count += 1
-        api.kron_adam_l1_step(self.params, grads, self.m, self.v, self.step_count, self.lr,
-                              self.beta1, self.beta2, self.eps, l1=self.l1)
+        rest = range(len(self.params))
+        if self.optimizer == "muon":
+            api.kron_muon_step(*([ts[i] for i in self.MUON] for ts in (self.params, grads, self.m)), lr=self.muon_lr,
+                               momentum=self.beta1)
+            rest = [i for i in rest if i not in self.MUON]
+        api.kron_adam_l1_step(*([ts[i] for i in rest] for ts in (self.params, grads, self.m, self.v)), self.step_count,
+                              self.lr, self.beta1, self.beta2, self.eps, l1=[self.l1[i] for i in rest])
         return loss
