@@ -19,10 +19,13 @@ What it computes, and the passage each function follows:
                  layers, ReLU, a dense 10-way head, cross-entropy plus the penalty,
                  backward and Adam (tutorial, "Setup").
 
+  * vocab_ce.py, adapters.py, muon.py -- the cross-entropy of a large vocabulary, low-rank
+                 adapters and the orthogonalised update, from their definitions.
+
 Everything is computed in float64 from the exact fp32 (or bf16) input values.
 Pins: every function is checked against facts fixed outside this package (closed
 forms, textbook identities, library routines, finite differences, printed
 quantities); see tests/test_oracle_*.py.  No function here is "parity unpinned".
 """
 
-from . import kron, ks, optim, mlp  # noqa: F401
+from . import adapters, kron, ks, muon, optim, mlp, vocab_ce  # noqa: F401
