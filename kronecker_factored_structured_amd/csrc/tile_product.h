@@ -40,22 +40,25 @@ __device__ inline f4 mma(u4 a, u4 b, f4 c) {
 
 typedef __attribute__((address_space(3))) char lds_t;
 
-constexpr int kBK = 64;      // contraction of a step
+constexpr int kBK = 64;      // contraction of a step: rows of 128 bytes, whole cache lines
 
 // ROW: the contraction runs along the operand's rows; COL: over its rows (read transposed from LDS).
 enum Side { ROW, COL };
 
-// One operand's tile of R rows (ROW) or columns (COL) x kBK, NW wavefronts loading it.
+// One operand's tile of R rows (ROW) or columns (COL) x kBK, loaded straight into LDS by NW wavefronts, a KB a load: eight
+// rows of 128 bytes (64 of the contraction; COL: 64 columns, the tile is R / 64 such blocks of kBK rows).  The 16-byte
+// pieces of a row are permuted, by the address that each lane loads from, so that fragment() reads without bank conflicts:
+// a ROW read is served eight lanes (rows) at a time, a COL read 32 lanes: 32 bytes of each of eight rows 0..3, 8..11.
 template <Side SD, int R, int NW>
 struct TileLoad {
   static constexpr int kLoads = R * kBK * 2 / 1024 / NW;      // 1 KB wave loads of each wavefront
-  static_assert(kLoads * NW * 1024 == R * kBK * 2, "");
-  static constexpr int kPer = SD == ROW ? 8 : 512 / R;        // rows of one wave load
+  static_assert(kLoads * NW * 1024 == R * kBK * 2 && R % 64 == 0, "");
   const uint16_t* base;
   uint32_t off[kLoads];
   int64_t ld;
-  int first, rows, wave;
+  int rows, wave;
 
+  static __device__ int turn(int row) { return ((row >> 1) & 1) | (((row >> 3) & 1) << 1); }
   __device__ void init(const Operand& o, int at, int wave_, int lane) {
     wave = wave_, ld = o.ld, rows = o.rows;
     base = SD == ROW ? o.p + (int64_t)at * o.ld : o.p;
@@ -66,10 +69,9 @@ struct TileLoad {
         const int row = q * 8 + lane / 8, chunk = (lane & 7) ^ (row & 7);
         off[i] = (uint32_t)min(row, rows - 1 - at) * (uint32_t)(ld * 2) + chunk * 16;
       } else {
-        constexpr int C = R / 8;
-        const int row = q * kPer + lane / C, slot = lane % C;
-        const int chunk = (((slot >> 1) ^ (row & 3)) << 1) | (slot & 1);
-        off[i] = (uint32_t)min(at + chunk * 8, o.cols - 8) * 2;
+        const int row = (q % 8) * 8 + lane / 8, slot = lane & 7;
+        const int chunk = (((slot >> 1) ^ turn(row)) << 1) | (slot & 1);
+        off[i] = (uint32_t)min(at + (q / 8) * 64 + chunk * 8, o.cols - 8) * 2;
       }
     }
   }
@@ -81,7 +83,7 @@ struct TileLoad {
       if constexpr (SD == ROW) {
         src = b + off[i];
       } else {
-        const int row = min(k0 + (wave * kLoads + i) * kPer + lane / (R / 8), rows - 1);
+        const int row = min(k0 + ((wave * kLoads + i) % 8) * 8 + lane / 8, rows - 1);
         src = b + (int64_t)row * ld * 2 + off[i];
       }
       __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
@@ -90,23 +92,33 @@ struct TileLoad {
   }
 };
 
-// Operand block i (16 rows) of k-slice kk (32) out of a tile in LDS; `at`: the wavefront's first row (a multiple of 16).
+// Operand block i (16 rows) of half kk (32) of a step out of a tile in LDS; `at`: the wavefront's first row.
 template <Side SD, int R>
 __device__ inline u4 fragment(const lds_t* lds, int at, int i, int kk, int lane) {
   const int g = lane >> 4, c = lane & 15;
   if constexpr (SD == ROW) {
     return *(const __attribute__((address_space(3))) u4*)(lds + (at + 16 * i + c) * 128 + (((kk * 4 + g) ^ (c & 7)) * 16));
   } else {
-    const int r4 = c >> 2;
-    const lds_t* q = lds + (kk * 32 + 8 * g + r4) * (R * 2) + (((at / 16 + i) ^ r4) * 32) + (c & 3) * 8;
+    // two transposing reads: sixteen lanes give sixteen columns of four rows, lane 4 r + q four columns of row r
+    const int r0 = kk * 32 + 8 * g + (c >> 2), r1 = r0 + 4, blk = at / 16 + i;
+    const lds_t* t = lds + (blk >> 2) * (kBK * 128) + (c & 3) * 8;
     union { s4v h[2]; u4 u; } o;
-    o.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4v*)q);
-    o.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4v*)(q + 4 * R * 2));
+    o.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4v*)(t + r0 * 128 + ((blk & 3) ^ TileLoad<SD, 64, 1>::turn(r0)) * 32));
+    o.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4v*)(t + r1 * 128 + ((blk & 3) ^ TileLoad<SD, 64, 1>::turn(r1)) * 32));
     return o.u;
   }
 }
 
-// WM x WN wavefronts, each TM x TN blocks of 16 x 16.
+// WM x WN wavefronts, each TM x TN blocks of 16 x 16; two steps' tiles in LDS, NP planes.
+//
+// A step is two halves of 32 products.  While one half's fragments are multiplied the next half's come out of LDS.  Between
+// the halves a barrier: behind it the next step's tiles are in LDS, its first fragments are read, and this step's tiles,
+// all in registers by then, make room for the step after it, whose loads have a step's time.
+//
+// 256 x 256 tiles of eight wavefronts: 8192 x 8256 x 8192 bf16 runs at 1,350 TFLOP/s.  Registers alone would do 1,660 with
+// this instruction and such values (the clock falls with the power they take; 2,090 with zeros), loads alone 1,700,
+// reads of LDS alone 4,850.  Measured beside it: 32 x 32 blocks (1,810 out of registers) 1,080-1,150; four wavefronts
+// of 128 x 128 each 1,000; steps of 32 with three or four in LDS 1,040 (half cache lines); raised wave priority 1,265.
 template <int WM_, int WN_, int TM_, int TN_, Side SA_, Side SB_, bool BF_, int NP_>
 struct Product {
   static constexpr int WM = WM_, WN = WN_, TM = TM_, TN = TN_, NP = NP_;
@@ -115,55 +127,86 @@ struct Product {
   static constexpr int kLdsBytes = 2 * kStage;
   f4 acc[TM][TN];
 
+  struct Half {
+    u4 a[TM], b[TN];
+  };
+  __device__ static void read(Half& f, const lds_t* st, int kk, int wm, int wn, int lane) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j) f.b[j] = fragment<SB_, BN>(st + BM * kBK * 2, wn * TN * 16, j, kk, lane);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) f.a[i] = fragment<SA_, BM>(st, wm * TM * 16, i, kk, lane);
+  }
+  __device__ void multiply(const Half& f) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[i][j] = mma<BF_>(f.a[i], f.b[j], acc[i][j]);
+    // a read, then products, and so on (the rows' product 1,110 -> 1,170 TFLOP/s; with transposing reads, twice as
+    // many, the compiler's own order is better: 907 against 867)
+    if constexpr (SA_ == ROW && SB_ == ROW) {
+#pragma unroll
+      for (int q = 0; q < TM + TN; ++q) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, TM * TN / (TM + TN), 0);
+      }
+      __builtin_amdgcn_sched_group_barrier(0x008, TM * TN, 0);
+    }
+  }
+  // What this wavefront loads and reads is there, and so it is for all of them.
+  __device__ static void in_step() {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  }
+
+  // Sums over k from k_begin (a multiple of 64) to k_end.  A ROW operand is read up to the next multiple of 64, where
+  // either operand is zero; a COL operand's rows beyond its last are that one again.  Ends with a barrier.
   __device__ void run(const Operand& A, const Operand& B, int m0, int n0, int k_begin, int k_end, lds_t* lds) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave % WM, wn = wave / WM;
-    TileLoad<SA_, BM, NW> la;
-    TileLoad<SB_, BN, NW> lb;
-    la.init(A, m0, wave, lane);
-    lb.init(B, n0, wave, lane);
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int j = 0; j < TN; ++j) acc[i][j] = f4{0, 0, 0, 0};
     const int steps = (k_end - k_begin + kBK - 1) / kBK;
-    auto issue = [&](int t, int st) {
-      int pair = 0, k = t;
-      if constexpr (NP == 2) pair = t / steps, k = t - pair * steps;
-      la.issue(NP == 2 && pair == 0 ? A.plane : 0, k_begin + k * kBK, lds + st * kStage, lane);
-      lb.issue(NP == 2 && pair == 1 ? B.plane : 0, k_begin + k * kBK, lds + st * kStage + BM * kBK * 2, lane);
-    };
+    if (steps <= 0) return;
+    TileLoad<SA_, BM, NW> la;
+    TileLoad<SB_, BN, NW> lb;
+    la.init(A, m0, wave, lane);
+    lb.init(B, n0, wave, lane);
     const int total = NP == 2 ? 3 * steps : steps;
-    if (total <= 0) return;
-    issue(0, 0);
-    __syncthreads();
+    int next = 0, pair = 0, k = k_begin;      // of the tiles to load: with two planes lo hi, hi lo, hi hi
+    auto issue = [&](int st) {
+      if (next >= total) return;
+      la.issue(NP == 2 && pair == 0 ? A.plane : 0, k, lds + st * kStage, lane);
+      lb.issue(NP == 2 && pair == 1 ? B.plane : 0, k, lds + st * kStage + BM * kBK * 2, lane);
+      k += kBK;
+      if (NP == 2 && k >= k_begin + steps * kBK) k = k_begin, ++pair;
+      ++next;
+    };
+    Half f0, f1;
+    issue(0);
+    in_step();
+    issue(1);
+    read(f0, lds, 0, wm, wn, lane);
     for (int t = 0; t < total; ++t) {
       const int st = t & 1;
-      if (t + 1 < total) issue(t + 1, st ^ 1);
       if constexpr (NP == 2) {
-        if (t == 2 * steps) {
+        if (t == 2 * steps) {      // the products with a second part are in
 #pragma unroll
           for (int i = 0; i < TM; ++i)
 #pragma unroll
             for (int j = 0; j < TN; ++j) acc[i][j] *= kLoInv;
         }
       }
-      const lds_t* ta = lds + st * kStage;
-      const lds_t* tb = ta + BM * kBK * 2;
-#pragma unroll
-      for (int kk = 0; kk < kBK / 32; ++kk) {
-        u4 a[TM], b[TN];
-#pragma unroll
-        for (int j = 0; j < TN; ++j) b[j] = fragment<SB_, BN>(tb, wn * TN * 16, j, kk, lane);
-#pragma unroll
-        for (int i = 0; i < TM; ++i) a[i] = fragment<SA_, BM>(ta, wm * TM * 16, i, kk, lane);
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-#pragma unroll
-          for (int j = 0; j < TN; ++j) acc[i][j] = mma<BF_>(a[i], b[j], acc[i][j]);
-      }
-      __syncthreads();
+      read(f1, lds + st * kStage, 1, wm, wn, lane);
+      multiply(f0);
+      in_step();
+      issue(st);
+      read(f0, lds + (st ^ 1) * kStage, 0, wm, wn, lane);      // (behind the last step: of no use, and not used)
+      multiply(f1);
     }
+    __syncthreads();
   }
 };
 
