@@ -367,7 +367,8 @@ struct VocabCE {
   float* part;                // tiles x N: maximum and sum
   float* zlab;                // N logits of the labels
   uint16_t* dz;
-  float* dhpart;
+  float* dhpart;              // parts x N x Kp
+  float* dwpart;              // parts x piece x Kp
 };
 size_t vocab_ce_workspace(int64_t N, int K, int V, bool bf, bool weights, bool backward);
 hipError_t launch_vocab_ce(const VocabCE& k, bool bf, bool backward, void* ws, hipStream_t s);

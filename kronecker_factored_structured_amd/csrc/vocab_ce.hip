@@ -23,8 +23,15 @@ struct VocabScales {
 
 namespace {
 
+// Exponentials are of the rounded log2(e): 2^(z kLog2e - t), one two-term product each, with a row's t in that scale.  It
+// stretches the logits by 2^-26 of themselves and is exact otherwise, as a difference of rounded products would not be.
 constexpr float kLog2e = 1.44269504088896340736f;
-__device__ inline float expo(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+__device__ inline float expo2(float x) { return __builtin_amdgcn_exp2f(x); }
+// Maximum and sum (of 2^(.. - maximum)) of two parts of a row.
+__device__ inline float2 joined(float2 a, float2 b) {
+  const float t = fmaxf(a.x, b.x), r = t == -INFINITY ? 0.f : t;
+  return float2{t, a.y * expo2(a.x - r) + b.y * expo2(b.x - r)};
+}
 
 // ------------------------------------------------------------------------------ rows in use and scales
 
@@ -81,18 +88,31 @@ __device__ inline int vocab_count(const VocabCE& a) { return a.sc ? a.sc->count 
 // The largest finite magnitude of h's rows in use (block.y 0) and of W (1).
 __global__ __launch_bounds__(256) void vocab_top_kernel(VocabCE a) {
   const bool w = blockIdx.y == 1;
-  const int rows = w ? a.V : vocab_count(a);
+  const int64_t n = (w ? a.V : vocab_count(a)) * (int64_t)a.K;
   const float* src = (const float*)(w ? a.W : a.h);
+  const bool rows = !w && a.idx;
   uint32_t top = 0;
-  for (int r = blockIdx.x; r < rows; r += gridDim.x) {
-    const float* row = src + (int64_t)(!w && a.idx ? a.idx[r] : r) * a.K;
-    for (int k = threadIdx.x; k < a.K; k += 256) {
-      const uint32_t v = __float_as_uint(row[k]) & 0x7fffffffu;
-      if (v < 0x7f800000u) top = max(top, v);
+  auto see = [&](float f) {
+    const uint32_t v = __float_as_uint(f) & 0x7fffffffu;
+    if (v < 0x7f800000u) top = max(top, v);
+  };
+  const int64_t stride = (int64_t)gridDim.x * 256, first = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (rows && (a.K & 3)) {
+    for (int64_t i = first; i < n; i += stride) see(src[(int64_t)a.idx[i / a.K] * a.K + i % a.K]);
+  } else {
+#pragma unroll 4
+    for (int64_t i = first * 4; i < n - 3; i += stride * 4) {
+      const f4 v = *(const f4*)(src + (rows ? (int64_t)a.idx[i / a.K] * a.K + i % a.K : i));
+      see(v[0]), see(v[1]), see(v[2]), see(v[3]);
     }
+    if (first < (n & 3)) see(src[n - 1 - first]);      // (none where rows are gathered: K is a multiple of four)
   }
+  __shared__ uint32_t red[4];
   for (int o = 32; o >= 1; o /= 2) top = max(top, (uint32_t)__shfl_xor((int)top, o, 64));
-  if ((threadIdx.x & 63) == 0 && top) atomicMax(w ? &a.sc->top_w : &a.sc->top_h, top);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = top;
+  __syncthreads();
+  // (one atomic of a workgroup: at four of each of 1024 they took 100 us of this kernel's 125)
+  if (threadIdx.x == 0) atomicMax(w ? &a.sc->top_w : &a.sc->top_h, max(max(red[0], red[1]), max(red[2], red[3])));
 }
 
 // Rows as operands: gathered (h), padded with zeros to Kp, fp32 split into its planes.
@@ -158,88 +178,81 @@ __global__ __launch_bounds__(P::kThreads) void vocab_fwd_kernel(VocabCE a, int t
   P p;
   p.run(w_operand(a), h_operand(a, count), m0, n0, 0, a.Kp, (lds_t*)smem);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
-  const int wm = wave % P::WM, wn = wave / P::WM;
+  const int wm = wave % P::WM, wn = wave / P::WM, first = m0 + wm * P::TM * 16 + 4 * g;
   const float down = BF ? 1.f : scale_down(a.sc->top_h), down2 = BF ? 1.f : scale_down(a.sc->top_w);
-  float* red = (float*)smem;      // (the product ended with a barrier)
+  float2* red = (float2*)smem;      // (the product ended with a barrier)
 #pragma unroll
   for (int j = 0; j < P::TN; ++j) {
     const int nl = wn * P::TN * 16 + 16 * j + c, n = n0 + nl;
-    const int lab = n < count ? (int)min<int64_t>(max<int64_t>(a.labels[a.idx ? a.idx[n] : n], -1), a.V) : -1;
+    const int64_t lab = n < count ? a.labels[a.idx ? a.idx[n] : n] : -1;
+    const int64_t off = lab - first;
+    const bool mine = off >= 0 && off < P::TM * 16 && (off & 15) < 4 && lab < a.V;
     float top = -INFINITY;
+    if (m0 + P::BM > a.V) {      // the last tile
 #pragma unroll
-    for (int i = 0; i < P::TM; ++i)
+      for (int i = 0; i < P::TM; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int v = m0 + wm * P::TM * 16 + 16 * i + 4 * g + e;
-        float z = p.acc[i][j][e];
-        if constexpr (!BF) z = z * down * down2;
-        if (v >= a.V) z = -INFINITY;
-        if (v == lab && v < a.V) a.zlab[n] = z;
-        p.acc[i][j][e] = z;
-        top = z > top || z != z ? z : top;      // (a NaN stays)
-      }
-    float sum = 0.f;
-    const float ref = top == -INFINITY ? 0.f : top;
-#pragma unroll
-    for (int i = 0; i < P::TM; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sum += expo(p.acc[i][j][e] - ref);
-#pragma unroll
-    for (int o = 16; o <= 32; o *= 2) {
-      const float t2 = __shfl_xor(top, o, 64), s2 = __shfl_xor(sum, o, 64);
-      const float t = t2 > top || t2 != t2 ? t2 : top, r = t == -INFINITY ? 0.f : t;
-      sum = sum * expo(top - r) + s2 * expo(t2 - r);
-      top = t;
+        for (int e = 0; e < 4; ++e)
+          if (first + 16 * i + e >= a.V) p.acc[i][j][e] = -INFINITY;
     }
-    if (g == 0) red[(wm * P::BN + nl) * 2] = top, red[(wm * P::BN + nl) * 2 + 1] = sum;
+    // (fmaxf passes over NaN: the sum has it)
+#pragma unroll
+    for (int i = 0; i < P::TM; ++i) {
+      if constexpr (!BF) p.acc[i][j] *= down;
+      top = fmaxf(fmaxf(top, fmaxf(p.acc[i][j][0], p.acc[i][j][1])), fmaxf(p.acc[i][j][2], p.acc[i][j][3]));
+    }
+    const float f = BF ? kLog2e : down2 * kLog2e;
+    if (__any(mine)) {
+#pragma unroll
+      for (int i = 0; i < P::TM; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (mine && off == 16 * i + e) a.zlab[n] = BF ? p.acc[i][j][e] : p.acc[i][j][e] * down2;
+    }
+    float2 s = {top * f, 0.f};
+    const float ref = top == -INFINITY ? 0.f : s.x;
+#pragma unroll
+    for (int i = 0; i < P::TM; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s.y += expo2(fmaf(p.acc[i][j][e], f, -ref));
+#pragma unroll
+    for (int o = 16; o <= 32; o *= 2) s = joined(s, float2{__shfl_xor(s.x, o, 64), __shfl_xor(s.y, o, 64)});
+    if (g == 0) red[wm * P::BN + nl] = s;
   }
   __syncthreads();
   for (int nl = threadIdx.x; nl < P::BN; nl += P::kThreads) {
     if (n0 + nl >= count) break;
-    float t = red[nl * 2];
+    float2 s = red[nl];
 #pragma unroll
-    for (int w = 1; w < P::WM; ++w) {
-      const float t2 = red[(w * P::BN + nl) * 2];
-      t = t2 > t || t2 != t2 ? t2 : t;
-    }
-    const float r = t == -INFINITY ? 0.f : t;
-    float s = 0.f;
-#pragma unroll
-    for (int w = 0; w < P::WM; ++w) s += red[(w * P::BN + nl) * 2 + 1] * expo(red[(w * P::BN + nl) * 2] - r);
-    ((float2*)a.part)[(int64_t)mt * a.N + n0 + nl] = float2{t, s};
+    for (int w = 1; w < P::WM; ++w) s = joined(s, red[w * P::BN + nl]);
+    ((float2*)a.part)[(int64_t)mt * a.N + n0 + nl] = s;
   }
 }
 
-// A row's statistics from its tiles': 32 rows by 8 slices of the tiles.
-__global__ __launch_bounds__(256) void vocab_join_kernel(VocabCE a, int tiles) {
-  __shared__ float2 red[8][32];
+// A row's statistics from its tiles': 32 rows by 32 slices of the tiles.
+__global__ __launch_bounds__(1024) void vocab_join_kernel(VocabCE a, int tiles) {
+  __shared__ float2 red[32][33];
   const int count = vocab_count(a), r = threadIdx.x & 31, sl = threadIdx.x >> 5;
   const int64_t i = (int64_t)blockIdx.x * 32 + r;
   const float2* part = (const float2*)a.part;
-  float t = -INFINITY, s = 0.f;
+  float2 s = {-INFINITY, 0.f};
   if (i < count)
-    for (int m = sl; m < tiles; m += 8) {
-      const float2 v = part[(int64_t)m * a.N + i];
-      const float n = v.x > t || v.x != v.x ? v.x : t, ref = n == -INFINITY ? 0.f : n;
-      s = s * expo(t - ref) + v.y * expo(v.x - ref);
-      t = n;
-    }
-  red[sl][r] = float2{t, s};
+    for (int m = sl; m < tiles; m += 32) s = joined(s, part[(int64_t)m * a.N + i]);
+  red[sl][r] = s;
   __syncthreads();
-  if (sl != 0 || i >= count) return;
+  // the row's 32 slices by half a wavefront
+  const int row32 = threadIdx.x >> 5;
+  s = red[threadIdx.x & 31][row32];
 #pragma unroll
-  for (int k = 1; k < 8; ++k) {
-    const float2 v = red[k][r];
-    const float n = v.x > t || v.x != v.x ? v.x : t, ref = n == -INFINITY ? 0.f : n;
-    s = s * expo(t - ref) + v.y * expo(v.x - ref);
-    t = n;
-  }
-  const int64_t row = a.idx ? a.idx[i] : i;
+  for (int o = 16; o >= 1; o /= 2) s = joined(s, float2{__shfl_xor(s.x, o, 32), __shfl_xor(s.y, o, 32)});
+  const int64_t k = (int64_t)blockIdx.x * 32 + row32;
+  if ((threadIdx.x & 31) != 0 || k >= count) return;
+  const int64_t row = a.idx ? a.idx[k] : k;
   const int64_t lab = a.labels[row];
-  const float nll = lab >= 0 && lab < a.V ? (t - a.zlab[i]) + logf(s) : NAN;
-  a.nll[row] = nll;
-  a.stats[2 * row] = t;
-  a.stats[2 * row + 1] = lab >= 0 && lab < a.V ? 1.f / s : NAN;
+  const bool token = lab >= 0 && lab < a.V;
+  a.nll[row] = token ? (float)(((double)s.x + (double)log2f(s.y)) / (double)kLog2e - (double)a.zlab[k]) : NAN;
+  a.stats[2 * row] = s.x;
+  a.stats[2 * row + 1] = token ? 1.f / s.y : NAN;
 }
 
 // loss = sum_n w_n nll_n in 64 bits, in a fixed order.
@@ -271,49 +284,59 @@ __global__ __launch_bounds__(P::kThreads) void vocab_dz_kernel(VocabCE a, int v0
   P p;
   p.run(w_operand(a), h_operand(a, count), v0 + m0, n0, 0, a.Kp, (lds_t*)smem);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
-  const int wm = wave % P::WM, wn = wave / P::WM;
+  const int wm = wave % P::WM, wn = wave / P::WM, first = v0 + m0 + wm * P::TM * 16 + 4 * g;
   const float down = BF ? 1.f : scale_down(a.sc->top_h), down2 = BF ? 1.f : scale_down(a.sc->top_w);
-  const float up = BF ? 1.f : scale_up(a.sc->top_dz);
+  const float up = BF ? 1.f : scale_up(a.sc->top_dz), f = BF ? kLog2e : down2 * kLog2e;
   const int padded = (count + kBK - 1) / kBK * kBK;      // rows that the contraction over them reads
+  const bool edge = v0 + m0 + P::BM > a.V || n0 + P::BN > count;
 #pragma unroll
   for (int j = 0; j < P::TN; ++j) {
     const int n = n0 + wn * P::TN * 16 + 16 * j + c;
-    if (n >= padded) continue;
-    int lab = -1;
+    int64_t lab = -1;
     float top = 0.f, inv = 0.f, w = 0.f;
     if (n < count) {
       const int64_t row = a.idx ? a.idx[n] : n;
-      lab = (int)min<int64_t>(max<int64_t>(a.labels[row], -1), a.V);
-      top = a.stats_in[2 * row], inv = a.stats_in[2 * row + 1];
+      lab = a.labels[row];
       w = (a.weights ? a.weights[row] : a.mean) * up;
+      top = a.stats_in[2 * row], inv = a.stats_in[2 * row + 1] * w;
     }
 #pragma unroll
-    for (int i = 0; i < P::TM; ++i) {
-      const int ml = m0 + wm * P::TM * 16 + 16 * i + 4 * g;
-      float d[4];
+    for (int i = 0; i < P::TM; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int v = v0 + ml + e;
-        float z = p.acc[i][j][e];
-        if constexpr (!BF) z = z * down * down2;
-        const float q = expo(z - top) * inv;
-        d[e] = v >= a.V || n >= count ? 0.f : (v == lab ? q - 1.f : q) * w;
-      }
-      uint16_t* out = a.dz + (int64_t)n * vc + ml;
-      if constexpr (BF) {
-        *(uint2*)out = uint2{bf16_pair(d[0], d[1]), bf16_pair(d[2], d[3])};
-      } else {
-        typedef _Float16 h4 __attribute__((ext_vector_type(4)));
-        h4 hi, lo;
+      for (int e = 0; e < 4; ++e) p.acc[i][j][e] = expo2(fmaf(BF ? p.acc[i][j][e] : p.acc[i][j][e] * down, f, -top)) * inv;
+    const int64_t off = lab - first;
+    const bool mine = off >= 0 && off < P::TM * 16 && (off & 15) < 4;
+    if (__any(mine)) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          hi[e] = (_Float16)d[e];
-          lo[e] = (_Float16)((d[e] - (float)hi[e]) * kLo);
-        }
-        *(h4*)out = hi;
-        *(h4*)(out + a.dzplane) = lo;
-      }
+      for (int i = 0; i < P::TM; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (mine && off == 16 * i + e) p.acc[i][j][e] -= w;
     }
+    if (edge) {
+#pragma unroll
+      for (int i = 0; i < P::TM; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (n >= count || first + 16 * i + e >= a.V) p.acc[i][j][e] = 0.f;
+    }
+  }
+  uint16_t* out = a.dz + (int64_t)n0 * vc + m0;
+  if constexpr (BF) {
+    store_rows<P>(smem, out, vc, padded - n0, [&](int i, int j) {
+      return uint2{bf16_pair(p.acc[i][j][0], p.acc[i][j][1]), bf16_pair(p.acc[i][j][2], p.acc[i][j][3])};
+    });
+  } else {
+    // the first parts, and what they leave, in the sums' place, as the second ones
+    typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+    auto part = [&](int i, int j) {
+      const f4 v = p.acc[i][j];
+      const h4 h = {(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
+      p.acc[i][j] = f4{v[0] - (float)h[0], v[1] - (float)h[1], v[2] - (float)h[2], v[3] - (float)h[3]} * kLo;
+      return __builtin_bit_cast(uint2, h);
+    };
+    store_rows<P>(smem, out, vc, padded - n0, part);
+    store_rows<P>(smem, out + a.dzplane, vc, padded - n0, part);
   }
 }
 
@@ -348,6 +371,29 @@ __global__ __launch_bounds__(P::kThreads) void vocab_dh_kernel(VocabCE a, int v0
   }
 }
 
+// Four gradients of a row of K, times f2 and f, in their type.
+template <bool BF>
+__device__ inline void put_grad(void* p, int64_t row, int k, int K, f4 s, float f2, float f) {
+  s = s * f2 * f;
+  if constexpr (BF) {
+    uint16_t* o = (uint16_t*)p + row * K + k;
+    if ((K & 3) == 0)
+      *(uint2*)o = uint2{bf16_pair(s[0], s[1]), bf16_pair(s[2], s[3])};
+    else
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (k + e < K) o[e] = (uint16_t)bf16_rne(s[e]);
+  } else {
+    float* o = (float*)p + row * K + k;
+    if ((K & 3) == 0)
+      *(f4*)o = s;
+    else
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (k + e < K) o[e] = s[e];
+  }
+}
+
 template <bool BF>
 __global__ __launch_bounds__(256) void vocab_dh_join_kernel(VocabCE a, int splits) {
   float f = a.gout[0], f2 = 1.f;
@@ -359,31 +405,13 @@ __global__ __launch_bounds__(256) void vocab_dh_join_kernel(VocabCE a, int split
     if (k >= a.K) continue;
     const int64_t at = a.idx ? a.pos[row] : row;
     f4 s = {0, 0, 0, 0};
-    if (at >= 0) {
+    if (at >= 0)
       for (int t = 0; t < splits; ++t) s += *(const f4*)(a.dhpart + ((int64_t)t * a.N + at) * a.Kp + k);
-      s = s * f2 * f;
-    }
-    if constexpr (BF) {
-      uint16_t* o = (uint16_t*)a.dh + row * a.K + k;
-      if ((a.K & 3) == 0)
-        *(uint2*)o = uint2{bf16_pair(s[0], s[1]), bf16_pair(s[2], s[3])};
-      else
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (k + e < a.K) o[e] = (uint16_t)bf16_rne(s[e]);
-    } else {
-      float* o = (float*)a.dh + row * a.K + k;
-      if ((a.K & 3) == 0)
-        *(f4*)o = s;
-      else
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (k + e < a.K) o[e] = s[e];
-    }
+    put_grad<BF>(a.dh, row, k, a.K, s, at >= 0 ? f2 : 0.f, at >= 0 ? f : 0.f);
   }
 }
 
-// dW of a piece: K (m) x vocabulary (n), the contraction over the rows.
+// dW of a piece: K (m) x vocabulary (n), the contraction over the rows, in gridDim.y parts (one: into dW itself).
 template <class P, bool BF>
 __global__ __launch_bounds__(P::kThreads) void vocab_dw_kernel(VocabCE a, int v0, int vc, int tm, int tn) {
   extern __shared__ char smem[];
@@ -391,39 +419,41 @@ __global__ __launch_bounds__(P::kThreads) void vocab_dw_kernel(VocabCE a, int v0
   tile_of(blockIdx.x, gridDim.x, tm, tn, mt, nt);
   const int count = vocab_count(a), m0 = mt * P::BM, n0 = nt * P::BN;
   const int padded = (count + kBK - 1) / kBK * kBK;
+  const int len = (padded / kBK + gridDim.y - 1) / gridDim.y * kBK, k0 = blockIdx.y * len;
   const Operand dz = {a.dz, vc, a.dzplane, padded, vc};
   P p;
-  p.run(h_operand(a, count), dz, m0, n0, 0, count, (lds_t*)smem);
+  p.run(h_operand(a, count), dz, m0, n0, k0, min(count, k0 + len), (lds_t*)smem);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
   float f = a.gout[0], f2 = 1.f;
   if constexpr (!BF) f *= scale_down(a.sc->top_dz), f2 = scale_down(a.sc->top_h);
 #pragma unroll
   for (int j = 0; j < P::TN; ++j) {
-    const int v = v0 + n0 + (wave / P::WM) * P::TN * 16 + 16 * j + c;
-    if (v >= a.V) continue;
+    const int n = n0 + (wave / P::WM) * P::TN * 16 + 16 * j + c;
+    if (v0 + n >= a.V) continue;
 #pragma unroll
     for (int i = 0; i < P::TM; ++i) {
       const int k = m0 + (wave % P::WM) * P::TM * 16 + 16 * i + 4 * g;
-      if (k >= a.K) continue;
-      const f4 s = p.acc[i][j] * f2 * f;
-      if constexpr (BF) {
-        uint16_t* o = (uint16_t*)a.dW + (int64_t)v * a.K + k;
-        if ((a.K & 3) == 0)
-          *(uint2*)o = uint2{bf16_pair(s[0], s[1]), bf16_pair(s[2], s[3])};
-        else
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (k + e < a.K) o[e] = (uint16_t)bf16_rne(s[e]);
-      } else {
-        float* o = (float*)a.dW + (int64_t)v * a.K + k;
-        if ((a.K & 3) == 0)
-          *(f4*)o = s;
-        else
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (k + e < a.K) o[e] = s[e];
+      if (gridDim.y > 1) {
+        if (k < a.Kp) *(f4*)(a.dwpart + ((int64_t)blockIdx.y * vc + n) * a.Kp + k) = p.acc[i][j];
+      } else if (k < a.K) {
+        put_grad<BF>(a.dW, v0 + n, k, a.K, p.acc[i][j], f2, f);
       }
     }
+  }
+}
+
+template <bool BF>
+__global__ __launch_bounds__(256) void vocab_dw_join_kernel(VocabCE a, int v0, int vc, int parts) {
+  float f = a.gout[0], f2 = 1.f;
+  if constexpr (!BF) f *= scale_down(a.sc->top_dz), f2 = scale_down(a.sc->top_h);
+  const int per = a.Kp / 4, rows = min(vc, a.V - v0);
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)rows * per; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / per;
+    const int k = (int)(i - row * per) * 4;
+    if (k >= a.K) continue;
+    f4 s = {0, 0, 0, 0};
+    for (int t = 0; t < parts; ++t) s += *(const f4*)(a.dwpart + ((int64_t)t * vc + row) * a.Kp + k);
+    put_grad<BF>(a.dW, v0 + row, k, a.K, s, f2, f);
   }
 }
 
@@ -431,7 +461,9 @@ __global__ __launch_bounds__(P::kThreads) void vocab_dw_kernel(VocabCE a, int v0
 template <bool BF, Side SA, Side SB>
 using Big = Product<2, 4, 8, 4, SA, SB, BF, BF ? 1 : 2>;
 template <bool BF, Side SA, Side SB>
-using Few = Product<4, 1, 4, 4, SA, SB, BF, BF ? 1 : 2>;
+using Three = Product<2, 4, 6, 4, SA, SB, BF, BF ? 1 : 2>;      // 192 x 256
+template <bool BF, Side SA, Side SB>
+using Few = Product<4, 1, 4, 4, SA, SB, BF, BF ? 1 : 2>;        // 256 x 64
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -439,13 +471,37 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 // Rows and width of a product with few rows: a tile of 64.
 bool few(int64_t N) { return N <= 64; }
 
+// Workgroups (one a CU) run in rounds of 256, so that a product of a few more tiles than that takes two.  The parts of the
+// contraction that cost least, with what was measured: a step of a 256 x 256 tile 1.9 us, its start and end 4 us, the
+// tile's sums through memory at 4.5 TB/s (`moves` times for each part).
+struct Parts {
+  int parts;
+  double us;
+};
+Parts best_parts(int64_t tiles, int64_t steps, double share, double moves, int most) {
+  Parts best{1, 1e30};
+  for (int s = 1; s <= most && (s == 1 || steps / s >= 4); ++s) {
+    const double rounds = (double)ceil_div(tiles * s, 256);
+    const double us = rounds * (ceil_div(steps, s) * 1.9 * share + 4) + (s > 1 || moves > 2 ? tiles * s * moves * 0.058 * share : 0);
+    if (us < best.us) best = {s, us};
+  }
+  return best;
+}
+
 struct VocabPlan {
   int Kp;
   bool rows, copy_h, copy_w;      // rows in use are listed; operands that are copies
   int tiles;                      // of the vocabulary, 256 wide
   int piece, pieces, splits;      // backward
-  size_t sc, idx, pos, hp, wp, part, zlab, dz, dhpart, bytes;
+  bool three;                     // dh in tiles of 192
+  size_t sc, idx, pos, hp, wp, part, zlab, dz, dhpart, dwpart, bytes;
 };
+
+// Parts of a piece's dW.
+int dw_parts(int64_t N, int Kp, int vc, int planes) {
+  const int64_t tiles = ceil_div(Kp, 256) * (vc / 256), steps = ceil_div(N, kBK) * (planes == 2 ? 3 : 1);
+  return tiles >= 256 ? 1 : best_parts(tiles, steps, 1, 2, 8).parts;
+}
 
 VocabPlan plan_of(int64_t N, int K, int V, bool bf, bool weights, bool backward) {
   VocabPlan p{};
@@ -467,15 +523,29 @@ VocabPlan plan_of(int64_t N, int K, int V, bool bf, bool weights, bool backward)
     p.part = take(8 * (size_t)p.tiles * N);
     p.zlab = take(4 * (size_t)N);
   } else {
-    // dz of a piece takes at most about 512 MB
-    const int64_t most = std::max<int64_t>(1, (int64_t(512) << 20) / (rows * 256 * 2 * planes));
-    p.pieces = (int)ceil_div(p.tiles, most);
-    p.piece = (int)ceil_div(p.tiles, p.pieces) * 256;
-    p.pieces = (int)ceil_div(V, p.piece);
+    // dz of a piece takes at most about 512 MB; where a tile of dW takes long, a piece's tiles fill whole rounds
+    const int64_t tk = ceil_div(p.Kp, 256), triple = bf ? 1 : 3;
+    int64_t piece = std::min<int64_t>(p.tiles, std::max<int64_t>(1, (int64_t(512) << 20) / (rows * 256 * 2 * planes)));
+    if (rows / kBK * triple >= 16 && piece * tk >= 256) piece = piece * tk / 256 * 256 / tk;
+    p.piece = (int)piece * 256;
+    p.pieces = (int)ceil_div(p.tiles, piece);
     p.dz = take(2 * (size_t)planes * rows * p.piece);
-    const int64_t t = ceil_div(p.Kp, 256) * ceil_div(std::max<int64_t>(N, 1), few(N) ? 64 : 256);
-    p.splits = (int)std::min<int64_t>(std::max<int64_t>(1, 512 / t), std::max(1, p.piece / 512));
+    const int64_t steps = p.piece / kBK * triple, moves = p.pieces > 1 ? 4 : 2;
+    if (few(N)) {
+      p.splits = (int)std::min<int64_t>(std::max<int64_t>(1, 512 / tk), std::max(1, p.piece / 512));
+    } else {
+      const int64_t tn = ceil_div(N, 256);
+      const Parts b = best_parts(tk * tn, steps, 1, moves, 16), c = best_parts(ceil_div(p.Kp, 192) * tn, steps, 0.75, moves, 16);
+      p.three = c.us < b.us;
+      p.splits = p.three ? c.parts : b.parts;
+    }
     p.dhpart = take(4 * (size_t)p.splits * N * p.Kp);
+    size_t most = 0;
+    for (int i = 0; i < p.pieces; ++i) {
+      const int vc = std::min(p.piece, (p.tiles - i * (p.piece / 256)) * 256), parts = dw_parts(N, p.Kp, vc, planes);
+      if (parts > 1) most = std::max(most, 4 * (size_t)parts * vc * p.Kp);
+    }
+    p.dwpart = take(most);
   }
   p.bytes = at;
   return p;
@@ -496,6 +566,7 @@ VocabCE bind(const VocabCE& k, const VocabPlan& p, char* ws, bool bf) {
   a.dz = (uint16_t*)(ws + p.dz);
   a.dzplane = ceil_div(std::max<int64_t>(k.N, 1), kBK) * kBK * (int64_t)p.piece;
   a.dhpart = (float*)(ws + p.dhpart);
+  a.dwpart = (float*)(ws + p.dwpart);
   return a;
 }
 
@@ -510,7 +581,7 @@ hipError_t go(dim3 grid, hipStream_t s, A... args) {
 template <bool BF>
 hipError_t prepare(const VocabCE& a, const VocabPlan& p, hipStream_t s) {
   if (p.rows || !BF) hipLaunchKernelGGL(vocab_rows_kernel, dim3(1), dim3(1024), 0, s, a);
-  if (!BF) hipLaunchKernelGGL(vocab_top_kernel, dim3(1024, 2), dim3(256), 0, s, a);
+  if (!BF) hipLaunchKernelGGL(vocab_top_kernel, dim3(512, 2), dim3(256), 0, s, a);
   const int per = p.Kp / 8;
   auto blocks = [&](int64_t rows) { return dim3((unsigned)std::min<int64_t>(4096, std::max<int64_t>(1, ceil_div(rows * per, 256)))); };
   if (p.copy_h && a.N) hipLaunchKernelGGL((vocab_pack_kernel<BF>), blocks(a.N), dim3(256), 0, s, a, 0);
@@ -529,7 +600,7 @@ hipError_t run_fwd(const VocabCE& a, const VocabPlan& p, hipStream_t s) {
     const dim3 grid((unsigned)(p.tiles * tn));
     e = few(a.N) ? go<PF, vocab_fwd_kernel<PF, BF>>(grid, s, a, p.tiles, tn) : go<PB, vocab_fwd_kernel<PB, BF>>(grid, s, a, p.tiles, tn);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(vocab_join_kernel, dim3((unsigned)ceil_div(a.N, 32)), dim3(256), 0, s, a, p.tiles);
+    hipLaunchKernelGGL(vocab_join_kernel, dim3((unsigned)ceil_div(a.N, 32)), dim3(1024), 0, s, a, p.tiles);
   }
   hipLaunchKernelGGL(vocab_loss_kernel, dim3(1), dim3(1024), 0, s, a);
   return hipGetLastError();
@@ -554,15 +625,22 @@ hipError_t run_bwd(const VocabCE& a, const VocabPlan& p, hipStream_t s) {
       typedef Few<BF, COL, ROW> PF;
       typedef Big<BF, COL, ROW> PB;
       const int len = (int)ceil_div(ceil_div(vc, p.splits), kBK) * kBK;
-      const dim3 grid((unsigned)(tk * tn), (unsigned)p.splits);
-      e = fw ? go<PF, vocab_dh_kernel<PF, BF>>(grid, s, a, v0, vc, tk, tn, len, (int)(i > 0))
+      typedef Three<BF, COL, ROW> PT;
+      const int th = p.three ? (int)ceil_div(p.Kp, 192) : tk;
+      const dim3 grid((unsigned)(th * tn), (unsigned)p.splits);
+      e = p.three ? go<PT, vocab_dh_kernel<PT, BF>>(grid, s, a, v0, vc, th, tn, len, (int)(i > 0))
+          : fw ? go<PF, vocab_dh_kernel<PF, BF>>(grid, s, a, v0, vc, tk, tn, len, (int)(i > 0))
              : go<PB, vocab_dh_kernel<PB, BF>>(grid, s, a, v0, vc, tk, tn, len, (int)(i > 0));
       if (e != hipSuccess) return e;
     }
     if (a.dW) {
       typedef Big<BF, COL, COL> PB;
-      e = go<PB, vocab_dw_kernel<PB, BF>>(dim3((unsigned)(tk * tm)), s, a, v0, vc, tk, tm);
+      const int parts = dw_parts(a.N, p.Kp, vc, BF ? 1 : 2);
+      e = go<PB, vocab_dw_kernel<PB, BF>>(dim3((unsigned)(tk * tm), (unsigned)parts), s, a, v0, vc, tk, tm);
       if (e != hipSuccess) return e;
+      if (parts > 1)
+        hipLaunchKernelGGL((vocab_dw_join_kernel<BF>), dim3((unsigned)std::min<int64_t>(4096, ceil_div((int64_t)vc * (p.Kp / 4), 256))), dim3(256),
+                           0, s, a, v0, vc, parts);
     }
   }
   if (a.dh && a.N)
