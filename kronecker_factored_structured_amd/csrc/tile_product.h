@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "kron_internal.h"
 
@@ -75,20 +76,17 @@ struct TileLoad {
       }
     }
   }
-  __device__ void issue(int64_t plane, int k0, lds_t* lds, int lane) const {
-    const char* b = (const char*)(base + plane + (SD == ROW ? k0 : 0));
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const char* src;
-      if constexpr (SD == ROW) {
-        src = b + off[i];
-      } else {
-        const int row = min(k0 + ((wave * kLoads + i) % 8) * 8 + lane / 8, rows - 1);
-        src = b + (int64_t)row * ld * 2 + off[i];
-      }
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                       (__attribute__((address_space(3))) void*)(lds + (wave * kLoads + i) * 1024), 16, 0, 0);
+  // Load i of the wavefront's share of the tile at k0.
+  __device__ void issue(int i, int64_t plane, int k0, lds_t* lds, int lane) const {
+    const char* src;
+    if constexpr (SD == ROW) {
+      src = (const char*)(base + plane + k0) + off[i];
+    } else {
+      const int row = min(k0 + ((wave * kLoads + i) % 8) * 8 + lane / 8, rows - 1);
+      src = (const char*)(base + plane) + (int64_t)row * ld * 2 + off[i];
     }
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+                                     (__attribute__((address_space(3))) void*)(lds + (wave * kLoads + i) * 1024), 16, 0, 0);
   }
 };
 
@@ -113,12 +111,14 @@ __device__ inline u4 fragment(const lds_t* lds, int at, int i, int kk, int lane)
 //
 // A step is two halves of 32 products.  While one half's fragments are multiplied the next half's come out of LDS.  Between
 // the halves a barrier: behind it the next step's tiles are in LDS, its first fragments are read, and this step's tiles,
-// all in registers by then, make room for the step after it, whose loads have a step's time.
+// all in registers by then, make room for the step after it, whose loads go out between the products (issued together
+// they hold the wavefronts up: dW of 768 x 21760 over 8192 rows 303 -> 280 us) and have a step's time.
 //
-// 256 x 256 tiles of eight wavefronts: 8192 x 8256 x 8192 bf16 runs at 1,350 TFLOP/s.  Registers alone would do 1,660 with
-// this instruction and such values (the clock falls with the power they take; 2,090 with zeros), loads alone 1,700,
-// reads of LDS alone 4,850.  Measured beside it: 32 x 32 blocks (1,810 out of registers) 1,080-1,150; four wavefronts
-// of 128 x 128 each 1,000; steps of 32 with three or four in LDS 1,040 (half cache lines); raised wave priority 1,265.
+// 256 x 256 tiles of eight wavefronts: 8192 x 8256 x 8192 bf16 runs at 1,370 TFLOP/s.  Registers alone would do 1,660 with
+// this instruction and such values (the clock falls to 2.0 GHz with the power they take; 2,090 with zeros), loads alone
+// 1,700, reads of LDS alone 4,850.  Measured beside it: 32 x 32 blocks (1,810 out of registers) 1,080-1,150; four
+// wavefronts of 128 x 128 each 1,000; steps of 32 with three to five in LDS 960-1,040; raised wave priority 1,265; reads,
+// loads and products interleaved by hand 1,350.
 template <int WM_, int WN_, int TM_, int TN_, Side SA_, Side SB_, bool BF_, int NP_>
 struct Product {
   static constexpr int WM = WM_, WN = WN_, TM = TM_, TN = TN_, NP = NP_;
@@ -136,22 +136,17 @@ struct Product {
 #pragma unroll
     for (int i = 0; i < TM; ++i) f.a[i] = fragment<SA_, BM>(st, wm * TM * 16, i, kk, lane);
   }
-  __device__ void multiply(const Half& f) {
+  // between(i): what is issued beside block row i's products.
+  template <class F>
+  __device__ void multiply(const Half& f, const F& between) {
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
+    for (int i = 0; i < TM; ++i) {
+      between(i);
 #pragma unroll
       for (int j = 0; j < TN; ++j) acc[i][j] = mma<BF_>(f.a[i], f.b[j], acc[i][j]);
-    // a read, then products, and so on (the rows' product 1,110 -> 1,170 TFLOP/s; with transposing reads, twice as
-    // many, the compiler's own order is better: 907 against 867)
-    if constexpr (SA_ == ROW && SB_ == ROW) {
-#pragma unroll
-      for (int q = 0; q < TM + TN; ++q) {
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x008, TM * TN / (TM + TN), 0);
-      }
-      __builtin_amdgcn_sched_group_barrier(0x008, TM * TN, 0);
     }
   }
+  static constexpr int kLoads = TileLoad<SA_, BM, NW>::kLoads + TileLoad<SB_, BN, NW>::kLoads;
   // What this wavefront loads and reads is there, and so it is for all of them.
   __device__ static void in_step() {
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
@@ -176,20 +171,29 @@ struct Product {
     lb.init(B, n0, wave, lane);
     const int total = NP == 2 ? 3 * steps : steps;
     int next = 0, pair = 0, k = k_begin;      // of the tiles to load: with two planes lo hi, hi lo, hi hi
-    auto issue = [&](int st) {
-      if (next >= total) return;
-      la.issue(NP == 2 && pair == 0 ? A.plane : 0, k, lds + st * kStage, lane);
-      lb.issue(NP == 2 && pair == 1 ? B.plane : 0, k, lds + st * kStage + BM * kBK * 2, lane);
+    auto load = [&](int st, int i) {      // load i of the wavefront's for the next tiles
+      if (i < TileLoad<SA_, BM, NW>::kLoads)
+        la.issue(i, NP == 2 && pair == 0 ? A.plane : 0, k, lds + st * kStage, lane);
+      else
+        lb.issue(i - TileLoad<SA_, BM, NW>::kLoads, NP == 2 && pair == 1 ? B.plane : 0, k, lds + st * kStage + BM * kBK * 2, lane);
+    };
+    auto loaded = [&]() {
       k += kBK;
       if (NP == 2 && k >= k_begin + steps * kBK) k = k_begin, ++pair;
       ++next;
     };
+    auto all = [&](int st) {
+      if (next >= total) return;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) load(st, i);
+      loaded();
+    };
     Half f0, f1;
-    issue(0);
+    all(0);
     in_step();
-    issue(1);
+    all(1);
     read(f0, lds, 0, wm, wn, lane);
-    for (int t = 0; t < total; ++t) {
+    auto step = [&](int t, auto more) {
       const int st = t & 1;
       if constexpr (NP == 2) {
         if (t == 2 * steps) {      // the products with a second part are in
@@ -200,12 +204,21 @@ struct Product {
         }
       }
       read(f1, lds + st * kStage, 1, wm, wn, lane);
-      multiply(f0);
+      multiply(f0, [](int) {});
       in_step();
-      issue(st);
       read(f0, lds + (st ^ 1) * kStage, 0, wm, wn, lane);      // (behind the last step: of no use, and not used)
-      multiply(f1);
-    }
+      multiply(f1, [&](int i) {
+        if (!more) return;
+        constexpr int per = (kLoads + TM - 1) / TM;
+#pragma unroll
+        for (int q = 0; q < per; ++q)
+          if (i * per + q < kLoads) load(st, i * per + q);
+      });
+      if (more) loaded();
+    };
+    int t = 0;
+    for (; t < total - 2; ++t) step(t, std::true_type{});
+    for (; t < total; ++t) step(t, std::false_type{});
     __syncthreads();
   }
 };

@@ -472,7 +472,7 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 bool few(int64_t N) { return N <= 64; }
 
 // Workgroups (one a CU) run in rounds of 256, so that a product of a few more tiles than that takes two.  The parts of the
-// contraction that cost least, with what was measured: a step of a 256 x 256 tile 1.9 us, its start and end 4 us, the
+// contraction that cost least, with what was measured: a step of a 256 x 256 tile 2.2 us, its start and end 4 us, the
 // tile's sums through memory at 4.5 TB/s (`moves` times for each part).
 struct Parts {
   int parts;
@@ -482,7 +482,7 @@ Parts best_parts(int64_t tiles, int64_t steps, double share, double moves, int m
   Parts best{1, 1e30};
   for (int s = 1; s <= most && (s == 1 || steps / s >= 4); ++s) {
     const double rounds = (double)ceil_div(tiles * s, 256);
-    const double us = rounds * (ceil_div(steps, s) * 1.9 * share + 4) + (s > 1 || moves > 2 ? tiles * s * moves * 0.058 * share : 0);
+    const double us = rounds * (ceil_div(steps, s) * 2.2 * share + 4) + (s > 1 || moves > 2 ? tiles * s * moves * 0.058 * share : 0);
     if (us < best.us) best = {s, us};
   }
   return best;
