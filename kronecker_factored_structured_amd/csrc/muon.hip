@@ -7,6 +7,7 @@
 // instruction).  Others run as tiled products over all matrices of their size; X, A and the polynomial of A
 // are fp16 planes (tile_product.h): two for fp32 parameters, one for bf16 ones.
 #include <algorithm>
+#include <type_traits>
 #include <utility>
 #include <vector>
 
@@ -23,6 +24,39 @@ template <bool BF>
 __device__ inline float get(const void* p, int64_t i) {
   return BF ? __uint_as_float((uint32_t)((const uint16_t*)p)[i] << 16) : ((const float*)p)[i];
 }
+// N neighbouring values, i a multiple of N.
+template <bool BF, int N>
+__device__ inline void get_n(const void* p, int64_t i, float (&v)[N]) {
+  if constexpr (N == 1) {
+    v[0] = get<BF>(p, i);
+  } else if constexpr (BF) {
+    const uint2 w = *(const uint2*)((const uint16_t*)p + i);
+    v[0] = bf16_lo(w.x), v[1] = bf16_hi(w.x), v[2] = bf16_lo(w.y), v[3] = bf16_hi(w.y);
+  } else {
+    const f4 w = *(const f4*)((const float*)p + i);
+    v[0] = w[0], v[1] = w[1], v[2] = w[2], v[3] = w[3];
+  }
+}
+template <bool BF, int N>
+__device__ inline void put_n(void* p, int64_t i, const float (&v)[N]) {
+  if constexpr (N == 1) {
+    if (BF) ((uint16_t*)p)[i] = (uint16_t)bf16_rne(v[0]);
+    else ((float*)p)[i] = v[0];
+  } else if constexpr (BF) {
+    *(uint2*)((uint16_t*)p + i) = uint2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+  } else {
+    *(f4*)((float*)p + i) = f4{v[0], v[1], v[2], v[3]};
+  }
+}
+// u of N neighbours from the gradient and the momentum before.
+template <int N>
+__device__ inline void momentum(const MuonHyper& h, const float (&g)[N], float (&m)[N], float (&u)[N]) {
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    m[e] = fmaf(h.mu, m[e], g[e]);
+    u[e] = h.nesterov ? fmaf(h.mu, m[e], g[e]) : m[e];
+  }
+}
 template <bool BF>
 __device__ inline void put(void* p, int64_t i, float v) {
   if (BF) ((uint16_t*)p)[i] = (uint16_t)bf16_rne(v);
@@ -30,7 +64,7 @@ __device__ inline void put(void* p, int64_t i, float v) {
 }
 
 // ------------------------------------------------------------------------------ matrices within a workgroup
-constexpr int kSmallThreads = 512, kSmallSide = 64, kSmallBatch = 40;
+constexpr int kSmallThreads = 512, kSmallSide = 64, kSmallBatch = 40, kBatch = 4;
 constexpr size_t kSmallLds = 156 * 1024;
 
 struct SmallBatch {
@@ -70,18 +104,39 @@ __global__ __launch_bounds__(kSmallThreads) void muon_small_kernel(SmallBatch ba
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, c = lane & 15;
   constexpr int NW = kSmallThreads / 64;
 
-  for (int i = tid; i < sp * ld; i += kSmallThreads) X[i] = 0.f;
-  __syncthreads();
+  // what pads X's rows and columns
+  for (int i = tid; i < sp * ld; i += kSmallThreads)
+    if (i >= s * ld || i % ld >= l) X[i] = 0.f;
   double sum = 0;
-  for (int i = tid; i < T.rows * T.cols; i += kSmallThreads) {
-    const int r = i / T.cols, k = i - r * T.cols;
-    const float gr = get<BF>(T.g, at + i);
-    const float m = fmaf(h.mu, T.m[at + i], gr);
-    T.m[at + i] = m;
-    const float u = h.nesterov ? fmaf(h.mu, m, gr) : m;
-    sum += (double)u * u;
-    X[tall ? k * ld + r : r * ld + k] = u;
-  }
+  // kBatch groups of neighbours are in flight together (one after the other, 2048 x 16 took 45 us to come in)
+  auto start = [&](auto n) {
+    constexpr int N = decltype(n)::value;
+    const int per = T.cols / N, all = T.rows * per;
+    for (int i0 = tid; i0 < all; i0 += kBatch * kSmallThreads) {
+      float g[kBatch][N], m[kBatch][N], u[N];
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) {
+        const int64_t e = at + (int64_t)min(i0 + q * kSmallThreads, all - 1) * N;
+        get_n<BF, N>(T.g, e, g[q]);
+        get_n<false, N>(T.m, e, m[q]);
+      }
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) {
+        const int i = i0 + q * kSmallThreads;
+        if (i >= all) break;
+        momentum<N>(h, g[q], m[q], u);
+        put_n<false, N>(T.m, at + (int64_t)i * N, m[q]);
+        const int r = i / per, k = (i - r * per) * N;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          sum += (double)u[e] * u[e];
+          X[tall ? (k + e) * ld + r : r * ld + k + e] = u[e];
+        }
+      }
+    }
+  };
+  if (T.cols % 4 == 0) start(std::integral_constant<int, 4>{});
+  else start(std::integral_constant<int, 1>{});
   sum = wave_sum(sum);
   if (lane == 0) dred[wave] = sum;
   __syncthreads();
@@ -163,16 +218,31 @@ __global__ __launch_bounds__(kSmallThreads) void muon_small_kernel(SmallBatch ba
     __syncthreads();
   }
   const float f = h.lr * T.scale;
-  for (int i = tid; i < T.rows * T.cols; i += kSmallThreads) {
-    const int r = i / T.cols, k = i - r * T.cols;
-    const float o = X[tall ? k * ld + r : r * ld + k];
-    put<BF>(T.p, at + i, fmaf(-f, o, get<BF>(T.p, at + i) * h.keep));
-  }
+  auto finish = [&](auto n) {
+    constexpr int N = decltype(n)::value;
+    const int per = T.cols / N, all = T.rows * per;
+    for (int i0 = tid; i0 < all; i0 += kBatch * kSmallThreads) {
+      float w[kBatch][N];
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) get_n<BF, N>(T.p, at + (int64_t)min(i0 + q * kSmallThreads, all - 1) * N, w[q]);
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) {
+        const int i = i0 + q * kSmallThreads;
+        if (i >= all) break;
+        const int r = i / per, k = (i - r * per) * N;
+#pragma unroll
+        for (int e = 0; e < N; ++e) w[q][e] = fmaf(-f, X[tall ? (k + e) * ld + r : r * ld + k + e], w[q][e] * h.keep);
+        put_n<BF, N>(T.p, at + (int64_t)i * N, w[q]);
+      }
+    }
+  };
+  if (T.cols % 4 == 0) finish(std::integral_constant<int, 4>{});
+  else finish(std::integral_constant<int, 1>{});
 }
 
 // ------------------------------------------------------------------------------ large matrices
 constexpr int kGroup = 40;           // tensors of one size in a launch
-constexpr int kNormParts = 64;       // workgroups of a matrix's norm
+constexpr int kNormParts = 256;      // workgroups of a matrix's norm
 // Scales of the planes: |X| <= 1.3, |A| <= 1.7 and |P| <= 3.5 stay below fp16's 65504, and small entries keep their bits
 constexpr float kX = 8192.f, kA = 8192.f, kP = 8192.f;
 
@@ -195,19 +265,22 @@ __device__ inline const MuonTensor& tensor_of(const MuonGroup& G, int mat, int64
 }
 
 // m = mu m + g, and the sums of u^2.
-template <bool BF>
+template <bool BF, int N>
 __global__ __launch_bounds__(256) void muon_momentum_kernel(MuonGroup G, MuonHyper h) {
   __shared__ double red[4];
   int64_t at;
   const MuonTensor& T = tensor_of(G, blockIdx.y, at);
-  const int64_t n = (int64_t)G.s * G.l;
+  const int64_t n = (int64_t)G.s * G.l / N;
   double sum = 0;
+#pragma unroll 2
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)kNormParts * 256) {
-    const float gr = get<BF>(T.g, at + i);
-    const float m = fmaf(h.mu, T.m[at + i], gr);
-    T.m[at + i] = m;
-    const float u = h.nesterov ? fmaf(h.mu, m, gr) : m;
-    sum += (double)u * u;
+    float g[N], m[N], u[N];
+    get_n<BF, N>(T.g, at + i * N, g);
+    get_n<false, N>(T.m, at + i * N, m);
+    momentum<N>(h, g, m, u);
+    put_n<false, N>(T.m, at + i * N, m);
+#pragma unroll
+    for (int e = 0; e < N; ++e) sum += (double)u[e] * u[e];
   }
   sum = wave_sum(sum);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = sum;
@@ -215,12 +288,6 @@ __global__ __launch_bounds__(256) void muon_momentum_kernel(MuonGroup G, MuonHyp
   if (threadIdx.x == 0) G.norm[(int64_t)blockIdx.y * kNormParts + blockIdx.x] = red[0] + red[1] + red[2] + red[3];
 }
 
-template <int NP>
-__device__ inline void put_planes(uint16_t* p, int64_t plane, float v) {
-  const _Float16 hi = (_Float16)v;
-  *(_Float16*)p = hi;
-  if constexpr (NP == 2) *(_Float16*)(p + plane) = (_Float16)((v - (float)hi) * kLo);
-}
 template <int NP>
 __device__ inline void put_planes4(uint16_t* p, int64_t plane, f4 v) {
   typedef _Float16 h4 __attribute__((ext_vector_type(4)));
@@ -255,12 +322,16 @@ __global__ __launch_bounds__(256) void muon_start_kernel(MuonGroup G, MuonHyper 
   const int tid = threadIdx.x;
   int64_t at;
   const MuonTensor& T = tensor_of(G, blockIdx.y, at);
-  double sum = 0;
-  for (int i = 0; i < kNormParts; ++i) sum += G.norm[(int64_t)blockIdx.y * kNormParts + i];
+  __shared__ double red[4];
+  double sum = wave_sum(G.norm[(int64_t)blockIdx.y * kNormParts + tid]);
+  if ((tid & 63) == 0) red[tid >> 6] = sum;
+  __syncthreads();
+  sum = red[0] + red[1] + red[2] + red[3];
   const float inv = (float)((double)kX / (sqrt(sum) + (double)h.eps));
   const bool tall = T.rows > T.cols;
   const int s0 = (blockIdx.x / tiles_l) * 64, l0 = (blockIdx.x % tiles_l) * 64;
   const int r0 = tall ? l0 : s0, c0 = tall ? s0 : l0;
+#pragma unroll 8
   for (int i = tid; i < 64 * 64; i += 256) {
     const int r = i >> 6, k = i & 63;
     float u = 0.f;
@@ -274,30 +345,38 @@ __global__ __launch_bounds__(256) void muon_start_kernel(MuonGroup G, MuonHyper 
   __syncthreads();
   const int64_t plane = (int64_t)G.s * G.lp;
   uint16_t* X = G.X[0] + (int64_t)blockIdx.y * NP * plane;
-  for (int i = tid; i < 64 * 64; i += 256) {
-    const int r = i >> 6, k = i & 63;      // k beyond l: zeros up to lp
-    if (s0 + r < G.s) put_planes<NP>(X + (int64_t)(s0 + r) * G.lp + l0 + k, plane, tall ? tile[k][r] : tile[r][k]);
+#pragma unroll
+  for (int i = tid; i < 64 * 16; i += 256) {
+    const int r = i >> 4, k = (i & 15) * 4;      // k beyond l: zeros up to lp
+    if (s0 + r < G.s)
+      put_planes4<NP>(X + (int64_t)(s0 + r) * G.lp + l0 + k, plane,
+                      tall ? f4{tile[k][r], tile[k + 1][r], tile[k + 2][r], tile[k + 3][r]} : f4{tile[r][k], tile[r][k + 1], tile[r][k + 2], tile[r][k + 3]});
   }
 }
 
-// MODE 0: A = X X^T.  1: P = a I + b A + c A A.  2: X' = P X.  3: the same, into the parameters.
+// MODE 0: A = X X^T.  1: P = a I + b A + c A A.  2: X' = P X.  3: the same, into the parameters of the wide
+// matrices; 4: into the tall ones' (turned: lanes hold neighbours of a row of the parameters in both).
 template <class Pr, bool BF, int NP, int MODE>
 __global__ __launch_bounds__(Pr::kThreads) void muon_product_kernel(MuonGroup G, MuonHyper h, int from, int tm, int tn) {
   extern __shared__ char smem[];
   int mt, nt;
   tile_of(blockIdx.x, gridDim.x, tm, tn, mt, nt);
   const int mat = blockIdx.y, m0 = mt * Pr::BM, n0 = nt * Pr::BN;
+  int64_t at;
+  const MuonTensor& T = tensor_of(G, mat, at);
+  if (MODE >= 3 && (T.rows > T.cols) != (MODE == 4)) return;
   const int64_t xplane = (int64_t)G.s * G.lp, aplane = (int64_t)G.s * G.sp;
   const Operand X = {G.X[from] + (int64_t)mat * NP * xplane, G.lp, xplane, G.s, G.lp};
   const Operand A = {G.A + (int64_t)mat * NP * aplane, G.sp, aplane, G.s, G.sp};
   const Operand Q = {G.P + (int64_t)mat * NP * aplane, G.sp, aplane, G.s, G.sp};
   Pr p;
-  p.run(MODE == 1 ? A : X, MODE == 0 ? X : MODE == 1 ? A : Q, m0, n0, 0, MODE == 0 ? G.lp : G.sp, (lds_t*)smem);
+  p.run(MODE == 4 ? Q : MODE == 1 ? A : X, MODE == 0 || MODE == 4 ? X : MODE == 1 ? A : Q, m0, n0, 0, MODE == 0 ? G.lp : G.sp, (lds_t*)smem);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
+  const int rows = MODE == 4 ? G.l : G.s;
 #pragma unroll
   for (int j = 0; j < Pr::TN; ++j) {
     const int n = n0 + (wave / Pr::WM) * Pr::TN * 16 + 16 * j + c;
-    if (n >= G.s) continue;
+    if (n >= rows) continue;
 #pragma unroll
     for (int i = 0; i < Pr::TM; ++i) {
       const int m = m0 + (wave % Pr::WM) * Pr::TM * 16 + 16 * i + 4 * g;
@@ -321,15 +400,21 @@ __global__ __launch_bounds__(Pr::kThreads) void muon_product_kernel(MuonGroup G,
         if (m >= G.lp) continue;
         put_planes4<NP>(G.X[from ^ 1] + (int64_t)mat * NP * xplane + (int64_t)n * G.lp + m, xplane, v * (1.f / kP));
       } else {
-        int64_t at;
-        const MuonTensor& T = tensor_of(G, mat, at);
-        const float f = h.lr * T.scale;
+        const int cols = MODE == 4 ? G.s : G.l;
+        const float f = h.lr * T.scale * (1.f / (kP * kX));
+        const int64_t o = at + (int64_t)n * cols + m;
+        if ((cols & 3) == 0) {
+          float w[4];
+          if (m >= cols) continue;
+          get_n<BF, 4>(T.p, o, w);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (m + e < G.l) {
-            const int64_t o = at + (T.rows > T.cols ? (int64_t)(m + e) * T.cols + n : (int64_t)n * T.cols + m + e);
-            put<BF>(T.p, o, fmaf(-f, v[e] * (1.f / (kP * kX)), get<BF>(T.p, o) * h.keep));
-          }
+          for (int e = 0; e < 4; ++e) w[e] = fmaf(-f, v[e], w[e] * h.keep);
+          put_n<BF, 4>(T.p, o, w);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (m + e < cols) put<BF>(T.p, o + e, fmaf(-f, v[e], get<BF>(T.p, o + e) * h.keep));
+        }
       }
     }
   }
@@ -346,32 +431,43 @@ hipError_t go(dim3 grid, hipStream_t s, const MuonGroup& G, const MuonHyper& h, 
 // The largest tiles that still give every CU one.
 template <bool BF, int NP, int MODE>
 hipError_t product(const MuonGroup& G, const MuonHyper& h, int from, int mats, hipStream_t s) {
-  constexpr Side SA = MODE >= 2 ? COL : ROW;
-  const int M = MODE >= 2 ? G.lp : G.sp, N = G.s;
+  constexpr Side SA = MODE == 2 || MODE == 3 ? COL : ROW, SB = MODE == 4 ? COL : ROW;
+  const int M = MODE == 2 || MODE == 3 ? G.lp : G.sp, N = MODE == 4 ? G.l : G.s;
   auto tiles = [&](int b) { return ceil_div(M, b) * ceil_div(N, b) * mats; };
-#define KRON_MUON_GO(B, ...)                                                                                        \
+#define KRON_MUON_GO(B, NS, ...)                                                                                    \
   {                                                                                                                 \
-    typedef Product<__VA_ARGS__, SA, ROW, false, NP> Pr;                                                            \
+    typedef Product<__VA_ARGS__, SA, SB, false, NP, NS> Pr;                                                         \
     const int tm = (int)ceil_div(M, B), tn = (int)ceil_div(N, B);                                                   \
     return go<Pr, muon_product_kernel<Pr, BF, NP, MODE>>(dim3((unsigned)(tm * tn), (unsigned)mats), s, G, h, from, tm, tn); \
   }
-  if (tiles(256) >= 256) KRON_MUON_GO(256, 2, 4, 8, 4)
-  if (tiles(128) >= 256) KRON_MUON_GO(128, 2, 2, 4, 4)
-  KRON_MUON_GO(64, 2, 2, 2, 2)
+  if (tiles(256) >= 256) KRON_MUON_GO(256, 2, 2, 4, 8, 4)
+  if (tiles(128) >= 256) KRON_MUON_GO(128, 4, 2, 2, 4, 4)
+  KRON_MUON_GO(64, 4, 2, 2, 2, 2)
 #undef KRON_MUON_GO
 }
 
 template <bool BF>
 hipError_t run_group(const MuonGroup& G, const MuonHyper& h, int mats, hipStream_t s) {
   constexpr int NP = BF ? 1 : 2;
-  hipLaunchKernelGGL((muon_momentum_kernel<BF>), dim3(kNormParts, (unsigned)mats), dim3(256), 0, s, G, h);
+  const dim3 grid(kNormParts, (unsigned)mats);
+  // (a matrix starts at a multiple of four values where all have as many)
+  if ((int64_t)G.s * G.l % 4 == 0) hipLaunchKernelGGL((muon_momentum_kernel<BF, 4>), grid, dim3(256), 0, s, G, h);
+  else hipLaunchKernelGGL((muon_momentum_kernel<BF, 1>), grid, dim3(256), 0, s, G, h);
   const int tl = G.lp / 64, ts = (int)ceil_div(G.s, 64);
   hipLaunchKernelGGL((muon_start_kernel<BF, NP>), dim3((unsigned)(tl * ts), (unsigned)mats), dim3(256), 0, s, G, h, tl);
+  bool wide = false, tall = false;
+  for (int i = 0; i < G.n; ++i) (G.t[i].rows > G.t[i].cols ? tall : wide) = true;
   hipError_t e = hipGetLastError();
   for (int i = 0; i < h.steps && e == hipSuccess; ++i) {
     e = product<BF, NP, 0>(G, h, i & 1, mats, s);
     if (e == hipSuccess) e = product<BF, NP, 1>(G, h, i & 1, mats, s);
-    if (e == hipSuccess) e = i + 1 < h.steps ? product<BF, NP, 2>(G, h, i & 1, mats, s) : product<BF, NP, 3>(G, h, i & 1, mats, s);
+    if (e != hipSuccess) break;
+    if (i + 1 < h.steps) {
+      e = product<BF, NP, 2>(G, h, i & 1, mats, s);
+    } else {
+      if (wide) e = product<BF, NP, 3>(G, h, i & 1, mats, s);
+      if (tall && e == hipSuccess) e = product<BF, NP, 4>(G, h, i & 1, mats, s);
+    }
   }
   return e;
 }

@@ -107,24 +107,25 @@ __device__ inline u4 fragment(const lds_t* lds, int at, int i, int kk, int lane)
   }
 }
 
-// WM x WN wavefronts, each TM x TN blocks of 16 x 16; two steps' tiles in LDS, NP planes.
+// WM x WN wavefronts, each TM x TN blocks of 16 x 16; NS steps' tiles in LDS (two, more for small tiles, whose steps are
+// shorter than their loads), NP planes.
 //
 // A step is two halves of 32 products.  While one half's fragments are multiplied the next half's come out of LDS.  Between
 // the halves a barrier: behind it the next step's tiles are in LDS, its first fragments are read, and this step's tiles,
-// all in registers by then, make room for the step after it, whose loads go out between the products (issued together
-// they hold the wavefronts up: dW of 768 x 21760 over 8192 rows 303 -> 280 us) and have a step's time.
+// all in registers by then, make room for step t + NS's, whose loads go out between the products (issued together
+// they hold the wavefronts up: dW of 768 x 21760 over 8192 rows 303 -> 280 us) and have NS - 1 steps' time.
 //
 // 256 x 256 tiles of eight wavefronts: 8192 x 8256 x 8192 bf16 runs at 1,370 TFLOP/s.  Registers alone would do 1,660 with
 // this instruction and such values (the clock falls to 2.0 GHz with the power they take; 2,090 with zeros), loads alone
 // 1,700, reads of LDS alone 4,850.  Measured beside it: 32 x 32 blocks (1,810 out of registers) 1,080-1,150; four
 // wavefronts of 128 x 128 each 1,000; steps of 32 with three to five in LDS 960-1,040; raised wave priority 1,265; reads,
 // loads and products interleaved by hand 1,350.
-template <int WM_, int WN_, int TM_, int TN_, Side SA_, Side SB_, bool BF_, int NP_>
+template <int WM_, int WN_, int TM_, int TN_, Side SA_, Side SB_, bool BF_, int NP_, int NS_ = 2>
 struct Product {
-  static constexpr int WM = WM_, WN = WN_, TM = TM_, TN = TN_, NP = NP_;
+  static constexpr int WM = WM_, WN = WN_, TM = TM_, TN = TN_, NP = NP_, NS = NS_;
   static constexpr int BM = WM * TM * 16, BN = WN * TN * 16, NW = WM * WN, kThreads = 64 * NW;
   static constexpr int kStage = (BM + BN) * kBK * 2;
-  static constexpr int kLdsBytes = 2 * kStage;
+  static constexpr int kLdsBytes = NS * kStage;
   f4 acc[TM][TN];
 
   struct Half {
@@ -147,9 +148,10 @@ struct Product {
     }
   }
   static constexpr int kLoads = TileLoad<SA_, BM, NW>::kLoads + TileLoad<SB_, BN, NW>::kLoads;
-  // What this wavefront loads and reads is there, and so it is for all of them.
+  // What this wavefront reads is there, and what it loads but for the last STAGES tiles; and so it is for all of them.
+  template <int STAGES>
   __device__ static void in_step() {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(STAGES * kLoads) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   }
@@ -190,11 +192,12 @@ struct Product {
     };
     Half f0, f1;
     all(0);
-    in_step();
-    all(1);
+    in_step<0>();
+#pragma unroll
+    for (int i = 1; i < NS; ++i) all(i);
     read(f0, lds, 0, wm, wn, lane);
+    int st = 0;
     auto step = [&](int t, auto more) {
-      const int st = t & 1;
       if constexpr (NP == 2) {
         if (t == 2 * steps) {      // the products with a second part are in
 #pragma unroll
@@ -205,8 +208,9 @@ struct Product {
       }
       read(f1, lds + st * kStage, 1, wm, wn, lane);
       multiply(f0, [](int) {});
-      in_step();
-      read(f0, lds + (st ^ 1) * kStage, 0, wm, wn, lane);      // (behind the last step: of no use, and not used)
+      in_step<more ? NS - 2 : 0>();
+      const int after = st + 1 == NS ? 0 : st + 1;
+      read(f0, lds + after * kStage, 0, wm, wn, lane);      // (behind the last step: of no use, and not used)
       multiply(f1, [&](int i) {
         if (!more) return;
         constexpr int per = (kLoads + TM - 1) / TM;
@@ -215,9 +219,10 @@ struct Product {
           if (i * per + q < kLoads) load(st, i * per + q);
       });
       if (more) loaded();
+      st = after;
     };
     int t = 0;
-    for (; t < total - 2; ++t) step(t, std::true_type{});
+    for (; t < total - NS; ++t) step(t, std::true_type{});
     for (; t < total; ++t) step(t, std::false_type{});
     __syncthreads();
   }
@@ -236,7 +241,7 @@ __device__ inline void tile_of(int id, int count, int tm, int tn, int& mt, int& 
 // through the LDS of the wavefront, so that whole lines are written (dz of 8192 x 12288: 195 -> 173 us against eight
 // bytes of each of sixteen rows at a time).  value(i, j): the four values of row(i) .. + 3, column j.
 template <class P, class F>
-__device__ inline void store_rows(char* smem, uint16_t* out, int64_t ld, int rows, const F& value) {
+__device__ __forceinline__ void store_rows(char* smem, uint16_t* out, int64_t ld, int rows, const F& value) {
   constexpr int RB = P::TM * 32, CH = RB / 16, PR = 64 / CH;      // bytes and 16-byte pieces of a row, rows at a time
   static_assert(CH * PR == 64, "");
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;

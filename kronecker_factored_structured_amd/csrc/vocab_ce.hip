@@ -329,7 +329,7 @@ __global__ __launch_bounds__(P::kThreads) void vocab_dz_kernel(VocabCE a, int v0
   } else {
     // the first parts, and what they leave, in the sums' place, as the second ones
     typedef _Float16 h4 __attribute__((ext_vector_type(4)));
-    auto part = [&](int i, int j) {
+    auto part = [&](int i, int j) __attribute__((always_inline)) {
       const f4 v = p.acc[i][j];
       const h4 h = {(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
       p.acc[i][j] = f4{v[0] - (float)h[0], v[1] - (float)h[1], v[2] - (float)h[2], v[3] - (float)h[3]} * kLo;
