@@ -37,7 +37,8 @@ def _need(t: Optional[torch.Tensor], name: str, shape: tuple, dtype=torch.float3
     """t (if given) must be a contiguous GPU tensor of exactly this shape and dtype (on
     `device` when one is given): libkron derives every extent from the sizes it is passed,
     so a tensor of another shape would be read or written past its end."""
-    if t is None:
+    if t is None or (t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()
+                     and (device is None or t.device == device)):
         return
     _dev(t, name, dtype)
     if tuple(t.shape) != tuple(shape):
@@ -860,21 +861,26 @@ def kron_muon_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor]
         return
     dev, dtype = params[0].device, params[0].dtype
     dt = _dtype_code(params[0])
+    _dev(params[0], "param[0]", dtype)
     count, rows, cols = [], [], []
-    for i in range(nt):
-        p = params[i]
-        _dev(p, f"param[{i}]", dtype)
-        if p.device != dev:
-            raise ValueError(f"param[{i}] is on {p.device}, expected {dev}")
-        if p.dim() < 2:
-            raise ValueError(f"param[{i}] must hold matrices, got {tuple(p.shape)}")
-        _need(grads[i], f"grad[{i}]", tuple(p.shape), dtype, dev)
-        _need(m[i], f"m[{i}]", tuple(p.shape), torch.float32, dev)
-        r, c = p.shape[-2:]
-        n = p.numel()
-        count.append(n // (r * c) if n else 0)
-        rows.append(max(r, 1))
-        cols.append(max(c, 1))
+    f32, index = torch.float32, dev.index
+    for i, (p, g, q) in enumerate(zip(params, grads, m)):
+        shape = p.shape
+        # (a model's many small tensors: one look at what is almost always so, 1 us of a tensor's 3)
+        if not (p.dtype is dtype and g.dtype is dtype and q.dtype is f32 and g.shape == shape and q.shape == shape
+                and p.get_device() == g.get_device() == q.get_device() == index
+                and p.is_contiguous() and g.is_contiguous() and q.is_contiguous()) or len(shape) < 2:
+            _dev(p, f"param[{i}]", dtype)
+            if p.device != dev:
+                raise ValueError(f"param[{i}] is on {p.device}, expected {dev}")
+            if p.dim() < 2:
+                raise ValueError(f"param[{i}] must hold matrices, got {tuple(shape)}")
+            _need(g, f"grad[{i}]", shape, dtype, dev)
+            _need(q, f"m[{i}]", shape, torch.float32, dev)
+        r, c = shape[-2], shape[-1]
+        count.append(shape.numel() // (r * c) if r * c else 0)
+        rows.append(r or 1)
+        cols.append(c or 1)
     if scales is None:
         scales = [max(1.0, r / c) ** 0.5 for r, c in zip(rows, cols)]
     arr = ctypes.c_void_p * nt

@@ -3,8 +3,8 @@
 //   y = base + s_e (x D_e^T) U_e^T
 //   backward, t = s_e x D_e^T and g = s_e dy U_e:  dx = base + g D_e,  dD_e = g^T x,  dU_e = dy^T t
 // Sixteen rows of one request are a workgroup's: their inner product stays on chip, x is read once and y written
-// once.  All products run on the fp32 matrix instruction (bf16 values are exact in it): the work is bound by
-// memory, and neither the inner products nor the gradients are rounded on the way.
+// once.  bf16 x and D_e are multiplied by the bf16 matrix instruction (exact products), everything else by the fp32
+// one: neither the inner products nor the gradients are rounded on the way.
 #include <algorithm>
 
 #include "kron_internal.h"
@@ -15,47 +15,81 @@ namespace {
 
 typedef float f4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+typedef __bf16 b8 __attribute__((ext_vector_type(8)));
 
 constexpr int kRows = 16;            // rows of a tile
 constexpr int kThreads = 256, kWaves = 4;
 
 __device__ inline f4 mma32(float a, float b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
+__device__ inline f4 mma16(u4 a, u4 b, f4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b8, a), __builtin_bit_cast(b8, b), c, 0, 0, 0);
+}
 
-// Four neighbouring values of a row at p + i; those from `end` on are zero.  VEC: the row and i are multiples of four.
-template <bool BF, bool VEC>
-__device__ inline f4 load4(const void* p, int64_t i, int left) {
-  f4 v = {0, 0, 0, 0};
-  if (VEC) {
-    if (left <= 0) return v;
-    if (BF) {
-      const uint2 w = *(const uint2*)((const uint16_t*)p + i);
-      return f4{bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
-    }
-    return *(const f4*)((const float*)p + i);
-  }
+// Sixteen bytes of a row (four fp32 values, eight bf16), of which `left` values are in it; the others are zero.  Rows
+// may start at any element (the memory pipes take a vector at any address, once aligned to its elements).
+template <bool BF>
+__device__ inline u4 load16(const void* p, int64_t i, int left) {
+  constexpr int N = BF ? 8 : 4;
+  const char* q = (const char*)p + i * (BF ? 2 : 4);
+  u4 v = {0, 0, 0, 0};
+  if (left >= N) {
+    __builtin_memcpy(&v, q, 16);
+  } else {
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (e < left) v[e] = BF ? __uint_as_float((uint32_t)((const uint16_t*)p)[i + e] << 16) : ((const float*)p)[i + e];
+    for (int e = 0; e < N; ++e)
+      if (e < left) {
+        if (BF) v[e / 2] |= (uint32_t)((const uint16_t*)q)[e] << (16 * (e & 1));
+        else v[e] = ((const uint32_t*)q)[e];
+      }
+  }
   return v;
 }
-template <bool BF, bool VEC>
-__device__ inline void store4(void* p, int64_t i, int left, f4 v) {
-  if (VEC) {
-    if (left <= 0) return;
-    if (BF) *(uint2*)((uint16_t*)p + i) = uint2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
-    else *(f4*)((float*)p + i) = v;
-    return;
+// Four neighbours as fp32.
+template <bool BF>
+__device__ inline f4 load4(const void* p, int64_t i, int left) {
+  if (!BF) return __builtin_bit_cast(f4, load16<false>(p, i, left));
+  const char* q = (const char*)p + i * 2;
+  uint2 w = {0, 0};
+  if (left >= 4) {
+    __builtin_memcpy(&w, q, 8);
+  } else {
+    if (left > 0) w.x = ((const uint16_t*)q)[0];
+    if (left > 1) w.x |= (uint32_t)((const uint16_t*)q)[1] << 16;
+    if (left > 2) w.y = ((const uint16_t*)q)[2];
   }
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (e < left) {
-      if (BF) ((uint16_t*)p)[i + e] = (uint16_t)bf16_rne(v[e]);
-      else ((float*)p)[i + e] = v[e];
-    }
+  return f4{bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
 }
 template <bool BF>
 __device__ inline float load1(const void* p, int64_t i) {
   return BF ? __uint_as_float((uint32_t)((const uint16_t*)p)[i] << 16) : ((const float*)p)[i];
+}
+// Value e of what load16 gave.
+template <bool BF>
+__device__ inline float value(const u4& v, int e) {
+  if (BF) return (e & 1) ? bf16_hi(v[e / 2]) : bf16_lo(v[e / 2]);
+  return __uint_as_float(v[e & 3]);
+}
+// base + acc of N neighbours (fp32: 4, bf16: 8), `left` of them in the row, rounded once.
+template <bool BF>
+__device__ inline void store16(void* p, int64_t i, int left, const u4& base, const f4* acc) {
+  constexpr int N = BF ? 8 : 4;
+  float v[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) v[e] = value<BF>(base, e) + acc[e / 4][e & 3];
+  char* q = (char*)p + i * (BF ? 2 : 4);
+  u4 o;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) o[w] = BF ? bf16_pair(v[(2 * w) % N], v[(2 * w + 1) % N]) : __float_as_uint(v[w % N]);
+  if (left >= N) {
+    __builtin_memcpy(q, &o, 16);
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (e < left) {
+        if (BF) ((uint16_t*)q)[e] = (uint16_t)(o[e / 2] >> (16 * (e & 1)));
+        else ((uint32_t*)q)[e] = o[e & 3];
+      }
+  }
 }
 
 // Segment i of B + 2: the requests, and the rows before the first and behind the last one (no adapter).
@@ -107,24 +141,10 @@ __device__ inline Tile find_tile(const Adapters& a, int64_t w, int* sh) {
   return {r0, (int)min<int64_t>(kRows, r1 - r0), i == 0 || i == a.B + 1 ? -1 : a.ids[i - 1]};
 }
 
-// t[16][R] = f v w^T for the tile's rows of v (width n) and w (R x n): the wavefronts share the contraction.
-template <bool BF, bool VEC, int RT>
-__device__ inline void inner(const Adapters& a, const Tile& T, const void* v, const void* w, int n, float f, float* red, float* t) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
-  f4 acc[RT];
-#pragma unroll
-  for (int i = 0; i < RT; ++i) acc[i] = f4{0, 0, 0, 0};
-  const int64_t vrow = (T.row + min(c, T.rows - 1)) * n;
-  for (int k = wave * 16; k < n; k += kWaves * 16) {
-    const int at = k + 4 * g;
-    const f4 x = load4<BF, VEC>(v, vrow + at, n - at);
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      const f4 d = load4<BF, VEC>(w, (int64_t)min(16 * i + c, a.R - 1) * n + at, n - at);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) acc[i] = mma32(x[q], d[q], acc[i]);      // rows x rank
-    }
-  }
+// The wavefronts' parts of a 16 x R product, joined, times f: t[16][RT * 16 + 4].
+template <int RT>
+__device__ inline void join(const Adapters& a, const f4* acc, float f, float* red, float* t) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
   for (int i = 0; i < RT; ++i) *(f4*)(red + ((wave * RT + i) * 64 + lane) * 4) = acc[i];
   __syncthreads();
@@ -139,37 +159,78 @@ __device__ inline void inner(const Adapters& a, const Tile& T, const void* v, co
   __syncthreads();
 }
 
-// g[16][R] = f v w for w (n x R): w's values one by one, sixteen neighbours of a row together.
-template <bool BF, bool VEC, int RT>
-__device__ inline void inner_t(const Adapters& a, const Tile& T, const void* v, const void* w, int n, float f, float* red, float* t) {
+// t = f v w^T for the tile's rows of v (width n) and w (R x n): the wavefronts share the contraction, each with
+// kBatch blocks of it in flight (a block's latency after the other's, 64 tokens of 1024 -> 4096 took 13.7 us).
+template <bool BF, int RT>
+__device__ inline void inner(const Adapters& a, const Tile& T, const void* v, const void* w, int n, float f, float* red, float* t) {
+  constexpr int KB = BF ? 32 : 16, VE = BF ? 8 : 4, kBatch = RT >= 8 ? 1 : 8 / RT;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
   f4 acc[RT];
 #pragma unroll
   for (int i = 0; i < RT; ++i) acc[i] = f4{0, 0, 0, 0};
   const int64_t vrow = (T.row + min(c, T.rows - 1)) * n;
-  for (int k = wave * 16; k < n; k += kWaves * 16) {
-    const int at = k + 4 * g;
-    const f4 x = load4<BF, VEC>(v, vrow + at, n - at);
+  int64_t wrow[RT];
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      const int r = min(16 * i + c, a.R - 1);
+  for (int i = 0; i < RT; ++i) wrow[i] = (int64_t)min(16 * i + c, a.R - 1) * n;
+  for (int k = wave * KB; k < n; k += kBatch * kWaves * KB) {
+    u4 x[kBatch], d[kBatch][RT];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) acc[i] = mma32(x[q], load1<BF>(w, (int64_t)min(at + q, n - 1) * a.R + r), acc[i]);
+    for (int b = 0; b < kBatch; ++b) {
+      const int at = k + b * kWaves * KB + VE * g;
+      x[b] = load16<BF>(v, vrow + at, n - at);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) d[b][i] = load16<BF>(w, wrow[i] + at, n - at);
     }
-  }
 #pragma unroll
-  for (int i = 0; i < RT; ++i) *(f4*)(red + ((wave * RT + i) * 64 + lane) * 4) = acc[i];
-  __syncthreads();
-  for (int e = threadIdx.x; e < RT * 256; e += kThreads) {
-    const int i = e >> 8, ln = (e & 255) >> 2, q = e & 3;
-    float s = 0.f;
+    for (int b = 0; b < kBatch; ++b)
 #pragma unroll
-    for (int k = 0; k < kWaves; ++k) s += red[(k * RT * 64) * 4 + e];
-    const int r = 16 * i + (ln & 15);
-    t[(4 * (ln >> 4) + q) * (RT * 16 + 4) + r] = r < a.R ? s * f : 0.f;
+      for (int i = 0; i < RT; ++i) {
+        if constexpr (BF) {
+          acc[i] = mma16(x[b], d[b][i], acc[i]);      // rows x rank
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) acc[i] = mma32(value<false>(x[b], q), value<false>(d[b][i], q), acc[i]);
+        }
+      }
   }
-  __syncthreads();
+  join<RT>(a, acc, f, red, t);
 }
+
+// g = f v w for w (n x R): w's values one by one, sixteen neighbours of a row together.
+template <bool BF, int RT>
+__device__ inline void inner_t(const Adapters& a, const Tile& T, const void* v, const void* w, int n, float f, float* red, float* t) {
+  constexpr int KB = BF ? 32 : 16, VE = BF ? 8 : 4, kBatch = RT >= 4 ? 1 : (BF ? 4 : 8) / RT;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
+  f4 acc[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) acc[i] = f4{0, 0, 0, 0};
+  const int64_t vrow = (T.row + min(c, T.rows - 1)) * n;
+  for (int k = wave * KB; k < n; k += kBatch * kWaves * KB) {
+    u4 x[kBatch];
+    float u[kBatch][RT][VE];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int at = k + b * kWaves * KB + VE * g;
+      x[b] = load16<BF>(v, vrow + at, n - at);
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int q = 0; q < VE; ++q) u[b][i][q] = load1<BF>(w, (int64_t)min(at + q, n - 1) * a.R + min(16 * i + c, a.R - 1));
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int q = 0; q < VE; ++q) acc[i] = mma32(value<BF>(x[b], q), u[b][i][q], acc[i]);
+  }
+  join<RT>(a, acc, f, red, t);
+}
+
+// Column of a row of y or dx that lane c of block h (of the two that bf16 takes together) stands for: the lane that
+// holds rows 4 g .. 4 g + 3 of both results then has eight neighbours, 16 bytes.
+template <bool BF>
+__device__ inline int column(int c, int h) { return BF ? 8 * (c >> 2) + 4 * h + (c & 3) : c; }
 
 // Rows without an adapter: out = base (zeros without one), NaN where the id is none of the table's.
 template <bool BF>
@@ -196,7 +257,7 @@ struct Shared {
   int find[8];
 };
 
-template <bool BF, bool VEC, bool RVEC, int RT>
+template <bool BF, int RT>
 __global__ __launch_bounds__(kThreads) void adapters_fwd_kernel(Adapters a) {
   __shared__ Shared<RT> sh;
   const Tile T = find_tile(a, blockIdx.x, sh.find);
@@ -205,32 +266,50 @@ __global__ __launch_bounds__(kThreads) void adapters_fwd_kernel(Adapters a) {
     plain_rows<BF>(a, T, a.base, a.y, a.M, blockIdx.y, gridDim.y);
     return;
   }
+  constexpr int H = BF ? 2 : 1, W = 16 * H, kBatch = RT >= 4 ? 1 : 4 / RT / H + (RT == 2 && BF);
   const size_t es = BF ? 2 : 4;
   const float f = a.scales ? a.scales[T.id] : 1.f;
   const char* D = (const char*)a.down + (size_t)T.id * a.R * a.K * es;
   const char* U = (const char*)a.up + (size_t)T.id * a.R * a.M * es;
-  inner<BF, VEC, RT>(a, T, a.x, D, a.K, f, sh.red, sh.t);
+  inner<BF, RT>(a, T, a.x, D, a.K, f, sh.red, sh.t);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
   f4 t[RT];
 #pragma unroll
   for (int i = 0; i < RT; ++i) t[i] = *(const f4*)(sh.t + c * (RT * 16 + 4) + 16 * i + 4 * g);
   const int64_t row = (T.row + min(c, T.rows - 1)) * a.M;
-  for (int m = (blockIdx.y * kWaves + wave) * 16; m < a.M; m += (int)gridDim.y * kWaves * 16) {
-    f4 acc = {0, 0, 0, 0};
-    const int64_t urow = (int64_t)min(m + c, a.M - 1) * a.R;
+  const int stride = (int)gridDim.y * kWaves * W;
+  for (int m = (blockIdx.y * kWaves + wave) * W; m < a.M; m += kBatch * stride) {
+    f4 u[kBatch][H][RT];
+    u4 base[kBatch];
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      const f4 u = load4<BF, RVEC>(U, urow + 16 * i + 4 * g, a.R - 16 * i - 4 * g);
+    for (int b = 0; b < kBatch; ++b) {
+      const int m0 = m + b * stride, at = m0 + 4 * H * g;
+      base[b] = load16<BF>(a.base, row + at, a.M - at);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) acc = mma32(u[q], t[i][q], acc);      // columns of y x rows
+      for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+          u[b][h][i] = load4<BF>(U, (int64_t)min(m0 + column<BF>(c, h), a.M - 1) * a.R + 16 * i + 4 * g, a.R - 16 * i - 4 * g);
     }
-    const int at = m + 4 * g;
-    if (c < T.rows) store4<BF, VEC>(a.y, row + at, a.M - at, load4<BF, VEC>(a.base, row + at, a.M - at) + acc);
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      f4 acc[H];
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        acc[h] = f4{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) acc[h] = mma32(u[b][h][i][q], t[i][q], acc[h]);      // columns of y x rows
+      }
+      const int at = m + b * stride + 4 * H * g;
+      if (c < T.rows) store16<BF>(a.y, row + at, a.M - at, base[b], acc);
+    }
   }
 }
 
 // The rows' part of the backward: t and g of each row for the gradients' kernel, and dx.
-template <bool BF, bool VEC, int RT>
+template <bool BF, int RT>
 __global__ __launch_bounds__(kThreads) void adapters_rows_kernel(Adapters a) {
   __shared__ Shared<RT> sh;
   const Tile T = find_tile(a, blockIdx.x, sh.find);
@@ -239,12 +318,13 @@ __global__ __launch_bounds__(kThreads) void adapters_rows_kernel(Adapters a) {
     if (a.y) plain_rows<BF>(a, T, a.base, a.y, a.K, 0, 1);
     return;
   }
+  constexpr int H = BF ? 2 : 1, W = 16 * H, kBatch = RT >= 4 ? 1 : 4 / RT / H + (RT == 2 && BF);
   const size_t es = BF ? 2 : 4;
   const float f = a.scales ? a.scales[T.id] : 1.f;
   const char* D = (const char*)a.down + (size_t)T.id * a.R * a.K * es;
   const char* U = (const char*)a.up + (size_t)T.id * a.R * a.M * es;
-  inner<BF, VEC, RT>(a, T, a.x, D, a.K, f, sh.red, sh.t);
-  inner_t<BF, VEC, RT>(a, T, a.dy, U, a.M, f, sh.red, sh.g);
+  inner<BF, RT>(a, T, a.x, D, a.K, f, sh.red, sh.t);
+  inner_t<BF, RT>(a, T, a.dy, U, a.M, f, sh.red, sh.g);
   float* keep = a.ws + T.row * 2 * (RT * 16);
   for (int e = threadIdx.x; e < T.rows * RT * 16; e += kThreads) {
     const int r = e / (RT * 16), k = e % (RT * 16);
@@ -257,43 +337,61 @@ __global__ __launch_bounds__(kThreads) void adapters_rows_kernel(Adapters a) {
 #pragma unroll
   for (int i = 0; i < RT; ++i) t[i] = *(const f4*)(sh.g + c * (RT * 16 + 4) + 16 * i + 4 * g);
   const int64_t row = (T.row + min(c, T.rows - 1)) * a.K;
-  for (int k = wave * 16; k < a.K; k += kWaves * 16) {
-    f4 acc = {0, 0, 0, 0};
-    const int col = min(k + c, a.K - 1);
+  for (int k = wave * W; k < a.K; k += kBatch * kWaves * W) {
+    float d[kBatch][H][RT][4];
+    u4 base[kBatch];
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
+    for (int b = 0; b < kBatch; ++b) {
+      const int k0 = k + b * kWaves * W, at = k0 + 4 * H * g;
+      base[b] = a.base ? load16<BF>(a.base, row + at, a.K - at) : u4{0, 0, 0, 0};
 #pragma unroll
-      for (int q = 0; q < 4; ++q) acc = mma32(load1<BF>(D, (int64_t)min(16 * i + 4 * g + q, a.R - 1) * a.K + col), t[i][q], acc);
-    const int at = k + 4 * g;
-    if (c < T.rows) {
-      if (a.base) acc += load4<BF, VEC>(a.base, row + at, a.K - at);
-      store4<BF, VEC>(a.y, row + at, a.K - at, acc);
+      for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            d[b][h][i][q] = load1<BF>(D, (int64_t)min(16 * i + 4 * g + q, a.R - 1) * a.K + min(k0 + column<BF>(c, h), a.K - 1));
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      f4 acc[H];
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        acc[h] = f4{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) acc[h] = mma32(d[b][h][i][q], t[i][q], acc[h]);
+      }
+      const int at = k + b * kWaves * W + 4 * H * g;
+      if (c < T.rows) store16<BF>(a.y, row + at, a.K - at, base[b], acc);
     }
   }
 }
 
-// The adapters' gradients: 64 columns of x (dD = g^T x) or of dy (dU = dy^T t) of one adapter, over every
-// `splits`-th block of its rows.
-constexpr int kCols = 64;
-template <bool BF, bool VEC, int RT>
+// The adapters' gradients: a block of columns of x (dD = g^T x) or of dy (dU = dy^T t) of one adapter, over every
+// `splits`-th four rows of its.  A lane has NC neighbouring columns: column NC c + q is lane c's of product q.
+template <bool BF, int RT>
+constexpr int lane_cols() { return BF && RT <= 2 ? 8 : 4; }
+template <bool BF, int RT>
 __global__ __launch_bounds__(kThreads) void adapters_params_kernel(Adapters a, int kblocks, int splits, float* part) {
-  __shared__ float red[kWaves][RT * 4][256];
+  constexpr int NC = lane_cols<BF, RT>(), kBatch = RT >= 4 ? 2 : 4;
+  __shared__ float red[kWaves][RT * NC][256];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
   const int e = blockIdx.y, split = blockIdx.z;
   const bool up = (int)blockIdx.x >= kblocks;
-  const int n = up ? a.M : a.K, col0 = (up ? blockIdx.x - kblocks : blockIdx.x) * kCols;
+  const int n = up ? a.M : a.K, col0 = (up ? blockIdx.x - kblocks : blockIdx.x) * 16 * NC, mine = col0 + NC * c;
   const void* v = up ? a.dy : a.x;
   const float* tg = a.ws + (up ? 0 : RT * 16);
-  f4 acc[RT][4];
+  f4 acc[RT][NC];
 #pragma unroll
   for (int i = 0; i < RT; ++i)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) acc[i][q] = f4{0, 0, 0, 0};
+    for (int q = 0; q < NC; ++q) acc[i][q] = f4{0, 0, 0, 0};
   const int stride = kWaves * splits, turn = split * kWaves + wave;
   int64_t seen = 0;      // blocks of four rows before
   for (int i0 = 0; i0 < a.B; i0 += 64) {
-    const bool mine = i0 + lane < a.B && a.ids[min(i0 + lane, a.B - 1)] == e;
-    uint64_t todo = __ballot(mine);
+    uint64_t todo = __ballot(i0 + lane < a.B && a.ids[min(i0 + lane, a.B - 1)] == e);
     while (todo) {
       const int i = i0 + __builtin_ctzll(todo);
       todo &= todo - 1;
@@ -302,33 +400,49 @@ __global__ __launch_bounds__(kThreads) void adapters_params_kernel(Adapters a, i
       const int64_t blocks = (r1 - r0 + 3) / 4;
       int64_t b = (turn - seen % stride + stride) % stride;
       seen += blocks;
-      for (; b < blocks; b += stride) {
-        const int64_t row = r0 + 4 * b + g;
-        const bool in = row < r1;
-        const int64_t rr = in ? row : r0;
-        const f4 x = load4<BF, VEC>(v, rr * n + col0 + 4 * c, n - col0 - 4 * c);
+      for (; b < blocks; b += kBatch * stride) {
+        u4 x[kBatch];
+        float w[kBatch][RT];
 #pragma unroll
-        for (int k = 0; k < RT; ++k) {
-          const float w = tg[rr * 2 * RT * 16 + 16 * k + c];
+        for (int t = 0; t < kBatch; ++t) {
+          const int64_t row = r0 + 4 * (b + t * stride) + g;
+          const bool in = row < r1;
+          x[t] = u4{0, 0, 0, 0};
+          if (in) {
+            if (NC == 4 && BF) {
+              const f4 y = load4<BF>(v, row * n + mine, n - mine);
+              x[t] = __builtin_bit_cast(u4, y);
+            } else {
+              x[t] = load16<BF>(v, row * n + mine, n - mine);
+            }
+          }
 #pragma unroll
-          for (int q = 0; q < 4; ++q) acc[k][q] = mma32(in ? w : 0.f, in ? x[q] : 0.f, acc[k][q]);      // rank x columns
+          for (int k = 0; k < RT; ++k) w[t][k] = in ? tg[row * 2 * RT * 16 + 16 * k + c] : 0.f;
         }
+#pragma unroll
+        for (int t = 0; t < kBatch; ++t)
+#pragma unroll
+          for (int k = 0; k < RT; ++k)
+#pragma unroll
+            for (int q = 0; q < NC; ++q) acc[k][q] = mma32(w[t][k], value<NC == 8>(x[t], q), acc[k][q]);      // rank x columns
       }
     }
   }
 #pragma unroll
   for (int k = 0; k < RT; ++k)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) *(f4*)&red[wave][k * 4 + q][lane * 4] = acc[k][q];
+    for (int q = 0; q < NC; ++q) *(f4*)&red[wave][k * NC + q][lane * 4] = acc[k][q];
   __syncthreads();
   float* out = splits > 1 ? part + (int64_t)split * a.E * a.R * (a.K + a.M) : nullptr;
-  for (int x = threadIdx.x; x < RT * 4 * 256; x += kThreads) {
-    const int kq = x >> 8, w = x & 255;
-    const int r = 16 * (kq >> 2) + 4 * (w >> 6) + (w & 3), col = col0 + 4 * ((w >> 2) & 15) + (kq & 3);
+  for (int x = threadIdx.x; x < RT * NC * 256; x += kThreads) {
+    // dD's neighbours along the columns, dU's along the rank
+    const int k = x / (NC * 256), w = x % (NC * 256);
+    const int rr = up ? w % 16 : w / (16 * NC), cc = up ? w / 16 : w % (16 * NC);
+    const int r = 16 * k + rr, col = col0 + cc, kq = k * NC + cc % NC, ln = (rr >> 2) * 16 + cc / NC;
     if (r >= a.R || col >= n) continue;
     float s = 0.f;
 #pragma unroll
-    for (int k = 0; k < kWaves; ++k) s += red[k][kq][w];
+    for (int t = 0; t < kWaves; ++t) s += red[t][kq][ln * 4 + (rr & 3)];
     if (up) (out ? out + (int64_t)a.E * a.R * a.K : a.dup)[((int64_t)e * a.M + col) * a.R + r] = s;
     else (out ? out : a.ddown)[((int64_t)e * a.R + r) * a.K + col] = s;
   }
@@ -350,28 +464,30 @@ int rank_blocks(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8; }
 
 int64_t tiles_of(const Adapters& a) { return a.starts ? ceil_div(a.N, kRows) + a.B + 1 : a.N; }
 
+int cols_of(const Adapters& a) { return 16 * (a.bf16 && a.R <= 32 ? 8 : 4); }      // lane_cols() of sixteen lanes
+
 // Workgroups that share an adapter's rows, so that every CU has two.
 int splits_of(const Adapters& a) {
-  const int64_t groups = (ceil_div(a.K, kCols) + ceil_div(a.M, kCols)) * a.E;
+  const int64_t groups = (ceil_div(a.K, cols_of(a)) + ceil_div(a.M, cols_of(a))) * a.E;
   return (int)std::max<int64_t>(1, std::min({ceil_div(512, groups), ceil_div(a.N, 256), int64_t(16)}));
 }
 
-template <bool BF, bool VEC, bool RVEC, int RT>
+template <bool BF, int RT>
 hipError_t fwd(const Adapters& a, hipStream_t s) {
   const int64_t tiles = tiles_of(a);
   // few tiles: several workgroups share a tile's columns, each with the inner product to itself
   const int gy = (int)std::max<int64_t>(1, std::min(256 / tiles, ceil_div(a.M, kWaves * 16)));
-  hipLaunchKernelGGL((adapters_fwd_kernel<BF, VEC, RVEC, RT>), dim3((unsigned)tiles, (unsigned)gy), dim3(kThreads), 0, s, a);
+  hipLaunchKernelGGL((adapters_fwd_kernel<BF, RT>), dim3((unsigned)tiles, (unsigned)gy), dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 
-template <bool BF, bool VEC, int RT>
+template <bool BF, int RT>
 hipError_t bwd(const Adapters& a, hipStream_t s) {
-  if (a.N) hipLaunchKernelGGL((adapters_rows_kernel<BF, VEC, RT>), dim3((unsigned)tiles_of(a)), dim3(kThreads), 0, s, a);
-  const int splits = splits_of(a), kb = (int)ceil_div(a.K, kCols), mb = (int)ceil_div(a.M, kCols);
+  if (a.N) hipLaunchKernelGGL((adapters_rows_kernel<BF, RT>), dim3((unsigned)tiles_of(a)), dim3(kThreads), 0, s, a);
+  const int splits = splits_of(a), kb = (int)ceil_div(a.K, cols_of(a)), mb = (int)ceil_div(a.M, cols_of(a));
   float* part = (float*)((char*)a.ws + up256(sizeof(float) * (size_t)a.N * 2 * RT * 16));
-  hipLaunchKernelGGL((adapters_params_kernel<BF, VEC, RT>), dim3((unsigned)(kb + mb), (unsigned)a.E, (unsigned)splits), dim3(kThreads), 0, s, a,
-                     kb, splits, part);
+  hipLaunchKernelGGL((adapters_params_kernel<BF, RT>), dim3((unsigned)(kb + mb), (unsigned)a.E, (unsigned)splits), dim3(kThreads), 0, s, a, kb,
+                     splits, part);
   if (splits > 1) {
     const int64_t n = (int64_t)a.E * a.R * (a.K + a.M);
     hipLaunchKernelGGL(adapters_join_kernel, dim3((unsigned)std::min<int64_t>(2048, ceil_div(n, kThreads))), dim3(kThreads), 0, s, a, splits, part);
@@ -379,16 +495,10 @@ hipError_t bwd(const Adapters& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <bool BF, int RT>
-hipError_t pick(const Adapters& a, bool backward, hipStream_t s) {
-  const bool vec = a.K % 4 == 0 && a.M % 4 == 0, rvec = a.R % 4 == 0;
-  if (backward) return vec ? bwd<BF, true, RT>(a, s) : bwd<BF, false, RT>(a, s);
-  if (vec) return rvec ? fwd<BF, true, true, RT>(a, s) : fwd<BF, true, false, RT>(a, s);
-  return rvec ? fwd<BF, false, true, RT>(a, s) : fwd<BF, false, false, RT>(a, s);
-}
 template <int RT>
 hipError_t pick(const Adapters& a, bool backward, hipStream_t s) {
-  return a.bf16 ? pick<true, RT>(a, backward, s) : pick<false, RT>(a, backward, s);
+  if (backward) return a.bf16 ? bwd<true, RT>(a, s) : bwd<false, RT>(a, s);
+  return a.bf16 ? fwd<true, RT>(a, s) : fwd<false, RT>(a, s);
 }
 
 }  // namespace
