@@ -498,7 +498,7 @@ kron_status_t kron_distill_bwd(const kron_distill_t* d, const void* logits, cons
  *   - A label outside [0, V) makes the loss, that row's nll and the gradients that it takes part in NaN
  *     (no out-of-bounds access).  So does a row with a NaN or a +infinity among its logits.
  *   - Sums and softmax statistics are fp32 or fp64.  fp32 operands of the products are the sum of two
- *     fp16 parts after a scaling by a power of two: off by less than 2^-22 of the value, or 2^-50 of the
+ *     fp16 parts after a scaling by a power of two: off by at most 2^-22 of the value, or 2^-40 of the
  *     tensor's largest where that is more.  For bf16 tensors the logits' gradient is rounded to
  *     bf16 once.  Every output is rounded once.
  * Limits: N <= KRON_VOCAB_CE_MAX_ROWS, K <= KRON_VOCAB_CE_MAX_WIDTH, V <= KRON_VOCAB_MAX.  N == 0 is
@@ -566,7 +566,7 @@ kron_status_t kron_adapters_bwd(const kron_adapters_t* d, const void* x, const v
  * grads and m are read from the host.  scale may be NULL (1).  A matrix of zeros stays zero (X = 0); one with
  * a non-finite value becomes non-finite and no other does.
  * Sums are fp32, norms fp64.  fp32: products of matrices that do not fit a CU's LDS take their operands as two
- * fp16 parts each (less than 2^-22 of the value, or 2^-38, of matrices whose entries are at most 1.3).
+ * fp16 parts each (off by at most 2^-22 of the value, or 2^-38, of matrices whose entries are at most 3.5).
  * bf16: as one fp16 part (2^-11).
  * Limits: ntensors <= 4096, 1 <= rows, cols <= KRON_MUON_MAX_SIDE, count <= 2^20 (0: skipped),
  * 1 <= steps <= KRON_MUON_MAX_STEPS, momentum >= 0, eps > 0.  Tensors must not overlap.  The workspace

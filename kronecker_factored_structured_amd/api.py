@@ -18,7 +18,7 @@ from ._lib import (KRON_ACCUMULATE, KRON_ACTS, KRON_BF16, KRON_DISTILL_STATS, KR
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()      # (the argument types make the pointer of it)
 
 
 def _dev(t: Optional[torch.Tensor], name: str, dtype=torch.float32) -> None:
@@ -54,8 +54,8 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 def _stream(device: torch.device):
     if _raw_stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-    return ctypes.c_void_p(_raw_stream(device.index))
+        return torch.cuda.current_stream(device).cuda_stream
+    return _raw_stream(device.index)
 
 
 _HERE = contextlib.nullcontext()

@@ -362,8 +362,8 @@ struct VocabCE {
   int* idx;                   // rows in use (NULL: all)
   int* pos;                   // a row's place among them
   uint16_t* hp;
+  uint16_t* hw;               // h times the weights (fp32)
   uint16_t* wp;
-  int64_t hplane, wplane, dzplane;
   float* part;                // tiles x N: maximum and sum
   float* zlab;                // N logits of the labels
   uint16_t* dz;

@@ -5,7 +5,7 @@
 //   W = keep W - lr scale X
 // A matrix that fits a CU's LDS is one workgroup's from the gradient to the parameters (fp32 matrix
 // instruction).  Others run as tiled products over all matrices of their size; X, A and the polynomial of A
-// are fp16 planes (tile_product.h): two for fp32 parameters, one for bf16 ones.
+// are fp16 parts (tile_product.h): two for fp32 parameters, one for bf16 ones.
 #include <algorithm>
 #include <type_traits>
 #include <utility>
@@ -243,7 +243,7 @@ __global__ __launch_bounds__(kSmallThreads) void muon_small_kernel(SmallBatch ba
 // ------------------------------------------------------------------------------ large matrices
 constexpr int kGroup = 40;           // tensors of one size in a launch
 constexpr int kNormParts = 256;      // workgroups of a matrix's norm
-// Scales of the planes: |X| <= 1.3, |A| <= 1.7 and |P| <= 3.5 stay below fp16's 65504, and small entries keep their bits
+// Scales of the parts: |X| <= 1.3, |A| <= 1.7 and |P| <= 3.5 stay below fp16's 65504, and small entries keep their bits
 constexpr float kX = 8192.f, kA = 8192.f, kP = 8192.f;
 
 struct MuonGroup {
@@ -252,8 +252,8 @@ struct MuonGroup {
   int n;
   int s, l, sp, lp;           // sides, and rounded up to kBK
   double* norm;               // matrices x kNormParts
-  uint16_t* X[2];             // matrices x planes x s x lp
-  uint16_t* A;                // matrices x planes x s x sp
+  uint16_t* X[2];             // matrices x s x lp, NP parts
+  uint16_t* A;                // matrices x s x sp, NP parts
   uint16_t* P;
 };
 
@@ -288,34 +288,40 @@ __global__ __launch_bounds__(256) void muon_momentum_kernel(MuonGroup G, MuonHyp
   if (threadIdx.x == 0) G.norm[(int64_t)blockIdx.y * kNormParts + blockIdx.x] = red[0] + red[1] + red[2] + red[3];
 }
 
+// Four neighbours, from column k (a multiple of four) of a row on, as NP parts.
 template <int NP>
-__device__ inline void put_planes4(uint16_t* p, int64_t plane, f4 v) {
-  typedef _Float16 h4 __attribute__((ext_vector_type(4)));
-  h4 hi, lo;
+__device__ inline void put_parts(uint16_t* row, int k, f4 v) {
+  uint16_t* p = NP == 2 ? row + (k / 32) * 64 + k % 32 : row + k;
+  *(h4*)p = first_part(v);
+  if constexpr (NP == 2) *(h4*)(p + 32) = first_part(v);
+}
+// The same of four rows, `ld` apart, at column k; `rows` of them are written.
+template <int NP>
+__device__ inline void put_parts_turned(uint16_t* first, int64_t ld, int rows, int k, f4 v) {
+  uint16_t* p = NP == 2 ? first + (k / 32) * 64 + k % 32 : first + k;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    hi[e] = (_Float16)v[e];
-    lo[e] = (_Float16)((v[e] - (float)hi[e]) * kLo);
+  for (int q = 0; q < NP; ++q) {
+    const h4 h = first_part(v);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < rows) *(_Float16*)(p + e * ld + 32 * q) = h[e];
   }
-  *(h4*)p = hi;
-  if constexpr (NP == 2) *(h4*)(p + plane) = lo;
 }
 template <int NP>
-__device__ inline f4 get_planes4(const uint16_t* p, int64_t plane) {
-  typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+__device__ inline f4 get_parts(const uint16_t* row, int k) {
+  const uint16_t* p = NP == 2 ? row + (k / 32) * 64 + k % 32 : row + k;
   const h4 hi = *(const h4*)p;
   f4 v;
 #pragma unroll
   for (int e = 0; e < 4; ++e) v[e] = (float)hi[e];
   if constexpr (NP == 2) {
-    const h4 lo = *(const h4*)(p + plane);
+    const h4 lo = *(const h4*)(p + 32);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] += (float)lo[e] * kLoInv;
+    for (int e = 0; e < 4; ++e) v[e] += (float)lo[e];
   }
   return v;
 }
-
-// X's planes: 64 x 64 of a matrix, turned where it is tall.
+// X's parts: 64 x 64 of a matrix, turned where it is tall.
 template <bool BF, int NP>
 __global__ __launch_bounds__(256) void muon_start_kernel(MuonGroup G, MuonHyper h, int tiles_l) {
   __shared__ float tile[64][65];
@@ -343,32 +349,41 @@ __global__ __launch_bounds__(256) void muon_start_kernel(MuonGroup G, MuonHyper 
     tile[r][k] = u * inv;
   }
   __syncthreads();
-  const int64_t plane = (int64_t)G.s * G.lp;
-  uint16_t* X = G.X[0] + (int64_t)blockIdx.y * NP * plane;
+  uint16_t* X = G.X[0] + (int64_t)blockIdx.y * NP * G.s * G.lp;
 #pragma unroll
   for (int i = tid; i < 64 * 16; i += 256) {
     const int r = i >> 4, k = (i & 15) * 4;      // k beyond l: zeros up to lp
     if (s0 + r < G.s)
-      put_planes4<NP>(X + (int64_t)(s0 + r) * G.lp + l0 + k, plane,
-                      tall ? f4{tile[k][r], tile[k + 1][r], tile[k + 2][r], tile[k + 3][r]} : f4{tile[r][k], tile[r][k + 1], tile[r][k + 2], tile[r][k + 3]});
+      put_parts<NP>(X + (int64_t)(s0 + r) * G.lp * NP, l0 + k,
+                    tall ? f4{tile[k][r], tile[k + 1][r], tile[k + 2][r], tile[k + 3][r]} : f4{tile[r][k], tile[r][k + 1], tile[r][k + 2], tile[r][k + 3]});
   }
 }
 
 // MODE 0: A = X X^T.  1: P = a I + b A + c A A.  2: X' = P X.  3: the same, into the parameters of the wide
 // matrices; 4: into the tall ones' (turned: lanes hold neighbours of a row of the parameters in both).
+// A and P are symmetric: their tiles on and below the diagonal are computed (tm: tiles of a side) and written twice.
 template <class Pr, bool BF, int NP, int MODE>
 __global__ __launch_bounds__(Pr::kThreads) void muon_product_kernel(MuonGroup G, MuonHyper h, int from, int tm, int tn) {
   extern __shared__ char smem[];
   int mt, nt;
-  tile_of(blockIdx.x, gridDim.x, tm, tn, mt, nt);
+  if constexpr (MODE <= 1) {
+    static_assert(Pr::BM == Pr::BN, "");
+    mt = (int)((sqrtf(8.f * (float)blockIdx.x + 1.f) - 1.f) * 0.5f);
+    while (mt * (mt + 1) / 2 > (int)blockIdx.x) --mt;
+    while ((mt + 1) * (mt + 2) / 2 <= (int)blockIdx.x) ++mt;
+    nt = blockIdx.x - mt * (mt + 1) / 2;
+  } else {
+    tile_of(blockIdx.x, gridDim.x, tm, tn, mt, nt);
+  }
   const int mat = blockIdx.y, m0 = mt * Pr::BM, n0 = nt * Pr::BN;
   int64_t at;
   const MuonTensor& T = tensor_of(G, mat, at);
   if (MODE >= 3 && (T.rows > T.cols) != (MODE == 4)) return;
-  const int64_t xplane = (int64_t)G.s * G.lp, aplane = (int64_t)G.s * G.sp;
-  const Operand X = {G.X[from] + (int64_t)mat * NP * xplane, G.lp, xplane, G.s, G.lp};
-  const Operand A = {G.A + (int64_t)mat * NP * aplane, G.sp, aplane, G.s, G.sp};
-  const Operand Q = {G.P + (int64_t)mat * NP * aplane, G.sp, aplane, G.s, G.sp};
+  const int64_t lx = (int64_t)G.lp * NP, la = (int64_t)G.sp * NP;      // rows of X, of A and P
+  uint16_t* Am = G.A + (int64_t)mat * G.s * la;
+  uint16_t* Pm = G.P + (int64_t)mat * G.s * la;
+  const Operand X = {G.X[from] + (int64_t)mat * G.s * lx, lx, G.s, G.lp};
+  const Operand A = {Am, la, G.s, G.sp}, Q = {Pm, la, G.s, G.sp};
   Pr p;
   p.run(MODE == 4 ? Q : MODE == 1 ? A : X, MODE == 0 || MODE == 4 ? X : MODE == 1 ? A : Q, m0, n0, 0, MODE == 0 ? G.lp : G.sp, (lds_t*)smem);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
@@ -383,11 +398,10 @@ __global__ __launch_bounds__(Pr::kThreads) void muon_product_kernel(MuonGroup G,
       f4 v = p.acc[i][j];
       if constexpr (MODE <= 1) {
         if (m >= G.sp) continue;
-        const int64_t o = (int64_t)n * G.sp + m;
         if constexpr (MODE == 0) {
           v = v * (kA / (kX * kX));
         } else {
-          v = v * (h.c * kP / (kA * kA)) + get_planes4<NP>(A.p + o, aplane) * (h.b * kP / kA);
+          v = v * (h.c * kP / (kA * kA)) + get_parts<NP>(Am + n * la, m) * (h.b * kP / kA);
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             if (m + e == n) v[e] += h.a * kP;
@@ -395,10 +409,12 @@ __global__ __launch_bounds__(Pr::kThreads) void muon_product_kernel(MuonGroup G,
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (m + e >= G.s) v[e] = 0.f;      // (what pads the rows, whatever the operands' rows beyond gave)
-        put_planes4<NP>((MODE == 0 ? G.A : G.P) + (int64_t)mat * NP * aplane + o, aplane, v);
+        uint16_t* out = MODE == 0 ? Am : Pm;
+        put_parts<NP>(out + n * la, m, v);
+        if (mt != nt) put_parts_turned<NP>(out + m * la, la, G.s - m, n, v);
       } else if constexpr (MODE == 2) {
         if (m >= G.lp) continue;
-        put_planes4<NP>(G.X[from ^ 1] + (int64_t)mat * NP * xplane + (int64_t)n * G.lp + m, xplane, v * (1.f / kP));
+        put_parts<NP>(G.X[from ^ 1] + ((int64_t)mat * G.s + n) * lx, m, v * (1.f / kP));
       } else {
         const int cols = MODE == 4 ? G.s : G.l;
         const float f = h.lr * T.scale * (1.f / (kP * kX));
@@ -428,20 +444,26 @@ hipError_t go(dim3 grid, hipStream_t s, const MuonGroup& G, const MuonHyper& h, 
   return hipGetLastError();
 }
 
-// The largest tiles that still give every CU one.
+// The largest tiles that still give every CU one.  Where there is no more than one for each, four steps' tiles are in LDS,
+// else two and more workgroups on a CU (1024 x 1024 fp32, 48 steps of 64 x 64: 23 -> 17 us; four 768 x 2048 bf16, 576 tiles:
+// 25 us with four, 21 with two).
 template <bool BF, int NP, int MODE>
 hipError_t product(const MuonGroup& G, const MuonHyper& h, int from, int mats, hipStream_t s) {
   constexpr Side SA = MODE == 2 || MODE == 3 ? COL : ROW, SB = MODE == 4 ? COL : ROW;
   const int M = MODE == 2 || MODE == 3 ? G.lp : G.sp, N = MODE == 4 ? G.l : G.s;
-  auto tiles = [&](int b) { return ceil_div(M, b) * ceil_div(N, b) * mats; };
+  auto tiles = [&](int b) {
+    const int64_t m = ceil_div(M, b), n = ceil_div(N, b);
+    return (MODE <= 1 ? m * (m + 1) / 2 : m * n) * mats;
+  };
 #define KRON_MUON_GO(B, NS, ...)                                                                                    \
   {                                                                                                                 \
     typedef Product<__VA_ARGS__, SA, SB, false, NP, NS> Pr;                                                         \
     const int tm = (int)ceil_div(M, B), tn = (int)ceil_div(N, B);                                                   \
-    return go<Pr, muon_product_kernel<Pr, BF, NP, MODE>>(dim3((unsigned)(tm * tn), (unsigned)mats), s, G, h, from, tm, tn); \
+    return go<Pr, muon_product_kernel<Pr, BF, NP, MODE>>(dim3((unsigned)(tiles(B) / mats), (unsigned)mats), s, G, h, from, tm, tn); \
   }
   if (tiles(256) >= 256) KRON_MUON_GO(256, 2, 2, 4, 8, 4)
-  if (tiles(128) >= 256) KRON_MUON_GO(128, 4, 2, 2, 4, 4)
+  if (tiles(128) >= 256) KRON_MUON_GO(128, 2, 2, 2, 4, 4)
+  if (tiles(64) > 256) KRON_MUON_GO(64, 2, 2, 2, 2, 2)
   KRON_MUON_GO(64, 4, 2, 2, 2, 2)
 #undef KRON_MUON_GO
 }

@@ -14,22 +14,39 @@ namespace kron {
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 typedef float f4 __attribute__((ext_vector_type(4)));
 
-// A 16-bit matrix whose rows are ld elements apart, in one plane or in two (fp32 values, see Planes below).
-// Rows start at a 16-byte boundary.
+// A 16-bit matrix whose rows are ld values apart and start at a 16-byte boundary.  With two planes (fp32 values, see
+// below) each 32 columns are 64 values, their first parts and then their second ones: a cache line.
 struct Operand {
   const uint16_t* p;
-  int64_t ld, plane;
-  int rows, cols;        // what may be read: cols is a multiple of 8
+  int64_t ld;
+  int rows, cols;        // what may be read: cols is a multiple of 8 (two planes: of 32)
 };
 
-// fp32 values as two planes of fp16: v 2^s = hi + lo 2^-11, both rounded to nearest.
-constexpr float kLo = 2048.f, kLoInv = 1.f / 2048.f;
+// fp32 values as two parts of fp16: v 2^s = hi + lo, both rounded to nearest, s so that the largest |v| 2^s is below 2^15.
+// They leave at most 2^-22 of the value, or 2^-25 (2^-40 of the largest) where lo is subnormal.  Of a product's
+// four terms lo lo, at most 2^-22 of it, is left out.
 
 namespace {
 
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef __bf16 b8 __attribute__((ext_vector_type(8)));
 typedef short s4v __attribute__((ext_vector_type(4)));
+
+typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+
+// The first part of four values, and what it leaves of them.  They are held as they are: folded into the conversion, the
+// product that made one may round to another first part there than in what is left (one value in 2^13, off by 2^-11).
+__device__ inline h4 first_part(f4& v) {
+  h4 h;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float x = v[e];
+    asm("" : "+v"(x));
+    h[e] = (_Float16)x;
+    v[e] = x - (float)h[e];
+  }
+  return h;
+}
 
 template <bool BF>
 __device__ inline f4 mma(u4 a, u4 b, f4 c) {
@@ -47,13 +64,15 @@ constexpr int kBK = 64;      // contraction of a step: rows of 128 bytes, whole 
 enum Side { ROW, COL };
 
 // One operand's tile of R rows (ROW) or columns (COL) x kBK, loaded straight into LDS by NW wavefronts, a KB a load: eight
-// rows of 128 bytes (64 of the contraction; COL: 64 columns, the tile is R / 64 such blocks of kBK rows).  The 16-byte
-// pieces of a row are permuted, by the address that each lane loads from, so that fragment() reads without bank conflicts:
-// a ROW read is served eight lanes (rows) at a time, a COL read 32 lanes: 32 bytes of each of eight rows 0..3, 8..11.
-template <Side SD, int R, int NW>
+// rows of 128 bytes.  ROW: 64 of the contraction (two planes: 32).  COL: 64 columns (32), the tile is R / 64 (R / 32) such
+// blocks of 64 (32) rows.  The 16-byte pieces of a row are permuted, by the address that each lane loads from, so that
+// fragment() reads without bank conflicts: a ROW read is served eight lanes (rows) at a time, a COL read 32 lanes: 32 bytes
+// of each of eight rows 0..3, 8..11.
+template <Side SD, int R, int NW, int NP>
 struct TileLoad {
-  static constexpr int kLoads = R * kBK * 2 / 1024 / NW;      // 1 KB wave loads of each wavefront
-  static_assert(kLoads * NW * 1024 == R * kBK * 2 && R % 64 == 0, "");
+  static constexpr int kLoads = R * 128 / 1024 / NW;      // 1 KB wave loads of each wavefront
+  static constexpr int kBlock = 64 / NP;                  // columns, and rows, of a COL block
+  static_assert(kLoads * NW * 1024 == R * 128 && R % 64 == 0, "");
   const uint16_t* base;
   uint32_t off[kLoads];
   int64_t ld;
@@ -70,39 +89,43 @@ struct TileLoad {
         const int row = q * 8 + lane / 8, chunk = (lane & 7) ^ (row & 7);
         off[i] = (uint32_t)min(row, rows - 1 - at) * (uint32_t)(ld * 2) + chunk * 16;
       } else {
-        const int row = (q % 8) * 8 + lane / 8, slot = lane & 7;
+        const int row = (q % (kBlock / 8)) * 8 + lane / 8, slot = lane & 7, blk = q / (kBlock / 8);
         const int chunk = (((slot >> 1) ^ turn(row)) << 1) | (slot & 1);
-        off[i] = (uint32_t)min(at + (q / 8) * 64 + chunk * 8, o.cols - 8) * 2;
+        off[i] = NP == 2 ? (uint32_t)min(at / 32 + blk, o.cols / 32 - 1) * 128 + chunk * 16
+                         : (uint32_t)min(at + blk * 64 + chunk * 8, o.cols - 8) * 2;
       }
     }
   }
   // Load i of the wavefront's share of the tile at k0.
-  __device__ void issue(int i, int64_t plane, int k0, lds_t* lds, int lane) const {
+  __device__ void issue(int i, int k0, lds_t* lds, int lane) const {
     const char* src;
     if constexpr (SD == ROW) {
-      src = (const char*)(base + plane + k0) + off[i];
+      src = (const char*)(base + k0 * NP) + off[i];
     } else {
-      const int row = min(k0 + ((wave * kLoads + i) % 8) * 8 + lane / 8, rows - 1);
-      src = (const char*)(base + plane) + (int64_t)row * ld * 2 + off[i];
+      const int row = min(k0 + ((wave * kLoads + i) % (kBlock / 8)) * 8 + lane / 8, rows - 1);
+      src = (const char*)base + (int64_t)row * ld * 2 + off[i];
     }
     __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
                                      (__attribute__((address_space(3))) void*)(lds + (wave * kLoads + i) * 1024), 16, 0, 0);
   }
 };
 
-// Operand block i (16 rows) of half kk (32) of a step out of a tile in LDS; `at`: the wavefront's first row.
-template <Side SD, int R>
+// Operand block i (16 rows) of half kk of a step (32 of its 64 products; two planes: part kk) out of a tile in LDS; `at`:
+// the wavefront's first row.
+template <Side SD, int NP>
 __device__ inline u4 fragment(const lds_t* lds, int at, int i, int kk, int lane) {
   const int g = lane >> 4, c = lane & 15;
   if constexpr (SD == ROW) {
     return *(const __attribute__((address_space(3))) u4*)(lds + (at + 16 * i + c) * 128 + (((kk * 4 + g) ^ (c & 7)) * 16));
   } else {
     // two transposing reads: sixteen lanes give sixteen columns of four rows, lane 4 r + q four columns of row r
-    const int r0 = kk * 32 + 8 * g + (c >> 2), r1 = r0 + 4, blk = at / 16 + i;
-    const lds_t* t = lds + (blk >> 2) * (kBK * 128) + (c & 3) * 8;
+    typedef TileLoad<SD, 64, 1, NP> L;
+    const int r0 = (NP == 2 ? 0 : kk * 32) + 8 * g + (c >> 2), r1 = r0 + 4, blk = at / 16 + i;
+    const int per = L::kBlock / 16, seg = NP == 2 ? kk * 2 + blk % per : blk % per;
+    const lds_t* t = lds + (blk / per) * (L::kBlock * 128) + (c & 3) * 8;
     union { s4v h[2]; u4 u; } o;
-    o.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4v*)(t + r0 * 128 + ((blk & 3) ^ TileLoad<SD, 64, 1>::turn(r0)) * 32));
-    o.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4v*)(t + r1 * 128 + ((blk & 3) ^ TileLoad<SD, 64, 1>::turn(r1)) * 32));
+    o.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4v*)(t + r0 * 128 + (seg ^ L::turn(r0)) * 32));
+    o.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4v*)(t + r1 * 128 + (seg ^ L::turn(r1)) * 32));
     return o.u;
   }
 }
@@ -113,7 +136,8 @@ __device__ inline u4 fragment(const lds_t* lds, int at, int i, int kk, int lane)
 // A step is two halves of 32 products.  While one half's fragments are multiplied the next half's come out of LDS.  Between
 // the halves a barrier: behind it the next step's tiles are in LDS, its first fragments are read, and this step's tiles,
 // all in registers by then, make room for step t + NS's, whose loads go out between the products (issued together
-// they hold the wavefronts up: dW of 768 x 21760 over 8192 rows 303 -> 280 us) and have NS - 1 steps' time.
+// they hold the wavefronts up: dW of 768 x 21760 over 8192 rows 303 -> 280 us) and have NS - 1 steps' time.  With two
+// planes a step is 32 products in three parts, lo hi, hi hi and hi lo: each part's fragments serve two of them.
 //
 // 256 x 256 tiles of eight wavefronts: 8192 x 8256 x 8192 bf16 runs at 1,370 TFLOP/s.  Registers alone would do 1,660 with
 // this instruction and such values (the clock falls to 2.0 GHz with the power they take; 2,090 with zeros), loads alone
@@ -124,30 +148,33 @@ template <int WM_, int WN_, int TM_, int TN_, Side SA_, Side SB_, bool BF_, int 
 struct Product {
   static constexpr int WM = WM_, WN = WN_, TM = TM_, TN = TN_, NP = NP_, NS = NS_;
   static constexpr int BM = WM * TM * 16, BN = WN * TN * 16, NW = WM * WN, kThreads = 64 * NW;
-  static constexpr int kStage = (BM + BN) * kBK * 2;
+  static constexpr int kStage = (BM + BN) * 128, kStep = kBK / NP;
   static constexpr int kLdsBytes = NS * kStage;
+  typedef TileLoad<SA_, BM, NW, NP> LA;
+  typedef TileLoad<SB_, BN, NW, NP> LB;
+  static constexpr int kLoads = LA::kLoads + LB::kLoads;
   f4 acc[TM][TN];
 
-  struct Half {
-    u4 a[TM], b[TN];
-  };
-  __device__ static void read(Half& f, const lds_t* st, int kk, int wm, int wn, int lane) {
+  struct FragsA { u4 f[TM]; };
+  struct FragsB { u4 f[TN]; };
+  __device__ static void read(FragsA& a, const lds_t* st, int kk, int wm, int lane) {
 #pragma unroll
-    for (int j = 0; j < TN; ++j) f.b[j] = fragment<SB_, BN>(st + BM * kBK * 2, wn * TN * 16, j, kk, lane);
+    for (int i = 0; i < TM; ++i) a.f[i] = fragment<SA_, NP>(st, wm * TM * 16, i, kk, lane);
+  }
+  __device__ static void read(FragsB& b, const lds_t* st, int kk, int wn, int lane) {
 #pragma unroll
-    for (int i = 0; i < TM; ++i) f.a[i] = fragment<SA_, BM>(st, wm * TM * 16, i, kk, lane);
+    for (int j = 0; j < TN; ++j) b.f[j] = fragment<SB_, NP>(st + BM * 128, wn * TN * 16, j, kk, lane);
   }
   // between(i): what is issued beside block row i's products.
   template <class F>
-  __device__ void multiply(const Half& f, const F& between) {
+  __device__ void multiply(const FragsA& a, const FragsB& b, const F& between) {
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
       between(i);
 #pragma unroll
-      for (int j = 0; j < TN; ++j) acc[i][j] = mma<BF_>(f.a[i], f.b[j], acc[i][j]);
+      for (int j = 0; j < TN; ++j) acc[i][j] = mma<BF_>(a.f[i], b.f[j], acc[i][j]);
     }
   }
-  static constexpr int kLoads = TileLoad<SA_, BM, NW>::kLoads + TileLoad<SB_, BN, NW>::kLoads;
   // What this wavefront reads is there, and what it loads but for the last STAGES tiles; and so it is for all of them.
   template <int STAGES>
   __device__ static void in_step() {
@@ -165,65 +192,65 @@ struct Product {
     for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int j = 0; j < TN; ++j) acc[i][j] = f4{0, 0, 0, 0};
-    const int steps = (k_end - k_begin + kBK - 1) / kBK;
-    if (steps <= 0) return;
-    TileLoad<SA_, BM, NW> la;
-    TileLoad<SB_, BN, NW> lb;
+    const int total = (k_end - k_begin + kStep - 1) / kStep;
+    if (total <= 0) return;
+    LA la;
+    LB lb;
     la.init(A, m0, wave, lane);
     lb.init(B, n0, wave, lane);
-    const int total = NP == 2 ? 3 * steps : steps;
-    int next = 0, pair = 0, k = k_begin;      // of the tiles to load: with two planes lo hi, hi lo, hi hi
+    int next = 0;      // of the tiles to load
     auto load = [&](int st, int i) {      // load i of the wavefront's for the next tiles
-      if (i < TileLoad<SA_, BM, NW>::kLoads)
-        la.issue(i, NP == 2 && pair == 0 ? A.plane : 0, k, lds + st * kStage, lane);
-      else
-        lb.issue(i - TileLoad<SA_, BM, NW>::kLoads, NP == 2 && pair == 1 ? B.plane : 0, k, lds + st * kStage + BM * kBK * 2, lane);
-    };
-    auto loaded = [&]() {
-      k += kBK;
-      if (NP == 2 && k >= k_begin + steps * kBK) k = k_begin, ++pair;
-      ++next;
+      const int k = k_begin + next * kStep;
+      if (i < LA::kLoads) la.issue(i, k, lds + st * kStage, lane);
+      else lb.issue(i - LA::kLoads, k, lds + st * kStage + BM * 128, lane);
     };
     auto all = [&](int st) {
       if (next >= total) return;
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) load(st, i);
-      loaded();
+      ++next;
     };
-    Half f0, f1;
+    FragsA a0, a1;
+    FragsB b0, b1;
+    constexpr int first = NP == 2 ? 1 : 0;      // of A's parts
     all(0);
     in_step<0>();
 #pragma unroll
     for (int i = 1; i < NS; ++i) all(i);
-    read(f0, lds, 0, wm, wn, lane);
+    read(b0, lds, 0, wn, lane);
+    read(a0, lds, first, wm, lane);
     int st = 0;
-    auto step = [&](int t, auto more) {
-      if constexpr (NP == 2) {
-        if (t == 2 * steps) {      // the products with a second part are in
-#pragma unroll
-          for (int i = 0; i < TM; ++i)
-#pragma unroll
-            for (int j = 0; j < TN; ++j) acc[i][j] *= kLoInv;
-        }
-      }
-      read(f1, lds + st * kStage, 1, wm, wn, lane);
-      multiply(f0, [](int) {});
-      in_step<more ? NS - 2 : 0>();
-      const int after = st + 1 == NS ? 0 : st + 1;
-      read(f0, lds + after * kStage, 0, wm, wn, lane);      // (behind the last step: of no use, and not used)
-      multiply(f1, [&](int i) {
+    auto step = [&](auto more) {
+      const lds_t* now = lds + st * kStage;
+      auto none = [](int) {};
+      auto loads = [&](int i) {
         if (!more) return;
         constexpr int per = (kLoads + TM - 1) / TM;
 #pragma unroll
         for (int q = 0; q < per; ++q)
           if (i * per + q < kLoads) load(st, i * per + q);
-      });
-      if (more) loaded();
+      };
+      const int after = st + 1 == NS ? 0 : st + 1;
+      if constexpr (NP == 2) {
+        read(a1, now, 0, wm, lane);
+        multiply(a0, b0, none);
+        read(b1, now, 1, wn, lane);
+        multiply(a1, b0, none);
+      } else {
+        read(b1, now, 1, wn, lane);
+        read(a1, now, 1, wm, lane);
+        multiply(a0, b0, none);
+      }
+      in_step<more ? NS - 2 : 0>();
+      read(b0, lds + after * kStage, 0, wn, lane);      // (behind the last step: of no use, and not used)
+      read(a0, lds + after * kStage, first, wm, lane);
+      multiply(a1, b1, loads);
+      if (more) ++next;
       st = after;
     };
     int t = 0;
-    for (; t < total - NS; ++t) step(t, std::true_type{});
-    for (; t < total; ++t) step(t, std::false_type{});
+    for (; t < total - NS; ++t) step(std::true_type{});
+    for (; t < total; ++t) step(std::false_type{});
     __syncthreads();
   }
 };
@@ -237,28 +264,34 @@ __device__ inline void tile_of(int id, int count, int tm, int tn, int& mt, int& 
   nt = first + in % wide, mt = in / wide;
 }
 
-// A tile's sums as 16-bit values into rows n of `out` (ld elements apart, m contiguous; `rows` of the tile's are written):
-// through the LDS of the wavefront, so that whole lines are written (dz of 8192 x 12288: 195 -> 173 us against eight
-// bytes of each of sixteen rows at a time).  value(i, j): the four values of row(i) .. + 3, column j.
+// A tile's sums as 16-bit values into rows n of `out` (ld values apart, m contiguous; `rows` of the tile's are written), with
+// two planes each 32 of m as their first parts and then their second: through the LDS of the wavefront, so that whole
+// lines are written (dz of 8192 x 12288: 195 -> 173 us against eight bytes of each of sixteen rows at a time).
+// value(i, j): part after part of the four values of block (i, j).
 template <class P, class F>
 __device__ __forceinline__ void store_rows(char* smem, uint16_t* out, int64_t ld, int rows, const F& value) {
-  constexpr int RB = P::TM * 32, CH = RB / 16, PR = 64 / CH;      // bytes and 16-byte pieces of a row, rows at a time
-  static_assert(CH * PR == 64, "");
+  constexpr int RB = P::TM * 32 * P::NP, CH = RB / 16, PR = 64 / CH;      // bytes and 16-byte pieces of a row, rows at a time
+  static_assert(CH * PR == 64 && P::NW * RB * 16 <= P::kLdsBytes, "");
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
   const int wm = wave % P::WM, wn = wave / P::WM;
-  char* mine = smem + wave * (RB * 16 * P::TN);
+  char* mine = smem + wave * (RB * 16);
 #pragma unroll
   for (int j = 0; j < P::TN; ++j) {
-    char* rows16 = mine + 16 * j * RB;
 #pragma unroll
-    for (int i = 0; i < P::TM; ++i) *(uint2*)(rows16 + c * RB + (((2 * i + (g >> 1)) ^ (c & (CH - 1))) * 16) + (g & 1) * 8) = value(i, j);
+    for (int i = 0; i < P::TM; ++i)
+#pragma unroll
+      for (int q = 0; q < P::NP; ++q) {
+        const int piece = (P::NP == 2 ? (i >> 1) * 8 + q * 4 + (i & 1) * 2 : 2 * i) + (g >> 1);
+        *(uint2*)(mine + c * RB + ((piece ^ (c & (CH - 1))) * 16) + (g & 1) * 8) = value(i, j);
+      }
     asm volatile("" ::: "memory");
 #pragma unroll
     for (int q = 0; q < 16 / PR; ++q) {
       const int r = q * PR + lane / CH, ch = lane % CH, n = wn * P::TN * 16 + 16 * j + r;
-      const u4 v = *(const u4*)(rows16 + r * RB + ((ch ^ (r & (CH - 1))) * 16));
-      if (n < rows) *(u4*)(out + (int64_t)n * ld + wm * P::TM * 16 + ch * 8) = v;
+      const u4 v = *(const u4*)(mine + r * RB + ((ch ^ (r & (CH - 1))) * 16));
+      if (n < rows) *(u4*)(out + (int64_t)n * ld + wm * P::TM * 16 * P::NP + ch * 8) = v;
     }
+    asm volatile("" ::: "memory");
   }
 }
 

@@ -6,7 +6,8 @@
 // gradient to 16 bits, and its two products.
 //
 // bf16 inputs go into the products as they are (sums in fp32), and dz is rounded to bf16 once.  fp32 inputs, and
-// their dz, are two fp16 planes each (tile_product.h).
+// their softmax minus the label's indicator, are two fp16 parts each (tile_product.h): the rows' weights, which may
+// lie far apart, then stand beside h in dW and beside the sums in dh.
 #include <algorithm>
 #include <cmath>
 
@@ -17,7 +18,7 @@ namespace kron {
 
 // Rows in use, and what the scales of fp32 values come from.
 struct VocabScales {
-  uint32_t top_h, top_w, top_dz;      // bits of the largest finite |value|
+  uint32_t top_h, top_w, top_weight;      // bits of the largest finite |value|
   int count;              // rows in use
 };
 
@@ -77,7 +78,7 @@ __global__ __launch_bounds__(1024) void vocab_rows_kernel(VocabCE a) {
   __syncthreads();
   if (tid == 0) {
     for (int i = 1; i < 16; ++i) top = max(top, wtop[i]);
-    a.sc->top_dz = top;
+    a.sc->top_weight = top;
     a.sc->top_h = a.sc->top_w = 0;
     a.sc->count = base;
   }
@@ -115,20 +116,23 @@ __global__ __launch_bounds__(256) void vocab_top_kernel(VocabCE a) {
   if (threadIdx.x == 0) atomicMax(w ? &a.sc->top_w : &a.sc->top_h, max(max(red[0], red[1]), max(red[2], red[3])));
 }
 
-// Rows as operands: gathered (h), padded with zeros to Kp, fp32 split into its planes.
+// Rows as operands: gathered (h), padded with zeros to Kp, fp32 split into its parts.  which 0: h, 1: W, 2: h times the
+// rows' weights.
+constexpr float kOne = 32768.f;      // scale of what is at most 1
 template <bool BF>
 __global__ __launch_bounds__(256) void vocab_pack_kernel(VocabCE a, int which) {
   const bool w = which == 1;
   const int rows = w ? a.V : vocab_count(a);
   const int per = a.Kp / 8;
-  uint16_t* dst = w ? a.wp : a.hp;
-  const int64_t plane = w ? a.wplane : a.hplane;
-  float up = 1.f;
-  if constexpr (!BF) up = scale_up(w ? a.sc->top_w : a.sc->top_h);
+  uint16_t* dst = w ? a.wp : which == 2 ? a.hw : a.hp;
+  float up = 1.f, up_weight = 1.f;
+  if constexpr (!BF) {
+    up = scale_up(w ? a.sc->top_w : a.sc->top_h);
+    if (which == 2) up_weight = scale_up(a.sc->top_weight);
+  }
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)rows * per; i += (int64_t)gridDim.x * 256) {
     const int r = (int)(i / per), k = (int)(i - (int64_t)r * per) * 8;
-    const int64_t from = (int64_t)(!w && a.idx ? a.idx[r] : r) * a.K + k;
-    const int64_t to = (int64_t)r * a.Kp + k;
+    const int64_t row = !w && a.idx ? a.idx[r] : r, from = row * a.K + k;
     if constexpr (BF) {
       const uint16_t* s = (const uint16_t*)(w ? a.W : a.h) + from;
       u4 o = {0, 0, 0, 0};
@@ -138,7 +142,7 @@ __global__ __launch_bounds__(256) void vocab_pack_kernel(VocabCE a, int which) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           if (k + e < a.K) o[e / 2] |= (uint32_t)s[e] << (16 * (e & 1));
-      *(u4*)(dst + to) = o;
+      *(u4*)(dst + (int64_t)r * a.Kp + k) = o;
     } else {
       const float* s = (const float*)(w ? a.W : a.h) + from;
       float v[8];
@@ -150,21 +154,23 @@ __global__ __launch_bounds__(256) void vocab_pack_kernel(VocabCE a, int which) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = k + e < a.K ? s[e] : 0.f;
       }
-      h8 hi, lo;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float x = v[e] * up;
-        hi[e] = (_Float16)x;
-        lo[e] = (_Float16)((x - (float)hi[e]) * kLo);
-      }
-      *(h8*)(dst + to) = hi;
-      *(h8*)(dst + plane + to) = lo;
+      const float weight = which == 2 ? a.weights[row] * up_weight * (1.f / kOne) : 1.f;
+      f4 x = f4{v[0], v[1], v[2], v[3]} * up * weight, y = f4{v[4], v[5], v[6], v[7]} * up * weight;
+      uint16_t* d = dst + (int64_t)r * a.Kp * 2 + (k / 32) * 64 + k % 32;
+      *(h4*)d = first_part(x);
+      *(h4*)(d + 4) = first_part(y);
+      *(h4*)(d + 32) = first_part(x);
+      *(h4*)(d + 36) = first_part(y);
     }
   }
 }
 
-__device__ inline Operand h_operand(const VocabCE& a, int count) { return {a.hp, a.Kp, a.hplane, count, a.Kp}; }
-__device__ inline Operand w_operand(const VocabCE& a) { return {a.wp, a.Kp, a.wplane, a.V, a.Kp}; }
+template <int NP>
+__device__ inline Operand h_operand(const VocabCE& a, int count) { return {a.hp, (int64_t)a.Kp * NP, count, a.Kp}; }
+template <int NP>
+__device__ inline Operand w_operand(const VocabCE& a, int v0 = 0) {
+  return {a.wp + (int64_t)v0 * a.Kp * NP, (int64_t)a.Kp * NP, a.V - v0, a.Kp};
+}
 
 // ------------------------------------------------------------------------------ forward
 // Tiles of the vocabulary (m) x rows (n): each lane holds four neighbouring tokens of one row.
@@ -176,7 +182,7 @@ __global__ __launch_bounds__(P::kThreads) void vocab_fwd_kernel(VocabCE a, int t
   const int count = vocab_count(a), m0 = mt * P::BM, n0 = nt * P::BN;
   if (n0 >= count) return;
   P p;
-  p.run(w_operand(a), h_operand(a, count), m0, n0, 0, a.Kp, (lds_t*)smem);
+  p.run(w_operand<P::NP>(a), h_operand<P::NP>(a, count), m0, n0, 0, a.Kp, (lds_t*)smem);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
   const int wm = wave % P::WM, wn = wave / P::WM, first = m0 + wm * P::TM * 16 + 4 * g;
   const float down = BF ? 1.f : scale_down(a.sc->top_h), down2 = BF ? 1.f : scale_down(a.sc->top_w);
@@ -273,7 +279,8 @@ __global__ __launch_bounds__(1024) void vocab_loss_kernel(VocabCE a) {
 }
 
 // ------------------------------------------------------------------------------ backward
-// The gradient of the logits of one piece of the vocabulary, [rows][vc] in 16 bits (without the factor g).
+// The gradient of the logits of one piece of the vocabulary, [rows][vc] in 16 bits, without the factor g (fp32: and
+// without the weights).
 template <class P, bool BF>
 __global__ __launch_bounds__(P::kThreads) void vocab_dz_kernel(VocabCE a, int v0, int vc, int tm, int tn) {
   extern __shared__ char smem[];
@@ -282,11 +289,11 @@ __global__ __launch_bounds__(P::kThreads) void vocab_dz_kernel(VocabCE a, int v0
   const int count = vocab_count(a), m0 = mt * P::BM, n0 = nt * P::BN;
   if (n0 >= count) return;
   P p;
-  p.run(w_operand(a), h_operand(a, count), v0 + m0, n0, 0, a.Kp, (lds_t*)smem);
+  p.run(w_operand<P::NP>(a), h_operand<P::NP>(a, count), v0 + m0, n0, 0, a.Kp, (lds_t*)smem);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
   const int wm = wave % P::WM, wn = wave / P::WM, first = v0 + m0 + wm * P::TM * 16 + 4 * g;
   const float down = BF ? 1.f : scale_down(a.sc->top_h), down2 = BF ? 1.f : scale_down(a.sc->top_w);
-  const float up = BF ? 1.f : scale_up(a.sc->top_dz), f = BF ? kLog2e : down2 * kLog2e;
+  const float f = BF ? kLog2e : down2 * kLog2e;
   const int padded = (count + kBK - 1) / kBK * kBK;      // rows that the contraction over them reads
   const bool edge = v0 + m0 + P::BM > a.V || n0 + P::BN > count;
 #pragma unroll
@@ -297,7 +304,7 @@ __global__ __launch_bounds__(P::kThreads) void vocab_dz_kernel(VocabCE a, int v0
     if (n < count) {
       const int64_t row = a.idx ? a.idx[n] : n;
       lab = a.labels[row];
-      w = (a.weights ? a.weights[row] : a.mean) * up;
+      w = !BF ? kOne : a.weights ? a.weights[row] : a.mean;
       top = a.stats_in[2 * row], inv = a.stats_in[2 * row + 1] * w;
     }
 #pragma unroll
@@ -321,22 +328,16 @@ __global__ __launch_bounds__(P::kThreads) void vocab_dz_kernel(VocabCE a, int v0
           if (n >= count || first + 16 * i + e >= a.V) p.acc[i][j][e] = 0.f;
     }
   }
-  uint16_t* out = a.dz + (int64_t)n0 * vc + m0;
+  uint16_t* out = a.dz + ((int64_t)n0 * vc + m0) * P::NP;
   if constexpr (BF) {
     store_rows<P>(smem, out, vc, padded - n0, [&](int i, int j) {
       return uint2{bf16_pair(p.acc[i][j][0], p.acc[i][j][1]), bf16_pair(p.acc[i][j][2], p.acc[i][j][3])};
     });
   } else {
-    // the first parts, and what they leave, in the sums' place, as the second ones
-    typedef _Float16 h4 __attribute__((ext_vector_type(4)));
-    auto part = [&](int i, int j) __attribute__((always_inline)) {
-      const f4 v = p.acc[i][j];
-      const h4 h = {(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
-      p.acc[i][j] = f4{v[0] - (float)h[0], v[1] - (float)h[1], v[2] - (float)h[2], v[3] - (float)h[3]} * kLo;
-      return __builtin_bit_cast(uint2, h);
-    };
-    store_rows<P>(smem, out, vc, padded - n0, part);
-    store_rows<P>(smem, out + a.dzplane, vc, padded - n0, part);
+    // a first part, and what it leaves, in the sum's place, as the second one
+    store_rows<P>(smem, out, (int64_t)vc * 2, padded - n0, [&](int i, int j) __attribute__((always_inline)) {
+      return __builtin_bit_cast(uint2, first_part(p.acc[i][j]));
+    });
   }
 }
 
@@ -349,12 +350,9 @@ __global__ __launch_bounds__(P::kThreads) void vocab_dh_kernel(VocabCE a, int v0
   const int count = vocab_count(a), m0 = mt * P::BM, n0 = nt * P::BN;
   if (n0 >= count) return;
   const int k0 = blockIdx.y * len, k1 = min(vc, k0 + len);
-  Operand W = w_operand(a);
-  W.p += (int64_t)v0 * a.Kp;
-  W.rows = a.V - v0;
-  const Operand dz = {a.dz, vc, a.dzplane, count, vc};
+  const Operand dz = {a.dz, (int64_t)vc * P::NP, count, vc};
   P p;
-  p.run(W, dz, m0, n0, k0, k1, (lds_t*)smem);
+  p.run(w_operand<P::NP>(a, v0), dz, m0, n0, k0, k1, (lds_t*)smem);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
   float* out = a.dhpart + (int64_t)blockIdx.y * a.N * a.Kp;
 #pragma unroll
@@ -396,11 +394,11 @@ __device__ inline void put_grad(void* p, int64_t row, int k, int K, f4 s, float 
 
 template <bool BF>
 __global__ __launch_bounds__(256) void vocab_dh_join_kernel(VocabCE a, int splits) {
-  float f = a.gout[0], f2 = 1.f;
-  if constexpr (!BF) f *= scale_down(a.sc->top_dz), f2 = scale_down(a.sc->top_w);
+  const float gout = a.gout[0], f2 = BF ? 1.f : scale_down(a.sc->top_w);
   const int per = a.Kp / 4;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < a.N * per; i += (int64_t)gridDim.x * 256) {
     const int64_t row = i / per;
+    const float f = BF ? gout : (a.weights ? a.weights[row] : a.mean) * (1.f / kOne) * gout;
     const int k = (int)(i - row * per) * 4;
     if (k >= a.K) continue;
     const int64_t at = a.idx ? a.pos[row] : row;
@@ -408,6 +406,16 @@ __global__ __launch_bounds__(256) void vocab_dh_join_kernel(VocabCE a, int split
     if (at >= 0)
       for (int t = 0; t < splits; ++t) s += *(const f4*)(a.dhpart + ((int64_t)t * a.N + at) * a.Kp + k);
     put_grad<BF>(a.dh, row, k, a.K, s, at >= 0 ? f2 : 0.f, at >= 0 ? f : 0.f);
+  }
+}
+
+// What dW's sums are times: f2, then f.
+template <bool BF>
+__device__ inline void dw_factors(const VocabCE& a, float& f, float& f2) {
+  f = a.gout[0], f2 = 1.f;
+  if constexpr (!BF) {
+    f2 = scale_down(a.sc->top_h);
+    f *= a.weights ? scale_down(a.sc->top_weight) : a.mean * (1.f / kOne);
   }
 }
 
@@ -420,12 +428,14 @@ __global__ __launch_bounds__(P::kThreads) void vocab_dw_kernel(VocabCE a, int v0
   const int count = vocab_count(a), m0 = mt * P::BM, n0 = nt * P::BN;
   const int padded = (count + kBK - 1) / kBK * kBK;
   const int len = (padded / kBK + gridDim.y - 1) / gridDim.y * kBK, k0 = blockIdx.y * len;
-  const Operand dz = {a.dz, vc, a.dzplane, padded, vc};
+  const Operand dz = {a.dz, (int64_t)vc * P::NP, padded, vc};
+  Operand h = h_operand<P::NP>(a, count);
+  if (P::NP == 2 && a.weights) h.p = a.hw;
   P p;
-  p.run(h_operand(a, count), dz, m0, n0, k0, min(count, k0 + len), (lds_t*)smem);
+  p.run(h, dz, m0, n0, k0, min(count, k0 + len), (lds_t*)smem);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
-  float f = a.gout[0], f2 = 1.f;
-  if constexpr (!BF) f *= scale_down(a.sc->top_dz), f2 = scale_down(a.sc->top_h);
+  float f, f2;
+  dw_factors<BF>(a, f, f2);
 #pragma unroll
   for (int j = 0; j < P::TN; ++j) {
     const int n = n0 + (wave / P::WM) * P::TN * 16 + 16 * j + c;
@@ -444,8 +454,8 @@ __global__ __launch_bounds__(P::kThreads) void vocab_dw_kernel(VocabCE a, int v0
 
 template <bool BF>
 __global__ __launch_bounds__(256) void vocab_dw_join_kernel(VocabCE a, int v0, int vc, int parts) {
-  float f = a.gout[0], f2 = 1.f;
-  if constexpr (!BF) f *= scale_down(a.sc->top_dz), f2 = scale_down(a.sc->top_h);
+  float f, f2;
+  dw_factors<BF>(a, f, f2);
   const int per = a.Kp / 4, rows = min(vc, a.V - v0);
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)rows * per; i += (int64_t)gridDim.x * 256) {
     const int64_t row = i / per;
@@ -494,7 +504,7 @@ struct VocabPlan {
   int tiles;                      // of the vocabulary, 256 wide
   int piece, pieces, splits;      // backward
   bool three;                     // dh in tiles of 192
-  size_t sc, idx, pos, hp, wp, part, zlab, dz, dhpart, dwpart, bytes;
+  size_t sc, idx, pos, hp, hw, wp, part, zlab, dz, dhpart, dwpart, bytes;
 };
 
 // Parts of a piece's dW.
@@ -518,6 +528,7 @@ VocabPlan plan_of(int64_t N, int K, int V, bool bf, bool weights, bool backward)
   p.idx = take(p.rows ? 4 * (size_t)N : 0);
   p.pos = take(p.rows ? 4 * (size_t)N : 0);
   p.hp = take(p.copy_h ? 2 * (size_t)planes * N * p.Kp : 0);
+  p.hw = take(backward && !bf && weights ? 2 * (size_t)planes * N * p.Kp : 0);
   p.wp = take(p.copy_w ? 2 * (size_t)planes * V * p.Kp : 0);
   if (!backward) {
     p.part = take(8 * (size_t)p.tiles * N);
@@ -559,12 +570,10 @@ VocabCE bind(const VocabCE& k, const VocabPlan& p, char* ws, bool bf) {
   a.pos = (int*)(ws + p.pos);
   a.hp = p.copy_h ? (uint16_t*)(ws + p.hp) : (uint16_t*)k.h;
   a.wp = p.copy_w ? (uint16_t*)(ws + p.wp) : (uint16_t*)k.W;
-  a.hplane = k.N * p.Kp;
-  a.wplane = (int64_t)k.V * p.Kp;
+  a.hw = (uint16_t*)(ws + p.hw);
   a.part = (float*)(ws + p.part);
   a.zlab = (float*)(ws + p.zlab);
   a.dz = (uint16_t*)(ws + p.dz);
-  a.dzplane = ceil_div(std::max<int64_t>(k.N, 1), kBK) * kBK * (int64_t)p.piece;
   a.dhpart = (float*)(ws + p.dhpart);
   a.dwpart = (float*)(ws + p.dwpart);
   return a;
@@ -585,6 +594,7 @@ hipError_t prepare(const VocabCE& a, const VocabPlan& p, hipStream_t s) {
   const int per = p.Kp / 8;
   auto blocks = [&](int64_t rows) { return dim3((unsigned)std::min<int64_t>(4096, std::max<int64_t>(1, ceil_div(rows * per, 256)))); };
   if (p.copy_h && a.N) hipLaunchKernelGGL((vocab_pack_kernel<BF>), blocks(a.N), dim3(256), 0, s, a, 0);
+  if (!BF && a.dW && a.weights && a.N) hipLaunchKernelGGL((vocab_pack_kernel<BF>), blocks(a.N), dim3(256), 0, s, a, 2);
   if (p.copy_w) hipLaunchKernelGGL((vocab_pack_kernel<BF>), blocks(a.V), dim3(256), 0, s, a, 1);
   return hipGetLastError();
 }
