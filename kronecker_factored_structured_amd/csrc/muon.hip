@@ -64,7 +64,7 @@ __device__ inline void put(void* p, int64_t i, float v) {
 }
 
 // ------------------------------------------------------------------------------ matrices within a workgroup
-constexpr int kSmallThreads = 512, kSmallSide = 64, kSmallBatch = 40, kBatch = 4;
+constexpr int kSmallSide = 64, kSmallBatch = 40, kBatch = 4;
 constexpr size_t kSmallLds = 156 * 1024;
 
 struct SmallBatch {
@@ -74,10 +74,10 @@ struct SmallBatch {
 };
 
 int pad16(int v) { return (v + 15) / 16 * 16; }
-// Floats of LDS: X (rows of l rounded up to 16 and 4 more, so that 16 rows start in different banks), A and the polynomial, sums.
+// LDS: X (rows of l rounded up to 16 and 4 more, so that 16 rows start in different banks), A and the polynomial, sums.
 size_t small_lds(int s, int l) {
   const int sp = pad16(s), ld = pad16(l) + 4;
-  return sizeof(float) * ((size_t)sp * ld + 2 * (size_t)sp * (sp + 4) + 8 * 256) + 64 * sizeof(double);
+  return sizeof(float) * ((size_t)sp * ld + 2 * (size_t)sp * (sp + 4) + 16 * 256) + 64 * sizeof(double);
 }
 bool is_small(int rows, int cols) {
   const int s = std::min(rows, cols), l = std::max(rows, cols);
@@ -86,8 +86,8 @@ bool is_small(int rows, int cols) {
 
 __device__ inline f4 mma32(float a, float b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
 
-template <bool BF>
-__global__ __launch_bounds__(kSmallThreads) void muon_small_kernel(SmallBatch batch, MuonHyper h) {
+template <bool BF, int NT>
+__global__ __launch_bounds__(NT) void muon_small_kernel(SmallBatch batch, MuonHyper h) {
   extern __shared__ char smem[];
   int ti = 0;
   while (ti + 1 < batch.n && (int)blockIdx.x >= batch.first[ti + 1]) ++ti;
@@ -100,29 +100,29 @@ __global__ __launch_bounds__(kSmallThreads) void muon_small_kernel(SmallBatch ba
   float* X = (float*)(dred + 64);
   float* A = X + (size_t)sp * ld;
   float* P = A + sp * la;
-  float* red = P + sp * la;      // 8 x 256
+  float* red = P + sp * la;      // wavefronts x 256
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, c = lane & 15;
-  constexpr int NW = kSmallThreads / 64;
+  constexpr int NW = NT / 64;
 
   // what pads X's rows and columns
-  for (int i = tid; i < sp * ld; i += kSmallThreads)
-    if (i >= s * ld || i % ld >= l) X[i] = 0.f;
+  for (int i = s * ld + tid; i < sp * ld; i += NT) X[i] = 0.f;
+  for (int i = tid; i < s * (lp - l); i += NT) X[i / (lp - l) * ld + l + i % (lp - l)] = 0.f;
   double sum = 0;
   // kBatch groups of neighbours are in flight together (one after the other, 2048 x 16 took 45 us to come in)
   auto start = [&](auto n) {
     constexpr int N = decltype(n)::value;
     const int per = T.cols / N, all = T.rows * per;
-    for (int i0 = tid; i0 < all; i0 += kBatch * kSmallThreads) {
+    for (int i0 = tid; i0 < all; i0 += kBatch * NT) {
       float g[kBatch][N], m[kBatch][N], u[N];
 #pragma unroll
       for (int q = 0; q < kBatch; ++q) {
-        const int64_t e = at + (int64_t)min(i0 + q * kSmallThreads, all - 1) * N;
+        const int64_t e = at + (int64_t)min(i0 + q * NT, all - 1) * N;
         get_n<BF, N>(T.g, e, g[q]);
         get_n<false, N>(T.m, e, m[q]);
       }
 #pragma unroll
       for (int q = 0; q < kBatch; ++q) {
-        const int i = i0 + q * kSmallThreads;
+        const int i = i0 + q * NT;
         if (i >= all) break;
         momentum<N>(h, g[q], m[q], u);
         put_n<false, N>(T.m, at + (int64_t)i * N, m[q]);
@@ -143,18 +143,16 @@ __global__ __launch_bounds__(kSmallThreads) void muon_small_kernel(SmallBatch ba
   sum = 0;
   for (int i = 0; i < NW; ++i) sum += dred[i];
   const float inv = (float)(1.0 / (sqrt(sum) + (double)h.eps));
-  for (int i = tid; i < sp * ld; i += kSmallThreads) X[i] *= inv;
-  __syncthreads();
-
   const int S = sp / 16, tiles = S * S;
   // wavefronts that share a tile's contraction when there are few tiles
   const int share = tiles == 1 ? NW : tiles == 4 ? NW / 4 : 1;
   for (int step = 0; step < h.steps; ++step) {
+    const float first = step == 0 ? inv : 1.f;      // X is the unscaled u until its first product
     for (int t = wave / share; t < tiles; t += NW / share) {
       const int i = t / S, j = t % S, part = wave % share;
       f4 acc = {0, 0, 0, 0};
       for (int k = part * 16; k < lp; k += share * 16) {
-        const f4 x = *(const f4*)(X + (16 * i + c) * ld + k + 4 * g), y = *(const f4*)(X + (16 * j + c) * ld + k + 4 * g);
+        const f4 x = *(const f4*)(X + (16 * i + c) * ld + k + 4 * g) * first, y = *(const f4*)(X + (16 * j + c) * ld + k + 4 * g) * first;
 #pragma unroll
         for (int q = 0; q < 4; ++q) acc = mma32(x[q], y[q], acc);
       }
@@ -167,7 +165,7 @@ __global__ __launch_bounds__(kSmallThreads) void muon_small_kernel(SmallBatch ba
     }
     __syncthreads();
     if (share > 1) {
-      for (int q = tid; q < tiles * 256; q += kSmallThreads) {
+      for (int q = tid; q < tiles * 256; q += NT) {
         const int t = q >> 8, w = q & 255, i = t / S, j = t % S, ln = w >> 2;
         float v = 0.f;
         for (int p = 0; p < share; ++p) v += red[(t * share + p) * 256 + w];
@@ -199,7 +197,7 @@ __global__ __launch_bounds__(kSmallThreads) void muon_small_kernel(SmallBatch ba
       for (int k = 0; k < sp; k += 16) {
         float y[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) y[q] = X[(k + 4 * g + q) * ld + 16 * j + c];
+        for (int q = 0; q < 4; ++q) y[q] = X[(k + 4 * g + q) * ld + 16 * j + c] * first;
 #pragma unroll
         for (int i = 0; i < kSmallSide / 16; ++i) {
           if (i >= S) break;
@@ -221,13 +219,13 @@ __global__ __launch_bounds__(kSmallThreads) void muon_small_kernel(SmallBatch ba
   auto finish = [&](auto n) {
     constexpr int N = decltype(n)::value;
     const int per = T.cols / N, all = T.rows * per;
-    for (int i0 = tid; i0 < all; i0 += kBatch * kSmallThreads) {
+    for (int i0 = tid; i0 < all; i0 += kBatch * NT) {
       float w[kBatch][N];
 #pragma unroll
-      for (int q = 0; q < kBatch; ++q) get_n<BF, N>(T.p, at + (int64_t)min(i0 + q * kSmallThreads, all - 1) * N, w[q]);
+      for (int q = 0; q < kBatch; ++q) get_n<BF, N>(T.p, at + (int64_t)min(i0 + q * NT, all - 1) * N, w[q]);
 #pragma unroll
       for (int q = 0; q < kBatch; ++q) {
-        const int i = i0 + q * kSmallThreads;
+        const int i = i0 + q * NT;
         if (i >= all) break;
         const int r = i / per, k = (i - r * per) * N;
 #pragma unroll
@@ -384,56 +382,65 @@ __global__ __launch_bounds__(Pr::kThreads) void muon_product_kernel(MuonGroup G,
   uint16_t* Pm = G.P + (int64_t)mat * G.s * la;
   const Operand X = {G.X[from] + (int64_t)mat * G.s * lx, lx, G.s, G.lp};
   const Operand A = {Am, la, G.s, G.sp}, Q = {Pm, la, G.s, G.sp};
+  // what the end needs is asked for before the product
+  constexpr bool early = Pr::TM * Pr::TN <= 4;
+  f4 old[early ? Pr::TN : 1][early ? Pr::TM : 1];
+  auto end = [&](auto f) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int j = 0; j < Pr::TN; ++j)
+#pragma unroll
+      for (int i = 0; i < Pr::TM; ++i)
+        f(i, j, m0 + (wave % Pr::WM) * Pr::TM * 16 + 16 * i + 4 * (lane >> 4), n0 + (wave / Pr::WM) * Pr::TN * 16 + 16 * j + (lane & 15));
+  };
+  if constexpr (early && MODE == 1)
+    end([&](int i, int j, int m, int n) { old[j][i] = n < G.s && m < G.sp ? get_parts<NP>(Am + n * la, m) : f4{0, 0, 0, 0}; });
   Pr p;
   p.run(MODE == 4 ? Q : MODE == 1 ? A : X, MODE == 0 || MODE == 4 ? X : MODE == 1 ? A : Q, m0, n0, 0, MODE == 0 ? G.lp : G.sp, (lds_t*)smem);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
   const int rows = MODE == 4 ? G.l : G.s;
-#pragma unroll
-  for (int j = 0; j < Pr::TN; ++j) {
-    const int n = n0 + (wave / Pr::WM) * Pr::TN * 16 + 16 * j + c;
-    if (n >= rows) continue;
-#pragma unroll
-    for (int i = 0; i < Pr::TM; ++i) {
-      const int m = m0 + (wave % Pr::WM) * Pr::TM * 16 + 16 * i + 4 * g;
-      f4 v = p.acc[i][j];
-      if constexpr (MODE <= 1) {
-        if (m >= G.sp) continue;
-        if constexpr (MODE == 0) {
-          v = v * (kA / (kX * kX));
-        } else {
-          v = v * (h.c * kP / (kA * kA)) + get_parts<NP>(Am + n * la, m) * (h.b * kP / kA);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (m + e == n) v[e] += h.a * kP;
-        }
+  end([&](int i, int j, int m, int n) {
+    if (n >= rows) return;
+    f4 v = p.acc[i][j];
+    if constexpr (MODE <= 1) {
+      if (m >= G.sp) return;
+      if constexpr (MODE == 0) {
+        v = v * (kA / (kX * kX));
+      } else {
+        f4 a1;
+        if constexpr (early) a1 = old[j][i];
+        else a1 = get_parts<NP>(Am + n * la, m);
+        v = v * (h.c * kP / (kA * kA)) + a1 * (h.b * kP / kA);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (m + e >= G.s) v[e] = 0.f;      // (what pads the rows, whatever the operands' rows beyond gave)
-        uint16_t* out = MODE == 0 ? Am : Pm;
-        put_parts<NP>(out + n * la, m, v);
-        if (mt != nt) put_parts_turned<NP>(out + m * la, la, G.s - m, n, v);
-      } else if constexpr (MODE == 2) {
-        if (m >= G.lp) continue;
-        put_parts<NP>(G.X[from ^ 1] + ((int64_t)mat * G.s + n) * lx, m, v * (1.f / kP));
+          if (m + e == n) v[e] += h.a * kP;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (m + e >= G.s) v[e] = 0.f;      // (what pads the rows, whatever the operands' rows beyond gave)
+      uint16_t* out = MODE == 0 ? Am : Pm;
+      put_parts<NP>(out + n * la, m, v);
+      if (mt != nt) put_parts_turned<NP>(out + m * la, la, G.s - m, n, v);
+    } else if constexpr (MODE == 2) {
+      if (m >= G.lp) return;
+      put_parts<NP>(G.X[from ^ 1] + ((int64_t)mat * G.s + n) * lx, m, v * (1.f / kP));
+    } else {
+      const int cols = MODE == 4 ? G.s : G.l;
+      const float f = h.lr * T.scale * (1.f / (kP * kX));
+      const int64_t o = at + (int64_t)n * cols + m;
+      if ((cols & 3) == 0) {
+        float w[4];
+        if (m >= cols) return;
+        get_n<BF, 4>(T.p, o, w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = fmaf(-f, v[e], w[e] * h.keep);
+        put_n<BF, 4>(T.p, o, w);
       } else {
-        const int cols = MODE == 4 ? G.s : G.l;
-        const float f = h.lr * T.scale * (1.f / (kP * kX));
-        const int64_t o = at + (int64_t)n * cols + m;
-        if ((cols & 3) == 0) {
-          float w[4];
-          if (m >= cols) continue;
-          get_n<BF, 4>(T.p, o, w);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = fmaf(-f, v[e], w[e] * h.keep);
-          put_n<BF, 4>(T.p, o, w);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (m + e < cols) put<BF>(T.p, o + e, fmaf(-f, v[e], get<BF>(T.p, o + e) * h.keep));
-        }
+        for (int e = 0; e < 4; ++e)
+          if (m + e < cols) put<BF>(T.p, o + e, fmaf(-f, v[e], get<BF>(T.p, o + e) * h.keep));
       }
     }
-  }
+  });
 }
 
 template <class Pr, auto kernel>
@@ -578,10 +585,16 @@ struct RunGroup {
 };
 
 template <bool BF>
-hipError_t run_small(const SmallBatch& b, int lds, const MuonHyper& h, hipStream_t s) {
-  const hipError_t e = allow_lds<muon_small_kernel<BF>>();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((muon_small_kernel<BF>), dim3((unsigned)b.first[b.n]), dim3(kSmallThreads), lds, s, b, h);
+hipError_t run_small(const SmallBatch& b, size_t lds, bool large, const MuonHyper& h, hipStream_t s) {
+  const dim3 grid((unsigned)b.first[b.n]);
+  hipError_t e;
+  if (large) {
+    if ((e = allow_lds<muon_small_kernel<BF, 1024>>()) != hipSuccess) return e;
+    hipLaunchKernelGGL((muon_small_kernel<BF, 1024>), grid, dim3(1024), lds, s, b, h);
+  } else {
+    if ((e = allow_lds<muon_small_kernel<BF, 512>>()) != hipSuccess) return e;
+    hipLaunchKernelGGL((muon_small_kernel<BF, 512>), grid, dim3(512), lds, s, b, h);
+  }
   return hipGetLastError();
 }
 
@@ -594,27 +607,31 @@ size_t muon_workspace(const MuonTensor* t, int n, bool bf16) {
 }
 
 hipError_t launch_muon(const MuonTensor* t, int n, const MuonHyper& h, void* ws, hipStream_t s) {
-  SmallBatch b{};
-  size_t lds = 0;
-  auto flush = [&]() {
-    hipError_t e = hipSuccess;
-    if (b.n) e = h.bf16 ? run_small<true>(b, (int)lds, h, s) : run_small<false>(b, (int)lds, h, s);
-    b.n = 0, lds = 0;
-    return e;
-  };
-  for (int i = 0; i < n; ++i) {
-    if (t[i].count == 0 || !is_small(t[i].rows, t[i].cols)) continue;
-    if (b.n == kSmallBatch || b.first[b.n] + t[i].count > (1 << 20)) {
-      const hipError_t e = flush();
-      if (e != hipSuccess) return e;
+  // Workgroups of 16 wavefronts where a matrix has over 8192 values (2048 x 16 bf16: 65 -> 43 us), of eight else, and more of
+  // them on a CU.
+  for (int large = 0; large < 2; ++large) {
+    SmallBatch b{};
+    size_t lds = 0;
+    auto flush = [&]() {
+      hipError_t e = hipSuccess;
+      if (b.n) e = h.bf16 ? run_small<true>(b, lds, large != 0, h, s) : run_small<false>(b, lds, large != 0, h, s);
+      b.n = 0, lds = 0;
+      return e;
+    };
+    for (int i = 0; i < n; ++i) {
+      if (t[i].count == 0 || !is_small(t[i].rows, t[i].cols) || (t[i].rows * t[i].cols > 8192) != (large != 0)) continue;
+      if (b.n == kSmallBatch || b.first[b.n] + t[i].count > (1 << 20)) {
+        const hipError_t e = flush();
+        if (e != hipSuccess) return e;
+      }
+      b.t[b.n] = t[i];
+      b.first[b.n + 1] = b.first[b.n] + (int)t[i].count;
+      ++b.n;
+      lds = std::max(lds, small_lds(std::min(t[i].rows, t[i].cols), std::max(t[i].rows, t[i].cols)));
     }
-    b.t[b.n] = t[i];
-    b.first[b.n + 1] = b.first[b.n] + (int)t[i].count;
-    ++b.n;
-    lds = std::max(lds, small_lds(std::min(t[i].rows, t[i].cols), std::max(t[i].rows, t[i].cols)));
+    const hipError_t e = flush();
+    if (e != hipSuccess) return e;
   }
-  const hipError_t e = flush();
-  if (e != hipSuccess) return e;
   return for_groups(t, n, RunGroup{h.bf16 != 0, &h, (char*)ws, s});
 }
 

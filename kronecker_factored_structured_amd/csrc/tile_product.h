@@ -153,6 +153,7 @@ struct Product {
   typedef TileLoad<SA_, BM, NW, NP> LA;
   typedef TileLoad<SB_, BN, NW, NP> LB;
   static constexpr int kLoads = LA::kLoads + LB::kLoads;
+  static constexpr bool kWhole = TM * TN <= 16;      // a step's fragments fit the registers twice
   f4 acc[TM][TN];
 
   struct FragsA { u4 f[TM]; };
@@ -210,19 +211,56 @@ struct Product {
       for (int i = 0; i < kLoads; ++i) load(st, i);
       ++next;
     };
+#pragma unroll
+    for (int i = 0; i < NS; ++i) all(i);
+    if (total >= NS) in_step<NS - 1>();
+    else in_step<0>();
+    int st = 0;
+    auto none = [](int) {};
+    if constexpr (kWhole) {
+      // two sets of a step's fragments: the next step's come in while this one's are multiplied
+      FragsA a[2][2];
+      FragsB b[2][2];
+      auto fetch = [&](int set, int at) {
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+          read(a[set][kk], lds + at * kStage, kk, wm, lane);
+          read(b[set][kk], lds + at * kStage, kk, wn, lane);
+        }
+      };
+      fetch(0, 0);
+      auto step = [&](auto set, auto more) {
+        in_step<more ? NS - 2 : 0>();
+        all(st);
+        st = st + 1 == NS ? 0 : st + 1;
+        fetch(1 - set, st);      // (behind the last step: of no use, and not used)
+        if constexpr (NP == 2) multiply(a[set][1], b[set][0], none);
+        else multiply(a[set][1], b[set][1], none);
+        if constexpr (NP == 2) multiply(a[set][0], b[set][1], none);
+        multiply(a[set][0], b[set][0], none);
+      };
+      std::integral_constant<int, 0> even;
+      std::integral_constant<int, 1> odd;
+      int t = 0;
+      for (; t + 1 < total - NS; t += 2) {
+        step(even, std::true_type{});
+        step(odd, std::true_type{});
+      }
+      for (; t + 1 < total; t += 2) {
+        step(even, std::false_type{});
+        step(odd, std::false_type{});
+      }
+      if (t < total) step(even, std::false_type{});
+      __syncthreads();
+      return;
+    }
     FragsA a0, a1;
     FragsB b0, b1;
     constexpr int first = NP == 2 ? 1 : 0;      // of A's parts
-    all(0);
-    in_step<0>();
-#pragma unroll
-    for (int i = 1; i < NS; ++i) all(i);
     read(b0, lds, 0, wn, lane);
     read(a0, lds, first, wm, lane);
-    int st = 0;
     auto step = [&](auto more) {
       const lds_t* now = lds + st * kStage;
-      auto none = [](int) {};
       auto loads = [&](int i) {
         if (!more) return;
         constexpr int per = (kLoads + TM - 1) / TM;
