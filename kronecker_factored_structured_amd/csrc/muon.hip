@@ -86,6 +86,108 @@ bool is_small(int rows, int cols) {
 
 __device__ inline f4 mma32(float a, float b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
 
+// c += a b^T over 16 of the contraction, two chains of sums.
+__device__ inline void dot16(f4 a, f4 b, f4& c0, f4& c1) {
+  c0 = mma32(a[0], b[0], c0);
+  c1 = mma32(a[1], b[1], c1);
+  c0 = mma32(a[2], b[2], c0);
+  c1 = mma32(a[3], b[3], c1);
+}
+
+// The steps on X (16 S rows of ld = lp + 4) in LDS, by NW wavefronts; X times `inv` is the first one's.  What bounds them
+// is the chain of LDS reads, products and barriers of one CU: chains are split in two, contractions among the wavefronts,
+// and four of X's column blocks go together (2048 x 16: 8.3 -> 5.8 us a step, 64 x 64 5.5 -> 3.5, 32 x 64 2.2 -> 1.8).
+template <int S, int NW>
+__device__ __forceinline__ void small_steps(float* X, float* A, float* P, float* red, int lp, float inv, const MuonHyper& h) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, c = lane & 15;
+  const int ld = lp + 4;
+  constexpr int la = 16 * S + 4, T = S * (S + 1) / 2;      // tiles on and below the diagonal
+  constexpr int share = NW / T > 0 ? NW / T : 1;           // wavefronts of a tile
+  auto tile = [](int t, int& i, int& j) {
+    i = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0;
+    j = t - i * (i + 1) / 2;
+  };
+  auto put = [&](float* M, int i, int j, f4 v) {      // and its mirror image
+#pragma unroll
+    for (int e = 0; e < 4; ++e) M[(16 * i + 4 * g + e) * la + 16 * j + c] = v[e];
+    if (i != j) *(f4*)(M + (16 * j + c) * la + 16 * i + 4 * g) = v;
+  };
+  for (int step = 0; step < h.steps; ++step) {
+    const float first = step == 0 ? inv : 1.f;
+    for (int t = wave / share; t < T; t += NW / share) {
+      int i, j;
+      tile(t, i, j);
+      f4 c0 = {0, 0, 0, 0}, c1 = {0, 0, 0, 0};
+      for (int k = wave % share * 16; k < lp; k += share * 16)
+        dot16(*(const f4*)(X + (16 * i + c) * ld + k + 4 * g) * first, *(const f4*)(X + (16 * j + c) * ld + k + 4 * g) * first, c0, c1);
+      if (share == 1) put(A, i, j, c0 + c1);
+      else *(f4*)(red + wave * 256 + lane * 4) = c0 + c1;
+    }
+    __syncthreads();
+    if (share > 1) {
+      if (wave < T) {
+        int i, j;
+        tile(wave, i, j);
+        f4 v = {0, 0, 0, 0};
+#pragma unroll
+        for (int p = 0; p < share; ++p) v += *(const f4*)(red + (wave * share + p) * 256 + lane * 4);
+        put(A, i, j, v);
+      }
+      __syncthreads();
+    }
+    // P = a I + b A + c A^2 (A is symmetric: its rows are its columns)
+    for (int t = wave; t < T; t += NW) {
+      int i, j;
+      tile(t, i, j);
+      f4 c0 = {0, 0, 0, 0}, c1 = {0, 0, 0, 0}, v;
+#pragma unroll
+      for (int k = 0; k < 16 * S; k += 16)
+        dot16(*(const f4*)(A + (16 * i + c) * la + k + 4 * g), *(const f4*)(A + (16 * j + c) * la + k + 4 * g), c0, c1);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = 16 * i + 4 * g + e, k = 16 * j + c;
+        v[e] = (r == k ? h.a : 0.f) + h.b * A[r * la + k] + h.c * (c0[e] + c1[e]);
+      }
+      put(P, i, j, v);
+    }
+    __syncthreads();
+    // X = P X: a wavefront's columns are its own
+    constexpr int JB = S == 1 ? 4 : S == 2 ? 2 : 1;
+    const int blocks = lp / 16;
+    for (int j0 = wave; j0 < blocks; j0 += JB * NW) {
+      f4 acc[JB][S];
+#pragma unroll
+      for (int b = 0; b < JB; ++b)
+#pragma unroll
+        for (int i = 0; i < S; ++i) acc[b][i] = f4{0, 0, 0, 0};
+#pragma unroll
+      for (int k = 0; k < 16 * S; k += 16) {
+        f4 y[JB], x[S];
+#pragma unroll
+        for (int b = 0; b < JB; ++b)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) y[b][q] = X[(k + 4 * g + q) * ld + 16 * min(j0 + b * NW, blocks - 1) + c] * first;
+#pragma unroll
+        for (int i = 0; i < S; ++i) x[i] = *(const f4*)(P + (16 * i + c) * la + k + 4 * g);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int b = 0; b < JB; ++b)
+#pragma unroll
+            for (int i = 0; i < S; ++i) acc[b][i] = mma32(x[i][q], y[b][q], acc[b][i]);
+      }
+#pragma unroll
+      for (int b = 0; b < JB; ++b)
+        if (j0 + b * NW < blocks)
+#pragma unroll
+          for (int i = 0; i < S; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) X[(16 * i + 4 * g + e) * ld + 16 * (j0 + b * NW) + c] = acc[b][i][e];
+    }
+    __syncthreads();
+  }
+}
+
 template <bool BF, int NT>
 __global__ __launch_bounds__(NT) void muon_small_kernel(SmallBatch batch, MuonHyper h) {
   extern __shared__ char smem[];
@@ -101,7 +203,7 @@ __global__ __launch_bounds__(NT) void muon_small_kernel(SmallBatch batch, MuonHy
   float* A = X + (size_t)sp * ld;
   float* P = A + sp * la;
   float* red = P + sp * la;      // wavefronts x 256
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, c = lane & 15;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   constexpr int NW = NT / 64;
 
   // what pads X's rows and columns
@@ -143,77 +245,11 @@ __global__ __launch_bounds__(NT) void muon_small_kernel(SmallBatch batch, MuonHy
   sum = 0;
   for (int i = 0; i < NW; ++i) sum += dred[i];
   const float inv = (float)(1.0 / (sqrt(sum) + (double)h.eps));
-  const int S = sp / 16, tiles = S * S;
-  // wavefronts that share a tile's contraction when there are few tiles
-  const int share = tiles == 1 ? NW : tiles == 4 ? NW / 4 : 1;
-  for (int step = 0; step < h.steps; ++step) {
-    const float first = step == 0 ? inv : 1.f;      // X is the unscaled u until its first product
-    for (int t = wave / share; t < tiles; t += NW / share) {
-      const int i = t / S, j = t % S, part = wave % share;
-      f4 acc = {0, 0, 0, 0};
-      for (int k = part * 16; k < lp; k += share * 16) {
-        const f4 x = *(const f4*)(X + (16 * i + c) * ld + k + 4 * g) * first, y = *(const f4*)(X + (16 * j + c) * ld + k + 4 * g) * first;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) acc = mma32(x[q], y[q], acc);
-      }
-      if (share == 1) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) A[(16 * i + 4 * g + e) * la + 16 * j + c] = acc[e];
-      } else {
-        *(f4*)(red + wave * 256 + lane * 4) = acc;
-      }
-    }
-    __syncthreads();
-    if (share > 1) {
-      for (int q = tid; q < tiles * 256; q += NT) {
-        const int t = q >> 8, w = q & 255, i = t / S, j = t % S, ln = w >> 2;
-        float v = 0.f;
-        for (int p = 0; p < share; ++p) v += red[(t * share + p) * 256 + w];
-        A[(16 * i + 4 * (ln >> 4) + (w & 3)) * la + 16 * j + (ln & 15)] = v;
-      }
-      __syncthreads();
-    }
-    // P = a I + b A + c A^2 (A is symmetric: its rows are its columns)
-    for (int t = wave; t < tiles; t += NW) {
-      const int i = t / S, j = t % S;
-      f4 acc = {0, 0, 0, 0};
-      for (int k = 0; k < sp; k += 16) {
-        const f4 x = *(const f4*)(A + (16 * i + c) * la + k + 4 * g), y = *(const f4*)(A + (16 * j + c) * la + k + 4 * g);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) acc = mma32(x[q], y[q], acc);
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int r = 16 * i + 4 * g + e, k = 16 * j + c;
-        P[r * la + k] = (r == k ? h.a : 0.f) + h.b * A[r * la + k] + h.c * acc[e];
-      }
-    }
-    __syncthreads();
-    // X = P X: a wavefront's 16 columns are its own
-    for (int j = wave; j < lp / 16; j += NW) {
-      f4 acc[kSmallSide / 16];
-#pragma unroll
-      for (int i = 0; i < kSmallSide / 16; ++i) acc[i] = f4{0, 0, 0, 0};
-      for (int k = 0; k < sp; k += 16) {
-        float y[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) y[q] = X[(k + 4 * g + q) * ld + 16 * j + c] * first;
-#pragma unroll
-        for (int i = 0; i < kSmallSide / 16; ++i) {
-          if (i >= S) break;
-          const f4 x = *(const f4*)(P + (16 * i + c) * la + k + 4 * g);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) acc[i] = mma32(x[q], y[q], acc[i]);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kSmallSide / 16; ++i) {
-        if (i >= S) break;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) X[(16 * i + 4 * g + e) * ld + 16 * j + c] = acc[i][e];
-      }
-    }
-    __syncthreads();
+  switch (sp / 16) {
+    case 1: small_steps<1, NW>(X, A, P, red, lp, inv, h); break;
+    case 2: small_steps<2, NW>(X, A, P, red, lp, inv, h); break;
+    case 3: small_steps<3, NW>(X, A, P, red, lp, inv, h); break;
+    default: small_steps<4, NW>(X, A, P, red, lp, inv, h); break;
   }
   const float f = h.lr * T.scale;
   auto finish = [&](auto n) {
@@ -607,8 +643,8 @@ size_t muon_workspace(const MuonTensor* t, int n, bool bf16) {
 }
 
 hipError_t launch_muon(const MuonTensor* t, int n, const MuonHyper& h, void* ws, hipStream_t s) {
-  // Workgroups of 16 wavefronts where a matrix has over 8192 values (2048 x 16 bf16: 65 -> 43 us), of eight else, and more of
-  // them on a CU.
+  // Workgroups of 16 wavefronts where a matrix has over 8192 values or more than three tiles of A, of eight else, and more
+  // of them on a CU.
   for (int large = 0; large < 2; ++large) {
     SmallBatch b{};
     size_t lds = 0;
@@ -619,7 +655,7 @@ hipError_t launch_muon(const MuonTensor* t, int n, const MuonHyper& h, void* ws,
       return e;
     };
     for (int i = 0; i < n; ++i) {
-      if (t[i].count == 0 || !is_small(t[i].rows, t[i].cols) || (t[i].rows * t[i].cols > 8192) != (large != 0)) continue;
+      if (t[i].count == 0 || !is_small(t[i].rows, t[i].cols) || (t[i].rows * t[i].cols > 8192 || std::min(t[i].rows, t[i].cols) > 32) != (large != 0)) continue;
       if (b.n == kSmallBatch || b.first[b.n] + t[i].count > (1 << 20)) {
         const hipError_t e = flush();
         if (e != hipSuccess) return e;
