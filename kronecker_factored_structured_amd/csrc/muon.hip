@@ -397,8 +397,8 @@ __global__ __launch_bounds__(256) void muon_start_kernel(MuonGroup G, MuonHyper 
 // matrices; 4: into the tall ones' (turned: lanes hold neighbours of a row of the parameters in both).
 // A and P are symmetric: their tiles on and below the diagonal are computed (tm: tiles of a side) and written twice.
 template <class Pr, bool BF, int NP, int MODE>
-__global__ __launch_bounds__(Pr::kThreads) void muon_product_kernel(MuonGroup G, MuonHyper h, int from, int tm, int tn) {
-  extern __shared__ char smem[];
+__device__ __forceinline__ void muon_tile(const MuonGroup& G, const MuonHyper& h, const MuonTensor& T, int64_t at, int from, int tm, int tn,
+                                          char* smem) {
   int mt, nt;
   if constexpr (MODE <= 1) {
     static_assert(Pr::BM == Pr::BN, "");
@@ -410,9 +410,6 @@ __global__ __launch_bounds__(Pr::kThreads) void muon_product_kernel(MuonGroup G,
     tile_of(blockIdx.x, gridDim.x, tm, tn, mt, nt);
   }
   const int mat = blockIdx.y, m0 = mt * Pr::BM, n0 = nt * Pr::BN;
-  int64_t at;
-  const MuonTensor& T = tensor_of(G, mat, at);
-  if (MODE >= 3 && (T.rows > T.cols) != (MODE == 4)) return;
   const int64_t lx = (int64_t)G.lp * NP, la = (int64_t)G.sp * NP;      // rows of X, of A and P
   uint16_t* Am = G.A + (int64_t)mat * G.s * la;
   uint16_t* Pm = G.P + (int64_t)mat * G.s * la;
@@ -479,6 +476,16 @@ __global__ __launch_bounds__(Pr::kThreads) void muon_product_kernel(MuonGroup G,
   });
 }
 
+// Pr; the tall matrices' last product is PrT, of as many tiles the other way round.
+template <class Pr, class PrT, bool BF, int NP, int MODE>
+__global__ __launch_bounds__(Pr::kThreads) void muon_product_kernel(MuonGroup G, MuonHyper h, int from, int tm, int tn) {
+  extern __shared__ char smem[];
+  int64_t at;
+  const MuonTensor& T = tensor_of(G, blockIdx.y, at);
+  if (MODE == 3 && T.rows > T.cols) muon_tile<PrT, BF, NP, 4>(G, h, T, at, from, tn, tm, smem);
+  else muon_tile<Pr, BF, NP, MODE>(G, h, T, at, from, tm, tn, smem);
+}
+
 template <class Pr, auto kernel>
 hipError_t go(dim3 grid, hipStream_t s, const MuonGroup& G, const MuonHyper& h, int from, int tm, int tn) {
   const hipError_t e = allow_lds<kernel>();
@@ -492,17 +499,18 @@ hipError_t go(dim3 grid, hipStream_t s, const MuonGroup& G, const MuonHyper& h, 
 // 25 us with four, 21 with two).
 template <bool BF, int NP, int MODE>
 hipError_t product(const MuonGroup& G, const MuonHyper& h, int from, int mats, hipStream_t s) {
-  constexpr Side SA = MODE == 2 || MODE == 3 ? COL : ROW, SB = MODE == 4 ? COL : ROW;
-  const int M = MODE == 2 || MODE == 3 ? G.lp : G.sp, N = MODE == 4 ? G.l : G.s;
+  constexpr Side SA = MODE >= 2 ? COL : ROW;
+  const int M = MODE >= 2 ? G.lp : G.sp, N = G.s;
   auto tiles = [&](int b) {
     const int64_t m = ceil_div(M, b), n = ceil_div(N, b);
     return (MODE <= 1 ? m * (m + 1) / 2 : m * n) * mats;
   };
 #define KRON_MUON_GO(B, NS, ...)                                                                                    \
   {                                                                                                                 \
-    typedef Product<__VA_ARGS__, SA, SB, false, NP, NS> Pr;                                                         \
+    typedef Product<__VA_ARGS__, SA, ROW, false, NP, NS> Pr;                                                        \
+    typedef Product<__VA_ARGS__, ROW, COL, false, NP, NS> PrT;                                                      \
     const int tm = (int)ceil_div(M, B), tn = (int)ceil_div(N, B);                                                   \
-    return go<Pr, muon_product_kernel<Pr, BF, NP, MODE>>(dim3((unsigned)(tiles(B) / mats), (unsigned)mats), s, G, h, from, tm, tn); \
+    return go<Pr, muon_product_kernel<Pr, PrT, BF, NP, MODE>>(dim3((unsigned)(tiles(B) / mats), (unsigned)mats), s, G, h, from, tm, tn); \
   }
   if (tiles(256) >= 256) KRON_MUON_GO(256, 2, 2, 4, 8, 4)
   if (tiles(128) >= 256) KRON_MUON_GO(128, 2, 2, 2, 4, 4)
@@ -520,19 +528,11 @@ hipError_t run_group(const MuonGroup& G, const MuonHyper& h, int mats, hipStream
   else hipLaunchKernelGGL((muon_momentum_kernel<BF, 1>), grid, dim3(256), 0, s, G, h);
   const int tl = G.lp / 64, ts = (int)ceil_div(G.s, 64);
   hipLaunchKernelGGL((muon_start_kernel<BF, NP>), dim3((unsigned)(tl * ts), (unsigned)mats), dim3(256), 0, s, G, h, tl);
-  bool wide = false, tall = false;
-  for (int i = 0; i < G.n; ++i) (G.t[i].rows > G.t[i].cols ? tall : wide) = true;
   hipError_t e = hipGetLastError();
   for (int i = 0; i < h.steps && e == hipSuccess; ++i) {
     e = product<BF, NP, 0>(G, h, i & 1, mats, s);
     if (e == hipSuccess) e = product<BF, NP, 1>(G, h, i & 1, mats, s);
-    if (e != hipSuccess) break;
-    if (i + 1 < h.steps) {
-      e = product<BF, NP, 2>(G, h, i & 1, mats, s);
-    } else {
-      if (wide) e = product<BF, NP, 3>(G, h, i & 1, mats, s);
-      if (tall && e == hipSuccess) e = product<BF, NP, 4>(G, h, i & 1, mats, s);
-    }
+    if (e == hipSuccess) e = i + 1 < h.steps ? product<BF, NP, 2>(G, h, i & 1, mats, s) : product<BF, NP, 3>(G, h, i & 1, mats, s);
   }
   return e;
 }

@@ -293,12 +293,12 @@ struct Product {
   }
 };
 
-// Workgroup `id` of tm x tn tiles as (mt, nt): each of the eight XCDs takes a run of them, in bands of eight nt
+// Workgroup `id` of tm x tn tiles as (mt, nt): each of the eight XCDs takes a run of them, in bands of `width` nt
 // tiles (what is read again soon stays in its L2).
-__device__ inline void tile_of(int id, int count, int tm, int tn, int& mt, int& nt) {
+__device__ inline void tile_of(int id, int count, int tm, int tn, int& mt, int& nt, int width = 8) {
   const int x = id & 7, q = count / 8, r = count % 8;
   id = x * q + min(x, r) + (id >> 3);
-  const int band = id / (8 * tm), first = band * 8, wide = min(8, tn - first), in = id - band * 8 * tm;
+  const int band = id / (width * tm), first = band * width, wide = min(width, tn - first), in = id - band * width * tm;
   nt = first + in % wide, mt = in / wide;
 }
 

@@ -235,35 +235,8 @@ __global__ __launch_bounds__(P::kThreads) void vocab_fwd_kernel(VocabCE a, int t
   }
 }
 
-// A row's statistics from its tiles': 32 rows by 32 slices of the tiles.
-__global__ __launch_bounds__(1024) void vocab_join_kernel(VocabCE a, int tiles) {
-  __shared__ float2 red[32][33];
-  const int count = vocab_count(a), r = threadIdx.x & 31, sl = threadIdx.x >> 5;
-  const int64_t i = (int64_t)blockIdx.x * 32 + r;
-  const float2* part = (const float2*)a.part;
-  float2 s = {-INFINITY, 0.f};
-  if (i < count)
-    for (int m = sl; m < tiles; m += 32) s = joined(s, part[(int64_t)m * a.N + i]);
-  red[sl][r] = s;
-  __syncthreads();
-  // the row's 32 slices by half a wavefront
-  const int row32 = threadIdx.x >> 5;
-  s = red[threadIdx.x & 31][row32];
-#pragma unroll
-  for (int o = 16; o >= 1; o /= 2) s = joined(s, float2{__shfl_xor(s.x, o, 32), __shfl_xor(s.y, o, 32)});
-  const int64_t k = (int64_t)blockIdx.x * 32 + row32;
-  if ((threadIdx.x & 31) != 0 || k >= count) return;
-  const int64_t row = a.idx ? a.idx[k] : k;
-  const int64_t lab = a.labels[row];
-  const bool token = lab >= 0 && lab < a.V;
-  a.nll[row] = token ? (float)(((double)s.x + (double)log2f(s.y)) / (double)kLog2e - (double)a.zlab[k]) : NAN;
-  a.stats[2 * row] = s.x;
-  a.stats[2 * row + 1] = token ? 1.f / s.y : NAN;
-}
-
-// loss = sum_n w_n nll_n in 64 bits, in a fixed order.
-__global__ __launch_bounds__(1024) void vocab_loss_kernel(VocabCE a) {
-  __shared__ double red[16];
+// loss = sum_n w_n nll_n in 64 bits, in a fixed order (1024 threads).
+__device__ inline void vocab_sum(const VocabCE& a, double* red) {
   double s = 0;
   for (int64_t n = threadIdx.x; n < a.N; n += 1024) {
     const float w = a.weights ? a.weights[n] : a.mean;
@@ -276,6 +249,46 @@ __global__ __launch_bounds__(1024) void vocab_loss_kernel(VocabCE a) {
     for (int i = 1; i < 16; ++i) s += red[i];
     a.loss[0] = (float)s;
   }
+}
+
+// A row's statistics from its tiles': 32 rows by 32 slices of the tiles.  One workgroup alone (few rows) takes them all, and
+// the loss.
+__global__ __launch_bounds__(1024) void vocab_join_kernel(VocabCE a, int tiles) {
+  __shared__ float2 red[32][33];
+  __shared__ double sums[16];
+  const int count = vocab_count(a), r = threadIdx.x & 31, sl = threadIdx.x >> 5;
+  const float2* part = (const float2*)a.part;
+  for (int64_t row0 = (int64_t)blockIdx.x * 32; row0 < count; row0 += (int64_t)gridDim.x * 32) {
+    float2 s = {-INFINITY, 0.f};
+    if (row0 + r < count)
+#pragma unroll 8
+      for (int m = sl; m < tiles; m += 32) s = joined(s, part[(int64_t)m * a.N + row0 + r]);
+    red[sl][r] = s;
+    __syncthreads();
+    // the row's 32 slices by half a wavefront
+    s = red[r][sl];
+#pragma unroll
+    for (int o = 16; o >= 1; o /= 2) s = joined(s, float2{__shfl_xor(s.x, o, 32), __shfl_xor(s.y, o, 32)});
+    const int64_t k = row0 + sl;
+    if (r == 0 && k < count) {
+      const int64_t row = a.idx ? a.idx[k] : k;
+      const int64_t lab = a.labels[row];
+      const bool token = lab >= 0 && lab < a.V;
+      a.nll[row] = token ? (float)(((double)s.x + (double)log2f(s.y)) / (double)kLog2e - (double)a.zlab[k]) : NAN;
+      a.stats[2 * row] = s.x;
+      a.stats[2 * row + 1] = token ? 1.f / s.y : NAN;
+    }
+    __syncthreads();
+  }
+  if (gridDim.x == 1) {
+    __threadfence_block();
+    vocab_sum(a, sums);
+  }
+}
+
+__global__ __launch_bounds__(1024) void vocab_loss_kernel(VocabCE a) {
+  __shared__ double red[16];
+  vocab_sum(a, red);
 }
 
 // ------------------------------------------------------------------------------ backward
@@ -346,7 +359,7 @@ template <class P, bool BF>
 __global__ __launch_bounds__(P::kThreads) void vocab_dh_kernel(VocabCE a, int v0, int vc, int tm, int tn, int len, int add) {
   extern __shared__ char smem[];
   int mt, nt;
-  tile_of(blockIdx.x, gridDim.x, tm, tn, mt, nt);
+  tile_of(blockIdx.x, gridDim.x, tm, tn, mt, nt, 4);
   const int count = vocab_count(a), m0 = mt * P::BM, n0 = nt * P::BN;
   if (n0 >= count) return;
   const int k0 = blockIdx.y * len, k1 = min(vc, k0 + len);
@@ -610,7 +623,9 @@ hipError_t run_fwd(const VocabCE& a, const VocabPlan& p, hipStream_t s) {
     const dim3 grid((unsigned)(p.tiles * tn));
     e = few(a.N) ? go<PF, vocab_fwd_kernel<PF, BF>>(grid, s, a, p.tiles, tn) : go<PB, vocab_fwd_kernel<PB, BF>>(grid, s, a, p.tiles, tn);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(vocab_join_kernel, dim3((unsigned)ceil_div(a.N, 32)), dim3(1024), 0, s, a, p.tiles);
+    const bool one = a.N <= 128;      // a workgroup's few turns are shorter than another launch
+    hipLaunchKernelGGL(vocab_join_kernel, dim3(one ? 1u : (unsigned)ceil_div(a.N, 32)), dim3(1024), 0, s, a, p.tiles);
+    if (one) return hipGetLastError();
   }
   hipLaunchKernelGGL(vocab_loss_kernel, dim3(1), dim3(1024), 0, s, a);
   return hipGetLastError();
