@@ -2,8 +2,8 @@
 // adapter e (or none): with D_e = down[e] (R x K) and U_e = up[e] (M x R)
 //   y = base + s_e (x D_e^T) U_e^T
 //   backward, t = s_e x D_e^T and g = s_e dy U_e:  dx = base + g D_e,  dD_e = g^T x,  dU_e = dy^T t
-// Sixteen rows of one request are a workgroup's: their inner product stays on chip, x is read once and y written
-// once.  bf16 x and D_e are multiplied by the bf16 matrix instruction (exact products), everything else by the fp32
+// Sixteen rows of one request are a workgroup's, or 32 and twice the wavefronts where there are many (D_e and U_e are
+// read once for all of them): their inner product stays on chip, x is read once and y written once.  bf16 x and D_e are multiplied by the bf16 matrix instruction (exact products), everything else by the fp32
 // one: neither the inner products nor the gradients are rounded on the way.
 #include <algorithm>
 
@@ -17,8 +17,8 @@ typedef float f4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 typedef __bf16 b8 __attribute__((ext_vector_type(8)));
 
-constexpr int kRows = 16;            // rows of a tile
-constexpr int kThreads = 256, kWaves = 4;
+constexpr int kThreads = 256;        // of a workgroup for each sixteen rows (RB of them)
+constexpr int kWaves = 4;
 
 __device__ inline f4 mma32(float a, float b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
 __device__ inline f4 mma16(u4 a, u4 b, f4 c) {
@@ -104,13 +104,15 @@ struct Tile {
   int rows, id;      // 0 rows: none
 };
 
-// The tile of workgroup `w`: the w-th block of sixteen rows, counted request by request.
+// The tile of workgroup `w`: the w-th block of 16 RB rows, counted request by request.  sh: 2 + the wavefronts.
+template <int RB>
 __device__ inline Tile find_tile(const Adapters& a, int64_t w, int* sh) {
+  constexpr int kRows = 16 * RB, NW = kWaves * RB;
   if (!a.starts) return {w, w < a.N ? 1 : 0, w < a.N ? a.ids[w] : -1};
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int64_t before = 0;
-  if (tid == 0) sh[5] = -1;
-  for (int i0 = 0; i0 < a.B + 2; i0 += kThreads) {
+  if (tid == 0) sh[NW + 1] = -1;
+  for (int i0 = 0; i0 < a.B + 2; i0 += RB * kThreads) {
     int64_t r0 = 0, r1 = 0;
     if (i0 + tid < a.B + 2) segment(a, i0 + tid, r0, r1);
     const int mine = (int)((r1 - r0 + kRows - 1) / kRows);
@@ -124,94 +126,107 @@ __device__ inline Tile find_tile(const Adapters& a, int64_t w, int* sh) {
     __syncthreads();
     int64_t at = before + sum - mine;
     int64_t all = 0;
-    for (int k = 0; k < kWaves; ++k) {
+    for (int k = 0; k < NW; ++k) {
       if (k < wave) at += sh[k];
       all += sh[k];
     }
-    if (w >= at && w < at + mine) sh[4] = (int)(w - at), sh[5] = i0 + tid;
+    if (w >= at && w < at + mine) sh[NW] = (int)(w - at), sh[NW + 1] = i0 + tid;
     before += all;
     __syncthreads();
     if (w < before) break;
   }
-  const int i = sh[5];
+  const int i = sh[NW + 1];
   if (i < 0) return {0, 0, -1};
   int64_t r0, r1;
   segment(a, i, r0, r1);
-  r0 += (int64_t)sh[4] * kRows;
+  r0 += (int64_t)sh[NW] * kRows;
   return {r0, (int)min<int64_t>(kRows, r1 - r0), i == 0 || i == a.B + 1 ? -1 : a.ids[i - 1]};
 }
 
-// The wavefronts' parts of a 16 x R product, joined, times f: t[16][RT * 16 + 4].
-template <int RT>
-__device__ inline void join(const Adapters& a, const f4* acc, float f, float* red, float* t) {
+// The wavefronts' parts of a (16 RB) x R product, joined, times f: t[16 RB][RT * 16 + 4].
+template <int RT, int RB>
+__device__ inline void join(const Adapters& a, const f4 (*acc)[RT], float f, float* red, float* t) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
-  for (int i = 0; i < RT; ++i) *(f4*)(red + ((wave * RT + i) * 64 + lane) * 4) = acc[i];
+  for (int y = 0; y < RB; ++y)
+#pragma unroll
+    for (int i = 0; i < RT; ++i) *(f4*)(red + (((wave * RB + y) * RT + i) * 64 + lane) * 4) = acc[y][i];
   __syncthreads();
-  for (int e = threadIdx.x; e < RT * 256; e += kThreads) {
-    const int i = e >> 8, ln = (e & 255) >> 2, q = e & 3;
+  for (int e = threadIdx.x; e < RB * RT * 256; e += RB * kThreads) {
+    const int yi = e >> 8, ln = (e & 255) >> 2, q = e & 3;
     float s = 0.f;
 #pragma unroll
-    for (int k = 0; k < kWaves; ++k) s += red[(k * RT * 64) * 4 + e];
-    const int r = 16 * i + (ln & 15);
-    t[(4 * (ln >> 4) + q) * (RT * 16 + 4) + r] = r < a.R ? s * f : 0.f;
+    for (int k = 0; k < kWaves * RB; ++k) s += red[(k * RB * RT * 64) * 4 + e];
+    const int r = 16 * (yi % RT) + (ln & 15);
+    t[(16 * (yi / RT) + 4 * (ln >> 4) + q) * (RT * 16 + 4) + r] = r < a.R ? s * f : 0.f;
   }
   __syncthreads();
 }
 
 // t = f v w^T for the tile's rows of v (width n) and w (R x n): the wavefronts share the contraction, each with
 // kBatch blocks of it in flight (a block's latency after the other's, 64 tokens of 1024 -> 4096 took 13.7 us).
-template <bool BF, int RT>
+template <bool BF, int RT, int RB>
 __device__ inline void inner(const Adapters& a, const Tile& T, const void* v, const void* w, int n, float f, float* red, float* t) {
-  constexpr int KB = BF ? 32 : 16, VE = BF ? 8 : 4, kBatch = RT >= 8 ? 1 : 8 / RT;
+  constexpr int KB = BF ? 32 : 16, VE = BF ? 8 : 4, NW = kWaves * RB, kBatch = RT * RB >= 8 ? 1 : 8 / (RT * RB);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
-  f4 acc[RT];
+  f4 acc[RB][RT];
+  int64_t vrow[RB], wrow[RT];
 #pragma unroll
-  for (int i = 0; i < RT; ++i) acc[i] = f4{0, 0, 0, 0};
-  const int64_t vrow = (T.row + min(c, T.rows - 1)) * n;
-  int64_t wrow[RT];
+  for (int y = 0; y < RB; ++y) {
+    vrow[y] = (T.row + min(16 * y + c, T.rows - 1)) * n;
+#pragma unroll
+    for (int i = 0; i < RT; ++i) acc[y][i] = f4{0, 0, 0, 0};
+  }
 #pragma unroll
   for (int i = 0; i < RT; ++i) wrow[i] = (int64_t)min(16 * i + c, a.R - 1) * n;
-  for (int k = wave * KB; k < n; k += kBatch * kWaves * KB) {
-    u4 x[kBatch], d[kBatch][RT];
+  for (int k = wave * KB; k < n; k += kBatch * NW * KB) {
+    u4 x[kBatch][RB], d[kBatch][RT];
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      const int at = k + b * kWaves * KB + VE * g;
-      x[b] = load16<BF>(v, vrow + at, n - at);
+      const int at = k + b * NW * KB + VE * g;
+#pragma unroll
+      for (int y = 0; y < RB; ++y) x[b][y] = load16<BF>(v, vrow[y] + at, n - at);
 #pragma unroll
       for (int i = 0; i < RT; ++i) d[b][i] = load16<BF>(w, wrow[i] + at, n - at);
     }
 #pragma unroll
     for (int b = 0; b < kBatch; ++b)
 #pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        if constexpr (BF) {
-          acc[i] = mma16(x[b], d[b][i], acc[i]);      // rows x rank
-        } else {
+      for (int y = 0; y < RB; ++y)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) acc[i] = mma32(value<false>(x[b], q), value<false>(d[b][i], q), acc[i]);
+        for (int i = 0; i < RT; ++i) {
+          if constexpr (BF) {
+            acc[y][i] = mma16(x[b][y], d[b][i], acc[y][i]);      // rows x rank
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) acc[y][i] = mma32(value<false>(x[b][y], q), value<false>(d[b][i], q), acc[y][i]);
+          }
         }
-      }
   }
-  join<RT>(a, acc, f, red, t);
+  join<RT, RB>(a, acc, f, red, t);
 }
 
 // g = f v w for w (n x R): w's values one by one, sixteen neighbours of a row together.
-template <bool BF, int RT>
+template <bool BF, int RT, int RB>
 __device__ inline void inner_t(const Adapters& a, const Tile& T, const void* v, const void* w, int n, float f, float* red, float* t) {
-  constexpr int KB = BF ? 32 : 16, VE = BF ? 8 : 4, kBatch = RT >= 4 ? 1 : (BF ? 4 : 8) / RT;
+  constexpr int KB = BF ? 32 : 16, VE = BF ? 8 : 4, NW = kWaves * RB, kBatch = RT >= 4 ? 1 : (BF ? 4 : 8) / RT;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
-  f4 acc[RT];
+  f4 acc[RB][RT];
+  int64_t vrow[RB];
 #pragma unroll
-  for (int i = 0; i < RT; ++i) acc[i] = f4{0, 0, 0, 0};
-  const int64_t vrow = (T.row + min(c, T.rows - 1)) * n;
-  for (int k = wave * KB; k < n; k += kBatch * kWaves * KB) {
-    u4 x[kBatch];
+  for (int y = 0; y < RB; ++y) {
+    vrow[y] = (T.row + min(16 * y + c, T.rows - 1)) * n;
+#pragma unroll
+    for (int i = 0; i < RT; ++i) acc[y][i] = f4{0, 0, 0, 0};
+  }
+  for (int k = wave * KB; k < n; k += kBatch * NW * KB) {
+    u4 x[kBatch][RB];
     float u[kBatch][RT][VE];
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      const int at = k + b * kWaves * KB + VE * g;
-      x[b] = load16<BF>(v, vrow + at, n - at);
+      const int at = k + b * NW * KB + VE * g;
+#pragma unroll
+      for (int y = 0; y < RB; ++y) x[b][y] = load16<BF>(v, vrow[y] + at, n - at);
 #pragma unroll
       for (int i = 0; i < RT; ++i)
 #pragma unroll
@@ -220,11 +235,13 @@ __device__ inline void inner_t(const Adapters& a, const Tile& T, const void* v, 
 #pragma unroll
     for (int b = 0; b < kBatch; ++b)
 #pragma unroll
-      for (int i = 0; i < RT; ++i)
+      for (int q = 0; q < VE; ++q)
 #pragma unroll
-        for (int q = 0; q < VE; ++q) acc[i] = mma32(value<BF>(x[b], q), u[b][i][q], acc[i]);
+        for (int y = 0; y < RB; ++y)
+#pragma unroll
+          for (int i = 0; i < RT; ++i) acc[y][i] = mma32(value<BF>(x[b][y], q), u[b][i][q], acc[y][i]);
   }
-  join<RT>(a, acc, f, red, t);
+  join<RT, RB>(a, acc, f, red, t);
 }
 
 // Column of a row of y or dx that lane c of block h (of the two that bf16 takes together) stands for: the lane that
@@ -236,7 +253,7 @@ __device__ inline int column(int c, int h) { return BF ? 8 * (c >> 2) + 4 * h + 
 template <bool BF>
 __device__ inline void plain_rows(const Adapters& a, const Tile& T, const void* base, void* out, int n, int part, int parts) {
   if (T.id < 0 && base == out) return;
-  for (int64_t i = (int64_t)part * kThreads + threadIdx.x; i < (int64_t)T.rows * n; i += (int64_t)parts * kThreads) {
+  for (int64_t i = (int64_t)part * blockDim.x + threadIdx.x; i < (int64_t)T.rows * n; i += (int64_t)parts * blockDim.x) {
     const int64_t at = T.row * n + i;
     if (T.id >= 0) {
       if (BF) ((uint16_t*)out)[at] = 0x7fc0;
@@ -249,202 +266,189 @@ __device__ inline void plain_rows(const Adapters& a, const Tile& T, const void* 
   }
 }
 
-template <int RT>
+template <int RT, int RB>
 struct Shared {
-  float red[kWaves * RT * 256];
-  float t[kRows * (RT * 16 + 4)];
-  float g[kRows * (RT * 16 + 4)];
-  int find[8];
+  float red[kWaves * RB * RB * RT * 256];
+  float t[16 * RB * (RT * 16 + 4)];
+  float g[16 * RB * (RT * 16 + 4)];
+  int find[kWaves * RB + 2];
 };
 
-template <bool BF, int RT>
-__global__ __launch_bounds__(kThreads) void adapters_fwd_kernel(Adapters a) {
-  __shared__ Shared<RT> sh;
-  const Tile T = find_tile(a, blockIdx.x, sh.find);
+// out = base + t w for the tile's rows (width n), kBatch blocks of 16 or (bf16) 32 columns in flight.  factors(m, i, g): w's
+// values 16 i + 4 g .. + 3 of the rank at column m.
+template <bool BF, int RT, int RB, class F>
+__device__ inline void outer(const Adapters& a, const Tile& T, const float* t, const void* base, void* out, int n, int part, int parts,
+                             const F& factors) {
+  constexpr int H = BF ? 2 : 1, W = 16 * H, NW = kWaves * RB, kBatch = RT >= 4 ? 1 : 4 / RT / H + (RT == 2 && BF);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
+  f4 tr[RB][RT];
+  int64_t row[RB];
+#pragma unroll
+  for (int y = 0; y < RB; ++y) {
+    row[y] = (T.row + min(16 * y + c, T.rows - 1)) * n;
+#pragma unroll
+    for (int i = 0; i < RT; ++i) tr[y][i] = *(const f4*)(t + (16 * y + c) * (RT * 16 + 4) + 16 * i + 4 * g);
+  }
+  const int stride = parts * NW * W;
+  for (int m = (part * NW + wave) * W; m < n; m += kBatch * stride) {
+    f4 w[kBatch][H][RT];
+    u4 old[kBatch][RB];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int m0 = m + b * stride, at = m0 + 4 * H * g;
+#pragma unroll
+      for (int y = 0; y < RB; ++y) old[b][y] = base ? load16<BF>(base, row[y] + at, n - at) : u4{0, 0, 0, 0};
+#pragma unroll
+      for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int i = 0; i < RT; ++i) w[b][h][i] = factors(min(m0 + column<BF>(c, h), n - 1), i, g);
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int at = m + b * stride + 4 * H * g;
+#pragma unroll
+      for (int y = 0; y < RB; ++y) {
+        f4 acc[H];
+#pragma unroll
+        for (int h = 0; h < H; ++h) acc[h] = f4{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int h = 0; h < H; ++h) acc[h] = mma32(w[b][h][i][q], tr[y][i][q], acc[h]);      // columns x rows
+        if (16 * y + c < T.rows) store16<BF>(out, row[y] + at, n - at, old[b][y], acc);
+      }
+    }
+  }
+}
+
+template <bool BF, int RT, int RB>
+__global__ __launch_bounds__(RB * kThreads) void adapters_fwd_kernel(Adapters a) {
+  __shared__ Shared<RT, RB> sh;
+  const Tile T = find_tile<RB>(a, blockIdx.x, sh.find);
   if (T.rows == 0) return;
   if (T.id < 0 || T.id >= a.E) {
     plain_rows<BF>(a, T, a.base, a.y, a.M, blockIdx.y, gridDim.y);
     return;
   }
-  constexpr int H = BF ? 2 : 1, W = 16 * H, kBatch = RT >= 4 ? 1 : 4 / RT / H + (RT == 2 && BF);
   const size_t es = BF ? 2 : 4;
   const float f = a.scales ? a.scales[T.id] : 1.f;
   const char* D = (const char*)a.down + (size_t)T.id * a.R * a.K * es;
   const char* U = (const char*)a.up + (size_t)T.id * a.R * a.M * es;
-  inner<BF, RT>(a, T, a.x, D, a.K, f, sh.red, sh.t);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
-  f4 t[RT];
-#pragma unroll
-  for (int i = 0; i < RT; ++i) t[i] = *(const f4*)(sh.t + c * (RT * 16 + 4) + 16 * i + 4 * g);
-  const int64_t row = (T.row + min(c, T.rows - 1)) * a.M;
-  const int stride = (int)gridDim.y * kWaves * W;
-  for (int m = (blockIdx.y * kWaves + wave) * W; m < a.M; m += kBatch * stride) {
-    f4 u[kBatch][H][RT];
-    u4 base[kBatch];
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const int m0 = m + b * stride, at = m0 + 4 * H * g;
-      base[b] = load16<BF>(a.base, row + at, a.M - at);
-#pragma unroll
-      for (int h = 0; h < H; ++h)
-#pragma unroll
-        for (int i = 0; i < RT; ++i)
-          u[b][h][i] = load4<BF>(U, (int64_t)min(m0 + column<BF>(c, h), a.M - 1) * a.R + 16 * i + 4 * g, a.R - 16 * i - 4 * g);
-    }
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      f4 acc[H];
-#pragma unroll
-      for (int h = 0; h < H; ++h) {
-        acc[h] = f4{0, 0, 0, 0};
-#pragma unroll
-        for (int i = 0; i < RT; ++i)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) acc[h] = mma32(u[b][h][i][q], t[i][q], acc[h]);      // columns of y x rows
-      }
-      const int at = m + b * stride + 4 * H * g;
-      if (c < T.rows) store16<BF>(a.y, row + at, a.M - at, base[b], acc);
-    }
-  }
+  inner<BF, RT, RB>(a, T, a.x, D, a.K, f, sh.red, sh.t);
+  outer<BF, RT, RB>(a, T, sh.t, a.base, a.y, a.M, blockIdx.y, gridDim.y,
+                    [&](int m, int i, int g) { return load4<BF>(U, (int64_t)m * a.R + 16 * i + 4 * g, a.R - 16 * i - 4 * g); });
 }
 
 // The rows' part of the backward: t and g of each row for the gradients' kernel, and dx.
-template <bool BF, int RT>
-__global__ __launch_bounds__(kThreads) void adapters_rows_kernel(Adapters a) {
-  __shared__ Shared<RT> sh;
-  const Tile T = find_tile(a, blockIdx.x, sh.find);
+template <bool BF, int RT, int RB>
+__global__ __launch_bounds__(RB * kThreads) void adapters_rows_kernel(Adapters a) {
+  __shared__ Shared<RT, RB> sh;
+  const Tile T = find_tile<RB>(a, blockIdx.x, sh.find);
   if (T.rows == 0) return;
   if (T.id < 0 || T.id >= a.E) {
     if (a.y) plain_rows<BF>(a, T, a.base, a.y, a.K, 0, 1);
     return;
   }
-  constexpr int H = BF ? 2 : 1, W = 16 * H, kBatch = RT >= 4 ? 1 : 4 / RT / H + (RT == 2 && BF);
   const size_t es = BF ? 2 : 4;
   const float f = a.scales ? a.scales[T.id] : 1.f;
   const char* D = (const char*)a.down + (size_t)T.id * a.R * a.K * es;
   const char* U = (const char*)a.up + (size_t)T.id * a.R * a.M * es;
-  inner<BF, RT>(a, T, a.x, D, a.K, f, sh.red, sh.t);
-  inner_t<BF, RT>(a, T, a.dy, U, a.M, f, sh.red, sh.g);
+  inner<BF, RT, RB>(a, T, a.x, D, a.K, f, sh.red, sh.t);
+  inner_t<BF, RT, RB>(a, T, a.dy, U, a.M, f, sh.red, sh.g);
   float* keep = a.ws + T.row * 2 * (RT * 16);
-  for (int e = threadIdx.x; e < T.rows * RT * 16; e += kThreads) {
+  for (int e = threadIdx.x; e < T.rows * RT * 16; e += RB * kThreads) {
     const int r = e / (RT * 16), k = e % (RT * 16);
     keep[(int64_t)r * 2 * RT * 16 + k] = sh.t[r * (RT * 16 + 4) + k];
     keep[(int64_t)r * 2 * RT * 16 + RT * 16 + k] = sh.g[r * (RT * 16 + 4) + k];
   }
   if (!a.y) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
-  f4 t[RT];
+  outer<BF, RT, RB>(a, T, sh.g, a.base, a.y, a.K, 0, 1, [&](int k, int i, int g) {
+    f4 d;
 #pragma unroll
-  for (int i = 0; i < RT; ++i) t[i] = *(const f4*)(sh.g + c * (RT * 16 + 4) + 16 * i + 4 * g);
-  const int64_t row = (T.row + min(c, T.rows - 1)) * a.K;
-  for (int k = wave * W; k < a.K; k += kBatch * kWaves * W) {
-    float d[kBatch][H][RT][4];
-    u4 base[kBatch];
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const int k0 = k + b * kWaves * W, at = k0 + 4 * H * g;
-      base[b] = a.base ? load16<BF>(a.base, row + at, a.K - at) : u4{0, 0, 0, 0};
-#pragma unroll
-      for (int h = 0; h < H; ++h)
-#pragma unroll
-        for (int i = 0; i < RT; ++i)
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            d[b][h][i][q] = load1<BF>(D, (int64_t)min(16 * i + 4 * g + q, a.R - 1) * a.K + min(k0 + column<BF>(c, h), a.K - 1));
-    }
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      f4 acc[H];
-#pragma unroll
-      for (int h = 0; h < H; ++h) {
-        acc[h] = f4{0, 0, 0, 0};
-#pragma unroll
-        for (int i = 0; i < RT; ++i)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) acc[h] = mma32(d[b][h][i][q], t[i][q], acc[h]);
-      }
-      const int at = k + b * kWaves * W + 4 * H * g;
-      if (c < T.rows) store16<BF>(a.y, row + at, a.K - at, base[b], acc);
-    }
-  }
+    for (int q = 0; q < 4; ++q) d[q] = load1<BF>(D, (int64_t)min(16 * i + 4 * g + q, a.R - 1) * a.K + k);
+    return d;
+  });
 }
 
-// The adapters' gradients: a block of columns of x (dD = g^T x) or of dy (dU = dy^T t) of one adapter, over every
-// `splits`-th four rows of its.  A lane has NC neighbouring columns: column NC c + q is lane c's of product q.
+// The adapters' gradients: 64 columns of x (dD = g^T x) or of dy (dU = dy^T t) of one adapter, over every `splits`-th four
+// rows of its.  A lane has four neighbouring columns: column 4 c + q is lane c's of product q.
+constexpr int kCols = 64, kParamWaves = 8;
 template <bool BF, int RT>
-constexpr int lane_cols() { return BF && RT <= 2 ? 8 : 4; }
-template <bool BF, int RT>
-__global__ __launch_bounds__(kThreads) void adapters_params_kernel(Adapters a, int kblocks, int splits, float* part) {
-  constexpr int NC = lane_cols<BF, RT>(), kBatch = RT >= 4 ? 2 : 4;
-  __shared__ float red[kWaves][RT * NC][256];
+__global__ __launch_bounds__(64 * kParamWaves) void adapters_params_kernel(Adapters a, int kblocks, int splits, float* part) {
+  constexpr int kBatch = 8 / RT;
+  __shared__ float red[kParamWaves][4][256];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
   const int e = blockIdx.y, split = blockIdx.z;
   const bool up = (int)blockIdx.x >= kblocks;
-  const int n = up ? a.M : a.K, col0 = (up ? blockIdx.x - kblocks : blockIdx.x) * 16 * NC, mine = col0 + NC * c;
+  const int n = up ? a.M : a.K, col0 = (up ? blockIdx.x - kblocks : blockIdx.x) * kCols, mine = col0 + 4 * c;
   const void* v = up ? a.dy : a.x;
   const float* tg = a.ws + (up ? 0 : RT * 16);
-  f4 acc[RT][NC];
+  f4 acc[RT][4];
 #pragma unroll
   for (int i = 0; i < RT; ++i)
 #pragma unroll
-    for (int q = 0; q < NC; ++q) acc[i][q] = f4{0, 0, 0, 0};
-  const int stride = kWaves * splits, turn = split * kWaves + wave;
-  int64_t seen = 0;      // blocks of four rows before
+    for (int q = 0; q < 4; ++q) acc[i][q] = f4{0, 0, 0, 0};
+  // The adapter's blocks of four rows, 64 requests at a time (a lane has one's rows) and numbered through them: the
+  // wavefronts take turns, kBatch blocks of any requests in flight (request by request, 512 of 16 rows took 105 us).
+  const int stride = kParamWaves * splits, turn = split * kParamWaves + wave;
+  int64_t seen = 0;
   for (int i0 = 0; i0 < a.B; i0 += 64) {
-    uint64_t todo = __ballot(i0 + lane < a.B && a.ids[min(i0 + lane, a.B - 1)] == e);
-    while (todo) {
-      const int i = i0 + __builtin_ctzll(todo);
-      todo &= todo - 1;
-      int64_t r0 = i, r1 = min<int64_t>(i + 1, a.N);
-      if (a.starts) segment(a, i + 1, r0, r1);
-      const int64_t blocks = (r1 - r0 + 3) / 4;
-      int64_t b = (turn - seen % stride + stride) % stride;
-      seen += blocks;
-      for (; b < blocks; b += kBatch * stride) {
-        u4 x[kBatch];
-        float w[kBatch][RT];
-#pragma unroll
-        for (int t = 0; t < kBatch; ++t) {
-          const int64_t row = r0 + 4 * (b + t * stride) + g;
-          const bool in = row < r1;
-          x[t] = u4{0, 0, 0, 0};
-          if (in) {
-            if (NC == 4 && BF) {
-              const f4 y = load4<BF>(v, row * n + mine, n - mine);
-              x[t] = __builtin_bit_cast(u4, y);
-            } else {
-              x[t] = load16<BF>(v, row * n + mine, n - mine);
-            }
-          }
-#pragma unroll
-          for (int k = 0; k < RT; ++k) w[t][k] = in ? tg[row * 2 * RT * 16 + 16 * k + c] : 0.f;
-        }
-#pragma unroll
-        for (int t = 0; t < kBatch; ++t)
-#pragma unroll
-          for (int k = 0; k < RT; ++k)
-#pragma unroll
-            for (int q = 0; q < NC; ++q) acc[k][q] = mma32(w[t][k], value<NC == 8>(x[t], q), acc[k][q]);      // rank x columns
-      }
+    int r0 = 0, r1 = 0;
+    if (i0 + lane < a.B && a.ids[i0 + lane] == e) {
+      int64_t lo = i0 + lane, hi = min<int64_t>(i0 + lane + 1, a.N);
+      if (a.starts) segment(a, i0 + lane + 1, lo, hi);
+      r0 = (int)lo, r1 = (int)hi;
     }
+    const int blocks = (r1 - r0 + 3) / 4;
+    int upto = blocks;      // blocks of the requests up to this lane's
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2) {
+      const int y = __shfl_up(upto, o, 64);
+      if (lane >= o) upto += y;
+    }
+    const int total = __builtin_amdgcn_readlane(upto, 63);
+    for (int b = (int)((turn - seen % stride + stride) % stride); b < total; b += kBatch * stride) {
+      f4 x[kBatch];
+      float w[kBatch][RT];
+#pragma unroll
+      for (int t = 0; t < kBatch; ++t) {
+        const int at = b + t * stride;
+        const int i = min(63, (int)__builtin_ctzll(__ballot(upto > at) | uint64_t(1) << 63));
+        const int row = __builtin_amdgcn_readlane(r0, i) + 4 * (at - __builtin_amdgcn_readlane(upto - blocks, i)) + g;
+        const bool in = at < total && row < __builtin_amdgcn_readlane(r1, i);
+        x[t] = load4<BF>(v, (int64_t)row * n + mine, in ? n - mine : 0);
+#pragma unroll
+        for (int k = 0; k < RT; ++k) w[t][k] = in ? tg[(int64_t)row * 2 * RT * 16 + 16 * k + c] : 0.f;
+      }
+#pragma unroll
+      for (int t = 0; t < kBatch; ++t)
+#pragma unroll
+        for (int k = 0; k < RT; ++k)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) acc[k][q] = mma32(w[t][k], x[t][q], acc[k][q]);      // rank x columns
+    }
+    seen += total;
   }
-#pragma unroll
-  for (int k = 0; k < RT; ++k)
-#pragma unroll
-    for (int q = 0; q < NC; ++q) *(f4*)&red[wave][k * NC + q][lane * 4] = acc[k][q];
-  __syncthreads();
   float* out = splits > 1 ? part + (int64_t)split * a.E * a.R * (a.K + a.M) : nullptr;
-  for (int x = threadIdx.x; x < RT * NC * 256; x += kThreads) {
-    // dD's neighbours along the columns, dU's along the rank
-    const int k = x / (NC * 256), w = x % (NC * 256);
-    const int rr = up ? w % 16 : w / (16 * NC), cc = up ? w / 16 : w % (16 * NC);
-    const int r = 16 * k + rr, col = col0 + cc, kq = k * NC + cc % NC, ln = (rr >> 2) * 16 + cc / NC;
-    if (r >= a.R || col >= n) continue;
-    float s = 0.f;
 #pragma unroll
-    for (int t = 0; t < kWaves; ++t) s += red[t][kq][ln * 4 + (rr & 3)];
-    if (up) (out ? out + (int64_t)a.E * a.R * a.K : a.dup)[((int64_t)e * a.M + col) * a.R + r] = s;
-    else (out ? out : a.ddown)[((int64_t)e * a.R + r) * a.K + col] = s;
+  for (int k = 0; k < RT; ++k) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) *(f4*)&red[wave][q][lane * 4] = acc[k][q];
+    __syncthreads();
+    for (int x = threadIdx.x; x < 1024; x += 64 * kParamWaves) {
+      // dD's neighbours along the columns, dU's along the rank
+      const int rr = up ? x % 16 : x / kCols, cc = up ? x / 16 : x % kCols;
+      const int r = 16 * k + rr, col = col0 + cc, ln = (rr >> 2) * 16 + cc / 4;
+      if (r >= a.R || col >= n) continue;
+      float s = 0.f;
+#pragma unroll
+      for (int t = 0; t < kParamWaves; ++t) s += red[t][cc % 4][ln * 4 + (rr & 3)];
+      if (up) (out ? out + (int64_t)a.E * a.R * a.K : a.dup)[((int64_t)e * a.M + col) * a.R + r] = s;
+      else (out ? out : a.ddown)[((int64_t)e * a.R + r) * a.K + col] = s;
+    }
+    __syncthreads();
   }
 }
 
@@ -462,32 +466,34 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 int rank_blocks(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8; }
 
-int64_t tiles_of(const Adapters& a) { return a.starts ? ceil_div(a.N, kRows) + a.B + 1 : a.N; }
+// Tiles of 32 rows where two of sixteen would be on every CU anyway, in bf16 (8192 x (768 -> 2048): rank 16 23.3 -> 21.9 us,
+// rank 64 47 -> 41; else two workgroups' phases overlap better than one's: fp32 1024 -> 1024 of rank 24 39 us against 42,
+// the rows' backward of rank 16 30 us against 34).
+bool wide(const Adapters& a, bool backward) { return a.bf16 && a.N >= 8192 && a.starts && a.R <= 64 && (a.R > 16 || !backward); }
+int64_t tiles_of(const Adapters& a, int RB) { return a.starts ? ceil_div(a.N, 16 * RB) + a.B + 1 : a.N; }
 
-int cols_of(const Adapters& a) { return 16 * (a.bf16 && a.R <= 32 ? 8 : 4); }      // lane_cols() of sixteen lanes
-
-// Workgroups that share an adapter's rows, so that every CU has two.
+// Workgroups that share an adapter's rows, so that every CU has one.
 int splits_of(const Adapters& a) {
-  const int64_t groups = (ceil_div(a.K, cols_of(a)) + ceil_div(a.M, cols_of(a))) * a.E;
-  return (int)std::max<int64_t>(1, std::min({ceil_div(512, groups), ceil_div(a.N, 256), int64_t(16)}));
+  const int64_t groups = (ceil_div(a.K, kCols) + ceil_div(a.M, kCols)) * a.E;
+  return (int)std::max<int64_t>(1, std::min({256 / groups, ceil_div(a.N, 256), int64_t(16)}));
 }
 
-template <bool BF, int RT>
+template <bool BF, int RT, int RB>
 hipError_t fwd(const Adapters& a, hipStream_t s) {
-  const int64_t tiles = tiles_of(a);
+  const int64_t tiles = tiles_of(a, RB);
   // few tiles: several workgroups share a tile's columns, each with the inner product to itself
   const int gy = (int)std::max<int64_t>(1, std::min(256 / tiles, ceil_div(a.M, kWaves * 16)));
-  hipLaunchKernelGGL((adapters_fwd_kernel<BF, RT>), dim3((unsigned)tiles, (unsigned)gy), dim3(kThreads), 0, s, a);
+  hipLaunchKernelGGL((adapters_fwd_kernel<BF, RT, RB>), dim3((unsigned)tiles, (unsigned)gy), dim3(RB * kThreads), 0, s, a);
   return hipGetLastError();
 }
 
-template <bool BF, int RT>
+template <bool BF, int RT, int RB>
 hipError_t bwd(const Adapters& a, hipStream_t s) {
-  if (a.N) hipLaunchKernelGGL((adapters_rows_kernel<BF, RT>), dim3((unsigned)tiles_of(a)), dim3(kThreads), 0, s, a);
-  const int splits = splits_of(a), kb = (int)ceil_div(a.K, cols_of(a)), mb = (int)ceil_div(a.M, cols_of(a));
+  if (a.N) hipLaunchKernelGGL((adapters_rows_kernel<BF, RT, RB>), dim3((unsigned)tiles_of(a, RB)), dim3(RB * kThreads), 0, s, a);
+  const int splits = splits_of(a), kb = (int)ceil_div(a.K, kCols), mb = (int)ceil_div(a.M, kCols);
   float* part = (float*)((char*)a.ws + up256(sizeof(float) * (size_t)a.N * 2 * RT * 16));
-  hipLaunchKernelGGL((adapters_params_kernel<BF, RT>), dim3((unsigned)(kb + mb), (unsigned)a.E, (unsigned)splits), dim3(kThreads), 0, s, a, kb,
-                     splits, part);
+  hipLaunchKernelGGL((adapters_params_kernel<BF, RT>), dim3((unsigned)(kb + mb), (unsigned)a.E, (unsigned)splits), dim3(64 * kParamWaves), 0, s, a,
+                     kb, splits, part);
   if (splits > 1) {
     const int64_t n = (int64_t)a.E * a.R * (a.K + a.M);
     hipLaunchKernelGGL(adapters_join_kernel, dim3((unsigned)std::min<int64_t>(2048, ceil_div(n, kThreads))), dim3(kThreads), 0, s, a, splits, part);
@@ -497,8 +503,11 @@ hipError_t bwd(const Adapters& a, hipStream_t s) {
 
 template <int RT>
 hipError_t pick(const Adapters& a, bool backward, hipStream_t s) {
-  if (backward) return a.bf16 ? bwd<true, RT>(a, s) : bwd<false, RT>(a, s);
-  return a.bf16 ? fwd<true, RT>(a, s) : fwd<false, RT>(a, s);
+  if (!a.bf16) return backward ? bwd<false, RT, 1>(a, s) : fwd<false, RT, 1>(a, s);
+  if constexpr (RT <= 4) {      // (more would take the registers and LDS of too many)
+    if (wide(a, backward)) return backward ? bwd<true, RT, 2>(a, s) : fwd<true, RT, 2>(a, s);
+  }
+  return backward ? bwd<true, RT, 1>(a, s) : fwd<true, RT, 1>(a, s);
 }
 
 }  // namespace
