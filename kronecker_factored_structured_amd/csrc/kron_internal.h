@@ -357,7 +357,7 @@ struct VocabCE {
   void* dh;                   // NULL: not computed
   void* dW;                   // NULL: not computed
   // set by launch_vocab_ce: K rounded up, the operands, and the workspace
-  int32_t Kp;
+  int32_t Kp, Kh, Kw;         // (bf16: widths of hp's and wp's rows)
   VocabScales* sc;            // NULL: every row in use, nothing scaled
   int* idx;                   // rows in use (NULL: all)
   int* pos;                   // a row's place among them

@@ -20,6 +20,7 @@ struct Operand {
   const uint16_t* p;
   int64_t ld;
   int rows, cols;        // what may be read: cols is a multiple of 8 (two planes: of 32)
+  const int* idx = nullptr;      // ROW: where the rows are, if not in order (all within 4 GB)
 };
 
 // fp32 values as two parts of fp16: v 2^s = hi + lo, both rounded to nearest, s so that the largest |v| 2^s is below 2^15.
@@ -72,7 +73,7 @@ template <Side SD, int R, int NW, int NP>
 struct TileLoad {
   static constexpr int kLoads = R * 128 / 1024 / NW;      // 1 KB wave loads of each wavefront
   static constexpr int kBlock = 64 / NP;                  // columns, and rows, of a COL block
-  static_assert(kLoads * NW * 1024 == R * 128 && R % 64 == 0, "");
+  static_assert(kLoads * NW * 1024 == R * 128 && (SD == ROW || R % 64 == 0), "");
   const uint16_t* base;
   uint32_t off[kLoads];
   int64_t ld;
@@ -81,13 +82,14 @@ struct TileLoad {
   static __device__ int turn(int row) { return ((row >> 1) & 1) | (((row >> 3) & 1) << 1); }
   __device__ void init(const Operand& o, int at, int wave_, int lane) {
     wave = wave_, ld = o.ld, rows = o.rows;
-    base = SD == ROW ? o.p + (int64_t)at * o.ld : o.p;
+    base = SD == ROW && !o.idx ? o.p + (int64_t)at * o.ld : o.p;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int q = wave * kLoads + i;
       if constexpr (SD == ROW) {
         const int row = q * 8 + lane / 8, chunk = (lane & 7) ^ (row & 7);
-        off[i] = (uint32_t)min(row, rows - 1 - at) * (uint32_t)(ld * 2) + chunk * 16;
+        const int r = min(row, rows - 1 - at);
+        off[i] = (uint32_t)(o.idx ? o.idx[at + r] : r) * (uint32_t)(ld * 2) + chunk * 16;
       } else {
         const int row = (q % (kBlock / 8)) * 8 + lane / 8, slot = lane & 7, blk = q / (kBlock / 8);
         const int chunk = (((slot >> 1) ^ turn(row)) << 1) | (slot & 1);
@@ -109,6 +111,22 @@ struct TileLoad {
                                      (__attribute__((address_space(3))) void*)(lds + (wave * kLoads + i) * 1024), 16, 0, 0);
   }
 };
+
+// Up to 16 bytes of a row, of which `left` values are there; zeros behind them.
+template <bool F32>
+__device__ inline u4 row_end(const char* p, int left) {
+  constexpr int PER = F32 ? 4 : 8;
+  typedef u4 any __attribute__((aligned(2)));
+  if (left >= PER) return *(const any*)p;
+  u4 o = {0, 0, 0, 0};
+#pragma unroll
+  for (int e = 0; e < PER; ++e)
+    if (e < left) {
+      if constexpr (F32) o[e] = ((const uint32_t*)p)[e];
+      else o[e / 2] |= (uint32_t)((const uint16_t*)p)[e] << (16 * (e & 1));
+    }
+  return o;
+}
 
 // Operand block i (16 rows) of half kk of a step (32 of its 64 products; two planes: part kk) out of a tile in LDS; `at`:
 // the wavefront's first row.
@@ -139,13 +157,17 @@ __device__ inline u4 fragment(const lds_t* lds, int at, int i, int kk, int lane)
 // they hold the wavefronts up: dW of 768 x 21760 over 8192 rows 303 -> 280 us) and have NS - 1 steps' time.  With two
 // planes a step is 32 products in three parts, lo hi, hi hi and hi lo: each part's fragments serve two of them.
 //
+// F32: two "planes" that are fp32 values as they are (ROW, whole rows of 128 bytes), on the fp32 instruction.  The four
+// products of a lane's 16 bytes are of every fourth k, of both operands alike.
+//
 // 256 x 256 tiles of eight wavefronts: 8192 x 8256 x 8192 bf16 runs at 1,370 TFLOP/s.  Registers alone would do 1,660 with
 // this instruction and such values (the clock falls to 2.0 GHz with the power they take; 2,090 with zeros), loads alone
 // 1,700, reads of LDS alone 4,850.  Measured beside it: 32 x 32 blocks (1,810 out of registers) 1,080-1,150; four
 // wavefronts of 128 x 128 each 1,000; steps of 32 with three to five in LDS 960-1,040; raised wave priority 1,265; reads,
 // loads and products interleaved by hand 1,350.
-template <int WM_, int WN_, int TM_, int TN_, Side SA_, Side SB_, bool BF_, int NP_, int NS_ = 2>
+template <int WM_, int WN_, int TM_, int TN_, Side SA_, Side SB_, bool BF_, int NP_, int NS_ = 2, bool F32_ = false>
 struct Product {
+  static constexpr bool F32 = F32_;
   static constexpr int WM = WM_, WN = WN_, TM = TM_, TN = TN_, NP = NP_, NS = NS_;
   static constexpr int BM = WM * TM * 16, BN = WN * TN * 16, NW = WM * WN, kThreads = 64 * NW;
   static constexpr int kStage = (BM + BN) * 128, kStep = kBK / NP;
@@ -166,14 +188,25 @@ struct Product {
 #pragma unroll
     for (int j = 0; j < TN; ++j) b.f[j] = fragment<SB_, NP>(st + BM * 128, wn * TN * 16, j, kk, lane);
   }
+  __device__ void multiply_row(int i, const FragsA& a, const FragsB& b) {
+    if constexpr (F32) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a.f[i][e]), __uint_as_float(b.f[j][e]), acc[i][j], 0, 0, 0);
+    } else {
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[i][j] = mma<BF_>(a.f[i], b.f[j], acc[i][j]);
+    }
+  }
   // between(i): what is issued beside block row i's products.
   template <class F>
   __device__ void multiply(const FragsA& a, const FragsB& b, const F& between) {
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
       between(i);
-#pragma unroll
-      for (int j = 0; j < TN; ++j) acc[i][j] = mma<BF_>(a.f[i], b.f[j], acc[i][j]);
+      multiply_row(i, a, b);
     }
   }
   // What this wavefront reads is there, and what it loads but for the last STAGES tiles; and so it is for all of them.
@@ -234,9 +267,9 @@ struct Product {
         all(st);
         st = st + 1 == NS ? 0 : st + 1;
         fetch(1 - set, st);      // (behind the last step: of no use, and not used)
-        if constexpr (NP == 2) multiply(a[set][1], b[set][0], none);
+        if constexpr (NP == 2 && !F32) multiply(a[set][1], b[set][0], none);
         else multiply(a[set][1], b[set][1], none);
-        if constexpr (NP == 2) multiply(a[set][0], b[set][1], none);
+        if constexpr (NP == 2 && !F32) multiply(a[set][0], b[set][1], none);
         multiply(a[set][0], b[set][0], none);
       };
       std::integral_constant<int, 0> even;
@@ -254,6 +287,7 @@ struct Product {
       __syncthreads();
       return;
     }
+    static_assert(!F32 || kWhole, "");
     FragsA a0, a1;
     FragsB b0, b1;
     constexpr int first = NP == 2 ? 1 : 0;      // of A's parts
@@ -290,6 +324,31 @@ struct Product {
     for (; t < total - NS; ++t) step(std::true_type{});
     for (; t < total; ++t) step(std::false_type{});
     __syncthreads();
+  }
+
+  // What is left of rows (ROW, as they are) behind the last whole step, from `at` to K; row_a(m), row_b(n): where they begin.
+  template <class RA, class RB>
+  __device__ void run_end(const RA& row_a, const RB& row_b, int at, int K) {
+    static_assert(NP == 1 || F32, "");
+    constexpr int SZ = F32 ? 4 : 2, PER = 16 / SZ;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, c = lane & 15;
+    const char *pa[TM], *pb[TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i) pa[i] = row_a((wave % WM) * TM * 16 + 16 * i + c);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) pb[j] = row_b((wave / WM) * TN * 16 + 16 * j + c);
+#pragma unroll 1
+    for (int k = at + g * PER; k - g * PER < K; k += 4 * PER) {
+      FragsA a;
+      FragsB b;
+#pragma unroll
+      for (int j = 0; j < TN; ++j) b.f[j] = row_end<F32>(pb[j] + k * SZ, K - k);
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        a.f[i] = row_end<F32>(pa[i] + k * SZ, K - k);
+        multiply_row(i, a, b);
+      }
+    }
   }
 };
 

@@ -165,11 +165,25 @@ __global__ __launch_bounds__(256) void vocab_pack_kernel(VocabCE a, int which) {
   }
 }
 
-template <int NP>
-__device__ inline Operand h_operand(const VocabCE& a, int count) { return {a.hp, (int64_t)a.Kp * NP, count, a.Kp}; }
-template <int NP>
-__device__ inline Operand w_operand(const VocabCE& a, int v0 = 0) {
-  return {a.wp + (int64_t)v0 * a.Kp * NP, (int64_t)a.Kp * NP, a.V - v0, a.Kp};
+// The logits of a tile: tokens from v0 (m) x rows from n0 (n).  bf16 rows, and an fp32 tile's of few rows, are taken as they
+// are, whatever their width.
+template <class P, bool BF>
+__device__ inline void vocab_logits(P& p, const VocabCE& a, int count, int v0, int n0, lds_t* lds) {
+  if constexpr (BF || P::F32) {
+    const Operand w = P::F32 ? Operand{(const uint16_t*)a.W, (int64_t)a.K * 2, a.V, a.K} : Operand{a.wp, a.Kw, a.V, a.Kw};
+    const Operand h = P::F32 ? Operand{(const uint16_t*)a.h, (int64_t)a.K * 2, count, a.K, a.idx} : Operand{a.hp, a.Kh, count, a.Kh};
+    const int whole = a.K / P::kStep * P::kStep;
+    p.run(w, h, v0, n0, 0, whole, lds);
+    if (whole < a.K)
+      p.run_end([&](int m) { return (const char*)w.p + (int64_t)min(v0 + m, a.V - 1) * w.ld * 2; },
+                [&](int n) {
+                  const int r = min(n0 + n, count - 1);
+                  return (const char*)h.p + (int64_t)(h.idx ? h.idx[r] : r) * h.ld * 2;
+                },
+                whole, a.K);
+  } else {
+    p.run(Operand{a.wp, (int64_t)a.Kp * 2, a.V, a.Kp}, Operand{a.hp, (int64_t)a.Kp * 2, count, a.Kp}, v0, n0, 0, a.Kp, lds);
+  }
 }
 
 // ------------------------------------------------------------------------------ forward
@@ -182,10 +196,11 @@ __global__ __launch_bounds__(P::kThreads) void vocab_fwd_kernel(VocabCE a, int t
   const int count = vocab_count(a), m0 = mt * P::BM, n0 = nt * P::BN;
   if (n0 >= count) return;
   P p;
-  p.run(w_operand<P::NP>(a), h_operand<P::NP>(a, count), m0, n0, 0, a.Kp, (lds_t*)smem);
+  constexpr bool scaled = !BF && !P::F32;
+  vocab_logits<P, BF>(p, a, count, m0, n0, (lds_t*)smem);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
   const int wm = wave % P::WM, wn = wave / P::WM, first = m0 + wm * P::TM * 16 + 4 * g;
-  const float down = BF ? 1.f : scale_down(a.sc->top_h), down2 = BF ? 1.f : scale_down(a.sc->top_w);
+  const float down = scaled ? scale_down(a.sc->top_h) : 1.f, down2 = scaled ? scale_down(a.sc->top_w) : 1.f;
   float2* red = (float2*)smem;      // (the product ended with a barrier)
 #pragma unroll
   for (int j = 0; j < P::TN; ++j) {
@@ -204,16 +219,16 @@ __global__ __launch_bounds__(P::kThreads) void vocab_fwd_kernel(VocabCE a, int t
     // (fmaxf passes over NaN: the sum has it)
 #pragma unroll
     for (int i = 0; i < P::TM; ++i) {
-      if constexpr (!BF) p.acc[i][j] *= down;
+      if constexpr (scaled) p.acc[i][j] *= down;
       top = fmaxf(fmaxf(top, fmaxf(p.acc[i][j][0], p.acc[i][j][1])), fmaxf(p.acc[i][j][2], p.acc[i][j][3]));
     }
-    const float f = BF ? kLog2e : down2 * kLog2e;
+    const float f = scaled ? down2 * kLog2e : kLog2e;
     if (__any(mine)) {
 #pragma unroll
       for (int i = 0; i < P::TM; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (mine && off == 16 * i + e) a.zlab[n] = BF ? p.acc[i][j][e] : p.acc[i][j][e] * down2;
+          if (mine && off == 16 * i + e) a.zlab[n] = scaled ? p.acc[i][j][e] * down2 : p.acc[i][j][e];
     }
     float2 s = {top * f, 0.f};
     const float ref = top == -INFINITY ? 0.f : s.x;
@@ -300,13 +315,14 @@ __global__ __launch_bounds__(P::kThreads) void vocab_dz_kernel(VocabCE a, int v0
   int mt, nt;
   tile_of(blockIdx.x, gridDim.x, tm, tn, mt, nt);
   const int count = vocab_count(a), m0 = mt * P::BM, n0 = nt * P::BN;
-  if (n0 >= count) return;
+  if (n0 >= count || v0 + m0 >= a.V) return;      // (what is read behind V of dz lies in the tile of V - 1)
   P p;
-  p.run(w_operand<P::NP>(a), h_operand<P::NP>(a, count), v0 + m0, n0, 0, a.Kp, (lds_t*)smem);
+  constexpr bool scaled = !BF && !P::F32;
+  vocab_logits<P, BF>(p, a, count, v0 + m0, n0, (lds_t*)smem);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
   const int wm = wave % P::WM, wn = wave / P::WM, first = v0 + m0 + wm * P::TM * 16 + 4 * g;
-  const float down = BF ? 1.f : scale_down(a.sc->top_h), down2 = BF ? 1.f : scale_down(a.sc->top_w);
-  const float f = BF ? kLog2e : down2 * kLog2e;
+  const float down = scaled ? scale_down(a.sc->top_h) : 1.f, down2 = scaled ? scale_down(a.sc->top_w) : 1.f;
+  const float f = scaled ? down2 * kLog2e : kLog2e;
   const int padded = (count + kBK - 1) / kBK * kBK;      // rows that the contraction over them reads
   const bool edge = v0 + m0 + P::BM > a.V || n0 + P::BN > count;
 #pragma unroll
@@ -323,7 +339,7 @@ __global__ __launch_bounds__(P::kThreads) void vocab_dz_kernel(VocabCE a, int v0
 #pragma unroll
     for (int i = 0; i < P::TM; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) p.acc[i][j][e] = expo2(fmaf(BF ? p.acc[i][j][e] : p.acc[i][j][e] * down, f, -top)) * inv;
+      for (int e = 0; e < 4; ++e) p.acc[i][j][e] = expo2(fmaf(scaled ? p.acc[i][j][e] * down : p.acc[i][j][e], f, -top)) * inv;
     const int64_t off = lab - first;
     const bool mine = off >= 0 && off < P::TM * 16 && (off & 15) < 4;
     if (__any(mine)) {
@@ -365,7 +381,8 @@ __global__ __launch_bounds__(P::kThreads) void vocab_dh_kernel(VocabCE a, int v0
   const int k0 = blockIdx.y * len, k1 = min(vc, k0 + len);
   const Operand dz = {a.dz, (int64_t)vc * P::NP, count, vc};
   P p;
-  p.run(w_operand<P::NP>(a, v0), dz, m0, n0, k0, k1, (lds_t*)smem);
+  const int64_t ld = P::NP == 2 ? a.Kp * 2 : a.Kw;
+  p.run(Operand{a.wp + v0 * ld, ld, a.V - v0, P::NP == 2 ? a.Kp : a.Kw}, dz, m0, n0, k0, k1, (lds_t*)smem);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
   float* out = a.dhpart + (int64_t)blockIdx.y * a.N * a.Kp;
 #pragma unroll
@@ -378,6 +395,102 @@ __global__ __launch_bounds__(P::kThreads) void vocab_dh_kernel(VocabCE a, int v0
       if (m >= a.Kp) continue;
       f4* q = (f4*)(out + (int64_t)n * a.Kp + m);
       *q = add ? *q + p.acc[i][j] : p.acc[i][j];
+    }
+  }
+}
+
+// dh's parts of few rows, of fp32's W as it is: 256 of K (four wavefronts' 64) x TN x 16 rows, the contraction over the
+// tokens on the fp32 instruction.  A lane holds four neighbouring k of a token: they are rows of four products, so that row m
+// of product i is k = 4 m + i.  Three steps of sixteen tokens are on their way to each wavefront's registers.
+template <int TN>
+__global__ __launch_bounds__(256, 2) void vocab_dh_few_kernel(VocabCE a, int v0, int vc, int tn, int len, int add) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4, c = lane & 15;
+  const int count = vocab_count(a), n0 = (blockIdx.x % tn) * TN * 16, k0 = (blockIdx.x / tn * 4 + wave) * 64;
+  if (n0 >= count || k0 >= a.K) return;
+  typedef f4 any __attribute__((aligned(4)));
+  const int b0 = blockIdx.y * len, b1 = min(min(vc, b0 + len), a.V - v0);
+  const float* W = (const float*)a.W + (int64_t)(v0 + b0) * a.K + k0;
+  const uint16_t* dz[TN];
+#pragma unroll
+  for (int j = 0; j < TN; ++j) dz[j] = a.dz + (int64_t)min(n0 + 16 * j + c, count - 1) * vc * 2;
+  f4 acc[4][TN];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = f4{0, 0, 0, 0};
+  struct Step {
+    f4 w[4];
+    h4 d[TN][2];
+  };
+  const uint32_t mine = (uint32_t)(4 * g * a.K + 4 * c);
+  auto load_dz = [&](Step& s, int b) __attribute__((always_inline)) {      // (zero from V to the end of its piece)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      const uint16_t* p = dz[j] + ((b + 4 * g) / 32) * 64 + (b + 4 * g) % 32;
+      s.d[j][0] = *(const h4*)p, s.d[j][1] = *(const h4*)(p + 32);
+    }
+  };
+  auto load = [&](Step& s, int b) __attribute__((always_inline)) {      // tokens b .. b + 15 of the piece, all there
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s.w[e] = *(const any*)(W + (int64_t)(b - b0) * a.K + (mine + e * a.K));
+    load_dz(s, b);
+    __builtin_amdgcn_sched_barrier(0);      // (the compiler would move them behind the products)
+  };
+  auto multiply = [&](const Step& s) __attribute__((always_inline)) {
+    f4 d[TN];
+#pragma unroll
+    for (int j = 0; j < TN; ++j) d[j] = __builtin_convertvector(s.d[j][0], f4) + __builtin_convertvector(s.d[j][1], f4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(s.w[e][i], d[j][e], acc[i][j], 0, 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  int b = b0;
+  if (k0 + 64 <= a.K) {
+    const int steps = (b1 - b0) / 16;
+    Step s[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (i < steps) load(s[i], b0 + 16 * i);
+    int t = 0;
+    for (; t + 6 <= steps; t += 3)
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        multiply(s[i]);
+        load(s[i], b0 + 16 * (t + 3 + i));
+      }
+#pragma unroll
+    for (int i = 0; i < 5; ++i)
+      if (t + i < steps) {
+        multiply(s[i % 3]);
+        if (t + 3 + i < steps) load(s[i % 3], b0 + 16 * (t + 3 + i));
+      }
+    b += 16 * steps;
+  }
+  const int left = a.K - k0 - 4 * c;
+  for (; b < b1; b += 16) {      // the last tokens, or the last of K
+    Step s;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int v = b + 4 * g + e;
+      s.w[e] = __builtin_bit_cast(f4, row_end<true>((const char*)(W + (int64_t)(v - b0) * a.K + 4 * c), v < b1 ? left : 0));
+    }
+    load_dz(s, b);
+    multiply(s);
+  }
+  float* out = a.dhpart + (int64_t)blockIdx.y * a.N * a.Kp;
+#pragma unroll
+  for (int j = 0; j < TN; ++j) {
+    const int n = n0 + 16 * j + c;
+    if (n >= count) continue;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      f4* q = (f4*)(out + (int64_t)n * a.Kp + k0 + 16 * g + 4 * r);
+      const f4 s = {acc[0][j][r], acc[1][j][r], acc[2][j][r], acc[3][j][r]};
+      *q = add ? *q + s : s;
     }
   }
 }
@@ -417,6 +530,7 @@ __global__ __launch_bounds__(256) void vocab_dh_join_kernel(VocabCE a, int split
     const int64_t at = a.idx ? a.pos[row] : row;
     f4 s = {0, 0, 0, 0};
     if (at >= 0)
+#pragma unroll 8
       for (int t = 0; t < splits; ++t) s += *(const f4*)(a.dhpart + ((int64_t)t * a.N + at) * a.Kp + k);
     put_grad<BF>(a.dh, row, k, a.K, s, at >= 0 ? f2 : 0.f, at >= 0 ? f : 0.f);
   }
@@ -442,8 +556,8 @@ __global__ __launch_bounds__(P::kThreads) void vocab_dw_kernel(VocabCE a, int v0
   const int padded = (count + kBK - 1) / kBK * kBK;
   const int len = (padded / kBK + gridDim.y - 1) / gridDim.y * kBK, k0 = blockIdx.y * len;
   const Operand dz = {a.dz, (int64_t)vc * P::NP, padded, vc};
-  Operand h = h_operand<P::NP>(a, count);
-  if (P::NP == 2 && a.weights) h.p = a.hw;
+  const int wide = P::NP == 2 ? a.Kp : a.Kh;
+  const Operand h = {P::NP == 2 && a.weights ? a.hw : a.hp, (int64_t)wide * P::NP, count, wide};
   P p;
   p.run(h, dz, m0, n0, k0, min(count, k0 + len), (lds_t*)smem);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
@@ -494,6 +608,11 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 // Rows and width of a product with few rows: a tile of 64.
 bool few(int64_t N) { return N <= 64; }
 
+// Whether fp32's products with W take it as it is, on the fp32 instruction.
+bool direct_of(int64_t N, bool bf) { return !bf && N > 0 && N <= 128; }
+template <int WN, int TN, int NS>
+using Whole = Product<4, WN, 2, TN, ROW, ROW, false, 2, NS, true>;      // 128 x WN TN 16
+
 // Workgroups (one a CU) run in rounds of 256, so that a product of a few more tiles than that takes two.  The parts of the
 // contraction that cost least, with what was measured: a step of a 256 x 256 tile 2.2 us, its start and end 4 us, the
 // tile's sums through memory at 4.5 TB/s (`moves` times for each part).
@@ -514,9 +633,10 @@ Parts best_parts(int64_t tiles, int64_t steps, double share, double moves, int m
 struct VocabPlan {
   int Kp;
   bool rows, copy_h, copy_w;      // rows in use are listed; operands that are copies
-  int tiles;                      // of the vocabulary, 256 wide
+  int tiles;                      // of the vocabulary, 256 wide (the direct forward's: 128)
   int piece, pieces, splits;      // backward
   bool three;                     // dh in tiles of 192
+  bool direct;                    // W as it is
   size_t sc, idx, pos, hp, hw, wp, part, zlab, dz, dhpart, dwpart, bytes;
 };
 
@@ -530,9 +650,11 @@ VocabPlan plan_of(int64_t N, int K, int V, bool bf, bool weights, bool backward)
   VocabPlan p{};
   p.Kp = (int)ceil_div(K, kBK) * kBK;
   p.rows = weights;
-  p.copy_h = !bf || weights || K != p.Kp;
-  p.copy_w = !bf || K != p.Kp;
-  p.tiles = (int)ceil_div(V, 256);
+  p.direct = direct_of(N, bf);
+  // (the products over rows of W or h take whole 16-byte pieces)
+  p.copy_h = bf ? weights || (backward && K % 8) : backward || !p.direct;
+  p.copy_w = bf ? backward && K % 8 : !p.direct;
+  p.tiles = (int)ceil_div(V, p.direct && !backward ? 128 : 256);
   size_t at = 0;
   auto take = [&](size_t bytes) { const size_t r = at; at += up256(bytes); return r; };
   const int planes = bf ? 1 : 2;
@@ -555,7 +677,7 @@ VocabPlan plan_of(int64_t N, int K, int V, bool bf, bool weights, bool backward)
     p.pieces = (int)ceil_div(p.tiles, piece);
     p.dz = take(2 * (size_t)planes * rows * p.piece);
     const int64_t steps = p.piece / kBK * triple, moves = p.pieces > 1 ? 4 : 2;
-    if (few(N)) {
+    if (few(N) || p.direct) {
       p.splits = (int)std::min<int64_t>(std::max<int64_t>(1, 512 / tk), std::max(1, p.piece / 512));
     } else {
       const int64_t tn = ceil_div(N, 256);
@@ -578,7 +700,9 @@ VocabPlan plan_of(int64_t N, int K, int V, bool bf, bool weights, bool backward)
 VocabCE bind(const VocabCE& k, const VocabPlan& p, char* ws, bool bf) {
   VocabCE a = k;
   a.Kp = p.Kp;
-  a.sc = p.rows || !bf ? (VocabScales*)(ws + p.sc) : nullptr;
+  a.Kh = p.copy_h ? p.Kp : k.K;
+  a.Kw = p.copy_w ? p.Kp : k.K;
+  a.sc = p.rows || (p.copy_h && !bf) ? (VocabScales*)(ws + p.sc) : nullptr;
   a.idx = p.rows ? (int*)(ws + p.idx) : nullptr;
   a.pos = (int*)(ws + p.pos);
   a.hp = p.copy_h ? (uint16_t*)(ws + p.hp) : (uint16_t*)k.h;
@@ -602,8 +726,8 @@ hipError_t go(dim3 grid, hipStream_t s, A... args) {
 
 template <bool BF>
 hipError_t prepare(const VocabCE& a, const VocabPlan& p, hipStream_t s) {
-  if (p.rows || !BF) hipLaunchKernelGGL(vocab_rows_kernel, dim3(1), dim3(1024), 0, s, a);
-  if (!BF) hipLaunchKernelGGL(vocab_top_kernel, dim3(512, 2), dim3(256), 0, s, a);
+  if (a.sc) hipLaunchKernelGGL(vocab_rows_kernel, dim3(1), dim3(1024), 0, s, a);
+  if (!BF && p.copy_h) hipLaunchKernelGGL(vocab_top_kernel, dim3(p.copy_w ? 512 : 64, p.copy_w ? 2 : 1), dim3(256), 0, s, a);
   const int per = p.Kp / 8;
   auto blocks = [&](int64_t rows) { return dim3((unsigned)std::min<int64_t>(4096, std::max<int64_t>(1, ceil_div(rows * per, 256)))); };
   if (p.copy_h && a.N) hipLaunchKernelGGL((vocab_pack_kernel<BF>), blocks(a.N), dim3(256), 0, s, a, 0);
@@ -617,11 +741,21 @@ hipError_t run_fwd(const VocabCE& a, const VocabPlan& p, hipStream_t s) {
   hipError_t e = prepare<BF>(a, p, s);
   if (e != hipSuccess) return e;
   if (a.N) {
-    const int tn = (int)ceil_div(a.N, few(a.N) ? 64 : 256);
+    const int tn = p.direct ? 1 : (int)ceil_div(a.N, few(a.N) ? 64 : 256);
     typedef Few<BF, ROW, ROW> PF;
     typedef Big<BF, ROW, ROW> PB;
     const dim3 grid((unsigned)(p.tiles * tn));
-    e = few(a.N) ? go<PF, vocab_fwd_kernel<PF, BF>>(grid, s, a, p.tiles, tn) : go<PB, vocab_fwd_kernel<PB, BF>>(grid, s, a, p.tiles, tn);
+    if constexpr (!BF)
+      if (p.direct) {
+        typedef Whole<1, 2, 4> P1;
+        typedef Whole<1, 4, 3> P2;
+        typedef Whole<1, 8, 2> P4;
+        e = a.N <= 32 ? go<P1, vocab_fwd_kernel<P1, BF>>(grid, s, a, p.tiles, 1)
+            : a.N <= 64 ? go<P2, vocab_fwd_kernel<P2, BF>>(grid, s, a, p.tiles, 1)
+                        : go<P4, vocab_fwd_kernel<P4, BF>>(grid, s, a, p.tiles, 1);
+      }
+    if (!p.direct)
+      e = few(a.N) ? go<PF, vocab_fwd_kernel<PF, BF>>(grid, s, a, p.tiles, tn) : go<PB, vocab_fwd_kernel<PB, BF>>(grid, s, a, p.tiles, tn);
     if (e != hipSuccess) return e;
     const bool one = a.N <= 128;      // a workgroup's few turns are shorter than another launch
     hipLaunchKernelGGL(vocab_join_kernel, dim3(one ? 1u : (unsigned)ceil_div(a.N, 32)), dim3(1024), 0, s, a, p.tiles);
@@ -636,14 +770,23 @@ hipError_t run_bwd(const VocabCE& a, const VocabPlan& p, hipStream_t s) {
   hipError_t e = prepare<BF>(a, p, s);
   if (e != hipSuccess) return e;
   const bool fw = few(a.N);
-  const int tn = (int)ceil_div(a.N, fw ? 64 : 256), tk = (int)ceil_div(p.Kp, 256);
+  const int tn = p.direct ? 1 : (int)ceil_div(a.N, fw ? 64 : 256), tk = (int)ceil_div(p.Kp, 256);
   for (int i = 0; i < p.pieces; ++i) {
     const int v0 = i * p.piece, vc = std::min(p.piece, (int)ceil_div(a.V - v0, 256) * 256), tm = vc / 256;
     if (a.N) {
       typedef Few<BF, ROW, ROW> PF;
       typedef Big<BF, ROW, ROW> PB;
       const dim3 grid((unsigned)(tm * tn));
-      e = fw ? go<PF, vocab_dz_kernel<PF, BF>>(grid, s, a, v0, vc, tm, tn) : go<PB, vocab_dz_kernel<PB, BF>>(grid, s, a, v0, vc, tm, tn);
+      if constexpr (!BF)
+        if (p.direct) {
+          typedef Whole<1, 2, 4> P1;
+          typedef Whole<1, 4, 3> P2;
+          typedef Whole<1, 8, 2> P4;
+          const dim3 all((unsigned)(2 * tm));
+          e = a.N <= 32 ? go<P1, vocab_dz_kernel<P1, BF>>(all, s, a, v0, vc, 2 * tm, 1) : a.N <= 64 ? go<P2, vocab_dz_kernel<P2, BF>>(all, s, a, v0, vc, 2 * tm, 1) : go<P4, vocab_dz_kernel<P4, BF>>(all, s, a, v0, vc, 2 * tm, 1);
+        }
+      if (!p.direct)
+        e = fw ? go<PF, vocab_dz_kernel<PF, BF>>(grid, s, a, v0, vc, tm, tn) : go<PB, vocab_dz_kernel<PB, BF>>(grid, s, a, v0, vc, tm, tn);
       if (e != hipSuccess) return e;
     }
     if (a.dh && a.N) {
@@ -653,7 +796,14 @@ hipError_t run_bwd(const VocabCE& a, const VocabPlan& p, hipStream_t s) {
       typedef Three<BF, COL, ROW> PT;
       const int th = p.three ? (int)ceil_div(p.Kp, 192) : tk;
       const dim3 grid((unsigned)(th * tn), (unsigned)p.splits);
-      e = p.three ? go<PT, vocab_dh_kernel<PT, BF>>(grid, s, a, v0, vc, th, tn, len, (int)(i > 0))
+      if (p.direct) {
+        const int tn = a.N <= 64 ? 1 : 2;
+        const dim3 all((unsigned)(tk * tn), (unsigned)p.splits);
+        if (a.N <= 32) hipLaunchKernelGGL((vocab_dh_few_kernel<2>), all, dim3(256), 0, s, a, v0, vc, tn, len, (int)(i > 0));
+        else hipLaunchKernelGGL((vocab_dh_few_kernel<4>), all, dim3(256), 0, s, a, v0, vc, tn, len, (int)(i > 0));
+        e = hipGetLastError();
+      } else
+        e = p.three ? go<PT, vocab_dh_kernel<PT, BF>>(grid, s, a, v0, vc, th, tn, len, (int)(i > 0))
           : fw ? go<PF, vocab_dh_kernel<PF, BF>>(grid, s, a, v0, vc, tk, tn, len, (int)(i > 0))
              : go<PB, vocab_dh_kernel<PB, BF>>(grid, s, a, v0, vc, tk, tn, len, (int)(i > 0));
       if (e != hipSuccess) return e;

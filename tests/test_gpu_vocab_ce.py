@@ -242,3 +242,36 @@ def test_binding_refuses():
             bad()
     with pytest.raises(ValueError):
         k.kron_vocab_ce_bwd(h, W, lab, torch.zeros(10, 3, device="cuda"), torch.ones(1, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("N,Kf,V", [(1, 7, 31), (1, 70, 4000), (15, 33, 129), (16, 130, 127), (17, 333, 700), (33, 36, 2000), (50, 257, 1100),
+                                    (64, 1001, 300), (65, 68, 900), (100, 190, 515), (128, 65, 3001)])
+def test_few_rows(N, Kf, V, dtype):
+    compare(*case(N + Kf, N, Kf, V, dtype))
+    h, W, lab, w = case(N + V, N, Kf, V, dtype, 0.4)
+    h[w == 0] = float("nan")
+    compare(h, W, lab, w, dead=True)
+
+
+def test_few_rows_of_any_address_are_refused():
+    """Operands that start one value into their storage: addresses are multiples of 16 bytes, rows of any width."""
+    k = K()
+    h, W, lab, _ = case(9, 9, 77, 400, torch.float32)
+    moved = torch.zeros(h.numel() + 1, device="cuda")[1:].view(h.shape)
+    with pytest.raises(k._lib.KronError):
+        k.kron_vocab_ce_fwd(moved, W, lab)
+
+
+def test_few_rows_and_tokens_at_infinity():
+    """A token of W at -infinity changes no other token's logit, whatever K is."""
+    k = K()
+    h, W, lab, _ = case(16, 33, 45, 200, torch.float32)
+    h[:, 0] = 1
+    W[7], W[7, 0] = 0, float("-inf")
+    lab[lab == 7] = 8
+    keep = torch.tensor([v for v in range(200) if v != 7], device="cuda")
+    for t in (torch.float32, torch.bfloat16):
+        _, nll, _ = k.kron_vocab_ce_fwd(h.to(t), W.to(t), lab)
+        o = OV.forward_backward(f64(h.to(t)), f64(W[keep].to(t)), (lab - (lab > 7).long()).cpu().numpy())
+        assert np.abs(f64(nll) - o["nll"]).max() <= 1e-5 * max(1, np.abs(o["nll"]).max())
