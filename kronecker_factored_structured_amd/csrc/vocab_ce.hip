@@ -134,28 +134,14 @@ __global__ __launch_bounds__(256) void vocab_pack_kernel(VocabCE a, int which) {
     const int r = (int)(i / per), k = (int)(i - (int64_t)r * per) * 8;
     const int64_t row = !w && a.idx ? a.idx[r] : r, from = row * a.K + k;
     if constexpr (BF) {
-      const uint16_t* s = (const uint16_t*)(w ? a.W : a.h) + from;
-      u4 o = {0, 0, 0, 0};
-      if (k + 8 <= a.K && (a.K & 7) == 0)
-        o = *(const u4*)s;
-      else
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (k + e < a.K) o[e / 2] |= (uint32_t)s[e] << (16 * (e & 1));
+      const u4 o = row_end<false>((const char*)((const uint16_t*)(w ? a.W : a.h) + from), a.K - k);
       *(u4*)(dst + (int64_t)r * a.Kp + k) = o;
     } else {
       const float* s = (const float*)(w ? a.W : a.h) + from;
-      float v[8];
-      if (k + 8 <= a.K && (a.K & 3) == 0) {
-        const f4 x = *(const f4*)s, y = *(const f4*)(s + 4);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = x[e], v[4 + e] = y[e];
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = k + e < a.K ? s[e] : 0.f;
-      }
+      const f4 v0 = __builtin_bit_cast(f4, row_end<true>((const char*)s, a.K - k));
+      const f4 v1 = __builtin_bit_cast(f4, row_end<true>((const char*)(s + 4), a.K - k - 4));
       const float weight = which == 2 ? a.weights[row] * up_weight * (1.f / kOne) : 1.f;
-      f4 x = f4{v[0], v[1], v[2], v[3]} * up * weight, y = f4{v[4], v[5], v[6], v[7]} * up * weight;
+      f4 x = v0 * up * weight, y = v1 * up * weight;
       uint16_t* d = dst + (int64_t)r * a.Kp * 2 + (k / 32) * 64 + k % 32;
       *(h4*)d = first_part(x);
       *(h4*)(d + 4) = first_part(y);
@@ -172,7 +158,7 @@ __device__ inline void vocab_logits(P& p, const VocabCE& a, int count, int v0, i
   if constexpr (BF || P::F32) {
     const Operand w = P::F32 ? Operand{(const uint16_t*)a.W, (int64_t)a.K * 2, a.V, a.K} : Operand{a.wp, a.Kw, a.V, a.Kw};
     const Operand h = P::F32 ? Operand{(const uint16_t*)a.h, (int64_t)a.K * 2, count, a.K, a.idx} : Operand{a.hp, a.Kh, count, a.Kh};
-    const int whole = a.K / P::kStep * P::kStep;
+    const int whole = BF && a.Kw == a.Kp && a.Kh == a.Kp ? a.Kp : a.K / P::kStep * P::kStep;
     p.run(w, h, v0, n0, 0, whole, lds);
     if (whole < a.K)
       p.run_end([&](int m) { return (const char*)w.p + (int64_t)min(v0 + m, a.V - 1) * w.ld * 2; },
@@ -651,9 +637,11 @@ VocabPlan plan_of(int64_t N, int K, int V, bool bf, bool weights, bool backward)
   p.Kp = (int)ceil_div(K, kBK) * kBK;
   p.rows = weights;
   p.direct = direct_of(N, bf);
-  // (the products over rows of W or h take whole 16-byte pieces)
-  p.copy_h = bf ? weights || (backward && K % 8) : backward || !p.direct;
-  p.copy_w = bf ? backward && K % 8 : !p.direct;
+  // bf16 rows that are not whole cache lines load slower, and are copied where a copy costs less than that: 2050 x 1000 x 32003
+  // takes 175 us with copies and 194 without, 300 x 1000 x 100000 287 and 145.  (dh and dW take whole 16-byte pieces of rows.)
+  const bool copies = (K % kBK && N > 512) || (backward && K % 8);
+  p.copy_h = bf ? weights || copies : backward || !p.direct;
+  p.copy_w = bf ? copies : !p.direct;
   p.tiles = (int)ceil_div(V, p.direct && !backward ? 128 : 256);
   size_t at = 0;
   auto take = [&](size_t bytes) { const size_t r = at; at += up256(bytes); return r; };
