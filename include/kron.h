@@ -536,11 +536,13 @@ kron_status_t kron_vocab_ce_bwd(int64_t N, int32_t K, int32_t V, int32_t dtype, 
  *   dup   [E, M, R] = sum over e's rows of scales[e] dy^T (x down[e]^T)    (fp32)
  * An adapter without rows has gradients 0; rows with an id >= E have dx NaN and no part in the others.
  * All products and sums are fp32; every output is rounded once.
- * Limits: 1 <= K, M <= 65536, 1 <= R <= KRON_ADAPTERS_MAX_RANK, 1 <= E <= 65535, N <= 2^24, B <= 2^20.
+ * Limits: 1 <= K, M <= 65536, 1 <= R <= KRON_ADAPTERS_MAX_RANK, 1 <= E <= 65535, N <= 2^24; B <= 2^20, with
+ * starts KRON_ADAPTERS_MAX_REQUESTS.
  * All arrays 16-byte aligned but ids and starts (4).  The forward needs no workspace; the backward's is
  * kron_adapters_workspace_bytes(N, K, M, R, E) bytes, 256-byte aligned (0 for rejected sizes).
  */
 #define KRON_ADAPTERS_MAX_RANK 128
+#define KRON_ADAPTERS_MAX_REQUESTS 65536
 typedef struct {
   int64_t N;                 /* rows, >= 0                                  */
   int32_t K, M, R, E, B;     /* widths, rank, adapters, requests            */
@@ -569,7 +571,7 @@ kron_status_t kron_adapters_bwd(const kron_adapters_t* d, const void* x, const v
  * fp16 parts each (off by at most 2^-22 of the value, or 2^-38, of matrices whose entries are at most 3.5).
  * bf16: as one fp16 part (2^-11).
  * Limits: ntensors <= 4096, 1 <= rows, cols <= KRON_MUON_MAX_SIDE, count <= 2^20 (0: skipped),
- * 1 <= steps <= KRON_MUON_MAX_STEPS, momentum >= 0, eps > 0.  Tensors must not overlap.  The workspace
+ * 1 <= steps <= KRON_MUON_MAX_STEPS, momentum >= 0, eps > 0 (all finite, eps no less than fp32 holds).  Tensors must not overlap.  The workspace
  * is kron_muon_workspace_bytes(...) bytes, 256-byte aligned (0: none is needed, or rejected sizes).
  */
 #define KRON_MUON_MAX_SIDE 16384

@@ -44,6 +44,7 @@ KRON_VOCAB_CE_STATS = 2
 KRON_VOCAB_CE_MAX_ROWS = 1048576
 KRON_VOCAB_CE_MAX_WIDTH = 16384
 KRON_ADAPTERS_MAX_RANK = 128
+KRON_ADAPTERS_MAX_REQUESTS = 65536
 KRON_MUON_MAX_SIDE = 16384
 KRON_MUON_MAX_STEPS = 16
 

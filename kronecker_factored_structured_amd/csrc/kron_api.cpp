@@ -1135,7 +1135,9 @@ kron::Adapters adapters_args(const kron_adapters_t* d) {
 }
 
 kron_status_t adapters_tables(const kron_adapters_t* d, const int32_t* ids, const int32_t* starts) {
-  if (d->N > 0 && !ids) return fail(KRON_E_NULL, "ids is required");
+  if (d->B > 0 && !ids) return fail(KRON_E_NULL, "ids is required");
+  if (starts && d->B > KRON_ADAPTERS_MAX_REQUESTS)
+    return fail(KRON_E_UNSUPPORTED, "B = %d requests of given bounds beyond the limit (%d)", d->B, KRON_ADAPTERS_MAX_REQUESTS);
   if (!starts && d->B != d->N) return fail(KRON_E_SHAPE, "B = %d requests of one row each, but N = %lld", d->B, (long long)d->N);
   if ((((uintptr_t)ids | (uintptr_t)starts) & 3u) != 0) return fail(KRON_E_ALIGN, "ids or starts is not aligned to its elements");
   return KRON_OK;
@@ -1257,9 +1259,10 @@ kron_status_t kron_muon_step(const kron_muon_t* h, int32_t ntensors, int32_t dty
   kron_status_t st;
   if (!h) return fail(KRON_E_NULL, "the hyper-parameters are NULL");
   if (!muon_sizes(ntensors, count, rows, cols, dtype, st)) return st;
-  if (!std::isfinite(h->lr) || !(h->momentum >= 0.0) || !std::isfinite(h->momentum) || !std::isfinite(h->weight_decay) ||
-      !std::isfinite(h->a) || !std::isfinite(h->b) || !std::isfinite(h->c) || !(h->eps > 0.0) || h->steps < 1 ||
-      h->steps > KRON_MUON_MAX_STEPS)
+  // as the kernels take them, in fp32 (an eps that is 0 there makes NaN of zeros)
+  for (double v : {h->lr, h->momentum, h->weight_decay, h->lr * h->weight_decay, h->a, h->b, h->c, h->eps})
+    if (!std::isfinite((float)v)) return fail(KRON_E_ARG, "hyper-parameters out of range");
+  if (!(h->momentum >= 0.0) || !((float)h->eps > 0.f) || h->steps < 1 || h->steps > KRON_MUON_MAX_STEPS)
     return fail(KRON_E_ARG, "hyper-parameters out of range");
   if (ntensors == 0) return ok();
   if (!params || !grads || !m) return fail(KRON_E_NULL, "pointer arrays are required");

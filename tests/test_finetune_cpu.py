@@ -172,6 +172,23 @@ def test_adapters_refusals(f):
     assert ada_fwd(N=0, B=0, starts=None, x=None, base=None, y=None, ids=None) == _lib.KRON_OK      # nothing launched
 
 
+@pytest.mark.parametrize("f", [ada_fwd, ada_bwd])
+def test_adapters_requests(f):
+    """ids belong to the requests, not to the rows: none of them is read without rows either, and all are without ids."""
+    for kw, want in ((dict(N=0, x=None, ids=None), "NULL"), (dict(N=0, B=5, ids=None), "NULL"),
+                     (dict(B=_lib.KRON_ADAPTERS_MAX_REQUESTS + 1), "UNSUPPORTED")):
+        assert f(**kw) == getattr(_lib, "KRON_E_" + want), (kw, _lib.last_error())
+    assert ada_fwd(N=0, B=0, ids=None) == _lib.KRON_OK      # nothing launched
+    # (a refusal that comes after ids': no request, no ids)
+    assert f(B=0, ids=None, x=P(8)) == _lib.KRON_E_ALIGN
+
+
+def test_muon_refuses_what_fp32_does_not_hold():
+    for kw in (dict(eps=1e-60), dict(lr=1e60), dict(momentum=1e39), dict(weight_decay=1e300), dict(b=-1e39), dict(lr=1e30, weight_decay=1e30),
+               dict(eps=1e39)):
+        assert muon(**kw) == _lib.KRON_E_ARG, kw
+
+
 def muon(tensors=((P(), P(MB), P(2 * MB), 2, 8, 4),), dtype=0, hyper=None, ws=P(64 * MB), nbytes=64 * MB, n=None, **kw):
     d = dict(lr=0.02, momentum=0.95, weight_decay=0.0, a=3.4445, b=-4.775, c=2.0315, eps=1e-7, nesterov=1, steps=5)
     d.update(kw)

@@ -158,6 +158,16 @@ def test_no_rows():
     assert torch.count_nonzero(g["ddown"]) == 0 and torch.count_nonzero(g["dup"]) == 0
 
 
+def test_no_requests():
+    """Rows of no request at all: y = base, gradients of nothing."""
+    k = K()
+    c = case(7, 20, 8, 12, 2, 2, [20], torch.float32)
+    none, starts = c["ids"][:0], c["starts"][:1]
+    assert torch.equal(k.kron_adapters_fwd(c["x"], c["base"], c["down"], c["up"], none, starts), c["base"])
+    g = k.kron_adapters_bwd(c["x"], c["dy"], c["down"], c["up"], none, starts)
+    assert torch.count_nonzero(g["dx"]) == 0 and torch.count_nonzero(g["ddown"]) == 0 and torch.count_nonzero(g["dup"]) == 0
+
+
 def test_repeatable():
     k = K()
     c = case(8, 3000, 96, 64, 16, 2, [1700, 1300], torch.bfloat16, none=False)
