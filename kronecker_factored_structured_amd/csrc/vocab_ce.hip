@@ -252,26 +252,29 @@ __device__ inline void vocab_sum(const VocabCE& a, double* red) {
   }
 }
 
-// A row's statistics from its tiles': 32 rows by 32 slices of the tiles.  One workgroup alone (few rows) takes them all, and
-// the loss.
+// A row's statistics from its tiles': R rows by SL slices of the tiles.  One workgroup alone (few rows: 64 at a time)
+// takes them all, and the loss.
+template <int R>
 __global__ __launch_bounds__(1024) void vocab_join_kernel(VocabCE a, int tiles) {
-  __shared__ float2 red[32][33];
+  constexpr int SL = 1024 / R;
+  __shared__ float2 red[SL][R + 1];
   __shared__ double sums[16];
-  const int count = vocab_count(a), r = threadIdx.x & 31, sl = threadIdx.x >> 5;
+  const int count = vocab_count(a), r = threadIdx.x % R, sl = threadIdx.x / R;
   const float2* part = (const float2*)a.part;
-  for (int64_t row0 = (int64_t)blockIdx.x * 32; row0 < count; row0 += (int64_t)gridDim.x * 32) {
+  for (int64_t row0 = (int64_t)blockIdx.x * R; row0 < count; row0 += (int64_t)gridDim.x * R) {
     float2 s = {-INFINITY, 0.f};
     if (row0 + r < count)
 #pragma unroll 8
-      for (int m = sl; m < tiles; m += 32) s = joined(s, part[(int64_t)m * a.N + row0 + r]);
+      for (int m = sl; m < tiles; m += SL) s = joined(s, part[(int64_t)m * a.N + row0 + r]);
     red[sl][r] = s;
     __syncthreads();
-    // the row's 32 slices by half a wavefront
-    s = red[r][sl];
+    // the row's slices by SL neighbouring lanes
+    const int slice = threadIdx.x % SL;
+    const int64_t k = row0 + threadIdx.x / SL;
+    s = red[slice][threadIdx.x / SL];
 #pragma unroll
-    for (int o = 16; o >= 1; o /= 2) s = joined(s, float2{__shfl_xor(s.x, o, 32), __shfl_xor(s.y, o, 32)});
-    const int64_t k = row0 + sl;
-    if (r == 0 && k < count) {
+    for (int o = SL / 2; o >= 1; o /= 2) s = joined(s, float2{__shfl_xor(s.x, o, SL), __shfl_xor(s.y, o, SL)});
+    if (slice == 0 && k < count) {
       const int64_t row = a.idx ? a.idx[k] : k;
       const int64_t lab = a.labels[row];
       const bool token = lab >= 0 && lab < a.V;
@@ -746,8 +749,11 @@ hipError_t run_fwd(const VocabCE& a, const VocabPlan& p, hipStream_t s) {
       e = few(a.N) ? go<PF, vocab_fwd_kernel<PF, BF>>(grid, s, a, p.tiles, tn) : go<PB, vocab_fwd_kernel<PB, BF>>(grid, s, a, p.tiles, tn);
     if (e != hipSuccess) return e;
     const bool one = a.N <= 128;      // a workgroup's few turns are shorter than another launch
-    hipLaunchKernelGGL(vocab_join_kernel, dim3(one ? 1u : (unsigned)ceil_div(a.N, 32)), dim3(1024), 0, s, a, p.tiles);
-    if (one) return hipGetLastError();
+    if (one) {
+      hipLaunchKernelGGL((vocab_join_kernel<64>), dim3(1), dim3(1024), 0, s, a, p.tiles);
+      return hipGetLastError();
+    }
+    hipLaunchKernelGGL((vocab_join_kernel<32>), dim3((unsigned)ceil_div(a.N, 32)), dim3(1024), 0, s, a, p.tiles);
   }
   hipLaunchKernelGGL(vocab_loss_kernel, dim3(1), dim3(1024), 0, s, a);
   return hipGetLastError();
