@@ -367,7 +367,7 @@ __global__ __launch_bounds__(P::kThreads) void vocab_dh_kernel(VocabCE a, int v0
   tile_of(blockIdx.x, gridDim.x, tm, tn, mt, nt, 4);
   const int count = vocab_count(a), m0 = mt * P::BM, n0 = nt * P::BN;
   if (n0 >= count) return;
-  const int k0 = blockIdx.y * len, k1 = min(vc, k0 + len);
+  const int k0 = blockIdx.y * len, k1 = min(min(vc, a.V - v0), k0 + len);
   const Operand dz = {a.dz, (int64_t)vc * P::NP, count, vc};
   P p;
   const int64_t ld = P::NP == 2 ? a.Kp * 2 : a.Kw;
@@ -439,7 +439,7 @@ __global__ __launch_bounds__(256, 2) void vocab_dh_few_kernel(VocabCE a, int v0,
   };
   int b = b0;
   if (k0 + 64 <= a.K) {
-    const int steps = (b1 - b0) / 16;
+    const int steps = max(0, b1 - b0) / 16;
     Step s[3];
 #pragma unroll
     for (int i = 0; i < 3; ++i)
@@ -584,12 +584,17 @@ __global__ __launch_bounds__(256) void vocab_dw_join_kernel(VocabCE a, int v0, i
 }
 
 // ------------------------------------------------------------------------------ host
-template <bool BF, Side SA, Side SB>
-using Big = Product<2, 4, 8, 4, SA, SB, BF, BF ? 1 : 2>;
-template <bool BF, Side SA, Side SB>
-using Three = Product<2, 4, 6, 4, SA, SB, BF, BF ? 1 : 2>;      // 192 x 256
-template <bool BF, Side SA, Side SB>
-using Few = Product<4, 1, 4, 4, SA, SB, BF, BF ? 1 : 2>;        // 256 x 64
+// Tiles of a product, m x n.
+enum Tile { kBig, kWide, kMid, kSmall, kFew };      // 256 x 256, 192 x 256, 128 x 128, 64 x 64, 256 x 64
+template <int T, bool BF, Side SA, Side SB>
+using Tiled = std::conditional_t<T == kBig, Product<2, 4, 8, 4, SA, SB, BF, BF ? 1 : 2>,
+              std::conditional_t<T == kWide, Product<2, 4, 6, 4, SA, SB, BF, BF ? 1 : 2>,
+              std::conditional_t<T == kMid, Product<2, 2, 4, 4, SA, SB, BF, BF ? 1 : 2>,
+              std::conditional_t<T == kSmall, Product<2, 2, 2, 2, SA, SB, BF, BF ? 1 : 2, 4>,
+                                 Product<4, 1, 4, 4, SA, SB, BF, BF ? 1 : 2>>>>>;
+// fp32 as it is: 128 x TN 16.
+template <int TN, int NS>
+using Whole = Product<4, 1, 2, TN, ROW, ROW, false, 2, NS, true>;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -599,41 +604,56 @@ bool few(int64_t N) { return N <= 64; }
 
 // Whether fp32's products with W take it as it is, on the fp32 instruction.
 bool direct_of(int64_t N, bool bf) { return !bf && N > 0 && N <= 128; }
-template <int WN, int TN, int NS>
-using Whole = Product<4, WN, 2, TN, ROW, ROW, false, 2, NS, true>;      // 128 x WN TN 16
 
-// Workgroups (one a CU) run in rounds of 256, so that a product of a few more tiles than that takes two.  The parts of the
-// contraction that cost least, with what was measured: a step of a 256 x 256 tile 2.2 us, its start and end 4 us, the
-// tile's sums through memory at 4.5 TB/s (`moves` times for each part).
-struct Parts {
-  int parts;
-  double us;
+// The tile and the parts of the contraction that cost least, with what was measured of each tile: a step of 64 where its
+// workgroup has the CU to itself and where `resident` share it, and start and end; the parts' sums go through memory at
+// 4.5 TB/s, `moves` times.  (362 x 424 x 6552 fp32: its products in tiles of 256 alone 33, 36, 30 and 21 us.)
+struct TileCost {
+  Tile tile;
+  int m, n, resident;
+  double alone, shared, ends;
 };
-Parts best_parts(int64_t tiles, int64_t steps, double share, double moves, int most) {
-  Parts best{1, 1e30};
-  for (int s = 1; s <= most && (s == 1 || steps / s >= 4); ++s) {
-    const double rounds = (double)ceil_div(tiles * s, 256);
-    const double us = rounds * (ceil_div(steps, s) * 2.2 * share + 4) + (s > 1 || moves > 2 ? tiles * s * moves * 0.058 * share : 0);
-    if (us < best.us) best = {s, us};
+constexpr TileCost kTiles[] = {{kBig, 256, 256, 1, 2.2, 2.2, 4}, {kWide, 192, 256, 1, 1.65, 1.65, 4}, {kMid, 128, 128, 2, 0.85, 0.62, 3.5},
+                               {kSmall, 64, 64, 2, 0.5, 0.25, 3}, {kFew, 256, 64, 2, 0.85, 0.62, 3.5}};
+struct Choice {
+  Tile tile;
+  int parts;
+};
+// tiles: a mask of the ones to choose from; steps of 64 of the contraction (fp32: of its three products).
+Choice choose(int64_t m, int64_t n, int64_t steps, int most, double moves, unsigned tiles) {
+  Choice best{kBig, 1};
+  double least = 1e300;
+  for (const TileCost& t : kTiles) {
+    if (!(tiles >> t.tile & 1)) continue;
+    const int64_t all = ceil_div(m, t.m) * ceil_div(n, t.n);
+    for (int s = 1; s <= most && (s == 1 || steps / s >= 4); ++s) {
+      const int64_t each = ceil_div(all * s, 256), rounds = each / t.resident, rest = each % t.resident, len = ceil_div(steps, s);
+      auto run = [&](int64_t c) { return c ? len * std::max(t.alone, c * t.shared) + t.ends : 0.0; };
+      const double us = rounds * run(t.resident) + run(rest) + (s > 1 || moves > 2 ? (double)m * n * s * moves * 8.9e-7 : 0);
+      if (us < least) least = us, best = {t.tile, s};
+    }
   }
   return best;
 }
+const TileCost& cost_of(Tile t) { return kTiles[t]; }
+constexpr unsigned kSquares = 1u << kBig | 1u << kMid | 1u << kSmall;
 
 struct VocabPlan {
   int Kp;
   bool rows, copy_h, copy_w;      // rows in use are listed; operands that are copies
-  int tiles;                      // of the vocabulary, 256 wide (the direct forward's: 128)
-  int piece, pieces, splits;      // backward
-  bool three;                     // dh in tiles of 192
   bool direct;                    // W as it is
+  Tile fwd;
+  int tiles;                      // of the vocabulary in the forward
+  int piece, pieces;              // backward
+  Choice dh;
   size_t sc, idx, pos, hp, hw, wp, part, zlab, dz, dhpart, dwpart, bytes;
 };
 
-// Parts of a piece's dW.
-int dw_parts(int64_t N, int Kp, int vc, int planes) {
-  const int64_t tiles = ceil_div(Kp, 256) * (vc / 256), steps = ceil_div(N, kBK) * (planes == 2 ? 3 : 1);
-  return tiles >= 256 ? 1 : best_parts(tiles, steps, 1, 2, 8).parts;
+int64_t steps_of(int64_t n, int planes) { return ceil_div(n, kBK) * (planes == 2 ? 3 : 1); }
+Choice logits_tile(int64_t N, int Kp, int64_t vc, int planes) {
+  return choose(vc, N, steps_of(Kp, planes), 1, 2, few(N) ? 1u << kFew | 1u << kSmall : kSquares);
 }
+Choice dw_tile(int64_t N, int Kp, int vc, int planes) { return choose(Kp, vc, steps_of(N, planes), 8, 2, kSquares); }
 
 VocabPlan plan_of(int64_t N, int K, int V, bool bf, bool weights, bool backward) {
   VocabPlan p{};
@@ -645,10 +665,11 @@ VocabPlan plan_of(int64_t N, int K, int V, bool bf, bool weights, bool backward)
   const bool copies = (K % kBK && N > 512) || (backward && K % 8);
   p.copy_h = bf ? weights || copies : backward || !p.direct;
   p.copy_w = bf ? copies : !p.direct;
-  p.tiles = (int)ceil_div(V, p.direct && !backward ? 128 : 256);
   size_t at = 0;
   auto take = [&](size_t bytes) { const size_t r = at; at += up256(bytes); return r; };
   const int planes = bf ? 1 : 2;
+  p.fwd = logits_tile(N, p.Kp, V, planes).tile;
+  p.tiles = (int)ceil_div(V, p.direct ? 128 : cost_of(p.fwd).m);
   const int64_t rows = ceil_div(std::max<int64_t>(N, 1), kBK) * kBK;
   p.sc = take(sizeof(VocabScales));
   p.idx = take(p.rows ? 4 * (size_t)N : 0);
@@ -661,25 +682,23 @@ VocabPlan plan_of(int64_t N, int K, int V, bool bf, bool weights, bool backward)
     p.zlab = take(4 * (size_t)N);
   } else {
     // dz of a piece takes at most about 512 MB; where a tile of dW takes long, a piece's tiles fill whole rounds
-    const int64_t tk = ceil_div(p.Kp, 256), triple = bf ? 1 : 3;
-    int64_t piece = std::min<int64_t>(p.tiles, std::max<int64_t>(1, (int64_t(512) << 20) / (rows * 256 * 2 * planes)));
-    if (rows / kBK * triple >= 16 && piece * tk >= 256) piece = piece * tk / 256 * 256 / tk;
+    const int64_t tk = ceil_div(p.Kp, 256), wide = ceil_div(V, 256);
+    int64_t piece = std::min<int64_t>(wide, std::max<int64_t>(1, (int64_t(512) << 20) / (rows * 256 * 2 * planes)));
+    if (steps_of(rows, planes) >= 16 && piece * tk >= 256) piece = piece * tk / 256 * 256 / tk;
     p.piece = (int)piece * 256;
-    p.pieces = (int)ceil_div(p.tiles, piece);
+    p.pieces = (int)ceil_div(wide, piece);
     p.dz = take(2 * (size_t)planes * rows * p.piece);
-    const int64_t steps = p.piece / kBK * triple, moves = p.pieces > 1 ? 4 : 2;
-    if (few(N) || p.direct) {
-      p.splits = (int)std::min<int64_t>(std::max<int64_t>(1, 512 / tk), std::max(1, p.piece / 512));
+    if (p.direct) {      // (parts of 128 tokens at least)
+      const int64_t groups = tk * (few(N) ? 1 : 2);
+      p.dh.parts = (int)std::min<int64_t>(std::max<int64_t>(1, 512 / groups), p.piece / 128);
     } else {
-      const int64_t tn = ceil_div(N, 256);
-      const Parts b = best_parts(tk * tn, steps, 1, moves, 16), c = best_parts(ceil_div(p.Kp, 192) * tn, steps, 0.75, moves, 16);
-      p.three = c.us < b.us;
-      p.splits = p.three ? c.parts : b.parts;
+      p.dh = choose(p.Kp, N, steps_of(p.piece, planes), few(N) ? 128 : 16, p.pieces > 1 ? 4 : 2,
+                    few(N) ? 1u << kFew | 1u << kSmall : kSquares | 1u << kWide);
     }
-    p.dhpart = take(4 * (size_t)p.splits * N * p.Kp);
+    p.dhpart = take(4 * (size_t)p.dh.parts * N * p.Kp);
     size_t most = 0;
     for (int i = 0; i < p.pieces; ++i) {
-      const int vc = std::min(p.piece, (p.tiles - i * (p.piece / 256)) * 256), parts = dw_parts(N, p.Kp, vc, planes);
+      const int vc = (int)std::min<int64_t>(p.piece, (wide - i * piece) * 256), parts = dw_tile(N, p.Kp, vc, planes).parts;
       if (parts > 1) most = std::max(most, 4 * (size_t)parts * vc * p.Kp);
     }
     p.dwpart = take(most);
@@ -718,7 +737,11 @@ hipError_t go(dim3 grid, hipStream_t s, A... args) {
 template <bool BF>
 hipError_t prepare(const VocabCE& a, const VocabPlan& p, hipStream_t s) {
   if (a.sc) hipLaunchKernelGGL(vocab_rows_kernel, dim3(1), dim3(1024), 0, s, a);
-  if (!BF && p.copy_h) hipLaunchKernelGGL(vocab_top_kernel, dim3(p.copy_w ? 512 : 64, p.copy_w ? 2 : 1), dim3(256), 0, s, a);
+  if (!BF && p.copy_h) {
+    // (one after the other, 512 atomics take 12 us: a workgroup has 32 KB at least)
+    const int64_t most = std::max<int64_t>(a.N, p.copy_w ? a.V : 0) * a.K;
+    hipLaunchKernelGGL(vocab_top_kernel, dim3((unsigned)std::min<int64_t>(512, ceil_div(most, 8192)), p.copy_w ? 2 : 1), dim3(256), 0, s, a);
+  }
   const int per = p.Kp / 8;
   auto blocks = [&](int64_t rows) { return dim3((unsigned)std::min<int64_t>(4096, std::max<int64_t>(1, ceil_div(rows * per, 256)))); };
   if (p.copy_h && a.N) hipLaunchKernelGGL((vocab_pack_kernel<BF>), blocks(a.N), dim3(256), 0, s, a, 0);
@@ -727,26 +750,44 @@ hipError_t prepare(const VocabCE& a, const VocabPlan& p, hipStream_t s) {
   return hipGetLastError();
 }
 
+// f(tile) with the tile as a constant, of the ones in `tiles`.
+template <unsigned tiles, class F>
+hipError_t with_tile(Tile t, const F& f) {
+  hipError_t e = hipErrorInvalidValue;
+  auto one = [&](auto tile) {
+    if constexpr (tiles >> tile.value & 1)
+      if (t == tile.value) e = f(tile);
+  };
+  one(std::integral_constant<int, kBig>{}), one(std::integral_constant<int, kWide>{}), one(std::integral_constant<int, kMid>{});
+  one(std::integral_constant<int, kSmall>{}), one(std::integral_constant<int, kFew>{});
+  return e;
+}
+// f(Product) of fp32 W as it is.
+template <class F>
+hipError_t with_rows(int64_t N, const F& f) {
+  if (N <= 32) return f((Whole<2, 4>*)nullptr);
+  if (N <= 64) return f((Whole<4, 3>*)nullptr);
+  return f((Whole<8, 2>*)nullptr);
+}
+
 template <bool BF>
 hipError_t run_fwd(const VocabCE& a, const VocabPlan& p, hipStream_t s) {
   hipError_t e = prepare<BF>(a, p, s);
   if (e != hipSuccess) return e;
   if (a.N) {
-    const int tn = p.direct ? 1 : (int)ceil_div(a.N, few(a.N) ? 64 : 256);
-    typedef Few<BF, ROW, ROW> PF;
-    typedef Big<BF, ROW, ROW> PB;
-    const dim3 grid((unsigned)(p.tiles * tn));
-    if constexpr (!BF)
-      if (p.direct) {
-        typedef Whole<1, 2, 4> P1;
-        typedef Whole<1, 4, 3> P2;
-        typedef Whole<1, 8, 2> P4;
-        e = a.N <= 32 ? go<P1, vocab_fwd_kernel<P1, BF>>(grid, s, a, p.tiles, 1)
-            : a.N <= 64 ? go<P2, vocab_fwd_kernel<P2, BF>>(grid, s, a, p.tiles, 1)
-                        : go<P4, vocab_fwd_kernel<P4, BF>>(grid, s, a, p.tiles, 1);
-      }
-    if (!p.direct)
-      e = few(a.N) ? go<PF, vocab_fwd_kernel<PF, BF>>(grid, s, a, p.tiles, tn) : go<PB, vocab_fwd_kernel<PB, BF>>(grid, s, a, p.tiles, tn);
+    if (p.direct) {
+      if constexpr (!BF)
+        e = with_rows(a.N, [&](auto* product) {
+          typedef std::remove_pointer_t<decltype(product)> P;
+          return go<P, vocab_fwd_kernel<P, BF>>(dim3((unsigned)p.tiles), s, a, p.tiles, 1);
+        });
+    } else {
+      const int tn = (int)ceil_div(a.N, cost_of(p.fwd).n);
+      e = with_tile<kSquares | 1u << kFew>(p.fwd, [&](auto tile) {
+        typedef Tiled<tile, BF, ROW, ROW> P;
+        return go<P, vocab_fwd_kernel<P, BF>>(dim3((unsigned)(p.tiles * tn)), s, a, p.tiles, tn);
+      });
+    }
     if (e != hipSuccess) return e;
     const bool one = a.N <= 128;      // a workgroup's few turns are shorter than another launch
     if (one) {
@@ -760,62 +801,67 @@ hipError_t run_fwd(const VocabCE& a, const VocabPlan& p, hipStream_t s) {
 }
 
 template <bool BF>
+hipError_t run_dz(const VocabCE& a, const VocabPlan& p, int v0, int vc, hipStream_t s) {
+  if (p.direct) {
+    if constexpr (!BF)
+      return with_rows(a.N, [&](auto* product) {
+        typedef std::remove_pointer_t<decltype(product)> P;
+        return go<P, vocab_dz_kernel<P, BF>>(dim3((unsigned)(vc / P::BM)), s, a, v0, vc, vc / P::BM, 1);
+      });
+  }
+  return with_tile<kSquares | 1u << kFew>(logits_tile(a.N, p.Kp, vc, BF ? 1 : 2).tile, [&](auto tile) {
+    typedef Tiled<tile, BF, ROW, ROW> P;
+    const int tm = vc / P::BM, tn = (int)ceil_div(a.N, P::BN);
+    return go<P, vocab_dz_kernel<P, BF>>(dim3((unsigned)(tm * tn)), s, a, v0, vc, tm, tn);
+  });
+}
+
+template <bool BF>
+hipError_t run_dh(const VocabCE& a, const VocabPlan& p, int v0, int vc, hipStream_t s) {
+  const int len = (int)ceil_div(ceil_div(vc, p.dh.parts), kBK) * kBK, add = v0 > 0;
+  if (p.direct) {
+    const int tn = few(a.N) ? 1 : 2;
+    const dim3 grid((unsigned)(ceil_div(p.Kp, 256) * tn), (unsigned)p.dh.parts);
+    if (a.N <= 32) hipLaunchKernelGGL((vocab_dh_few_kernel<2>), grid, dim3(256), 0, s, a, v0, vc, tn, len, add);
+    else hipLaunchKernelGGL((vocab_dh_few_kernel<4>), grid, dim3(256), 0, s, a, v0, vc, tn, len, add);
+    return hipGetLastError();
+  }
+  return with_tile<kSquares | 1u << kWide | 1u << kFew>(p.dh.tile, [&](auto tile) {
+    typedef Tiled<tile, BF, COL, ROW> P;
+    const int tm = (int)ceil_div(p.Kp, P::BM), tn = (int)ceil_div(a.N, P::BN);
+    return go<P, vocab_dh_kernel<P, BF>>(dim3((unsigned)(tm * tn), (unsigned)p.dh.parts), s, a, v0, vc, tm, tn, len, add);
+  });
+}
+
+template <bool BF>
+hipError_t run_dw(const VocabCE& a, const VocabPlan& p, int v0, int vc, hipStream_t s) {
+  const Choice w = dw_tile(a.N, p.Kp, vc, BF ? 1 : 2);
+  const hipError_t e = with_tile<kSquares>(w.tile, [&](auto tile) {
+    typedef Tiled<tile, BF, COL, COL> P;
+    const int tm = (int)ceil_div(p.Kp, P::BM), tn = vc / P::BN;
+    return go<P, vocab_dw_kernel<P, BF>>(dim3((unsigned)(tm * tn), (unsigned)w.parts), s, a, v0, vc, tm, tn);
+  });
+  if (e != hipSuccess || w.parts == 1) return e;
+  hipLaunchKernelGGL((vocab_dw_join_kernel<BF>), dim3((unsigned)std::min<int64_t>(4096, ceil_div((int64_t)vc * (p.Kp / 4), 256))), dim3(256), 0, s,
+                     a, v0, vc, w.parts);
+  return hipGetLastError();
+}
+
+template <bool BF>
 hipError_t run_bwd(const VocabCE& a, const VocabPlan& p, hipStream_t s) {
   hipError_t e = prepare<BF>(a, p, s);
-  if (e != hipSuccess) return e;
-  const bool fw = few(a.N);
-  const int tn = p.direct ? 1 : (int)ceil_div(a.N, fw ? 64 : 256), tk = (int)ceil_div(p.Kp, 256);
-  for (int i = 0; i < p.pieces; ++i) {
-    const int v0 = i * p.piece, vc = std::min(p.piece, (int)ceil_div(a.V - v0, 256) * 256), tm = vc / 256;
-    if (a.N) {
-      typedef Few<BF, ROW, ROW> PF;
-      typedef Big<BF, ROW, ROW> PB;
-      const dim3 grid((unsigned)(tm * tn));
-      if constexpr (!BF)
-        if (p.direct) {
-          typedef Whole<1, 2, 4> P1;
-          typedef Whole<1, 4, 3> P2;
-          typedef Whole<1, 8, 2> P4;
-          const dim3 all((unsigned)(2 * tm));
-          e = a.N <= 32 ? go<P1, vocab_dz_kernel<P1, BF>>(all, s, a, v0, vc, 2 * tm, 1) : a.N <= 64 ? go<P2, vocab_dz_kernel<P2, BF>>(all, s, a, v0, vc, 2 * tm, 1) : go<P4, vocab_dz_kernel<P4, BF>>(all, s, a, v0, vc, 2 * tm, 1);
-        }
-      if (!p.direct)
-        e = fw ? go<PF, vocab_dz_kernel<PF, BF>>(grid, s, a, v0, vc, tm, tn) : go<PB, vocab_dz_kernel<PB, BF>>(grid, s, a, v0, vc, tm, tn);
-      if (e != hipSuccess) return e;
-    }
-    if (a.dh && a.N) {
-      typedef Few<BF, COL, ROW> PF;
-      typedef Big<BF, COL, ROW> PB;
-      const int len = (int)ceil_div(ceil_div(vc, p.splits), kBK) * kBK;
-      typedef Three<BF, COL, ROW> PT;
-      const int th = p.three ? (int)ceil_div(p.Kp, 192) : tk;
-      const dim3 grid((unsigned)(th * tn), (unsigned)p.splits);
-      if (p.direct) {
-        const int tn = a.N <= 64 ? 1 : 2;
-        const dim3 all((unsigned)(tk * tn), (unsigned)p.splits);
-        if (a.N <= 32) hipLaunchKernelGGL((vocab_dh_few_kernel<2>), all, dim3(256), 0, s, a, v0, vc, tn, len, (int)(i > 0));
-        else hipLaunchKernelGGL((vocab_dh_few_kernel<4>), all, dim3(256), 0, s, a, v0, vc, tn, len, (int)(i > 0));
-        e = hipGetLastError();
-      } else
-        e = p.three ? go<PT, vocab_dh_kernel<PT, BF>>(grid, s, a, v0, vc, th, tn, len, (int)(i > 0))
-          : fw ? go<PF, vocab_dh_kernel<PF, BF>>(grid, s, a, v0, vc, tk, tn, len, (int)(i > 0))
-             : go<PB, vocab_dh_kernel<PB, BF>>(grid, s, a, v0, vc, tk, tn, len, (int)(i > 0));
-      if (e != hipSuccess) return e;
-    }
-    if (a.dW) {
-      typedef Big<BF, COL, COL> PB;
-      const int parts = dw_parts(a.N, p.Kp, vc, BF ? 1 : 2);
-      e = go<PB, vocab_dw_kernel<PB, BF>>(dim3((unsigned)(tk * tm), (unsigned)parts), s, a, v0, vc, tk, tm);
-      if (e != hipSuccess) return e;
-      if (parts > 1)
-        hipLaunchKernelGGL((vocab_dw_join_kernel<BF>), dim3((unsigned)std::min<int64_t>(4096, ceil_div((int64_t)vc * (p.Kp / 4), 256))), dim3(256),
-                           0, s, a, v0, vc, parts);
-    }
+  for (int i = 0; i < p.pieces && e == hipSuccess; ++i) {
+    const int v0 = i * p.piece, vc = std::min(p.piece, (int)ceil_div(a.V - v0, 256) * 256);
+    if (a.N) e = run_dz<BF>(a, p, v0, vc, s);
+    if (a.dh && a.N && e == hipSuccess) e = run_dh<BF>(a, p, v0, vc, s);
+    if (a.dW && e == hipSuccess) e = run_dw<BF>(a, p, v0, vc, s);
   }
-  if (a.dh && a.N)
+  if (e == hipSuccess && a.dh && a.N) {
     hipLaunchKernelGGL((vocab_dh_join_kernel<BF>), dim3((unsigned)std::min<int64_t>(8192, ceil_div(a.N * (p.Kp / 4), 256))), dim3(256), 0, s, a,
-                       p.splits);
-  return hipGetLastError();
+                       p.dh.parts);
+    e = hipGetLastError();
+  }
+  return e;
 }
 
 }  // namespace
