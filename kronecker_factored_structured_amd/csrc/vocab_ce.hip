@@ -86,34 +86,40 @@ __global__ __launch_bounds__(1024) void vocab_rows_kernel(VocabCE a) {
 
 __device__ inline int vocab_count(const VocabCE& a) { return a.sc ? a.sc->count : (int)a.N; }
 
-// The largest finite magnitude of h's rows in use (block.y 0) and of W (1).
-__global__ __launch_bounds__(256) void vocab_top_kernel(VocabCE a) {
+// The largest finite magnitude of h's rows in use (block.y 0) and of W (1): a wavefront has four rows at a time.
+__global__ __launch_bounds__(1024) void vocab_top_kernel(VocabCE a) {
   const bool w = blockIdx.y == 1;
-  const int64_t n = (w ? a.V : vocab_count(a)) * (int64_t)a.K;
+  const int rows = w ? a.V : vocab_count(a), waves = gridDim.x * 16, lane = threadIdx.x & 63;
   const float* src = (const float*)(w ? a.W : a.h);
-  const bool rows = !w && a.idx;
   uint32_t top = 0;
-  auto see = [&](float f) {
-    const uint32_t v = __float_as_uint(f) & 0x7fffffffu;
-    if (v < 0x7f800000u) top = max(top, v);
-  };
-  const int64_t stride = (int64_t)gridDim.x * 256, first = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (rows && (a.K & 3)) {
-    for (int64_t i = first; i < n; i += stride) see(src[(int64_t)a.idx[i / a.K] * a.K + i % a.K]);
-  } else {
-#pragma unroll 4
-    for (int64_t i = first * 4; i < n - 3; i += stride * 4) {
-      const f4 v = *(const f4*)(src + (rows ? (int64_t)a.idx[i / a.K] * a.K + i % a.K : i));
-      see(v[0]), see(v[1]), see(v[2]), see(v[3]);
+  for (int r0 = blockIdx.x * 16 + (threadIdx.x >> 6); r0 < rows; r0 += 4 * waves) {
+    const char* p[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int r = min(r0 + q * waves, rows - 1);
+      p[q] = (const char*)(src + (int64_t)(!w && a.idx ? a.idx[r] : r) * a.K);
     }
-    if (first < (n & 3)) see(src[n - 1 - first]);      // (none where rows are gathered: K is a multiple of four)
+    for (int k = lane * 4; k < a.K; k += 256) {
+      u4 v[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = row_end<true>(p[q] + k * 4, a.K - k);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t x = v[q][e] & 0x7fffffffu;
+          if (x < 0x7f800000u) top = max(top, x);
+        }
+    }
   }
-  __shared__ uint32_t red[4];
+  __shared__ uint32_t red[16];
   for (int o = 32; o >= 1; o /= 2) top = max(top, (uint32_t)__shfl_xor((int)top, o, 64));
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = top;
   __syncthreads();
-  // (one atomic of a workgroup: at four of each of 1024 they took 100 us of this kernel's 125)
-  if (threadIdx.x == 0) atomicMax(w ? &a.sc->top_w : &a.sc->top_h, max(max(red[0], red[1]), max(red[2], red[3])));
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < 16; ++i) top = max(top, red[i]);
+    atomicMax(w ? &a.sc->top_w : &a.sc->top_h, top);
+  }
 }
 
 // Rows as operands: gathered (h), padded with zeros to Kp, fp32 split into its parts.  which 0: h, 1: W, 2: h times the
@@ -738,9 +744,9 @@ template <bool BF>
 hipError_t prepare(const VocabCE& a, const VocabPlan& p, hipStream_t s) {
   if (a.sc) hipLaunchKernelGGL(vocab_rows_kernel, dim3(1), dim3(1024), 0, s, a);
   if (!BF && p.copy_h) {
-    // (one after the other, 512 atomics take 12 us: a workgroup has 32 KB at least)
+    // (the atomics of 256 workgroups on a line take 9 us: each has 64 KB at least)
     const int64_t most = std::max<int64_t>(a.N, p.copy_w ? a.V : 0) * a.K;
-    hipLaunchKernelGGL(vocab_top_kernel, dim3((unsigned)std::min<int64_t>(512, ceil_div(most, 8192)), p.copy_w ? 2 : 1), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(vocab_top_kernel, dim3((unsigned)std::min<int64_t>(256, ceil_div(most, 16384)), p.copy_w ? 2 : 1), dim3(1024), 0, s, a);
   }
   const int per = p.Kp / 8;
   auto blocks = [&](int64_t rows) { return dim3((unsigned)std::min<int64_t>(4096, std::max<int64_t>(1, ceil_div(rows * per, 256)))); };
