@@ -363,25 +363,29 @@ __global__ __launch_bounds__(256) void muon_start_kernel(MuonGroup G, MuonHyper 
   int64_t at;
   const MuonTensor& T = tensor_of(G, blockIdx.y, at);
   __shared__ double red[4];
+  const bool tall = T.rows > T.cols;
+  const int s0 = (blockIdx.x / tiles_l) * 64, l0 = (blockIdx.x % tiles_l) * 64;
+  const int r0 = tall ? l0 : s0, c0 = tall ? s0 : l0;
+  // the tile and the norm's parts are asked for together (a branch around each load: 10 us of this kernel at any size)
+  float u[16], g[16];
+  const int64_t first = at + min(c0 + (tid & 63), T.cols - 1);
+  auto row = [&](int q) { return first + (int64_t)min(r0 + q * 4 + (tid >> 6), T.rows - 1) * T.cols; };
+#pragma unroll
+  for (int q = 0; q < 16; ++q) u[q] = T.m[row(q)];
+#pragma unroll
+  for (int q = 0; q < 16; ++q) g[q] = h.nesterov ? get<BF>(T.g, row(q)) : 0.f;
+#pragma unroll
+  for (int q = 0; q < 16; ++q) {
+    if (h.nesterov) u[q] = fmaf(h.mu, u[q], g[q]);
+    if (r0 + q * 4 + (tid >> 6) >= T.rows || c0 + (tid & 63) >= T.cols) u[q] = 0.f;
+  }
   double sum = wave_sum(G.norm[(int64_t)blockIdx.y * kNormParts + tid]);
   if ((tid & 63) == 0) red[tid >> 6] = sum;
   __syncthreads();
   sum = red[0] + red[1] + red[2] + red[3];
   const float inv = (float)((double)kX / (sqrt(sum) + (double)h.eps));
-  const bool tall = T.rows > T.cols;
-  const int s0 = (blockIdx.x / tiles_l) * 64, l0 = (blockIdx.x % tiles_l) * 64;
-  const int r0 = tall ? l0 : s0, c0 = tall ? s0 : l0;
-#pragma unroll 8
-  for (int i = tid; i < 64 * 64; i += 256) {
-    const int r = i >> 6, k = i & 63;
-    float u = 0.f;
-    if (r0 + r < T.rows && c0 + k < T.cols) {
-      const int64_t e = at + (int64_t)(r0 + r) * T.cols + c0 + k;
-      const float m = T.m[e];
-      u = h.nesterov ? fmaf(h.mu, m, get<BF>(T.g, e)) : m;
-    }
-    tile[r][k] = u * inv;
-  }
+#pragma unroll
+  for (int q = 0; q < 16; ++q) tile[q * 4 + (tid >> 6)][tid & 63] = u[q] * inv;
   __syncthreads();
   uint16_t* X = G.X[0] + (int64_t)blockIdx.y * NP * G.s * G.lp;
 #pragma unroll
@@ -430,6 +434,7 @@ __device__ __forceinline__ void muon_tile(const MuonGroup& G, const MuonHyper& h
     end([&](int i, int j, int m, int n) { old[j][i] = n < G.s && m < G.sp ? get_parts<NP>(Am + n * la, m) : f4{0, 0, 0, 0}; });
   Pr p;
   p.run(MODE == 4 ? Q : MODE == 1 ? A : X, MODE == 0 || MODE == 4 ? X : MODE == 1 ? A : Q, m0, n0, 0, MODE == 0 ? G.lp : G.sp, (lds_t*)smem);
+  if (Pr::KG > 1 && threadIdx.x >= 64 * Pr::NW) return;
   const int rows = MODE == 4 ? G.l : G.s;
   end([&](int i, int j, int m, int n) {
     if (n >= rows) return;
@@ -496,7 +501,8 @@ hipError_t go(dim3 grid, hipStream_t s, const MuonGroup& G, const MuonHyper& h, 
 
 // The largest tiles that still give every CU one.  Where there is no more than one for each, four steps' tiles are in LDS,
 // else two and more workgroups on a CU (1024 x 1024 fp32, 48 steps of 64 x 64: 23 -> 17 us; four 768 x 2048 bf16, 576 tiles:
-// 25 us with four, 21 with two).
+// 25 us with four, 21 with two).  Of P X over many steps four groups of wavefronts share the contraction (1024 x 1024 fp32:
+// 21.3 -> 15.6 us; the symmetric products, of which only 136 CUs have one, 13.0 -> 16.6, 59 x 3540 bf16 4.0 -> 5.6).
 template <bool BF, int NP, int MODE>
 hipError_t product(const MuonGroup& G, const MuonHyper& h, int from, int mats, hipStream_t s) {
   constexpr Side SA = MODE >= 2 ? COL : ROW;
@@ -505,17 +511,19 @@ hipError_t product(const MuonGroup& G, const MuonHyper& h, int from, int mats, h
     const int64_t m = ceil_div(M, b), n = ceil_div(N, b);
     return (MODE <= 1 ? m * (m + 1) / 2 : m * n) * mats;
   };
-#define KRON_MUON_GO(B, NS, ...)                                                                                    \
+#define KRON_MUON_GO(B, NS, KG, ...)                                                                                \
   {                                                                                                                 \
-    typedef Product<__VA_ARGS__, SA, ROW, false, NP, NS> Pr;                                                        \
-    typedef Product<__VA_ARGS__, ROW, COL, false, NP, NS> PrT;                                                      \
+    typedef Product<__VA_ARGS__, SA, ROW, false, NP, NS, false, KG> Pr;                                             \
+    typedef Product<__VA_ARGS__, ROW, COL, false, NP, NS, false, KG> PrT;                                           \
     const int tm = (int)ceil_div(M, B), tn = (int)ceil_div(N, B);                                                   \
     return go<Pr, muon_product_kernel<Pr, PrT, BF, NP, MODE>>(dim3((unsigned)(tiles(B) / mats), (unsigned)mats), s, G, h, from, tm, tn); \
   }
-  if (tiles(256) >= 256) KRON_MUON_GO(256, 2, 2, 4, 8, 4)
-  if (tiles(128) >= 256) KRON_MUON_GO(128, 2, 2, 2, 4, 4)
-  if (tiles(64) > 256) KRON_MUON_GO(64, 2, 2, 2, 2, 2)
-  KRON_MUON_GO(64, 4, 2, 2, 2, 2)
+  if (tiles(256) >= 256) KRON_MUON_GO(256, 2, 1, 2, 4, 8, 4)
+  if (tiles(128) >= 256) KRON_MUON_GO(128, 2, 1, 2, 2, 4, 4)
+  if (tiles(64) > 256) KRON_MUON_GO(64, 2, 1, 2, 2, 2, 2)
+  if constexpr (MODE >= 2)
+    if (G.sp * NP >= 1024) KRON_MUON_GO(64, 2, 4, 2, 2, 2, 2)
+  KRON_MUON_GO(64, 4, 1, 2, 2, 2, 2)
 #undef KRON_MUON_GO
 }
 

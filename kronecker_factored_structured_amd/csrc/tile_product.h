@@ -157,6 +157,9 @@ __device__ inline u4 fragment(const lds_t* lds, int at, int i, int kk, int lane)
 // they hold the wavefronts up: dW of 768 x 21760 over 8192 rows 303 -> 280 us) and have NS - 1 steps' time.  With two
 // planes a step is 32 products in three parts, lo hi, hi hi and hi lo: each part's fragments serve two of them.
 //
+// KG: as many groups of WM x WN wavefronts share a tile's contraction, each with its own tiles in LDS; the first group has
+// the sums in the end.
+//
 // F32: two "planes" that are fp32 values as they are (ROW, whole rows of 128 bytes), on the fp32 instruction.  The four
 // products of a lane's 16 bytes are of every fourth k, of both operands alike.
 //
@@ -165,13 +168,14 @@ __device__ inline u4 fragment(const lds_t* lds, int at, int i, int kk, int lane)
 // 1,700, reads of LDS alone 4,850.  Measured beside it: 32 x 32 blocks (1,810 out of registers) 1,080-1,150; four
 // wavefronts of 128 x 128 each 1,000; steps of 32 with three to five in LDS 960-1,040; raised wave priority 1,265; reads,
 // loads and products interleaved by hand 1,350.
-template <int WM_, int WN_, int TM_, int TN_, Side SA_, Side SB_, bool BF_, int NP_, int NS_ = 2, bool F32_ = false>
+template <int WM_, int WN_, int TM_, int TN_, Side SA_, Side SB_, bool BF_, int NP_, int NS_ = 2, bool F32_ = false, int KG_ = 1>
 struct Product {
   static constexpr bool F32 = F32_;
+  static constexpr int KG = KG_;
   static constexpr int WM = WM_, WN = WN_, TM = TM_, TN = TN_, NP = NP_, NS = NS_;
-  static constexpr int BM = WM * TM * 16, BN = WN * TN * 16, NW = WM * WN, kThreads = 64 * NW;
+  static constexpr int BM = WM * TM * 16, BN = WN * TN * 16, NW = WM * WN, kThreads = 64 * NW * KG;
   static constexpr int kStage = (BM + BN) * 128, kStep = kBK / NP;
-  static constexpr int kLdsBytes = NS * kStage;
+  static constexpr int kLdsBytes = KG * NS * kStage;
   typedef TileLoad<SA_, BM, NW, NP> LA;
   typedef TileLoad<SB_, BN, NW, NP> LB;
   static constexpr int kLoads = LA::kLoads + LB::kLoads;
@@ -220,14 +224,20 @@ struct Product {
   // Sums over k from k_begin (a multiple of 64) to k_end.  A ROW operand is read up to the next multiple of 64, where
   // either operand is zero; a COL operand's rows beyond its last are that one again.  Ends with a barrier.
   __device__ void run(const Operand& A, const Operand& B, int m0, int n0, int k_begin, int k_end, lds_t* lds) {
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, group = KG > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) / NW : 0;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) - group * NW;
     const int wm = wave % WM, wn = wave / WM;
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int j = 0; j < TN; ++j) acc[i][j] = f4{0, 0, 0, 0};
-    const int total = (k_end - k_begin + kStep - 1) / kStep;
-    if (total <= 0) return;
+    const int all_steps = (k_end - k_begin + kStep - 1) / kStep;
+    if (all_steps <= 0) return;
+    // every group takes part in `most` steps' barriers, and has `total` steps of its own
+    const int most = (all_steps + KG - 1) / KG, total = KG == 1 ? all_steps : min(most, all_steps - group * most);
+    k_begin += group * most * kStep;
+    lds_t* const whole_lds = lds;
+    lds += group * NS * kStage;
     LA la;
     LB lb;
     la.init(A, m0, wave, lane);
@@ -279,15 +289,41 @@ struct Product {
         step(even, std::true_type{});
         step(odd, std::true_type{});
       }
-      for (; t + 1 < total; t += 2) {
-        step(even, std::false_type{});
-        step(odd, std::false_type{});
+      if constexpr (KG == 1) {
+        for (; t + 1 < total; t += 2) {
+          step(even, std::false_type{});
+          step(odd, std::false_type{});
+        }
+        if (t < total) step(even, std::false_type{});
+        __syncthreads();
+      } else {
+        for (; t < most; t += 2) {
+          if (t < total) step(even, std::false_type{});
+          else __builtin_amdgcn_s_barrier();
+          if (t + 1 >= most) break;
+          if (t + 1 < total) step(odd, std::false_type{});
+          else __builtin_amdgcn_s_barrier();
+        }
+        __syncthreads();
+        typedef __attribute__((address_space(3))) f4 lf4;
+        static_assert((KG - 1) * NW * TM * TN * 1024 <= kLdsBytes, "");
+        if (group > 0)
+#pragma unroll
+          for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) *(lf4*)(whole_lds + ((((group - 1) * NW + wave) * TM + i) * TN + j) * 1024 + lane * 16) = acc[i][j];
+        __syncthreads();
+        if (group == 0)
+#pragma unroll
+          for (int q = 0; q < KG - 1; ++q)
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+              for (int j = 0; j < TN; ++j) acc[i][j] += *(const lf4*)(whole_lds + (((q * NW + wave) * TM + i) * TN + j) * 1024 + lane * 16);
       }
-      if (t < total) step(even, std::false_type{});
-      __syncthreads();
       return;
     }
-    static_assert(!F32 || kWhole, "");
+    static_assert((!F32 && KG == 1) || kWhole, "");
     FragsA a0, a1;
     FragsB b0, b1;
     constexpr int first = NP == 2 ? 1 : 0;      // of A's parts
