@@ -558,6 +558,15 @@ __global__ __launch_bounds__(P::kThreads) void vocab_dw_kernel(VocabCE a, int v0
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
   float f, f2;
   dw_factors<BF>(a, f, f2);
+  if constexpr (BF) {
+    if (gridDim.y == 1 && m0 + P::BM <= a.K && a.K % 8 == 0) {      // whole lines
+      store_rows<P>(smem, (uint16_t*)a.dW + (int64_t)(v0 + n0) * a.K + m0, a.K, a.V - v0 - n0, [&](int i, int j) __attribute__((always_inline)) {
+        const f4 s = p.acc[i][j] * f;
+        return uint2{bf16_pair(s[0], s[1]), bf16_pair(s[2], s[3])};
+      });
+      return;
+    }
+  }
 #pragma unroll
   for (int j = 0; j < P::TN; ++j) {
     const int n = n0 + (wave / P::WM) * P::TN * 16 + 16 * j + c;
