@@ -3,8 +3,14 @@
 //   y = base + s_e (x D_e^T) U_e^T
 //   backward, t = s_e x D_e^T and g = s_e dy U_e:  dx = base + g D_e,  dD_e = g^T x,  dU_e = dy^T t
 // Sixteen rows of one request are a workgroup's, or 32 and twice the wavefronts where there are many (D_e and U_e are
-// read once for all of them): their inner product stays on chip, x is read once and y written once.  bf16 x and D_e are multiplied by the bf16 matrix instruction (exact products), everything else by the fp32
-// one: neither the inner products nor the gradients are rounded on the way.
+// read once for all of them): their inner product stays on chip, x is read once and y written once.  bf16 x and D_e are
+// multiplied by the bf16 matrix instruction (exact products), everything else by the fp32 one: neither the inner products
+// nor the gradients are rounded on the way.
+//
+// What bounds it: for few rows a chain of two dependent loads with a join between them (one token of 768 -> 2048 rank 16
+// 5.1 us, 64 tokens of 1024 -> 4096 8.1), for many the reading of x and base and the writing of y in turn (8192 rows of
+// 1024 -> 1024 rank 24 fp32: 39.7 us, 2.5 TB/s; matrix cores busy 0.26).  Backward of 8192 rows of 768 -> 2048 rank 16 bf16:
+// the rows' kernel 29.5 us, the parameters' 27.7.
 #include <algorithm>
 
 #include "kron_internal.h"

