@@ -212,10 +212,17 @@ __device__ inline void inner(const Adapters& a, const Tile& T, const void* v, co
   join<RT, RB>(a, acc, f, red, t);
 }
 
-// g = f v w for w (n x R): w's values one by one, sixteen neighbours of a row together.
+// Blocks of the contraction that inner_t has in flight.
+template <bool BF>
+constexpr int turned(int RT) { return RT >= 4 ? 1 : (BF ? 4 : 8) / RT; }
+
+// g = f v w for w (n x R).  fp32: w's values one by one, sixteen neighbours of a row together.  bf16: 32 rows of w and
+// sixteen columns go through a KB of the wavefront's LDS, whose transposing reads give the columns their rows, eight neighbours
+// of the contraction as the bf16 instruction takes them (8192 rows of
+// 768 -> 2048, one value a lane's load: 29.5 us of the rows' kernel, so 23).
 template <bool BF, int RT, int RB>
 __device__ inline void inner_t(const Adapters& a, const Tile& T, const void* v, const void* w, int n, float f, float* red, float* t) {
-  constexpr int KB = BF ? 32 : 16, VE = BF ? 8 : 4, NW = kWaves * RB, kBatch = RT >= 4 ? 1 : (BF ? 4 : 8) / RT;
+  constexpr int KB = BF ? 32 : 16, VE = BF ? 8 : 4, NW = kWaves * RB, kBatch = turned<BF>(RT);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
   f4 acc[RB][RT];
   int64_t vrow[RB];
@@ -227,26 +234,64 @@ __device__ inline void inner_t(const Adapters& a, const Tile& T, const void* v, 
   }
   for (int k = wave * KB; k < n; k += kBatch * NW * KB) {
     u4 x[kBatch][RB];
-    float u[kBatch][RT][VE];
+    if constexpr (BF) {
+      typedef short s4 __attribute__((ext_vector_type(4)));
+      typedef __attribute__((address_space(3))) char lds;
+      typedef __attribute__((address_space(3))) s4 lds4;
+      lds* mine = (lds*)(char*)red + wave * (kBatch * RT * 1024);      // (Shared's KB)
+      u4 u[kBatch][RT];
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const int at = k + b * NW * KB + VE * g;
+      for (int b = 0; b < kBatch; ++b) {
+        const int k0 = k + b * NW * KB, at = k0 + VE * g, m = k0 + (lane >> 1);
 #pragma unroll
-      for (int y = 0; y < RB; ++y) x[b][y] = load16<BF>(v, vrow[y] + at, n - at);
+        for (int y = 0; y < RB; ++y) x[b][y] = load16<BF>(v, vrow[y] + at, n - at);
 #pragma unroll
-      for (int i = 0; i < RT; ++i)
+        for (int i = 0; i < RT; ++i) {
+          const int r = 16 * i + 8 * (lane & 1);
+          u[b][i] = load16<BF>(w, (int64_t)m * a.R + r, m < n ? a.R - r : 0);
+        }
+      }
 #pragma unroll
-        for (int q = 0; q < VE; ++q) u[b][i][q] = load1<BF>(w, (int64_t)min(at + q, n - 1) * a.R + min(16 * i + c, a.R - 1));
+      for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+        for (int i = 0; i < RT; ++i) *(__attribute__((address_space(3))) u4*)(mine + (b * RT + i) * 1024 + lane * 16) = u[b][i];
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          lds* q = mine + (b * RT + i) * 1024 + (8 * g + (c >> 2)) * 32 + (c & 3) * 8;
+          union { s4 h[2]; u4 u; } o;
+          o.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)q);
+          o.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(q + 128));
+#pragma unroll
+          for (int y = 0; y < RB; ++y) acc[y][i] = mma16(x[b][y], o.u, acc[y][i]);
+        }
+      asm volatile("" ::: "memory");
+    } else {
+      float u[kBatch][RT][VE];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int at = k + b * NW * KB + VE * g;
+#pragma unroll
+        for (int y = 0; y < RB; ++y) x[b][y] = load16<BF>(v, vrow[y] + at, n - at);
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+          for (int q = 0; q < VE; ++q) u[b][i][q] = load1<BF>(w, (int64_t)min(at + q, n - 1) * a.R + min(16 * i + c, a.R - 1));
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+        for (int q = 0; q < VE; ++q)
+#pragma unroll
+          for (int y = 0; y < RB; ++y)
+#pragma unroll
+            for (int i = 0; i < RT; ++i) acc[y][i] = mma32(value<BF>(x[b][y], q), u[b][i][q], acc[y][i]);
     }
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b)
-#pragma unroll
-      for (int q = 0; q < VE; ++q)
-#pragma unroll
-        for (int y = 0; y < RB; ++y)
-#pragma unroll
-          for (int i = 0; i < RT; ++i) acc[y][i] = mma32(value<BF>(x[b][y], q), u[b][i][q], acc[y][i]);
   }
+  // (all have read what join writes over)
+  __syncthreads();
   join<RT, RB>(a, acc, f, red, t);
 }
 
@@ -272,9 +317,10 @@ __device__ inline void plain_rows(const Adapters& a, const Tile& T, const void* 
   }
 }
 
-template <int RT, int RB>
+// KB: of w's rows that inner_t turns, for each wavefront.
+template <int RT, int RB, int KB = 0>
 struct Shared {
-  float red[kWaves * RB * RB * RT * 256];
+  float red[kWaves * RB * (KB > RB * RT ? KB : RB * RT) * 256];
   float t[16 * RB * (RT * 16 + 4)];
   float g[16 * RB * (RT * 16 + 4)];
   int find[kWaves * RB + 2];
@@ -350,7 +396,7 @@ __global__ __launch_bounds__(RB * kThreads) void adapters_fwd_kernel(Adapters a)
 // The rows' part of the backward: t and g of each row for the gradients' kernel, and dx.
 template <bool BF, int RT, int RB>
 __global__ __launch_bounds__(RB * kThreads) void adapters_rows_kernel(Adapters a) {
-  __shared__ Shared<RT, RB> sh;
+  __shared__ Shared<RT, RB, BF ? turned<BF>(RT) * RT : 0> sh;
   const Tile T = find_tile<RB>(a, blockIdx.x, sh.find);
   if (T.rows == 0) return;
   if (T.id < 0 || T.id >= a.E) {
