@@ -10,7 +10,7 @@
 // What bounds it: for few rows a chain of two dependent loads with a join between them (one token of 768 -> 2048 rank 16
 // 5.1 us, 64 tokens of 1024 -> 4096 8.1), for many the reading of x and base and the writing of y in turn (8192 rows of
 // 1024 -> 1024 rank 24 fp32: 39.7 us, 2.5 TB/s; matrix cores busy 0.26).  Backward of 8192 rows of 768 -> 2048 rank 16 bf16:
-// the rows' kernel 29.5 us, the parameters' 27.7.
+// the rows' kernel 23.5 us, the parameters' 27.7 (x and dy once more, in 352 workgroups of unlike many rows).
 #include <algorithm>
 
 #include "kron_internal.h"
@@ -520,7 +520,7 @@ int rank_blocks(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8; }
 
 // Tiles of 32 rows where two of sixteen would be on every CU anyway, in bf16 (8192 x (768 -> 2048): rank 16 23.3 -> 21.9 us,
 // rank 64 47 -> 41; else two workgroups' phases overlap better than one's: fp32 1024 -> 1024 of rank 24 39 us against 42,
-// the rows' backward of rank 16 30 us against 34).
+// the rows' backward of rank 16 23.5 us against 28).
 bool wide(const Adapters& a, bool backward) { return a.bf16 && a.N >= 8192 && a.starts && a.R <= 64 && (a.R > 16 || !backward); }
 int64_t tiles_of(const Adapters& a, int RB) { return a.starts ? ceil_div(a.N, 16 * RB) + a.B + 1 : a.N; }
 
