@@ -239,6 +239,24 @@ def test_many_rows_against_blocks_of_them():
     assert bool(((nll.double() - torch.cat(parts).double()).abs() <= 2 * eps).all())
 
 
+def test_equal_weights_are_not_rounded():
+    """bf16: weights of 1 / N each, and none at all, give the same gradients, and so do weights of any size but for their
+    size: what is rounded to bf16 is (softmax - [label]) over the largest weight, the same in all three.  c dW is then off
+    from c times dW by the last roundings alone, half a step of each."""
+    k = K()
+    N = 300
+    h, W, lab, _ = case(13, N, 64, 700, torch.bfloat16)
+    g = torch.ones(1, device="cuda")
+    outs = []
+    for w in (None, torch.full((N,), 1 / N, device="cuda"), torch.full((N,), 0.77, device="cuda")):
+        _, _, stats = k.kron_vocab_ce_fwd(h, W, lab, weights=w)
+        outs.append(k.kron_vocab_ce_bwd(h, W, lab, stats, g, weights=w))
+    for key in ("dh", "dW"):
+        assert torch.equal(outs[0][key], outs[1][key])
+        a, b = outs[0][key].double() * (0.77 * N), outs[2][key].double()
+        assert bool(((a - b).abs() <= (2.0 ** -8 + 8 * u) * (a.abs() + b.abs())).all())
+
+
 def test_binding_refuses():
     k = K()
     h, W, lab, w = case(12, 10, 8, 20, torch.float32, 0.2)
