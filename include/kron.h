@@ -568,15 +568,19 @@ kron_status_t kron_adapters_bwd(const kron_adapters_t* d, const void* x, const v
  * param and grad are fp32 or bf16 (dtype), m fp32.  All arguments but the device pointers in params,
  * grads and m are read from the host.  scale may be NULL (1).  A matrix of zeros stays zero (X = 0); one with
  * a non-finite value becomes non-finite and no other does.
- * Sums are fp32, norms fp64.  fp32: products of matrices that do not fit a CU's LDS take their operands as two
- * fp16 parts each (off by at most 2^-22 of the value, or 2^-38, of matrices whose entries are at most 3.5).
- * bf16: as one fp16 part (2^-11).
+ * Sums are fp32, norms fp64.  fp32: products of matrices that do not fit a CU's LDS (smaller side over 64, or over
+ * 156 KB) take their operands as two fp16 parts each: off by at most 2^-22 of the value, or 2^-38 (2^-40 of what a
+ * singular value can become, where that is more).  bf16: as one fp16 part (2^-11).  Their scales follow from a, b and c: with
+ * p(l) = a + b l + c l^2 the largest singular value goes from at most 1 to at most max |v p(v^2)| over those so far, in each
+ * step; where it, but for the last step's, or |p| passes KRON_MUON_MAX_GROWTH the call is refused (KRON_E_UNSUPPORTED) if
+ * it has such a matrix.
  * Limits: ntensors <= 4096, 1 <= rows, cols <= KRON_MUON_MAX_SIDE, count <= 2^20 (0: skipped),
  * 1 <= steps <= KRON_MUON_MAX_STEPS, momentum >= 0, eps > 0 (all finite, eps no less than fp32 holds).  Tensors must not overlap.  The workspace
  * is kron_muon_workspace_bytes(...) bytes, 256-byte aligned (0: none is needed, or rejected sizes).
  */
 #define KRON_MUON_MAX_SIDE 16384
 #define KRON_MUON_MAX_STEPS 16
+#define KRON_MUON_MAX_GROWTH 1024
 typedef struct {
   double lr, momentum, weight_decay, a, b, c, eps;
   int32_t nesterov, steps;

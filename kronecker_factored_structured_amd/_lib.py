@@ -47,6 +47,7 @@ KRON_ADAPTERS_MAX_RANK = 128
 KRON_ADAPTERS_MAX_REQUESTS = 65536
 KRON_MUON_MAX_SIDE = 16384
 KRON_MUON_MAX_STEPS = 16
+KRON_MUON_MAX_GROWTH = 1024
 
 # Every symbol include/kron.h declares.
 EXPORTS = (

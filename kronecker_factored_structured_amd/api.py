@@ -853,7 +853,8 @@ def kron_muon_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor]
     """One orthogonalised (Muon) update of every tensor, in place: the last two dimensions of a tensor are matrices, each
     on its own.  m = momentum m + g; u = g + momentum m (nesterov) or m; u / (|u|_F + eps) goes through `steps`
     Newton-Schulz steps of the quintic `coeffs`; param = param (1 - lr weight_decay) - lr scales[t] u.  params and grads
-    are all float32 or all bfloat16, m float32.  scales None: sqrt(max(1, rows / cols)) of each tensor."""
+    are all float32 or all bfloat16, m float32.  scales None: sqrt(max(1, rows / cols)) of each tensor.  Coefficients that
+    can take a singular value beyond KRON_MUON_MAX_GROWTH are refused where a matrix does not fit a CU's LDS."""
     nt = len(params)
     if not (len(grads) == len(m) == nt) or (scales is not None and len(scales) != nt):
         raise ValueError("params, grads, m (and scales) must have the same length")

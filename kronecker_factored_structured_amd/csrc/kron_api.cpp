@@ -1300,7 +1300,11 @@ kron_status_t kron_muon_step(const kron_muon_t* h, int32_t ntensors, int32_t dty
     hp.lr = (float)h->lr; hp.mu = (float)h->momentum; hp.keep = (float)(1.0 - h->lr * h->weight_decay);
     hp.a = (float)h->a; hp.b = (float)h->b; hp.c = (float)h->c; hp.eps = (float)h->eps;
     hp.nesterov = h->nesterov != 0; hp.steps = h->steps; hp.bf16 = dtype == KRON_BF16;
-    const hipError_t e = kron::launch_muon(t.data(), ntensors, hp, workspace, stream);
+    kron::MuonScales scales[KRON_MUON_MAX_STEPS];
+    if (need > 0 && !kron::muon_scales(hp, scales))
+      return fail(KRON_E_UNSUPPORTED, "a = %g, b = %g, c = %g take a singular value of 1 beyond %d in %d steps, for a matrix that does not fit LDS",
+                  h->a, h->b, h->c, KRON_MUON_MAX_GROWTH, h->steps);
+    const hipError_t e = kron::launch_muon(t.data(), ntensors, hp, scales, workspace, stream);
     if (e != hipSuccess) return hip_fail(e, "kron_muon_step launch");
   } catch (...) {
     return fail(KRON_E_ARG, "out of host memory");

@@ -389,8 +389,14 @@ struct MuonHyper {
   float a, b, c, eps;
   int32_t nesterov, steps, bf16;
 };
+// Scales of a step's 16-bit parts: of X, A, P and the next step's X.
+struct MuonScales {
+  float x, a, p, next;
+};
 size_t muon_workspace(const MuonTensor* t, int n, bool bf16);
-hipError_t launch_muon(const MuonTensor* t, int n, const MuonHyper& h, void* ws, hipStream_t s);
+// Every step's scales (h.steps of them); false where the coefficients take a value beyond KRON_MUON_MAX_GROWTH.
+bool muon_scales(const MuonHyper& h, MuonScales* k);
+hipError_t launch_muon(const MuonTensor* t, int n, const MuonHyper& h, const MuonScales* k, void* ws, hipStream_t s);
 
 // ---------------------------------------------------------------------------------
 // Low-rank adapters of many requests (adapters.hip).

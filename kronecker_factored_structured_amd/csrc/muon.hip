@@ -11,6 +11,7 @@
 // 1024 x 1024 fp32 fifteen dependent products of 11.6 to 15.5 us (6.4 GFLOP of parts each for P X: 410 TFLOP/s), their tiles'
 // loads out of L2 at 6 TB/s.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 #include <utility>
 #include <vector>
@@ -281,8 +282,9 @@ __global__ __launch_bounds__(NT) void muon_small_kernel(SmallBatch batch, MuonHy
 // ------------------------------------------------------------------------------ large matrices
 constexpr int kGroup = 40;           // tensors of one size in a launch
 constexpr int kNormParts = 256;      // workgroups of a matrix's norm
-// Scales of the parts: |X| <= 1.3, |A| <= 1.7 and |P| <= 3.5 stay below fp16's 65504, and small entries keep their bits
-constexpr float kX = 8192.f, kA = 8192.f, kP = 8192.f;
+// Scales of the parts, powers of two: what a step's X, A and P can be (muon_scales) stays below fp16's 65504, and small
+// entries keep their bits.  Of the default quintic |X| <= 1.3, |A| <= 1.6 and |P| <= 3.5: all three are kScale.
+constexpr float kScale = 8192.f;
 
 struct MuonGroup {
   MuonTensor t[kGroup];
@@ -387,7 +389,7 @@ __global__ __launch_bounds__(256) void muon_start_kernel(MuonGroup G, MuonHyper 
   if ((tid & 63) == 0) red[tid >> 6] = sum;
   __syncthreads();
   sum = red[0] + red[1] + red[2] + red[3];
-  const float inv = (float)((double)kX / (sqrt(sum) + (double)h.eps));
+  const float inv = (float)((double)kScale / (sqrt(sum) + (double)h.eps));
 #pragma unroll
   for (int q = 0; q < 16; ++q) tile[q * 4 + (tid >> 6)][tid & 63] = u[q] * inv;
   __syncthreads();
@@ -405,8 +407,8 @@ __global__ __launch_bounds__(256) void muon_start_kernel(MuonGroup G, MuonHyper 
 // matrices; 4: into the tall ones' (turned: lanes hold neighbours of a row of the parameters in both).
 // A and P are symmetric: their tiles on and below the diagonal are computed (tm: tiles of a side) and written twice.
 template <class Pr, bool BF, int NP, int MODE>
-__device__ __forceinline__ void muon_tile(const MuonGroup& G, const MuonHyper& h, const MuonTensor& T, int64_t at, int from, int tm, int tn,
-                                          char* smem) {
+__device__ __forceinline__ void muon_tile(const MuonGroup& G, const MuonHyper& h, const MuonScales& k, const MuonTensor& T, int64_t at, int from,
+                                          int tm, int tn, char* smem) {
   int mt, nt;
   if constexpr (MODE <= 1) {
     static_assert(Pr::BM == Pr::BN, "");
@@ -446,15 +448,15 @@ __device__ __forceinline__ void muon_tile(const MuonGroup& G, const MuonHyper& h
     if constexpr (MODE <= 1) {
       if (m >= G.sp) return;
       if constexpr (MODE == 0) {
-        v = v * (kA / (kX * kX));
+        v = v * (k.a / (k.x * k.x));
       } else {
         f4 a1;
         if constexpr (early) a1 = old[j][i];
         else a1 = get_parts<NP>(Am + n * la, m);
-        v = v * (h.c * kP / (kA * kA)) + a1 * (h.b * kP / kA);
+        v = v * (h.c * k.p / (k.a * k.a)) + a1 * (h.b * k.p / k.a);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (m + e == n) v[e] += h.a * kP;
+          if (m + e == n) v[e] += h.a * k.p;
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e)
@@ -464,10 +466,10 @@ __device__ __forceinline__ void muon_tile(const MuonGroup& G, const MuonHyper& h
       if (mt != nt) put_parts_turned<NP>(out + m * la, la, G.s - m, n, v);
     } else if constexpr (MODE == 2) {
       if (m >= G.lp) return;
-      put_parts<NP>(G.X[from ^ 1] + ((int64_t)mat * G.s + n) * lx, m, v * (1.f / kP));
+      put_parts<NP>(G.X[from ^ 1] + ((int64_t)mat * G.s + n) * lx, m, v * (k.next / (k.p * k.x)));
     } else {
       const int cols = MODE == 4 ? G.s : G.l;
-      const float f = h.lr * T.scale * (1.f / (kP * kX));
+      const float f = h.lr * T.scale * (1.f / (k.p * k.x));
       const int64_t o = at + (int64_t)n * cols + m;
       if ((cols & 3) == 0) {
         float w[4];
@@ -487,19 +489,19 @@ __device__ __forceinline__ void muon_tile(const MuonGroup& G, const MuonHyper& h
 
 // Pr; the tall matrices' last product is PrT, of as many tiles the other way round.
 template <class Pr, class PrT, bool BF, int NP, int MODE>
-__global__ __launch_bounds__(Pr::kThreads) void muon_product_kernel(MuonGroup G, MuonHyper h, int from, int tm, int tn) {
+__global__ __launch_bounds__(Pr::kThreads) void muon_product_kernel(MuonGroup G, MuonHyper h, MuonScales k, int from, int tm, int tn) {
   extern __shared__ char smem[];
   int64_t at;
   const MuonTensor& T = tensor_of(G, blockIdx.y, at);
-  if (MODE == 3 && T.rows > T.cols) muon_tile<PrT, BF, NP, 4>(G, h, T, at, from, tn, tm, smem);
-  else muon_tile<Pr, BF, NP, MODE>(G, h, T, at, from, tm, tn, smem);
+  if (MODE == 3 && T.rows > T.cols) muon_tile<PrT, BF, NP, 4>(G, h, k, T, at, from, tn, tm, smem);
+  else muon_tile<Pr, BF, NP, MODE>(G, h, k, T, at, from, tm, tn, smem);
 }
 
 template <class Pr, auto kernel>
-hipError_t go(dim3 grid, hipStream_t s, const MuonGroup& G, const MuonHyper& h, int from, int tm, int tn) {
+hipError_t go(dim3 grid, hipStream_t s, const MuonGroup& G, const MuonHyper& h, const MuonScales& k, int from, int tm, int tn) {
   const hipError_t e = allow_lds<kernel>();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kernel, grid, dim3(Pr::kThreads), Pr::kLdsBytes, s, G, h, from, tm, tn);
+  hipLaunchKernelGGL(kernel, grid, dim3(Pr::kThreads), Pr::kLdsBytes, s, G, h, k, from, tm, tn);
   return hipGetLastError();
 }
 
@@ -508,7 +510,7 @@ hipError_t go(dim3 grid, hipStream_t s, const MuonGroup& G, const MuonHyper& h, 
 // 25 us with four, 21 with two).  Of P X over many steps four groups of wavefronts share the contraction (1024 x 1024 fp32:
 // 21.3 -> 15.6 us; the symmetric products, of which only 136 CUs have one, 13.0 -> 16.6, 59 x 3540 bf16 4.0 -> 5.6).
 template <bool BF, int NP, int MODE>
-hipError_t product(const MuonGroup& G, const MuonHyper& h, int from, int mats, hipStream_t s) {
+hipError_t product(const MuonGroup& G, const MuonHyper& h, const MuonScales& k, int from, int mats, hipStream_t s) {
   constexpr Side SA = MODE >= 2 ? COL : ROW;
   const int M = MODE >= 2 ? G.lp : G.sp, N = G.s;
   auto tiles = [&](int b) {
@@ -520,7 +522,7 @@ hipError_t product(const MuonGroup& G, const MuonHyper& h, int from, int mats, h
     typedef Product<__VA_ARGS__, SA, ROW, false, NP, NS, false, KG> Pr;                                             \
     typedef Product<__VA_ARGS__, ROW, COL, false, NP, NS, false, KG> PrT;                                           \
     const int tm = (int)ceil_div(M, B), tn = (int)ceil_div(N, B);                                                   \
-    return go<Pr, muon_product_kernel<Pr, PrT, BF, NP, MODE>>(dim3((unsigned)(tiles(B) / mats), (unsigned)mats), s, G, h, from, tm, tn); \
+    return go<Pr, muon_product_kernel<Pr, PrT, BF, NP, MODE>>(dim3((unsigned)(tiles(B) / mats), (unsigned)mats), s, G, h, k, from, tm, tn); \
   }
   if (tiles(256) >= 256) KRON_MUON_GO(256, 2, 1, 2, 4, 8, 4)
   if (tiles(128) >= 256) KRON_MUON_GO(128, 2, 1, 2, 2, 4, 4)
@@ -532,7 +534,7 @@ hipError_t product(const MuonGroup& G, const MuonHyper& h, int from, int mats, h
 }
 
 template <bool BF>
-hipError_t run_group(const MuonGroup& G, const MuonHyper& h, int mats, hipStream_t s) {
+hipError_t run_group(const MuonGroup& G, const MuonHyper& h, const MuonScales* k, int mats, hipStream_t s) {
   constexpr int NP = BF ? 1 : 2;
   const dim3 grid(kNormParts, (unsigned)mats);
   // (a matrix starts at a multiple of four values where all have as many)
@@ -542,9 +544,9 @@ hipError_t run_group(const MuonGroup& G, const MuonHyper& h, int mats, hipStream
   hipLaunchKernelGGL((muon_start_kernel<BF, NP>), dim3((unsigned)(tl * ts), (unsigned)mats), dim3(256), 0, s, G, h, tl);
   hipError_t e = hipGetLastError();
   for (int i = 0; i < h.steps && e == hipSuccess; ++i) {
-    e = product<BF, NP, 0>(G, h, i & 1, mats, s);
-    if (e == hipSuccess) e = product<BF, NP, 1>(G, h, i & 1, mats, s);
-    if (e == hipSuccess) e = i + 1 < h.steps ? product<BF, NP, 2>(G, h, i & 1, mats, s) : product<BF, NP, 3>(G, h, i & 1, mats, s);
+    e = product<BF, NP, 0>(G, h, k[i], i & 1, mats, s);
+    if (e == hipSuccess) e = product<BF, NP, 1>(G, h, k[i], i & 1, mats, s);
+    if (e == hipSuccess) e = i + 1 < h.steps ? product<BF, NP, 2>(G, h, k[i], i & 1, mats, s) : product<BF, NP, 3>(G, h, k[i], i & 1, mats, s);
   }
   return e;
 }
@@ -618,6 +620,7 @@ struct RunGroup {
   bool bf16;
   int element() const { return bf16 ? 2 : 4; }
   const MuonHyper* h;
+  const MuonScales* k;
   char* ws;
   hipStream_t stream;
   hipError_t operator()(int s, int l, const MuonTensor* t, int n, int64_t mats) const {
@@ -628,7 +631,7 @@ struct RunGroup {
       G.t[i] = t[i];
       G.first[i + 1] = G.first[i] + (int)t[i].count;
     }
-    return bf16 ? run_group<true>(G, *h, (int)mats, stream) : run_group<false>(G, *h, (int)mats, stream);
+    return bf16 ? run_group<true>(G, *h, k, (int)mats, stream) : run_group<false>(G, *h, k, (int)mats, stream);
   }
 };
 
@@ -654,7 +657,39 @@ size_t muon_workspace(const MuonTensor* t, int n, bool bf16) {
   return most;
 }
 
-hipError_t launch_muon(const MuonTensor* t, int n, const MuonHyper& h, void* ws, hipStream_t s) {
+// The singular values of X are at most 1 at first; a step takes v to v p(v^2), p(l) = a + b l + c l^2, and the values of a
+// matrix are at most its largest singular value.  What 16-bit parts leave of A and P (2^-11 at most) comes on top.
+bool muon_scales(const MuonHyper& h, MuonScales* k) {
+  const double a = h.a, b = h.b, c = h.c;
+  auto scale = [](double most) {
+    return most * kScale <= 49152 ? kScale : (float)std::exp2(std::floor(std::log2(49152 / most)));
+  };
+  double x = 1;      // of X
+  for (int i = 0; i < h.steps; ++i) {
+    const double top = x * x * (1 + 1.0 / 64);      // of A
+    const double off = (std::abs(a) + std::abs(b) * top + std::abs(c) * top * top) / 512;
+    double p = 0, next = 0;
+    auto at = [&](double l) {
+      if (!(l >= 0 && l <= top)) return;
+      const double v = std::abs(a + l * (b + l * c)) + off;
+      p = std::max(p, v), next = std::max(next, std::sqrt(l) * v);
+    };
+    at(0), at(top);
+    if (c != 0) {
+      at(-b / (2 * c));      // where p and v p(v^2) turn
+      const double d = 9 * b * b - 20 * a * c;
+      if (d >= 0) at((-3 * b + std::sqrt(d)) / (10 * c)), at((-3 * b - std::sqrt(d)) / (10 * c));
+    } else if (b != 0) {
+      at(-a / (3 * b));
+    }
+    if (!(x <= KRON_MUON_MAX_GROWTH && p <= KRON_MUON_MAX_GROWTH)) return false;
+    k[i] = MuonScales{scale(x), scale(top), scale(p), scale(next)};
+    x = next;
+  }
+  return true;
+}
+
+hipError_t launch_muon(const MuonTensor* t, int n, const MuonHyper& h, const MuonScales* k, void* ws, hipStream_t s) {
   // Workgroups of 16 wavefronts where a matrix has over 8192 values or more than three tiles of A, of eight else, and more
   // of them on a CU.
   for (int large = 0; large < 2; ++large) {
@@ -680,7 +715,7 @@ hipError_t launch_muon(const MuonTensor* t, int n, const MuonHyper& h, void* ws,
     const hipError_t e = flush();
     if (e != hipSuccess) return e;
   }
-  return for_groups(t, n, RunGroup{h.bf16 != 0, &h, (char*)ws, s});
+  return for_groups(t, n, RunGroup{h.bf16 != 0, &h, k, (char*)ws, s});
 }
 
 }  // namespace kron

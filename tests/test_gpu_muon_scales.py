@@ -1,0 +1,103 @@
+"""kron_muon_step where the default coefficients' bounds do not hold: other quintics, and matrices that grow or shrink from step to
+step.
+
+Tolerances as in test_gpu_muon.py: the error of X, as a Frobenius norm, may be four times what plain arithmetic of the same
+precision leaves on the same inputs (fp32, or operands rounded to fp16's eleven bits), and at least sixteen roundings of X;
+then the parameter's own rounding.  `half` rounds to eleven bits whatever the matrix's size."""
+import numpy as np
+import pytest
+
+from oracle import muon as OM
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+u = 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _needs_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def K():
+    import kronecker_factored_structured_amd as k
+    return k
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def half(v):
+    """Rounded to eleven bits, over the largest value as the kernels' scales have it."""
+    up = 2.0 ** (12 - np.frexp(np.abs(v).max())[1]) if np.abs(v).max() > 0 else 1.0
+    return (v * up).astype(np.float16).astype(v.dtype) / v.dtype.type(up)
+
+
+def tensors(seed, shape, dtype):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda s: torch.randn(shape, generator=g) * s
+    return r(1.0).to(dtype).cuda(), r(0.01).to(dtype).cuda(), r(0.05).cuda()
+
+
+def compare(shape, dtype, coeffs, steps, lr=0.1, seed=0):
+    k = K()
+    W, G, m = tensors(seed + sum(shape), shape, dtype)
+    before = [f64(t).reshape(-1, *shape[-2:]) for t in (W, G, m)]
+    k.kron_muon_step([W], [G], [m], lr=lr, coeffs=coeffs, steps=steps, scales=[1.0])
+    bf = dtype == torch.bfloat16
+    got = f64(W).reshape(-1, *shape[-2:])
+    for j, (w, g, mo) in enumerate(zip(*before)):
+        kw = dict(steps=steps, coeffs=coeffs)
+        want, _, o = OM.step(w, g, mo, lr, **kw)
+        _, _, plain = OM.step(w, g, mo, lr, dtype=np.float32, part=half if bf else (lambda v: v), **kw)
+        err = max(4 * np.linalg.norm(plain - o), 16 * (2.0 ** -11 if bf else u) * np.linalg.norm(o))
+        r = 2.0 ** -8 if bf else 3 * u
+        off = np.abs(got[j] - want) - r * (np.abs(want) + np.abs(w))
+        assert np.linalg.norm(np.maximum(off, 0)) <= lr * err, (shape, j, np.linalg.norm(o))
+
+
+# a cubic and quintics that stay next to 1, a steep one of one step, ones that make every singular value larger or smaller
+QUINTICS = [((1.5, -0.5, 0.0), 5), ((1.875, -1.25, 0.375), 6), ((8.28721201814563, -23.595886519098837, 17.300387312530933), 1),
+            ((4.0, -6.0, 2.5), 3), ((2.0, 0.0, 0.0), 10), ((15.0, 0.0, 0.0), 1), ((1000.0, 0.0, 0.0), 1), ((12.0, -20.0, 9.0), 1),
+            ((0.5, 0.0, 0.0), 6), ((-2.0, 1.5, -0.5), 5), ((0.0, 0.0, 900.0), 1)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shape", [(20, 30), (90, 80), (80, 300), (2, 200, 70)])
+@pytest.mark.parametrize("coeffs,steps", QUINTICS)
+def test_other_quintics(coeffs, steps, shape, dtype):
+    """Coefficients for which P, A or X leave fp16's range at the default's scale, on matrices that fit LDS and that do not."""
+    compare(shape, dtype, coeffs, steps)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shape", [(20, 30), (90, 80)])
+def test_rank_one_grows(shape, dtype):
+    """The gradient of one sample: a singular value of 1, and the bound itself is reached."""
+    k = K()
+    g = torch.Generator().manual_seed(1)
+    G = (torch.randn(shape[0], 1, generator=g) @ torch.randn(1, shape[1], generator=g)).to(dtype).cuda()
+    for coeffs, steps in (((2.0, 0.0, 0.0), 10), ((8.0, -4.0, 1.0), 2), ((1000.0, 0.0, 0.0), 1), ((1.0, 1.0, 1.0), 2)):
+        W, m = torch.zeros_like(G), torch.zeros(shape, device="cuda")
+        k.kron_muon_step([W], [G], [m], lr=1.0, coeffs=coeffs, steps=steps, scales=[1.0], nesterov=False)
+        o = OM.orthogonalise(f64(G), steps=steps, coeffs=coeffs)
+        # P's roundings and the products', each relative to P's and X's bound: steps of at most sixteen (eight at 2^-11)
+        tol = (8 * 2.0 ** -11 + 2.0 ** -8 if dtype == torch.bfloat16 else 32 * u) * steps * np.linalg.norm(o)
+        assert np.linalg.norm(f64(W) + o) <= tol, (coeffs, steps)
+
+
+def test_growth_beyond_the_limit_is_refused():
+    """Matrices that do not fit LDS are held in 16-bit parts: a quintic that takes a singular value beyond what these
+    hold is refused for them, before anything is launched; in LDS it is fp32 and runs."""
+    k = K()
+    from kronecker_factored_structured_amd._lib import KronError
+    for coeffs, steps in (((8.28721201814563, -23.595886519098837, 17.300387312530933), 5), ((1e6, 0.0, 0.0), 1), ((2.0, 0.0, 0.0), 16),
+                          ((1e38, 1e38, 1e38), 16), ((0.0, 0.0, -1e5), 2)):
+        W, G, m = tensors(3, (80, 90), torch.float32)
+        keep = [W.clone(), m.clone()]
+        with pytest.raises(KronError):
+            k.kron_muon_step([W], [G], [m], lr=0.1, coeffs=coeffs, steps=steps)
+        assert torch.equal(W, keep[0]) and torch.equal(m, keep[1])
+    compare((20, 30), torch.float32, (2.0, 0.0, 0.0), 16)

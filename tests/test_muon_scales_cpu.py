@@ -1,0 +1,18 @@
+"""Refusals of coefficients whose update would leave the range of the tiled products' 16-bit parts (CPU only: nothing is
+launched)."""
+import pytest
+
+from kronecker_factored_structured_amd import _lib
+from test_finetune_cpu import MB, P, muon
+
+BIG = ((P(), P(MB), P(2 * MB), 1, 128, 128),)      # does not fit LDS
+STEEP = dict(a=8.28721201814563, b=-23.595886519098837, c=17.300387312530933)
+
+
+@pytest.mark.parametrize("kw", [dict(STEEP, steps=5), dict(a=1025.0, b=0.0, c=0.0, steps=1), dict(a=2.0, b=0.0, c=0.0, steps=12),
+                                dict(a=1e38, b=1e38, c=1e38, steps=16), dict(a=0.0, b=0.0, c=-1e5, steps=2), dict(a=0.0, b=2000.0, c=0.0, steps=1)])
+def test_growth_is_refused(kw):
+    assert muon(tensors=BIG, **kw) == _lib.KRON_E_UNSUPPORTED, _lib.last_error()
+    assert "singular value" in _lib.last_error()
+    # (what is wrong whatever the coefficients are comes first)
+    assert muon(tensors=BIG, ws=None, **kw) == _lib.KRON_E_WORKSPACE
