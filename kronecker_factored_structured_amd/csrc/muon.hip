@@ -62,6 +62,9 @@ __device__ inline void momentum(const MuonHyper& h, const float (&g)[N], float (
     u[e] = h.nesterov ? fmaf(h.mu, m[e], g[e]) : m[e];
   }
 }
+// Whether fp32 holds a factor with all its bits: with the smallest eps, zeros' is infinite there, and that of gradients next
+// to either end of the range is infinite or has few bits.  64 bits do then.
+__device__ inline bool in_range(float v) { return v >= 0x1p-126f && v < INFINITY; }
 template <bool BF>
 __device__ inline void put(void* p, int64_t i, float v) {
   if (BF) ((uint16_t*)p)[i] = (uint16_t)bf16_rne(v);
@@ -249,7 +252,13 @@ __global__ __launch_bounds__(NT) void muon_small_kernel(SmallBatch batch, MuonHy
   __syncthreads();
   sum = 0;
   for (int i = 0; i < NW; ++i) sum += dred[i];
-  const float inv = (float)(1.0 / (sqrt(sum) + (double)h.eps));
+  const double inverse = 1.0 / (sqrt(sum) + (double)h.eps);
+  float inv = (float)inverse;
+  if (!in_range(inv)) {
+    for (int i = tid; i < s * ld; i += NT) X[i] = (float)(X[i] * inverse);
+    inv = 1.f;
+    __syncthreads();
+  }
   switch (sp / 16) {
     case 1: small_steps<1, NW>(X, A, P, red, lp, inv, h); break;
     case 2: small_steps<2, NW>(X, A, P, red, lp, inv, h); break;
@@ -389,9 +398,11 @@ __global__ __launch_bounds__(256) void muon_start_kernel(MuonGroup G, MuonHyper 
   if ((tid & 63) == 0) red[tid >> 6] = sum;
   __syncthreads();
   sum = red[0] + red[1] + red[2] + red[3];
-  const float inv = (float)((double)kScale / (sqrt(sum) + (double)h.eps));
+  const double inverse = (double)kScale / (sqrt(sum) + (double)h.eps);
+  const float inv = (float)inverse;
+  const bool whole = in_range(inv);
 #pragma unroll
-  for (int q = 0; q < 16; ++q) tile[q * 4 + (tid >> 6)][tid & 63] = u[q] * inv;
+  for (int q = 0; q < 16; ++q) tile[q * 4 + (tid >> 6)][tid & 63] = whole ? u[q] * inv : (float)(u[q] * inverse);
   __syncthreads();
   uint16_t* X = G.X[0] + (int64_t)blockIdx.y * NP * G.s * G.lp;
 #pragma unroll

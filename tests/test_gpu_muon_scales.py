@@ -1,5 +1,5 @@
-"""kron_muon_step where the default coefficients' bounds do not hold: other quintics, and matrices that grow or shrink from step to
-step.
+"""kron_muon_step where the default coefficients' bounds do not hold: other quintics, matrices that grow or shrink from step to
+step, the smallest eps and gradients at both ends of fp32's range.
 
 Tolerances as in test_gpu_muon.py: the error of X, as a Frobenius norm, may be four times what plain arithmetic of the same
 precision leaves on the same inputs (fp32, or operands rounded to fp16's eleven bits), and at least sixteen roundings of X;
@@ -101,3 +101,38 @@ def test_growth_beyond_the_limit_is_refused():
             k.kron_muon_step([W], [G], [m], lr=0.1, coeffs=coeffs, steps=steps)
         assert torch.equal(W, keep[0]) and torch.equal(m, keep[1])
     compare((20, 30), torch.float32, (2.0, 0.0, 0.0), 16)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shape", [(3, 20, 30), (3, 80, 90)])
+@pytest.mark.parametrize("eps", [1e-30, 1e-36, 1e-40, 1.5e-45])
+def test_zeros_and_the_smallest_eps(shape, dtype, eps):
+    """A matrix of zeros stays where 1 / eps is beyond fp32."""
+    k = K()
+    W, G, m = tensors(6, shape, dtype)
+    G[0], m[0] = 0, 0
+    w0 = W.clone()
+    k.kron_muon_step([W], [G], [m], lr=0.1, eps=eps)
+    assert torch.equal(W[0], w0[0]) and torch.count_nonzero(m[0]) == 0
+    assert torch.isfinite(W).all() and not torch.equal(W[1], w0[1])
+
+
+@pytest.mark.parametrize("shape", [(20, 30), (80, 90), (300, 16)])
+@pytest.mark.parametrize("up", [-130, -126, -120, 100, 119])
+def test_gradients_at_the_ends_of_the_range(shape, up):
+    """The update does not depend on the gradient's size, up to where fp32 itself ends: values of 2^-130 have 2^-149 / 2^-130 =
+    2^-19 of rounding, which five steps of the quintic multiply by at most 3.45^5 = 489 where the singular value is small, so
+    X, of values below 1.3, is off by at most 2^-19 * 489 * 2 as a norm over sqrt of the smaller side."""
+    k = K()
+    W, G, m = tensors(7, shape, torch.float32)
+    G = G / G.abs().max()
+    m.zero_()
+    W2, m2 = W.clone(), torch.zeros_like(m)
+    k.kron_muon_step([W], [G], [m], lr=1.0, eps=1.5e-45)
+    small = torch.ldexp(G, torch.tensor(up // 2, device="cuda"))
+    small = torch.ldexp(small, torch.tensor(up - up // 2, device="cuda"))
+    k.kron_muon_step([W2], [small], [m2], lr=1.0, eps=1.5e-45)
+    o = f64(W2) - f64(W)
+    assert np.isfinite(o).all()
+    tol = 2.0 ** -19 * 489 * 2 * min(shape) ** 0.5 if up < -100 else 1e-5 * min(shape) ** 0.5
+    assert np.linalg.norm(o) <= tol
