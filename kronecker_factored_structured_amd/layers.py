@@ -248,7 +248,8 @@ class KronAdapters(nn.Module):
     down[e]^T) up[e]^T, for each request with its own adapter e.  down ~ randn / sqrt(in), up zeros, scale = alpha /
     rank (alpha None: rank).  forward(x, ids, starts): x [N, in] (or [..., in] without ids: adapter 0 everywhere), request
     i the rows starts[i] to starts[i + 1] (int32; None: one row each) with adapter ids[i] (int32, negative: none).
-    down and up are rounded to x's type for the products; their gradients are computed in float32."""
+    down and up are rounded to x's type for the products; their gradients are computed in float32.  The scales are
+    float32 whatever type the module is converted to."""
 
     def __init__(self, projection: nn.Module, in_features: int, out_features: int, rank: int, adapters: int = 1,
                  alpha: Optional[float] = None, device=None, dtype=None):
@@ -261,6 +262,13 @@ class KronAdapters(nn.Module):
         self.up = nn.Parameter(torch.zeros(adapters, out_features, rank, **kw))
         scale = 1.0 if alpha is None else alpha / rank
         self.register_buffer("scales", torch.full((adapters,), scale, device=device, dtype=torch.float32))
+
+    def _apply(self, fn, recurse=True):
+        scales = self.scales
+        super()._apply(fn, recurse)
+        if self.scales.dtype != torch.float32:      # .bfloat16() and the like convert floating buffers too
+            self.scales = scales.to(self.scales.device)
+        return self
 
     def forward(self, x, ids=None, starts=None):
         base = self.projection(x)
