@@ -35,6 +35,10 @@ typedef short s4v __attribute__((ext_vector_type(4)));
 
 typedef _Float16 h4 __attribute__((ext_vector_type(4)));
 
+// Values whose small ones count as well (the softmax of unlikely tokens) have their second part 2^11 up, next to where the first
+// one ends: 2^-36 where it is subnormal.  The other operand's first part goes 2^-11 down for that product, in registers (its values
+// below 2^-3 of 2^15 lose bits then, at most 2^-25 times the second part: 2^-41 of the largest).
+
 // The first part of four values, and what it leaves of them.  They are held as they are: folded into the conversion, the
 // product that made one may round to another first part there than in what is left (one value in 2^13, off by 2^-11).
 __device__ inline h4 first_part(f4& v) {
@@ -160,6 +164,8 @@ __device__ inline u4 fragment(const lds_t* lds, int at, int i, int kk, int lane)
 // KG: as many groups of WM x WN wavefronts share a tile's contraction, each with its own tiles in LDS; the first group has
 // the sums in the end.
 //
+// UP: B's second parts are 2^UP up (two planes).
+//
 // F32: two "planes" that are fp32 values as they are (ROW, whole rows of 128 bytes), on the fp32 instruction.  The four
 // products of a lane's 16 bytes are of every fourth k, of both operands alike.
 //
@@ -168,7 +174,7 @@ __device__ inline u4 fragment(const lds_t* lds, int at, int i, int kk, int lane)
 // 1,700, reads of LDS alone 4,850.  Measured beside it: 32 x 32 blocks (1,810 out of registers) 1,080-1,150; four
 // wavefronts of 128 x 128 each 1,000; steps of 32 with three to five in LDS 960-1,040; raised wave priority 1,265; reads,
 // loads and products interleaved by hand 1,350.
-template <int WM_, int WN_, int TM_, int TN_, Side SA_, Side SB_, bool BF_, int NP_, int NS_ = 2, bool F32_ = false, int KG_ = 1>
+template <int WM_, int WN_, int TM_, int TN_, Side SA_, Side SB_, bool BF_, int NP_, int NS_ = 2, bool F32_ = false, int KG_ = 1, int UP = 0>
 struct Product {
   static constexpr bool F32 = F32_;
   static constexpr int KG = KG_;
@@ -203,6 +209,10 @@ struct Product {
 #pragma unroll
       for (int j = 0; j < TN; ++j) acc[i][j] = mma<BF_>(a.f[i], b.f[j], acc[i][j]);
     }
+  }
+  // Block row i of A's first part for products with B's second one.
+  __device__ static void lower(FragsA& a, int i) {
+    if constexpr (UP > 0) a.f[i] = __builtin_bit_cast(u4, __builtin_bit_cast(h8, a.f[i]) * (_Float16)(1.f / (1 << UP)));
   }
   // between(i): what is issued beside block row i's products.
   template <class F>
@@ -279,8 +289,13 @@ struct Product {
         fetch(1 - set, st);      // (behind the last step: of no use, and not used)
         if constexpr (NP == 2 && !F32) multiply(a[set][1], b[set][0], none);
         else multiply(a[set][1], b[set][1], none);
-        if constexpr (NP == 2 && !F32) multiply(a[set][0], b[set][1], none);
-        multiply(a[set][0], b[set][0], none);
+        if constexpr (UP > 0) {
+          multiply(a[set][0], b[set][0], none);
+          multiply(a[set][0], b[set][1], [&](int i) { lower(a[set][0], i); });
+        } else {
+          if constexpr (NP == 2 && !F32) multiply(a[set][0], b[set][1], none);
+          multiply(a[set][0], b[set][0], none);
+        }
       };
       std::integral_constant<int, 0> even;
       std::integral_constant<int, 1> odd;
@@ -344,6 +359,14 @@ struct Product {
         multiply(a0, b0, none);
         read(b1, now, 1, wn, lane);
         multiply(a1, b0, none);
+        if constexpr (UP > 0) {
+          // (in place, behind the products that need it as it was: with both of them alive tiles of 256 spill, 1.55 -> 1.76 ms
+          // of 2050 x 1024 x 32003 with gradients; so 1.56)
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int i = 0; i < TM; ++i) lower(a1, i);
+          __builtin_amdgcn_sched_barrier(0);
+        }
       } else {
         read(b1, now, 1, wn, lane);
         read(a1, now, 1, wm, lane);

@@ -129,6 +129,7 @@ __global__ __launch_bounds__(1024) void vocab_top_kernel(VocabCE a) {
 // Rows as operands: gathered (h), padded with zeros to Kp, fp32 split into its parts.  which 0: h, 1: W, 2: h times the
 // rows' weights.
 constexpr float kOne = 32768.f;      // scale of what is at most 1
+constexpr int kUp = 11;              // and of its second part beside it: fp32's dz is off by 2^-22 of itself or 2^-51
 template <bool BF>
 __global__ __launch_bounds__(256) void vocab_pack_kernel(VocabCE a, int which) {
   const bool w = which == 1;
@@ -370,7 +371,9 @@ __global__ __launch_bounds__(P::kThreads) void vocab_dz_kernel(VocabCE a, int v0
   } else {
     // a first part, and what it leaves, in the sum's place, as the second one
     store_rows<P>(smem, out, (int64_t)vc * 2, padded - n0, [&](int i, int j) __attribute__((always_inline)) {
-      return __builtin_bit_cast(uint2, first_part(p.acc[i][j]));
+      const uint2 part = __builtin_bit_cast(uint2, first_part(p.acc[i][j]));
+      p.acc[i][j] *= (float)(1 << kUp);
+      return part;
     });
   }
 }
@@ -446,7 +449,7 @@ __global__ __launch_bounds__(256, 2) void vocab_dh_few_kernel(VocabCE a, int v0,
   auto multiply = [&](const Step& s) __attribute__((always_inline)) {
     f4 d[TN];
 #pragma unroll
-    for (int j = 0; j < TN; ++j) d[j] = __builtin_convertvector(s.d[j][0], f4) + __builtin_convertvector(s.d[j][1], f4);
+    for (int j = 0; j < TN; ++j) d[j] = __builtin_convertvector(s.d[j][0], f4) + __builtin_convertvector(s.d[j][1], f4) * (1.f / (1 << kUp));
 #pragma unroll
     for (int e = 0; e < 4; ++e)
 #pragma unroll
@@ -629,14 +632,15 @@ __global__ __launch_bounds__(256) void vocab_dw_join_kernel(VocabCE a, int v0, i
 }
 
 // ------------------------------------------------------------------------------ host
-// Tiles of a product, m x n.
+// Tiles of a product, m x n; what has a COL operand multiplies dz (B).
 enum Tile { kBig, kWide, kMid, kSmall, kFew };      // 256 x 256, 192 x 256, 128 x 128, 64 x 64, 256 x 64
+template <int WM, int WN, int TM, int TN, Side SA, Side SB, bool BF, int NS = 2>
+using TileOf = Product<WM, WN, TM, TN, SA, SB, BF, BF ? 1 : 2, NS, false, 1, !BF && SA == COL ? kUp : 0>;
 template <int T, bool BF, Side SA, Side SB>
-using Tiled = std::conditional_t<T == kBig, Product<2, 4, 8, 4, SA, SB, BF, BF ? 1 : 2>,
-              std::conditional_t<T == kWide, Product<2, 4, 6, 4, SA, SB, BF, BF ? 1 : 2>,
-              std::conditional_t<T == kMid, Product<2, 2, 4, 4, SA, SB, BF, BF ? 1 : 2>,
-              std::conditional_t<T == kSmall, Product<2, 2, 2, 2, SA, SB, BF, BF ? 1 : 2, 4>,
-                                 Product<4, 1, 4, 4, SA, SB, BF, BF ? 1 : 2>>>>>;
+using Tiled = std::conditional_t<T == kBig, TileOf<2, 4, 8, 4, SA, SB, BF>,
+              std::conditional_t<T == kWide, TileOf<2, 4, 6, 4, SA, SB, BF>,
+              std::conditional_t<T == kMid, TileOf<2, 2, 4, 4, SA, SB, BF>,
+              std::conditional_t<T == kSmall, TileOf<2, 2, 2, 2, SA, SB, BF, 4>, TileOf<4, 1, 4, 4, SA, SB, BF>>>>>;
 // fp32 as it is: 128 x TN 16.  The instruction's rate bounds it from about 64 rows on, W's reading below: 32 x 1024 x 60000
 // 4.6 TB/s, 64 x 1024 x 32000 42 us (3.1 TB/s, 100 TFLOP/s; loads into registers, 64 bytes of sixteen rows each: 60).
 template <int TN, int NS>
