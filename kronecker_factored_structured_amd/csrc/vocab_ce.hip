@@ -47,6 +47,11 @@ __device__ inline float scale_up(uint32_t top) {
   return __uint_as_float((uint32_t)(s + 127) << 23);
 }
 __device__ inline float scale_down(uint32_t top) { return 1.f / scale_up(top); }
+// What a product of both tensors' parts is times (a factor beyond fp32's range: its end, which takes them there as well).
+__device__ inline float scale_down(uint32_t a, uint32_t b) {
+  const int up = (int)(__float_as_uint(scale_up(a)) >> 23) + (int)(__float_as_uint(scale_up(b)) >> 23) - 254;
+  return __uint_as_float((uint32_t)(min(127, max(-126, -up)) + 127) << 23);
+}
 
 // Rows of nonzero weight in order (idx), their places (pos, -1: not in use), and what the outputs of the others are.
 __global__ __launch_bounds__(1024) void vocab_rows_kernel(VocabCE a) {
@@ -198,7 +203,7 @@ __global__ __launch_bounds__(P::kThreads) void vocab_fwd_kernel(VocabCE a, int t
   vocab_logits<P, BF>(p, a, count, m0, n0, (lds_t*)smem);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
   const int wm = wave % P::WM, wn = wave / P::WM, first = m0 + wm * P::TM * 16 + 4 * g;
-  const float down = scaled ? scale_down(a.sc->top_h) : 1.f, down2 = scaled ? scale_down(a.sc->top_w) : 1.f;
+  const float down = scaled ? scale_down(a.sc->top_h, a.sc->top_w) : 1.f;
   float2* red = (float2*)smem;      // (the product ended with a barrier)
 #pragma unroll
   for (int j = 0; j < P::TN; ++j) {
@@ -220,20 +225,19 @@ __global__ __launch_bounds__(P::kThreads) void vocab_fwd_kernel(VocabCE a, int t
       if constexpr (scaled) p.acc[i][j] *= down;
       top = fmaxf(fmaxf(top, fmaxf(p.acc[i][j][0], p.acc[i][j][1])), fmaxf(p.acc[i][j][2], p.acc[i][j][3]));
     }
-    const float f = scaled ? down2 * kLog2e : kLog2e;
     if (__any(mine)) {
 #pragma unroll
       for (int i = 0; i < P::TM; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (mine && off == 16 * i + e) a.zlab[n] = scaled ? p.acc[i][j][e] * down2 : p.acc[i][j][e];
+          if (mine && off == 16 * i + e) a.zlab[n] = p.acc[i][j][e];
     }
-    float2 s = {top * f, 0.f};
+    float2 s = {top * kLog2e, 0.f};
     const float ref = top == -INFINITY ? 0.f : s.x;
 #pragma unroll
     for (int i = 0; i < P::TM; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s.y += expo2(fmaf(p.acc[i][j][e], f, -ref));
+      for (int e = 0; e < 4; ++e) s.y += expo2(fmaf(p.acc[i][j][e], kLog2e, -ref));
 #pragma unroll
     for (int o = 16; o <= 32; o *= 2) s = joined(s, float2{__shfl_xor(s.x, o, 64), __shfl_xor(s.y, o, 64)});
     if (g == 0) red[wm * P::BN + nl] = s;
@@ -327,8 +331,7 @@ __global__ __launch_bounds__(P::kThreads) void vocab_dz_kernel(VocabCE a, int v0
   vocab_logits<P, BF>(p, a, count, v0 + m0, n0, (lds_t*)smem);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
   const int wm = wave % P::WM, wn = wave / P::WM, first = v0 + m0 + wm * P::TM * 16 + 4 * g;
-  const float down = scaled ? scale_down(a.sc->top_h) : 1.f, down2 = scaled ? scale_down(a.sc->top_w) : 1.f;
-  const float f = scaled ? down2 * kLog2e : kLog2e;
+  const float down = scaled ? scale_down(a.sc->top_h, a.sc->top_w) : 1.f;
   const int padded = (count + kBK - 1) / kBK * kBK;      // rows that the contraction over them reads
   const bool edge = v0 + m0 + P::BM > a.V || n0 + P::BN > count;
 #pragma unroll
@@ -345,7 +348,7 @@ __global__ __launch_bounds__(P::kThreads) void vocab_dz_kernel(VocabCE a, int v0
 #pragma unroll
     for (int i = 0; i < P::TM; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) p.acc[i][j][e] = expo2(fmaf(scaled ? p.acc[i][j][e] * down : p.acc[i][j][e], f, -top)) * inv;
+      for (int e = 0; e < 4; ++e) p.acc[i][j][e] = expo2(fmaf(scaled ? p.acc[i][j][e] * down : p.acc[i][j][e], kLog2e, -top)) * inv;
     const int64_t off = lab - first;
     const bool mine = off >= 0 && off < P::TM * 16 && (off & 15) < 4;
     if (__any(mine)) {
@@ -449,7 +452,7 @@ __global__ __launch_bounds__(256, 2) void vocab_dh_few_kernel(VocabCE a, int v0,
   auto multiply = [&](const Step& s) __attribute__((always_inline)) {
     f4 d[TN];
 #pragma unroll
-    for (int j = 0; j < TN; ++j) d[j] = __builtin_convertvector(s.d[j][0], f4) + __builtin_convertvector(s.d[j][1], f4) * (1.f / (1 << kUp));
+    for (int j = 0; j < TN; ++j) d[j] = __builtin_convertvector(s.d[j][0], f4) * (1 / kOne) + __builtin_convertvector(s.d[j][1], f4) * (1 / kOne / (1 << kUp));
 #pragma unroll
     for (int e = 0; e < 4; ++e)
 #pragma unroll
@@ -505,10 +508,12 @@ __global__ __launch_bounds__(256, 2) void vocab_dh_few_kernel(VocabCE a, int v0,
   }
 }
 
-// Four gradients of a row of K, times f2 and f, in their type.
+// Four gradients of a row of K, times f and then f2, in their type.  Of fp32 sums f2 is the power of two of the tensor's largest
+// value, and kSums goes with f: s f stays within fp32's range where the gradient does.
+constexpr float kSums = 1.f / 16384 / kOne;      // of parts below 2^15, and dz's
 template <bool BF>
 __device__ inline void put_grad(void* p, int64_t row, int k, int K, f4 s, float f2, float f) {
-  s = s * f2 * f;
+  s = s * f * f2;
   if constexpr (BF) {
     uint16_t* o = (uint16_t*)p + row * K + k;
     if ((K & 3) == 0)
@@ -534,7 +539,8 @@ template <bool BF, int SL>
 __global__ __launch_bounds__(256) void vocab_dh_join_kernel(VocabCE a, int splits) {
   constexpr int G = 256 / SL;
   __shared__ f4 red[SL][G];
-  const float gout = a.gout[0], f2 = BF ? 1.f : scale_down(a.sc->top_w);
+  const bool as_it_is = BF || a.wp == a.W;      // (dz without its scale, times W)
+  const float gout = a.gout[0], f2 = as_it_is ? 1.f : scale_down(a.sc->top_w) * 16384.f;
   const int per = a.Kp / 4, slice = threadIdx.x / G, mine = threadIdx.x % G;
   for (int64_t i0 = (int64_t)blockIdx.x * G; i0 < a.N * per; i0 += (int64_t)gridDim.x * G) {
     const int64_t i = i0 + mine, row = i / per;
@@ -554,21 +560,21 @@ __global__ __launch_bounds__(256) void vocab_dh_join_kernel(VocabCE a, int split
       __syncthreads();
     }
     if (in && slice == 0) {
-      const float f = BF ? unit_weight(a) * gout : (a.weights ? a.weights[row] : a.mean) * (1.f / kOne) * gout;
+      const float f = BF ? unit_weight(a) * gout : (a.weights ? a.weights[row] : a.mean) * (as_it_is ? 1.f : kSums) * gout;
       put_grad<BF>(a.dh, row, k, a.K, s, at >= 0 ? f2 : 0.f, at >= 0 ? f : 0.f);
     }
   }
 }
 
-// What dW's sums are times: f2, then f.
+// What dW's sums are times: f, then f2.
 template <bool BF>
 __device__ inline void dw_factors(const VocabCE& a, float& f, float& f2) {
   f = a.gout[0], f2 = 1.f;
   if constexpr (BF) {
     f *= unit_weight(a);
   } else {
-    f2 = scale_down(a.sc->top_h);
-    f *= a.weights ? scale_down(a.sc->top_weight) : a.mean * (1.f / kOne);
+    f2 = scale_down(a.sc->top_h) * 16384.f;
+    f *= a.weights ? scale_down(a.sc->top_weight) * (1.f / 16384) : a.mean * kSums;
   }
 }
 

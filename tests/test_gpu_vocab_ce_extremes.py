@@ -1,4 +1,5 @@
-"""kron_vocab_ce_bwd in fp32 where the gradients' terms are small: tokens that every row finds unlikely.
+"""The vocabulary cross-entropy in fp32 where the gradients' terms are small, tokens that every row finds unlikely, and where
+h and W lie at opposite ends of fp32's range.
 
 Tolerances as derived in test_gpu_vocab_ce.py, entry by entry: a logit is off by eps_z = (K + 20) u S, S = sum |h| |W|, and a
 probability by eps = 2 eps_z + u (4 spread + 3 (V / 2048 + 64) + 8) of itself.  The entry of a row's own label is a difference,
@@ -76,3 +77,30 @@ def test_unlikely_tokens(N, Kf, V, weights):
     rows = np.abs(o["dW"]).max(1)
     assert (likely < 1e-9).any() and (likely < 1e-11).any()
     assert np.all((off.max(1) <= 1e-3 * rows)[likely > 1e-12])
+
+
+@pytest.mark.parametrize("N", [20, 60, 110, 200])
+@pytest.mark.parametrize("up", [-121, -100, 100, 121])
+def test_operands_at_the_ends_of_the_range(N, up):
+    """h 2^up and W 2^-up: the logits and the losses are those of h and W, bit by bit; dh is 2^-up of theirs, dW 2^up.  (Every
+    scale is a power of two; gradients that fp32 has no normal number for are left out.)"""
+    k = K()
+    g = torch.Generator().manual_seed(N)
+    h, W = torch.randn(N, 40, generator=g).cuda(), (torch.randn(300, 40, generator=g) * 0.4).cuda()
+    h, W = (torch.where(t.abs() < 2.0 ** -5, torch.full_like(t, 0.25), t) for t in (h, W))      # (normal at either end)
+    lab, gout = torch.randint(0, 300, (N,), generator=g).cuda(), torch.ones(1, device="cuda")
+
+    def times(t, e):
+        return torch.ldexp(torch.ldexp(t, torch.tensor(e // 2, device="cuda")), torch.tensor(e - e // 2, device="cuda"))
+
+    outs = []
+    for a, b in ((h, W), (times(h, up), times(W, -up))):
+        loss, nll, stats = k.kron_vocab_ce_fwd(a, b, lab)
+        outs.append((nll, k.kron_vocab_ce_bwd(a, b, lab, stats, gout)))
+    assert torch.equal(outs[0][0], outs[1][0])
+    for key, e in (("dh", -up), ("dW", up)):
+        want, got = times(outs[0][1][key].double(), e), outs[1][1][key].double()
+        there = want.abs() >= 2.0 ** -100
+        assert bool(torch.isfinite(got).all())
+        assert torch.equal(got[there], want[there]), key
+        assert bool((got[~there].abs() < 2.0 ** -99).all())
