@@ -197,24 +197,24 @@ class _KronVocabCEFn(torch.autograd.Function):
     def forward(ctx, h, W, labels, weights):
         ctx.type = W.dtype
         w = _whole(W if W.dtype == h.dtype or h.dtype != torch.bfloat16 else W.to(h.dtype))
-        loss, _, stats = api.kron_vocab_ce_fwd(h, w, labels, weights)
-        ctx.save_for_backward(h, w, labels, weights, stats)
+        loss, nll, stats = api.kron_vocab_ce_fwd(h, w, labels, weights)
+        ctx.save_for_backward(h, w, labels, weights, stats, nll if ctx.needs_input_grad[3] else None)
         return loss.view(())
 
     @staticmethod
     @once_differentiable
     def backward(ctx, gout):
-        h, W, labels, weights, stats = ctx.saved_tensors
+        h, W, labels, weights, stats, nll = ctx.saved_tensors
         g = api.kron_vocab_ce_bwd(h, W, labels, stats, _whole(gout.reshape(1)), weights,
                                   want_dh=ctx.needs_input_grad[0], want_dW=ctx.needs_input_grad[1])
-        return g["dh"], None if g["dW"] is None else g["dW"].to(ctx.type), None, None
+        return g["dh"], None if g["dW"] is None else g["dW"].to(ctx.type), None, None if nll is None else nll * gout
 
 
 class KronVocabCE(nn.Module):
     """The cross-entropy of the logits h W^T on labels, without the logits in memory: sum_n weights[n] nll[n]
-    (weights None: the mean over the rows; weight 0: a padded position, or one of a prompt).  h [..., K], W [V, K]
+    (weights None: the mean over the rows; weight 0: a padded position, or one of a prompt, that is left out).  h [..., K], W [V, K]
     (an embedding table; a float32 one with bfloat16 h is rounded to bfloat16), labels and weights [...].  The
-    backward computes the logits once more."""
+    backward computes the logits once more.  The gradient of weights is nll (0 for a row that is left out)."""
 
     def forward(self, h, W, labels, weights=None):
         rows = _whole(h.reshape(-1, h.shape[-1]))

@@ -1,8 +1,10 @@
-"""KronAdapters as a user's model holds it: converted to bfloat16 after it was made."""
+"""KronAdapters and KronVocabCE as a user's model holds them: converted to bfloat16 after it was made, with weights that are
+learnt."""
 import numpy as np
 import pytest
 
 from oracle import adapters as OA
+from oracle import vocab_ce as OV
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -41,3 +43,32 @@ def test_adapters_of_a_converted_model():
     for key, t in (("ddown", m.down.grad), ("dup", m.up.grad)):
         assert t.dtype == torch.bfloat16
         assert np.all(np.abs(f64(t) - g[key]) <= 88 * u * size[key] * 1.01 + 2.0 ** -8 * np.abs(g[key])), key
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_learnt_weights(dtype):
+    """d loss / d weights[n] is the row's own nll; a row of weight 0 is left out, and so is its gradient (0), whatever it
+    holds.  Weights of any shape, beside the gradients of h and W or alone."""
+    import kronecker_factored_structured_amd as K
+    g = torch.Generator().manual_seed(4)
+    h, W = torch.randn(3, 7, 16, generator=g).to(dtype).cuda(), torch.randn(50, 16, generator=g).to(dtype).cuda()
+    lab = torch.randint(0, 50, (3, 7), generator=g).cuda()
+    raw = torch.rand(3, 7, generator=g).cuda()
+    raw[1, 2:5] = 0
+    h[1, 3], lab[1, 4] = float("nan"), -100
+    _, nll, _ = K.kron_vocab_ce_fwd(h.view(21, 16), W, lab.view(21), weights=raw.view(21))
+    for others in (False, True):
+        leaf = raw.clone().requires_grad_()
+        hh, WW = h.clone().requires_grad_(others), W.clone().requires_grad_(others)
+        (K.KronVocabCE()(hh, WW, lab, 2 * leaf) * 3).backward()
+        assert torch.equal(leaf.grad, 6 * nll.view(3, 7)) and torch.count_nonzero(leaf.grad[1, 2:5]) == 0
+        assert (hh.grad is not None) == others and (WW.grad is not None) == others
+    keep = torch.tensor([n for n in range(21) if n not in (9, 10, 11)])
+    o = OV.forward_backward(f64(h.view(21, 16))[keep], f64(W), lab.view(21).cpu().numpy()[keep])
+    # (eps_nll of test_gpu_vocab_ce.py)
+    eps = 2 * 36 * u * o["zs"] + u * (4 * (o["z"].max(1) - o["z"].min(1)) + 3 * (50 / 2048 + 64) + 8) + u * (np.abs(o["z"]).max(1) + np.abs(o["nll"]))
+    assert np.all(np.abs(f64(nll)[keep] - o["nll"]) <= eps)
+    plain = raw.clone()      # (weights that need no gradient get none)
+    WW = W.clone().requires_grad_()
+    K.KronVocabCE()(h, WW, lab, plain).backward()
+    assert plain.grad is None and WW.grad is not None
