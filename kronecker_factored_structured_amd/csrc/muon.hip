@@ -581,8 +581,11 @@ size_t group_bytes(int s, int l, int64_t mats, bool bf, MuonGroup* G, char* ws) 
 }
 
 // Calls f(s, l, tensors, n, matrices) for the groups of large matrices: tensors of one size, at most kGroup tensors
-// and kGroupMats matrices together.  They run one after the other in the same workspace.
-constexpr int kGroupMats = 64;
+// and group_mats matrices together.  They run one after the other in the same workspace, which 2^28 values keep below 4.6 GB
+// (fp32; one matrix of 16384 x 16384, sixteen of 4096 x 4096, 64 of which would take 17 GB).  By then a few fill the GPU: of
+// 4096 x 4096 fp32 one takes 3.76 ms, eight 3.37 each and sixteen 3.29.
+constexpr int64_t kGroupMats = 64, kGroupValues = int64_t(1) << 28;
+int64_t group_mats(int64_t s, int64_t l) { return std::min(kGroupMats, std::max<int64_t>(1, kGroupValues / (s * l))); }
 template <class F>
 hipError_t for_groups(const MuonTensor* t, int n, const F& f) {
   std::vector<int> order;
@@ -596,10 +599,11 @@ hipError_t for_groups(const MuonTensor* t, int n, const F& f) {
   for (size_t o = 0; o < order.size(); ++o) {
     MuonTensor rest = t[order[o]];
     const auto sl = size(order[o]);
+    const int64_t most = group_mats(sl.first, sl.second);
     const bool last = o + 1 == order.size() || size(order[o + 1]) != sl;
     while (rest.count > 0) {
       MuonTensor now = rest;
-      now.count = std::min<int64_t>(rest.count, kGroupMats - mats);
+      now.count = std::min(rest.count, most - mats);
       got[k++] = now;
       mats += now.count;
       const int64_t skip = now.count * rest.rows * rest.cols;
@@ -607,7 +611,7 @@ hipError_t for_groups(const MuonTensor* t, int n, const F& f) {
       rest.m += skip;
       rest.p = (char*)rest.p + skip * f.element();
       rest.g = (const char*)rest.g + skip * f.element();
-      if (k == kGroup || mats == kGroupMats || (last && rest.count == 0)) {
+      if (k == kGroup || mats == most || (last && rest.count == 0)) {
         const hipError_t e = f(sl.first, sl.second, got, k, mats);
         if (e != hipSuccess) return e;
         k = 0, mats = 0;
