@@ -655,7 +655,7 @@ using Whole = Product<4, 1, 2, TN, ROW, ROW, false, 2, NS, true>;
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-// Rows and width of a product with few rows: a tile of 64.
+// Rows and width of a product with few rows: a tile of 64 (bf16).
 bool few(int64_t N) { return N <= 64; }
 
 // Whether fp32's products with W take it as it is, on the fp32 instruction.
@@ -693,6 +693,8 @@ Choice choose(int64_t m, int64_t n, int64_t steps, int most, double moves, unsig
 }
 const TileCost& cost_of(Tile t) { return kTiles[t]; }
 constexpr unsigned kSquares = 1u << kBig | 1u << kMid | 1u << kSmall;
+constexpr unsigned squares_or_few(bool bf) { return kSquares | (bf ? 1u << kFew : 0); }
+unsigned tiles_for(int64_t N, int planes, unsigned many) { return planes == 1 && few(N) ? 1u << kFew | 1u << kSmall : many; }
 
 struct VocabPlan {
   int Kp;
@@ -707,7 +709,7 @@ struct VocabPlan {
 
 int64_t steps_of(int64_t n, int planes) { return ceil_div(n, kBK) * (planes == 2 ? 3 : 1); }
 Choice logits_tile(int64_t N, int Kp, int64_t vc, int planes) {
-  return choose(vc, N, steps_of(Kp, planes), 1, 2, few(N) ? 1u << kFew | 1u << kSmall : kSquares);
+  return choose(vc, N, steps_of(Kp, planes), 1, 2, tiles_for(N, planes, kSquares));
 }
 Choice dw_tile(int64_t N, int Kp, int vc, int planes) { return choose(Kp, vc, steps_of(N, planes), 8, 2, kSquares); }
 
@@ -748,8 +750,7 @@ VocabPlan plan_of(int64_t N, int K, int V, bool bf, bool weights, bool backward)
       const int64_t groups = tk * (few(N) ? 1 : 2);
       p.dh.parts = (int)std::min<int64_t>(std::max<int64_t>(1, 512 / groups), p.piece / 128);
     } else {
-      p.dh = choose(p.Kp, N, steps_of(p.piece, planes), few(N) ? 128 : 16, p.pieces > 1 ? 4 : 2,
-                    few(N) ? 1u << kFew | 1u << kSmall : kSquares | 1u << kWide);
+      p.dh = choose(p.Kp, N, steps_of(p.piece, planes), few(N) ? 128 : 16, p.pieces > 1 ? 4 : 2, tiles_for(N, planes, kSquares | 1u << kWide));
     }
     p.dhpart = take(4 * (size_t)p.dh.parts * N * p.Kp);
     size_t most = 0;
@@ -839,7 +840,7 @@ hipError_t run_fwd(const VocabCE& a, const VocabPlan& p, hipStream_t s) {
         });
     } else {
       const int tn = (int)ceil_div(a.N, cost_of(p.fwd).n);
-      e = with_tile<kSquares | 1u << kFew>(p.fwd, [&](auto tile) {
+      e = with_tile<squares_or_few(BF)>(p.fwd, [&](auto tile) {
         typedef Tiled<tile, BF, ROW, ROW> P;
         return go<P, vocab_fwd_kernel<P, BF>>(dim3((unsigned)(p.tiles * tn)), s, a, p.tiles, tn);
       });
@@ -865,7 +866,7 @@ hipError_t run_dz(const VocabCE& a, const VocabPlan& p, int v0, int vc, hipStrea
         return go<P, vocab_dz_kernel<P, BF>>(dim3((unsigned)(vc / P::BM)), s, a, v0, vc, vc / P::BM, 1);
       });
   }
-  return with_tile<kSquares | 1u << kFew>(logits_tile(a.N, p.Kp, vc, BF ? 1 : 2).tile, [&](auto tile) {
+  return with_tile<squares_or_few(BF)>(logits_tile(a.N, p.Kp, vc, BF ? 1 : 2).tile, [&](auto tile) {
     typedef Tiled<tile, BF, ROW, ROW> P;
     const int tm = vc / P::BM, tn = (int)ceil_div(a.N, P::BN);
     return go<P, vocab_dz_kernel<P, BF>>(dim3((unsigned)(tm * tn)), s, a, v0, vc, tm, tn);
@@ -882,7 +883,7 @@ hipError_t run_dh(const VocabCE& a, const VocabPlan& p, int v0, int vc, hipStrea
     else hipLaunchKernelGGL((vocab_dh_few_kernel<4>), grid, dim3(256), 0, s, a, v0, vc, tn, len, add);
     return hipGetLastError();
   }
-  return with_tile<kSquares | 1u << kWide | 1u << kFew>(p.dh.tile, [&](auto tile) {
+  return with_tile<squares_or_few(BF) | 1u << kWide>(p.dh.tile, [&](auto tile) {
     typedef Tiled<tile, BF, COL, ROW> P;
     const int tm = (int)ceil_div(p.Kp, P::BM), tn = (int)ceil_div(a.N, P::BN);
     return go<P, vocab_dh_kernel<P, BF>>(dim3((unsigned)(tm * tn), (unsigned)p.dh.parts), s, a, v0, vc, tm, tn, len, add);
