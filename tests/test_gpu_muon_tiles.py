@@ -73,3 +73,34 @@ def compare(shapes, dtype, steps=5, lr=0.1, only=None):
 def test_more_matrices_than_a_group_takes():
     """Seventeen of 4096 x 4096: sixteen share a workspace, the last one has it to itself."""
     compare([(17, 4096, 4096)], torch.bfloat16, steps=1, only=(0, 15, 16))
+
+
+# What a product's tile follows from is the number of tiles of all matrices: 64 x 64 with four groups of wavefronts (one matrix),
+# 64 x 64 with two steps in LDS, 128 x 128 and 256 x 256; ragged sides, wide and tall ones together
+@pytest.mark.parametrize("shapes", [[(530, 700)], [(700, 530)], [(5, 700, 720)], [(3, 720, 700), (2, 700, 720)], [(9, 520, 530), (9, 530, 520)],
+                                    [(40, 520, 530), (24, 530, 520)], [(4, 768, 2048)], [(2, 2048, 768), (2, 768, 2048)], [(1100, 1000)], [(2, 2100, 2000)]])
+def test_fp32(shapes):
+    compare(shapes, torch.float32)
+
+
+@pytest.mark.parametrize("shapes", [[(1000, 1020)], [(1020, 1000)], [(5, 700, 720)], [(3, 720, 700), (2, 700, 720)], [(9, 520, 530), (9, 530, 520)],
+                                    [(40, 520, 530), (24, 530, 520)], [(4, 768, 2048)], [(2, 2048, 768), (2, 768, 2048)], [(1001, 1015)], [(2, 2100, 2000)]])
+def test_bf16(shapes):
+    compare(shapes, torch.bfloat16)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_non_finite_matrices_stay_alone(dtype):
+    """In tiles of 128 and 256, of one group each: the others are what they are without it."""
+    k = K()
+    for shape in ((18, 520, 530), (64, 520, 530)):
+        W, G, m = tensors(3, shape, dtype)
+        W2, m2 = W.clone(), m.clone()
+        k.kron_muon_step([W2], [G], [m2], lr=0.1)
+        G[7, 100, 3], G[11, 519, 529] = float("nan"), float("inf")
+        G[13], m[13] = 0, 0
+        w13 = W[13].clone()
+        k.kron_muon_step([W], [G], [m], lr=0.1)
+        keep = [i for i in range(shape[0]) if i not in (7, 11, 13)]
+        assert torch.equal(W[keep], W2[keep]) and torch.equal(W[13], w13)
+        assert torch.isnan(W[7]).all() and not torch.isfinite(W[11]).any()
