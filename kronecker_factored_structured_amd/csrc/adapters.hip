@@ -557,7 +557,10 @@ template <int RT>
 hipError_t pick(const Adapters& a, bool backward, hipStream_t s) {
   if (!a.bf16) return backward ? bwd<false, RT, 1>(a, s) : fwd<false, RT, 1>(a, s);
   if constexpr (RT <= 4) {      // (more would take the registers and LDS of too many)
-    if (wide(a, backward)) return backward ? bwd<true, RT, 2>(a, s) : fwd<true, RT, 2>(a, s);
+    if (wide(a, false) && !backward) return fwd<true, RT, 2>(a, s);
+  }
+  if constexpr (RT == 2 || RT == 4) {
+    if (wide(a, true) && backward) return bwd<true, RT, 2>(a, s);
   }
   return backward ? bwd<true, RT, 1>(a, s) : fwd<true, RT, 1>(a, s);
 }

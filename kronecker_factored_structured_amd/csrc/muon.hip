@@ -517,9 +517,10 @@ hipError_t go(dim3 grid, hipStream_t s, const MuonGroup& G, const MuonHyper& h, 
 }
 
 // The largest tiles that still give every CU one.  Where there is no more than one for each, four steps' tiles are in LDS,
-// else two and more workgroups on a CU (1024 x 1024 fp32, 48 steps of 64 x 64: 23 -> 17 us; four 768 x 2048 bf16, 576 tiles:
-// 25 us with four, 21 with two).  Of P X over many steps four groups of wavefronts share the contraction (1024 x 1024 fp32:
-// 21.3 -> 15.6 us; the symmetric products, of which only 136 CUs have one, 13.0 -> 16.6, 59 x 3540 bf16 4.0 -> 5.6).
+// else two and more workgroups on a CU (1024 x 1024 fp32, 32 steps of its symmetric products' 136 tiles: 200 us with four, 272
+// with two; four 768 x 2048 bf16, 312 tiles: 283 with four, 276 with two, five 700 x 720 210 and 179).  Of P X over many steps
+// four groups of wavefronts share the contraction (1024 x 1024 fp32: 21.3 -> 15.6 us; the symmetric products, of which only 136
+// CUs have one, 13.0 -> 16.6, 59 x 3540 bf16 4.0 -> 5.6).
 template <bool BF, int NP, int MODE>
 hipError_t product(const MuonGroup& G, const MuonHyper& h, const MuonScales& k, int from, int mats, hipStream_t s) {
   constexpr Side SA = MODE >= 2 ? COL : ROW;
