@@ -494,10 +494,12 @@ kron_status_t kron_distill_bwd(const kron_distill_t* d, const void* logits, cons
  * The backward computes the logits once more, in pieces of the vocabulary: the workspace holds the
  * gradient of one piece in 16 bits (512 MB at most, or 256 tokens' if that is more).
  *   - A row of weight 0 is left out whole (padding): nothing of it is read, its nll and gradient are 0.
- *     The backward of the other rows costs what they do.
+ *     The logits, twice, and dW cost what the other rows do; dh takes fewer workgroups, each as long as with all rows.
  *   - A label outside [0, V) makes the loss, that row's nll and the gradients that it takes part in NaN
- *     (no out-of-bounds access).  So does a row with a NaN or a +infinity among its logits (fp32: or with
- *     one of a value of h or W that is not finite).
+ *     (no out-of-bounds access).  So does a row with a NaN or a +infinity among its logits.  A token
+ *     whose logit is -infinity has probability 0 (and dh 0 times infinity, NaN, in a column where W is -infinity); but
+ *     of more than 128 rows fp32 values of h and W that are not finite have no parts, and make the rows that they take part
+ *     in NaN.
  *   - Sums and softmax statistics are fp32 or fp64.  fp32 operands of the products are taken as they are
  *     (few rows), or as the sum of two fp16 parts after a scaling by a power of two: off by at most
  *     2^-22 of the value, or 2^-40 of the tensor's largest where that is more.  The softmax less the label's indicator
@@ -542,7 +544,7 @@ kron_status_t kron_vocab_ce_bwd(int64_t N, int32_t K, int32_t V, int32_t dtype, 
  * Limits: 1 <= K, M <= 65536, 1 <= R <= KRON_ADAPTERS_MAX_RANK, 1 <= E <= 65535, N <= 2^24; B <= 2^20, with
  * starts KRON_ADAPTERS_MAX_REQUESTS.
  * All arrays 16-byte aligned but ids and starts (4).  The forward needs no workspace; the backward's is
- * kron_adapters_workspace_bytes(N, K, M, R, E) bytes, 256-byte aligned (0 for rejected sizes).
+ * kron_adapters_workspace_bytes(d) bytes, 256-byte aligned (0 for rejected sizes, or if none is needed).
  */
 #define KRON_ADAPTERS_MAX_RANK 128
 #define KRON_ADAPTERS_MAX_REQUESTS 65536

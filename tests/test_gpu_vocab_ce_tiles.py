@@ -131,3 +131,25 @@ def test_labels_of_no_token(dtype):
         out = k.kron_vocab_ce_bwd(h, W, l2, stats, torch.ones(1, device="cuda"))
         assert torch.isnan(out["dh"][257]).all() and torch.isnan(out["dh"]).any(1).sum() == 1
         assert torch.isnan(out["dW"]).all()
+
+
+@pytest.mark.parametrize("N,dtype", [(128, torch.float32), (129, torch.float32), (300, torch.bfloat16)])
+def test_tokens_at_minus_infinity(N, dtype):
+    """A token of W at -infinity has probability 0 where W is taken as it is; from 129 rows on fp32 values are two parts, and an
+    infinity has none: NaN."""
+    k = K()
+    h, W, lab, _ = case(N, 40, 300, torch.float32, 0)
+    h[:, 0] = 1
+    lab[lab == 7] = 8
+    keep = torch.tensor([v for v in range(300) if v != 7], device="cuda")
+    want = k.kron_vocab_ce_fwd(h.to(dtype), W[keep].to(dtype).contiguous(), lab - (lab > 7).long())[1]
+    W[7], W[7, 0] = 0, float("-inf")
+    h, W = h.to(dtype), W.to(dtype)
+    loss, nll, stats = k.kron_vocab_ce_fwd(h, W, lab)
+    out = k.kron_vocab_ce_bwd(h, W, lab, stats, torch.ones(1, device="cuda"))
+    if dtype == torch.float32 and N > 128:
+        assert torch.isnan(nll).all() and torch.isnan(loss).all()
+        return
+    assert (nll - want).abs().max().item() <= 1e-5 * want.abs().max().item() + 1e-5
+    assert torch.count_nonzero(out["dW"][7]) == 0 and torch.isfinite(out["dW"]).all()
+    assert torch.isnan(out["dh"][:, 0]).all() and torch.isfinite(out["dh"][:, 1:]).all()
