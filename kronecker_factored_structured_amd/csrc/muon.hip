@@ -609,9 +609,11 @@ hipError_t for_groups(const MuonTensor* t, int n, const F& f) {
       mats += now.count;
       const int64_t skip = now.count * rest.rows * rest.cols;
       rest.count -= now.count;
-      rest.m += skip;
-      rest.p = (char*)rest.p + skip * f.element();
-      rest.g = (const char*)rest.g + skip * f.element();
+      if (rest.p) {      // (sizes alone have no pointers)
+        rest.m += skip;
+        rest.p = (char*)rest.p + skip * f.element();
+        rest.g = (const char*)rest.g + skip * f.element();
+      }
       if (k == kGroup || mats == most || (last && rest.count == 0)) {
         const hipError_t e = f(sl.first, sl.second, got, k, mats);
         if (e != hipSuccess) return e;
