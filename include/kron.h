@@ -573,8 +573,8 @@ kron_status_t kron_adapters_bwd(const kron_adapters_t* d, const void* x, const v
  * grads and m are read from the host.  scale may be NULL (1).  A matrix of zeros stays zero (X = 0); one with
  * a non-finite value becomes non-finite and no other does.
  * Sums are fp32, norms fp64.  fp32: products of matrices that do not fit a CU's LDS (smaller side over 64, or over
- * 156 KB) take their operands as two fp16 parts each: off by at most 2^-22 of the value, or 2^-38 (2^-40 of what a
- * singular value can become, where that is more).  bf16: as one fp16 part (2^-11).  Their scales follow from a, b and c: with
+ * 156 KB) take their operands as two fp16 parts each: off by at most 2^-22 of the value, or 2^-37 of the most that
+ * it can be.  bf16: as one fp16 part (2^-11).  Their scales follow from a, b and c: with
  * p(l) = a + b l + c l^2 the largest singular value goes from at most 1 to at most max |v p(v^2)| over those so far, in each
  * step; where it, but for the last step's, or |p| passes KRON_MUON_MAX_GROWTH the call is refused (KRON_E_UNSUPPORTED) if
  * it has such a matrix.

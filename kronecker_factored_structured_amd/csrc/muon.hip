@@ -679,8 +679,8 @@ size_t muon_workspace(const MuonTensor* t, int n, bool bf16) {
 // matrix are at most its largest singular value.  What 16-bit parts leave of A and P (2^-11 at most) comes on top.
 bool muon_scales(const MuonHyper& h, MuonScales* k) {
   const double a = h.a, b = h.b, c = h.c;
-  auto scale = [](double most) {
-    return most * kScale <= 49152 ? kScale : (float)std::exp2(std::floor(std::log2(49152 / most)));
+  auto scale = [](double most) {      // (matrices that shrink from step to step keep their bits as well, down to 2^-25)
+    return most >= 0.5 && most <= 6 ? kScale : (float)std::exp2(std::min(40.0, std::floor(std::log2(49152 / most))));
   };
   double x = 1;      // of X
   for (int i = 0; i < h.steps; ++i) {
