@@ -77,6 +77,14 @@ def test_other_quintics(coeffs, steps, shape, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shape", [(1, 1), (5, 1), (3, 7), (17, 15), (2, 4, 32, 64), (48, 24), (64, 64), (64, 300), (16, 1500), (2000, 9), (5, 63, 49),
+                                   (65, 65), (65, 130), (200, 70), (64, 1000), (16, 3000), (3001, 17), (1, 5000), (3, 100, 260), (2, 300, 66)])
+def test_the_default(shape, dtype):
+    """X alone (the rounding of parameters next to 1 would hide it)."""
+    compare(shape, dtype, OM.COEFFS, 5)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("shape", [(20, 30), (90, 80)])
 def test_rank_one_grows(shape, dtype):
     """The gradient of one sample: a singular value of 1, and the bound itself is reached."""

@@ -47,6 +47,8 @@ def compare(shapes, dtype, steps=5, lr=0.1, only=None):
     """Every matrix of every tensor (only: the numbers of those that are looked at)."""
     k = K()
     T = [tensors(i + sum(s), s, dtype) for i, s in enumerate(shapes)]
+    for W, _, _ in T:
+        W.zero_()      # (the rounding of parameters next to 1 would hide most of X's)
     before = [(W.clone(), m.clone()) for W, _, m in T]
     k.kron_muon_step(*([t[i] for t in T] for i in range(3)), lr=lr, steps=steps)
     bf = dtype == torch.bfloat16
