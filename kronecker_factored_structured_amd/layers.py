@@ -278,7 +278,7 @@ class KronAdapters(nn.Module):
                 raise ValueError("starts needs ids")
             ids = torch.zeros(1, dtype=torch.int32, device=x.device)
             starts = torch.arange(2, dtype=torch.int32, device=x.device) * rows.shape[0]
-        return _KronAdaptersFn.apply(rows, wide, self.down, self.up, ids, starts, self.scales).view(base.shape)
+        return _KronAdaptersFn.apply(rows, wide, self.down, self.up, ids, starts, self.scales.float()).view(base.shape)
 
 
 class KSLinear(nn.Module):

@@ -45,6 +45,24 @@ def test_adapters_of_a_converted_model():
         assert np.all(np.abs(f64(t) - g[key]) <= 88 * u * size[key] * 1.01 + 2.0 ** -8 * np.abs(g[key])), key
 
 
+def test_adapters_of_an_assigned_state():
+    """load_state_dict(assign=True) puts a checkpoint's own tensors in the scales' place, bfloat16 ones too."""
+    import kronecker_factored_structured_amd as K
+
+    def model(device):
+        return K.KronAdapters(torch.nn.Linear(16, 8, device=device), 16, 8, rank=2, adapters=2, alpha=3.0, device=device)
+
+    torch.manual_seed(5)
+    saved = model("cuda").bfloat16()
+    with torch.no_grad():
+        saved.up.normal_()
+    state = {k: v.bfloat16() for k, v in saved.state_dict().items()}
+    mod = model("meta")
+    mod.load_state_dict(state, assign=True)
+    x = torch.randn(5, 16, device="cuda").bfloat16()
+    assert torch.equal(mod(x), saved(x))      # (3 / 2 is what bfloat16 holds)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_learnt_weights(dtype):
     """d loss / d weights[n] is the row's own nll; a row of weight 0 is left out, and so is its gradient (0), whatever it
