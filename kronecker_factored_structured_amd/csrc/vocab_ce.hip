@@ -508,12 +508,21 @@ __global__ __launch_bounds__(256, 2) void vocab_dh_few_kernel(VocabCE a, int v0,
   }
 }
 
-// Four gradients of a row of K, times f and then f2, in their type.  Of fp32 sums f2 is the power of two of the tensor's largest
-// value, and kSums goes with f: s f stays within fp32's range where the gradient does.
-constexpr float kSums = 1.f / 16384 / kOne;      // of parts below 2^15, and dz's
+// What the sums of a gradient are times, in two steps: those of fp32 parts lie between 2^-20 and 2^50, whatever the tensors'
+// and the weights' sizes are, and sum f is within fp32's range then where sum f f2 is.
+struct Factor {
+  float f, f2;
+};
+__device__ inline Factor factor(double v) {
+  const int e = (int)((uint64_t)__double_as_longlong(v) >> 52 & 0x7ff) - 1023;
+  const int near = v == 0 || e == 1024 ? e : min(60, max(-90, e)), rest = min(127, max(-126, e - near));
+  return {(float)(v * __longlong_as_double((int64_t)(1023 + near - e) << 52)), __uint_as_float((uint32_t)(rest + 127) << 23)};
+}
+
+// Four gradients of a row of K in their type.
 template <bool BF>
-__device__ inline void put_grad(void* p, int64_t row, int k, int K, f4 s, float f2, float f) {
-  s = s * f * f2;
+__device__ inline void put_grad(void* p, int64_t row, int k, int K, f4 s, Factor f) {
+  s = s * f.f * f.f2;
   if constexpr (BF) {
     uint16_t* o = (uint16_t*)p + row * K + k;
     if ((K & 3) == 0)
@@ -539,8 +548,8 @@ template <bool BF, int SL>
 __global__ __launch_bounds__(256) void vocab_dh_join_kernel(VocabCE a, int splits) {
   constexpr int G = 256 / SL;
   __shared__ f4 red[SL][G];
-  const bool as_it_is = BF || a.wp == a.W;      // (dz without its scale, times W)
-  const float gout = a.gout[0], f2 = as_it_is ? 1.f : scale_down(a.sc->top_w) * 16384.f;
+  // (W as it is was multiplied by dz without its scale)
+  const double gout = a.gout[0], down = BF || a.wp == a.W ? 1.0 : (double)scale_down(a.sc->top_w) / kOne;
   const int per = a.Kp / 4, slice = threadIdx.x / G, mine = threadIdx.x % G;
   for (int64_t i0 = (int64_t)blockIdx.x * G; i0 < a.N * per; i0 += (int64_t)gridDim.x * G) {
     const int64_t i = i0 + mine, row = i / per;
@@ -560,22 +569,18 @@ __global__ __launch_bounds__(256) void vocab_dh_join_kernel(VocabCE a, int split
       __syncthreads();
     }
     if (in && slice == 0) {
-      const float f = BF ? unit_weight(a) * gout : (a.weights ? a.weights[row] : a.mean) * (as_it_is ? 1.f : kSums) * gout;
-      put_grad<BF>(a.dh, row, k, a.K, s, at >= 0 ? f2 : 0.f, at >= 0 ? f : 0.f);
+      const double f = (BF ? unit_weight(a) : a.weights ? a.weights[row] : a.mean) * gout * down;
+      put_grad<BF>(a.dh, row, k, a.K, s, at >= 0 ? factor(f) : Factor{0.f, 0.f});
     }
   }
 }
 
-// What dW's sums are times: f, then f2.
+// What dW's sums are times.
 template <bool BF>
-__device__ inline void dw_factors(const VocabCE& a, float& f, float& f2) {
-  f = a.gout[0], f2 = 1.f;
-  if constexpr (BF) {
-    f *= unit_weight(a);
-  } else {
-    f2 = scale_down(a.sc->top_h) * 16384.f;
-    f *= a.weights ? scale_down(a.sc->top_weight) * (1.f / 16384) : a.mean * kSums;
-  }
+__device__ inline Factor dw_factor(const VocabCE& a) {
+  const double gout = a.gout[0];
+  if constexpr (BF) return factor(gout * unit_weight(a));
+  else return factor(gout * scale_down(a.sc->top_h) * (a.weights ? (double)scale_down(a.sc->top_weight) : (double)a.mean / kOne));
 }
 
 // dW of a piece: K (m) x vocabulary (n), the contraction over the rows, in gridDim.y parts (one: into dW itself).  A piece's
@@ -595,12 +600,11 @@ __global__ __launch_bounds__(P::kThreads) void vocab_dw_kernel(VocabCE a, int v0
   P p;
   p.run(h, dz, m0, n0, k0, min(count, k0 + len), (lds_t*)smem);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
-  float f, f2;
-  dw_factors<BF>(a, f, f2);
+  const Factor f = dw_factor<BF>(a);
   if constexpr (BF) {
     if (gridDim.y == 1 && m0 + P::BM <= a.K && a.K % 8 == 0) {      // whole lines
       store_rows<P>(smem, (uint16_t*)a.dW + (int64_t)(v0 + n0) * a.K + m0, a.K, a.V - v0 - n0, [&](int i, int j) __attribute__((always_inline)) {
-        const f4 s = p.acc[i][j] * f;
+        const f4 s = p.acc[i][j] * f.f * f.f2;
         return uint2{bf16_pair(s[0], s[1]), bf16_pair(s[2], s[3])};
       });
       return;
@@ -616,7 +620,7 @@ __global__ __launch_bounds__(P::kThreads) void vocab_dw_kernel(VocabCE a, int v0
       if (gridDim.y > 1) {
         if (k < a.Kp) *(f4*)(a.dwpart + ((int64_t)blockIdx.y * vc + n) * a.Kp + k) = p.acc[i][j];
       } else if (k < a.K) {
-        put_grad<BF>(a.dW, v0 + n, k, a.K, p.acc[i][j], f2, f);
+        put_grad<BF>(a.dW, v0 + n, k, a.K, p.acc[i][j], f);
       }
     }
   }
@@ -624,8 +628,7 @@ __global__ __launch_bounds__(P::kThreads) void vocab_dw_kernel(VocabCE a, int v0
 
 template <bool BF>
 __global__ __launch_bounds__(256) void vocab_dw_join_kernel(VocabCE a, int v0, int vc, int parts) {
-  float f, f2;
-  dw_factors<BF>(a, f, f2);
+  const Factor f = dw_factor<BF>(a);
   const int per = a.Kp / 4, rows = min(vc, a.V - v0);
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < (int64_t)rows * per; i += (int64_t)gridDim.x * 256) {
     const int64_t row = i / per;
@@ -633,7 +636,7 @@ __global__ __launch_bounds__(256) void vocab_dw_join_kernel(VocabCE a, int v0, i
     if (k >= a.K) continue;
     f4 s = {0, 0, 0, 0};
     for (int t = 0; t < parts; ++t) s += *(const f4*)(a.dwpart + ((int64_t)t * vc + row) * a.Kp + k);
-    put_grad<BF>(a.dW, v0 + row, k, a.K, s, f2, f);
+    put_grad<BF>(a.dW, v0 + row, k, a.K, s, f);
   }
 }
 

@@ -104,3 +104,29 @@ def test_operands_at_the_ends_of_the_range(N, up):
         assert bool(torch.isfinite(got).all())
         assert torch.equal(got[there], want[there]), key
         assert bool((got[~there].abs() < 2.0 ** -99).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("N", [40, 200])
+@pytest.mark.parametrize("heavier,up", [(100, 0), (-100, 0), (120, -60), (125, -90), (-100, 60), (-90, 100)])
+def test_weights_at_the_ends_of_the_range(N, heavier, up, dtype):
+    """Weights 2^heavier, h 2^up and W 2^-up: dh is 2^(heavier - up) and dW 2^(heavier + up) of what they are without, bit by bit,
+    where that is within the range."""
+    k = K()
+    g = torch.Generator().manual_seed(N)
+    h, W = torch.randn(N, 40, generator=g).cuda(), (torch.randn(300, 40, generator=g) * 0.4).cuda()
+    h, W = (torch.where(t.abs() < 2.0 ** -5, torch.full_like(t, 0.25), t).to(dtype) for t in (h, W))
+    w = (torch.rand(N, generator=g) + 0.5).cuda()
+    lab, gout = torch.randint(0, 300, (N,), generator=g).cuda(), torch.ones(1, device="cuda")
+
+    def times(t, e):
+        return (t.double() * 2.0 ** e).to(t.dtype)
+
+    outs = []
+    for a, b, c in ((h, W, w), (times(h, up), times(W, -up), times(w, heavier))):
+        _, _, stats = k.kron_vocab_ce_fwd(a, b, lab, weights=c)
+        outs.append(k.kron_vocab_ce_bwd(a, b, lab, stats, gout, weights=c))
+    for key, e in (("dh", heavier - up), ("dW", heavier + up)):
+        want, got = outs[0][key].double() * 2.0 ** e, outs[1][key].double()
+        there = (want.abs() >= 2.0 ** -100) & (want.abs() < 2.0 ** 127)
+        assert torch.equal(got[there], want[there]), key
