@@ -503,7 +503,7 @@ kron_status_t kron_distill_bwd(const kron_distill_t* d, const void* logits, cons
  *   - Sums and softmax statistics are fp32 or fp64.  fp32 operands of the products are taken as they are
  *     (few rows), or as the sum of two fp16 parts after a scaling by a power of two: off by at most
  *     2^-22 of the value, or 2^-40 of the tensor's largest where that is more.  The softmax less the label's indicator
- *     is two such parts in both of the gradients' products, off by 2^-22 of itself, or 2^-51 (of 1) where that is more: dW of a
+ *     is two such parts in both of the gradients' products, off by 2^-22 of itself, or 2^-50 (of 1) where that is more: dW of a
  *     token that every row finds unlikelier than 1e-12 has fewer than ten bits.  For bf16 tensors the logits' gradient,
  *     over the largest weight, is rounded to bf16 once.  Every output is rounded once.
  * Limits: N <= KRON_VOCAB_CE_MAX_ROWS, K <= KRON_VOCAB_CE_MAX_WIDTH, V <= KRON_VOCAB_MAX.  N == 0 is

@@ -134,7 +134,8 @@ __global__ __launch_bounds__(1024) void vocab_top_kernel(VocabCE a) {
 // Rows as operands: gathered (h), padded with zeros to Kp, fp32 split into its parts.  which 0: h, 1: W, 2: h times the
 // rows' weights.
 constexpr float kOne = 32768.f;      // scale of what is at most 1
-constexpr int kUp = 11;              // and of its second part beside it: fp32's dz is off by 2^-22 of itself or 2^-51
+constexpr int kUp = 11;              // and of its second part beside it: fp32's dz is off by 2^-22 of itself or 2^-51 (and
+                                     // its products by as much, without that of both second parts)
 template <bool BF>
 __global__ __launch_bounds__(256) void vocab_pack_kernel(VocabCE a, int which) {
   const bool w = which == 1;

@@ -52,7 +52,7 @@ def test_vocabulary(N, dtype):
     bf = dtype == torch.bfloat16
     r = 2.0 ** -8 if bf else 2 * u
     dz = torch.exp(z - lse[:, None]) / N
-    off = dz * eps[:, None] + 2.0 ** -51 / N
+    off = dz * eps[:, None] + 2.0 ** -50 / N
     off[row, lab] += 4 * u / N
     dz[row, lab] -= 1.0 / N
     off += dz.abs() * (2.0 ** -8 if bf else 2.0 ** -22)

@@ -4,8 +4,9 @@ h and W lie at opposite ends of fp32's range.
 Tolerances as derived in test_gpu_vocab_ce.py, entry by entry: a logit is off by eps_z = (K + 20) u S, S = sum |h| |W|, and a
 probability by eps = 2 eps_z + u (4 spread + 3 (V / 2048 + 64) + 8) of itself.  The entry of a row's own label is a difference,
 off by 4 u of the weight more; every other entry of dz is off by eps of itself and its two parts' rounding, 2^-22 of itself or
-2^-51 of the weight (a second part that is subnormal: 2^-25 over 2^15 and 2^11).  dW sums N of them times h with (N + 40) u, dh
-V of them times W."""
+2^-50 of the weight: a second part that is subnormal is off by 2^-25 over 2^15 and 2^11, 2^-51, and as much is left out with the
+product of both second parts, where dz's is at most 2^-25 over 2^15 (its first one is subnormal) and h's 2^-11 of h.  dW sums N
+of them times h with (N + 40) u, dh V of them times W."""
 import numpy as np
 import pytest
 
@@ -42,7 +43,7 @@ def compare(h, W, lab, w, g=0.75):
     eps = 2 * (Kf + 20) * u * o["zs"] + u * (4 * spread + 3 * (V / 2048 + 64) + 8)
     assert np.all(np.abs(f64(nll)[used] - o["nll"][used]) <= eps + u * (np.abs(o["z"]).max(1) + np.abs(o["nll"][used])))
     label = np.arange(V) == lab.cpu().numpy()[used][:, None]
-    ddz = abs(g) * wn[:, None] * (o["p"] * eps[:, None] + 4 * u * label + 2.0 ** -51) + np.abs(o["dz"]) * 2.0 ** -22
+    ddz = abs(g) * wn[:, None] * (o["p"] * eps[:, None] + 4 * u * label + 2.0 ** -50) + np.abs(o["dz"]) * 2.0 ** -22
     sz = np.abs(o["dz"]) + ddz
     bound = ddz @ np.abs(f64(W)) + (V + 40) * u * (sz @ np.abs(f64(W)))
     assert np.all(np.abs(f64(out["dh"])[used] - o["dh"][used]) <= bound * (1 + 2 * u) + 2 * u * np.abs(o["dh"][used]))
@@ -72,11 +73,11 @@ def test_unlikely_tokens(N, Kf, V, weights):
         w[0] = 1
         w = w.cuda()
     o, off = compare(h.cuda(), W.cuda(), lab.cuda(), w)
-    # of a token's largest gradient: 1e-3 down to probabilities of 1e-12 (2^-51 is 4.4e-4 of that)
+    # of a token's largest gradient: 2e-3 down to probabilities of 1e-12 (2^-50 is 8.9e-4 of that, eps up to 2e-4)
     likely = o["p"].max(0)
     rows = np.abs(o["dW"]).max(1)
     assert (likely < 1e-9).any() and (likely < 1e-11).any()
-    assert np.all((off.max(1) <= 1e-3 * rows)[likely > 1e-12])
+    assert np.all((off.max(1) <= 2e-3 * rows)[likely > 1e-12])
 
 
 @pytest.mark.parametrize("N", [20, 60, 110, 200])
